@@ -341,6 +341,147 @@ hq_status hq_quantize_i8_rows(const float *W, int8_t *Wq, float *scale,
 hq_status hq_quantize_q4_k(const float *W, void *out, int64_t rows, int64_t cols, hq_stream_t stream);
 
 /*
+ * The batched step: the products of any number of tokens with the same stored
+ * weights, the probabilities of their logits, and the verification of drafted
+ * tokens.  The matvec calls above stay the right ones for one request's 1..8
+ * fp32 vectors; these serve prompts, and the verify step of many requests.
+ *
+ * Element types of x, y and logits in these calls (`dtype`): */
+#define HQ_DT_F32 0
+#define HQ_DT_F16 1
+#define HQ_DT_BF16 2
+/*
+ * hq_weight_exponents -- set-up of the many-token products, once per weight:
+ * w_exp[m] = e with every finite |weight| of matrix m below 2^(e + 14), read off the
+ * block scales d (e + 14 = the exponent of 128 max|d| for Q8_0, 8 max|d| for
+ * Q4_0, with max|d| = f 2^k, 0.5 <= f < 1, having exponent k; -14 when no d is finite and non-zero).  The products
+ * multiply in 16-bit floats; weights times 2^-e use their range fully
+ * whatever the scale of the matrix.
+ *   fmt : HQ_FMT_Q8_0 or HQ_FMT_Q4_0 (HQ_ERR_UNSUPPORTED otherwise).
+ *   W : n_mats matrices of rows x cols back to back, cols % 32 == 0, 16-byte aligned.
+ *   w_exp : int32 [n_mats] (device).  n_mats in [1, 65535].
+ * Source: none on the pages (a property of this implementation).
+ */
+hq_status hq_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_mats, int64_t rows, int64_t cols,
+                              hq_stream_t stream);
+
+/*
+ * hq_moe_matmul_q8_0 -- the expert-indexed Q8_0 product of any number of
+ * tokens: y[t][k] = W_bank[ids[t][k]] . x(t,k), as hq_moe_matvec_q8_0_ex
+ * computes for up to 8.  Slots are grouped by expert on the device (ragged
+ * groups, no host synchronisation).
+ *   W_bank, expert_ids, x_per_slot, router_w, epilogue : as for
+ *       hq_moe_matvec_q8_0_ex; expert_ids is int32 [n_tokens][n_active].
+ *   w_exp : int32 [n_experts], from hq_weight_exponents.
+ *   x, y  : `dtype`, the layouts of hq_moe_matvec_q8_0_ex with n_tokens for
+ *           n_vec; x 16-byte aligned, y aligned to its element.
+ *   n_tokens : >= 0 (0 returns HQ_OK and launches nothing);
+ *       n_tokens * n_active <= 2^27.  cols % 256 == 0; HQ_MOE_EPI_SWIGLU
+ *       needs an even number of rows; y may not overlap x.
+ *   workspace : device memory of hq_moe_matmul_workspace() bytes, 256-byte
+ *       aligned, not in use by other work until the call's kernels end.
+ *       hq_moe_matmul_workspace is a HOST function; a negative result is the
+ *       hq_status of arguments that the call itself would refuse.
+ * Accuracy: f16 and bf16: each weight is rounded to 11 bits, x is exact (elements below 2^-29
+ * of their row's largest are rounded to multiples of 2^-39 of it), sums are fp32, y is rounded
+ * once.  f32: both factors are split in two 11-bit terms and the
+ * product of the two small terms is left out: relative error of a
+ * product below 2^-20.  The fp32 sums of f32 leave the tensor core
+ * every 256 columns.
+ * Deterministic: the bits of a token's y do not depend on the other tokens, except through the
+ * split of the columns over CTAs that the launch's sizes choose.
+ * An id outside [0, n_experts): as for hq_moe_matvec_q8_0 (NaN, HQ_FAULT_EXPERT_ID).
+ * Source: as hq_moe_matvec_q8_0; the pages' prefill core is the same
+ * unified core ("One Native Stack ...", section "The Unified Quant Core").
+ */
+int64_t hq_moe_matmul_workspace(int64_t n_experts, int n_active, int64_t rows, int64_t cols, int64_t n_tokens,
+                                int x_per_slot, int dtype, int epilogue);
+hq_status hq_moe_matmul_q8_0(const void *W_bank, const int32_t *w_exp, const int32_t *expert_ids, const void *x,
+                             int x_per_slot, const float *router_w, void *y, int64_t n_experts, int n_active,
+                             int64_t rows, int64_t cols, int64_t n_tokens, int dtype, int epilogue,
+                             void *workspace, int64_t workspace_bytes, hq_stream_t stream);
+
+/*
+ * hq_matmul_q8_0_adapters, hq_matmul_q4_0_adapters -- the shared projection
+ * of many requests' tokens, each with its request's adapter:
+ *   y[t][i] = sum_j w_deq[i][j] x[t][j]
+ *             + scales[a] sum_k B[a][i][k] (sum_j A[a][k][j] x[t][j]),  a = adapter_ids[t].
+ *   w_exp : int32 [1], from hq_weight_exponents.
+ *   x : `dtype` [n_tokens][cols], 16-byte aligned.   y : `dtype` [n_tokens][rows].
+ *   adapter_ids : int32 [n_tokens], each in [-1, n_adapters); -1: no adapter.
+ *       Tokens of one request next to each other share the adapter's bytes.
+ *   lora_A : bf16 [n_adapters][rank][cols], 16-byte aligned.
+ *   lora_B : bf16 [n_adapters][rows][rank], 2-byte aligned.
+ *   scales : fp32 [n_adapters].   rank : 1..64 (adapters of smaller rank are padded with zeros).
+ *   n_adapters : >= 0; with 0 the adapter arguments are not read (they may be NULL) and the
+ *       call is the plain many-token product.
+ *   n_tokens : 0..2^27 (0 launches nothing).  cols % 256 == 0.
+ *   workspace : hq_matmul_adapters_workspace() bytes, 256-byte aligned (a HOST
+ *       function; negative: the hq_status of refused arguments).
+ * Accuracy of the base term as for hq_moe_matmul_q8_0; the adapter term takes x and A
+ * exactly and sums in fp32.  An id outside [-1, n_adapters) gives a NaN row of y and
+ * HQ_FAULT_ADAPTER_ID.
+ * Source: as hq_matvec_q8_0_lora (the Lemma "QLoRA over the unified core is
+ * exact"), for a batch in which every request brings its own adapter.
+ */
+int64_t hq_matmul_adapters_workspace(int rank, int64_t rows, int64_t cols, int64_t n_tokens, int dtype);
+hq_status hq_matmul_q8_0_adapters(const void *W, const int32_t *w_exp, const void *x, const int32_t *adapter_ids,
+                                  const uint16_t *lora_A, const uint16_t *lora_B, const float *scales,
+                                  int64_t n_adapters, int rank, void *y, int64_t rows, int64_t cols,
+                                  int64_t n_tokens, int dtype, void *workspace, int64_t workspace_bytes,
+                                  hq_stream_t stream);
+hq_status hq_matmul_q4_0_adapters(const void *W, const int32_t *w_exp, const void *x, const int32_t *adapter_ids,
+                                  const uint16_t *lora_A, const uint16_t *lora_B, const float *scales,
+                                  int64_t n_adapters, int rank, void *y, int64_t rows, int64_t cols,
+                                  int64_t n_tokens, int dtype, void *workspace, int64_t workspace_bytes,
+                                  hq_stream_t stream);
+
+/*
+ * hq_softmax_rows -- probabilities of logits, one temperature per row:
+ *   p[r][j] = exp((l[r][j] - max_j l[r][j]) / t_r) / sum_j exp(...),  t_r > 0;
+ *   t_r <= 0 : greedy, p[r] is 1 at the first maximum and 0 elsewhere.
+ *   logits : `dtype` [n_rows][vocab], aligned to its element.
+ *   temperature : fp32 [n_rows], or NULL for 1.   p : fp32 [n_rows][vocab].
+ *   n_rows : 0..2^31-1 (0 launches nothing).  vocab : 1..2^22.
+ * Logits of -inf give 0.  A row of nothing but -inf gives zeros (greedy too).  A row with
+ * a NaN or +inf gives NaNs (greedy: the first maximum of what is not NaN; a row of nothing
+ * but NaN and -inf gives zeros).  p may be the logits' own
+ * memory when dtype is HQ_DT_F32.
+ * Source: "DeepSeek-V4 on Hanzo Engine" (the verify rows whose
+ * probabilities a speculative step compares).
+ */
+hq_status hq_softmax_rows(const void *logits, const float *temperature, float *p, int64_t n_rows, int64_t vocab,
+                          int dtype, hq_stream_t stream);
+
+/*
+ * hq_verify_drafts -- speculative verification of n_req requests at once.
+ * Request r drafted tokens drafts[off[r] .. off[r+1]); n_r = off[r+1] - off[r] >= 0.
+ *   p  : fp32 [n_drafts + n_req][vocab], the target's probabilities: row off[r] + r + i
+ *        is the target's distribution of request r's draft i, i = n_r the one after its last.
+ *   q  : fp32 [n_drafts][vocab], the drafting probabilities, or NULL: drafts were certain (q = 1 at the draft).
+ *   u_accept : fp32 [n_drafts], u_sample : fp32 [n_req], uniform numbers in [0, 1), the caller's.
+ * Draft i is accepted while u_i * q_i(d_i) < p_i(d_i) (one fp32 product) and all before it were; a_r counts
+ * them.  One more token is then sampled, from s = max(p - q, 0) (fp32) of the first refused draft, or from
+ * s = p of the row after the last draft: s is taken as the integers S_j = floor(2^40 s_j), and the token is the
+ * lowest j with S_0 + ... + S_j > floor(U sum S / 2^24), U = floor(2^24 u_sample[r]).  Integer sums have no
+ * order, so the token is exact.  If the residual's integers are all zero, s = p is used; if those
+ * are all zero too, the token is -1.
+ *   n_accepted : int32 [n_req] = a_r.
+ *   tokens     : int32 [n_drafts + n_req]; request r's at off[r] + r: the a_r accepted
+ *                drafts, the sampled token, then -1 for each refused draft after the first.
+ *   draft_offsets : int32 [n_req + 1] (device), from 0 to n_drafts.
+ *   n_req : 0..2^24 (0 launches nothing); n_drafts >= 0 (0: drafts, q and u_accept are not read);
+ *   n_drafts + n_req <= 2^30; vocab 1..2^22.
+ * Probabilities are clamped to [0, 1], NaN counts as 0.  A draft outside
+ * [0, vocab) is refused and sets HQ_FAULT_DRAFT, as do offsets that do not rise from 0 to n_drafts
+ * (that request's outputs are then left unwritten).
+ * Source: "DeepSeek-V4 on Hanzo Engine", the speculative-verify widths q in [1, 8].
+ */
+hq_status hq_verify_drafts(const float *p, const float *q, const int32_t *drafts, const int32_t *draft_offsets,
+                           const float *u_accept, const float *u_sample, int32_t *n_accepted, int32_t *tokens,
+                           int64_t n_req, int64_t n_drafts, int64_t vocab, hq_stream_t stream);
+
+/*
  * hq_requant_params -- HOST function: real multipliers M[i] in (0, 1) to
  * (mult, shift) with M ~= mult * 2^-31 * 2^-shift: M = f * 2^-shift with
  * f in [0.5, 1), mult = round(f * 2^31) (half away from zero; 2^31 becomes
@@ -374,6 +515,8 @@ hq_status hq_requant_i32_debug(const int32_t *acc, const int32_t *mult, const in
  */
 #define HQ_FAULT_WAIT_TIMEOUT 1u   /* an mbarrier wait exceeded its time limit */
 #define HQ_FAULT_EXPERT_ID    2u   /* an expert id outside [0, n_experts)      */
+#define HQ_FAULT_ADAPTER_ID   4u   /* an adapter id outside [-1, n_adapters)   */
+#define HQ_FAULT_DRAFT        8u   /* draft offsets that do not rise from 0 to n_drafts, or a draft outside [0, vocab) */
 hq_status hq_device_fault(uint32_t *fault);
 
 /*

@@ -21,6 +21,9 @@ from ._binding import (  # noqa: F401
     hq_moe_matvec_q8_0_swiglu, hq_moe_matvec_q8_0_combine, hq_moe_matvec_q8_0_ex,
     HQ_MOE_EPI_NONE, HQ_MOE_EPI_SWIGLU, HQ_MOE_EPI_COMBINE, HQ_MOE_IDS_READY,
     hq_matvec_q8_0_lora, hq_matvec_q4_0_lora, hq_matvec_q8_0_lora_noalloc,
+    hq_weight_exponents, hq_moe_matmul_workspace, hq_moe_matmul_q8_0, hq_matmul_adapters_workspace,
+    hq_matmul_q8_0_adapters, hq_matmul_q4_0_adapters, hq_softmax_rows, hq_verify_drafts,
+    HQ_FAULT_ADAPTER_ID, HQ_FAULT_DRAFT, HQ_DT_F32, HQ_DT_F16, HQ_DT_BF16, DTYPE_CODES,
     hq_quantize_q8_0, hq_quantize_q4_0, hq_quantize_i8_rows, hq_requant_params,
     hq_requant_i32_debug, hq_device_fault, hq_selftest_wait_timeout, hq_launch_count, hq_debug_plan,
     Q8_0_BLOCK_BYTES, Q4_0_BLOCK_BYTES, QK, row_bytes,

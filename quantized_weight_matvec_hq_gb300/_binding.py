@@ -18,6 +18,8 @@ HQ_ERR_UNSUPPORTED = -6
 HQ_ERR_DEVICE = -7
 HQ_FAULT_WAIT_TIMEOUT = 1
 HQ_FAULT_EXPERT_ID = 2
+HQ_FAULT_ADAPTER_ID = 4
+HQ_FAULT_DRAFT = 8
 
 QK = 32
 Q8_0_BLOCK_BYTES = 34
@@ -26,6 +28,9 @@ QK_K = 256
 Q4_K_BLOCK_BYTES = 144
 # format codes of hq_debug_plan
 FMT_CODES = {"q8_0": 8, "q4_0": 4, "q4_k": 75, "i8": 1}
+# element types of the many-token calls
+HQ_DT_F32, HQ_DT_F16, HQ_DT_BF16 = 0, 1, 2
+DTYPE_CODES = {"f32": HQ_DT_F32, "f16": HQ_DT_F16, "bf16": HQ_DT_BF16}
 
 _NAMES = {HQ_ERR_NULL: "HQ_ERR_NULL", HQ_ERR_SHAPE: "HQ_ERR_SHAPE", HQ_ERR_ALIGN: "HQ_ERR_ALIGN",
           HQ_ERR_NVEC: "HQ_ERR_NVEC", HQ_ERR_LAUNCH: "HQ_ERR_LAUNCH",
@@ -65,6 +70,17 @@ _SIGS = {
     "hq_quantize_i8_rows": ([_vp, _vp, _vp, _i64, _i64, _vp], _int),
     "hq_requant_params": ([_vp, _i64, _vp, _vp], _int),
     "hq_requant_i32_debug": ([_vp, _vp, _vp, _vp, _i64, _i64, _vp], _int),
+    "hq_weight_exponents": ([_int, _vp, _vp, _i64, _i64, _i64, _vp], _int),
+    "hq_moe_matmul_workspace": ([_i64, _int, _i64, _i64, _i64, _int, _int, _int], _i64),
+    "hq_moe_matmul_q8_0": ([_vp, _vp, _vp, _vp, _int, _vp, _vp, _i64, _int, _i64, _i64, _i64, _int, _int, _vp, _i64,
+                            _vp], _int),
+    "hq_matmul_adapters_workspace": ([_int, _i64, _i64, _i64, _int], _i64),
+    "hq_matmul_q8_0_adapters": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _vp, _i64, _i64, _i64, _int, _vp, _i64,
+                                 _vp], _int),
+    "hq_matmul_q4_0_adapters": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _vp, _i64, _i64, _i64, _int, _vp, _i64,
+                                 _vp], _int),
+    "hq_softmax_rows": ([_vp, _vp, _vp, _i64, _i64, _int, _vp], _int),
+    "hq_verify_drafts": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp], _int),
     "hq_device_fault": ([_vp], _int),
     "hq_selftest_wait_timeout": ([_i64, _vp], _int),
     "hq_launch_count": ([], ctypes.c_uint64),
@@ -209,6 +225,65 @@ def hq_moe_matvec_q8_0_ex(W_bank, expert_ids, x, x_per_slot: int, router_w, y, n
     return _check(lib().hq_moe_matvec_q8_0_ex(_addr(W_bank), _addr(expert_ids), _addr(x), int(x_per_slot),
                                               _addr(router_w), _addr(y), n_experts, n_active, rows, cols, n_vec,
                                               int(epilogue), int(flags), _stream(stream)))
+
+
+def _check_size(n: int) -> int:
+    if n < 0:
+        _check(n)
+    return int(n)
+
+
+def hq_weight_exponents(fmt: int, W, w_exp, n_mats: int, rows: int, cols: int, stream=None) -> int:
+    return _check(lib().hq_weight_exponents(int(fmt), _addr(W), _addr(w_exp), n_mats, rows, cols, _stream(stream)))
+
+
+def hq_moe_matmul_workspace(n_experts: int, n_active: int, rows: int, cols: int, n_tokens: int, x_per_slot: int,
+                            dtype: int, epilogue: int) -> int:
+    """HOST function: bytes of the workspace that hq_moe_matmul_q8_0 takes."""
+    return _check_size(lib().hq_moe_matmul_workspace(n_experts, n_active, rows, cols, n_tokens, int(x_per_slot),
+                                                     int(dtype), int(epilogue)))
+
+
+def hq_moe_matmul_q8_0(W_bank, w_exp, expert_ids, x, x_per_slot: int, router_w, y, n_experts: int, n_active: int,
+                       rows: int, cols: int, n_tokens: int, dtype: int, epilogue: int, workspace,
+                       workspace_bytes: int, stream=None) -> int:
+    return _check(lib().hq_moe_matmul_q8_0(_addr(W_bank), _addr(w_exp), _addr(expert_ids), _addr(x), int(x_per_slot),
+                                           _addr(router_w), _addr(y), n_experts, n_active, rows, cols, n_tokens,
+                                           int(dtype), int(epilogue), _addr(workspace), workspace_bytes,
+                                           _stream(stream)))
+
+
+def hq_matmul_adapters_workspace(rank: int, rows: int, cols: int, n_tokens: int, dtype: int) -> int:
+    """HOST function: bytes of the workspace that hq_matmul_*_adapters take."""
+    return _check_size(lib().hq_matmul_adapters_workspace(int(rank), rows, cols, n_tokens, int(dtype)))
+
+
+def hq_matmul_q8_0_adapters(W, w_exp, x, adapter_ids, lora_A, lora_B, scales, n_adapters: int, rank: int, y, rows: int,
+                            cols: int, n_tokens: int, dtype: int, workspace, workspace_bytes: int, stream=None) -> int:
+    return _check(lib().hq_matmul_q8_0_adapters(_addr(W), _addr(w_exp), _addr(x), _addr(adapter_ids), _addr(lora_A),
+                                                _addr(lora_B), _addr(scales), n_adapters, int(rank), _addr(y), rows,
+                                                cols, n_tokens, int(dtype), _addr(workspace), workspace_bytes,
+                                                _stream(stream)))
+
+
+def hq_matmul_q4_0_adapters(W, w_exp, x, adapter_ids, lora_A, lora_B, scales, n_adapters: int, rank: int, y, rows: int,
+                            cols: int, n_tokens: int, dtype: int, workspace, workspace_bytes: int, stream=None) -> int:
+    return _check(lib().hq_matmul_q4_0_adapters(_addr(W), _addr(w_exp), _addr(x), _addr(adapter_ids), _addr(lora_A),
+                                                _addr(lora_B), _addr(scales), n_adapters, int(rank), _addr(y), rows,
+                                                cols, n_tokens, int(dtype), _addr(workspace), workspace_bytes,
+                                                _stream(stream)))
+
+
+def hq_softmax_rows(logits, temperature, p, n_rows: int, vocab: int, dtype: int, stream=None) -> int:
+    return _check(lib().hq_softmax_rows(_addr(logits), _addr(temperature), _addr(p), n_rows, vocab, int(dtype),
+                                        _stream(stream)))
+
+
+def hq_verify_drafts(p, q, drafts, draft_offsets, u_accept, u_sample, n_accepted, tokens, n_req: int, n_drafts: int,
+                     vocab: int, stream=None) -> int:
+    return _check(lib().hq_verify_drafts(_addr(p), _addr(q), _addr(drafts), _addr(draft_offsets), _addr(u_accept),
+                                         _addr(u_sample), _addr(n_accepted), _addr(tokens), n_req, n_drafts, vocab,
+                                         _stream(stream)))
 
 
 def hq_quantize_q8_0(W, out, rows: int, cols: int, stream=None) -> int:

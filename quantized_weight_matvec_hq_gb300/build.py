@@ -18,7 +18,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhq.so")
 # (source, extra defines, object name): the kernel file is compiled in five parts
 # (Q8_0, Q4_0, int8 and helpers, MoE, Q4_K)
-SOURCES = [("hq_api.cu", [], "hq_api.o"), ("hq_quant.cu", [], "hq_quant.o")] + [
+SOURCES = [("hq_api.cu", [], "hq_api.o"), ("hq_quant.cu", [], "hq_quant.o"),
+           ("hq_matmul.cu", [], "hq_matmul.o"), ("hq_verify.cu", [], "hq_verify.o")] + [
     ("hq_kernels.cu", [f"-DHQ_PART={i}"], f"hq_kernels_{i}.o") for i in range(5)]
 HEADERS = ["hq_device.cuh", "hq_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -83,7 +84,7 @@ def kernel_resources(out_dir: str) -> dict:
     nvcc = _nvcc()
     jobs = [[nvcc, *ARCH, *NVCC_FLAGS, "-Xptxas", "-v", *defs, "-c", os.path.join(CSRC, src),
              "-o", os.path.join(out_dir, obj)]
-            for src, defs, obj in SOURCES if src == "hq_kernels.cu"]
+            for src, defs, obj in SOURCES if src not in ("hq_api.cu", "hq_quant.cu")]
     with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
         results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
     res, name, spill = {}, None, (0, 0)

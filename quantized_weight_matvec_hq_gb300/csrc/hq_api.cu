@@ -346,6 +346,226 @@ hq_status hq_quantize_i8_rows(const float *W, int8_t *Wq, float *scale, int64_t 
     return finish(launch_quantize(2, W, Wq, scale, rows, cols, (cudaStream_t)stream));
 }
 
+// ------------------------------------------------------------------ the batched step
+
+static size_t dtype_bytes(int dtype) { return dtype == HQ_DT_F32 ? 4 : 2; }
+
+static hq_status check_dtype(int dtype) {
+    if (dtype < HQ_DT_F32 || dtype > HQ_DT_BF16)
+        return set_error(HQ_ERR_UNSUPPORTED, "dtype %d is not HQ_DT_F32, _F16 or _BF16", dtype);
+    return HQ_OK;
+}
+
+hq_status hq_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_mats, int64_t rows, int64_t cols,
+                              hq_stream_t stream) {
+    if (!W || !w_exp) return set_error(HQ_ERR_NULL, "W and w_exp must be non-null");
+    if (fmt != HQ_FMT_Q8_0 && fmt != HQ_FMT_Q4_0)
+        return set_error(HQ_ERR_UNSUPPORTED, "fmt %d: 8 (Q8_0) or 4 (Q4_0)", fmt);
+    if (n_mats < 1 || n_mats > 65535 || rows < 1 || rows > 0x7fffffffLL || cols < 32 || cols % 32 != 0 ||
+        cols > (1LL << 31))
+        return set_error(HQ_ERR_SHAPE, "bad shape n_mats=%lld rows=%lld cols=%lld", (long long)n_mats,
+                         (long long)rows, (long long)cols);
+    if (!aligned(W, 16) || !aligned(w_exp, 4)) return set_error(HQ_ERR_ALIGN, "W must be 16-byte aligned, w_exp 4-byte");
+    return finish(launch_weight_exponents(fmt, W, w_exp, n_mats, rows, cols, (cudaStream_t)stream));
+}
+
+// Sizes and codes of the many-token products (no pointers).
+static hq_status check_moe_matmul_sizes(int64_t n_experts, int n_active, int64_t rows, int64_t cols, int64_t n_tokens,
+                                        int x_per_slot, int dtype, int epilogue) {
+    hq_status st = check_dtype(dtype);
+    if (st != HQ_OK) return st;
+    if (epilogue < HQ_MOE_EPI_NONE || epilogue > HQ_MOE_EPI_COMBINE)
+        return set_error(HQ_ERR_UNSUPPORTED, "epilogue %d is not HQ_MOE_EPI_NONE, _SWIGLU or _COMBINE", epilogue);
+    if (n_experts < 1 || n_experts > 65535 || n_active < 1 || n_active > n_experts || rows < 1 ||
+        rows > 0x7fffffffLL / n_experts || cols < 256 || cols % 256 != 0 || cols > (1LL << 30) || n_tokens < 0 ||
+        n_tokens > (1LL << 27) / n_active || (x_per_slot != 0 && x_per_slot != 1))
+        return set_error(HQ_ERR_SHAPE,
+                         "bad MoE shape n_experts=%lld n_active=%d rows=%lld cols=%lld n_tokens=%lld x_per_slot=%d "
+                         "(need 1<=n_active<=n_experts<=65535, n_tokens*n_active<=2^27, cols%%256==0)",
+                         (long long)n_experts, n_active, (long long)rows, (long long)cols, (long long)n_tokens,
+                         x_per_slot);
+    if (epilogue == HQ_MOE_EPI_SWIGLU && rows % 2 != 0)
+        return set_error(HQ_ERR_SHAPE, "SwiGLU needs interleaved gate/up rows: rows = %lld is odd", (long long)rows);
+    return HQ_OK;
+}
+
+static hq_status check_adapter_sizes(int rank, int64_t rows, int64_t cols, int64_t n_tokens, int dtype) {
+    hq_status st = check_dtype(dtype);
+    if (st != HQ_OK) return st;
+    if (rows < 1 || rows > 0x7fffffffLL || cols < 256 || cols % 256 != 0 || cols > (1LL << 30) || n_tokens < 0 ||
+        n_tokens > (1LL << 27))
+        return set_error(HQ_ERR_SHAPE, "bad shape rows=%lld cols=%lld n_tokens=%lld (need cols%%256==0, n_tokens<=2^27)",
+                         (long long)rows, (long long)cols, (long long)n_tokens);
+    if (rank < 0 || rank > 64) return set_error(HQ_ERR_SHAPE, "rank %d not in [0,64]", rank);
+    return HQ_OK;
+}
+
+static hq_status check_workspace(const MatmulArgs &a, int64_t workspace_bytes) {
+    const int64_t need = matmul_workspace(a);
+    if (need > 0 && !a.workspace) return set_error(HQ_ERR_NULL, "workspace must be non-null");
+    if (workspace_bytes < need)
+        return set_error(HQ_ERR_SHAPE, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
+    if (!aligned(a.workspace, 256)) return set_error(HQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+    return HQ_OK;
+}
+
+int64_t hq_moe_matmul_workspace(int64_t n_experts, int n_active, int64_t rows, int64_t cols, int64_t n_tokens,
+                                int x_per_slot, int dtype, int epilogue) {
+    hq_status st = check_moe_matmul_sizes(n_experts, n_active, rows, cols, n_tokens, x_per_slot, dtype, epilogue);
+    if (st != HQ_OK) return st;
+    MatmulArgs a;
+    a.moe = true;
+    a.n_mats = n_experts;
+    a.n_active = n_active;
+    a.rows = rows;
+    a.cols = cols;
+    a.n_tokens = n_tokens;
+    a.x_per_slot = x_per_slot;
+    a.dtype = dtype;
+    a.epilogue = epilogue;
+    finish(HQ_OK);
+    return matmul_workspace(a);
+}
+
+hq_status hq_moe_matmul_q8_0(const void *W_bank, const int32_t *w_exp, const int32_t *expert_ids, const void *x,
+                             int x_per_slot, const float *router_w, void *y, int64_t n_experts, int n_active,
+                             int64_t rows, int64_t cols, int64_t n_tokens, int dtype, int epilogue,
+                             void *workspace, int64_t workspace_bytes, hq_stream_t stream) {
+    hq_status st = check_moe_matmul_sizes(n_experts, n_active, rows, cols, n_tokens, x_per_slot, dtype, epilogue);
+    if (st != HQ_OK) return st;
+    if (n_tokens == 0) return finish(HQ_OK);
+    if (!W_bank || !w_exp || !expert_ids || !x || !y)
+        return set_error(HQ_ERR_NULL, "W_bank, w_exp, expert_ids, x and y must be non-null");
+    if (epilogue == HQ_MOE_EPI_COMBINE && !router_w) return set_error(HQ_ERR_NULL, "router_w must be non-null");
+    if (!aligned(W_bank, 16) || !aligned(x, 16) || !aligned(y, dtype_bytes(dtype)) || !aligned(w_exp, 4) ||
+        !aligned(expert_ids, 4) || !aligned(router_w, 4))
+        return set_error(HQ_ERR_ALIGN, "W_bank and x must be 16-byte aligned, the rest aligned to its elements");
+    MatmulArgs a;
+    a.moe = true;
+    a.fmt = HQ_FMT_Q8_0;
+    a.W = W_bank;
+    a.w_exp = w_exp;
+    a.idx = expert_ids;
+    a.x = x;
+    a.y = y;
+    a.n_mats = n_experts;
+    a.rows = rows;
+    a.cols = cols;
+    a.n_tokens = n_tokens;
+    a.dtype = dtype;
+    a.n_active = n_active;
+    a.x_per_slot = x_per_slot;
+    a.epilogue = epilogue;
+    a.router_w = epilogue == HQ_MOE_EPI_COMBINE ? router_w : nullptr;
+    a.workspace = workspace;
+    st = check_workspace(a, workspace_bytes);
+    if (st != HQ_OK) return st;
+    return finish(launch_matmul(a, (cudaStream_t)stream));
+}
+
+int64_t hq_matmul_adapters_workspace(int rank, int64_t rows, int64_t cols, int64_t n_tokens, int dtype) {
+    hq_status st = check_adapter_sizes(rank, rows, cols, n_tokens, dtype);
+    if (st != HQ_OK) return st;
+    MatmulArgs a;
+    a.rank = rank;
+    a.rows = rows;
+    a.cols = cols;
+    a.n_tokens = n_tokens;
+    a.dtype = dtype;
+    finish(HQ_OK);
+    return matmul_workspace(a);
+}
+
+static hq_status matmul_adapters(int fmt, const void *W, const int32_t *w_exp, const void *x,
+                                 const int32_t *adapter_ids, const uint16_t *lora_A, const uint16_t *lora_B,
+                                 const float *scales, int64_t n_adapters, int rank, void *y, int64_t rows,
+                                 int64_t cols, int64_t n_tokens, int dtype, void *workspace, int64_t workspace_bytes,
+                                 hq_stream_t stream) {
+    hq_status st = check_adapter_sizes(rank, rows, cols, n_tokens, dtype);
+    if (st != HQ_OK) return st;
+    if (n_adapters < 0 || n_adapters > 0x7fffffffLL)
+        return set_error(HQ_ERR_SHAPE, "n_adapters %lld out of range", (long long)n_adapters);
+    if (n_adapters > 0 && rank < 1) return set_error(HQ_ERR_SHAPE, "rank %d not in [1,64]", rank);
+    if (n_tokens == 0) return finish(HQ_OK);
+    if (!W || !w_exp || !x || !y) return set_error(HQ_ERR_NULL, "W, w_exp, x and y must be non-null");
+    if (n_adapters > 0 && (!adapter_ids || !lora_A || !lora_B || !scales))
+        return set_error(HQ_ERR_NULL, "adapter_ids, lora_A, lora_B and scales must be non-null");
+    if (!aligned(W, 16) || !aligned(x, 16) || !aligned(y, dtype_bytes(dtype)) || !aligned(w_exp, 4))
+        return set_error(HQ_ERR_ALIGN, "W and x must be 16-byte aligned, w_exp and y aligned to their elements");
+    if (n_adapters > 0 && (!aligned(lora_A, 16) || !aligned(lora_B, 2) || !aligned(scales, 4) || !aligned(adapter_ids, 4)))
+        return set_error(HQ_ERR_ALIGN, "lora_A must be 16-byte aligned, the other adapter arguments to their elements");
+    MatmulArgs a;
+    a.fmt = fmt;
+    a.W = W;
+    a.w_exp = w_exp;
+    a.x = x;
+    a.y = y;
+    a.rows = rows;
+    a.cols = cols;
+    a.n_tokens = n_tokens;
+    a.dtype = dtype;
+    a.n_adapters = n_adapters;
+    if (n_adapters > 0) {
+        a.rank = rank;
+        a.idx = adapter_ids;
+        a.A = lora_A;
+        a.B = lora_B;
+        a.scales = scales;
+    }
+    a.workspace = workspace;
+    st = check_workspace(a, workspace_bytes);
+    if (st != HQ_OK) return st;
+    return finish(launch_matmul(a, (cudaStream_t)stream));
+}
+
+hq_status hq_matmul_q8_0_adapters(const void *W, const int32_t *w_exp, const void *x, const int32_t *adapter_ids,
+                                  const uint16_t *lora_A, const uint16_t *lora_B, const float *scales,
+                                  int64_t n_adapters, int rank, void *y, int64_t rows, int64_t cols,
+                                  int64_t n_tokens, int dtype, void *workspace, int64_t workspace_bytes,
+                                  hq_stream_t stream) {
+    return matmul_adapters(HQ_FMT_Q8_0, W, w_exp, x, adapter_ids, lora_A, lora_B, scales, n_adapters, rank, y, rows,
+                           cols, n_tokens, dtype, workspace, workspace_bytes, stream);
+}
+
+hq_status hq_matmul_q4_0_adapters(const void *W, const int32_t *w_exp, const void *x, const int32_t *adapter_ids,
+                                  const uint16_t *lora_A, const uint16_t *lora_B, const float *scales,
+                                  int64_t n_adapters, int rank, void *y, int64_t rows, int64_t cols,
+                                  int64_t n_tokens, int dtype, void *workspace, int64_t workspace_bytes,
+                                  hq_stream_t stream) {
+    return matmul_adapters(HQ_FMT_Q4_0, W, w_exp, x, adapter_ids, lora_A, lora_B, scales, n_adapters, rank, y, rows,
+                           cols, n_tokens, dtype, workspace, workspace_bytes, stream);
+}
+
+hq_status hq_softmax_rows(const void *logits, const float *temperature, float *p, int64_t n_rows, int64_t vocab,
+                          int dtype, hq_stream_t stream) {
+    hq_status st = check_dtype(dtype);
+    if (st != HQ_OK) return st;
+    if (n_rows < 0 || n_rows > 0x7fffffffLL || vocab < 1 || vocab > (1LL << 22))
+        return set_error(HQ_ERR_SHAPE, "bad shape n_rows=%lld vocab=%lld", (long long)n_rows, (long long)vocab);
+    if (n_rows == 0) return finish(HQ_OK);
+    if (!logits || !p) return set_error(HQ_ERR_NULL, "logits and p must be non-null");
+    if (!aligned(logits, dtype_bytes(dtype)) || !aligned(temperature, 4) || !aligned(p, 4))
+        return set_error(HQ_ERR_ALIGN, "logits, temperature and p must be aligned to their elements");
+    return finish(launch_softmax(logits, temperature, p, n_rows, vocab, dtype, (cudaStream_t)stream));
+}
+
+hq_status hq_verify_drafts(const float *p, const float *q, const int32_t *drafts, const int32_t *draft_offsets,
+                           const float *u_accept, const float *u_sample, int32_t *n_accepted, int32_t *tokens,
+                           int64_t n_req, int64_t n_drafts, int64_t vocab, hq_stream_t stream) {
+    if (n_req < 0 || n_req > (1LL << 24) || n_drafts < 0 || n_drafts + n_req > (1LL << 30) || vocab < 1 ||
+        vocab > (1LL << 22))
+        return set_error(HQ_ERR_SHAPE, "bad shape n_req=%lld n_drafts=%lld vocab=%lld", (long long)n_req,
+                         (long long)n_drafts, (long long)vocab);
+    if (n_req == 0) return finish(HQ_OK);
+    if (!p || !draft_offsets || !u_sample || !n_accepted || !tokens || (n_drafts > 0 && (!drafts || !u_accept)))
+        return set_error(HQ_ERR_NULL, "p, drafts, draft_offsets, u_accept, u_sample, n_accepted and tokens must be non-null");
+    if (!aligned(p, 4) || !aligned(q, 4) || !aligned(drafts, 4) || !aligned(draft_offsets, 4) || !aligned(u_accept, 4) ||
+        !aligned(u_sample, 4) || !aligned(n_accepted, 4) || !aligned(tokens, 4))
+        return set_error(HQ_ERR_ALIGN, "every array must be 4-byte aligned");
+    return finish(launch_verify(p, q, drafts, draft_offsets, u_accept, u_sample, n_accepted, tokens, n_req, n_drafts,
+                                vocab, (cudaStream_t)stream));
+}
+
 hq_status hq_requant_params(const double *M, int64_t n, int32_t *mult, int32_t *shift) {
     if (!M || !mult || !shift) return set_error(HQ_ERR_NULL, "M, mult and shift must be non-null");
     for (int64_t i = 0; i < n; ++i) {

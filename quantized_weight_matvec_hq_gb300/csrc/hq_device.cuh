@@ -18,6 +18,8 @@ namespace hq {
 constexpr long long kWaitTimeoutCycles = 4000000000ll;
 constexpr uint32_t kFaultWaitTimeout = 1u;
 constexpr uint32_t kFaultExpertId = 2u;
+constexpr uint32_t kFaultAdapterId = 4u;
+constexpr uint32_t kFaultDraft = 8u;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -231,6 +233,11 @@ __device__ __forceinline__ int ld_shared_cluster_s32(uint32_t addr) {
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+
+// ------------------------------------------------------------------ programmatic dependent launch
+
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------ arithmetic helpers
 

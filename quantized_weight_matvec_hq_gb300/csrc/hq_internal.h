@@ -61,6 +61,37 @@ hq_status launch_requant_debug(const int32_t *acc, const int32_t *mult, const in
                                int8_t *y, int64_t n, int64_t rows, cudaStream_t stream);
 hq_status launch_quantize(int fmt, const float *W, void *out, float *scale, int64_t rows,
                           int64_t cols, cudaStream_t stream);
+// The products of many tokens (hq_matmul.cu).  `idx` groups the slots by expert
+// (n_active per token) or names each token's adapter.
+struct MatmulArgs {
+    int fmt = 8;                        // 8 Q8_0, 4 Q4_0
+    const void *W = nullptr;
+    const int32_t *w_exp = nullptr;
+    const int32_t *idx = nullptr;       // expert ids [n_tokens][n_active], or adapter ids [n_tokens]
+    const void *x = nullptr;
+    void *y = nullptr;
+    int64_t n_mats = 1, rows = 0, cols = 0, n_tokens = 0;
+    int dtype = 0;
+    // grouped by expert
+    bool moe = false;
+    int n_active = 1, x_per_slot = 0, epilogue = 0;
+    const float *router_w = nullptr;
+    // adapters
+    const uint16_t *A = nullptr, *B = nullptr;
+    const float *scales = nullptr;
+    int64_t n_adapters = 0;
+    int rank = 0;
+    void *workspace = nullptr;
+};
+int64_t matmul_workspace(const MatmulArgs &a);
+hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream);
+hq_status launch_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_mats, int64_t rows, int64_t cols,
+                                  cudaStream_t stream);
+hq_status launch_softmax(const void *logits, const float *temperature, float *p, int64_t n_rows, int64_t vocab,
+                         int dtype, cudaStream_t stream);
+hq_status launch_verify(const float *p, const float *q, const int32_t *drafts, const int32_t *off,
+                        const float *u_accept, const float *u_sample, int32_t *n_accepted, int32_t *tokens,
+                        int64_t n_req, int64_t n_drafts, int64_t vocab, cudaStream_t stream);
 // Test-only plan queries (no device touched): see hq_debug_plan in hq.h.
 hq_status debug_plan_float_q8_0(int n_vec, int64_t rows, int64_t cols, int num_sms, int smem_optin, int regs,
                                 int64_t *out);

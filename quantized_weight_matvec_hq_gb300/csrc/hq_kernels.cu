@@ -1097,8 +1097,6 @@ __device__ __forceinline__ void consume_cols(const uint8_t *wt, const uint8_t *x
     else P::template consume_pair<NV, R>(wt, xt, lane, warp, acc);
 }
 
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------ the kernel
 //
