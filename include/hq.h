@@ -376,7 +376,7 @@ hq_status hq_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_
  *   x, y  : `dtype`, the layouts of hq_moe_matvec_q8_0_ex with n_tokens for
  *           n_vec; x 16-byte aligned, y aligned to its element.
  *   n_tokens : >= 0 (0 returns HQ_OK and launches nothing);
- *       n_tokens * n_active <= 2^27.  cols % 256 == 0; HQ_MOE_EPI_SWIGLU
+ *       n_tokens * n_active <= 2^27; n_experts <= 8192.  cols % 256 == 0; HQ_MOE_EPI_SWIGLU
  *       needs an even number of rows; y may not overlap x.
  *   workspace : device memory of hq_moe_matmul_workspace() bytes, 256-byte
  *       aligned, not in use by other work until the call's kernels end.

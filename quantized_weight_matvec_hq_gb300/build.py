@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libhq.so")
 SOURCES = [("hq_api.cu", [], "hq_api.o"), ("hq_quant.cu", [], "hq_quant.o"),
            ("hq_matmul.cu", [], "hq_matmul.o"), ("hq_verify.cu", [], "hq_verify.o")] + [
     ("hq_kernels.cu", [f"-DHQ_PART={i}"], f"hq_kernels_{i}.o") for i in range(5)]
-HEADERS = ["hq_device.cuh", "hq_internal.h"]
+HEADERS = ["hq_device.cuh", "hq_internal.h", "hq_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-DNDEBUG"]

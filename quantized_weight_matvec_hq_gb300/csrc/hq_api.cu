@@ -376,12 +376,12 @@ static hq_status check_moe_matmul_sizes(int64_t n_experts, int n_active, int64_t
     if (st != HQ_OK) return st;
     if (epilogue < HQ_MOE_EPI_NONE || epilogue > HQ_MOE_EPI_COMBINE)
         return set_error(HQ_ERR_UNSUPPORTED, "epilogue %d is not HQ_MOE_EPI_NONE, _SWIGLU or _COMBINE", epilogue);
-    if (n_experts < 1 || n_experts > 65535 || n_active < 1 || n_active > n_experts || rows < 1 ||
+    if (n_experts < 1 || n_experts > 8192 || n_active < 1 || n_active > n_experts || rows < 1 ||
         rows > 0x7fffffffLL / n_experts || cols < 256 || cols % 256 != 0 || cols > (1LL << 30) || n_tokens < 0 ||
         n_tokens > (1LL << 27) / n_active || (x_per_slot != 0 && x_per_slot != 1))
         return set_error(HQ_ERR_SHAPE,
                          "bad MoE shape n_experts=%lld n_active=%d rows=%lld cols=%lld n_tokens=%lld x_per_slot=%d "
-                         "(need 1<=n_active<=n_experts<=65535, n_tokens*n_active<=2^27, cols%%256==0)",
+                         "(need 1<=n_active<=n_experts<=8192, n_tokens*n_active<=2^27, cols%%256==0)",
                          (long long)n_experts, n_active, (long long)rows, (long long)cols, (long long)n_tokens,
                          x_per_slot);
     if (epilogue == HQ_MOE_EPI_SWIGLU && rows % 2 != 0)

@@ -388,6 +388,26 @@ def test_no_adapters_is_the_bare_product(hq, fmt):
     assert torch.equal(bare, y)
 
 
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0"])
+def test_slow_outputs_do_not_disturb_the_products(hq, fmt):
+    """Rank-64 adapters of zeros over several tiles per CTA: the adapter term keeps
+    the load unit busy while later tiles are decoded.  Every run has the bits of
+    the bare product."""
+    g = synthetic.rng(75)
+    rows, cols, T, n = 6144, 1024, 2011, 8
+    blocks = weights(g, fmt, rows, cols)
+    W = dev(blocks)
+    e = exponents(hq, fmt, W, 1, rows, cols)
+    x = torch.from_numpy(g.standard_normal((T, cols)).astype(np.float32)).cuda().half()
+    A = torch.from_numpy(g.standard_normal((n, 64, cols)).astype(np.float32)).cuda().bfloat16()
+    B = torch.zeros((n, rows, 64), dtype=torch.bfloat16, device="cuda")
+    ids = dev(np.sort(g.integers(0, n, T)).astype(np.int32))
+    bare = run_lora(hq, fmt, W, e, x, None, None, None, None, 0, 0, rows, cols, "f16")
+    for _ in range(10):
+        y = run_lora(hq, fmt, W, e, x, ids, A, B, torch.ones(n, device="cuda"), n, 64, rows, cols, "f16")
+        assert torch.equal(bare, y)
+
+
 def test_adapter_ids_out_of_range(hq):
     g = synthetic.rng(72)
     ids = g.integers(-1, 3, 50)
