@@ -1,5 +1,5 @@
 // hq_tc.cuh -- sm_103a tensor-core primitives: tcgen05 allocation, products
-// with operands in shared memory, accumulator loads, and gathered TMA loads.
+// with operands in shared memory, and accumulator loads.
 // Inline PTX only.
 #pragma once
 
@@ -20,7 +20,7 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // D[128][N] (+)= A[128][16] B[N][16]^T, 16-bit floats in shared memory, fp32 in TMEM.
-__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
@@ -38,9 +38,9 @@ __device__ __forceinline__ uint64_t tc_desc_sw128(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3fffu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// f16 x f16 -> f32, both K-major, M = 128.
-__device__ __forceinline__ uint32_t tc_idesc_f16(int n) {
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+// fp32 sums of f16 (or bf16) products, both operands K-major, M = 128.
+__device__ __forceinline__ uint32_t tc_idesc(int n, bool bf16) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 // This warp's 32 lanes x 8 columns.  The values may be used only after
@@ -67,13 +67,11 @@ __device__ __forceinline__ void tmem_wait_ld(float (&v)[8]) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Four rows of a 2-D tensor (map box: one row high) to four consecutive rows of shared memory.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *m, int c, int4 rows, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w),
-          "r"(bar) : "memory");
+// One thread of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 
 __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
