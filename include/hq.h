@@ -442,7 +442,7 @@ hq_status hq_matmul_q4_0_adapters(const void *W, const int32_t *w_exp, const voi
  *   t_r <= 0 : greedy, p[r] is 1 at the first maximum and 0 elsewhere.
  *   logits : `dtype` [n_rows][vocab], aligned to its element.
  *   temperature : fp32 [n_rows], or NULL for 1.   p : fp32 [n_rows][vocab].
- *   n_rows : 0..2^31-1 (0 launches nothing).  vocab : 1..2^22.
+ *   n_rows : 0..2^28-1 (0 launches nothing).  vocab : 1..2^22.
  * Logits of -inf give 0.  A row of nothing but -inf gives zeros (greedy too).  A row with
  * a NaN or +inf gives NaNs (greedy: the first maximum of what is not NaN; a row of nothing
  * but NaN and -inf gives zeros).  p may be the logits' own

@@ -540,7 +540,7 @@ hq_status hq_softmax_rows(const void *logits, const float *temperature, float *p
                           int dtype, hq_stream_t stream) {
     hq_status st = check_dtype(dtype);
     if (st != HQ_OK) return st;
-    if (n_rows < 0 || n_rows > 0x7fffffffLL || vocab < 1 || vocab > (1LL << 22))
+    if (n_rows < 0 || n_rows > (1LL << 28) || vocab < 1 || vocab > (1LL << 22))
         return set_error(HQ_ERR_SHAPE, "bad shape n_rows=%lld vocab=%lld", (long long)n_rows, (long long)vocab);
     if (n_rows == 0) return finish(HQ_OK);
     if (!logits || !p) return set_error(HQ_ERR_NULL, "logits and p must be non-null");
