@@ -6,9 +6,11 @@
 // A prepare kernel lays the call out, then one persistent kernel multiplies:
 //  * The weights are the M operand (128 rows of W a tile) and the tokens the N
 //    operand (16 to 256 a tile), so ragged groups of tokens cost what they are.
-//  * Raw blocks come by TMA (256 columns of 128 rows a stage).  Two groups of four warps
-//    decode them, a quarter (64 columns) at a time, to 16-bit floats in the swizzled layout the tensor core
-//    reads; quarters take turns over four operand slots.
+//  * Raw blocks come by TMA (256 columns of 128 rows a chunk).  Four groups of four warps
+//    decode a quarter (64 columns) each to 16-bit floats, a row a thread, and store them to TMEM, from where
+//    the tensor core reads them.  (Through shared memory, decoded weights were written and read
+//    at 256 of the about 440 to 880 cycles of its bandwidth that 64 columns took, and it was the limit.)
+//    Each scheduler has a warp of every group, so that the groups' loads, waits and arithmetic overlap.
 //  * Tokens come by TMA, an expert's tokens next to each other (the prepare kernel sorts them).
 //  * Adapters are further columns of the same product: a tile's distinct adapters' B, side by side, times each token's
 //    u = A x at its own adapter's place and zero elsewhere.
@@ -39,28 +41,33 @@ namespace {
 // ------------------------------------------------------------------ shared with the host
 
 constexpr int kTileRows = 128;
-constexpr int kMaxTokens = 240;             // tokens of a tile: what four operand slots leave room for
+constexpr int kMaxTokens = 192;             // tokens of a tile: two accumulators and four operand slots are 512 columns
 constexpr int kMaxTokensSplit = 48;         // f32: twice the operands
-constexpr int kSlots = 4;
-constexpr int kABytes = kTileRows * 128;
-constexpr int kEpiWarps = 8, kDecodeWarps = 8;
-constexpr int kWarpW = kEpiWarps + kDecodeWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpX + 1;
-constexpr int kThreads = 32 * (kWarpMma + 1);
+constexpr int kSlotCols = 32;               // TMEM columns of a decoded quarter (f32: of each term)
+constexpr int kDecodeWarps = 16;
+// Warps of a block: outputs (one or two for each quarter of the rows), decode, and one each for the weights' copies,
+// the tokens' copies and the products.
+template <bool SPLIT> struct Roles {
+    static constexpr int kSides = SPLIT ? 1 : 2, kEpi = 4 * kSides, kW = kEpi + kDecodeWarps, kX = kW + 1, kMma = kX + 1;
+    static constexpr int kThreads = 32 * (kMma + 1);
+};
 constexpr int kPrepThreads = 512;
-constexpr int kMaxRaw = 4;
+constexpr int kMaxRaw = 4, kMaxX = 8;
+constexpr int kBoxes = 5;                   // boxes of 16, 32, 64, 128 and tile_n tokens
 
 template <int FMT> struct Fmt;
 template <> struct Fmt<8> { static constexpr int kChunk = 272, kVecs = 5; };   // bytes of 8 blocks; 16-byte units a quarter touches
 template <> struct Fmt<4> { static constexpr int kChunk = 144, kVecs = 3; };
 
-// Virtual ranks of an adapter stage: u is two bf16 terms (16 bits) of 32 ranks, or three (f32) of 16.
+// Virtual ranks of an adapter quarter: u is two bf16 terms (16 bits) of 32 ranks, or three (f32) of 16.
 template <bool SPLIT> struct Ext { static constexpr int kRanks = SPLIT ? 16 : 32, kTerms = SPLIT ? 3 : 2; };
 
 // One tile of tokens of one expert: sorted slots [start, start + n).
 struct TileRec { int mat, start, n, w_exp; };
 
-struct TcArgs {
-    CUtensorMap map_w, map_x64, map_x16, map_lo64, map_lo16;
+// What the kernel's warps keep in registers: they copy it, since what a pointer is taken from (the tensor maps) is read again
+// after every inline statement, a constant-cache access each time.
+struct Sizes {
     const int32_t *w_exp;
     const int32_t *x_exp;           // [sorted slots], or NULL: 0
     const int32_t *order;           // sorted slot -> slot, or NULL: the same
@@ -75,14 +82,19 @@ struct TcArgs {
     uint32_t *fault;
     long long rows;
     int n_tokens, n_tt, n_items, n_rt, n_chunks;
-    int tile_n, raw_slots, ksplit, tmem_cols;
-    int dtype, epilogue, rank, stream_w;
+    int tile_n, raw_slots, x_log, x_k, deep, ksplit, tmem_cols;   // 2^x_log slots of x_k (1, 2 or 4) times 64 columns of tokens
+    int epilogue, rank, stream_w;
     uint32_t zero;                  // 0, unknown to the compiler
-    uint32_t off_x, off_raw, off_red, off_meta;
+    uint32_t off_raw, off_red;
+};
+
+struct TcArgs {
+    CUtensorMap map_w, map_x[kBoxes], map_lo[kBoxes];
+    Sizes z;
 };
 
 struct Meta {
-    uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw], full[kSlots], empty[kSlots];
+    uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw], x_full[kMaxX], x_empty[kMaxX], full[4], empty[4];
     uint64_t acc_full[2], acc_empty[2], red_full, red_empty, done;
     uint32_t tmem;
     int abort;
@@ -90,12 +102,15 @@ struct Meta {
     float2 scale[kMaxTokens];
 };
 
+constexpr int kOffX = 4096;                 // shared memory: the barriers and a tile's columns, tokens, raw blocks, joined sums
+static_assert(sizeof(Meta) <= kOffX, "the head of shared memory");
+
 struct Item { int mat, rt, start, n, w_exp, count; };
 
 // Work item `w`: a tile of rows and a tile of tokens.  Grouped: an expert's row tiles follow one another, so
 // that its weights are read again from L2 if it has several tiles of tokens; one matrix: a row tile's token
 // tiles follow one another.
-__device__ __forceinline__ Item get_item(const TcArgs &a, int w) {
+__device__ __forceinline__ Item get_item(const Sizes &a, int w) {
     Item t;
     if (a.tiles) {
         const TileRec r = a.tiles[w / a.n_rt];
@@ -117,14 +132,22 @@ __device__ __forceinline__ Item get_item(const TcArgs &a, int w) {
     return t;
 }
 
-// Adapter stages of a tile, an even number, and this CTA's share of them.
+// Adapter quarters of a tile: this CTA's share of them.  They go through the pipeline as
+// chunks of four; the last one may hold fewer.
 template <bool SPLIT>
-__device__ __forceinline__ int2 ext_range(const TcArgs &a, const Item &t, int rank) {
-    const int pairs = (t.count * a.rank + 2 * Ext<SPLIT>::kRanks - 1) / (2 * Ext<SPLIT>::kRanks);
-    return make_int2(2 * (pairs * rank / a.ksplit), 2 * (pairs * (rank + 1) / a.ksplit));
+__device__ __forceinline__ int2 ext_range(const Sizes &a, const Item &t, int rank) {
+    const int all = (t.count * a.rank + Ext<SPLIT>::kRanks - 1) / Ext<SPLIT>::kRanks;
+    return make_int2(all * rank / a.ksplit, all * (rank + 1) / a.ksplit);
 }
 
 __device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
+
+// The box that fetches a tile of n tokens, and its rows.
+__device__ __forceinline__ int box_of(const Sizes &a, int n) {
+    const int b = n <= 16 ? 0 : n <= 32 ? 1 : n <= 64 ? 2 : n <= 128 ? 3 : 4;
+    return a.tiles && 16 << b < a.tile_n ? b : kBoxes - 1;
+}
+__device__ __forceinline__ int box_rows(const Sizes &a, int b) { return b == kBoxes - 1 ? a.tile_n : 16 << b; }
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
@@ -141,44 +164,36 @@ __device__ __forceinline__ void ld_shared_volatile(uint32_t addr, uint32_t *v) {
 // mantissa of 1024, whose integers f16 holds exactly; 1024 + bias is subtracted
 // exactly, and the product with the scaled d is rounded once.
 template <int FMT, bool SPLIT, int I0>
-__device__ __forceinline__ void decode_quarter(const uint32_t *w, float wscale, uint8_t *dst, int row) {
+__device__ __forceinline__ void decode_quarter(const uint32_t *w, float wscale, uint32_t dst) {
     const __half2 bias = FMT == 8 ? __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480))    // 1152
                                   : __half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));   // 1032
     constexpr int kWords = FMT == 8 ? 8 : 4;
-    uint8_t *line = dst + row * 128;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         const uint32_t dw = b == 0 ? w[I0] & 0xffffu : w[I0 + kWords] >> 16;
         const __half ds = __float2half_rn(__half2float(__ushort_as_half((unsigned short)dw)) * wscale);
         const __half2 d = __half2half2(ds);
-        uint32_t q[kWords];
+        uint32_t hi[16], lo[SPLIT ? 16 : 1];                // pairs of columns
 #pragma unroll
-        for (int j = 0; j < kWords; ++j)
-            q[j] = b == 0 ? __funnelshift_r(w[I0 + j], w[I0 + j + 1], 16) : w[I0 + kWords + 1 + j];
+        for (int h = 0; h < 8; ++h) {                       // four columns
+            const int j = FMT == 8 ? h : h & 3;
+            uint32_t v = b == 0 ? __funnelshift_r(w[I0 + j], w[I0 + j + 1], 16) : w[I0 + kWords + 1 + j];
+            if constexpr (FMT == 8) v ^= 0x80808080u;
+            else v = (h < 4 ? v : v >> 4) & 0x0f0f0f0fu;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {                    // 16-byte units of 8 columns
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t v;
-                if constexpr (FMT == 8) v = q[2 * c + h] ^ 0x80808080u;
-                else v = (c < 2 ? q[2 * c + h] : q[2 * (c - 2) + h] >> 4) & 0x0f0f0f0fu;
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const uint32_t m = prmt(v, 0x64646464u, p ? 0x4342u : 0x4140u);
-                    const __half2 n = __hsub2(*reinterpret_cast<const __half2 *>(&m), bias);
-                    const __half2 r = __hmul2(n, d);
-                    hi[2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
-                    if constexpr (SPLIT) {
-                        const __half2 l = __hfma2(n, d, __hneg2(r));
-                        lo[2 * h + p] = *reinterpret_cast<const uint32_t *>(&l);
-                    }
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t m = prmt(v, 0x64646464u, p ? 0x4342u : 0x4140u);
+                const __half2 n = __hsub2(*reinterpret_cast<const __half2 *>(&m), bias);
+                const __half2 r = __hmul2(n, d);
+                hi[2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
+                if constexpr (SPLIT) {
+                    const __half2 l = __hfma2(n, d, __hneg2(r));
+                    lo[2 * h + p] = *reinterpret_cast<const uint32_t *>(&l);
                 }
             }
-            const int unit = ((4 * b + c) ^ (row & 7)) << 4;
-            *reinterpret_cast<uint4 *>(line + unit) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if constexpr (SPLIT) *reinterpret_cast<uint4 *>(line + kABytes + unit) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
+        tmem_st16(dst + 16 * b, hi);
+        if constexpr (SPLIT) tmem_st16(dst + kSlotCols + 16 * b, lo);
     }
 }
 
@@ -193,37 +208,46 @@ __device__ __forceinline__ void store_elem(void *y, long long i, int dtype, floa
 // z / (1 + e^-z).  The approximate exponential and quotient are within 2^-21 (1 + |z| / 4) of it.
 __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
 
-// The 8 columns from c0 of output row `row` (its sums in v): scales, SwiGLU with the neighbouring lane's row, store.
-__device__ __forceinline__ void finish8(const TcArgs &a, const Meta *m, int c0, int n, long long row, float (&v)[8]) {
+template <int OT>
+__device__ __forceinline__ void store_out(void *y, long long i, float v) {
+    if constexpr (OT == HQ_DT_F32) static_cast<float *>(y)[i] = v;
+    else if constexpr (OT == HQ_DT_F16) static_cast<__half *>(y)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
+}
+
+// The W columns from c0 of output row `row` (its sums in v): scales, SwiGLU with the neighbouring lane's row, store.
+template <int OT, int W>
+__device__ __forceinline__ void finish(const Sizes &a, const Meta *m, int c0, int n, long long row, float (&v)[W]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < W; ++j) {
         const float2 s = m->scale[c0 + j];
         v[j] = v[j] * s.x * s.y;
     }
     if (a.epilogue == HQ_MOE_EPI_SWIGLU) {
         // even lanes hold gate rows, odd lanes up rows: each finishes every other token
         const bool odd = threadIdx.x & 1;
+        const long long half = a.rows / 2, i = row / 2;
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
+        for (int j = 0; j < W; j += 2) {
             const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-            const float h = odd ? silu(got) * v[j + 1] : silu(v[j]) * got;
+            const float h = silu(odd ? got : v[j]) * (odd ? v[j + 1] : got);
             const int c = c0 + j + (odd ? 1 : 0);
-            if (c < n && row < a.rows) store_elem(a.y, (long long)m->slot[c] * (a.rows / 2) + row / 2, a.dtype, h);
+            if (c < n && row < a.rows) store_out<OT>(a.y, m->slot[c] * half + i, h);
         }
         return;
     }
     if (row < a.rows) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + j < n) store_elem(a.y, (long long)m->slot[c0 + j] * a.rows + row, a.dtype, v[j]);
+        for (int j = 0; j < W; ++j)
+            if (c0 + j < n) store_out<OT>(a.y, m->slot[c0 + j] * a.rows + row, v[j]);
     }
 }
 
-// ------------------------------------------------------------------ adapter stages
+// ------------------------------------------------------------------ adapter quarters
 
 // Virtual ranks [v0, v0 + kRanks) of one row of the tile's adapters' B, packed in pairs.
 template <bool SPLIT>
-__device__ __forceinline__ void load_b(const TcArgs &a, const int32_t *list, int total, int v0, long long row, uint32_t (&b)[16]) {
+__device__ __forceinline__ void load_b(const Sizes &a, const int32_t *list, int total, int v0, long long row, uint32_t (&b)[16]) {
     constexpr int R = Ext<SPLIT>::kRanks;
     if ((a.rank & 7) == 0) {
 #pragma unroll
@@ -255,7 +279,7 @@ __device__ __forceinline__ void load_b(const TcArgs &a, const int32_t *list, int
 
 // Row `c` of the token operand: u of the token's own adapter at its virtual ranks, as bf16 terms side by side, zero elsewhere.
 template <bool SPLIT>
-__device__ __forceinline__ void store_u(const TcArgs &a, const Item &t, int v0, int c, uint8_t *dst) {
+__device__ __forceinline__ void store_u(const Sizes &a, const Item &t, int v0, int c, uint8_t *dst) {
     constexpr int R = Ext<SPLIT>::kRanks, T = Ext<SPLIT>::kTerms;
     const int place = c < t.n ? a.place[t.start + c] : -1;
     const int lo = place * a.rank - v0;                     // virtual rank v0 + k is rank k - lo of the adapter
@@ -292,239 +316,298 @@ __device__ __forceinline__ void store_u(const TcArgs &a, const Item &t, int v0, 
 
 // ------------------------------------------------------------------ the kernel
 
-template <int FMT, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) matmul_tc_kernel(const __grid_constant__ TcArgs a) {
+template <int FMT, bool SPLIT, int OT>
+__global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(const __grid_constant__ TcArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    Meta *m = reinterpret_cast<Meta *>(smem + a.off_meta);
+    Meta *m = reinterpret_cast<Meta *>(smem);
+    const Sizes z = a.z;
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    constexpr int kTerms = SPLIT ? 2 : 1;
+    constexpr int kTerms = SPLIT ? 2 : 1, kSides = Roles<SPLIT>::kSides;
+    constexpr int kEpiWarps = Roles<SPLIT>::kEpi, kWarpW = Roles<SPLIT>::kW, kWarpX = Roles<SPLIT>::kX, kWarpMma = Roles<SPLIT>::kMma;
     constexpr int kChunkBytes = kTileRows * Fmt<FMT>::kChunk;
-    const int rank = a.ksplit > 1 ? (int)cluster_ctarank() : 0;
-    const uint32_t a_base = smem_u32(smem), x_base = a_base + a.off_x, raw_base = a_base + a.off_raw;
-    const int x_bytes = a.tile_n * 128;
+    const int rank = z.ksplit > 1 ? (int)cluster_ctarank() : 0;
+    const uint32_t x_base = smem_u32(smem) + kOffX, raw_base = smem_u32(smem) + z.off_raw;
+    const uint32_t x_lo = z.x_k * z.tile_n * 128, x_slot = kTerms * x_lo, x_mask = (1u << z.x_log) - 1;     // bytes to the low terms, of a slot
     volatile int *abort = &m->abort;
-    uint32_t *fault = a.fault;
+    uint32_t *fault = z.fault;
 
     if (threadIdx.x == 0) {
         m->abort = 0;
-        for (int i = 0; i < a.raw_slots; ++i) { mbar_init(smem_u32(&m->raw_full[i]), 1); mbar_init(smem_u32(&m->raw_empty[i]), kDecodeWarps); }
-        for (int i = 0; i < kSlots; ++i) { mbar_init(smem_u32(&m->full[i]), 5); mbar_init(smem_u32(&m->empty[i]), 1); }
+        for (int i = 0; i < z.raw_slots; ++i) { mbar_init(smem_u32(&m->raw_full[i]), 1); mbar_init(smem_u32(&m->raw_empty[i]), kDecodeWarps); }
+        for (int i = 0; i < 1 << z.x_log; ++i) { mbar_init(smem_u32(&m->x_full[i]), 1); mbar_init(smem_u32(&m->x_empty[i]), 1); }
+        for (int i = 0; i < 4; ++i) { mbar_init(smem_u32(&m->full[i]), z.deep ? kDecodeWarps : 4); mbar_init(smem_u32(&m->empty[i]), 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&m->acc_full[i]), 1); mbar_init(smem_u32(&m->acc_empty[i]), kEpiWarps); }
         mbar_init(smem_u32(&m->done), 1);
-        mbar_init(smem_u32(&m->red_full), (uint32_t)max(1, (a.ksplit - 1) * kEpiWarps));
-        mbar_init(smem_u32(&m->red_empty), (uint32_t)max(1, (a.ksplit - 1) * kEpiWarps));
+        mbar_init(smem_u32(&m->red_full), (uint32_t)max(1, (z.ksplit - 1) * kEpiWarps));
+        mbar_init(smem_u32(&m->red_empty), (uint32_t)max(1, (z.ksplit - 1) * kEpiWarps));
         fence_mbar_init();
     }
-    if (warp == kWarpMma) tmem_alloc(smem_u32(&m->tmem), (uint32_t)a.tmem_cols);
+    if (warp == kWarpMma) tmem_alloc(smem_u32(&m->tmem), (uint32_t)z.tmem_cols);
     tc_fence_before();
-    if (a.ksplit > 1) cluster_sync(); else __syncthreads();
+    if (z.ksplit > 1) cluster_sync(); else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)&m->tmem;
+    // TMEM: two buffers of accumulators, (f32) the running sums, then the operand slots
+    const uint32_t half = (SPLIT ? 2 : 1) * z.tile_n, run = 2 * half, slots = run + (SPLIT ? z.tile_n : 0);
     griddep_launch_dependents();
 
-    const int first = blockIdx.x / a.ksplit, step = gridDim.x / a.ksplit;
-    const int c_lo = (int)((long long)a.n_chunks * rank / a.ksplit);
-    const int c_hi = (int)((long long)a.n_chunks * (rank + 1) / a.ksplit);
+    const int first = blockIdx.x / z.ksplit, step = gridDim.x / z.ksplit;
+    const int c_lo = (int)((long long)z.n_chunks * rank / z.ksplit);
+    const int c_hi = (int)((long long)z.n_chunks * (rank + 1) / z.ksplit);
     // one matrix's weights may be fetched before the prepare kernel is done; everything else waits for it
-    if (a.tiles || warp != kWarpW) griddep_wait();
+    if (z.tiles || warp != kWarpW) griddep_wait();
     Item t = {};
-    if (a.tiles || warp != kWarpW) t = get_item(a, min(first, a.n_items - 1));
-    const int n_items = a.tiles ? *a.n_tiles * a.n_rt : a.n_items;
+    if (z.tiles || warp != kWarpW) t = get_item(z, min(first, z.n_items - 1));
+    const int n_items = z.tiles ? *z.n_tiles * z.n_rt : z.n_items;
 
     if (warp == kWarpW) {
-        const uint64_t pol = a.stream_w ? l2_evict_first_policy() : l2_evict_normal_policy();
-        uint32_t s = 0, ph = 1, it = 0;
-        bool ok = true;
-        for (int w = first; w < n_items && ok; w += step) {
-            const int row0 = a.tiles ? (int)((long long)t.mat * a.rows + (long long)t.rt * kTileRows) : w / a.n_tt * kTileRows;
-            if (a.tiles && w + step < n_items) t = get_item(a, w + step);
-            for (int c = c_lo; c < c_hi; ++c, ++it) {
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m->raw_empty[s]), ph, abort, fault));
-                if (!ok) break;
-                if (elect_one()) {
+        if (elect_one()) {
+            const uint64_t pol = z.stream_w ? l2_evict_first_policy() : l2_evict_normal_policy();
+            uint32_t s = 0, ph = 1, it = 0;
+            bool ok = true;
+            for (int w = first; w < n_items && ok; w += step) {
+                const int row0 = z.tiles ? (int)((long long)t.mat * z.rows + (long long)t.rt * kTileRows) : w / z.n_tt * kTileRows;
+                if (z.tiles && w + step < n_items) t = get_item(z, w + step);
+                for (int c = c_lo; c < c_hi; ++c, ++it) {
+                    // past the first slots the wait is for this kernel's own warps, which wait for the prepare kernel
+                    if (!z.tiles && it == (uint32_t)z.raw_slots) griddep_wait();
+                    ok = tc_wait(smem_u32(&m->raw_empty[s]), ph, abort, fault);
+                    if (!ok) break;
                     const uint32_t bar = smem_u32(&m->raw_full[s]);
                     mbar_arrive_expect_tx(bar, kChunkBytes);
                     tma_load_2d(raw_base + s * kChunkBytes, &a.map_w, c * (Fmt<FMT>::kChunk / 2), row0, bar, pol);
+                    if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
                 }
-                if (++s == (uint32_t)a.raw_slots) { s = 0; ph ^= 1; }
             }
+            // copies in flight end before the block's memory is given back
+            for (uint32_t k = it > (uint32_t)z.raw_slots ? it - z.raw_slots : 0; !ok && k < it; ++k)
+                for (int tries = 0; tries < 1 << 8 && !mbar_try_wait(smem_u32(&m->raw_full[k % z.raw_slots]), (k / z.raw_slots) & 1); ++tries) {}
         }
-        // copies in flight end before the block's memory is given back
-        for (uint32_t k = it > (uint32_t)a.raw_slots ? it - a.raw_slots : 0; !ok && k < it; ++k)
-            for (int tries = 0; tries < 1 << 12 && !mbar_try_wait(smem_u32(&m->raw_full[k % a.raw_slots]), (k / a.raw_slots) & 1); ++tries) {}
+        __syncwarp();
     } else if (warp == kWarpX) {
-        const uint64_t pol = l2_evict_normal_policy();
-        uint32_t it = 0;
-        bool ok = true;
-        for (int w = first; w < n_items && ok; w += step) {
-            const Item cur = t;
-            if (w + step < n_items) t = get_item(a, w + step);
-            const int n16 = round16(cur.n);
-            const int2 ext = ext_range<SPLIT>(a, cur, rank);
-            const int main = 4 * (c_hi - c_lo), all = main + ext.y - ext.x;
-            for (int k = 0; k < all; ++k, ++it) {
-                const uint32_t s = it & 3;
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m->empty[s]), ((it >> 2) & 1) ^ 1, abort, fault));
-                if (!ok) break;
-                const uint32_t bar = smem_u32(&m->full[s]);
-                if (elect_one()) {
-                    if (k < main) {
-                        mbar_arrive_expect_tx(bar, (uint32_t)(kTerms * n16 * 128));
-                        const uint32_t dst = x_base + s * (kTerms * x_bytes);
-                        const int col = (4 * c_lo + k) * 64;
-                        int r = 0;
-                        for (; r + 64 <= n16; r += 64) {
-                            tma_load_2d(dst + r * 128, &a.map_x64, col, cur.start + r, bar, pol);
-                            if constexpr (SPLIT) tma_load_2d(dst + x_bytes + r * 128, &a.map_lo64, col, cur.start + r, bar, pol);
-                        }
-                        for (; r < n16; r += 16) {
-                            tma_load_2d(dst + r * 128, &a.map_x16, col, cur.start + r, bar, pol);
-                            if constexpr (SPLIT) tma_load_2d(dst + x_bytes + r * 128, &a.map_lo16, col, cur.start + r, bar, pol);
-                        }
+        if (elect_one()) {
+            const uint64_t pol = l2_evict_normal_policy();
+            uint32_t it = 0;
+            bool ok = true;
+            for (int w = first; w < n_items && ok; w += step) {
+                const Item cur = t;
+                if (w + step < n_items) t = get_item(z, w + step);
+                const int box = box_of(z, cur.n);
+                const int2 ext = ext_range<SPLIT>(z, cur, rank);
+                const uint32_t bytes = kTerms * z.x_k * box_rows(z, box) * 128;
+                const int hi = 4 * (c_hi + (ext.y - ext.x + 3) / 4);
+#pragma unroll 1
+                for (int k = 4 * c_lo; k < hi; k += z.x_k, ++it) {
+                    const uint32_t s = it & x_mask, bar = smem_u32(&m->x_full[s]);
+                    ok = tc_wait(smem_u32(&m->x_empty[s]), ((it >> z.x_log) & 1) ^ 1, abort, fault);
+                    if (!ok) break;
+                    if (k < 4 * c_hi) {
+                        mbar_arrive_expect_tx(bar, bytes);
+                        tma_load_3d(x_base + s * x_slot, &a.map_x[box], 0, cur.start, k, bar, pol);
+                        if constexpr (SPLIT) tma_load_3d(x_base + s * x_slot + x_lo, &a.map_lo[box], 0, cur.start, k, bar, pol);
                     } else {
-                        mbar_arrive(bar);               // the decode warps fill this stage
+                        mbar_arrive(bar);                   // the decode warps fill an adapter chunk
                     }
                 }
             }
+            // copies in flight end before the block's memory is given back
+            for (uint32_t k = it > x_mask ? it - x_mask - 1 : 0; !ok && k < it; ++k)
+                for (int tries = 0; tries < 1 << 8 && !mbar_try_wait(smem_u32(&m->x_full[k & x_mask]), (k >> z.x_log) & 1); ++tries) {}
         }
-        // a copy in flight ends before the block's memory is given back (a slot whose stage never
-        // fills up runs into the limit)
-        for (uint32_t k = it > 4 ? it - 4 : 0; !ok && k < it; ++k)
-            for (int tries = 0; tries < 1 << 12 && !mbar_try_wait(smem_u32(&m->full[k & 3]), (k >> 2) & 1); ++tries) {}
+        __syncwarp();
     } else if (warp == kWarpMma) {
-        uint32_t it = 0, acc = 0;
-        bool ok = true;
-        const uint32_t half = SPLIT ? 2u * a.tile_n : (uint32_t)a.tmem_cols / 2;
-        const uint64_t desc_a = tc_desc_sw128(a_base), desc_x = tc_desc_sw128(x_base);
-        const uint32_t a_step = (kTerms * kABytes) >> 4, x_step = (uint32_t)(kTerms * x_bytes) >> 4;
-        for (int w = first; w < n_items && ok; w += step) {
-            const Item cur = t;
-            if (w + step < n_items) t = get_item(a, w + step);
-            const int n16 = round16(cur.n);
-            const uint32_t idesc = tc_idesc(n16, false), idesc_b = tc_idesc(n16, true);
-            const int2 ext = ext_range<SPLIT>(a, cur, rank);
-            const int main = 4 * (c_hi - c_lo), all = main + ext.y - ext.x;
-            for (int k = 0; k < all; ++k, ++it) {
-                const bool fresh = k == 0 || (SPLIT && ((k & 3) == 0 && k <= main));
-                if (fresh) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault));
+        if (elect_one()) {
+            // chunk number, token slot and its parity, number of the accumulator
+            uint32_t it = 0, xs = 0, xp = 0, acc = 0;
+            bool ok = true;
+            const uint64_t desc_x = tc_desc_sw128(x_base);
+            const uint32_t x_units = x_slot >> 4, lo_units = x_lo >> 4;
+            // the products of one quarter: 64 columns of weights, or the terms of u times an adapter quarter
+            auto quarter = [&](uint32_t d, uint32_t ta, uint64_t db, uint32_t idesc, bool add) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    tc_mma(d, ta + 8 * j, db + 2 * j, idesc, add || j);
+                    if constexpr (SPLIT) {
+                        tc_mma(d + z.tile_n, ta + 8 * j, db + lo_units + 2 * j, idesc, add || j);
+                        tc_mma(d + z.tile_n, ta + kSlotCols + 8 * j, db + 2 * j, idesc, true);
+                    }
+                }
+            };
+            auto next_x = [&]() {
+                tc_commit(smem_u32(&m->x_empty[xs]));
+                xs = (xs + 1) & x_mask;
+                xp ^= xs == 0;
+            };
+            for (int w = first; w < n_items && ok; w += step) {
+                const Item cur = t;
+                if (w + step < n_items) t = get_item(z, w + step);
+                const int n16 = round16(cur.n);
+                const uint32_t idesc = tc_idesc(n16, false);
+                const uint32_t kb_step = (uint32_t)(box_rows(z, box_of(z, cur.n)) * 128) >> 4;
+                const int2 ext = ext_range<SPLIT>(z, cur, rank);
+                bool add = false;                           // to the accumulator, or start it
+                for (int c = c_lo; c < c_hi; ++c, ++it) {
+                    if (!add && !(ok = tc_wait(smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault))) break;
+                    const uint32_t d = tmem + (acc & 1) * half;
+                    if (z.deep) {
+                        // two buffers of four quarters, a barrier each; the chunk's tokens are one stage or two
+                        const uint32_t buf = it & 1, ta = tmem + slots + buf * 4 * kSlotCols;
+                        ok = tc_wait(smem_u32(&m->full[buf]), (it >> 1) & 1, abort, fault) && tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault);
+                        if (!ok) break;
+                        tc_fence_after();
+                        uint64_t db = desc_x + (uint64_t)(xs * x_units);
+                        quarter(d, ta, db, idesc, add);
+                        quarter(d, ta + kSlotCols, db + kb_step, idesc, true);
+                        if (z.x_k == 2) {
+                            next_x();
+                            if (!(ok = tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault))) break;
+                            db = desc_x + (uint64_t)(xs * x_units);
+                        } else {
+                            db += 2 * kb_step;
+                        }
+                        quarter(d, ta + 2 * kSlotCols, db, idesc, true);
+                        quarter(d, ta + 3 * kSlotCols, db + kb_step, idesc, true);
+                        tc_commit(smem_u32(&m->empty[buf]));
+                        next_x();
+                    } else {
+                        // one buffer, a barrier a quarter
+                        uint64_t db = 0;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if ((q & (z.x_k - 1)) == 0) {
+                                ok = tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault);
+                                db = desc_x + (uint64_t)(xs * x_units);
+                            } else {
+                                db += kb_step;
+                            }
+                            ok = ok && tc_wait(smem_u32(&m->full[q]), it & 1, abort, fault);
+                            if (!ok) break;
+                            tc_fence_after();
+                            quarter(d, tmem + slots + q * kTerms * kSlotCols, db, idesc, add || q);
+                            tc_commit(smem_u32(&m->empty[q]));
+                            if ((q & (z.x_k - 1)) == z.x_k - 1) next_x();
+                        }
+                        if (!ok) break;
+                    }
+                    add = true;
+                    if (SPLIT || (c + 1 == c_hi && ext.x == ext.y)) {
+                        tc_commit(smem_u32(&m->acc_full[acc & 1]));
+                        ++acc;
+                        add = false;
+                    }
+                }
+                if (!ok || ext.x == ext.y) continue;
+                // adapter chunks
+                if (!add && !(ok = tc_wait(smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault))) continue;
+                const uint32_t d = tmem + (acc & 1) * half, idesc_b = tc_idesc(n16, true);
+                for (int e = ext.x; e < ext.y; e += 4, ++it) {
+                    const uint32_t buf = z.deep ? it & 1 : 0, par = z.deep ? (it >> 1) & 1 : it & 1;
+                    uint32_t ta = tmem + slots + buf * 4 * kSlotCols;
+                    uint64_t db = 0;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q, ta += kTerms * kSlotCols, db += kb_step) {
+                        if ((q & (z.x_k - 1)) == 0) {
+                            ok = tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault);
+                            db = desc_x + (uint64_t)(xs * x_units);
+                        }
+                        if (!z.deep || q == 0) ok = ok && tc_wait(smem_u32(&m->full[buf + q]), par, abort, fault);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (e + q < ext.y) {
+                            // the terms of u times the same columns of B
+                            constexpr int kPer = Ext<SPLIT>::kRanks / 16;
+#pragma unroll
+                            for (int j = 0; j < kPer * Ext<SPLIT>::kTerms; ++j)
+                                tc_mma(d, ta + 8 * (j % kPer), db + 2 * j, idesc_b, add || j);
+                            add = true;
+                        }
+                        if (!z.deep || q == 3) tc_commit(smem_u32(&m->empty[z.deep ? buf : q]));
+                        if ((q & (z.x_k - 1)) == z.x_k - 1) next_x();
+                    }
                     if (!ok) break;
                 }
-                const uint32_t s = it & 3;
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m->full[s]), (it >> 2) & 1, abort, fault));
-                if (!ok) break;
-                tc_fence_after();
-                const bool last = k == all - 1 || (SPLIT && k < main && (k & 3) == 3);
-                if (elect_one()) {
-                    const uint32_t d = tmem + (acc & 1) * half;
-                    const uint64_t da = desc_a + s * a_step, db = desc_x + s * x_step;
-                    if (k < main) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            tc_mma(d, da + 2 * j, db + 2 * j, idesc, !(fresh && j == 0));
-                            if constexpr (SPLIT) {
-                                tc_mma(d + a.tile_n, da + 2 * j, db + (x_bytes >> 4) + 2 * j, idesc, !(fresh && j == 0));
-                                tc_mma(d + a.tile_n, da + (kABytes >> 4) + 2 * j, db + 2 * j, idesc, true);
-                            }
-                        }
-                    } else {
-                        // the terms of u times the same columns of B
-                        constexpr int kPer = Ext<SPLIT>::kRanks / 16;
-#pragma unroll
-                        for (int j = 0; j < kPer * Ext<SPLIT>::kTerms; ++j)
-                            tc_mma(d, da + 2 * (j % kPer), db + 2 * j, idesc_b, !(fresh && j == 0));
-                    }
-                    tc_commit(smem_u32(&m->empty[s]));
-                    if (last) tc_commit(smem_u32(&m->acc_full[acc & 1]));
-                }
-                __syncwarp();
-                if (last) ++acc;
+                tc_commit(smem_u32(&m->acc_full[acc & 1]));
+                ++acc;
             }
+            // every product ends before TMEM is given back
+            tc_commit(smem_u32(&m->done));
+            for (int tries = 0; tries < 1 << 20 && !mbar_try_wait(smem_u32(&m->done), 0); ++tries) {}
         }
-        // every product ends before TMEM is given back
-        if (elect_one()) tc_commit(smem_u32(&m->done));
-        for (int tries = 0; tries < 1 << 20 && !mbar_try_wait(smem_u32(&m->done), 0); ++tries) {}
         __syncwarp();
     } else if (warp >= kEpiWarps) {
         const int g = (warp - kEpiWarps) >> 2, row = (warp & 3) * 32 + lane;
         constexpr int kUnit = FMT == 8 ? 64 : 32;           // quarter q begins within the 16-byte unit at q * kUnit bytes
-        const uint32_t src = raw_base + row * Fmt<FMT>::kChunk + g * kUnit;
-        uint32_t it = 0, s = 0, ph = 0;
+        const uint32_t src = raw_base + row * Fmt<FMT>::kChunk;
+        const uint32_t lane_base = tmem + slots + ((uint32_t)((warp & 3) * 32) << 16);
+        // raw slot and its parity, chunk number
+        uint32_t s = 0, ph = 0, it = 0;
         bool ok = true;
         for (int w = first; w < n_items && ok; w += step) {
             const Item cur = t;
-            if (w + step < n_items) t = get_item(a, w + step);
+            if (w + step < n_items) t = get_item(z, w + step);
             const float wscale = pow2(-cur.w_exp);
-            for (int c = c_lo; c < c_hi; ++c, it += 4) {
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m->raw_full[s]), ph, abort, fault));
+            for (int c = c_lo; c < c_hi; ++c, ++it) {
+                ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->raw_full[s]), ph, abort, fault));
                 if (!ok) break;
-                uint32_t v[2][4 * Fmt<FMT>::kVecs];         // quarters g and g + 2
-                uint32_t seen = 0;
+                uint32_t v[4 * Fmt<FMT>::kVecs], seen = 0;         // words 0 to 4 kVecs - 1, of which quarter g begins at g
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < Fmt<FMT>::kVecs; ++i) {
-                        ld_shared_volatile(src + s * kChunkBytes + 2 * h * kUnit + 16 * i, v[h] + 4 * i);
-                        seen |= v[h][4 * i];
-                    }
+                for (int i = 0; i < Fmt<FMT>::kVecs; ++i) {
+                    ld_shared_volatile(src + s * kChunkBytes + g * kUnit + 16 * i, v + 4 * i);
+                    seen |= v[4 * i];
+                }
                 // The buffer goes back to the copy engine once its values are here.  The arrival
                 // takes them as an operand (masked to nothing): an arrival alone does not wait for loads
                 // in flight, and overtakes them when the load unit is busy.
-                seen = __reduce_or_sync(0xffffffffu, seen & a.zero);
+                seen = __reduce_or_sync(0xffffffffu, seen & z.zero);
                 if (lane == 0) mbar_arrive_count(smem_u32(&m->raw_empty[s]), 1 + seen);
-                if (++s == (uint32_t)a.raw_slots) { s = 0; ph ^= 1; }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t k = it + g + 2 * h, slot = k & 3;
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m->empty[slot]), ((k >> 2) & 1) ^ 1, abort, fault));
-                    if (!ok) break;
-                    uint8_t *dst = smem + slot * (kTerms * kABytes);
-                    if (g == 0) decode_quarter<FMT, SPLIT, 0>(v[h] + 2 * h, wscale, dst, row);
-                    else decode_quarter<FMT, SPLIT, 1>(v[h] + 2 * h, wscale, dst, row);
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&m->full[slot]));
-                }
+                if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
+                const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
+                const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
+                ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault));
                 if (!ok) break;
+                tc_fence_after();
+                if (g == 0) decode_quarter<FMT, SPLIT, 0>(v, wscale, dst);
+                else if (g == 1) decode_quarter<FMT, SPLIT, 1>(v, wscale, dst);
+                else if (g == 2) decode_quarter<FMT, SPLIT, 2>(v, wscale, dst);
+                else decode_quarter<FMT, SPLIT, 3>(v, wscale, dst);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&m->full[bar]));
             }
             if (!ok || cur.count == 0) continue;
-            // adapter stages: group g takes every other one
-            const int2 ext = ext_range<SPLIT>(a, cur, rank);
-            const int32_t *list = a.tile_list + cur.start;
-            const int total = cur.count * a.rank;
-            const long long r = min((long long)cur.rt * kTileRows + row, a.rows - 1);
-            uint32_t b[2][16];
-            if (ext.x < ext.y) load_b<SPLIT>(a, list, total, (ext.x + g) * Ext<SPLIT>::kRanks, r, b[0]);
-            for (int e = ext.x + g; e < ext.y; e += 4) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int ee = e + 2 * h;
-                    if (ee >= ext.y) break;
-                    if (ee + 2 < ext.y) load_b<SPLIT>(a, list, total, (ee + 2) * Ext<SPLIT>::kRanks, r, b[h ^ 1]);
-                    const uint32_t k = it + (ee - ext.x), slot = k & 3;
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m->empty[slot]), ((k >> 2) & 1) ^ 1, abort, fault));
-                    if (!ok) break;
-                    uint8_t *line = smem + slot * (kTerms * kABytes) + row * 128;
-#pragma unroll
-                    for (int i = 0; i < Ext<SPLIT>::kRanks / 8; ++i)
-                        *reinterpret_cast<uint4 *>(line + ((i ^ (row & 7)) << 4)) =
-                            make_uint4(b[h][4 * i], b[h][4 * i + 1], b[h][4 * i + 2], b[h][4 * i + 3]);
-                    for (int x = row; x < round16(cur.n); x += kTileRows)
-                        store_u<SPLIT>(a, cur, ee * Ext<SPLIT>::kRanks, x, smem + a.off_x + slot * (kTerms * x_bytes));
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&m->full[slot]));
-                }
+            // adapter chunks: group g has their quarter g
+            const int2 ext = ext_range<SPLIT>(z, cur, rank);
+            const int32_t *list = z.tile_list + cur.start;
+            const int total = cur.count * z.rank;
+            const long long r = min((long long)cur.rt * kTileRows + row, z.rows - 1);
+            for (int e = ext.x + g; e < (ext.y - ext.x + 3) / 4 * 4 + ext.x; e += 4, ++it) {
+                const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
+                const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
+                uint32_t b[16] = {};
+                if (e < ext.y) load_b<SPLIT>(z, list, total, e * Ext<SPLIT>::kRanks, r, b);
+                // the token stage that quarter g of this chunk falls on
+                const uint32_t xi = (it * 4 + g) / z.x_k, sx = xi & x_mask;
+                ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) &&
+                                                 tc_wait(smem_u32(&m->x_empty[sx]), ((xi >> z.x_log) & 1) ^ 1, abort, fault));
                 if (!ok) break;
+                tc_fence_after();
+                if (e < ext.y) {
+                    tmem_st16(dst, b);
+                    uint8_t *x = smem + kOffX + sx * x_slot + (g & (z.x_k - 1)) * z.tile_n * 128;
+                    for (int c = row; c < round16(cur.n); c += kTileRows) store_u<SPLIT>(z, cur, e * Ext<SPLIT>::kRanks, c, x);
+                    fence_proxy_async_shared();
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&m->full[bar]));
             }
-            it += ext.y - ext.x;
         }
     } else {
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const int side = warp >> 2;                         // of the two warps of these rows
-        const uint32_t half = SPLIT ? 2u * a.tile_n : (uint32_t)a.tmem_cols / 2;
-        const uint32_t run = 4u * a.tile_n;                 // SPLIT: the running sums
-        float *red = reinterpret_cast<float *>(smem + a.off_red);
+        float *red = reinterpret_cast<float *>(smem + z.off_red);
         const uint32_t red_addr = smem_u32(red);
         const int my_row = (warp & 3) * 32 + lane;
         uint32_t acc = 0, item = 0;
@@ -533,83 +616,87 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tc_kernel(const __grid_con
             // the warps leave together, and the last tile's columns are read
             if (!named_barrier_and(1, 32 * kEpiWarps, ok)) break;
             const Item cur = t;
-            if (w + step < n_items) t = get_item(a, w + step);
+            if (w + step < n_items) t = get_item(z, w + step);
             const int n8 = round16(cur.n) / 8;
             const long long row = (long long)cur.rt * kTileRows + my_row;
-            if ((int)threadIdx.x < round16(cur.n)) {
-                const int j = threadIdx.x, at = cur.start + min(j, cur.n - 1);
-                const int e = cur.w_exp + (a.x_exp ? a.x_exp[at] : 0);
-                const bool bad = a.place && a.place[at] == -2;      // an adapter id out of range
-                m->slot[j] = a.order ? a.order[at] : at;
+            for (int j = threadIdx.x; j < round16(cur.n); j += 32 * kEpiWarps) {
+                const int at = cur.start + min(j, cur.n - 1);
+                const int e = cur.w_exp + (z.x_exp ? z.x_exp[at] : 0);
+                const bool bad = z.place && z.place[at] == -2;      // an adapter id out of range
+                m->slot[j] = z.order ? z.order[at] : at;
                 m->scale[j] = make_float2(bad ? __int_as_float(0x7fc00000) : pow2(e / 2), pow2(e - e / 2));
             }
             named_barrier(1, 32 * kEpiWarps);
-            // One group of 8 columns of the current accumulator; f32 adds the small products' and the
-            // running sums.
-            auto load8 = [&](uint32_t base, int g, bool cross, bool join, float (&v)[8]) {
-                tmem_ld8(base + 8 * g, v);
-                if constexpr (SPLIT) {
-                    float x[8], r[8];
-                    if (cross) tmem_ld8(base + a.tile_n + 8 * g, x);
-                    if (join) tmem_ld8(lane_base + run + 8 * g, r);
-                    tmem_wait_ld(v);
-                    if (cross) {
-                        tmem_wait_ld(x);
+            const int ks = z.ksplit;
+            uint32_t base = lane_base + run;                // where the tile's sums are
+            if constexpr (SPLIT) {
+                // Each chunk's sums (and the adapters') leave the accumulator for the running sums.
+                const int2 ext = ext_range<SPLIT>(z, cur, rank);
+                const int chunks = c_hi - c_lo, rounds = chunks + (ext.x < ext.y ? 1 : 0);
+                for (int i = 0; i < rounds; ++i, ++acc) {
+                    ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->acc_full[acc & 1]), (acc >> 1) & 1, abort, fault));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t from = lane_base + (acc & 1) * half;
+#pragma unroll 1
+                    for (int g = side; g < n8; g += kSides) {
+                        float v[8], x[8], r[8];
+                        tmem_ld8(from + 8 * g, v);
+                        if (i < chunks) tmem_ld8(from + z.tile_n + 8 * g, x);       // the small products
+                        if (i > 0) tmem_ld8(base + 8 * g, r);
+                        tmem_wait_ld(v);
+                        if (i < chunks) {
+                            tmem_wait_ld(x);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] += x[j];
-                    }
-                    if (join) {
-                        tmem_wait_ld(r);
+                            for (int j = 0; j < 8; ++j) v[j] += x[j];
+                        }
+                        if (i > 0) {
+                            tmem_wait_ld(r);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] += r[j];
+                            for (int j = 0; j < 8; ++j) v[j] += r[j];
+                        }
+                        tmem_st8(base + 8 * g, v);
                     }
-                } else {
-                    tmem_wait_ld(v);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&m->acc_empty[acc & 1]));
                 }
-            };
-            const int2 ext = ext_range<SPLIT>(a, cur, rank);
-            const int rounds = SPLIT ? c_hi - c_lo + (ext.x < ext.y ? 1 : 0) : 1;
-            const int ks = a.ksplit;
-            // the columns this warp sums: every other group, or (with a split) those it sends or finishes
-            for (int i = 0; i < rounds - 1 && ok; ++i, ++acc) {
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m->acc_full[acc & 1]), (acc >> 1) & 1, abort, fault));
-                if (!ok) break;
+                if (!ok) continue;
+            } else {
+                ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->acc_full[acc & 1]), (acc >> 1) & 1, abort, fault));
+                if (!ok) continue;
                 tc_fence_after();
-                for (int g = side; g < n8; g += 2) {
-                    float v[8];
-                    load8(lane_base + (acc & 1) * half, g, true, i > 0, v);
-                    tmem_st8(lane_base + run + 8 * g, v);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&m->acc_empty[acc & 1]));
+                base = lane_base + (acc & 1) * half;
             }
-            if (!ok) continue;
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m->acc_full[acc & 1]), (acc >> 1) & 1, abort, fault));
-            if (!ok) continue;
-            tc_fence_after();
-            const uint32_t base = lane_base + (acc & 1) * half;
-            const bool join = SPLIT && rounds > 1, cross = SPLIT && ext.x == ext.y;
             if (ks == 1) {
-                for (int g = side; g < n8; g += 2) {
-                    float v[8];
-                    load8(base, g, cross, join, v);
-                    finish8(a, m, 8 * g, cur.n, row, v);
+                // 8 columns at a time, the next ones on their way meanwhile
+                float v[8], next[8];
+                tmem_ld8(base + 8 * side, next);
+                tmem_wait_ld(next);
+#pragma unroll 1
+                for (int g = side; g < n8; g += kSides) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = next[j];
+                    if (g + kSides < n8) tmem_ld8(base + 8 * (g + kSides), next);
+                    finish<OT>(z, m, 8 * g, cur.n, row, v);
+                    tmem_wait_ld(next);
                 }
             } else {
                 // group g of 8 columns is finished by rank (g / 2) % ks, which receives the other ranks' sums
-                const int per = (a.tile_n / 16 + ks - 1) / ks * 2;
+                const int per = (z.tile_n / 16 + ks - 1) / ks * 2;
                 if (item > 0) {
                     ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&m->red_empty), (item - 1) & 1, abort, fault));
                     if (!ok) continue;
                 }
-                for (int g = side; g < n8; g += 2) {
+#pragma unroll 1
+                for (int g = side; g < n8; g += kSides) {
                     const int to = (g >> 1) % ks;
                     if (to == rank) continue;
                     float v[8];
-                    load8(base, g, cross, join, v);
-                    const int from = rank - (rank > to ? 1 : 0), at = (g >> 1) / ks * 2 + side;
+                    tmem_ld8(base + 8 * g, v);
+                    tmem_wait_ld(v);
+                    const int from = rank - (rank > to ? 1 : 0), at = (g >> 1) / ks * 2 + (g & 1);
                     const uint32_t dst = map_shared_rank(red_addr + (uint32_t)(((from * per + at) * 8 * kTileRows + my_row) * 4), (uint32_t)to);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) st_shared_cluster_f32(dst + j * (kTileRows * 4), v[j]);
@@ -618,10 +705,14 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tc_kernel(const __grid_con
                 if (lane < ks && lane != rank) mbar_arrive_remote(map_shared_rank(smem_u32(&m->red_full), (uint32_t)lane));
                 ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&m->red_full), item & 1, abort, fault));
                 if (!ok) continue;
-                for (int g = 2 * rank + side; g < n8; g += 2 * ks) {
+#pragma unroll 1
+                for (int g = side; g < n8; g += kSides) {
+                    if ((g >> 1) % ks != rank) continue;
                     float v[8], o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    load8(base, g, cross, join, v);
-                    const int at = (g >> 1) / ks * 2 + side;
+                    tmem_ld8(base + 8 * g, v);
+                    tmem_wait_ld(v);
+                    const int at = (g >> 1) / ks * 2 + (g & 1);
+#pragma unroll 1
                     for (int r = 0; r < ks; ++r) {
                         if (r == rank) {
 #pragma unroll
@@ -632,22 +723,24 @@ __global__ void __launch_bounds__(kThreads, 1) matmul_tc_kernel(const __grid_con
                             for (int j = 0; j < 8; ++j) o[j] += src[j * kTileRows];
                         }
                     }
-                    finish8(a, m, 8 * g, cur.n, row, o);
+                    finish<OT>(z, m, 8 * g, cur.n, row, o);
                 }
                 __syncwarp();
                 if (lane < ks && lane != rank) mbar_arrive_remote(map_shared_rank(smem_u32(&m->red_empty), (uint32_t)lane));
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&m->acc_empty[acc & 1]));
-            ++acc;
+            if constexpr (!SPLIT) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&m->acc_empty[acc & 1]));
+                ++acc;
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (a.ksplit > 1) cluster_sync();
-    if (warp == kWarpMma) tmem_dealloc(tmem, (uint32_t)a.tmem_cols);
+    if (z.ksplit > 1) cluster_sync();
+    if (warp == kWarpMma) tmem_dealloc(tmem, (uint32_t)z.tmem_cols);
 }
 
 // ------------------------------------------------------------------ prepare
@@ -1122,15 +1215,14 @@ hq_status launch(void (*kern)(P...), int grid, int threads, size_t smem, int clu
     return HQ_OK;
 }
 
-hq_status encode(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
-                 uint64_t stride, uint32_t box_inner, uint32_t box_outer, bool swizzle) {
+hq_status encode(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint32_t rank, const uint64_t *dims,
+                 const uint64_t *strides, const uint32_t *box, bool swizzle) {
     auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
     if (!enc) return set_error(HQ_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is unavailable");
-    cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {stride};
-    cuuint32_t box[2] = {box_inner, box_outer};
-    cuuint32_t estr[2] = {1, 1};
-    const CUresult r = enc(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    cuuint64_t d[3], s[2];
+    cuuint32_t b[3], one[3] = {1, 1, 1};
+    for (uint32_t i = 0; i < rank; ++i) { d[i] = dims[i]; b[i] = box[i]; if (i) s[i - 1] = strides[i - 1]; }
+    const CUresult r = enc(m, dt, rank, const_cast<void *>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return set_error(HQ_ERR_LAUNCH, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
@@ -1178,7 +1270,7 @@ Layout layout(const MatmulArgs &a) {
     return l;
 }
 
-struct TcPlan { int tile_n, ksplit, grid, raw_slots, tmem_cols; size_t smem; uint32_t off_x, off_raw, off_red, off_meta; };
+struct TcPlan { int tile_n, ksplit, grid, raw_slots, x_log, x_k, deep, tmem_cols; size_t smem; uint32_t off_raw, off_red; };
 
 // Memory of a launch with tiles of p->tile_n tokens and the columns split over p->ksplit CTAs; false if it does not fit.
 bool fit_smem(const DeviceInfo &dev, int fmt, bool split, TcPlan *p) {
@@ -1186,19 +1278,23 @@ bool fit_smem(const DeviceInfo &dev, int fmt, bool split, TcPlan *p) {
     const int chunk = (fmt == 8 ? Fmt<8>::kChunk : Fmt<4>::kChunk) * kTileRows;
     const int per = (p->tile_n / 16 + p->ksplit - 1) / p->ksplit * 2;
     const size_t red = p->ksplit > 1 ? (size_t)(p->ksplit - 1) * per * 8 * kTileRows * 4 : 0;
-    const size_t fixed = (size_t)kSlots * (kABytes + p->tile_n * 128) * terms + red + sizeof(Meta) + 128;
-    const size_t room = (size_t)dev.max_smem_optin;
-    if (fixed + chunk > room) return false;
-    p->raw_slots = (int)std::min<size_t>(kMaxRaw, (room - fixed) / chunk);
-    uint32_t at = (uint32_t)(kSlots * kABytes * terms);
-    p->off_x = at;
-    at += (uint32_t)(kSlots * p->tile_n * 128 * terms);
+    const size_t fixed = red + kOffX;
+    const size_t room = (size_t)dev.max_smem_optin, xb = (size_t)p->tile_n * 128 * terms;
+    // tokens: a chunk (256 columns) in flight at least, two where they fit, in stages as long as leave four slots;
+    // raw blocks take the rest
+    auto fits = [&](int raw, int columns) { return fixed + xb * columns + (size_t)raw * chunk <= room; };
+    if (!fits(1, 4)) return false;
+    int columns = fits(2, 8) ? 8 : 4;                       // in units of 64
+    p->raw_slots = 1;
+    while (p->raw_slots < kMaxRaw && fits(p->raw_slots + 1, columns)) ++p->raw_slots;
+    while (columns < 16 && fits(p->raw_slots, 2 * columns)) columns *= 2;
+    p->x_k = columns / 4;
+    p->x_log = 2;
+    uint32_t at = (uint32_t)(kOffX + xb * columns);
     p->off_raw = at;
     at += (uint32_t)(p->raw_slots * chunk);
     p->off_red = at;
-    at += (uint32_t)red;
-    p->off_meta = (at + 127) & ~127u;
-    p->smem = p->off_meta + sizeof(Meta);
+    p->smem = at + red;
     return true;
 }
 
@@ -1228,8 +1324,11 @@ bool make_plan(const DeviceInfo &dev, int fmt, bool split, int64_t groups, int64
         }
     }
     if (!any) return false;
+    // TMEM: two buffers of accumulators (f32: of both kinds, and the running sums), and one or two buffers of decoded chunks
+    const int sums = best->tile_n * (split ? 5 : 2), slots = 4 * kSlotCols * (split ? 2 : 1);
+    best->deep = sums + 2 * slots <= 512 && best->x_k > 1;
     best->tmem_cols = 32;
-    while (best->tmem_cols < best->tile_n * (split ? 5 : 2)) best->tmem_cols *= 2;
+    while (best->tmem_cols < sums + slots * (best->deep ? 2 : 1)) best->tmem_cols *= 2;
     best->grid = dev.num_sms / best->ksplit * best->ksplit;
     return true;
 }
@@ -1247,11 +1346,20 @@ hq_status configure(int dynamic) {
     return HQ_OK;
 }
 
-template <int FMT, bool SPLIT>
+template <int FMT, bool SPLIT, int OT>
 hq_status launch_tc(const TcArgs &t, const TcPlan &p, cudaStream_t stream) {
-    auto kern = matmul_tc_kernel<FMT, SPLIT>;
-    hq_status st = configure<matmul_tc_kernel<FMT, SPLIT>>(232448);
-    return st != HQ_OK ? st : launch(kern, p.grid, kThreads, p.smem, p.ksplit, stream, "matmul", t);
+    hq_status st = configure<matmul_tc_kernel<FMT, SPLIT, OT>>(232448);
+    return st != HQ_OK ? st : launch(matmul_tc_kernel<FMT, SPLIT, OT>, p.grid, Roles<SPLIT>::kThreads, p.smem, p.ksplit, stream, "matmul", t);
+}
+
+template <int FMT>
+hq_status launch_tc(const TcArgs &t, const TcPlan &p, bool split, int out, cudaStream_t stream) {
+    if (split) return launch_tc<FMT, true, HQ_DT_F32>(t, p, stream);
+    if (out == HQ_DT_F32) {                                 // the sums that the combine kernel takes
+        if constexpr (FMT == 8) return launch_tc<FMT, false, HQ_DT_F32>(t, p, stream);
+        return set_error(HQ_ERR_UNSUPPORTED, "f32 sums of 16-bit tokens are grouped products'");
+    }
+    return out == HQ_DT_F16 ? launch_tc<FMT, false, HQ_DT_F16>(t, p, stream) : launch_tc<FMT, false, HQ_DT_BF16>(t, p, stream);
 }
 
 }  // namespace
@@ -1348,52 +1456,55 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
     }
 
     TcArgs t = {};
-    st = encode(&t.map_w, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.W, (uint64_t)n_chunks * chunk / 2, (uint64_t)(a.n_mats * a.rows),
-                (uint64_t)n_chunks * chunk, (uint32_t)chunk / 2, kTileRows, false);
+    const uint64_t w_dims[2] = {(uint64_t)n_chunks * chunk / 2, (uint64_t)(a.n_mats * a.rows)}, w_stride = (uint64_t)n_chunks * chunk;
+    const uint32_t w_box[2] = {(uint32_t)chunk / 2, kTileRows};
+    st = encode(&t.map_w, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.W, 2, w_dims, &w_stride, w_box, false);
     const void *xh = pack ? (const void *)(ws + l.hi) : a.x;
-    auto encode_x = [&](CUtensorMap *m, const void *base, uint32_t box) {
-        if (st == HQ_OK)
-            st = encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, (uint64_t)a.cols, (uint64_t)slots, (uint64_t)a.cols * 2, 64, box, true);
+    // the tokens as [64 columns][tokens][groups of 64 columns]: a box is a stage, laid out as its operands are
+    auto encode_x = [&](CUtensorMap *m, const void *base, uint32_t rows) {
+        const uint64_t dims[3] = {64, (uint64_t)slots, (uint64_t)a.cols / 64}, strides[2] = {(uint64_t)a.cols * 2, 128};
+        const uint32_t box[3] = {64, rows, (uint32_t)p.x_k};
+        if (st == HQ_OK) st = encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 3, dims, strides, box, true);
     };
-    encode_x(&t.map_x64, xh, 64);
-    encode_x(&t.map_x16, xh, 16);
-    if (split) {
-        encode_x(&t.map_lo64, ws + l.lo, 64);
-        encode_x(&t.map_lo16, ws + l.lo, 16);
+    for (int b = a.moe ? 0 : kBoxes - 1; b < kBoxes; ++b) {
+        const uint32_t rows = b == kBoxes - 1 ? (uint32_t)p.tile_n : 16u << b;
+        if (rows > (uint32_t)p.tile_n) continue;
+        encode_x(&t.map_x[b], xh, rows);
+        if (split) encode_x(&t.map_lo[b], ws + l.lo, rows);
     }
     if (st != HQ_OK) return st;
-    t.w_exp = a.w_exp;
-    t.x_exp = q.x_exp;
-    t.order = q.order;
-    t.tiles = q.tiles;
-    t.n_tiles = q.n_tiles;
-    t.tile_count = q.tile_count;
-    t.tile_list = q.tile_list;
-    t.place = q.place;
-    t.B = a.B;
-    t.u = q.u;
-    t.rank = a.rank;
-    t.y = a.moe ? q.y : a.y;
-    t.fault = dev->fault;
-    t.rows = a.rows;
-    t.n_tokens = (int)a.n_tokens;
-    t.n_tt = (int)((a.n_tokens + p.tile_n - 1) / p.tile_n);
-    t.n_rt = (int)n_rt;
-    t.n_items = (int)((a.moe ? most_tiles(a) : t.n_tt) * n_rt);
-    t.n_chunks = n_chunks;
-    t.tile_n = p.tile_n;
-    t.raw_slots = p.raw_slots;
-    t.ksplit = p.ksplit;
-    t.tmem_cols = p.tmem_cols;
-    t.dtype = a.epilogue == HQ_MOE_EPI_COMBINE ? HQ_DT_F32 : a.dtype;
-    t.epilogue = a.epilogue == HQ_MOE_EPI_SWIGLU ? HQ_MOE_EPI_SWIGLU : 0;
-    t.stream_w = !a.moe && t.n_tt == 1;
-    t.off_x = p.off_x;
-    t.off_raw = p.off_raw;
-    t.off_red = p.off_red;
-    t.off_meta = p.off_meta;
-    st = a.fmt == 8 ? (split ? launch_tc<8, true>(t, p, stream) : launch_tc<8, false>(t, p, stream))
-                    : (split ? launch_tc<4, true>(t, p, stream) : launch_tc<4, false>(t, p, stream));
+    t.z.w_exp = a.w_exp;
+    t.z.x_exp = q.x_exp;
+    t.z.order = q.order;
+    t.z.tiles = q.tiles;
+    t.z.n_tiles = q.n_tiles;
+    t.z.tile_count = q.tile_count;
+    t.z.tile_list = q.tile_list;
+    t.z.place = q.place;
+    t.z.B = a.B;
+    t.z.u = q.u;
+    t.z.rank = a.rank;
+    t.z.y = a.moe ? q.y : a.y;
+    t.z.fault = dev->fault;
+    t.z.rows = a.rows;
+    t.z.n_tokens = (int)a.n_tokens;
+    t.z.n_tt = (int)((a.n_tokens + p.tile_n - 1) / p.tile_n);
+    t.z.n_rt = (int)n_rt;
+    t.z.n_items = (int)((a.moe ? most_tiles(a) : t.z.n_tt) * n_rt);
+    t.z.n_chunks = n_chunks;
+    t.z.tile_n = p.tile_n;
+    t.z.raw_slots = p.raw_slots;
+    t.z.x_log = p.x_log;
+    t.z.x_k = p.x_k;
+    t.z.deep = p.deep;
+    t.z.ksplit = p.ksplit;
+    t.z.tmem_cols = p.tmem_cols;
+    t.z.epilogue = a.epilogue == HQ_MOE_EPI_SWIGLU ? HQ_MOE_EPI_SWIGLU : 0;
+    t.z.stream_w = !a.moe && t.z.n_tt == 1;
+    t.z.off_raw = p.off_raw;
+    t.z.off_red = p.off_red;
+    const int out = a.epilogue == HQ_MOE_EPI_COMBINE ? HQ_DT_F32 : a.dtype;
+    st = a.fmt == 8 ? launch_tc<8>(t, p, split, out, stream) : launch_tc<4>(t, p, split, out, stream);
     if (st != HQ_OK) return st;
     if (a.epilogue == HQ_MOE_EPI_COMBINE) {
         const bool four = a.rows % 4 == 0;

@@ -1,5 +1,5 @@
 // hq_tc.cuh -- sm_103a tensor-core primitives: tcgen05 allocation, products
-// with operands in shared memory, and accumulator loads.
+// with one operand in TMEM and one in shared memory, TMEM loads and stores.
 // Inline PTX only.
 #pragma once
 
@@ -19,12 +19,28 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// D[128][N] (+)= A[128][16] B[N][16]^T, 16-bit floats in shared memory, fp32 in TMEM.
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// Bounded wait on phase `parity` of an mbarrier, small in code: the thread sleeps in hardware for up to 20 us a
+// try, and gives up after 2^17 tries (seconds at the full sleep), or as soon as another wait of the block has.
+// `abort` is the block's; the fault word gets the time-out.
+__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *fault) {
+#pragma unroll 1
+    for (uint32_t tries = 0; !mbar_try_wait_sleep(bar, parity, 20000u); ++tries) {
+        if (*abort) return false;
+        if (tries >> 17) {
+            atomicCAS(fault, 0u, ((blockIdx.x & 0x7fffffu) << 9) | kFaultWaitTimeout);
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// D[128][N] (+)= A[128][16] B[N][16]^T: 16-bit floats, A in TMEM (8 columns of pairs), B in shared memory, fp32 in TMEM.
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
 }
 
 // Arrives on `bar` once every product this thread has issued so far is done.
@@ -65,6 +81,12 @@ __device__ __forceinline__ void tmem_wait_ld(float (&v)[8]) {
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
                  :: "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+                 ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+                   "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr) : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // One thread of a converged warp, the same one every time.
@@ -72,6 +94,14 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t one;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
     return one != 0;
+}
+
+// 3-D tiled tensor load into this CTA's shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy) : "memory");
 }
 
 __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
