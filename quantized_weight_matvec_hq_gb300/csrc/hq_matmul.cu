@@ -19,15 +19,19 @@
 //  * Few tiles: a cluster splits the columns and joins its partial sums in a
 //    fixed order through distributed shared memory.
 //
-// Numbers.  Decoded weights are d 2^-e q rounded to f16 (11 bits; e per matrix,
-// so that the range of f16 fits the matrix), where bf16 would keep 8.  Tokens of
+// Numbers.  A decoded weight is d q rounded to f16 (11 bits, where bf16 would keep 8), scaled by a power of two per
+// matrix so that its largest weight is just below 1/2: weights below 2^-13 of that are rounded to
+// multiples of 2^-24 of it.  (That range is what a decode with one multiply-add for two weights takes: the quant is a
+// subnormal f16.)  Tokens of
 // bf16 become f16 exactly, scaled by a power of two per token (what lies 2^-29 below a
 // token's largest element is rounded to 2^-39 of it).  f32 tokens and weights are two
-// f16 terms each (22 bits) and three products; sums of 256 columns leave the
+// f16 terms each (22 bits, weights scaled to just below 2^14) and three products; sums of 256 columns leave the
 // tensor core, whose adds may truncate, and are added in fp32 to the running
 // sum, with the two small products in an accumulator of their own.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+
+#include <stddef.h>
 
 #include <algorithm>
 #include <atomic>
@@ -84,7 +88,6 @@ struct Sizes {
     int n_tokens, n_tt, n_items, n_rt, n_chunks;
     int tile_n, raw_slots, x_log, x_k, deep, ksplit, tmem_cols;   // 2^x_log slots of x_k (1, 2 or 4) times 64 columns of tokens
     int epilogue, rank, stream_w;
-    uint32_t zero;                  // 0, unknown to the compiler
     uint32_t off_raw, off_red;
 };
 
@@ -95,39 +98,57 @@ struct TcArgs {
 
 struct Meta {
     uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw], x_full[kMaxX], x_empty[kMaxX], full[4], empty[4];
-    uint64_t acc_full[2], acc_empty[2], red_full, red_empty, done;
+    uint64_t acc_full[2], acc_empty[2], columns, red_full, red_empty, done;
     uint32_t tmem;
-    int abort;
-    int slot[kMaxTokens];
-    float2 scale[kMaxTokens];
+    int abort, wide;                // wide: number of the last item with a column whose scale is no float
+    // of a tile's columns: output slot, scale (a power of two; NaN for a bad adapter id), its exponent, the adapter's place
+    alignas(16) int slot[kMaxTokens];
+    alignas(16) float scale[kMaxTokens];
+    int list[kMaxTokens];           // the tile's adapters
+    int16_t e[kMaxTokens], place[kMaxTokens];
 };
 
 constexpr int kOffX = 4096;                 // shared memory: the barriers and a tile's columns, tokens, raw blocks, joined sums
-static_assert(sizeof(Meta) <= kOffX, "the head of shared memory");
+static_assert(sizeof(Meta) <= kOffX && offsetof(Meta, slot) % 16 == 0 && offsetof(Meta, scale) % 16 == 0,
+              "the head of shared memory, read 16 bytes at a time");
 
 struct Item { int mat, rt, start, n, w_exp, count; };
 
-// Work item `w`: a tile of rows and a tile of tokens.  Grouped: an expert's row tiles follow one another, so
-// that its weights are read again from L2 if it has several tiles of tokens; one matrix: a row tile's token
-// tiles follow one another.
-__device__ __forceinline__ Item get_item(const Sizes &a, int w) {
+// Work items, tiles of rows times tiles of tokens, in the order a CTA takes every step-th of.  Grouped: an expert's row
+// tiles follow one another (inner), so that its weights are read again from L2 if it has several tiles of tokens; one
+// matrix: a row tile's token tiles follow one another.
+struct Cursor {
+    int outer, inner;
+    __device__ __forceinline__ void next(const Sizes &a, const Cursor &step) {
+        const int count = a.tiles ? a.n_rt : a.n_tt;
+        outer += step.outer;
+        inner += step.inner;
+        if (inner >= count) { inner -= count; ++outer; }
+    }
+};
+
+__device__ __forceinline__ Cursor cursor_at(const Sizes &a, int w) {
+    const int count = a.tiles ? a.n_rt : a.n_tt;
+    return Cursor{w / count, w % count};
+}
+
+__device__ __forceinline__ Item get_item(const Sizes &a, const Cursor &c) {
     Item t;
     if (a.tiles) {
-        const TileRec r = a.tiles[w / a.n_rt];
-        t.rt = w % a.n_rt;
+        const TileRec r = a.tiles[c.outer];
+        t.rt = c.inner;
         t.mat = r.mat;
         t.start = r.start;
         t.n = r.n;
         t.w_exp = r.w_exp;
         t.count = 0;
     } else {
-        const int tt = w % a.n_tt;
         t.mat = 0;
-        t.rt = w / a.n_tt;
-        t.start = tt * a.tile_n;
+        t.rt = c.outer;
+        t.start = c.inner * a.tile_n;
         t.n = min(a.tile_n, a.n_tokens - t.start);
         t.w_exp = *a.w_exp;
-        t.count = a.tile_count ? a.tile_count[tt] : 0;
+        t.count = a.tile_count ? a.tile_count[c.inner] : 0;
     }
     return t;
 }
@@ -159,36 +180,42 @@ __device__ __forceinline__ void ld_shared_volatile(uint32_t addr, uint32_t *v) {
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
 
-// Two blocks (64 columns) of one row: `w` holds the quarter's 16-byte units,
-// block 0 starts at word I0.  The bytes q + 128 (Q8_0) or n (Q4_0) go into the
-// mantissa of 1024, whose integers f16 holds exactly; 1024 + bias is subtracted
-// exactly, and the product with the scaled d is rounded once.
+// Two blocks (64 columns) of one row to TMEM: `w` holds the 16-byte units that the quarter touches, block 0 begins at
+// word I0.  The byte u = q + 128 (Q8_0) in the low bits of a half is the subnormal u 2^-24, and
+// one multiply-add gives u 2^-24 (d 2^24) - 128 d, rounded once: both factors and the offset are exact.  Q4_0: the byte
+// 16 n, n 2^-20 (d 2^20) - 8 d; d 2^24 or d 2^20 is then below 2^16 (d: scaled as the weights are).
+// f32: the byte goes into the mantissa of 1024 instead, 1024 + bias is subtracted exactly, and the product with d is
+// rounded to f16 and its rest, which a multiply-add gives exactly.
 template <int FMT, bool SPLIT, int I0>
 __device__ __forceinline__ void decode_quarter(const uint32_t *w, float wscale, uint32_t dst) {
+    constexpr int kWords = FMT == 8 ? 8 : 4;
     const __half2 bias = FMT == 8 ? __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480))    // 1152
                                   : __half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));   // 1032
-    constexpr int kWords = FMT == 8 ? 8 : 4;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         const uint32_t dw = b == 0 ? w[I0] & 0xffffu : w[I0 + kWords] >> 16;
-        const __half ds = __float2half_rn(__half2float(__ushort_as_half((unsigned short)dw)) * wscale);
-        const __half2 d = __half2half2(ds);
+        const float df = __half2float(__ushort_as_half((unsigned short)dw)) * wscale;
+        const __half2 d = __half2half2(__float2half_rn(SPLIT ? df : df * (FMT == 8 ? 16777216.f : 1048576.f)));
+        const __half2 off = __half2half2(__float2half_rn(df * (FMT == 8 ? -128.f : -8.f)));
         uint32_t hi[16], lo[SPLIT ? 16 : 1];                // pairs of columns
 #pragma unroll
         for (int h = 0; h < 8; ++h) {                       // four columns
             const int j = FMT == 8 ? h : h & 3;
             uint32_t v = b == 0 ? __funnelshift_r(w[I0 + j], w[I0 + j + 1], 16) : w[I0 + kWords + 1 + j];
             if constexpr (FMT == 8) v ^= 0x80808080u;
-            else v = (h < 4 ? v : v >> 4) & 0x0f0f0f0fu;
+            else if constexpr (SPLIT) v = (h < 4 ? v : v >> 4) & 0x0f0f0f0fu;
+            else v = (h < 4 ? v << 4 : v) & 0xf0f0f0f0u;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const uint32_t m = prmt(v, 0x64646464u, p ? 0x4342u : 0x4140u);
-                const __half2 n = __hsub2(*reinterpret_cast<const __half2 *>(&m), bias);
-                const __half2 r = __hmul2(n, d);
-                hi[2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
+                const uint32_t u = prmt(v, SPLIT ? 0x64646464u : 0u, p ? 0x4342u : 0x4140u);
+                const __half2 n = *reinterpret_cast<const __half2 *>(&u);
                 if constexpr (SPLIT) {
-                    const __half2 l = __hfma2(n, d, __hneg2(r));
+                    const __half2 s = __hsub2(n, bias), r = __hmul2(s, d), l = __hfma2(s, d, __hneg2(r));
+                    hi[2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
                     lo[2 * h + p] = *reinterpret_cast<const uint32_t *>(&l);
+                } else {
+                    const __half2 r = __hfma2(n, d, off);
+                    hi[2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
                 }
             }
         }
@@ -196,6 +223,9 @@ __device__ __forceinline__ void decode_quarter(const uint32_t *w, float wscale, 
         if constexpr (SPLIT) tmem_st16(dst + kSlotCols + 16 * b, lo);
     }
 }
+
+// The exponent that scales a matrix's decoded weights (see above), from the one kept beside it.
+template <bool SPLIT> __device__ __forceinline__ int decode_exp(int w_exp) { return SPLIT ? w_exp : w_exp + 15; }
 
 // ------------------------------------------------------------------ outputs
 
@@ -215,31 +245,40 @@ __device__ __forceinline__ void store_out(void *y, long long i, float v) {
     else static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
 }
 
-// The W columns from c0 of output row `row` (its sums in v): scales, SwiGLU with the neighbouring lane's row, store.
-template <int OT, int W>
-__device__ __forceinline__ void finish(const Sizes &a, const Meta *m, int c0, int n, long long row, float (&v)[W]) {
+// The 8 columns from c0 of output row `row` (its sums in v): scales, SwiGLU with the neighbouring lane's row, store.
+template <int OT>
+__device__ __forceinline__ void finish(const Sizes &a, const Meta *m, bool wide, int c0, int n, long long row, float (&v)[8]) {
+    const float4 *sp = reinterpret_cast<const float4 *>(m->scale + c0);
+    const int4 *op = reinterpret_cast<const int4 *>(m->slot + c0);
+    const float4 s0 = sp[0], s1 = sp[1];
+    const int4 o0 = op[0], o1 = op[1];
+    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    const int slot[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        const float2 s = m->scale[c0 + j];
-        v[j] = v[j] * s.x * s.y;
+    for (int j = 0; j < 8; ++j) v[j] *= s[j];
+    if (wide) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = m->e[c0 + j];
+            v[j] *= pow2(e - max(-126, min(127, e)));
+        }
     }
     if (a.epilogue == HQ_MOE_EPI_SWIGLU) {
         // even lanes hold gate rows, odd lanes up rows: each finishes every other token
         const bool odd = threadIdx.x & 1;
         const long long half = a.rows / 2, i = row / 2;
 #pragma unroll
-        for (int j = 0; j < W; j += 2) {
+        for (int j = 0; j < 8; j += 2) {
             const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
             const float h = silu(odd ? got : v[j]) * (odd ? v[j + 1] : got);
-            const int c = c0 + j + (odd ? 1 : 0);
-            if (c < n && row < a.rows) store_out<OT>(a.y, m->slot[c] * half + i, h);
+            if (c0 + j + (odd ? 1 : 0) < n && row < a.rows) store_out<OT>(a.y, (odd ? slot[j + 1] : slot[j]) * half + i, h);
         }
         return;
     }
     if (row < a.rows) {
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            if (c0 + j < n) store_out<OT>(a.y, m->slot[c0 + j] * a.rows + row, v[j]);
+        for (int j = 0; j < 8; ++j)
+            if (c0 + j < n) store_out<OT>(a.y, slot[j] * a.rows + row, v[j]);
     }
 }
 
@@ -247,7 +286,7 @@ __device__ __forceinline__ void finish(const Sizes &a, const Meta *m, int c0, in
 
 // Virtual ranks [v0, v0 + kRanks) of one row of the tile's adapters' B, packed in pairs.
 template <bool SPLIT>
-__device__ __forceinline__ void load_b(const Sizes &a, const int32_t *list, int total, int v0, long long row, uint32_t (&b)[16]) {
+__device__ __forceinline__ void load_b(const Sizes &a, const int *list, int total, int v0, long long row, uint32_t (&b)[16]) {
     constexpr int R = Ext<SPLIT>::kRanks;
     if ((a.rank & 7) == 0) {
 #pragma unroll
@@ -279,17 +318,13 @@ __device__ __forceinline__ void load_b(const Sizes &a, const int32_t *list, int 
 
 // Row `c` of the token operand: u of the token's own adapter at its virtual ranks, as bf16 terms side by side, zero elsewhere.
 template <bool SPLIT>
-__device__ __forceinline__ void store_u(const Sizes &a, const Item &t, int v0, int c, uint8_t *dst) {
+__device__ __forceinline__ void store_u(const Sizes &a, const Meta *m, const Item &t, int v0, int c, uint8_t *dst) {
     constexpr int R = Ext<SPLIT>::kRanks, T = Ext<SPLIT>::kTerms;
-    const int place = c < t.n ? a.place[t.start + c] : -1;
+    const int place = c < t.n ? m->place[c] : -1;
     const int lo = place * a.rank - v0;                     // virtual rank v0 + k is rank k - lo of the adapter
     const bool any = place >= 0 && lo < R && lo + a.rank > 0;
-    float s1 = 0.f, s2 = 0.f;
-    if (any) {
-        const int e = -(t.w_exp + (a.x_exp ? a.x_exp[t.start + c] : 0));
-        s1 = pow2(e / 2);
-        s2 = pow2(e - e / 2);
-    }
+    const int e = -m->e[c];
+    const float s1 = pow2(e / 2), s2 = pow2(e - e / 2);
     uint8_t *line = dst + c * 128;
     const float *u = a.u + (long long)(t.start + c) * a.rank;
 #pragma unroll
@@ -337,7 +372,9 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         for (int i = 0; i < 1 << z.x_log; ++i) { mbar_init(smem_u32(&m->x_full[i]), 1); mbar_init(smem_u32(&m->x_empty[i]), 1); }
         for (int i = 0; i < 4; ++i) { mbar_init(smem_u32(&m->full[i]), z.deep ? kDecodeWarps : 4); mbar_init(smem_u32(&m->empty[i]), 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&m->acc_full[i]), 1); mbar_init(smem_u32(&m->acc_empty[i]), kEpiWarps); }
+        m->wide = 0;
         mbar_init(smem_u32(&m->done), 1);
+        mbar_init(smem_u32(&m->columns), 1);
         mbar_init(smem_u32(&m->red_full), (uint32_t)max(1, (z.ksplit - 1) * kEpiWarps));
         mbar_init(smem_u32(&m->red_empty), (uint32_t)max(1, (z.ksplit - 1) * kEpiWarps));
         fence_mbar_init();
@@ -354,10 +391,12 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     const int first = blockIdx.x / z.ksplit, step = gridDim.x / z.ksplit;
     const int c_lo = (int)((long long)z.n_chunks * rank / z.ksplit);
     const int c_hi = (int)((long long)z.n_chunks * (rank + 1) / z.ksplit);
+    const Cursor stride = cursor_at(z, step);
+    Cursor at = cursor_at(z, min(first, z.n_items - 1));
     // one matrix's weights may be fetched before the prepare kernel is done; everything else waits for it
     if (z.tiles || warp != kWarpW) griddep_wait();
     Item t = {};
-    if (z.tiles || warp != kWarpW) t = get_item(z, min(first, z.n_items - 1));
+    if (z.tiles || warp != kWarpW) t = get_item(z, at);
     const int n_items = z.tiles ? *z.n_tiles * z.n_rt : z.n_items;
 
     if (warp == kWarpW) {
@@ -366,8 +405,9 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             uint32_t s = 0, ph = 1, it = 0;
             bool ok = true;
             for (int w = first; w < n_items && ok; w += step) {
-                const int row0 = z.tiles ? (int)((long long)t.mat * z.rows + (long long)t.rt * kTileRows) : w / z.n_tt * kTileRows;
-                if (z.tiles && w + step < n_items) t = get_item(z, w + step);
+                const int row0 = z.tiles ? (int)((long long)t.mat * z.rows + (long long)t.rt * kTileRows) : at.outer * kTileRows;
+                at.next(z, stride);
+                if (z.tiles && w + step < n_items) t = get_item(z, at);
                 for (int c = c_lo; c < c_hi; ++c, ++it) {
                     // past the first slots the wait is for this kernel's own warps, which wait for the prepare kernel
                     if (!z.tiles && it == (uint32_t)z.raw_slots) griddep_wait();
@@ -391,7 +431,8 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             bool ok = true;
             for (int w = first; w < n_items && ok; w += step) {
                 const Item cur = t;
-                if (w + step < n_items) t = get_item(z, w + step);
+                at.next(z, stride);
+            if (w + step < n_items) t = get_item(z, at);
                 const int box = box_of(z, cur.n);
                 const int2 ext = ext_range<SPLIT>(z, cur, rank);
                 const uint32_t bytes = kTerms * z.x_k * box_rows(z, box) * 128;
@@ -440,7 +481,8 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             };
             for (int w = first; w < n_items && ok; w += step) {
                 const Item cur = t;
-                if (w + step < n_items) t = get_item(z, w + step);
+                at.next(z, stride);
+            if (w + step < n_items) t = get_item(z, at);
                 const int n16 = round16(cur.n);
                 const uint32_t idesc = tc_idesc(n16, false);
                 const uint32_t kb_step = (uint32_t)(box_rows(z, box_of(z, cur.n)) * 128) >> 4;
@@ -539,32 +581,25 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         constexpr int kUnit = FMT == 8 ? 64 : 32;           // quarter q begins within the 16-byte unit at q * kUnit bytes
         const uint32_t src = raw_base + row * Fmt<FMT>::kChunk;
         const uint32_t lane_base = tmem + slots + ((uint32_t)((warp & 3) * 32) << 16);
-        // raw slot and its parity, chunk number
-        uint32_t s = 0, ph = 0, it = 0;
+        // raw slot and its parity, chunk number, item number
+        uint32_t s = 0, ph = 0, it = 0, item = ~0u;
         bool ok = true;
         for (int w = first; w < n_items && ok; w += step) {
+            ++item;
             const Item cur = t;
-            if (w + step < n_items) t = get_item(z, w + step);
-            const float wscale = pow2(-cur.w_exp);
+            at.next(z, stride);
+            if (w + step < n_items) t = get_item(z, at);
+            const float wscale = pow2(-decode_exp<SPLIT>(cur.w_exp));
             for (int c = c_lo; c < c_hi; ++c, ++it) {
-                ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->raw_full[s]), ph, abort, fault));
-                if (!ok) break;
-                uint32_t v[4 * Fmt<FMT>::kVecs], seen = 0;         // words 0 to 4 kVecs - 1, of which quarter g begins at g
+                ok = tc_wait(smem_u32(&m->raw_full[s]), ph, abort, fault);
+                uint32_t v[4 * Fmt<FMT>::kVecs];            // words 0 to 4 kVecs - 1, of which quarter g begins at g
 #pragma unroll
-                for (int i = 0; i < Fmt<FMT>::kVecs; ++i) {
+                for (int i = 0; i < Fmt<FMT>::kVecs; ++i)
                     ld_shared_volatile(src + s * kChunkBytes + g * kUnit + 16 * i, v + 4 * i);
-                    seen |= v[4 * i];
-                }
-                // The buffer goes back to the copy engine once its values are here.  The arrival
-                // takes them as an operand (masked to nothing): an arrival alone does not wait for loads
-                // in flight, and overtakes them when the load unit is busy.
-                seen = __reduce_or_sync(0xffffffffu, seen & z.zero);
-                if (lane == 0) mbar_arrive_count(smem_u32(&m->raw_empty[s]), 1 + seen);
-                if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
                 const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
                 const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
-                ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault));
-                if (!ok) break;
+                ok = ok && tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 tc_fence_after();
                 if (g == 0) decode_quarter<FMT, SPLIT, 0>(v, wscale, dst);
                 else if (g == 1) decode_quarter<FMT, SPLIT, 1>(v, wscale, dst);
@@ -573,19 +608,26 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&m->full[bar]));
+                // Only now, with every value decoded, does the raw buffer go back to the copy engine: an arrival does
+                // not wait for loads in flight, and overtakes them when the load unit is busy.
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&m->full[bar]));
+                    mbar_arrive(smem_u32(&m->raw_empty[s]));
+                }
+                if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
             }
             if (!ok || cur.count == 0) continue;
             // adapter chunks: group g has their quarter g
             const int2 ext = ext_range<SPLIT>(z, cur, rank);
-            const int32_t *list = z.tile_list + cur.start;
+            ok = tc_wait(smem_u32(&m->columns), item & 1, abort, fault);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; continue; }
             const int total = cur.count * z.rank;
             const long long r = min((long long)cur.rt * kTileRows + row, z.rows - 1);
             for (int e = ext.x + g; e < (ext.y - ext.x + 3) / 4 * 4 + ext.x; e += 4, ++it) {
                 const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
                 const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
                 uint32_t b[16] = {};
-                if (e < ext.y) load_b<SPLIT>(z, list, total, e * Ext<SPLIT>::kRanks, r, b);
+                if (e < ext.y) load_b<SPLIT>(z, m->list, total, e * Ext<SPLIT>::kRanks, r, b);
                 // the token stage that quarter g of this chunk falls on
                 const uint32_t xi = (it * 4 + g) / z.x_k, sx = xi & x_mask;
                 ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) &&
@@ -595,7 +637,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 if (e < ext.y) {
                     tmem_st16(dst, b);
                     uint8_t *x = smem + kOffX + sx * x_slot + (g & (z.x_k - 1)) * z.tile_n * 128;
-                    for (int c = row; c < round16(cur.n); c += kTileRows) store_u<SPLIT>(z, cur, e * Ext<SPLIT>::kRanks, c, x);
+                    for (int c = row; c < round16(cur.n); c += kTileRows) store_u<SPLIT>(z, m, cur, e * Ext<SPLIT>::kRanks, c, x);
                     fence_proxy_async_shared();
                     tmem_wait_st();
                 }
@@ -616,17 +658,24 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             // the warps leave together, and the last tile's columns are read
             if (!named_barrier_and(1, 32 * kEpiWarps, ok)) break;
             const Item cur = t;
-            if (w + step < n_items) t = get_item(z, w + step);
+            at.next(z, stride);
+            if (w + step < n_items) t = get_item(z, at);
             const int n8 = round16(cur.n) / 8;
             const long long row = (long long)cur.rt * kTileRows + my_row;
             for (int j = threadIdx.x; j < round16(cur.n); j += 32 * kEpiWarps) {
-                const int at = cur.start + min(j, cur.n - 1);
-                const int e = cur.w_exp + (z.x_exp ? z.x_exp[at] : 0);
-                const bool bad = z.place && z.place[at] == -2;      // an adapter id out of range
-                m->slot[j] = z.order ? z.order[at] : at;
-                m->scale[j] = make_float2(bad ? __int_as_float(0x7fc00000) : pow2(e / 2), pow2(e - e / 2));
+                const int i = cur.start + min(j, cur.n - 1);
+                const int e = decode_exp<SPLIT>(cur.w_exp) + (z.x_exp ? z.x_exp[i] : 0), near = max(-126, min(127, e));
+                const int place = z.place ? z.place[i] : -1;
+                m->slot[j] = z.order ? z.order[i] : i;
+                m->scale[j] = place == -2 ? __int_as_float(0x7fc00000) : pow2(near);
+                m->e[j] = (int16_t)e;
+                m->place[j] = (int16_t)place;
+                if (e != near) m->wide = (int)item + 1;
+                if (j < cur.count) m->list[j] = z.tile_list[cur.start + j];
             }
             named_barrier(1, 32 * kEpiWarps);
+            if (threadIdx.x == 0) mbar_arrive(smem_u32(&m->columns));
+            const bool wide = *(volatile int *)&m->wide == (int)item + 1;
             const int ks = z.ksplit;
             uint32_t base = lane_base + run;                // where the tile's sums are
             if constexpr (SPLIT) {
@@ -679,7 +728,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = next[j];
                     if (g + kSides < n8) tmem_ld8(base + 8 * (g + kSides), next);
-                    finish<OT>(z, m, 8 * g, cur.n, row, v);
+                    finish<OT>(z, m, wide, 8 * g, cur.n, row, v);
                     tmem_wait_ld(next);
                 }
             } else {
@@ -723,7 +772,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                             for (int j = 0; j < 8; ++j) o[j] += src[j * kTileRows];
                         }
                     }
-                    finish<OT>(z, m, 8 * g, cur.n, row, o);
+                    finish<OT>(z, m, wide, 8 * g, cur.n, row, o);
                 }
                 __syncwarp();
                 if (lane < ks && lane != rank) mbar_arrive_remote(map_shared_rank(smem_u32(&m->red_empty), (uint32_t)lane));
