@@ -96,21 +96,25 @@ struct TcArgs {
     Sizes z;
 };
 
-struct Meta {
-    uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw], x_full[kMaxX], x_empty[kMaxX], full[4], empty[4];
-    uint64_t acc_full[2], acc_empty[2], columns, red_full, red_empty, done;
-    uint32_t tmem;
-    int abort, wide;                // wide: number of the last item with a column whose scale is no float
-    // of a tile's columns: output slot, scale (a power of two; NaN for a bad adapter id), its exponent, the adapter's place
+// A tile's columns: output slot, scale (a power of two; NaN for a bad adapter id), its exponent, the adapter's place; and the
+// tile's adapters.
+struct Columns {
     alignas(16) int slot[kMaxTokens];
     alignas(16) float scale[kMaxTokens];
-    int list[kMaxTokens];           // the tile's adapters
+    int list[kMaxTokens];
     int16_t e[kMaxTokens], place[kMaxTokens];
 };
 
-constexpr int kOffX = 4096;                 // shared memory: the barriers and a tile's columns, tokens, raw blocks, joined sums
-static_assert(sizeof(Meta) <= kOffX && offsetof(Meta, slot) % 16 == 0 && offsetof(Meta, scale) % 16 == 0,
-              "the head of shared memory, read 16 bytes at a time");
+struct Meta {
+    uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw], x_full[kMaxX], x_empty[kMaxX], full[4], empty[4];
+    uint64_t acc_full[2], acc_empty[2], columns_full[2], red_full, red_empty, done;
+    uint32_t tmem;
+    int abort, wide;                // wide: number of the last item with a column whose scale is no float
+    Columns columns[2];             // of this item and the next
+};
+
+constexpr int kOffX = 7168;                 // shared memory: the barriers and a tile's columns, tokens, raw blocks, joined sums
+static_assert(sizeof(Meta) <= kOffX && kOffX % 1024 == 0 && offsetof(Meta, columns) % 16 == 0, "the head of shared memory");
 
 struct Item { int mat, rt, start, n, w_exp, count; };
 
@@ -239,15 +243,16 @@ __device__ __forceinline__ void store_elem(void *y, long long i, int dtype, floa
 __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
 
 template <int OT>
-__device__ __forceinline__ void store_out(void *y, long long i, float v) {
-    if constexpr (OT == HQ_DT_F32) static_cast<float *>(y)[i] = v;
-    else if constexpr (OT == HQ_DT_F16) static_cast<__half *>(y)[i] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
+__device__ __forceinline__ void store_out(void *y, float v) {
+    if constexpr (OT == HQ_DT_F32) *static_cast<float *>(y) = v;
+    else if constexpr (OT == HQ_DT_F16) *static_cast<__half *>(y) = __float2half_rn(v);
+    else *static_cast<__nv_bfloat16 *>(y) = __float2bfloat16_rn(v);
 }
 
-// The 8 columns from c0 of output row `row` (its sums in v): scales, SwiGLU with the neighbouring lane's row, store.
+// The 8 columns from c0 of one output row (its sums in v): scales, SwiGLU with the neighbouring lane's row, store.
+// `out` is the row's place in output row 0 and `pitch` the bytes of an output row; `live`: the row exists.
 template <int OT>
-__device__ __forceinline__ void finish(const Sizes &a, const Meta *m, bool wide, int c0, int n, long long row, float (&v)[8]) {
+__device__ __forceinline__ void finish(const Columns *m, bool swiglu, bool wide, int c0, int n, bool live, char *out, uint32_t pitch, float (&v)[8]) {
     const float4 *sp = reinterpret_cast<const float4 *>(m->scale + c0);
     const int4 *op = reinterpret_cast<const int4 *>(m->slot + c0);
     const float4 s0 = sp[0], s1 = sp[1];
@@ -263,23 +268,20 @@ __device__ __forceinline__ void finish(const Sizes &a, const Meta *m, bool wide,
             v[j] *= pow2(e - max(-126, min(127, e)));
         }
     }
-    if (a.epilogue == HQ_MOE_EPI_SWIGLU) {
+    if (swiglu) {
         // even lanes hold gate rows, odd lanes up rows: each finishes every other token
         const bool odd = threadIdx.x & 1;
-        const long long half = a.rows / 2, i = row / 2;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
             const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
             const float h = silu(odd ? got : v[j]) * (odd ? v[j + 1] : got);
-            if (c0 + j + (odd ? 1 : 0) < n && row < a.rows) store_out<OT>(a.y, (odd ? slot[j + 1] : slot[j]) * half + i, h);
+            if (live && c0 + j + (odd ? 1 : 0) < n) store_out<OT>(out + (uint64_t)(uint32_t)(odd ? slot[j + 1] : slot[j]) * pitch, h);
         }
         return;
     }
-    if (row < a.rows) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + j < n) store_out<OT>(a.y, slot[j] * a.rows + row, v[j]);
-    }
+    for (int j = 0; j < 8; ++j)
+        if (live && c0 + j < n) store_out<OT>(out + (uint64_t)(uint32_t)slot[j] * pitch, v[j]);
 }
 
 // ------------------------------------------------------------------ adapter quarters
@@ -318,7 +320,7 @@ __device__ __forceinline__ void load_b(const Sizes &a, const int *list, int tota
 
 // Row `c` of the token operand: u of the token's own adapter at its virtual ranks, as bf16 terms side by side, zero elsewhere.
 template <bool SPLIT>
-__device__ __forceinline__ void store_u(const Sizes &a, const Meta *m, const Item &t, int v0, int c, uint8_t *dst) {
+__device__ __forceinline__ void store_u(const Sizes &a, const Columns *m, const Item &t, int v0, int c, uint8_t *dst) {
     constexpr int R = Ext<SPLIT>::kRanks, T = Ext<SPLIT>::kTerms;
     const int place = c < t.n ? m->place[c] : -1;
     const int lo = place * a.rank - v0;                     // virtual rank v0 + k is rank k - lo of the adapter
@@ -326,27 +328,38 @@ __device__ __forceinline__ void store_u(const Sizes &a, const Meta *m, const Ite
     const int e = -m->e[c];
     const float s1 = pow2(e / 2), s2 = pow2(e - e / 2);
     uint8_t *line = dst + c * 128;
-    const float *u = a.u + (long long)(t.start + c) * a.rank;
+    const float *u = a.u + (long long)(t.start + c) * a.rank - lo;
+    const bool four = ((a.rank | lo) & 3) == 0;
+    float f[R];
 #pragma unroll
-    for (int k0 = 0; k0 < R; k0 += 8) {
-        uint32_t w[T][4] = {};
+    for (int k = 0; k < R; k += 4) {
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
         if (any) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int r = k0 + k - lo;
-                float f = r >= 0 && r < a.rank ? u[r] * s1 * s2 : 0.f;
-#pragma unroll
-                for (int i = 0; i < T; ++i) {
-                    const __nv_bfloat16 h = __float2bfloat16_rn(f);
-                    f -= __bfloat162float(h);
-                    w[i][k / 2] |= (uint32_t)__bfloat16_as_ushort(h) << (16 * (k & 1));
-                }
+            if (four) {
+                if (k >= lo && k < lo + a.rank) q = *reinterpret_cast<const float4 *>(u + k);
+            } else {
+                if (k >= lo && k < lo + a.rank) q.x = u[k];
+                if (k + 1 >= lo && k + 1 < lo + a.rank) q.y = u[k + 1];
+                if (k + 2 >= lo && k + 2 < lo + a.rank) q.z = u[k + 2];
+                if (k + 3 >= lo && k + 3 < lo + a.rank) q.w = u[k + 3];
             }
         }
-#pragma unroll
-        for (int i = 0; i < T; ++i)
-            *reinterpret_cast<uint4 *>(line + (((i * R + k0) / 8 ^ (c & 7)) << 4)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        f[k] = q.x * s1 * s2; f[k + 1] = q.y * s1 * s2; f[k + 2] = q.z * s1 * s2; f[k + 3] = q.w * s1 * s2;
     }
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int k0 = 0; k0 < R; k0 += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[k0 + 2 * k], f[k0 + 2 * k + 1]);
+                f[k0 + 2 * k] -= __low2float(h);
+                f[k0 + 2 * k + 1] -= __high2float(h);
+                w[k] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            *reinterpret_cast<uint4 *>(line + (((i * R + k0) / 8 ^ (c & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -374,7 +387,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&m->acc_full[i]), 1); mbar_init(smem_u32(&m->acc_empty[i]), kEpiWarps); }
         m->wide = 0;
         mbar_init(smem_u32(&m->done), 1);
-        mbar_init(smem_u32(&m->columns), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&m->columns_full[i]), 1);
         mbar_init(smem_u32(&m->red_full), (uint32_t)max(1, (z.ksplit - 1) * kEpiWarps));
         mbar_init(smem_u32(&m->red_empty), (uint32_t)max(1, (z.ksplit - 1) * kEpiWarps));
         fence_mbar_init();
@@ -436,13 +449,13 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 const int box = box_of(z, cur.n);
                 const int2 ext = ext_range<SPLIT>(z, cur, rank);
                 const uint32_t bytes = kTerms * z.x_k * box_rows(z, box) * 128;
-                const int hi = 4 * (c_hi + (ext.y - ext.x + 3) / 4);
+                // the adapter chunks come first
 #pragma unroll 1
-                for (int k = 4 * c_lo; k < hi; k += z.x_k, ++it) {
+                for (int k = 4 * (c_lo - (ext.y - ext.x + 3) / 4); k < 4 * c_hi; k += z.x_k, ++it) {
                     const uint32_t s = it & x_mask, bar = smem_u32(&m->x_full[s]);
                     ok = tc_wait(smem_u32(&m->x_empty[s]), ((it >> z.x_log) & 1) ^ 1, abort, fault);
                     if (!ok) break;
-                    if (k < 4 * c_hi) {
+                    if (k >= 4 * c_lo) {
                         mbar_arrive_expect_tx(bar, bytes);
                         tma_load_3d(x_base + s * x_slot, &a.map_x[box], 0, cur.start, k, bar, pol);
                         if constexpr (SPLIT) tma_load_3d(x_base + s * x_slot + x_lo, &a.map_lo[box], 0, cur.start, k, bar, pol);
@@ -488,6 +501,44 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 const uint32_t kb_step = (uint32_t)(box_rows(z, box_of(z, cur.n)) * 128) >> 4;
                 const int2 ext = ext_range<SPLIT>(z, cur, rank);
                 bool add = false;                           // to the accumulator, or start it
+                // adapter chunks, ahead of the weights' (which are on their way meanwhile)
+                if (ext.x < ext.y) {
+                    ok = tc_wait(smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault);
+                    if (!ok) break;
+                    const uint32_t d = tmem + (acc & 1) * half, idesc_b = tc_idesc(n16, true);
+                    for (int e = ext.x; e < ext.y; e += 4, ++it) {
+                        const uint32_t buf = z.deep ? it & 1 : 0, par = z.deep ? (it >> 1) & 1 : it & 1;
+                        uint32_t ta = tmem + slots + buf * 4 * kSlotCols;
+                        uint64_t db = 0;
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q, ta += kTerms * kSlotCols, db += kb_step) {
+                            if ((q & (z.x_k - 1)) == 0) {
+                                ok = tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault);
+                                db = desc_x + (uint64_t)(xs * x_units);
+                            }
+                            if (!z.deep || q == 0) ok = ok && tc_wait(smem_u32(&m->full[buf + q]), par, abort, fault);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (e + q < ext.y) {
+                                // the terms of u times the same columns of B
+                                constexpr int kPer = Ext<SPLIT>::kRanks / 16;
+#pragma unroll
+                                for (int j = 0; j < kPer * Ext<SPLIT>::kTerms; ++j)
+                                    tc_mma(d, ta + 8 * (j % kPer), db + 2 * j, idesc_b, add || j);
+                                add = true;
+                            }
+                            if (!z.deep || q == 3) tc_commit(smem_u32(&m->empty[z.deep ? buf : q]));
+                            if ((q & (z.x_k - 1)) == z.x_k - 1) next_x();
+                        }
+                        if (!ok) break;
+                    }
+                    if (!ok) break;
+                    if (SPLIT) {                            // an accumulator of their own: they have no small products
+                        tc_commit(smem_u32(&m->acc_full[acc & 1]));
+                        ++acc;
+                        add = false;
+                    }
+                }
                 for (int c = c_lo; c < c_hi; ++c, ++it) {
                     if (!add && !(ok = tc_wait(smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault))) break;
                     const uint32_t d = tmem + (acc & 1) * half;
@@ -532,44 +583,12 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                         if (!ok) break;
                     }
                     add = true;
-                    if (SPLIT || (c + 1 == c_hi && ext.x == ext.y)) {
+                    if (SPLIT || c + 1 == c_hi) {
                         tc_commit(smem_u32(&m->acc_full[acc & 1]));
                         ++acc;
                         add = false;
                     }
                 }
-                if (!ok || ext.x == ext.y) continue;
-                // adapter chunks
-                if (!add && !(ok = tc_wait(smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault))) continue;
-                const uint32_t d = tmem + (acc & 1) * half, idesc_b = tc_idesc(n16, true);
-                for (int e = ext.x; e < ext.y; e += 4, ++it) {
-                    const uint32_t buf = z.deep ? it & 1 : 0, par = z.deep ? (it >> 1) & 1 : it & 1;
-                    uint32_t ta = tmem + slots + buf * 4 * kSlotCols;
-                    uint64_t db = 0;
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q, ta += kTerms * kSlotCols, db += kb_step) {
-                        if ((q & (z.x_k - 1)) == 0) {
-                            ok = tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault);
-                            db = desc_x + (uint64_t)(xs * x_units);
-                        }
-                        if (!z.deep || q == 0) ok = ok && tc_wait(smem_u32(&m->full[buf + q]), par, abort, fault);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (e + q < ext.y) {
-                            // the terms of u times the same columns of B
-                            constexpr int kPer = Ext<SPLIT>::kRanks / 16;
-#pragma unroll
-                            for (int j = 0; j < kPer * Ext<SPLIT>::kTerms; ++j)
-                                tc_mma(d, ta + 8 * (j % kPer), db + 2 * j, idesc_b, add || j);
-                            add = true;
-                        }
-                        if (!z.deep || q == 3) tc_commit(smem_u32(&m->empty[z.deep ? buf : q]));
-                        if ((q & (z.x_k - 1)) == z.x_k - 1) next_x();
-                    }
-                    if (!ok) break;
-                }
-                tc_commit(smem_u32(&m->acc_full[acc & 1]));
-                ++acc;
             }
             // every product ends before TMEM is given back
             tc_commit(smem_u32(&m->done));
@@ -589,6 +608,37 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             const Item cur = t;
             at.next(z, stride);
             if (w + step < n_items) t = get_item(z, at);
+            if (cur.count) {
+                // adapter chunks: group g has their quarter g
+                const int2 ext = ext_range<SPLIT>(z, cur, rank);
+                ok = tc_wait(smem_u32(&m->columns_full[item & 1]), (item >> 1) & 1, abort, fault);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                const int total = cur.count * z.rank;
+                const long long r = min((long long)cur.rt * kTileRows + row, z.rows - 1);
+                for (int e = ext.x + g; e < (ext.y - ext.x + 3) / 4 * 4 + ext.x; e += 4, ++it) {
+                    const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
+                    const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
+                    uint32_t b[16] = {};
+                    if (e < ext.y) load_b<SPLIT>(z, m->columns[item & 1].list, total, e * Ext<SPLIT>::kRanks, r, b);
+                    // the token stage that quarter g of this chunk falls on
+                    const uint32_t xi = (it * 4 + g) / z.x_k, sx = xi & x_mask;
+                    ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) &&
+                                                     tc_wait(smem_u32(&m->x_empty[sx]), ((xi >> z.x_log) & 1) ^ 1, abort, fault));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (e < ext.y) {
+                        tmem_st16(dst, b);
+                        uint8_t *x = smem + kOffX + sx * x_slot + (g & (z.x_k - 1)) * z.tile_n * 128;
+                        for (int c = row; c < round16(cur.n); c += kTileRows) store_u<SPLIT>(z, &m->columns[item & 1], cur, e * Ext<SPLIT>::kRanks, c, x);
+                        fence_proxy_async_shared();
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&m->full[bar]));
+                }
+                if (!ok) break;
+            }
             const float wscale = pow2(-decode_exp<SPLIT>(cur.w_exp));
             for (int c = c_lo; c < c_hi; ++c, ++it) {
                 ok = tc_wait(smem_u32(&m->raw_full[s]), ph, abort, fault);
@@ -616,35 +666,6 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 }
                 if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
             }
-            if (!ok || cur.count == 0) continue;
-            // adapter chunks: group g has their quarter g
-            const int2 ext = ext_range<SPLIT>(z, cur, rank);
-            ok = tc_wait(smem_u32(&m->columns), item & 1, abort, fault);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; continue; }
-            const int total = cur.count * z.rank;
-            const long long r = min((long long)cur.rt * kTileRows + row, z.rows - 1);
-            for (int e = ext.x + g; e < (ext.y - ext.x + 3) / 4 * 4 + ext.x; e += 4, ++it) {
-                const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
-                const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
-                uint32_t b[16] = {};
-                if (e < ext.y) load_b<SPLIT>(z, m->list, total, e * Ext<SPLIT>::kRanks, r, b);
-                // the token stage that quarter g of this chunk falls on
-                const uint32_t xi = (it * 4 + g) / z.x_k, sx = xi & x_mask;
-                ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) &&
-                                                 tc_wait(smem_u32(&m->x_empty[sx]), ((xi >> z.x_log) & 1) ^ 1, abort, fault));
-                if (!ok) break;
-                tc_fence_after();
-                if (e < ext.y) {
-                    tmem_st16(dst, b);
-                    uint8_t *x = smem + kOffX + sx * x_slot + (g & (z.x_k - 1)) * z.tile_n * 128;
-                    for (int c = row; c < round16(cur.n); c += kTileRows) store_u<SPLIT>(z, m, cur, e * Ext<SPLIT>::kRanks, c, x);
-                    fence_proxy_async_shared();
-                    tmem_wait_st();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&m->full[bar]));
-            }
         }
     } else {
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -652,36 +673,49 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         float *red = reinterpret_cast<float *>(smem + z.off_red);
         const uint32_t red_addr = smem_u32(red);
         const int my_row = (warp & 3) * 32 + lane;
+        constexpr int kOut = OT == HQ_DT_F32 ? 4 : 2;
+        const bool swiglu = z.epilogue == HQ_MOE_EPI_SWIGLU;
+        const uint32_t pitch = (uint32_t)(swiglu ? z.rows / 2 : z.rows) * kOut;     // rows x 272 bytes of weights fit the device
         uint32_t acc = 0, item = 0;
         bool ok = true;
+        // Fills the columns of item `i`, tile `c`, for this warp's own use and the decode warps'; true if a scale is no float.
+        auto fill = [&](const Item &c, uint32_t i) -> bool {
+            Columns *to = &m->columns[i & 1];
+            for (int j = threadIdx.x; j < round16(c.n); j += 32 * kEpiWarps) {
+                const int k = c.start + min(j, c.n - 1);
+                const int e = decode_exp<SPLIT>(c.w_exp) + (z.x_exp ? z.x_exp[k] : 0), near = max(-126, min(127, e));
+                const int place = z.place ? z.place[k] : -1;
+                to->slot[j] = z.order ? z.order[k] : k;
+                to->scale[j] = place == -2 ? __int_as_float(0x7fc00000) : pow2(near);
+                to->e[j] = (int16_t)e;
+                to->place[j] = (int16_t)place;
+                if (e != near) m->wide = (int)i + 1;
+                if (j < c.count) to->list[j] = z.tile_list[c.start + j];
+            }
+            named_barrier(1, 32 * kEpiWarps);
+            if (threadIdx.x == 0) mbar_arrive(smem_u32(&m->columns_full[i & 1]));
+            return *(volatile int *)&m->wide == (int)i + 1;
+        };
+        bool wide_next = first < n_items ? fill(t, 0) : false;
         for (int w = first; w < n_items; w += step, ++item) {
             // the warps leave together, and the last tile's columns are read
             if (!named_barrier_and(1, 32 * kEpiWarps, ok)) break;
             const Item cur = t;
+            const bool wide = wide_next;
             at.next(z, stride);
-            if (w + step < n_items) t = get_item(z, at);
+            if (w + step < n_items) {
+                t = get_item(z, at);
+                wide_next = fill(t, item + 1);
+            }
             const int n8 = round16(cur.n) / 8;
             const long long row = (long long)cur.rt * kTileRows + my_row;
-            for (int j = threadIdx.x; j < round16(cur.n); j += 32 * kEpiWarps) {
-                const int i = cur.start + min(j, cur.n - 1);
-                const int e = decode_exp<SPLIT>(cur.w_exp) + (z.x_exp ? z.x_exp[i] : 0), near = max(-126, min(127, e));
-                const int place = z.place ? z.place[i] : -1;
-                m->slot[j] = z.order ? z.order[i] : i;
-                m->scale[j] = place == -2 ? __int_as_float(0x7fc00000) : pow2(near);
-                m->e[j] = (int16_t)e;
-                m->place[j] = (int16_t)place;
-                if (e != near) m->wide = (int)item + 1;
-                if (j < cur.count) m->list[j] = z.tile_list[cur.start + j];
-            }
-            named_barrier(1, 32 * kEpiWarps);
-            if (threadIdx.x == 0) mbar_arrive(smem_u32(&m->columns));
-            const bool wide = *(volatile int *)&m->wide == (int)item + 1;
+            char *out = static_cast<char *>(z.y) + (swiglu ? row / 2 : row) * kOut;
             const int ks = z.ksplit;
             uint32_t base = lane_base + run;                // where the tile's sums are
             if constexpr (SPLIT) {
                 // Each chunk's sums (and the adapters') leave the accumulator for the running sums.
                 const int2 ext = ext_range<SPLIT>(z, cur, rank);
-                const int chunks = c_hi - c_lo, rounds = chunks + (ext.x < ext.y ? 1 : 0);
+                const int own = ext.x < ext.y ? 1 : 0, rounds = c_hi - c_lo + own;    // the adapters' round is the first
                 for (int i = 0; i < rounds; ++i, ++acc) {
                     ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->acc_full[acc & 1]), (acc >> 1) & 1, abort, fault));
                     if (!ok) break;
@@ -691,10 +725,10 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                     for (int g = side; g < n8; g += kSides) {
                         float v[8], x[8], r[8];
                         tmem_ld8(from + 8 * g, v);
-                        if (i < chunks) tmem_ld8(from + z.tile_n + 8 * g, x);       // the small products
+                        if (i >= own) tmem_ld8(from + z.tile_n + 8 * g, x);         // the small products
                         if (i > 0) tmem_ld8(base + 8 * g, r);
                         tmem_wait_ld(v);
-                        if (i < chunks) {
+                        if (i >= own) {
                             tmem_wait_ld(x);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) v[j] += x[j];
@@ -728,7 +762,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = next[j];
                     if (g + kSides < n8) tmem_ld8(base + 8 * (g + kSides), next);
-                    finish<OT>(z, m, wide, 8 * g, cur.n, row, v);
+                    finish<OT>(&m->columns[item & 1], swiglu, wide, 8 * g, cur.n, row < z.rows, out, pitch, v);
                     tmem_wait_ld(next);
                 }
             } else {
@@ -772,7 +806,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                             for (int j = 0; j < 8; ++j) o[j] += src[j * kTileRows];
                         }
                     }
-                    finish<OT>(z, m, wide, 8 * g, cur.n, row, o);
+                    finish<OT>(&m->columns[item & 1], swiglu, wide, 8 * g, cur.n, row < z.rows, out, pitch, o);
                 }
                 __syncwarp();
                 if (lane < ks && lane != rank) mbar_arrive_remote(map_shared_rank(smem_u32(&m->red_empty), (uint32_t)lane));
@@ -795,7 +829,6 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
 // ------------------------------------------------------------------ prepare
 
 constexpr int kSelfPlan = 1024;         // slots up to which every block finds its own places (one launch less)
-constexpr int kDownTokens = 16;         // tokens of an adapter block at most
 
 struct PrepArgs {
     const void *x;
@@ -820,7 +853,7 @@ struct PrepArgs {
     const uint16_t *A;
     const float *scales;
     long long n_adapters;
-    int n_tokens, rank, list_blocks, down_tokens, down_split;
+    int n_tokens, rank, list_blocks, down_tokens, down_turns, down_split;
     int32_t *tile_count, *tile_list, *place;
     float *u;
     uint32_t *fault;
@@ -848,25 +881,38 @@ __device__ __forceinline__ int block_scan(int v, int *red, int *all) {
     return __shfl_sync(0xffffffffu, sum - part, warp) + inc - v;
 }
 
-// One block: counts the experts' slots, cuts each expert's slots into tiles of tokens, and (place) gives every slot its
-// place.  The order within an expert is whatever the counters give; an output does not depend on it.
-template <int THREADS>
-__device__ void plan_slots(const PrepArgs &a, int *count, bool place) {
+// Counts the experts' slots, cuts each expert's slots into tiles of tokens, and (PLACE) gives every slot its
+// place.  The order within an expert is whatever the counters give; an output does not depend on it.  A cluster shares the
+// slots: each block counts its own, and reads the others' counts.
+template <int THREADS, bool PLACE>
+__device__ void plan_slots(const PrepArgs &a, int *count, int blocks, int rank) {
     __shared__ int red[32];
+    constexpr int U = 4;                                    // loads in flight
+    const int lo = (int)((long long)a.n_slots * rank / blocks), hi = (int)((long long)a.n_slots * (rank + 1) / blocks);
     for (int e = threadIdx.x; e < a.n_mats; e += THREADS) count[e] = 0;
     __syncthreads();
-    for (int s0 = 0; s0 < a.n_slots; s0 += 4 * THREADS) {
-        int e[4];
+    for (int s0 = lo; s0 < hi; s0 += U * THREADS) {
+        int e[U];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { const int s = s0 + i * THREADS + threadIdx.x; e[i] = s < a.n_slots ? a.ids[s] : -1; }
+        for (int i = 0; i < U; ++i) { const int s = s0 + i * THREADS + threadIdx.x; e[i] = s < hi ? a.ids[s] : -1; }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) if (e[i] >= 0 && e[i] < a.n_mats) atomicAdd(&count[e[i]], 1);
+        for (int i = 0; i < U; ++i) if (e[i] >= 0 && e[i] < a.n_mats) atomicAdd(&count[e[i]], 1);
     }
-    __syncthreads();
+    if (blocks > 1) cluster_sync(); else __syncthreads();
     int base_n = 0, base_t = 0;
+    int *first = count + a.n_mats;                          // places of this block's slots (the counts are still read by others)
     for (int e0 = 0; e0 < a.n_mats; e0 += THREADS) {
         const int e = e0 + threadIdx.x;
-        const int n = e < a.n_mats ? count[e] : 0;
+        int n = 0, before = 0;
+        if (e < a.n_mats) {
+            if (blocks == 1) n = count[e];
+            else
+                for (int r = 0; r < blocks; ++r) {
+                    const int c = ld_shared_cluster_s32(map_shared_rank(smem_u32(&count[e]), (uint32_t)r));
+                    n += c;
+                    before += r < rank ? c : 0;
+                }
+        }
         int size = 0, nt = 0;
         if (n) {
             nt = (n + a.tile_n - 1) / a.tile_n;
@@ -876,37 +922,41 @@ __device__ void plan_slots(const PrepArgs &a, int *count, bool place) {
         int all_n, all_t;
         const int at = base_n + block_scan<THREADS>(n, red, &all_n);
         const int tile = base_t + block_scan<THREADS>(nt, red, &all_t);
-        const int we = n ? a.w_exp[e] : 0;
-        for (int i = 0; i < nt; ++i) a.tiles[tile + i] = TileRec{e, at + i * size, min(size, n - i * size), we};
-        if (e < a.n_mats) count[e] = at;
+        if (rank == 0) {
+            const int we = n ? a.w_exp[e] : 0;
+            for (int i = 0; i < nt; ++i) a.tiles[tile + i] = TileRec{e, at + i * size, min(size, n - i * size), we};
+        }
+        if (PLACE && e < a.n_mats) first[e] = at + before;
         base_n += all_n;
         base_t += all_t;
     }
-    if (threadIdx.x == 0) *a.n_tiles = base_t;
-    if (!place) return;
-    __syncthreads();
-    for (int s0 = 0; s0 < a.n_slots; s0 += 4 * THREADS) {
-        int e[4];
+    if (rank == 0 && threadIdx.x == 0) *a.n_tiles = base_t;
+    if constexpr (PLACE) {
+        __syncthreads();
+        for (int s0 = lo; s0 < hi; s0 += U * THREADS) {
+            int e[U];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { const int s = s0 + i * THREADS + threadIdx.x; e[i] = s < a.n_slots ? a.ids[s] : -1; }
+            for (int i = 0; i < U; ++i) { const int s = s0 + i * THREADS + threadIdx.x; e[i] = s < hi ? a.ids[s] : -1; }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int s = s0 + i * THREADS + threadIdx.x;
-            if (s >= a.n_slots) continue;
-            const bool ok = e[i] >= 0 && e[i] < a.n_mats;
-            const int at = ok ? atomicAdd(&count[e[i]], 1) : -1;
-            a.pos[s] = at;
-            if (ok) a.order[at] = s;
-            else atomicOr(a.fault, kFaultExpertId);
+            for (int i = 0; i < U; ++i) {
+                const bool ok = e[i] >= 0 && e[i] < a.n_mats;
+                const int at = ok ? atomicAdd(&first[e[i]], 1) : -1, s = s0 + i * THREADS + threadIdx.x;
+                if (s < hi) {
+                    a.pos[s] = at;
+                    if (ok) a.order[at] = s;
+                    else atomicOr(a.fault, kFaultExpertId);
+                }
+            }
         }
     }
+    if (blocks > 1) cluster_sync();
 }
 
 __global__ void __launch_bounds__(1024) plan_kernel(PrepArgs a) {
-    extern __shared__ int count[];
+    extern __shared__ int count[];                          // [2][n_mats]
     griddep_launch_dependents();
     griddep_wait();
-    plan_slots<1024>(a, count, true);
+    plan_slots<1024, true>(a, count, (int)gridDim.x, gridDim.x > 1 ? (int)cluster_ctarank() : 0);
 }
 
 // max over the row_threads threads of a row (a power of two of at least a warp); every thread of the block takes part
@@ -980,13 +1030,16 @@ __device__ void pack_rows(const PrepArgs &a, int block) {
             s1 = pow2(-(e / 2));
             s2 = pow2(-(e - e / 2));
         }
-        for (int c = 0; c < a.copies; ++c) {
-            const int slot = r * a.copies + c;
-            int at = slot;
-            if (a.ids) {
-                if (a.pos) {
-                    at = live ? a.pos[slot] : -1;
-                } else {
+        constexpr int U = 8;                                // copies that one reading of the row serves
+        for (int c0 = 0; c0 < a.copies; c0 += U) {
+            int at[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int slot = r * a.copies + c0 + u;
+                const bool mine = live && c0 + u < a.copies;
+                at[u] = mine && !a.ids ? slot : -1;
+                if (a.pos && mine) at[u] = a.pos[slot];
+                if (a.ids && !a.pos && c0 + u < a.copies) {
                     // few slots: the place is the number of slots that sort before this one
                     const int id = live ? a.ids[slot] : -1;
                     int before = 0;
@@ -994,23 +1047,20 @@ __device__ void pack_rows(const PrepArgs &a, int block) {
                         const int o = a.ids[s];
                         before += o >= 0 && (o < id || (o == id && s < slot)) ? 1 : 0;
                     }
-                    at = row_sum(before, a.row_threads, redi);
-                    if (id < 0 || id >= a.n_mats) {
-                        at = -1;
-                        if (live && tr == 0) atomicOr(a.fault, kFaultExpertId);
-                    } else if (tr == 0) {
-                        a.order[at] = slot;
+                    before = row_sum(before, a.row_threads, redi);
+                    const bool ok = id >= 0 && id < a.n_mats;
+                    at[u] = ok ? before : -1;
+                    if (live && tr == 0) {
+                        if (ok) a.order[before] = slot;
+                        else atomicOr(a.fault, kFaultExpertId);
                     }
                 }
+                if (mine && at[u] < 0)
+                    for (long long j = tr; j < a.y_cols; j += a.row_threads)
+                        store_elem(a.y, (long long)slot * a.y_cols + j, a.y_dtype, __int_as_float(0x7fc00000));
+                if (at[u] >= 0 && a.x_exp && tr == 0) a.x_exp[at[u]] = e;
             }
-            if (!live) continue;
-            if (at < 0) {
-                for (long long j = tr; j < a.y_cols; j += a.row_threads)
-                    store_elem(a.y, (long long)slot * a.y_cols + j, a.y_dtype, __int_as_float(0x7fc00000));
-                continue;
-            }
-            if (a.x_exp && tr == 0) a.x_exp[at] = e;
-            for (long long j = 8 * tr; j < a.cols; j += 8 * a.row_threads) {
+            for (long long j = 8 * tr; live && j < a.cols; j += 8 * a.row_threads) {
                 float v[8];
                 uint32_t h[4], l[4];
                 load8x(a.x, base + j, a.dtype, v);
@@ -1024,8 +1074,12 @@ __device__ void pack_rows(const PrepArgs &a, int block) {
                     const __half2 q = __floats2half2_rn(fabsf(f0) < INFINITY ? g0 : 0.f, fabsf(f1) < INFINITY ? g1 : 0.f);
                     l[k] = *reinterpret_cast<const uint32_t *>(&q);
                 }
-                *reinterpret_cast<uint4 *>(a.hi + (long long)at * a.cols + j) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (a.lo) *reinterpret_cast<uint4 *>(a.lo + (long long)at * a.cols + j) = make_uint4(l[0], l[1], l[2], l[3]);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (at[u] < 0) continue;
+                    *reinterpret_cast<uint4 *>(a.hi + (long long)at[u] * a.cols + j) = make_uint4(h[0], h[1], h[2], h[3]);
+                    if (a.lo) *reinterpret_cast<uint4 *>(a.lo + (long long)at[u] * a.cols + j) = make_uint4(l[0], l[1], l[2], l[3]);
+                }
             }
         }
     }
@@ -1069,121 +1123,126 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t a0, const
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// u[t][k] = scale A[adapter][k] . x[t] for a group of 8 NT tokens: each distinct adapter of the group times all its
-// tokens, of which its own are kept.  x is one (bf16), two (f16) or three (f32) bf16 terms, exactly.  The columns
-// are split over the warps and a cluster; their order inside a product is a lane's own (8 neighbours a
+// u[t][k] = scale A[adapter][k] . x[t] for a group of 8 NT tokens: an adapter of the group times all its
+// tokens, of which its own are kept; blocks (group, turn) take every turns-th distinct adapter.  x is one (bf16),
+// two (f16) or three (f32) bf16 terms, exactly.  Warps take 32 ranks each, and the columns are split over what warps that
+// leaves and over a cluster; their order inside a product is a lane's own (8 neighbours a
 // lane), the same for both operands.
 template <int DT, int NT>
-__device__ void adapter_down(const PrepArgs &a, int group) {
+__device__ void adapter_down(const PrepArgs &a, int group, int turn) {
     constexpr int TERMS = DT == HQ_DT_BF16 ? 1 : DT == HQ_DT_F16 ? 2 : 3, N = 8 * NT, WARPS = kPrepThreads / 32;
-    extern __shared__ float part[];                         // [WARPS][16 mt][N], then [down_split][16 mt][N]
+    constexpr int kUnroll = TERMS == 3 ? 1 : 2;
+    extern __shared__ float part[];                         // [slices][32 halves][N], then [down_split][32 halves][N]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int mt = (a.rank + 15) / 16, vals = mt * 16 * N;
-    float *joined = part + WARPS * vals;
+    const int halves = a.rank <= 32 ? 1 : 2, slices = WARPS / halves, vals = halves * 32 * N;
+    const int r0 = warp % halves * 32 + g, slice = warp / halves;
+    float *joined = part + slices * vals;
     const int t0 = group * N, crank = a.down_split > 1 ? (int)cluster_ctarank() : 0;
     const int units = (int)(a.cols / 32);
     const int u_lo = (int)((long long)units * crank / a.down_split), u_hi = (int)((long long)units * (crank + 1) / a.down_split);
     const int id = lane < N && t0 + lane < a.n_tokens ? a.adapter_ids[t0 + lane] : -1;
     uint32_t left = __ballot_sync(0xffffffffu, id >= 0 && id < a.n_adapters);
-    while (left) {
+    for (int nth = 0; left; ++nth) {
         const int ad = __shfl_sync(0xffffffffu, id, __ffs(left) - 1);
         const uint32_t mine = __ballot_sync(0xffffffffu, id == ad);
         left &= ~mine;
-        float acc[4][NT][4];
+        if (nth % a.down_turns != turn) continue;
+        float acc[2][NT][4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-        const uint16_t *A = a.A + (long long)ad * a.rank * a.cols;
-        for (int un = u_lo + warp; un < u_hi; un += WARPS) {
-            const long long col = un * 32ll + c * 8;
-            uint32_t b[NT][TERMS][4];
+        const uint16_t *A = a.A + ((long long)ad * a.rank + r0) * a.cols + c * 8;
+#pragma unroll kUnroll
+        for (int un = u_lo + slice; un < u_hi; un += slices) {
+            const long long col = un * 32ll;
+            uint4 p[2][2];                                  // rows g and g + 8 of two tiles of 16 ranks
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                p[h >> 1][h & 1] = make_uint4(0, 0, 0, 0);
+                if (r0 + 8 * h < a.rank) p[h >> 1][h & 1] = *reinterpret_cast<const uint4 *>(A + 8 * h * a.cols + col);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int t = t0 + 8 * n + g;
                 float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if ((mine >> (8 * n + g)) & 1) load8x(a.x, (long long)t * a.cols + col, DT, v);
+                if ((mine >> (8 * n + g)) & 1) load8x(a.x, (long long)(t0 + 8 * n + g) * a.cols + col + c * 8, DT, v);
 #pragma unroll
-                for (int i = 0; i < TERMS; ++i)
+                for (int i = 0; i < TERMS; ++i) {
+                    uint32_t b[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                        b[n][i][k] = *reinterpret_cast<const uint32_t *>(&h);
+                        b[k] = *reinterpret_cast<const uint32_t *>(&h);
                         v[2 * k] -= __low2float(h);
                         v[2 * k + 1] -= __high2float(h);
                     }
-            }
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                if (m < mt) {
-                    const int r = 16 * m + g;
-                    uint4 p = make_uint4(0, 0, 0, 0), q = make_uint4(0, 0, 0, 0);
-                    if (r < a.rank) p = *reinterpret_cast<const uint4 *>(A + r * a.cols + col);
-                    if (r + 8 < a.rank) q = *reinterpret_cast<const uint4 *>(A + (r + 8) * a.cols + col);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < TERMS; ++i) {
-                            mma_bf16(acc[m][n], p.x, q.x, p.y, q.y, b[n][i][0], b[n][i][1]);
-                            mma_bf16(acc[m][n], p.z, q.z, p.w, q.w, b[n][i][2], b[n][i][3]);
-                        }
+                    for (int m = 0; m < 2; ++m) {
+                        mma_bf16(acc[m][n], p[m][0].x, p[m][1].x, p[m][0].y, p[m][1].y, b[0], b[1]);
+                        mma_bf16(acc[m][n], p[m][0].z, p[m][1].z, p[m][0].w, p[m][1].w, b[2], b[3]);
+                    }
                 }
             }
         }
         __syncthreads();                                    // the last adapter's sums are read
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-            if (m < mt) {
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        part[warp * vals + (16 * m + g + (i >> 1) * 8) * N + 8 * n + 2 * c + (i & 1)] = acc[m][n][i];
-            }
+                for (int i = 0; i < 4; ++i)
+                    part[slice * vals + (r0 + 16 * m + (i >> 1) * 8) * N + 8 * n + 2 * c + (i & 1)] = acc[m][n][i];
         __syncthreads();
-        for (int i = threadIdx.x; i < vals; i += kPrepThreads) {
+        for (int i = threadIdx.x; i < a.rank * N; i += kPrepThreads) {
             float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) s += part[w * vals + i];
+            for (int w = 0; w < slices; ++w) s += part[w * vals + i];
             if (a.down_split > 1) st_shared_cluster_f32(map_shared_rank(smem_u32(joined + crank * vals + i), 0), s);
             else joined[i] = s;
         }
         if (a.down_split > 1) cluster_sync(); else __syncthreads();
         if (crank == 0) {
             const float scale = a.scales[ad];
-            for (int i = threadIdx.x; i < vals; i += kPrepThreads) {
+            for (int i = threadIdx.x; i < a.rank * N; i += kPrepThreads) {
                 const int k = i / N, t = i % N;
                 float s = 0.f;
-                for (int r = 0; r < a.down_split; ++r) s += joined[r * vals + i];
-                if (((mine >> t) & 1) && k < a.rank) a.u[(long long)(t0 + t) * a.rank + k] = scale * s;
+                for (int d = 0; d < a.down_split; ++d) s += joined[d * vals + i];
+                if ((mine >> t) & 1) a.u[(long long)(t0 + t) * a.rank + k] = scale * s;
             }
         }
         if (a.down_split > 1) cluster_sync();
     }
 }
 
+// Grouped products, and tokens without adapters: the tiles (of few slots), and the tokens' terms.
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_constant__ PrepArgs a) {
     extern __shared__ float dyn[];
     griddep_launch_dependents();
     griddep_wait();
+    const int b = blockIdx.x;
+    if (b < a.plan_blocks) plan_slots<kPrepThreads, false>(a, reinterpret_cast<int *>(dyn), 1, 0);
+    else pack_rows(a, b - a.plan_blocks);
+}
+
+// With adapters: the tokens' terms, each tile's adapters, and u, at once.
+__global__ void __launch_bounds__(kPrepThreads) prepare_adapters_kernel(const __grid_constant__ PrepArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
     int b = blockIdx.x;
-    if (b < a.plan_blocks) { plan_slots<kPrepThreads>(a, reinterpret_cast<int *>(dyn), false); return; }
-    b -= a.plan_blocks;
     if (b < a.pack_blocks) { pack_rows(a, b); return; }
     b -= a.pack_blocks;
     if (b < a.list_blocks) { if (b * (long long)a.tile_n < a.n_tokens) list_tile(a, b); return; }
     b = (b - a.list_blocks) / a.down_split;
-    if (b * (long long)a.down_tokens >= a.n_tokens) return;
-    if (a.down_tokens == 8) {
-        if (a.dtype == HQ_DT_BF16) adapter_down<HQ_DT_BF16, 1>(a, b);
-        else if (a.dtype == HQ_DT_F16) adapter_down<HQ_DT_F16, 1>(a, b);
-        else adapter_down<HQ_DT_F32, 1>(a, b);
+    const int turn = b % a.down_turns;
+    b /= a.down_turns;
+    if (a.dtype == HQ_DT_F32) adapter_down<HQ_DT_F32, 1>(a, b, turn);
+    else if (a.down_tokens == 8) {
+        if (a.dtype == HQ_DT_BF16) adapter_down<HQ_DT_BF16, 1>(a, b, turn);
+        else adapter_down<HQ_DT_F16, 1>(a, b, turn);
     } else {
-        if (a.dtype == HQ_DT_BF16) adapter_down<HQ_DT_BF16, 2>(a, b);
-        else if (a.dtype == HQ_DT_F16) adapter_down<HQ_DT_F16, 2>(a, b);
-        else adapter_down<HQ_DT_F32, 2>(a, b);
+        if (a.dtype == HQ_DT_BF16) adapter_down<HQ_DT_BF16, 2>(a, b, turn);
+        else adapter_down<HQ_DT_F16, 2>(a, b, turn);
     }
 }
 
@@ -1365,10 +1424,12 @@ bool make_plan(const DeviceInfo &dev, int fmt, bool split, int64_t groups, int64
             if (!fit_smem(dev, fmt, split, &p)) continue;
             const int64_t clusters = dev.num_sms / ks;
             const int64_t waves = (groups * tt * n_rt + clusters - 1) / clusters;
-            // cycles of 64 columns: the products, or decode and the weights' share of the memory bandwidth
-            const double stage = std::max<double>(split ? 9.0 * std::max(tn, 32) : 2.2 * tn, 380.0);
-            const double end = 1500.0 + 16.0 * tn + (ks > 1 ? 1500.0 + 12.0 * tn : 0.0);
-            const double time = waves * (stage * 4 * ((n_chunks + ks - 1) / ks)) + end * (1 + 0.15 * (waves - 1));
+            // cycles of a chunk: its products, or decode and the weights' share of the memory bandwidth; of an item, the
+            // gap between two tiles' products; at the end, the last tile's outputs, which a column split makes every
+            // item wait for
+            const double chunk = std::max<double>(split ? 28.0 * std::max(tn, 32) : 8.5 * tn, split ? 2200.0 : 1700.0);
+            const double out = 3000.0 + 100.0 * tn;
+            const double time = waves * (chunk * ((n_chunks + ks - 1) / ks) + 1200.0 + (ks > 1 ? 5000.0 + out / ks : 0.0)) + out;
             if (!any || time < best_t) { any = true; best_t = time; *best = p; }
         }
     }
@@ -1473,7 +1534,10 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
             prep_smem = (size_t)a.n_mats * 4;
         } else {
             q.pos = reinterpret_cast<int32_t *>(ws + l.pos);
-            st = launch(plan_kernel, 1, 1024, (size_t)a.n_mats * 4, 1, stream, "plan", q);
+            // a cluster of blocks where one would take more than a few loads a thread
+            const int blocks = slots > 8192 ? 8 : 1;
+            st = configure<plan_kernel>(2 * 8192 * 4);
+            if (st == HQ_OK) st = launch(plan_kernel, blocks, 1024, (size_t)a.n_mats * 8, blocks, stream, "plan", q);
             if (st != HQ_OK) return st;
         }
     } else if (a.n_adapters > 0) {
@@ -1486,21 +1550,27 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
         q.tile_count = reinterpret_cast<int32_t *>(ws + l.tile_count);
         q.tile_list = reinterpret_cast<int32_t *>(ws + l.tile_list);
         q.place = reinterpret_cast<int32_t *>(ws + l.place);
-        // 8 tokens a block while the blocks are few, and a cluster of blocks over the columns to fill the device
-        q.down_tokens = a.n_tokens <= 512 ? 8 : kDownTokens;
-        const int64_t tg = (a.n_tokens + q.down_tokens - 1) / q.down_tokens;
-        while (q.down_split < 8 && tg * q.down_split * 2 <= 2 * dev->num_sms && a.cols / 32 / (q.down_split * 2) >= 16) q.down_split *= 2;
+        // 8 tokens a group while the groups are few, 16 (fewer readings of A) past that; blocks for 8 or 2 adapters of a
+        // group at once, and a cluster of blocks over the columns to fill the device
+        q.down_tokens = a.n_tokens <= 1024 || split ? 8 : 16;
+        q.down_turns = (int)std::min<int64_t>(std::min<int64_t>(a.n_adapters, a.n_tokens), q.down_tokens == 8 ? 8 : 2);
+        const int64_t work = (a.n_tokens + q.down_tokens - 1) / q.down_tokens * q.down_turns;
+        while (q.down_split < 8 && work * q.down_split * 2 <= 4 * dev->num_sms && a.cols / 32 / (q.down_split * 2) >= 16) q.down_split *= 2;
         const int ks = q.down_split;
         q.pack_blocks = (q.pack_blocks + ks - 1) / ks * ks;
         q.list_blocks = (int)(((a.n_tokens + p.tile_n - 1) / p.tile_n + ks - 1) / ks * ks);
-        down_blocks = (int)tg * ks;
-        prep_smem = (size_t)(kPrepThreads / 32 + ks) * ((a.rank + 15) / 16 * 16) * q.down_tokens * 4;
+        down_blocks = (int)work * ks;
+        const int halves = a.rank <= 32 ? 1 : 2;
+        prep_smem = (size_t)(kPrepThreads / 32 / halves + ks) * (halves * 32) * q.down_tokens * 4;
     }
     const int prep_grid = q.plan_blocks + q.pack_blocks + q.list_blocks + down_blocks;
     if (prep_grid > 0) {
-        st = configure<prepare_kernel>(160 * 1024);
-        if (st != HQ_OK) return st;
-        st = launch(prepare_kernel, prep_grid, kPrepThreads, prep_smem, q.down_split, stream, "prepare", q);
+        if (down_blocks > 0) {
+            st = configure<prepare_adapters_kernel>(64 * 1024);
+            if (st == HQ_OK) st = launch(prepare_adapters_kernel, prep_grid, kPrepThreads, prep_smem, q.down_split, stream, "prepare", q);
+        } else {
+            st = launch(prepare_kernel, prep_grid, kPrepThreads, prep_smem, 1, stream, "prepare", q);
+        }
         if (st != HQ_OK) return st;
     }
 
