@@ -86,7 +86,7 @@ struct Sizes {
     uint32_t *fault;
     long long rows;
     int n_tokens, n_tt, n_items, n_rt, n_chunks;
-    int tile_n, raw_slots, x_log, x_k, deep, ksplit, tmem_cols;   // 2^x_log slots of x_k (1, 2 or 4) times 64 columns of tokens
+    int tile_n, raw_slots, x_slots, x_k, deep, ksplit, share, cluster, step, tmem_cols;   // x_slots slots of x_k (1, 2 or 4) times 64 columns of tokens
     int epilogue, rank, stream_w;
     uint32_t off_raw, off_red;
 };
@@ -330,36 +330,38 @@ __device__ __forceinline__ void store_u(const Sizes &a, const Columns *m, const 
     uint8_t *line = dst + c * 128;
     const float *u = a.u + (long long)(t.start + c) * a.rank - lo;
     const bool four = ((a.rank | lo) & 3) == 0;
-    float f[R];
 #pragma unroll
-    for (int k = 0; k < R; k += 4) {
-        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (any) {
-            if (four) {
-                if (k >= lo && k < lo + a.rank) q = *reinterpret_cast<const float4 *>(u + k);
-            } else {
-                if (k >= lo && k < lo + a.rank) q.x = u[k];
-                if (k + 1 >= lo && k + 1 < lo + a.rank) q.y = u[k + 1];
-                if (k + 2 >= lo && k + 2 < lo + a.rank) q.z = u[k + 2];
-                if (k + 3 >= lo && k + 3 < lo + a.rank) q.w = u[k + 3];
+    for (int k0 = 0; k0 < R; k0 += 8) {
+        float f[8];
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+            const int k = k0 + h;
+            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (any) {
+                if (four) {
+                    if (k >= lo && k < lo + a.rank) q = *reinterpret_cast<const float4 *>(u + k);
+                } else {
+                    if (k >= lo && k < lo + a.rank) q.x = u[k];
+                    if (k + 1 >= lo && k + 1 < lo + a.rank) q.y = u[k + 1];
+                    if (k + 2 >= lo && k + 2 < lo + a.rank) q.z = u[k + 2];
+                    if (k + 3 >= lo && k + 3 < lo + a.rank) q.w = u[k + 3];
+                }
             }
+            f[h] = q.x * s1 * s2; f[h + 1] = q.y * s1 * s2; f[h + 2] = q.z * s1 * s2; f[h + 3] = q.w * s1 * s2;
         }
-        f[k] = q.x * s1 * s2; f[k + 1] = q.y * s1 * s2; f[k + 2] = q.z * s1 * s2; f[k + 3] = q.w * s1 * s2;
-    }
 #pragma unroll
-    for (int i = 0; i < T; ++i)
-#pragma unroll
-        for (int k0 = 0; k0 < R; k0 += 8) {
+        for (int i = 0; i < T; ++i) {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(f[k0 + 2 * k], f[k0 + 2 * k + 1]);
-                f[k0 + 2 * k] -= __low2float(h);
-                f[k0 + 2 * k + 1] -= __high2float(h);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+                f[2 * k] -= __low2float(h);
+                f[2 * k + 1] -= __high2float(h);
                 w[k] = *reinterpret_cast<const uint32_t *>(&h);
             }
             *reinterpret_cast<uint4 *>(line + (((i * R + k0) / 8 ^ (c & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+    }
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -373,16 +375,19 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     constexpr int kTerms = SPLIT ? 2 : 1, kSides = Roles<SPLIT>::kSides;
     constexpr int kEpiWarps = Roles<SPLIT>::kEpi, kWarpW = Roles<SPLIT>::kW, kWarpX = Roles<SPLIT>::kX, kWarpMma = Roles<SPLIT>::kMma;
     constexpr int kChunkBytes = kTileRows * Fmt<FMT>::kChunk;
+    // a cluster shares an item's columns, or its tokens: then its CTAs take neighbouring row tiles
     const int rank = z.ksplit > 1 ? (int)cluster_ctarank() : 0;
+    // (asked for where it is needed, which costs no register)
+    auto row_rank = [&]() { return z.share > 1 ? (int)cluster_ctarank() : 0; };
     const uint32_t x_base = smem_u32(smem) + kOffX, raw_base = smem_u32(smem) + z.off_raw;
-    const uint32_t x_lo = z.x_k * z.tile_n * 128, x_slot = kTerms * x_lo, x_mask = (1u << z.x_log) - 1;     // bytes to the low terms, of a slot
+    const uint32_t x_lo = z.x_k * z.tile_n * 128, x_slot = kTerms * x_lo;     // bytes to the low terms, of a slot
     volatile int *abort = &m->abort;
     uint32_t *fault = z.fault;
 
     if (threadIdx.x == 0) {
         m->abort = 0;
         for (int i = 0; i < z.raw_slots; ++i) { mbar_init(smem_u32(&m->raw_full[i]), 1); mbar_init(smem_u32(&m->raw_empty[i]), kDecodeWarps); }
-        for (int i = 0; i < 1 << z.x_log; ++i) { mbar_init(smem_u32(&m->x_full[i]), 1); mbar_init(smem_u32(&m->x_empty[i]), 1); }
+        for (int i = 0; i < z.x_slots; ++i) { mbar_init(smem_u32(&m->x_full[i]), 1); mbar_init(smem_u32(&m->x_empty[i]), (uint32_t)z.share); }
         for (int i = 0; i < 4; ++i) { mbar_init(smem_u32(&m->full[i]), z.deep ? kDecodeWarps : 4); mbar_init(smem_u32(&m->empty[i]), 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&m->acc_full[i]), 1); mbar_init(smem_u32(&m->acc_empty[i]), kEpiWarps); }
         m->wide = 0;
@@ -394,14 +399,14 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     }
     if (warp == kWarpMma) tmem_alloc(smem_u32(&m->tmem), (uint32_t)z.tmem_cols);
     tc_fence_before();
-    if (z.ksplit > 1) cluster_sync(); else __syncthreads();
+    if (z.cluster > 1) cluster_sync(); else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)&m->tmem;
     // TMEM: two buffers of accumulators, (f32) the running sums, then the operand slots
     const uint32_t half = (SPLIT ? 2 : 1) * z.tile_n, run = 2 * half, slots = run + (SPLIT ? z.tile_n : 0);
     griddep_launch_dependents();
 
-    const int first = blockIdx.x / z.ksplit, step = gridDim.x / z.ksplit;
+    const int first = (int)cluster_id(), step = z.step;
     const int c_lo = (int)((long long)z.n_chunks * rank / z.ksplit);
     const int c_hi = (int)((long long)z.n_chunks * (rank + 1) / z.ksplit);
     const Cursor stride = cursor_at(z, step);
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             uint32_t s = 0, ph = 1, it = 0;
             bool ok = true;
             for (int w = first; w < n_items && ok; w += step) {
-                const int row0 = z.tiles ? (int)((long long)t.mat * z.rows + (long long)t.rt * kTileRows) : at.outer * kTileRows;
+                const int row0 = z.tiles ? (int)((long long)t.mat * z.rows + ((long long)t.rt * z.share + row_rank()) * kTileRows) : (at.outer * z.share + row_rank()) * kTileRows;
                 at.next(z, stride);
                 if (z.tiles && w + step < n_items) t = get_item(z, at);
                 for (int c = c_lo; c < c_hi; ++c, ++it) {
@@ -440,33 +445,41 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     } else if (warp == kWarpX) {
         if (elect_one()) {
             const uint64_t pol = l2_evict_normal_policy();
-            uint32_t it = 0;
-            bool ok = true;
+            const uint16_t all = (uint16_t)((1 << z.share) - 1);
+            uint32_t it = 0, s = 0, ph = 1;
+            bool ok = true, free = false;                   // free: the next slot is known to be
             for (int w = first; w < n_items && ok; w += step) {
                 const Item cur = t;
                 at.next(z, stride);
-            if (w + step < n_items) t = get_item(z, at);
+                if (w + step < n_items) t = get_item(z, at);
                 const int box = box_of(z, cur.n);
                 const int2 ext = ext_range<SPLIT>(z, cur, rank);
                 const uint32_t bytes = kTerms * z.x_k * box_rows(z, box) * 128;
                 // the adapter chunks come first
 #pragma unroll 1
                 for (int k = 4 * (c_lo - (ext.y - ext.x + 3) / 4); k < 4 * c_hi; k += z.x_k, ++it) {
-                    const uint32_t s = it & x_mask, bar = smem_u32(&m->x_full[s]);
-                    ok = tc_wait(smem_u32(&m->x_empty[s]), ((it >> z.x_log) & 1) ^ 1, abort, fault);
+                    const uint32_t bar = smem_u32(&m->x_full[s]), dst = x_base + s * x_slot;
+                    ok = free || tc_wait(smem_u32(&m->x_empty[s]), ph, abort, fault);
                     if (!ok) break;
+                    if (++s == (uint32_t)z.x_slots) { s = 0; ph ^= 1; }
+                    free = tc_test(smem_u32(&m->x_empty[s]), ph);
                     if (k >= 4 * c_lo) {
                         mbar_arrive_expect_tx(bar, bytes);
-                        tma_load_3d(x_base + s * x_slot, &a.map_x[box], 0, cur.start, k, bar, pol);
-                        if constexpr (SPLIT) tma_load_3d(x_base + s * x_slot + x_lo, &a.map_lo[box], 0, cur.start, k, bar, pol);
+                        if (SPLIT || z.share == 1) {
+                            tma_load_3d(dst, &a.map_x[box], 0, cur.start, k, bar, pol);
+                            if constexpr (SPLIT) tma_load_3d(dst + x_lo, &a.map_lo[box], 0, cur.start, k, bar, pol);
+                        } else if ((int)(it & (z.share - 1)) == row_rank()) {
+                            // every CTA's slot is free: all have committed the last products that read it
+                            tma_load_3d_multicast(dst, &a.map_x[box], 0, cur.start, k, bar, pol, all);
+                        }
                     } else {
                         mbar_arrive(bar);                   // the decode warps fill an adapter chunk
                     }
                 }
             }
             // copies in flight end before the block's memory is given back
-            for (uint32_t k = it > x_mask ? it - x_mask - 1 : 0; !ok && k < it; ++k)
-                for (int tries = 0; tries < 1 << 8 && !mbar_try_wait(smem_u32(&m->x_full[k & x_mask]), (k >> z.x_log) & 1); ++tries) {}
+            for (uint32_t k = it > (uint32_t)z.x_slots ? it - z.x_slots : 0; !ok && k < it; ++k)
+                for (int tries = 0; tries < 1 << 8 && !mbar_try_wait(smem_u32(&m->x_full[k % z.x_slots]), (k / z.x_slots) & 1); ++tries) {}
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -488,14 +501,33 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 }
             };
             auto next_x = [&]() {
-                tc_commit(smem_u32(&m->x_empty[xs]));
-                xs = (xs + 1) & x_mask;
-                xp ^= xs == 0;
+                if (SPLIT || z.share == 1) tc_commit(smem_u32(&m->x_empty[xs]));
+                else tc_commit_multicast(smem_u32(&m->x_empty[xs]), (uint16_t)((1 << z.share) - 1));
+                if (++xs == (uint32_t)z.x_slots) { xs = 0; xp ^= 1; }
             };
+            // A wait costs hundreds of cycles even if there is nothing to wait for (the question queues behind the other
+            // warps' shared-memory accesses): the next stage's barriers are asked about before this one's products are
+            // issued, and waited for only if the answer was no.
+            bool x_ready = false, w_ready = false;
+            auto wait_x = [&]() {
+                const bool r = x_ready || tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault);
+                x_ready = false;
+                return r;
+            };
+            auto wait_w = [&](uint32_t bar, uint32_t par) {
+                const bool r = w_ready || tc_wait(smem_u32(&m->full[bar]), par, abort, fault);
+                w_ready = false;
+                return r;
+            };
+            auto ask_x = [&]() {
+                const bool wrap = xs + 1 == (uint32_t)z.x_slots;
+                x_ready = tc_test(smem_u32(&m->x_full[wrap ? 0 : xs + 1]), xp ^ (wrap ? 1u : 0u));
+            };
+            auto ask_w = [&](uint32_t bar, uint32_t par) { w_ready = tc_test(smem_u32(&m->full[bar]), par); };
             for (int w = first; w < n_items && ok; w += step) {
                 const Item cur = t;
                 at.next(z, stride);
-            if (w + step < n_items) t = get_item(z, at);
+                if (w + step < n_items) t = get_item(z, at);
                 const int n16 = round16(cur.n);
                 const uint32_t idesc = tc_idesc(n16, false);
                 const uint32_t kb_step = (uint32_t)(box_rows(z, box_of(z, cur.n)) * 128) >> 4;
@@ -513,10 +545,10 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q, ta += kTerms * kSlotCols, db += kb_step) {
                             if ((q & (z.x_k - 1)) == 0) {
-                                ok = tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault);
+                                ok = wait_x();
                                 db = desc_x + (uint64_t)(xs * x_units);
                             }
-                            if (!z.deep || q == 0) ok = ok && tc_wait(smem_u32(&m->full[buf + q]), par, abort, fault);
+                            if (!z.deep || q == 0) ok = ok && wait_w(buf + q, par);
                             if (!ok) break;
                             tc_fence_after();
                             if (e + q < ext.y) {
@@ -545,15 +577,18 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                     if (z.deep) {
                         // two buffers of four quarters, a barrier each; the chunk's tokens are one stage or two
                         const uint32_t buf = it & 1, ta = tmem + slots + buf * 4 * kSlotCols;
-                        ok = tc_wait(smem_u32(&m->full[buf]), (it >> 1) & 1, abort, fault) && tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault);
+                        ok = wait_w(buf, (it >> 1) & 1) && wait_x();
                         if (!ok) break;
                         tc_fence_after();
+                        ask_x();
+                        ask_w(buf ^ 1, ((it + 1) >> 1) & 1);
                         uint64_t db = desc_x + (uint64_t)(xs * x_units);
                         quarter(d, ta, db, idesc, add);
                         quarter(d, ta + kSlotCols, db + kb_step, idesc, true);
                         if (z.x_k == 2) {
                             next_x();
-                            if (!(ok = tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault))) break;
+                            if (!(ok = wait_x())) break;
+                            ask_x();
                             db = desc_x + (uint64_t)(xs * x_units);
                         } else {
                             db += 2 * kb_step;
@@ -568,14 +603,16 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             if ((q & (z.x_k - 1)) == 0) {
-                                ok = tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault);
+                                ok = wait_x();
                                 db = desc_x + (uint64_t)(xs * x_units);
                             } else {
                                 db += kb_step;
                             }
-                            ok = ok && tc_wait(smem_u32(&m->full[q]), it & 1, abort, fault);
+                            ok = ok && wait_w(q, it & 1);
                             if (!ok) break;
                             tc_fence_after();
+                            if ((q & (z.x_k - 1)) == z.x_k - 1) ask_x();
+                            ask_w((q + 1) & 3, (it + (q == 3 ? 1 : 0)) & 1);
                             quarter(d, tmem + slots + q * kTerms * kSlotCols, db, idesc, add || q);
                             tc_commit(smem_u32(&m->empty[q]));
                             if ((q & (z.x_k - 1)) == z.x_k - 1) next_x();
@@ -602,7 +639,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         const uint32_t lane_base = tmem + slots + ((uint32_t)((warp & 3) * 32) << 16);
         // raw slot and its parity, chunk number, item number
         uint32_t s = 0, ph = 0, it = 0, item = ~0u;
-        bool ok = true;
+        bool ok = true, ready = false;                      // ready: the next raw chunk is known to be
         for (int w = first; w < n_items && ok; w += step) {
             ++item;
             const Item cur = t;
@@ -614,16 +651,16 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 ok = tc_wait(smem_u32(&m->columns_full[item & 1]), (item >> 1) & 1, abort, fault);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 const int total = cur.count * z.rank;
-                const long long r = min((long long)cur.rt * kTileRows + row, z.rows - 1);
+                const long long r = min(((long long)cur.rt * z.share + row_rank()) * kTileRows + row, z.rows - 1);
                 for (int e = ext.x + g; e < (ext.y - ext.x + 3) / 4 * 4 + ext.x; e += 4, ++it) {
                     const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
                     const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
                     uint32_t b[16] = {};
                     if (e < ext.y) load_b<SPLIT>(z, m->columns[item & 1].list, total, e * Ext<SPLIT>::kRanks, r, b);
                     // the token stage that quarter g of this chunk falls on
-                    const uint32_t xi = (it * 4 + g) / z.x_k, sx = xi & x_mask;
+                    const uint32_t xi = (it * 4 + g) / z.x_k, sx = xi % z.x_slots;
                     ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) &&
-                                                     tc_wait(smem_u32(&m->x_empty[sx]), ((xi >> z.x_log) & 1) ^ 1, abort, fault));
+                                                     tc_wait(smem_u32(&m->x_empty[sx]), ((xi / z.x_slots) & 1) ^ 1, abort, fault));
                     if (!ok) break;
                     tc_fence_after();
                     if (e < ext.y) {
@@ -641,7 +678,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             }
             const float wscale = pow2(-decode_exp<SPLIT>(cur.w_exp));
             for (int c = c_lo; c < c_hi; ++c, ++it) {
-                ok = tc_wait(smem_u32(&m->raw_full[s]), ph, abort, fault);
+                ok = ready || tc_wait(smem_u32(&m->raw_full[s]), ph, abort, fault);
                 uint32_t v[4 * Fmt<FMT>::kVecs];            // words 0 to 4 kVecs - 1, of which quarter g begins at g
 #pragma unroll
                 for (int i = 0; i < Fmt<FMT>::kVecs; ++i)
@@ -650,6 +687,9 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
                 ok = ok && tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                const uint32_t here = s;
+                if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
+                ready = tc_test(smem_u32(&m->raw_full[s]), ph);
                 tc_fence_after();
                 if (g == 0) decode_quarter<FMT, SPLIT, 0>(v, wscale, dst);
                 else if (g == 1) decode_quarter<FMT, SPLIT, 1>(v, wscale, dst);
@@ -662,9 +702,8 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 // not wait for loads in flight, and overtakes them when the load unit is busy.
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&m->full[bar]));
-                    mbar_arrive(smem_u32(&m->raw_empty[s]));
+                    mbar_arrive(smem_u32(&m->raw_empty[here]));
                 }
-                if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
             }
         }
     } else {
@@ -708,7 +747,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 wide_next = fill(t, item + 1);
             }
             const int n8 = round16(cur.n) / 8;
-            const long long row = (long long)cur.rt * kTileRows + my_row;
+            const long long row = ((long long)cur.rt * z.share + row_rank()) * kTileRows + my_row;
             char *out = static_cast<char *>(z.y) + (swiglu ? row / 2 : row) * kOut;
             const int ks = z.ksplit;
             uint32_t base = lane_base + run;                // where the tile's sums are
@@ -822,7 +861,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (z.ksplit > 1) cluster_sync();
+    if (z.cluster > 1) cluster_sync();
     if (warp == kWarpMma) tmem_dealloc(tmem, (uint32_t)z.tmem_cols);
 }
 
@@ -1378,7 +1417,7 @@ Layout layout(const MatmulArgs &a) {
     return l;
 }
 
-struct TcPlan { int tile_n, ksplit, grid, raw_slots, x_log, x_k, deep, tmem_cols; size_t smem; uint32_t off_raw, off_red; };
+struct TcPlan { int tile_n, ksplit, share, grid, raw_slots, x_slots, x_k, deep, tmem_cols; size_t smem; uint32_t off_raw, off_red; };
 
 // Memory of a launch with tiles of p->tile_n tokens and the columns split over p->ksplit CTAs; false if it does not fit.
 bool fit_smem(const DeviceInfo &dev, int fmt, bool split, TcPlan *p) {
@@ -1388,16 +1427,20 @@ bool fit_smem(const DeviceInfo &dev, int fmt, bool split, TcPlan *p) {
     const size_t red = p->ksplit > 1 ? (size_t)(p->ksplit - 1) * per * 8 * kTileRows * 4 : 0;
     const size_t fixed = red + kOffX;
     const size_t room = (size_t)dev.max_smem_optin, xb = (size_t)p->tile_n * 128 * terms;
-    // tokens: a chunk (256 columns) in flight at least, two where they fit, in stages as long as leave four slots;
-    // raw blocks take the rest
-    auto fits = [&](int raw, int columns) { return fixed + xb * columns + (size_t)raw * chunk <= room; };
-    if (!fits(1, 4)) return false;
-    int columns = fits(2, 8) ? 8 : 4;                       // in units of 64
-    p->raw_slots = 1;
-    while (p->raw_slots < kMaxRaw && fits(p->raw_slots + 1, columns)) ++p->raw_slots;
-    while (columns < 16 && fits(p->raw_slots, 2 * columns)) columns *= 2;
-    p->x_k = columns / 4;
-    p->x_log = 2;
+    // Tokens in units of 64 columns, weights in chunks of 256: as many raw chunks as leave six units (eight for a fourth
+    // chunk), which at 400 cycles each or more cover a copy's way from L2; at least four and one.
+    auto units = [&](int raw) { return (int)((room - std::min(room, fixed + (size_t)raw * chunk)) / xb); };
+    p->raw_slots = 0;
+    for (int raw = kMaxRaw; raw >= 1 && !p->raw_slots; --raw)
+        if (units(raw) >= (raw == kMaxRaw ? 8 : 6)) p->raw_slots = raw;
+    for (int raw = kMaxRaw; raw >= 1 && !p->raw_slots; --raw)
+        if (units(raw) >= 4) p->raw_slots = raw;
+    if (!p->raw_slots) return false;
+    // in as few slots as leave four
+    const int n = units(p->raw_slots);
+    p->x_k = n >= 16 ? 4 : n >= 8 ? 2 : 1;
+    p->x_slots = p->x_k == 4 ? 4 : std::min(kMaxX, n / p->x_k);
+    const int columns = p->x_k * p->x_slots;
     uint32_t at = (uint32_t)(kOffX + xb * columns);
     p->off_raw = at;
     at += (uint32_t)(p->raw_slots * chunk);
@@ -1421,6 +1464,7 @@ bool make_plan(const DeviceInfo &dev, int fmt, bool split, int64_t groups, int64
             TcPlan p = {};
             p.tile_n = tn;
             p.ksplit = ks;
+            p.share = 1;
             if (!fit_smem(dev, fmt, split, &p)) continue;
             const int64_t clusters = dev.num_sms / ks;
             const int64_t waves = (groups * tt * n_rt + clusters - 1) / clusters;
@@ -1439,7 +1483,8 @@ bool make_plan(const DeviceInfo &dev, int fmt, bool split, int64_t groups, int64
     best->deep = sums + 2 * slots <= 512 && best->x_k > 1;
     best->tmem_cols = 32;
     while (best->tmem_cols < sums + slots * (best->deep ? 2 : 1)) best->tmem_cols *= 2;
-    best->grid = dev.num_sms / best->ksplit * best->ksplit;
+    if (!split && best->ksplit == 1 && best->tile_n >= 64 && n_rt > 1) best->share = 2;
+    best->grid = dev.num_sms / (best->ksplit * best->share) * (best->ksplit * best->share);
     return true;
 }
 
@@ -1459,7 +1504,7 @@ hq_status configure(int dynamic) {
 template <int FMT, bool SPLIT, int OT>
 hq_status launch_tc(const TcArgs &t, const TcPlan &p, cudaStream_t stream) {
     hq_status st = configure<matmul_tc_kernel<FMT, SPLIT, OT>>(232448);
-    return st != HQ_OK ? st : launch(matmul_tc_kernel<FMT, SPLIT, OT>, p.grid, Roles<SPLIT>::kThreads, p.smem, p.ksplit, stream, "matmul", t);
+    return st != HQ_OK ? st : launch(matmul_tc_kernel<FMT, SPLIT, OT>, p.grid, Roles<SPLIT>::kThreads, p.smem, p.ksplit * p.share, stream, "matmul", t);
 }
 
 template <int FMT>
@@ -1608,15 +1653,18 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
     t.z.rows = a.rows;
     t.z.n_tokens = (int)a.n_tokens;
     t.z.n_tt = (int)((a.n_tokens + p.tile_n - 1) / p.tile_n);
-    t.z.n_rt = (int)n_rt;
-    t.z.n_items = (int)((a.moe ? most_tiles(a) : t.z.n_tt) * n_rt);
+    t.z.n_rt = (int)((n_rt + p.share - 1) / p.share);
+    t.z.n_items = (int)((a.moe ? most_tiles(a) : t.z.n_tt) * t.z.n_rt);
     t.z.n_chunks = n_chunks;
     t.z.tile_n = p.tile_n;
     t.z.raw_slots = p.raw_slots;
-    t.z.x_log = p.x_log;
+    t.z.x_slots = p.x_slots;
     t.z.x_k = p.x_k;
     t.z.deep = p.deep;
     t.z.ksplit = p.ksplit;
+    t.z.share = p.share;
+    t.z.cluster = p.ksplit * p.share;
+    t.z.step = p.grid / t.z.cluster;
     t.z.tmem_cols = p.tmem_cols;
     t.z.epilogue = a.epilogue == HQ_MOE_EPI_SWIGLU ? HQ_MOE_EPI_SWIGLU : 0;
     t.z.stream_w = !a.moe && t.z.n_tt == 1;
