@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                     if (!add && !(ok = tc_wait(smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault))) break;
                     const uint32_t d = tmem + (acc & 1) * half;
                     if (z.deep) {
-                        // two buffers of four quarters, a barrier each; the chunk's tokens are one stage or two
+                        // two buffers of four quarters, a barrier each; the chunk's tokens are one to four stages
                         const uint32_t buf = it & 1, ta = tmem + slots + buf * 4 * kSlotCols;
                         ok = wait_w(buf, (it >> 1) & 1) && wait_x();
                         if (!ok) break;
@@ -584,17 +584,19 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                         ask_w(buf ^ 1, ((it + 1) >> 1) & 1);
                         uint64_t db = desc_x + (uint64_t)(xs * x_units);
                         quarter(d, ta, db, idesc, add);
-                        quarter(d, ta + kSlotCols, db + kb_step, idesc, true);
-                        if (z.x_k == 2) {
-                            next_x();
-                            if (!(ok = wait_x())) break;
-                            ask_x();
-                            db = desc_x + (uint64_t)(xs * x_units);
-                        } else {
-                            db += 2 * kb_step;
+#pragma unroll
+                        for (int q = 1; q < 4; ++q) {
+                            if ((q & (z.x_k - 1)) == 0) {
+                                next_x();
+                                if (!(ok = wait_x())) break;
+                                ask_x();
+                                db = desc_x + (uint64_t)(xs * x_units);
+                            } else {
+                                db += kb_step;
+                            }
+                            quarter(d, ta + q * kSlotCols, db, idesc, true);
                         }
-                        quarter(d, ta + 2 * kSlotCols, db, idesc, true);
-                        quarter(d, ta + 3 * kSlotCols, db + kb_step, idesc, true);
+                        if (!ok) break;
                         tc_commit(smem_u32(&m->empty[buf]));
                         next_x();
                     } else {
@@ -639,7 +641,13 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         const uint32_t lane_base = tmem + slots + ((uint32_t)((warp & 3) * 32) << 16);
         // raw slot and its parity, chunk number, item number
         uint32_t s = 0, ph = 0, it = 0, item = ~0u;
-        bool ok = true, ready = false;                      // ready: the next raw chunk is known to be
+        // The first warp of a group waits for it, and a named barrier tells the others.
+        const bool leads = (warp & 3) == 0;
+        auto group_ok = [&](bool v) {
+            __syncwarp();
+            return named_barrier_and(2 + g, 128, v);
+        };
+        bool ok = true, ready = !leads;                     // ready: the next raw chunk is known to be
         for (int w = first; w < n_items && ok; w += step) {
             ++item;
             const Item cur = t;
@@ -648,8 +656,8 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             if (cur.count) {
                 // adapter chunks: group g has their quarter g
                 const int2 ext = ext_range<SPLIT>(z, cur, rank);
-                ok = tc_wait(smem_u32(&m->columns_full[item & 1]), (item >> 1) & 1, abort, fault);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                ok = group_ok(leads ? tc_wait(smem_u32(&m->columns_full[item & 1]), (item >> 1) & 1, abort, fault) : true);
+                if (!ok) break;
                 const int total = cur.count * z.rank;
                 const long long r = min(((long long)cur.rt * z.share + row_rank()) * kTileRows + row, z.rows - 1);
                 for (int e = ext.x + g; e < (ext.y - ext.x + 3) / 4 * 4 + ext.x; e += 4, ++it) {
@@ -659,8 +667,8 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                     if (e < ext.y) load_b<SPLIT>(z, m->columns[item & 1].list, total, e * Ext<SPLIT>::kRanks, r, b);
                     // the token stage that quarter g of this chunk falls on
                     const uint32_t xi = (it * 4 + g) / z.x_k, sx = xi % z.x_slots;
-                    ok = __all_sync(0xffffffffu, tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) &&
-                                                     tc_wait(smem_u32(&m->x_empty[sx]), ((xi / z.x_slots) & 1) ^ 1, abort, fault));
+                    ok = group_ok(leads ? tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) &&
+                                              tc_wait(smem_u32(&m->x_empty[sx]), ((xi / z.x_slots) & 1) ^ 1, abort, fault) : true);
                     if (!ok) break;
                     tc_fence_after();
                     if (e < ext.y) {
@@ -678,18 +686,19 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             }
             const float wscale = pow2(-decode_exp<SPLIT>(cur.w_exp));
             for (int c = c_lo; c < c_hi; ++c, ++it) {
-                ok = ready || tc_wait(smem_u32(&m->raw_full[s]), ph, abort, fault);
+                ok = group_ok(ready || tc_wait(smem_u32(&m->raw_full[s]), ph, abort, fault));
+                if (!ok) break;
                 uint32_t v[4 * Fmt<FMT>::kVecs];            // words 0 to 4 kVecs - 1, of which quarter g begins at g
 #pragma unroll
                 for (int i = 0; i < Fmt<FMT>::kVecs; ++i)
                     ld_shared_volatile(src + s * kChunkBytes + g * kUnit + 16 * i, v + 4 * i);
                 const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
                 const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
-                ok = ok && tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                ok = group_ok(leads ? tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) : true);
+                if (!ok) break;
                 const uint32_t here = s;
                 if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
-                ready = tc_test(smem_u32(&m->raw_full[s]), ph);
+                ready = !leads || tc_test(smem_u32(&m->raw_full[s]), ph);
                 tc_fence_after();
                 if (g == 0) decode_quarter<FMT, SPLIT, 0>(v, wscale, dst);
                 else if (g == 1) decode_quarter<FMT, SPLIT, 1>(v, wscale, dst);
@@ -867,6 +876,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
 
 // ------------------------------------------------------------------ prepare
 
+constexpr int kWindow = 128;            // tokens whose adapters are looked at together
 constexpr int kSelfPlan = 1024;         // slots up to which every block finds its own places (one launch less)
 
 struct PrepArgs {
@@ -1162,30 +1172,59 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t a0, const
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// u[t][k] = scale A[adapter][k] . x[t] for a group of 8 NT tokens: an adapter of the group times all its
-// tokens, of which its own are kept; blocks (group, turn) take every turns-th distinct adapter.  x is one (bf16),
-// two (f16) or three (f32) bf16 terms, exactly.  Warps take 32 ranks each, and the columns are split over what warps that
-// leaves and over a cluster; their order inside a product is a lane's own (8 neighbours a
+// u[t][k] = scale A[adapter][k] . x[t] for a window of tokens.  Its tokens are put into groups of at most 8 NT of one
+// adapter, numbered by their first token, of which this block takes every turns-th: an adapter's A is read once for a group.
+// x is one (bf16), two (f16) or three (f32) bf16 terms, exactly.  Warps take 32 ranks each, and the columns are split
+// over what warps that leaves and over a cluster; their order inside a product is a lane's own (8 neighbours a
 // lane), the same for both operands.
 template <int DT, int NT>
-__device__ void adapter_down(const PrepArgs &a, int group, int turn) {
+__device__ void adapter_down(const PrepArgs &a, int window, int turn) {
     constexpr int TERMS = DT == HQ_DT_BF16 ? 1 : DT == HQ_DT_F16 ? 2 : 3, N = 8 * NT, WARPS = kPrepThreads / 32;
     constexpr int kUnroll = TERMS == 3 ? 1 : 2;
     extern __shared__ float part[];                         // [slices][32 halves][N], then [down_split][32 halves][N]
+    __shared__ alignas(16) int ids[kWindow];
+    __shared__ int heads[kWindow / 32], tok[N], group_id, group_first;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int halves = a.rank <= 32 ? 1 : 2, slices = WARPS / halves, vals = halves * 32 * N;
     const int r0 = warp % halves * 32 + g, slice = warp / halves;
     float *joined = part + slices * vals;
-    const int t0 = group * N, crank = a.down_split > 1 ? (int)cluster_ctarank() : 0;
+    const int t0 = window * kWindow, crank = a.down_split > 1 ? (int)cluster_ctarank() : 0;
     const int units = (int)(a.cols / 32);
     const int u_lo = (int)((long long)units * crank / a.down_split), u_hi = (int)((long long)units * (crank + 1) / a.down_split);
-    const int id = lane < N && t0 + lane < a.n_tokens ? a.adapter_ids[t0 + lane] : -1;
-    uint32_t left = __ballot_sync(0xffffffffu, id >= 0 && id < a.n_adapters);
-    for (int nth = 0; left; ++nth) {
-        const int ad = __shfl_sync(0xffffffffu, id, __ffs(left) - 1);
-        const uint32_t mine = __ballot_sync(0xffffffffu, id == ad);
-        left &= ~mine;
-        if (nth % a.down_turns != turn) continue;
+    // of a token: how many before it share its adapter; every N-th of those heads a group
+    int id = -1, before = 0, nth = -1;
+    if (threadIdx.x < kWindow) {
+        if (t0 + threadIdx.x < a.n_tokens) id = a.adapter_ids[t0 + threadIdx.x];
+        if (id >= a.n_adapters) id = -1;
+        ids[threadIdx.x] = id;
+    }
+    __syncthreads();
+    if (threadIdx.x < kWindow) {
+        for (int k = 0; k < (int)threadIdx.x; k += 4) {
+            const int4 o = *reinterpret_cast<const int4 *>(ids + k);
+            before += (o.x == id) + (o.y == id && k + 1 < threadIdx.x) + (o.z == id && k + 2 < threadIdx.x) + (o.w == id && k + 3 < threadIdx.x);
+        }
+        const uint32_t h = __ballot_sync(0xffffffffu, id >= 0 && before % N == 0);
+        if (lane == 0) heads[warp] = __popc(h);
+        if ((h >> lane) & 1) nth = __popc(h & ((1u << lane) - 1));
+    }
+    __syncthreads();
+    int groups = 0;
+    for (int w = 0; w < kWindow / 32; ++w) {
+        if (nth >= 0 && w < warp) nth += heads[w];
+        groups += heads[w];
+    }
+    for (int grp = turn; grp < groups; grp += a.down_turns) {
+        __syncthreads();                                    // the last group's sums are read, and its tokens
+        if (nth == grp) { group_id = id; group_first = before; }
+        if (threadIdx.x < N) tok[threadIdx.x] = -1;
+        __syncthreads();
+        const int ad = group_id;
+        if (id >= 0 && id == ad && before >= group_first && before < group_first + N) tok[before - group_first] = t0 + threadIdx.x;
+        __syncthreads();
+        int mine[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mine[n] = tok[8 * n + g];
         float acc[2][NT][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -1206,7 +1245,7 @@ __device__ void adapter_down(const PrepArgs &a, int group, int turn) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if ((mine >> (8 * n + g)) & 1) load8x(a.x, (long long)(t0 + 8 * n + g) * a.cols + col + c * 8, DT, v);
+                if (mine[n] >= 0) load8x(a.x, (long long)mine[n] * a.cols + col + c * 8, DT, v);
 #pragma unroll
                 for (int i = 0; i < TERMS; ++i) {
                     uint32_t b[4];
@@ -1225,7 +1264,6 @@ __device__ void adapter_down(const PrepArgs &a, int group, int turn) {
                 }
             }
         }
-        __syncthreads();                                    // the last adapter's sums are read
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -1247,7 +1285,7 @@ __device__ void adapter_down(const PrepArgs &a, int group, int turn) {
                 const int k = i / N, t = i % N;
                 float s = 0.f;
                 for (int d = 0; d < a.down_split; ++d) s += joined[d * vals + i];
-                if ((mine >> t) & 1) a.u[(long long)(t0 + t) * a.rank + k] = scale * s;
+                if (tok[t] >= 0) a.u[(long long)tok[t] * a.rank + k] = scale * s;
             }
         }
         if (a.down_split > 1) cluster_sync();
@@ -1276,13 +1314,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_adapters_kernel(const __
     const int turn = b % a.down_turns;
     b /= a.down_turns;
     if (a.dtype == HQ_DT_F32) adapter_down<HQ_DT_F32, 1>(a, b, turn);
-    else if (a.down_tokens == 8) {
-        if (a.dtype == HQ_DT_BF16) adapter_down<HQ_DT_BF16, 1>(a, b, turn);
-        else adapter_down<HQ_DT_F16, 1>(a, b, turn);
-    } else {
-        if (a.dtype == HQ_DT_BF16) adapter_down<HQ_DT_BF16, 2>(a, b, turn);
-        else adapter_down<HQ_DT_F16, 2>(a, b, turn);
-    }
+    else if (a.dtype == HQ_DT_BF16) adapter_down<HQ_DT_BF16, 2>(a, b, turn);
+    else adapter_down<HQ_DT_F16, 2>(a, b, turn);
 }
 
 // y[t][i] = sum_k router_w[t][k] part[t][k][i], V columns a thread
@@ -1480,7 +1513,7 @@ bool make_plan(const DeviceInfo &dev, int fmt, bool split, int64_t groups, int64
     if (!any) return false;
     // TMEM: two buffers of accumulators (f32: of both kinds, and the running sums), and one or two buffers of decoded chunks
     const int sums = best->tile_n * (split ? 5 : 2), slots = 4 * kSlotCols * (split ? 2 : 1);
-    best->deep = sums + 2 * slots <= 512 && best->x_k > 1;
+    best->deep = sums + 2 * slots <= 512;
     best->tmem_cols = 32;
     while (best->tmem_cols < sums + slots * (best->deep ? 2 : 1)) best->tmem_cols *= 2;
     if (!split && best->ksplit == 1 && best->tile_n >= 64 && n_rt > 1) best->share = 2;
@@ -1595,12 +1628,14 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
         q.tile_count = reinterpret_cast<int32_t *>(ws + l.tile_count);
         q.tile_list = reinterpret_cast<int32_t *>(ws + l.tile_list);
         q.place = reinterpret_cast<int32_t *>(ws + l.place);
-        // 8 tokens a group while the groups are few, 16 (fewer readings of A) past that; blocks for 8 or 2 adapters of a
-        // group at once, and a cluster of blocks over the columns to fill the device
-        q.down_tokens = a.n_tokens <= 1024 || split ? 8 : 16;
-        q.down_turns = (int)std::min<int64_t>(std::min<int64_t>(a.n_adapters, a.n_tokens), q.down_tokens == 8 ? 8 : 2);
-        const int64_t work = (a.n_tokens + q.down_tokens - 1) / q.down_tokens * q.down_turns;
-        while (q.down_split < 8 && work * q.down_split * 2 <= 4 * dev->num_sms && a.cols / 32 / (q.down_split * 2) >= 16) q.down_split *= 2;
+        // groups of 8 tokens (f32: three terms) or 16; two blocks a multiprocessor over the windows and what groups they
+        // may have, and a cluster of blocks over the columns where those are few
+        q.down_tokens = split ? 8 : 16;
+        const int64_t windows = (a.n_tokens + kWindow - 1) / kWindow, in_window = std::min<int64_t>(kWindow, a.n_tokens);
+        const int64_t most = std::min<int64_t>(in_window, a.n_adapters + (in_window + q.down_tokens - 1) / q.down_tokens);
+        q.down_turns = (int)std::min<int64_t>(most, std::max<int64_t>(1, 2 * dev->num_sms / windows));
+        const int64_t work = windows * q.down_turns;
+        while (q.down_split < 8 && work * q.down_split * 2 <= dev->num_sms * 3 / 2 && a.cols / 32 / (q.down_split * 2) >= 16) q.down_split *= 2;
         const int ks = q.down_split;
         q.pack_blocks = (q.pack_blocks + ks - 1) / ks * ks;
         q.list_blocks = (int)(((a.n_tokens + p.tile_n - 1) / p.tile_n + ks - 1) / ks * ks);
