@@ -1032,17 +1032,18 @@ __device__ __forceinline__ int row_sum(int v, int row_threads, int *red) {
     return s;
 }
 
-__device__ __forceinline__ void load8x(const void *x, long long i, int dtype, float (&v)[8]) {
-    if (dtype == HQ_DT_F32) {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i);
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// 8 elements from their bytes.
+template <int DT>
+__device__ __forceinline__ void unpack8(const uint4 *w, float (&v)[8]) {
+    const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+    if constexpr (DT == HQ_DT_F32) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(u[k]);
+        v[4] = __uint_as_float(w[1].x); v[5] = __uint_as_float(w[1].y); v[6] = __uint_as_float(w[1].z); v[7] = __uint_as_float(w[1].w);
     } else {
-        const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (dtype == HQ_DT_BF16) {
+            if (DT == HQ_DT_BF16) {
                 v[2 * k] = __uint_as_float(u[k] << 16);
                 v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
             } else {
@@ -1051,6 +1052,16 @@ __device__ __forceinline__ void load8x(const void *x, long long i, int dtype, fl
                 v[2 * k + 1] = f.y;
             }
         }
+    }
+}
+
+__device__ __forceinline__ void load8x(const void *x, long long i, int dtype, float (&v)[8]) {
+    if (dtype == HQ_DT_F32) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + i), w[2] = {p[0], p[1]};
+        unpack8<HQ_DT_F32>(w, v);
+    } else {
+        const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i);
+        if (dtype == HQ_DT_BF16) unpack8<HQ_DT_BF16>(&w, v); else unpack8<HQ_DT_F16>(&w, v);
     }
 }
 
@@ -1180,7 +1191,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t a0, const
 template <int DT, int NT>
 __device__ void adapter_down(const PrepArgs &a, int window, int turn) {
     constexpr int TERMS = DT == HQ_DT_BF16 ? 1 : DT == HQ_DT_F16 ? 2 : 3, N = 8 * NT, WARPS = kPrepThreads / 32;
-    constexpr int kUnroll = TERMS == 3 ? 1 : 2;
+    constexpr int kXVecs = DT == HQ_DT_F32 ? 2 : 1;
     extern __shared__ float part[];                         // [slices][32 halves][N], then [down_split][32 halves][N]
     __shared__ alignas(16) int ids[kWindow];
     __shared__ int heads[kWindow / 32], tok[N], group_id, group_first;
@@ -1224,7 +1235,7 @@ __device__ void adapter_down(const PrepArgs &a, int window, int turn) {
         __syncthreads();
         int mine[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mine[n] = tok[8 * n + g];
+        for (int n = 0; n < NT; ++n) mine[n] = max(tok[8 * n + g], tok[0] & -(tok[8 * n + g] < 0));
         float acc[2][NT][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -1233,37 +1244,57 @@ __device__ void adapter_down(const PrepArgs &a, int window, int turn) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
         const uint16_t *A = a.A + ((long long)ad * a.rank + r0) * a.cols + c * 8;
-#pragma unroll kUnroll
-        for (int un = u_lo + slice; un < u_hi; un += slices) {
+        // Units of 32 columns, two on their way while one is multiplied.  Places without a token repeat the group's first:
+        // what they add up is not stored.
+        struct Unit { uint4 p[4], x[NT][kXVecs]; } buf[3];
+        auto load = [&](Unit &b, int un) {
             const long long col = un * 32ll;
-            uint4 p[2][2];                                  // rows g and g + 8 of two tiles of 16 ranks
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                p[h >> 1][h & 1] = make_uint4(0, 0, 0, 0);
-                if (r0 + 8 * h < a.rank) p[h >> 1][h & 1] = *reinterpret_cast<const uint4 *>(A + 8 * h * a.cols + col);
+            for (int h = 0; h < 4; ++h) {                   // rows g and g + 8 of two tiles of 16 ranks
+                b.p[h] = make_uint4(0, 0, 0, 0);
+                if (r0 + 8 * h < a.rank) b.p[h] = *reinterpret_cast<const uint4 *>(A + 8 * h * a.cols + col);
             }
 #pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < kXVecs; ++i)
+                    b.x[n][i] = reinterpret_cast<const uint4 *>(static_cast<const char *>(a.x) +
+                                                                ((long long)mine[n] * a.cols + col + c * 8) * (DT == HQ_DT_F32 ? 4 : 2))[i];
+        };
+        auto multiply = [&](const Unit &b) {
+#pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (mine[n] >= 0) load8x(a.x, (long long)mine[n] * a.cols + col + c * 8, DT, v);
+                float v[8];
+                unpack8<DT>(b.x[n], v);
 #pragma unroll
                 for (int i = 0; i < TERMS; ++i) {
-                    uint32_t b[4];
+                    uint32_t w[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                        b[k] = *reinterpret_cast<const uint32_t *>(&h);
+                        w[k] = *reinterpret_cast<const uint32_t *>(&h);
                         v[2 * k] -= __low2float(h);
                         v[2 * k + 1] -= __high2float(h);
                     }
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        mma_bf16(acc[m][n], p[m][0].x, p[m][1].x, p[m][0].y, p[m][1].y, b[0], b[1]);
-                        mma_bf16(acc[m][n], p[m][0].z, p[m][1].z, p[m][0].w, p[m][1].w, b[2], b[3]);
+                        const uint4 lo = b.p[2 * m], hi = b.p[2 * m + 1];
+                        mma_bf16(acc[m][n], lo.x, hi.x, lo.y, hi.y, w[0], w[1]);
+                        mma_bf16(acc[m][n], lo.z, hi.z, lo.w, hi.w, w[2], w[3]);
                     }
                 }
             }
-        }
+        };
+        const int u0 = u_lo + slice;
+        if (u0 < u_hi) load(buf[0], u0);
+        if (u0 + slices < u_hi) load(buf[1], u0 + slices);
+#pragma unroll 1
+        for (int un = u0; un < u_hi; un += 3 * slices)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                if (un + (k + 2) * slices < u_hi) load(buf[(k + 2) % 3], un + (k + 2) * slices);
+                if (un + k * slices < u_hi) multiply(buf[k]);
+            }
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
