@@ -184,14 +184,14 @@ __device__ __forceinline__ void ld_shared_volatile(uint32_t addr, uint32_t *v) {
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
 
-// Two blocks (64 columns) of one row to TMEM: `w` holds the 16-byte units that the quarter touches, block 0 begins at
+// Two blocks (64 columns) of one row, pairs of columns: `w` holds the 16-byte units that the quarter touches, block 0 begins at
 // word I0.  The byte u = q + 128 (Q8_0) in the low bits of a half is the subnormal u 2^-24, and
 // one multiply-add gives u 2^-24 (d 2^24) - 128 d, rounded once: both factors and the offset are exact.  Q4_0: the byte
 // 16 n, n 2^-20 (d 2^20) - 8 d; d 2^24 or d 2^20 is then below 2^16 (d: scaled as the weights are).
 // f32: the byte goes into the mantissa of 1024 instead, 1024 + bias is subtracted exactly, and the product with d is
 // rounded to f16 and its rest, which a multiply-add gives exactly.
 template <int FMT, bool SPLIT, int I0>
-__device__ __forceinline__ void decode_quarter(const uint32_t *w, float wscale, uint32_t dst) {
+__device__ __forceinline__ void decode_quarter(const uint32_t *w, float wscale, uint32_t (&hi)[2][16], uint32_t (&lo)[2][SPLIT ? 16 : 1]) {
     constexpr int kWords = FMT == 8 ? 8 : 4;
     const __half2 bias = FMT == 8 ? __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480))    // 1152
                                   : __half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));   // 1032
@@ -201,7 +201,6 @@ __device__ __forceinline__ void decode_quarter(const uint32_t *w, float wscale, 
         const float df = __half2float(__ushort_as_half((unsigned short)dw)) * wscale;
         const __half2 d = __half2half2(__float2half_rn(SPLIT ? df : df * (FMT == 8 ? 16777216.f : 1048576.f)));
         const __half2 off = __half2half2(__float2half_rn(df * (FMT == 8 ? -128.f : -8.f)));
-        uint32_t hi[16], lo[SPLIT ? 16 : 1];                // pairs of columns
 #pragma unroll
         for (int h = 0; h < 8; ++h) {                       // four columns
             const int j = FMT == 8 ? h : h & 3;
@@ -215,16 +214,14 @@ __device__ __forceinline__ void decode_quarter(const uint32_t *w, float wscale, 
                 const __half2 n = *reinterpret_cast<const __half2 *>(&u);
                 if constexpr (SPLIT) {
                     const __half2 s = __hsub2(n, bias), r = __hmul2(s, d), l = __hfma2(s, d, __hneg2(r));
-                    hi[2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
-                    lo[2 * h + p] = *reinterpret_cast<const uint32_t *>(&l);
+                    hi[b][2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
+                    lo[b][2 * h + p] = *reinterpret_cast<const uint32_t *>(&l);
                 } else {
                     const __half2 r = __hfma2(n, d, off);
-                    hi[2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
+                    hi[b][2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
                 }
             }
         }
-        tmem_st16(dst + 16 * b, hi);
-        if constexpr (SPLIT) tmem_st16(dst + kSlotCols + 16 * b, lo);
     }
 }
 
@@ -692,18 +689,25 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
 #pragma unroll
                 for (int i = 0; i < Fmt<FMT>::kVecs; ++i)
                     ld_shared_volatile(src + s * kChunkBytes + g * kUnit + 16 * i, v + 4 * i);
+                const uint32_t here = s;
+                if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
+                ready = !leads || tc_test(smem_u32(&m->raw_full[s]), ph);
+                // decoded before the slot is waited for: that wait is then for the products alone
+                uint32_t hi[2][16], lo[2][SPLIT ? 16 : 1];
+                if (g == 0) decode_quarter<FMT, SPLIT, 0>(v, wscale, hi, lo);
+                else if (g == 1) decode_quarter<FMT, SPLIT, 1>(v, wscale, hi, lo);
+                else if (g == 2) decode_quarter<FMT, SPLIT, 2>(v, wscale, hi, lo);
+                else decode_quarter<FMT, SPLIT, 3>(v, wscale, hi, lo);
                 const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
                 const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
                 ok = group_ok(leads ? tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) : true);
                 if (!ok) break;
-                const uint32_t here = s;
-                if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
-                ready = !leads || tc_test(smem_u32(&m->raw_full[s]), ph);
                 tc_fence_after();
-                if (g == 0) decode_quarter<FMT, SPLIT, 0>(v, wscale, dst);
-                else if (g == 1) decode_quarter<FMT, SPLIT, 1>(v, wscale, dst);
-                else if (g == 2) decode_quarter<FMT, SPLIT, 2>(v, wscale, dst);
-                else decode_quarter<FMT, SPLIT, 3>(v, wscale, dst);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    tmem_st16(dst + 16 * b, hi[b]);
+                    if constexpr (SPLIT) tmem_st16(dst + kSlotCols + 16 * b, lo[b]);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -1211,7 +1215,7 @@ __device__ void adapter_down(const PrepArgs &a, int window, int turn) {
     }
     __syncthreads();
     if (threadIdx.x < kWindow) {
-        for (int k = 0; k < (int)threadIdx.x; k += 4) {
+        for (int k = 0; id >= 0 && k < (int)threadIdx.x; k += 4) {
             const int4 o = *reinterpret_cast<const int4 *>(ids + k);
             before += (o.x == id) + (o.y == id && k + 1 < threadIdx.x) + (o.z == id && k + 2 < threadIdx.x) + (o.w == id && k + 3 < threadIdx.x);
         }
@@ -1345,8 +1349,13 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_adapters_kernel(const __
     const int turn = b % a.down_turns;
     b /= a.down_turns;
     if (a.dtype == HQ_DT_F32) adapter_down<HQ_DT_F32, 1>(a, b, turn);
-    else if (a.dtype == HQ_DT_BF16) adapter_down<HQ_DT_BF16, 2>(a, b, turn);
-    else adapter_down<HQ_DT_F16, 2>(a, b, turn);
+    else if (a.down_tokens == 8) {
+        if (a.dtype == HQ_DT_BF16) adapter_down<HQ_DT_BF16, 1>(a, b, turn);
+        else adapter_down<HQ_DT_F16, 1>(a, b, turn);
+    } else {
+        if (a.dtype == HQ_DT_BF16) adapter_down<HQ_DT_BF16, 2>(a, b, turn);
+        else adapter_down<HQ_DT_F16, 2>(a, b, turn);
+    }
 }
 
 // y[t][i] = sum_k router_w[t][k] part[t][k][i], V columns a thread
@@ -1659,9 +1668,9 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
         q.tile_count = reinterpret_cast<int32_t *>(ws + l.tile_count);
         q.tile_list = reinterpret_cast<int32_t *>(ws + l.tile_list);
         q.place = reinterpret_cast<int32_t *>(ws + l.place);
-        // groups of 8 tokens (f32: three terms) or 16; two blocks a multiprocessor over the windows and what groups they
+        // groups of 8 tokens (f32: three terms; or all there are) or 16; two blocks a multiprocessor over the windows and what groups they
         // may have, and a cluster of blocks over the columns where those are few
-        q.down_tokens = split ? 8 : 16;
+        q.down_tokens = split || a.n_tokens <= 8 ? 8 : 16;
         const int64_t windows = (a.n_tokens + kWindow - 1) / kWindow, in_window = std::min<int64_t>(kWindow, a.n_tokens);
         const int64_t most = std::min<int64_t>(in_window, a.n_adapters + (in_window + q.down_tokens - 1) / q.down_tokens);
         q.down_turns = (int)std::min<int64_t>(most, std::max<int64_t>(1, 2 * dev->num_sms / windows));
