@@ -35,6 +35,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "hq_internal.h"
 #include "hq_tc.cuh"
@@ -109,7 +110,7 @@ struct Meta {
     uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw], x_full[kMaxX], x_empty[kMaxX], full[4], empty[4];
     uint64_t acc_full[2], acc_empty[2], columns_full[2], red_full, red_empty, done;
     uint32_t tmem;
-    int abort, wide;                // wide: number of the last item with a column whose scale is no float
+    int abort, wide[2];             // wide: number of the last (even, odd) item with a column whose scale is no float
     Columns columns[2];             // of this item and the next
 };
 
@@ -184,42 +185,39 @@ __device__ __forceinline__ void ld_shared_volatile(uint32_t addr, uint32_t *v) {
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
 
-// Two blocks (64 columns) of one row, pairs of columns: `w` holds the 16-byte units that the quarter touches, block 0 begins at
+// Block B (32 columns) of the two of one row's quarter, pairs of columns: `w` holds the 16-byte units that the quarter touches, block 0 begins at
 // word I0.  The byte u = q + 128 (Q8_0) in the low bits of a half is the subnormal u 2^-24, and
 // one multiply-add gives u 2^-24 (d 2^24) - 128 d, rounded once: both factors and the offset are exact.  Q4_0: the byte
 // 16 n, n 2^-20 (d 2^20) - 8 d; d 2^24 or d 2^20 is then below 2^16 (d: scaled as the weights are).
 // f32: the byte goes into the mantissa of 1024 instead, 1024 + bias is subtracted exactly, and the product with d is
 // rounded to f16 and its rest, which a multiply-add gives exactly.
-template <int FMT, bool SPLIT, int I0>
-__device__ __forceinline__ void decode_quarter(const uint32_t *w, float wscale, uint32_t (&hi)[2][16], uint32_t (&lo)[2][SPLIT ? 16 : 1]) {
+template <int FMT, bool SPLIT, int I0, int B>
+__device__ __forceinline__ void decode_block(const uint32_t *w, float wscale, uint32_t (&hi)[16], uint32_t (&lo)[SPLIT ? 16 : 1]) {
     constexpr int kWords = FMT == 8 ? 8 : 4;
     const __half2 bias = FMT == 8 ? __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480))    // 1152
                                   : __half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));   // 1032
+    const uint32_t dw = B == 0 ? w[I0] & 0xffffu : w[I0 + kWords] >> 16;
+    const float df = __half2float(__ushort_as_half((unsigned short)dw)) * wscale;
+    const __half2 d = __half2half2(__float2half_rn(SPLIT ? df : df * (FMT == 8 ? 16777216.f : 1048576.f)));
+    const __half2 off = __half2half2(__float2half_rn(df * (FMT == 8 ? -128.f : -8.f)));
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const uint32_t dw = b == 0 ? w[I0] & 0xffffu : w[I0 + kWords] >> 16;
-        const float df = __half2float(__ushort_as_half((unsigned short)dw)) * wscale;
-        const __half2 d = __half2half2(__float2half_rn(SPLIT ? df : df * (FMT == 8 ? 16777216.f : 1048576.f)));
-        const __half2 off = __half2half2(__float2half_rn(df * (FMT == 8 ? -128.f : -8.f)));
+    for (int h = 0; h < 8; ++h) {                       // four columns
+        const int j = FMT == 8 ? h : h & 3;
+        uint32_t v = B == 0 ? __funnelshift_r(w[I0 + j], w[I0 + j + 1], 16) : w[I0 + kWords + 1 + j];
+        if constexpr (FMT == 8) v ^= 0x80808080u;
+        else if constexpr (SPLIT) v = (h < 4 ? v : v >> 4) & 0x0f0f0f0fu;
+        else v = (h < 4 ? v << 4 : v) & 0xf0f0f0f0u;
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {                       // four columns
-            const int j = FMT == 8 ? h : h & 3;
-            uint32_t v = b == 0 ? __funnelshift_r(w[I0 + j], w[I0 + j + 1], 16) : w[I0 + kWords + 1 + j];
-            if constexpr (FMT == 8) v ^= 0x80808080u;
-            else if constexpr (SPLIT) v = (h < 4 ? v : v >> 4) & 0x0f0f0f0fu;
-            else v = (h < 4 ? v << 4 : v) & 0xf0f0f0f0u;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const uint32_t u = prmt(v, SPLIT ? 0x64646464u : 0u, p ? 0x4342u : 0x4140u);
-                const __half2 n = *reinterpret_cast<const __half2 *>(&u);
-                if constexpr (SPLIT) {
-                    const __half2 s = __hsub2(n, bias), r = __hmul2(s, d), l = __hfma2(s, d, __hneg2(r));
-                    hi[b][2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
-                    lo[b][2 * h + p] = *reinterpret_cast<const uint32_t *>(&l);
-                } else {
-                    const __half2 r = __hfma2(n, d, off);
-                    hi[b][2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
-                }
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t u = prmt(v, SPLIT ? 0x64646464u : 0u, p ? 0x4342u : 0x4140u);
+            const __half2 n = *reinterpret_cast<const __half2 *>(&u);
+            if constexpr (SPLIT) {
+                const __half2 s = __hsub2(n, bias), r = __hmul2(s, d), l = __hfma2(s, d, __hneg2(r));
+                hi[2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
+                lo[2 * h + p] = *reinterpret_cast<const uint32_t *>(&l);
+            } else {
+                const __half2 r = __hfma2(n, d, off);
+                hi[2 * h + p] = *reinterpret_cast<const uint32_t *>(&r);
             }
         }
     }
@@ -381,15 +379,17 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     volatile int *abort = &m->abort;
     uint32_t *fault = z.fault;
 
+    // (after a time-out a list may be read that is not this tile's: whatever is there is an adapter)
+    if (threadIdx.x < 2 * kMaxTokens) m->columns[threadIdx.x / kMaxTokens].list[threadIdx.x % kMaxTokens] = 0;
     if (threadIdx.x == 0) {
         m->abort = 0;
         for (int i = 0; i < z.raw_slots; ++i) { mbar_init(smem_u32(&m->raw_full[i]), 1); mbar_init(smem_u32(&m->raw_empty[i]), kDecodeWarps); }
         for (int i = 0; i < z.x_slots; ++i) { mbar_init(smem_u32(&m->x_full[i]), 1); mbar_init(smem_u32(&m->x_empty[i]), (uint32_t)z.share); }
         for (int i = 0; i < 4; ++i) { mbar_init(smem_u32(&m->full[i]), z.deep ? kDecodeWarps : 4); mbar_init(smem_u32(&m->empty[i]), 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&m->acc_full[i]), 1); mbar_init(smem_u32(&m->acc_empty[i]), kEpiWarps); }
-        m->wide = 0;
+        m->wide[0] = m->wide[1] = 0;
         mbar_init(smem_u32(&m->done), 1);
-        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&m->columns_full[i]), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&m->columns_full[i]), kEpiWarps);
         mbar_init(smem_u32(&m->red_full), (uint32_t)max(1, (z.ksplit - 1) * kEpiWarps));
         mbar_init(smem_u32(&m->red_empty), (uint32_t)max(1, (z.ksplit - 1) * kEpiWarps));
         fence_mbar_init();
@@ -483,7 +483,6 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         if (elect_one()) {
             // chunk number, token slot and its parity, number of the accumulator
             uint32_t it = 0, xs = 0, xp = 0, acc = 0;
-            bool ok = true;
             const uint64_t desc_x = tc_desc_sw128(x_base);
             const uint32_t x_units = x_slot >> 4, lo_units = x_lo >> 4;
             // the products of one quarter: 64 columns of weights, or the terms of u times an adapter quarter
@@ -507,21 +506,19 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             // issued, and waited for only if the answer was no.
             bool x_ready = false, w_ready = false;
             auto wait_x = [&]() {
-                const bool r = x_ready || tc_wait(smem_u32(&m->x_full[xs]), xp, abort, fault);
+                tc_wait_go(x_ready, smem_u32(&m->x_full[xs]), xp, abort, fault);
                 x_ready = false;
-                return r;
             };
             auto wait_w = [&](uint32_t bar, uint32_t par) {
-                const bool r = w_ready || tc_wait(smem_u32(&m->full[bar]), par, abort, fault);
+                tc_wait_go(w_ready, smem_u32(&m->full[bar]), par, abort, fault);
                 w_ready = false;
-                return r;
             };
             auto ask_x = [&]() {
                 const bool wrap = xs + 1 == (uint32_t)z.x_slots;
                 x_ready = tc_test(smem_u32(&m->x_full[wrap ? 0 : xs + 1]), xp ^ (wrap ? 1u : 0u));
             };
             auto ask_w = [&](uint32_t bar, uint32_t par) { w_ready = tc_test(smem_u32(&m->full[bar]), par); };
-            for (int w = first; w < n_items && ok; w += step) {
+            for (int w = first; w < n_items && !*abort; w += step) {
                 const Item cur = t;
                 at.next(z, stride);
                 if (w + step < n_items) t = get_item(z, at);
@@ -532,8 +529,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 bool add = false;                           // to the accumulator, or start it
                 // adapter chunks, ahead of the weights' (which are on their way meanwhile)
                 if (ext.x < ext.y) {
-                    ok = tc_wait(smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault);
-                    if (!ok) break;
+                    tc_wait_go(false, smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault);
                     const uint32_t d = tmem + (acc & 1) * half, idesc_b = tc_idesc(n16, true);
                     for (int e = ext.x; e < ext.y; e += 4, ++it) {
                         const uint32_t buf = z.deep ? it & 1 : 0, par = z.deep ? (it >> 1) & 1 : it & 1;
@@ -542,11 +538,10 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q, ta += kTerms * kSlotCols, db += kb_step) {
                             if ((q & (z.x_k - 1)) == 0) {
-                                ok = wait_x();
+                                wait_x();
                                 db = desc_x + (uint64_t)(xs * x_units);
                             }
-                            if (!z.deep || q == 0) ok = ok && wait_w(buf + q, par);
-                            if (!ok) break;
+                            if (!z.deep || q == 0) wait_w(buf + q, par);
                             tc_fence_after();
                             if (e + q < ext.y) {
                                 // the terms of u times the same columns of B
@@ -559,9 +554,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                             if (!z.deep || q == 3) tc_commit(smem_u32(&m->empty[z.deep ? buf : q]));
                             if ((q & (z.x_k - 1)) == z.x_k - 1) next_x();
                         }
-                        if (!ok) break;
                     }
-                    if (!ok) break;
                     if (SPLIT) {                            // an accumulator of their own: they have no small products
                         tc_commit(smem_u32(&m->acc_full[acc & 1]));
                         ++acc;
@@ -569,13 +562,13 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                     }
                 }
                 for (int c = c_lo; c < c_hi; ++c, ++it) {
-                    if (!add && !(ok = tc_wait(smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault))) break;
+                    if (!add) tc_wait_go(false, smem_u32(&m->acc_empty[acc & 1]), ((acc >> 1) & 1) ^ 1, abort, fault);
                     const uint32_t d = tmem + (acc & 1) * half;
                     if (z.deep) {
                         // two buffers of four quarters, a barrier each; the chunk's tokens are one to four stages
                         const uint32_t buf = it & 1, ta = tmem + slots + buf * 4 * kSlotCols;
-                        ok = wait_w(buf, (it >> 1) & 1) && wait_x();
-                        if (!ok) break;
+                        wait_w(buf, (it >> 1) & 1);
+                        wait_x();
                         tc_fence_after();
                         ask_x();
                         ask_w(buf ^ 1, ((it + 1) >> 1) & 1);
@@ -585,7 +578,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                         for (int q = 1; q < 4; ++q) {
                             if ((q & (z.x_k - 1)) == 0) {
                                 next_x();
-                                if (!(ok = wait_x())) break;
+                                wait_x();
                                 ask_x();
                                 db = desc_x + (uint64_t)(xs * x_units);
                             } else {
@@ -593,7 +586,6 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                             }
                             quarter(d, ta + q * kSlotCols, db, idesc, true);
                         }
-                        if (!ok) break;
                         tc_commit(smem_u32(&m->empty[buf]));
                         next_x();
                     } else {
@@ -602,13 +594,12 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             if ((q & (z.x_k - 1)) == 0) {
-                                ok = wait_x();
+                                wait_x();
                                 db = desc_x + (uint64_t)(xs * x_units);
                             } else {
                                 db += kb_step;
                             }
-                            ok = ok && wait_w(q, it & 1);
-                            if (!ok) break;
+                            wait_w(q, it & 1);
                             tc_fence_after();
                             if ((q & (z.x_k - 1)) == z.x_k - 1) ask_x();
                             ask_w((q + 1) & 3, (it + (q == 3 ? 1 : 0)) & 1);
@@ -616,7 +607,6 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                             tc_commit(smem_u32(&m->empty[q]));
                             if ((q & (z.x_k - 1)) == z.x_k - 1) next_x();
                         }
-                        if (!ok) break;
                     }
                     add = true;
                     if (SPLIT || c + 1 == c_hi) {
@@ -638,14 +628,17 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         const uint32_t lane_base = tmem + slots + ((uint32_t)((warp & 3) * 32) << 16);
         // raw slot and its parity, chunk number, item number
         uint32_t s = 0, ph = 0, it = 0, item = ~0u;
-        // The first warp of a group waits for it, and a named barrier tells the others.
-        const bool leads = (warp & 3) == 0;
-        auto group_ok = [&](bool v) {
-            __syncwarp();
-            return named_barrier_and(2 + g, 128, v);
+        uint32_t v[4 * Fmt<FMT>::kVecs];                    // words 0 to 4 kVecs - 1, of which quarter g begins at g
+        auto fetch = [&]() {
+#pragma unroll
+            for (int i = 0; i < Fmt<FMT>::kVecs; ++i)
+                ld_shared_volatile(src + s * kChunkBytes + g * kUnit + 16 * i, v + 4 * i);
         };
-        bool ok = true, ready = !leads;                     // ready: the next raw chunk is known to be
-        for (int w = first; w < n_items && ok; w += step) {
+        if (first < n_items) {
+            tc_wait_go(false, smem_u32(&m->raw_full[0]), 0, abort, fault);
+            fetch();
+        }
+        for (int w = first; w < n_items && !__any_sync(0xffffffffu, *abort); w += step) {
             ++item;
             const Item cur = t;
             at.next(z, stride);
@@ -653,8 +646,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             if (cur.count) {
                 // adapter chunks: group g has their quarter g
                 const int2 ext = ext_range<SPLIT>(z, cur, rank);
-                ok = group_ok(leads ? tc_wait(smem_u32(&m->columns_full[item & 1]), (item >> 1) & 1, abort, fault) : true);
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, tc_wait(smem_u32(&m->columns_full[item & 1]), (item >> 1) & 1, abort, fault))) break;
                 const int total = cur.count * z.rank;
                 const long long r = min(((long long)cur.rt * z.share + row_rank()) * kTileRows + row, z.rows - 1);
                 for (int e = ext.x + g; e < (ext.y - ext.x + 3) / 4 * 4 + ext.x; e += 4, ++it) {
@@ -664,9 +656,9 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                     if (e < ext.y) load_b<SPLIT>(z, m->columns[item & 1].list, total, e * Ext<SPLIT>::kRanks, r, b);
                     // the token stage that quarter g of this chunk falls on
                     const uint32_t xi = (it * 4 + g) / z.x_k, sx = xi % z.x_slots;
-                    ok = group_ok(leads ? tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) &&
-                                              tc_wait(smem_u32(&m->x_empty[sx]), ((xi / z.x_slots) & 1) ^ 1, abort, fault) : true);
-                    if (!ok) break;
+                    tc_wait_go(false, smem_u32(&m->empty[bar]), par ^ 1, abort, fault);
+                    tc_wait_go(false, smem_u32(&m->x_empty[sx]), ((xi / z.x_slots) & 1) ^ 1, abort, fault);
+                    __syncwarp();
                     tc_fence_after();
                     if (e < ext.y) {
                         tmem_st16(dst, b);
@@ -679,35 +671,38 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&m->full[bar]));
                 }
-                if (!ok) break;
             }
             const float wscale = pow2(-decode_exp<SPLIT>(cur.w_exp));
             for (int c = c_lo; c < c_hi; ++c, ++it) {
-                ok = group_ok(ready || tc_wait(smem_u32(&m->raw_full[s]), ph, abort, fault));
-                if (!ok) break;
-                uint32_t v[4 * Fmt<FMT>::kVecs];            // words 0 to 4 kVecs - 1, of which quarter g begins at g
-#pragma unroll
-                for (int i = 0; i < Fmt<FMT>::kVecs; ++i)
-                    ld_shared_volatile(src + s * kChunkBytes + g * kUnit + 16 * i, v + 4 * i);
-                const uint32_t here = s;
-                if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
-                ready = !leads || tc_test(smem_u32(&m->raw_full[s]), ph);
-                // decoded before the slot is waited for: that wait is then for the products alone
-                uint32_t hi[2][16], lo[2][SPLIT ? 16 : 1];
-                if (g == 0) decode_quarter<FMT, SPLIT, 0>(v, wscale, hi, lo);
-                else if (g == 1) decode_quarter<FMT, SPLIT, 1>(v, wscale, hi, lo);
-                else if (g == 2) decode_quarter<FMT, SPLIT, 2>(v, wscale, hi, lo);
-                else decode_quarter<FMT, SPLIT, 3>(v, wscale, hi, lo);
-                const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
+                const bool more = c + 1 < c_hi || w + step < n_items;
+                const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1, here = s;
                 const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
-                ok = group_ok(leads ? tc_wait(smem_u32(&m->empty[bar]), par ^ 1, abort, fault) : true);
-                if (!ok) break;
+                if (++s == (uint32_t)z.raw_slots) { s = 0; ph ^= 1; }
+                // asked about now, while this quarter is decoded: the slot it goes to and the next raw chunk
+                const bool free = tc_test(smem_u32(&m->empty[bar]), par ^ 1), ready = tc_test(smem_u32(&m->raw_full[s]), ph);
+                auto decode = [&](auto block, uint32_t (&hi)[16], uint32_t (&lo)[SPLIT ? 16 : 1]) {
+                    constexpr int B = decltype(block)::value;
+                    if (g == 0) decode_block<FMT, SPLIT, 0, B>(v, wscale, hi, lo);
+                    else if (g == 1) decode_block<FMT, SPLIT, 1, B>(v, wscale, hi, lo);
+                    else if (g == 2) decode_block<FMT, SPLIT, 2, B>(v, wscale, hi, lo);
+                    else decode_block<FMT, SPLIT, 3, B>(v, wscale, hi, lo);
+                };
+                // (f32: half of it ahead, for the registers)
+                uint32_t hi[16], lo[SPLIT ? 16 : 1], rest[16];
+                decode(std::integral_constant<int, 0>(), hi, lo);
+                if constexpr (!SPLIT) decode(std::integral_constant<int, 1>(), rest, lo);
+                tc_wait_go(free, smem_u32(&m->empty[bar]), par ^ 1, abort, fault);
+                __syncwarp();
                 tc_fence_after();
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    tmem_st16(dst + 16 * b, hi[b]);
-                    if constexpr (SPLIT) tmem_st16(dst + kSlotCols + 16 * b, lo[b]);
+                const bool early = __all_sync(0xffffffffu, ready) && more;
+                tmem_st16(dst, hi);
+                if constexpr (SPLIT) {
+                    tmem_st16(dst + kSlotCols, lo);
+                    decode(std::integral_constant<int, 1>(), rest, lo);
+                    tmem_st16(dst + kSlotCols + 16, lo);
                 }
+                tmem_st16(dst + 16, rest);
+                if (early) fetch();
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -716,6 +711,10 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&m->full[bar]));
                     mbar_arrive(smem_u32(&m->raw_empty[here]));
+                }
+                if (more && !early) {
+                    tc_wait_go(false, smem_u32(&m->raw_full[s]), ph, abort, fault);
+                    fetch();
                 }
             }
         }
@@ -730,35 +729,53 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         const uint32_t pitch = (uint32_t)(swiglu ? z.rows / 2 : z.rows) * kOut;     // rows x 272 bytes of weights fit the device
         uint32_t acc = 0, item = 0;
         bool ok = true;
-        // Fills the columns of item `i`, tile `c`, for this warp's own use and the decode warps'; true if a scale is no float.
-        auto fill = [&](const Item &c, uint32_t i) -> bool {
-            Columns *to = &m->columns[i & 1];
-            for (int j = threadIdx.x; j < round16(c.n); j += 32 * kEpiWarps) {
-                const int k = c.start + min(j, c.n - 1);
-                const int e = decode_exp<SPLIT>(c.w_exp) + (z.x_exp ? z.x_exp[k] : 0), near = max(-126, min(127, e));
-                const int place = z.place ? z.place[k] : -1;
-                to->slot[j] = z.order ? z.order[k] : k;
-                to->scale[j] = place == -2 ? __int_as_float(0x7fc00000) : pow2(near);
-                to->e[j] = (int16_t)e;
-                to->place[j] = (int16_t)place;
-                if (e != near) m->wide = (int)i + 1;
-                if (j < c.count) to->list[j] = z.tile_list[c.start + j];
-            }
-            named_barrier(1, 32 * kEpiWarps);
-            if (threadIdx.x == 0) mbar_arrive(smem_u32(&m->columns_full[i & 1]));
-            return *(volatile int *)&m->wide == (int)i + 1;
+        // An item's columns, a thread each: loaded a whole item before they are stored, and its tile an item before that.
+        struct Column { int slot, e, place, list; } col = {};
+        auto load = [&](const Item &c) {
+            const int k = c.start + min((int)threadIdx.x, c.n - 1);
+            if (threadIdx.x >= round16(c.n)) return;
+            col.e = decode_exp<SPLIT>(c.w_exp) + (z.x_exp ? z.x_exp[k] : 0);
+            col.place = z.place ? z.place[k] : -1;
+            col.slot = z.order ? z.order[k] : k;
+            if (threadIdx.x < c.count) col.list = z.tile_list[c.start + threadIdx.x];
         };
-        bool wide_next = first < n_items ? fill(t, 0) : false;
+        // To where the decode warps and, after the next named barrier, these warps read them.
+        auto store = [&](const Item &c, uint32_t i) {
+            Columns *to = &m->columns[i & 1];
+            const int j = threadIdx.x, near = max(-126, min(127, col.e));
+            if (j < round16(c.n)) {
+                to->slot[j] = col.slot;
+                to->scale[j] = col.place == -2 ? __int_as_float(0x7fc00000) : pow2(near);
+                to->e[j] = (int16_t)col.e;
+                to->place[j] = (int16_t)col.place;
+                if (col.e != near) m->wide[i & 1] = (int)i + 1;
+                if (j < c.count) to->list[j] = col.list;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&m->columns_full[i & 1]));
+        };
+        Item next_t = {}, after = {};
+        if (first < n_items) {
+            load(t);
+            store(t, 0);
+        }
+        auto ahead = [&](int w) -> Item {                   // the item after the cursor's, if it is one
+            at.next(z, stride);
+            return w < n_items ? get_item(z, at) : Item{};
+        };
+        next_t = ahead(first + step);
+        if (first + step < n_items) load(next_t);
+        after = ahead(first + 2 * step);
         for (int w = first; w < n_items; w += step, ++item) {
-            // the warps leave together, and the last tile's columns are read
+            // the warps leave together, the last tile's columns are read and this one's stored
             if (!named_barrier_and(1, 32 * kEpiWarps, ok)) break;
             const Item cur = t;
-            const bool wide = wide_next;
-            at.next(z, stride);
-            if (w + step < n_items) {
-                t = get_item(z, at);
-                wide_next = fill(t, item + 1);
-            }
+            const bool wide = *(volatile int *)&m->wide[item & 1] == (int)item + 1;
+            t = next_t;
+            if (w + step < n_items) store(t, item + 1);
+            next_t = after;
+            if (w + 2 * step < n_items) load(next_t);
+            after = ahead(w + 3 * step);
             const int n8 = round16(cur.n) / 8;
             const long long row = ((long long)cur.rt * z.share + row_rank()) * kTileRows + my_row;
             char *out = static_cast<char *>(z.y) + (swiglu ? row / 2 : row) * kOut;
@@ -1602,7 +1619,7 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     const bool split = a.dtype == HQ_DT_F32;
     const int64_t slots = a.n_tokens * a.n_active, n_rt = (a.rows + kTileRows - 1) / kTileRows;
-    if (most_tiles(a) * n_rt > 0x7fffffffLL)
+    if (most_tiles(a) * n_rt > 0x7fff0000LL)                  // (a few steps of the grid fit an int behind them)
         return set_error(HQ_ERR_SHAPE, "more than 2^31 tiles");
     const int chunk = a.fmt == 8 ? Fmt<8>::kChunk : Fmt<4>::kChunk;
     const int n_chunks = (int)(a.cols / 256);

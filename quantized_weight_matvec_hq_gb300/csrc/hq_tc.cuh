@@ -35,6 +35,34 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile 
     return true;
 }
 
+// The same on a path that counts every cycle, unless `known`: the thread goes on after a time-out as well (`*abort` is then
+// set, no later wait of the block takes longer than its question, and the caller looks at the end of an item).
+// A result that the caller tests costs more than the question: of two waits that are
+// over, in one thread of a warp, 460 cycles with it and 200 without.
+__device__ __forceinline__ void tc_wait_go(bool known, uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *fault) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .u32 n, a;\n\t"
+        "setp.ne.u32 p, %0, 0;\n\t"
+        "@p bra D%=;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra D%=;\n\t"
+        "mov.u32 n, 131072;\n"
+        "W%=:\n\t"
+        "ld.volatile.shared.u32 a, [%3];\n\t"
+        "setp.ne.u32 p, a, 0;\n\t"
+        "@p bra D%=;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "@p bra D%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 p, n, 0;\n\t"
+        "@p bra W%=;\n\t"
+        "st.volatile.shared.u32 [%3], 1;\n\t"
+        "atom.global.cas.b32 a, [%4], 0, %5;\n"
+        "D%=:\n\t}"
+        ::"r"((uint32_t)known), "r"(bar), "r"(parity), "r"(smem_u32(const_cast<int *>(abort))), "l"(fault),
+          "r"(((blockIdx.x & 0x7fffffu) << 9) | kFaultWaitTimeout) : "memory");
+}
+
 // Whether phase `parity` of an mbarrier is complete.
 __device__ __forceinline__ bool tc_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
