@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "hq_device.cuh"
 #include "hq_internal.h"
@@ -131,33 +132,63 @@ __global__ void __launch_bounds__(kThreads) softmax_kernel(SoftmaxArgs a) {
         }
     };
     const int end = min(hi, a.vocab);
+    const bool greedy = !(t > 0.f);
     float m = -INFINITY;
     int at = 0x7fffffff;
-#pragma unroll 2
-    for (int i = lo + 8 * (int)threadIdx.x; i < end; i += 8 * kThreads) {
-        float v[8];
-        load(i, v);
+    if (greedy) {
+        for (int i = lo + 8 * (int)threadIdx.x; i < end; i += 8 * kThreads) {
+            float v[8];
+            load(i, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) if (v[k] > m) { m = v[k]; at = i + k; }
-        if (CACHED) put8(i, v);
+            for (int k = 0; k < 8; ++k) if (v[k] > m) { m = v[k]; at = i + k; }
+        }
+    } else {
+#pragma unroll 2
+        for (int i = lo + 8 * (int)threadIdx.x; i < end; i += 8 * kThreads) {
+            float v[8];
+            load(i, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m = fmaxf(m, v[k]);
+            if (CACHED) put8(i, v);
+        }
     }
     block_first_max(m, at, red, redi);
 
-    const bool greedy = !(t > 0.f);
     float s = 0.f;
     const float mc = m == -INFINITY ? 0.f : m;
-    if (!greedy) {
+    // e^((v - mc) / t) of 8 columns.  Mode 0: t is 1.  Mode 1: the quotient as a product with 1/t and one correction by its
+    // remainder, three instructions for a division's ten; z is cut at -200 t, whose power is 0 as well, so that the
+    // remainder of -inf is no NaN (a NaN stays).  Mode 2: t so small or so large that 1/t or the cut leaves the range.
+    const int mode = t == 1.f ? 0 : t > 1e-18f && t < 1e18f ? 1 : 2;
+    const float rt = __frcp_rn(t), least = -200.f * t;
+    auto power = [&](auto which, float (&v)[8]) {
+        constexpr int MODE = decltype(which)::value;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float z = v[k] - mc;
+            if constexpr (MODE == 1) {
+                asm("max.NaN.f32 %0, %0, %1;" : "+f"(z) : "f"(least));
+                const float q = z * rt;
+                z = fmaf(fmaf(-q, t, z), rt, q);
+            }
+            if constexpr (MODE == 2) z = __fdiv_rn(z, t);
+            v[k] = expf(z);
+        }
+    };
+    auto sum = [&](auto which) {
         for (int i = lo + 8 * (int)threadIdx.x; i < end; i += 8 * kThreads) {
             float v[8];
             if (CACHED) take8(i, v); else load(i, v);
+            power(which, v);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float z = v[k] - mc;
-                v[k] = expf(t == 1.f ? z : __fdiv_rn(z, t));
-                s += v[k];
-            }
+            for (int k = 0; k < 8; ++k) s += v[k];
             if (CACHED) put8(i, v);
         }
+    };
+    if (!greedy) {
+        if (mode == 0) sum(std::integral_constant<int, 0>());
+        else if (mode == 1) sum(std::integral_constant<int, 1>());
+        else sum(std::integral_constant<int, 2>());
         for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
         if (lane == 0) red2[warp] = s;
         __syncthreads();
@@ -192,19 +223,18 @@ __global__ void __launch_bounds__(kThreads) softmax_kernel(SoftmaxArgs a) {
         return;
     }
     const float scale = S == 0.f ? 0.f : __fdiv_rn(mine, S);
-    for (int i = lo + 8 * (int)threadIdx.x; i < end; i += 8 * kThreads) {
-        float v[8];
-        if (CACHED) {
-            take8(i, v);
-        } else {
-            load(i, v);
+    auto finish = [&](auto which) {
+        for (int i = lo + 8 * (int)threadIdx.x; i < end; i += 8 * kThreads) {
+            float v[8];
+            if (CACHED) take8(i, v); else { load(i, v); power(which, v); }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = expf(t == 1.f ? v[k] - mc : __fdiv_rn(v[k] - mc, t));
+            for (int k = 0; k < 8; ++k) v[k] *= scale;
+            store(i, v);
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= scale;
-        store(i, v);
-    }
+    };
+    if (CACHED || mode == 0) finish(std::integral_constant<int, 0>());
+    else if (mode == 1) finish(std::integral_constant<int, 1>());
+    else finish(std::integral_constant<int, 2>());
 }
 
 // ------------------------------------------------------------------ verification
