@@ -108,3 +108,11 @@ def test_workspace_is_host_arithmetic(hq):
         assert moe(hq, ws_bytes=need - 1) == hq.HQ_ERR_SHAPE
         assert moe(hq, ws=0, ws_bytes=need) == hq.HQ_ERR_NULL
         assert moe(hq, ws=FAKE + 16, ws_bytes=need) == hq.HQ_ERR_ALIGN
+
+
+def test_positions_of_a_step():
+    pytest.importorskip("torch")
+    from quantized_weight_matvec_hq_gb300 import batch_step
+    request, number = batch_step.positions(np.array([0, 2, 2, 5], np.int32))
+    assert request.tolist() == [0, 0, 0, 1, 2, 2, 2, 2]
+    assert number.tolist() == [0, 1, 2, 0, 0, 1, 2, 3]
