@@ -382,12 +382,13 @@ hq_status hq_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_
  *       aligned, not in use by other work until the call's kernels end.
  *       hq_moe_matmul_workspace is a HOST function; a negative result is the
  *       hq_status of arguments that the call itself would refuse.
- * Accuracy: f16 and bf16: each weight is rounded to 11 bits, x is exact (elements below 2^-29
+ * Accuracy: f16 and bf16: each weight is rounded to 11 bits or within 2^-22 of its matrix's
+ * largest, whichever is coarser; x is exact (bf16 elements below 2^-29
  * of their row's largest are rounded to multiples of 2^-39 of it), sums are fp32, y is rounded
  * once.  f32: both factors are split in two 11-bit terms and the
  * product of the two small terms is left out: relative error of a
- * product below 2^-20.  The fp32 sums of f32 leave the tensor core
- * every 256 columns.
+ * product below 2^-20 (weights below 2^-17 of their matrix's largest: 2^-36 of that).
+ * The fp32 sums of f32 leave the tensor core every 256 columns.
  * Deterministic: the bits of a token's y do not depend on the other tokens, except through the
  * split of the columns over CTAs that the launch's sizes choose.
  * An id outside [0, n_experts): as for hq_moe_matvec_q8_0 (NaN, HQ_FAULT_EXPERT_ID).
@@ -418,8 +419,8 @@ hq_status hq_moe_matmul_q8_0(const void *W_bank, const int32_t *w_exp, const int
  *   n_tokens : 0..2^27 (0 launches nothing).  cols % 256 == 0.
  *   workspace : hq_matmul_adapters_workspace() bytes, 256-byte aligned (a HOST
  *       function; negative: the hq_status of refused arguments).
- * Accuracy of the base term as for hq_moe_matmul_q8_0; the adapter term takes x and A
- * exactly and sums in fp32.  An id outside [-1, n_adapters) gives a NaN row of y and
+ * Accuracy of the base term as for hq_moe_matmul_q8_0; the adapter term takes x, A and B
+ * exactly and sums in fp32, with A x in between rounded to 16 bits (f32: 24).  An id outside [-1, n_adapters) gives a NaN row of y and
  * HQ_FAULT_ADAPTER_ID.
  * Source: as hq_matvec_q8_0_lora (the Lemma "QLoRA over the unified core is
  * exact"), for a batch in which every request brings its own adapter.

@@ -5,13 +5,16 @@
 //
 // A prepare kernel lays the call out, then one persistent kernel multiplies:
 //  * The weights are the M operand (128 rows of W a tile) and the tokens the N
-//    operand (16 to 256 a tile), so ragged groups of tokens cost what they are.
+//    operand (16 to 192 a tile), so ragged groups of tokens cost what they are.
 //  * Raw blocks come by TMA (256 columns of 128 rows a chunk).  Four groups of four warps
 //    decode a quarter (64 columns) each to 16-bit floats, a row a thread, and store them to TMEM, from where
 //    the tensor core reads them.  (Through shared memory, decoded weights were written and read
 //    at 256 of the about 440 to 880 cycles of its bandwidth that 64 columns took, and it was the limit.)
 //    Each scheduler has a warp of every group, so that the groups' loads, waits and arithmetic overlap.
-//  * Tokens come by TMA, an expert's tokens next to each other (the prepare kernel sorts them).
+//  * Tokens come by TMA, an expert's tokens next to each other (the prepare kernel sorts them).  From 64 tokens a
+//    tile, two CTAs of a cluster take neighbouring row tiles and each fetches every second stage of tokens for
+//    both by multicast (grouped, 4096 tokens: 257 -> 255 us; 2011 tokens with adapters: 162 -> 158 us; clusters of four lose
+//    to the multiprocessors they leave idle).
 //  * Adapters are further columns of the same product: a tile's distinct adapters' B, side by side, times each token's
 //    u = A x at its own adapter's place and zero elsewhere.
 //  * Accumulators live in TMEM, two of them, so a tile's outputs are formed while the next one is
@@ -19,9 +22,17 @@
 //  * Few tiles: a cluster splits the columns and joins its partial sums in a
 //    fixed order through distributed shared memory.
 //
+// What bounds it.  Few tokens: the weights' bytes (1560 cycles a chunk and CTA at 6.8 TB/s) against about 1700
+// cycles that a chunk takes through decode; 128 experts x 1536 x 2048 of which 40 slots choose 35 or so: 26.8 us for 118 MB.
+// Many tokens: the round of barriers between the copies, the decode warps and the one thread that issues the products, about
+// 2300 cycles a chunk, whatever the tile holds (192 tokens are 1536 cycles of products); so tiles are as large as TMEM lets
+// them be.  4096 tokens, 8 of 128 experts, 1536 x 2048: 193 us, 1.07 PFLOP/s in this kernel.  f32: three
+// products for one, 118 us at 131 tokens, 8 of 128 experts.
+//
 // Numbers.  A decoded weight is d q rounded to f16 (11 bits, where bf16 would keep 8), scaled by a power of two per
-// matrix so that its largest weight is just below 1/2: weights below 2^-13 of that are rounded to
-// multiples of 2^-24 of it.  (That range is what a decode with one multiply-add for two weights takes: the quant is a
+// matrix so that its largest weight is just below 1/2: what is smaller than 2^-13 of that is rounded to
+// multiples of 2^-24 of 1, and its block's offset (-128 d or -8 d) as well.  (That range is what a decode with one multiply-add for
+// two weights takes: the quant is a
 // subnormal f16.)  Tokens of
 // bf16 become f16 exactly, scaled by a power of two per token (what lies 2^-29 below a
 // token's largest element is rounded to 2^-39 of it).  f32 tokens and weights are two
