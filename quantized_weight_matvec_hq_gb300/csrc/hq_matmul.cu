@@ -214,13 +214,14 @@ __device__ __forceinline__ void decode_block(const uint32_t *w, float wscale, ui
 #pragma unroll
     for (int h = 0; h < 8; ++h) {                       // four columns
         const int j = FMT == 8 ? h : h & 3;
-        uint32_t v = B == 0 ? __funnelshift_r(w[I0 + j], w[I0 + j + 1], 16) : w[I0 + kWords + 1 + j];
-        if constexpr (FMT == 8) v ^= 0x80808080u;
-        else if constexpr (SPLIT) v = (h < 4 ? v : v >> 4) & 0x0f0f0f0fu;
-        else v = (h < 4 ? v << 4 : v) & 0xf0f0f0f0u;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            const uint32_t u = prmt(v, SPLIT ? 0x64646464u : 0u, p ? 0x4342u : 0x4140u);
+            // block 0 begins in the middle of a word, block 1 does not: a pair is the upper or the lower half of one
+            uint32_t v = w[B == 0 ? I0 + j + p : I0 + kWords + 1 + j];
+            if constexpr (FMT == 8) v ^= 0x80808080u;
+            else if constexpr (SPLIT) v = (h < 4 ? v : v >> 4) & 0x0f0f0f0fu;
+            else v = (h < 4 ? v << 4 : v) & 0xf0f0f0f0u;
+            const uint32_t u = prmt(v, SPLIT ? 0x64646464u : 0u, (p == 0) == (B == 0) ? 0x4342u : 0x4140u);
             const __half2 n = *reinterpret_cast<const __half2 *>(&u);
             if constexpr (SPLIT) {
                 const __half2 s = __hsub2(n, bias), r = __hmul2(s, d), l = __hfma2(s, d, __hneg2(r));
