@@ -23,11 +23,11 @@
 //    fixed order through distributed shared memory.
 //
 // What bounds it.  Few tokens: the weights' bytes (1560 cycles a chunk and CTA at 6.8 TB/s) against about 1700
-// cycles that a chunk takes through decode; 128 experts x 1536 x 2048 of which 40 slots choose 35 or so: 26.8 us for 118 MB.
+// cycles that a chunk takes through decode; 128 experts x 1536 x 2048 of which 40 slots choose 35 or so: 28 us for 118 MB.
 // Many tokens: the round of barriers between the copies, the decode warps and the one thread that issues the products, about
 // 2300 cycles a chunk, whatever the tile holds (192 tokens are 1536 cycles of products); so tiles are as large as TMEM lets
-// them be.  4096 tokens, 8 of 128 experts, 1536 x 2048: 193 us, 1.07 PFLOP/s in this kernel.  f32: three
-// products for one, 118 us at 131 tokens, 8 of 128 experts.
+// them be.  4096 tokens, 8 of 128 experts, 1536 x 2048: 194 us, 1.06 PFLOP/s in this kernel.  f32: three
+// products for one, 120 us at 131 tokens, 8 of 128 experts.
 //
 // Numbers.  A decoded weight is d q rounded to f16 (11 bits, where bf16 would keep 8), scaled by a power of two per
 // matrix so that its largest weight is just below 1/2: what is smaller than 2^-13 of that is rounded to

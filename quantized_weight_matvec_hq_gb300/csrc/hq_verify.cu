@@ -6,7 +6,7 @@
 // CTA, so that few rows still occupy several SMs; the parts' results are exchanged
 // through distributed shared memory.
 //
-// Measured: softmax of 512 rows of 128256 fp32 columns 155 us, 3.4 TB/s read and written, at half the issue
+// Measured: softmax of 512 rows of 128256 fp32 columns 153 us, 3.4 TB/s read and written, at half the issue
 // slots (43 instructions a column, most of them the accurate power); 5 rows of 151936 10 us, the latencies of three passes over a
 // part.  Verification of 64 requests of 0 to 7 drafts 31 us, 2.1 TB/s; of one 11 us.
 #include <cuda_bf16.h>
