@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kThreads) softmax_kernel(SoftmaxArgs a) {
     extern __shared__ float keep[];
     __shared__ float red[kWarps], red2[kWarps], peer_m[kMaxCluster], peer_s[kMaxCluster];
     __shared__ int redi[kWarps], peer_at[kMaxCluster];
+    if (a.cluster > 1) cluster_arrive_relaxed();
     griddep_launch_dependents();
     griddep_wait();
     const int rank = a.cluster > 1 ? (int)cluster_ctarank() : 0;
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(kThreads) softmax_kernel(SoftmaxArgs a) {
     }
     float M = m, S = s, mine = 1.f;
     if (a.cluster > 1) {
+        cluster_wait();                                     // the peers run: their shared memory may be written
         if (threadIdx.x < a.cluster) {
             st_shared_cluster_f32(map_shared_rank(smem_u32(&peer_m[rank]), threadIdx.x), m);
             st_shared_cluster_f32(map_shared_rank(smem_u32(&peer_s[rank]), threadIdx.x), s);
@@ -269,6 +271,7 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 // request, 31 us for 64, whose rows of p and q are 66 MB.
 __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
     __shared__ unsigned long long sums[kWarps], peer[2][kMaxCluster];
+    if (a.cluster > 1) cluster_arrive_relaxed();
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -279,6 +282,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
     const float us = a.u_sample[r] * 16777216.f;
     if (o0 < 0 || o1 < o0 || o1 > a.n_drafts || (r == 0 && o0 != 0) || (r == a.n_req - 1 && o1 != a.n_drafts)) {
         if (lead) atomicOr(a.fault, kFaultDraft);
+        if (a.cluster > 1) cluster_wait();
         return;                                             // the whole cluster
     }
     const int n = (int)(o1 - o0);
@@ -355,6 +359,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
         before = warp_sum(lane < warp ? w : 0ull);
         total = warp_sum(w);
         if (a.cluster > 1) {
+            if (tries == 0) cluster_wait();                 // the peers run: their shared memory may be written
             if (threadIdx.x < a.cluster) {
                 const uint32_t to = map_shared_rank(smem_u32(&peer[tries][rank]), threadIdx.x);
                 st_shared_cluster_s32(to, (int)(uint32_t)total);
