@@ -1237,7 +1237,10 @@ __device__ void adapter_down(const PrepArgs &a, int window, int turn) {
     const int t0 = window * kWindow, crank = a.down_split > 1 ? (int)cluster_ctarank() : 0;
     const int units = (int)(a.cols / 32);
     const int u_lo = (int)((long long)units * crank / a.down_split), u_hi = (int)((long long)units * (crank + 1) / a.down_split);
-    if (a.down_split > 1) cluster_arrive_relaxed();
+    if (a.down_split > 1) {
+        cluster_arrive_relaxed();
+        cluster_wait();                                     // the first block runs: its shared memory may be written
+    }
     // of a token: how many before it share its adapter; every N-th of those heads a group
     int id = -1, before = 0, nth = -1;
     if (threadIdx.x < kWindow) {
@@ -1261,7 +1264,6 @@ __device__ void adapter_down(const PrepArgs &a, int window, int turn) {
         if (nth >= 0 && w < warp) nth += heads[w];
         groups += heads[w];
     }
-    if (a.down_split > 1) cluster_wait();                   // the first block runs: its shared memory may be written
     for (int grp = turn; grp < groups; grp += a.down_turns) {
         __syncthreads();                                    // the last group's sums are read, and its tokens
         if (nth == grp) { group_id = id; group_first = before; }
