@@ -11,10 +11,9 @@
 //    the tensor core reads them.  (Through shared memory, decoded weights were written and read
 //    at 256 of the about 440 to 880 cycles of its bandwidth that 64 columns took, and it was the limit.)
 //    Each scheduler has a warp of every group, so that the groups' loads, waits and arithmetic overlap.
-//  * Tokens come by TMA, an expert's tokens next to each other (the prepare kernel sorts them).  From 64 tokens a
-//    tile, two CTAs of a cluster take neighbouring row tiles and each fetches every second stage of tokens for
-//    both by multicast (grouped, 4096 tokens: 257 -> 255 us; 2011 tokens with adapters: 162 -> 158 us; clusters of four lose
-//    to the multiprocessors they leave idle).
+//  * Tokens come by TMA, an expert's tokens next to each other (the prepare kernel sorts them).  Every CTA fetches its own:
+//    no load writes to more than one CTA, since x may lie in memory that is not this GPU's (neighbouring row tiles that shared
+//    their loads gained 1 to 2 %: grouped, 4096 tokens 252 -> 247 us; 2011 tokens with adapters 139 -> 136 us).
 //  * Adapters are further columns of the same product: a tile's distinct adapters' B, side by side, times each token's
 //    u = A x at its own adapter's place and zero elsewhere.
 //  * Accumulators live in TMEM, two of them, so a tile's outputs are formed while the next one is
@@ -98,7 +97,7 @@ struct Sizes {
     uint32_t *fault;
     long long rows;
     int n_tokens, n_tt, n_items, n_rt, n_chunks;
-    int tile_n, raw_slots, x_slots, x_k, deep, ksplit, share, cluster, step, tmem_cols;   // x_slots slots of x_k (1, 2 or 4) times 64 columns of tokens
+    int tile_n, raw_slots, x_slots, x_k, deep, ksplit, step, tmem_cols;    // x_slots slots of x_k (1, 2 or 4) times 64 columns of tokens
     int epilogue, rank, stream_w;
     uint32_t off_raw, off_red;
 };
@@ -384,10 +383,8 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     constexpr int kTerms = SPLIT ? 2 : 1, kSides = Roles<SPLIT>::kSides;
     constexpr int kEpiWarps = Roles<SPLIT>::kEpi, kWarpW = Roles<SPLIT>::kW, kWarpX = Roles<SPLIT>::kX, kWarpMma = Roles<SPLIT>::kMma;
     constexpr int kChunkBytes = kTileRows * Fmt<FMT>::kChunk;
-    // a cluster shares an item's columns, or its tokens: then its CTAs take neighbouring row tiles
+    // a cluster shares an item's columns
     const int rank = z.ksplit > 1 ? (int)cluster_ctarank() : 0;
-    // (asked for where it is needed, which costs no register)
-    auto row_rank = [&]() { return z.share > 1 ? (int)cluster_ctarank() : 0; };
     const uint32_t x_base = smem_u32(smem) + kOffX, raw_base = smem_u32(smem) + z.off_raw;
     const uint32_t x_lo = z.x_k * z.tile_n * 128, x_slot = kTerms * x_lo;     // bytes to the low terms, of a slot
     volatile int *abort = &m->abort;
@@ -398,7 +395,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     if (threadIdx.x == 0) {
         m->abort = 0;
         for (int i = 0; i < z.raw_slots; ++i) { mbar_init(smem_u32(&m->raw_full[i]), 1); mbar_init(smem_u32(&m->raw_empty[i]), kDecodeWarps); }
-        for (int i = 0; i < z.x_slots; ++i) { mbar_init(smem_u32(&m->x_full[i]), 1); mbar_init(smem_u32(&m->x_empty[i]), (uint32_t)z.share); }
+        for (int i = 0; i < z.x_slots; ++i) { mbar_init(smem_u32(&m->x_full[i]), 1); mbar_init(smem_u32(&m->x_empty[i]), 1); }
         for (int i = 0; i < 4; ++i) { mbar_init(smem_u32(&m->full[i]), z.deep ? kDecodeWarps : 4); mbar_init(smem_u32(&m->empty[i]), 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&m->acc_full[i]), 1); mbar_init(smem_u32(&m->acc_empty[i]), kEpiWarps); }
         m->wide[0] = m->wide[1] = 0;
@@ -410,7 +407,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     }
     if (warp == kWarpMma) tmem_alloc(smem_u32(&m->tmem), (uint32_t)z.tmem_cols);
     tc_fence_before();
-    if (z.cluster > 1) cluster_sync(); else __syncthreads();
+    if (z.ksplit > 1) cluster_sync(); else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)&m->tmem;
     // TMEM: two buffers of accumulators, (f32) the running sums, then the operand slots
@@ -434,7 +431,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             uint32_t s = 0, ph = 1, it = 0;
             bool ok = true;
             for (int w = first; w < n_items && ok; w += step) {
-                const int row0 = z.tiles ? (int)((long long)t.mat * z.rows + ((long long)t.rt * z.share + row_rank()) * kTileRows) : (at.outer * z.share + row_rank()) * kTileRows;
+                const int row0 = z.tiles ? (int)((long long)t.mat * z.rows + (long long)t.rt * kTileRows) : at.outer * kTileRows;
                 at.next(z, stride);
                 if (z.tiles && w + step < n_items) t = get_item(z, at);
                 for (int c = c_lo; c < c_hi; ++c, ++it) {
@@ -456,7 +453,6 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     } else if (warp == kWarpX) {
         if (elect_one()) {
             const uint64_t pol = l2_evict_normal_policy();
-            const uint16_t all = (uint16_t)((1 << z.share) - 1);
             uint32_t it = 0, s = 0, ph = 1;
             bool ok = true, free = false;                   // free: the next slot is known to be
             for (int w = first; w < n_items && ok; w += step) {
@@ -476,13 +472,8 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                     free = tc_test(smem_u32(&m->x_empty[s]), ph);
                     if (k >= 4 * c_lo) {
                         mbar_arrive_expect_tx(bar, bytes);
-                        if (SPLIT || z.share == 1) {
-                            tma_load_3d(dst, &a.map_x[box], 0, cur.start, k, bar, pol);
-                            if constexpr (SPLIT) tma_load_3d(dst + x_lo, &a.map_lo[box], 0, cur.start, k, bar, pol);
-                        } else if ((int)(it & (z.share - 1)) == row_rank()) {
-                            // every CTA's slot is free: all have committed the last products that read it
-                            tma_load_3d_multicast(dst, &a.map_x[box], 0, cur.start, k, bar, pol, all);
-                        }
+                        tma_load_3d(dst, &a.map_x[box], 0, cur.start, k, bar, pol);
+                        if constexpr (SPLIT) tma_load_3d(dst + x_lo, &a.map_lo[box], 0, cur.start, k, bar, pol);
                     } else {
                         mbar_arrive(bar);                   // the decode warps fill an adapter chunk
                     }
@@ -511,8 +502,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 }
             };
             auto next_x = [&]() {
-                if (SPLIT || z.share == 1) tc_commit(smem_u32(&m->x_empty[xs]));
-                else tc_commit_multicast(smem_u32(&m->x_empty[xs]), (uint16_t)((1 << z.share) - 1));
+                tc_commit(smem_u32(&m->x_empty[xs]));
                 if (++xs == (uint32_t)z.x_slots) { xs = 0; xp ^= 1; }
             };
             // A wait costs hundreds of cycles even if there is nothing to wait for (the question queues behind the other
@@ -662,7 +652,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 const int2 ext = ext_range<SPLIT>(z, cur, rank);
                 if (!__all_sync(0xffffffffu, tc_wait(smem_u32(&m->columns_full[item & 1]), (item >> 1) & 1, abort, fault))) break;
                 const int total = cur.count * z.rank;
-                const long long r = min(((long long)cur.rt * z.share + row_rank()) * kTileRows + row, z.rows - 1);
+                const long long r = min((long long)cur.rt * kTileRows + row, z.rows - 1);
                 for (int e = ext.x + g; e < (ext.y - ext.x + 3) / 4 * 4 + ext.x; e += 4, ++it) {
                     const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
                     const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
@@ -791,7 +781,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
             if (w + 2 * step < n_items) load(next_t);
             after = ahead(w + 3 * step);
             const int n8 = round16(cur.n) / 8;
-            const long long row = ((long long)cur.rt * z.share + row_rank()) * kTileRows + my_row;
+            const long long row = (long long)cur.rt * kTileRows + my_row;
             char *out = static_cast<char *>(z.y) + (swiglu ? row / 2 : row) * kOut;
             const int ks = z.ksplit;
             uint32_t base = lane_base + run;                // where the tile's sums are
@@ -905,7 +895,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (z.cluster > 1) cluster_sync();
+    if (z.ksplit > 1) cluster_sync();
     if (warp == kWarpMma) tmem_dealloc(tmem, (uint32_t)z.tmem_cols);
 }
 
@@ -1532,7 +1522,7 @@ Layout layout(const MatmulArgs &a) {
     return l;
 }
 
-struct TcPlan { int tile_n, ksplit, share, grid, raw_slots, x_slots, x_k, deep, tmem_cols; size_t smem; uint32_t off_raw, off_red; };
+struct TcPlan { int tile_n, ksplit, grid, raw_slots, x_slots, x_k, deep, tmem_cols; size_t smem; uint32_t off_raw, off_red; };
 
 // Memory of a launch with tiles of p->tile_n tokens and the columns split over p->ksplit CTAs; false if it does not fit.
 bool fit_smem(const DeviceInfo &dev, int fmt, bool split, TcPlan *p) {
@@ -1579,7 +1569,6 @@ bool make_plan(const DeviceInfo &dev, int fmt, bool split, int64_t groups, int64
             TcPlan p = {};
             p.tile_n = tn;
             p.ksplit = ks;
-            p.share = 1;
             if (!fit_smem(dev, fmt, split, &p)) continue;
             const int64_t clusters = dev.num_sms / ks;
             const int64_t waves = (groups * tt * n_rt + clusters - 1) / clusters;
@@ -1598,8 +1587,7 @@ bool make_plan(const DeviceInfo &dev, int fmt, bool split, int64_t groups, int64
     best->deep = sums + 2 * slots <= 512;
     best->tmem_cols = 32;
     while (best->tmem_cols < sums + slots * (best->deep ? 2 : 1)) best->tmem_cols *= 2;
-    if (!split && best->ksplit == 1 && best->tile_n >= 64 && n_rt > 1) best->share = 2;
-    best->grid = dev.num_sms / (best->ksplit * best->share) * (best->ksplit * best->share);
+    best->grid = dev.num_sms / best->ksplit * best->ksplit;
     return true;
 }
 
@@ -1619,7 +1607,7 @@ hq_status configure(int dynamic) {
 template <int FMT, bool SPLIT, int OT>
 hq_status launch_tc(const TcArgs &t, const TcPlan &p, cudaStream_t stream) {
     hq_status st = configure<matmul_tc_kernel<FMT, SPLIT, OT>>(232448);
-    return st != HQ_OK ? st : launch(matmul_tc_kernel<FMT, SPLIT, OT>, p.grid, Roles<SPLIT>::kThreads, p.smem, p.ksplit * p.share, stream, "matmul", t);
+    return st != HQ_OK ? st : launch(matmul_tc_kernel<FMT, SPLIT, OT>, p.grid, Roles<SPLIT>::kThreads, p.smem, p.ksplit, stream, "matmul", t);
 }
 
 template <int FMT>
@@ -1770,7 +1758,7 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
     t.z.rows = a.rows;
     t.z.n_tokens = (int)a.n_tokens;
     t.z.n_tt = (int)((a.n_tokens + p.tile_n - 1) / p.tile_n);
-    t.z.n_rt = (int)((n_rt + p.share - 1) / p.share);
+    t.z.n_rt = (int)n_rt;
     t.z.n_items = (int)((a.moe ? most_tiles(a) : t.z.n_tt) * t.z.n_rt);
     t.z.n_chunks = n_chunks;
     t.z.tile_n = p.tile_n;
@@ -1779,9 +1767,7 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
     t.z.x_k = p.x_k;
     t.z.deep = p.deep;
     t.z.ksplit = p.ksplit;
-    t.z.share = p.share;
-    t.z.cluster = p.ksplit * p.share;
-    t.z.step = p.grid / t.z.cluster;
+    t.z.step = p.grid / p.ksplit;
     t.z.tmem_cols = p.tmem_cols;
     t.z.epilogue = a.epilogue == HQ_MOE_EPI_SWIGLU ? HQ_MOE_EPI_SWIGLU : 0;
     t.z.stream_w = !a.moe && t.z.n_tt == 1;

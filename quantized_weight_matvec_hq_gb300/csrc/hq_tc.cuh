@@ -87,11 +87,6 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// The same on the barriers at this place in every CTA of the cluster that `mask` names.
-__device__ __forceinline__ void tc_commit_multicast(uint32_t bar, uint16_t mask) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"(mask) : "memory");
-}
-
 // Shared-memory descriptor of a K-major tile of 128-byte rows (64 16-bit
 // elements) in the 128-byte swizzle: rows of 8 repeat every 1024 bytes.
 __device__ __forceinline__ uint64_t tc_desc_sw128(uint32_t addr) {
@@ -146,15 +141,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%2, %3, %4}], [%5], %6;"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy) : "memory");
-}
-
-// The same into every CTA of the cluster that `mask` names, at the same place of its memory, completing on its barrier there.
-__device__ __forceinline__ void tma_load_3d_multicast(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar, uint64_t policy,
-                                                      uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6, %7;"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "h"(mask), "l"(policy) : "memory");
 }
 
 __device__ __forceinline__ uint64_t l2_evict_normal_policy() {

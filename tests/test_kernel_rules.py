@@ -39,3 +39,9 @@ def test_peers_have_started_before_their_shared_memory_is_accessed():
                 found.append(name)
                 assert re.search(r"\bcluster_(?:sync|wait)\s*\(\)", body[:first.start()]), name
     assert {"softmax_kernel", "verify_kernel", "adapter_down", "matmul_tc_kernel", "plan_slots", "matvec_tma_kernel"} <= set(found)
+
+
+def test_no_load_writes_to_more_than_one_block():
+    """Cluster multicast is for a GPU's own memory; a caller's x or W may be mapped from elsewhere."""
+    for path in sorted(glob.glob(os.path.join(CSRC, "*"))):
+        assert "multicast" not in source(os.path.basename(path)), path
