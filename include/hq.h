@@ -419,6 +419,7 @@ hq_status hq_moe_matmul_q8_0(const void *W_bank, const int32_t *w_exp, const int
  *   n_tokens : 0..2^27 (0 launches nothing).  cols % 256 == 0.
  *   workspace : hq_matmul_adapters_workspace() bytes, 256-byte aligned (a HOST
  *       function; negative: the hq_status of refused arguments).
+ * Each token's row depends on its own adapter only: infinities and NaN of another's stay with that one's tokens.
  * Accuracy of the base term as for hq_moe_matmul_q8_0; the adapter term takes x, A and B
  * exactly and sums in fp32, with A x in between rounded to 16 bits (f32: 24).  An id outside [-1, n_adapters) gives a NaN row of y and
  * HQ_FAULT_ADAPTER_ID.

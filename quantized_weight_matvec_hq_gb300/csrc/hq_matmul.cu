@@ -120,7 +120,8 @@ struct Meta {
     uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw], x_full[kMaxX], x_empty[kMaxX], full[4], empty[4];
     uint64_t acc_full[2], acc_empty[2], columns_full[2], red_full, red_empty, done;
     uint32_t tmem;
-    int abort, wide[2];             // wide: number of the last (even, odd) item with a column whose scale is no float
+    // wide: number of the last (even, odd) item with a column whose scale is no float; odd: with an infinity or NaN in B
+    int abort, wide[2], odd[2];
     Columns columns[2];             // of this item and the next
 };
 
@@ -324,6 +325,43 @@ __device__ __forceinline__ void load_b(const Sizes &a, const int *list, int tota
     }
 }
 
+// In the product, an infinity or NaN of B would meet the zeros of other adapters' tokens and spoil them: its exponent loses a
+// bit there (whether there was one), and add_odd_b adds what it stands for to its own adapter's tokens.
+__device__ __forceinline__ bool take_odd_b(uint32_t (&b)[16]) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) any = __vmaxu2(any, b[i] & 0x7fff7fffu);
+    if ((any & 0xffffu) < 0x7f80u && any >> 16 < 0x7f80u) return false;
+    // an exponent of ones carries into the sign's place
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i] &= ~((((b[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 1);
+    return true;
+}
+
+// The terms of B's infinities and NaN to 8 columns of one output row, over this CTA's virtual ranks.
+template <bool SPLIT>
+__device__ __forceinline__ void add_odd_b(const Sizes &a, const Columns *m, const Item &t, int rank, long long row, int c0, float (&v)[8]) {
+    const int2 ext = ext_range<SPLIT>(a, t, rank);
+    const int lo = ext.x * Ext<SPLIT>::kRanks, hi = ext.y * Ext<SPLIT>::kRanks;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+        const int place = c0 + j < t.n ? m->place[c0 + j] : -1;
+        float s = 0.f;
+        if (place >= 0 && row < a.rows) {
+            const uint16_t *b = a.B + ((long long)m->list[place] * a.rows + row) * a.rank;
+            const float *u = a.u + (long long)(t.start + c0 + j) * a.rank;
+#pragma unroll 1
+            for (int k = max(0, lo - place * a.rank); k < min(a.rank, hi - place * a.rank); ++k) {
+                const float f = __uint_as_float((uint32_t)b[k] << 16);
+                if (!(fabsf(f) < INFINITY)) s += f * u[k];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += i == j ? s : 0.f;
+    }
+    __syncwarp();
+}
+
 // Row `c` of the token operand: u of the token's own adapter at its virtual ranks, as bf16 terms side by side, zero elsewhere.
 template <bool SPLIT>
 __device__ __forceinline__ void store_u(const Sizes &a, const Columns *m, const Item &t, int v0, int c, uint8_t *dst) {
@@ -398,7 +436,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         for (int i = 0; i < z.x_slots; ++i) { mbar_init(smem_u32(&m->x_full[i]), 1); mbar_init(smem_u32(&m->x_empty[i]), 1); }
         for (int i = 0; i < 4; ++i) { mbar_init(smem_u32(&m->full[i]), z.deep ? kDecodeWarps : 4); mbar_init(smem_u32(&m->empty[i]), 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&m->acc_full[i]), 1); mbar_init(smem_u32(&m->acc_empty[i]), kEpiWarps); }
-        m->wide[0] = m->wide[1] = 0;
+        m->wide[0] = m->wide[1] = m->odd[0] = m->odd[1] = 0;
         mbar_init(smem_u32(&m->done), 1);
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&m->columns_full[i]), kEpiWarps);
         mbar_init(smem_u32(&m->red_full), (uint32_t)max(1, (z.ksplit - 1) * kEpiWarps));
@@ -657,7 +695,10 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                     const uint32_t bar = z.deep ? it & 1 : g, par = z.deep ? (it >> 1) & 1 : it & 1;
                     const uint32_t dst = lane_base + (z.deep ? (it & 1) * 4 * kSlotCols : 0) + g * kTerms * kSlotCols;
                     uint32_t b[16] = {};
-                    if (e < ext.y) load_b<SPLIT>(z, m->columns[item & 1].list, total, e * Ext<SPLIT>::kRanks, r, b);
+                    if (e < ext.y) {
+                        load_b<SPLIT>(z, m->columns[item & 1].list, total, e * Ext<SPLIT>::kRanks, r, b);
+                        if (take_odd_b(b)) *(volatile int *)&m->odd[item & 1] = (int)item + 1;
+                    }
                     // the token stage that quarter g of this chunk falls on
                     const uint32_t xi = (it * 4 + g) / z.x_k, sx = xi % z.x_slots;
                     tc_wait_go(false, smem_u32(&m->empty[bar]), par ^ 1, abort, fault);
@@ -824,6 +865,17 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 if (!ok) continue;
                 tc_fence_after();
                 base = lane_base + (acc & 1) * half;
+            }
+            if (*(volatile int *)&m->odd[item & 1] == (int)item + 1) {
+#pragma unroll 1
+                for (int g = side; g < n8; g += kSides) {
+                    float v[8];
+                    tmem_ld8(base + 8 * g, v);
+                    tmem_wait_ld(v);
+                    add_odd_b<SPLIT>(z, &m->columns[item & 1], cur, rank, row, 8 * g, v);
+                    tmem_st8(base + 8 * g, v);
+                }
+                tmem_wait_st();
             }
             if (ks == 1) {
                 // 8 columns at a time, the next ones on their way meanwhile

@@ -1,0 +1,78 @@
+"""Values at the ends of their range through the batched step, against plain
+64-bit statements: infinities and NaN stay where the definition has them."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import test_gpu_batch as tb
+from quantized_weight_matvec_hq_gb300 import synthetic
+from test_gpu_batch import DT, U_OUT, base_tol, dense, dev, exponents, hq, no_device_fault, run_lora, weights  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def assert_same_kind(y, ref, what):
+    """Infinities with their signs and NaN exactly where the reference has them."""
+    y = y.double().cpu().numpy()
+    for name, kind in (("NaN", np.isnan), ("+inf", lambda v: v == np.inf), ("-inf", lambda v: v == -np.inf)):
+        wrong = kind(y) != kind(ref)
+        assert not wrong.any(), (what, name, np.argwhere(wrong)[:5].tolist(), y[wrong][:5], ref[wrong][:5])
+
+
+def assert_near_or_same_kind(y, ref, tol, what):
+    assert_same_kind(y, ref, what)
+    ok = np.isfinite(ref)
+    got = y.double().cpu().numpy()
+    bad = ok & ~(np.abs(np.where(ok, got, 0) - np.where(ok, ref, 0)) <= np.where(ok, tol, 0))
+    assert not bad.any(), (what, np.argwhere(bad)[:5].tolist(), got[bad][:5], ref[bad][:5], tol[bad][:5])
+
+
+def adapted(hq, fmt, rows, cols, T, n, rank, dtype, seed, spoil=None):
+    """A call, the 64-bit result and its tolerance; `spoil` changes x, A, B and the scales before."""
+    g = synthetic.rng(seed)
+    blocks = weights(g, fmt, rows, cols)
+    W = dev(blocks)
+    e = exponents(hq, fmt, W, 1, rows, cols)
+    x = torch.from_numpy(g.standard_normal((T, cols)).astype(np.float32)).cuda().to(DT[dtype])
+    A = (torch.from_numpy(g.standard_normal((n, rank, cols)).astype(np.float32)) * 0.05).bfloat16().cuda()
+    B = (torch.from_numpy(g.standard_normal((n, rows, rank)).astype(np.float32)) * 0.05).bfloat16().cuda()
+    s = dev(g.uniform(0.5, 2, n).astype(np.float32) * np.where(np.arange(n) % 2, -1, 1).astype(np.float32))
+    ids = g.integers(-1, n, T)
+    ids[:min(T, n + 1)] = np.arange(-1, n)[:min(T, n + 1)]      # every adapter and none, in one tile
+    if spoil:
+        spoil(x, A, B, s)
+    y = run_lora(hq, fmt, W, e, x, dev(ids.astype(np.int32)), A, B, s, n, rank, rows, cols, dtype)
+    xd, Wd = x.double().cpu().numpy(), dense(fmt, blocks, rows, cols)
+    Ad, Bd, sd = A.double().cpu().numpy(), B.double().cpu().numpy(), s.double().cpu().numpy()
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref, tol = xd @ Wd.T, base_tol(dtype, np.abs(xd) @ np.abs(Wd).T, cols)
+        for a in range(n):
+            t = np.nonzero(ids == a)[0]
+            u, um = xd[t] @ Ad[a].T, np.abs(xd[t]) @ np.abs(Ad[a]).T
+            ref[t] += sd[a] * (u @ Bd[a].T)
+            # fp32 sums of the columns and of the ranks; u rounded to 16 bits (f32: 24)
+            tol[t] += abs(sd[a]) * (um @ np.abs(Bd[a]).T) * ((cols / 8 + 64 + rank) * 2.0 ** -23 + (0 if dtype == "f32" else 2.0 ** -16))
+        tol = tol + U_OUT[dtype] * (np.abs(ref) + tol) + 2.0 ** -25
+    return y, ref, tol, ids
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("fmt,rows,cols,T,n,rank", [("q8_0", 300, 1024, 70, 3, 16), ("q4_0", 130, 2048, 5, 3, 5),
+                                                    ("q8_0", 77, 512, 9, 4, 64), ("q8_0", 700, 512, 400, 5, 64),
+                                                    ("q4_0", 256, 768, 33, 6, 16), ("q8_0", 20000, 256, 40, 3, 5)])
+def test_non_finite_adapter_stays_with_its_tokens(hq, fmt, rows, cols, T, n, rank, dtype):
+    """Infinities and NaN in one adapter's B reach that adapter's tokens, in
+    those rows, and no token of another adapter or of none."""
+    def spoil(x, A, B, s):
+        B[1, 17, rank - 1] = float("inf")
+        B[1, 40, 0] = float("-inf")
+        B[1, rows - 1, rank // 2] = float("nan")
+        B[1, 5, 1], B[1, 5, 2] = float("inf"), float("-inf")
+        B[1, 6, :] = float("inf")
+        B[2, 17, 0] = float("inf")
+    y, ref, tol, ids = adapted(hq, fmt, rows, cols, T, n, rank, dtype, 300 + rows + rank, spoil)
+    assert np.isfinite(ref[ids != 1][:, 18:]).all() and np.isfinite(ref[(ids != 1) & (ids != 2)]).all()
+    assert np.isnan(ref[ids == 1][:, -1]).all() and np.isinf(ref[ids == 1][:, 17]).all()
+    assert_near_or_same_kind(y, ref, tol, "mixed adapters")
