@@ -1204,11 +1204,12 @@ __device__ void pack_rows(const PrepArgs &a, int block) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float f0 = v[2 * k] * s1 * s2, f1 = v[2 * k + 1] * s1 * s2;
-                    const __half2 p = __floats2half2_rn(f0, f1);
+                    // Of two terms, an infinity or a NaN is the second one: the first meets the weights' second terms as well,
+                    // whose zeros and other signs would make NaN of an infinity.
+                    const __half2 p = a.lo ? __floats2half2_rn(fminf(fmaxf(f0, -65504.f), 65504.f), fminf(fmaxf(f1, -65504.f), 65504.f))
+                                           : __floats2half2_rn(f0, f1);
                     h[k] = *reinterpret_cast<const uint32_t *>(&p);
-                    // the rest of an infinity or a NaN is nothing
-                    const float g0 = f0 - __low2float(p), g1 = f1 - __high2float(p);
-                    const __half2 q = __floats2half2_rn(fabsf(f0) < INFINITY ? g0 : 0.f, fabsf(f1) < INFINITY ? g1 : 0.f);
+                    const __half2 q = __floats2half2_rn(f0 - __low2float(p), f1 - __high2float(p));
                     l[k] = *reinterpret_cast<const uint32_t *>(&q);
                 }
 #pragma unroll

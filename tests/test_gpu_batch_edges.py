@@ -76,3 +76,25 @@ def test_non_finite_adapter_stays_with_its_tokens(hq, fmt, rows, cols, T, n, ran
     assert np.isfinite(ref[ids != 1][:, 18:]).all() and np.isfinite(ref[(ids != 1) & (ids != 2)]).all()
     assert np.isnan(ref[ids == 1][:, -1]).all() and np.isinf(ref[ids == 1][:, 17]).all()
     assert_near_or_same_kind(y, ref, tol, "mixed adapters")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,T", [(140, 37), (130, 200)])
+def test_infinite_tokens_have_the_sign_of_their_weights(hq, rows, T, dtype):
+    """One infinite element of a token: each output is the infinity of its
+    weight's sign, and NaN where that weight is zero."""
+    g = synthetic.rng(332 + rows)
+    cols = 512
+    blocks = weights(g, "q8_0", rows, cols)
+    Wd = dense("q8_0", blocks, rows, cols)
+    W = dev(blocks)
+    x = torch.from_numpy(g.standard_normal((T, cols)).astype(np.float32)).cuda().to(DT[dtype])
+    x[5, 7], x[20, 300], x[21, 9] = float("nan"), float("inf"), float("-inf")
+    y = run_lora(hq, "q8_0", W, exponents(hq, "q8_0", W, 1, rows, cols), x, None, None, None, None, 0, 0, rows, cols, dtype)
+    xd = x.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        ref = np.where(np.isfinite(xd), xd, 0) @ Wd.T
+        for t, j in ((5, 7), (20, 300), (21, 9)):
+            ref[t] = ref[t] + xd[t, j] * Wd[:, j]
+    assert np.isinf(ref[20]).any()
+    assert_same_kind(y, ref, dtype)
