@@ -387,7 +387,8 @@ hq_status hq_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_
  * of their row's largest are rounded to multiples of 2^-39 of it), sums are fp32, y is rounded
  * once.  f32: both factors are split in two 11-bit terms and the
  * product of the two small terms is left out: relative error of a
- * product below 2^-20 (weights below 2^-17 of their matrix's largest: 2^-36 of that).
+ * product below 2^-20 (weights below 2^-17 of their matrix's largest: 2^-36 of that; elements of x below 2^-17 of
+ * their row's largest: 2^-38 of that).
  * The fp32 sums of f32 leave the tensor core every 256 columns.
  * Deterministic: the bits of a token's y do not depend on the other tokens, except through the
  * split of the columns over CTAs that the launch's sizes choose.
@@ -413,13 +414,14 @@ hq_status hq_moe_matmul_q8_0(const void *W_bank, const int32_t *w_exp, const int
  *       Tokens of one request next to each other share the adapter's bytes.
  *   lora_A : bf16 [n_adapters][rank][cols], 16-byte aligned.
  *   lora_B : bf16 [n_adapters][rows][rank], 2-byte aligned.
- *   scales : fp32 [n_adapters].   rank : 1..64 (adapters of smaller rank are padded with zeros).
+ *   scales : fp32 [n_adapters], finite.   rank : 1..64 (adapters of smaller rank are padded with zeros).
  *   n_adapters : >= 0; with 0 the adapter arguments are not read (they may be NULL) and the
  *       call is the plain many-token product.
  *   n_tokens : 0..2^27 (0 launches nothing).  cols % 256 == 0.
  *   workspace : hq_matmul_adapters_workspace() bytes, 256-byte aligned (a HOST
  *       function; negative: the hq_status of refused arguments).
  * Each token's row depends on its own adapter only: infinities and NaN of another's stay with that one's tokens.
+ * An infinity or NaN in an adapter's A gives its tokens outputs that are infinite or NaN.
  * Accuracy of the base term as for hq_moe_matmul_q8_0; the adapter term takes x, A and B
  * exactly and sums in fp32, with A x in between rounded to 16 bits (f32: 24).  An id outside [-1, n_adapters) gives a NaN row of y and
  * HQ_FAULT_ADAPTER_ID.

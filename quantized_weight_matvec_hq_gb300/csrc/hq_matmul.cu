@@ -293,6 +293,18 @@ __device__ __forceinline__ void finish(const Columns *m, bool swiglu, bool wide,
 
 // ------------------------------------------------------------------ adapter quarters
 
+// The next bf16 terms of v0 and v1, which they lose.  Any but the last is kept finite: an infinity (or a finite value that rounds to
+// one) would leave a NaN behind, while as the last term it stays what it is.
+template <bool LAST>
+__device__ __forceinline__ uint32_t take_term(float &v0, float &v1) {
+    uint32_t h;
+    if constexpr (LAST) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(v1), "f"(v0));
+    else asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(v1), "f"(v0));
+    v0 -= __uint_as_float(h << 16);
+    v1 -= __uint_as_float(h & 0xffff0000u);
+    return h;
+}
+
 // Virtual ranks [v0, v0 + kRanks) of one row of the tile's adapters' B, packed in pairs.
 template <bool SPLIT>
 __device__ __forceinline__ void load_b(const Sizes &a, const int *list, int total, int v0, long long row, uint32_t (&b)[16]) {
@@ -397,12 +409,7 @@ __device__ __forceinline__ void store_u(const Sizes &a, const Columns *m, const 
         for (int i = 0; i < T; ++i) {
             uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-                f[2 * k] -= __low2float(h);
-                f[2 * k + 1] -= __high2float(h);
-                w[k] = *reinterpret_cast<const uint32_t *>(&h);
-            }
+            for (int k = 0; k < 4; ++k) w[k] = i + 1 < T ? take_term<false>(f[2 * k], f[2 * k + 1]) : take_term<true>(f[2 * k], f[2 * k + 1]);
             *reinterpret_cast<uint4 *>(line + (((i * R + k0) / 8 ^ (c & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
@@ -1352,12 +1359,7 @@ __device__ void adapter_down(const PrepArgs &a, int window, int turn) {
                 for (int i = 0; i < TERMS; ++i) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                        w[k] = *reinterpret_cast<const uint32_t *>(&h);
-                        v[2 * k] -= __low2float(h);
-                        v[2 * k + 1] -= __high2float(h);
-                    }
+                    for (int k = 0; k < 4; ++k) w[k] = i + 1 < TERMS ? take_term<false>(v[2 * k], v[2 * k + 1]) : take_term<true>(v[2 * k], v[2 * k + 1]);
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         const uint4 lo = b.p[2 * m], hi = b.p[2 * m + 1];

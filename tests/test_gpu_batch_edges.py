@@ -79,6 +79,42 @@ def test_non_finite_adapter_stays_with_its_tokens(hq, fmt, rows, cols, T, n, ran
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_infinite_adapter_leaves_other_tokens_alone(hq, dtype):
+    """An infinity in an adapter's A: its tokens' outputs are no numbers or
+    infinite, the others as ever."""
+    def spoil(x, A, B, s):
+        A[1, 3, 100] = float("inf")
+    y, ref, tol, ids = adapted(hq, "q8_0", 200, 512, 40, 4, 9, dtype, 330, spoil)
+    assert not np.isfinite(ref[ids == 1]).any() and not torch.isfinite(y[dev(ids == 1)]).any()
+    assert_near_or_same_kind(y[dev(ids != 1)], ref[ids != 1], tol[ids != 1], "the rest")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_infinite_tokens_through_an_adapter(hq, dtype):
+    """At rank 1 an infinite element gives infinities of the signs of W and of
+    B A, and NaN where the two differ."""
+    def spoil(x, A, B, s):
+        x[:8, 77] = float("inf")
+        x[8:16, 400] = float("-inf")
+    y, ref, tol, ids = adapted(hq, "q8_0", 200, 512, 40, 4, 1, dtype, 334, spoil)
+    assert np.isinf(ref[:16]).any() and np.isnan(ref[:16]).any()
+    assert_near_or_same_kind(y, ref, tol, "infinite tokens")
+
+
+def test_largest_fp32_tokens_through_an_adapter(hq):
+    """Finite fp32 elements above the largest 16-bit brain float: finite
+    outputs, near but for what lies 2^-38 below a token's largest element."""
+    def spoil(x, A, B, s):
+        x[3, 50], x[4, 51] = 3.4e38, -3.4e38
+        A[:, :, 50:52] = 1e-20
+    y, ref, tol, ids = adapted(hq, "q8_0", 200, 512, 12, 2, 8, "f32", 331, spoil)
+    assert ids[3] >= 0 or ids[4] >= 0
+    assert np.isfinite(ref).all()
+    tol[3:5] += 512 * 2.0 ** -38 * 3.4e38 * 0.25            # weights of deviation 0.02 are below 0.25
+    assert_near_or_same_kind(y, ref, tol, "near the largest")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows,T", [(140, 37), (130, 200)])
 def test_infinite_tokens_have_the_sign_of_their_weights(hq, rows, T, dtype):
     """One infinite element of a token: each output is the infinity of its
