@@ -443,11 +443,11 @@ hq_status hq_matmul_q4_0_adapters(const void *W, const int32_t *w_exp, const voi
 /*
  * hq_softmax_rows -- probabilities of logits, one temperature per row:
  *   p[r][j] = exp((l[r][j] - max_j l[r][j]) / t_r) / sum_j exp(...),  t_r > 0;
- *   t_r <= 0 : greedy, p[r] is 1 at the first maximum and 0 elsewhere.
+ *   t_r <= 0 or NaN : greedy, p[r] is 1 at the first maximum and 0 elsewhere.
  *   logits : `dtype` [n_rows][vocab], aligned to its element.
  *   temperature : fp32 [n_rows], or NULL for 1.   p : fp32 [n_rows][vocab].
  *   n_rows : 0..2^28-1 (0 launches nothing).  vocab : 1..2^22.
- * Logits of -inf give 0.  A row of nothing but -inf gives zeros (greedy too).  A row with
+ * Logits of -inf give 0, at an infinite temperature too (all others are then equal).  A row of nothing but -inf gives zeros (greedy too).  A row with
  * a NaN or +inf gives NaNs (greedy: the first maximum of what is not NaN; a row of nothing
  * but NaN and -inf gives zeros).  p may be the logits' own
  * memory when dtype is HQ_DT_F32.

@@ -161,22 +161,25 @@ __global__ void __launch_bounds__(kThreads) softmax_kernel(SoftmaxArgs a) {
 
     float s = 0.f;
     const float mc = m == -INFINITY ? 0.f : m;
-    // e^((v - mc) / t) of 8 columns.  Mode 0: t is 1.  Mode 1: the quotient as a product with 1/t and one correction by its
+    // e^((v - mc) / t) of 8 columns.  Mode 0: t is 1.  Otherwise the quotient is a product with 1/t and one correction by its
     // remainder, three instructions for a division's ten; z is cut at -200 t, whose power is 0 as well, so that the
-    // remainder of -inf is no NaN (a NaN stays).  Mode 2: t so small or so large that 1/t or the cut leaves the range.
-    const int mode = t == 1.f ? 0 : t > 1e-18f && t < 1e18f ? 1 : 2;
-    const float rt = __frcp_rn(t), least = -200.f * t;
+    // remainder of -inf is no NaN (a NaN stays).  Mode 2 keeps 1/t and the cut in range: a large t is taken in units of 2^64, and
+    // so are the values, whose difference may be too large a float and still count (an infinite t: 1e30 of them, which makes
+    // every finite difference 0); for a small t the differences are taken in units of 2^-64.
+    const bool large = t >= 1e18f;
+    const int mode = t == 1.f ? 0 : t > 1e-18f && !large ? 1 : 2;
+    const float unit = large ? 0x1p-64f : 1.f, back = mode == 2 && !large ? 0x1p64f : 1.f;
+    const float ut = large ? fminf(t * 0x1p-64f, 1e30f) : t * back, rt = __frcp_rn(ut), least = -200.f * ut;
     auto power = [&](auto which, float (&v)[8]) {
         constexpr int MODE = decltype(which)::value;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            float z = v[k] - mc;
-            if constexpr (MODE == 1) {
+            float z = MODE == 2 ? (v[k] * unit - mc * unit) * back : v[k] - mc;
+            if constexpr (MODE > 0) {
                 asm("max.NaN.f32 %0, %0, %1;" : "+f"(z) : "f"(least));
                 const float q = z * rt;
-                z = fmaf(fmaf(-q, t, z), rt, q);
+                z = fmaf(fmaf(-q, ut, z), rt, q);
             }
-            if constexpr (MODE == 2) z = __fdiv_rn(z, t);
             v[k] = expf(z);
         }
     };
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) softmax_kernel(SoftmaxArgs a) {
         S = 0.f;
         // a part of nothing but -inf (m_c = -inf) has the sum 0, or NaN
         for (int r = 0; r < a.cluster; ++r) {
-            const float f = peer_m[r] == -INFINITY ? 1.f : expf(__fdiv_rn(peer_m[r] - M, t));
+            const float f = peer_m[r] == -INFINITY ? 1.f : expf(__fdiv_rn((peer_m[r] * unit - M * unit) * back, ut));
             if (r == rank) mine = f;
             S += greedy ? 0.f : peer_s[r] * f;
         }

@@ -134,3 +134,30 @@ def test_infinite_tokens_have_the_sign_of_their_weights(hq, rows, T, dtype):
             ref[t] = ref[t] + xd[t, j] * Wd[:, j]
     assert np.isinf(ref[20]).any()
     assert_same_kind(y, ref, dtype)
+
+
+@pytest.mark.parametrize("vocab", [50, 9001, 300_000])
+def test_softmax_at_the_ends_of_the_temperature(hq, vocab):
+    """Infinite and huge temperatures, differences past the largest float,
+    masked columns, and a temperature that is no number (greedy)."""
+    g = synthetic.rng(333)
+    l = g.standard_normal((6, vocab)).astype(np.float32) * 5
+    l[:, 3::7] = -np.inf
+    l[1, :] = np.where(np.isfinite(l[1]), np.sign(l[1]) * 3e38, -np.inf)
+    l[2, :] = np.where(np.isfinite(l[2]), l[2] * 1e37, -np.inf)
+    l[5, vocab // 2:] = -np.inf
+    t = np.array([np.inf, 1e38, 2e37, 1e-30, np.nan, np.inf], np.float32)
+    p = torch.full((6, vocab), float("nan"), device="cuda")
+    hq.hq_softmax_rows(dev(l), dev(t), p, 6, vocab, hq.HQ_DT_F32)
+    ld, td = l.astype(np.float64), t.astype(np.float64)
+    for r in range(6):
+        if np.isnan(td[r]):
+            ref = (np.arange(vocab) == int(np.argmax(ld[r]))).astype(np.float64)
+        else:
+            z = (np.where(np.isfinite(ld[r]), ld[r], 0) - ld[r].max()) / td[r]
+            ex = np.where(np.isfinite(ld[r]), np.exp(np.maximum(z, -1000)), 0)
+            ref = ex / ex.sum()
+        # the argument rounded three times (2^-22 of it), power and quotient a few ulps, a sum of rounded terms
+        tol = ref * (120 * 2.0 ** -22 + 2.0 ** -19) + 1e-44
+        got = p[r].double().cpu().numpy()
+        assert (np.abs(got - ref) <= tol).all(), (r, got[:8], ref[:8])
