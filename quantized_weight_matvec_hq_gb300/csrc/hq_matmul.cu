@@ -257,9 +257,10 @@ __device__ __forceinline__ void store_out(void *y, float v) {
 }
 
 // The 8 columns from c0 of one output row (its sums in v): scales, SwiGLU with the neighbouring lane's row, store.
-// `out` is the row's place in output row 0 and `pitch` the bytes of an output row; `live`: the row exists.
+// `out` is the row's place in output row 0 and `pitch` the elements of an output row; `live`: the row exists.
 template <int OT>
 __device__ __forceinline__ void finish(const Columns *m, bool swiglu, bool wide, int c0, int n, bool live, char *out, uint32_t pitch, float (&v)[8]) {
+    constexpr int kOut = OT == HQ_DT_F32 ? 4 : 2;
     const float4 *sp = reinterpret_cast<const float4 *>(m->scale + c0);
     const int4 *op = reinterpret_cast<const int4 *>(m->slot + c0);
     const float4 s0 = sp[0], s1 = sp[1];
@@ -282,13 +283,13 @@ __device__ __forceinline__ void finish(const Columns *m, bool swiglu, bool wide,
         for (int j = 0; j < 8; j += 2) {
             const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
             const float h = silu(odd ? got : v[j]) * (odd ? v[j + 1] : got);
-            if (live && c0 + j + (odd ? 1 : 0) < n) store_out<OT>(out + (uint64_t)(uint32_t)(odd ? slot[j + 1] : slot[j]) * pitch, h);
+            if (live && c0 + j + (odd ? 1 : 0) < n) store_out<OT>(out + (uint64_t)(uint32_t)(odd ? slot[j + 1] : slot[j]) * pitch * kOut, h);
         }
         return;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        if (live && c0 + j < n) store_out<OT>(out + (uint64_t)(uint32_t)slot[j] * pitch, v[j]);
+        if (live && c0 + j < n) store_out<OT>(out + (uint64_t)(uint32_t)slot[j] * pitch * kOut, v[j]);
 }
 
 // ------------------------------------------------------------------ adapter quarters
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
         const int my_row = (warp & 3) * 32 + lane;
         constexpr int kOut = OT == HQ_DT_F32 ? 4 : 2;
         const bool swiglu = z.epilogue == HQ_MOE_EPI_SWIGLU;
-        const uint32_t pitch = (uint32_t)(swiglu ? z.rows / 2 : z.rows) * kOut;     // rows x 272 bytes of weights fit the device
+        const uint32_t pitch = (uint32_t)(swiglu ? z.rows / 2 : z.rows);
         uint32_t acc = 0, item = 0;
         bool ok = true;
         // An item's columns, a thread each: loaded a whole item before they are stored, and its tile an item before that.

@@ -161,3 +161,28 @@ def test_softmax_at_the_ends_of_the_temperature(hq, vocab):
         tol = ref * (120 * 2.0 ** -22 + 2.0 ** -19) + 1e-44
         got = p[r].double().cpu().numpy()
         assert (np.abs(got - ref) <= tol).all(), (r, got[:8], ref[:8])
+
+
+def test_output_rows_of_4_gigabytes(hq):
+    """2^30 rows of fp32 outputs: the second token's row begins at byte 2^32.
+    4-bit weights of one block of columns, 155 GB of them."""
+    torch.cuda.empty_cache()
+    rows, cols, T = 1 << 30, 256, 2
+    if torch.cuda.mem_get_info()[0] < 200 << 30:
+        pytest.skip("200 GiB of free device memory needed")
+    W = torch.zeros((rows, 8, 18), dtype=torch.uint8, device="cuda")        # d = 0: zeros
+    at = [0, 1, 77, 1 << 20, (1 << 29) + 5, rows - 1]
+    half = torch.tensor(list(np.float16(0.5).tobytes()), dtype=torch.uint8, device="cuda")
+    for i, r in enumerate(at):
+        W[r, 0, :2] = half
+        W[r, 0, 2:] = 0x88                                                  # quants of 0 ...
+        W[r, 0, 2] = 0x89 + i                                               # ... but the first: 1 + i
+    x = torch.zeros((T, cols), device="cuda")
+    x[0, 0], x[1, 0] = 2.0, -3.0
+    e = torch.tensor([-11], dtype=torch.int32, device="cuda")               # 8 * 0.5 < 2^(e + 14)
+    y = run_lora(hq, "q4_0", W, e, x, None, None, None, None, 0, 0, rows, cols, "f32")
+    for i, r in enumerate(at):
+        assert y[:, r].tolist() == [1.0 + i, -1.5 * (1 + i)], r
+    assert [int(torch.count_nonzero(y[t])) for t in range(T)] == [len(at)] * T
+    del W, y
+    torch.cuda.empty_cache()
