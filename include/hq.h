@@ -35,6 +35,12 @@
  *     validated on the host before any launch; a non-OK status means nothing
  *     was launched (except HQ_ERR_LAUNCH, which reports the launch failure).
  *     A fault inside a kernel surfaces at the caller's next synchronization.
+ *     The matvec calls begin to read W (and an adapter's A) as soon as the
+ *     kernel before them in the stream lets its programmatic dependents start,
+ *     which without a trigger of its own is at its end: a kernel that writes
+ *     weights must not trigger them before its last write.  No kernel of this
+ *     library does.  The many-token calls read nothing before what precedes
+ *     the call in the stream is done.
  *   - Row-major layouts.  Quantized rows are packed blocks with no padding:
  *     row i of a Q8_0 matrix is bytes [i*cols/32*34, (i+1)*cols/32*34).
  *   - Block layouts (little-endian): Q8_0 = { uint16 fp16 d; int8 q[32] },

@@ -99,6 +99,7 @@ struct Sizes {
     int n_tokens, n_tt, n_items, n_rt, n_chunks;
     int tile_n, raw_slots, x_slots, x_k, deep, ksplit, step, tmem_cols;    // x_slots slots of x_k (1, 2 or 4) times 64 columns of tokens
     int epilogue, rank, stream_w;
+    int early;                      // one matrix's weights may be copied before the wait for the kernel before
     uint32_t off_raw, off_red;
 };
 
@@ -465,8 +466,10 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
     const int c_hi = (int)((long long)z.n_chunks * (rank + 1) / z.ksplit);
     const Cursor stride = cursor_at(z, step);
     Cursor at = cursor_at(z, min(first, z.n_items - 1));
-    // one matrix's weights may be fetched before the prepare kernel is done; everything else waits for it
-    if (z.tiles || warp != kWarpW) griddep_wait();
+    // One matrix's weights may be fetched before the prepare kernel is done, since that lets this one start only after its own
+    // wait for whatever comes before it in the stream, which may have written them.  Everything else waits for the prepare
+    // kernel, and where there is none (f16 without adapters) so do the weights.
+    if (!z.early || warp != kWarpW) griddep_wait();
     Item t = {};
     if (z.tiles || warp != kWarpW) t = get_item(z, at);
     const int n_items = z.tiles ? *z.n_tiles * z.n_rt : z.n_items;
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 if (z.tiles && w + step < n_items) t = get_item(z, at);
                 for (int c = c_lo; c < c_hi; ++c, ++it) {
                     // past the first slots the wait is for this kernel's own warps, which wait for the prepare kernel
-                    if (!z.tiles && it == (uint32_t)z.raw_slots) griddep_wait();
+                    if (z.early && it == (uint32_t)z.raw_slots) griddep_wait();
                     ok = tc_wait(smem_u32(&m->raw_empty[s]), ph, abort, fault);
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&m->raw_full[s]);
@@ -1413,8 +1416,8 @@ __device__ void adapter_down(const PrepArgs &a, int window, int turn) {
 // tokens).  A copy a slot, so that the products fetch a tile of tokens with one instruction.
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_constant__ PrepArgs a) {
     extern __shared__ float dyn[];
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();                            // after the wait: the products' first weights rely on it
     const int b = blockIdx.x;
     if (b < a.plan_blocks) plan_slots<kPrepThreads, false>(a, reinterpret_cast<int *>(dyn), 1, 0);
     else pack_rows(a, b - a.plan_blocks);
@@ -1424,8 +1427,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
 // which a warp has two units on their way: 2011 tokens at rank 64 and 4096 columns 31 us, 64 tokens at rank 16 14 us, one token 11 us
 // (a block a group of tokens instead of one an adapter and 16 tokens: 44 us and 23 us before).
 __global__ void __launch_bounds__(kPrepThreads) prepare_adapters_kernel(const __grid_constant__ PrepArgs a) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();                            // after the wait: the products' first weights rely on it
     int b = blockIdx.x;
     if (b < a.pack_blocks) { pack_rows(a, b); return; }
     b -= a.pack_blocks;
@@ -1827,6 +1830,7 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
     t.z.tmem_cols = p.tmem_cols;
     t.z.epilogue = a.epilogue == HQ_MOE_EPI_SWIGLU ? HQ_MOE_EPI_SWIGLU : 0;
     t.z.stream_w = !a.moe && t.z.n_tt == 1;
+    t.z.early = !a.moe && prep_grid > 0;
     t.z.off_raw = p.off_raw;
     t.z.off_red = p.off_red;
     const int out = a.epilogue == HQ_MOE_EPI_COMBINE ? HQ_DT_F32 : a.dtype;

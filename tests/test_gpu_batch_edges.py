@@ -186,3 +186,52 @@ def test_output_rows_of_4_gigabytes(hq):
     assert [int(torch.count_nonzero(y[t])) for t in range(T)] == [len(at)] * T
     del W, y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("adapters", [0, 2])
+def test_weights_written_just_before_the_product(hq, dtype, adapters):
+    """Quantizing, the exponents and the product back to back on one stream, and
+    the weights rewritten between the replays of a graph."""
+    g = synthetic.rng(335)
+    rows, cols, T = 1280, 1024, 24
+    src = [dev(synthetic.weights(g, rows, cols, s)) for s in (0.02, 0.5, 3.0)]
+    x = torch.from_numpy(g.standard_normal((T, cols)).astype(np.float32)).cuda().to(DT[dtype])
+    A, B = torch.zeros((2, 4, cols), dtype=torch.bfloat16, device="cuda"), torch.zeros((2, rows, 4), dtype=torch.bfloat16, device="cuda")
+    s, ids = torch.ones(2, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    W = torch.empty(rows * cols // 32 * 34, dtype=torch.uint8, device="cuda")
+    e = torch.empty(1, dtype=torch.int32, device="cuda")
+    w = torch.empty_like(src[0])
+    y = torch.empty((T, rows), dtype=DT[dtype], device="cuda")
+    ws = tb.dirty(hq.hq_matmul_adapters_workspace(4 if adapters else 0, rows, cols, T, hq.DTYPE_CODES[dtype]))
+
+    def step():
+        hq.hq_quantize_q8_0(w, W, rows, cols)
+        hq.hq_weight_exponents(8, W, e, 1, rows, cols)
+        hq.hq_matmul_q8_0_adapters(W, e, x, ids, A, B, s, adapters, 4, y, rows, cols, T, hq.DTYPE_CODES[dtype], ws, ws.numel())
+
+    want = []
+    for m in src:
+        w.copy_(m)
+        hq.hq_quantize_q8_0(w, W, rows, cols)
+        torch.cuda.synchronize()
+        Wd = dense("q8_0", W.cpu().numpy(), rows, cols)
+        xd = x.double().cpu().numpy()
+        want.append((xd @ Wd.T, base_tol(dtype, np.abs(xd) @ np.abs(Wd).T, cols)))
+
+    def check(i):
+        ref, tol = want[i]
+        tb.assert_near(y, ref, tol + U_OUT[dtype] * (np.abs(ref) + tol) + 2.0 ** -25, f"weights {i}")
+    for i in (0, 1, 2, 0):
+        w.copy_(src[i])
+        step()
+        check(i)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for i in (1, 2, 0, 1):
+        w.copy_(src[i])
+        graph.replay()
+        check(i)

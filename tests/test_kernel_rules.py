@@ -45,3 +45,15 @@ def test_no_load_writes_to_more_than_one_block():
     """Cluster multicast is for a GPU's own memory; a caller's x or W may be mapped from elsewhere."""
     for path in sorted(glob.glob(os.path.join(CSRC, "*"))):
         assert "multicast" not in source(os.path.basename(path)), path
+
+
+def test_weights_are_copied_early_only_behind_a_kernel_that_has_waited():
+    """The many-token product may copy weights before its own wait, so the
+    kernel in front of it lets it start only after that kernel's wait: what
+    wrote the weights, one kernel further back, is then done."""
+    bodies = dict(device_functions("hq_matmul.cu"))
+    for name in ("prepare_kernel", "prepare_adapters_kernel"):
+        assert bodies[name].index("griddep_wait()") < bodies[name].index("griddep_launch_dependents()"), name
+    first = bodies["matmul_tc_kernel"].index("griddep_wait()")
+    assert bodies["matmul_tc_kernel"][:first].endswith("if (!z.early || warp != kWarpW) ")
+    assert "z.early = !a.moe && prep_grid > 0;" in source("hq_matmul.cu")
