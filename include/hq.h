@@ -515,9 +515,11 @@ hq_status hq_requant_i32_debug(const int32_t *acc, const int32_t *mult, const in
 
 /*
  * Device fault word.  Kernels never trap: a bounded wait that gives up (a
- * TMA transfer that never completes) or an out-of-range expert id sets a bit
- * in a per-device word and the kernel finishes without using the missing
- * data.  hq_device_fault() synchronizes the current device, returns the word
+ * TMA transfer that never completes) or an out-of-range id sets a bit
+ * in a per-device word, whatever it holds already, and the kernel finishes
+ * without the missing data (the many-token products run on over whatever their
+ * buffers hold, at the call's own addresses: after a time-out their
+ * outputs are wrong).  hq_device_fault() synchronizes the current device, returns the word
  * in *fault (0 = none) and clears it; it returns HQ_ERR_DEVICE if the word
  * was non-zero.  Bits 0..7 are the HQ_FAULT_* flags; when the first fault of
  * the word was a timeout, bits 9..31 hold the index of the CTA that gave up
@@ -540,6 +542,24 @@ hq_status hq_device_fault(uint32_t *fault);
  * Source: none on the pages (a property of this implementation's waits).
  */
 hq_status hq_selftest_wait_timeout(int64_t cycles, hq_stream_t stream);
+
+/*
+ * hq_selftest_wait -- test-only, the same for each kind of bounded wait, with a
+ * fault word that is not empty.
+ *   wait  : HQ_WAIT_MATVEC (as hq_selftest_wait_timeout), HQ_WAIT_CLUSTER (on
+ *           arrivals of another CTA of a cluster), HQ_WAIT_MATMUL and
+ *           HQ_WAIT_MATMUL_GO (the many-token products': whose result is
+ *           tested, and whose is not; the latter counts sleeps of about
+ *           65536 cycles).
+ *   fault : HQ_FAULT_* flags of data faults that are in the word before; the
+ *           time-out's flag has to join them.
+ * Source: none on the pages (a property of this implementation's waits).
+ */
+#define HQ_WAIT_MATVEC 0
+#define HQ_WAIT_CLUSTER 1
+#define HQ_WAIT_MATMUL 2
+#define HQ_WAIT_MATMUL_GO 3
+hq_status hq_selftest_wait(int wait, uint32_t fault, int64_t cycles, hq_stream_t stream);
 
 /*
  * hq_launch_count -- the number of kernels the library has launched (or

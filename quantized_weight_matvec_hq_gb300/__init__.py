@@ -25,6 +25,7 @@ from ._binding import (  # noqa: F401
     hq_matmul_q8_0_adapters, hq_matmul_q4_0_adapters, hq_softmax_rows, hq_verify_drafts,
     HQ_FAULT_ADAPTER_ID, HQ_FAULT_DRAFT, HQ_DT_F32, HQ_DT_F16, HQ_DT_BF16, DTYPE_CODES,
     hq_quantize_q8_0, hq_quantize_q4_0, hq_quantize_i8_rows, hq_requant_params,
-    hq_requant_i32_debug, hq_device_fault, hq_selftest_wait_timeout, hq_launch_count, hq_debug_plan,
+    hq_requant_i32_debug, hq_device_fault, hq_selftest_wait_timeout, hq_selftest_wait,
+    HQ_WAIT_MATVEC, HQ_WAIT_CLUSTER, HQ_WAIT_MATMUL, HQ_WAIT_MATMUL_GO, hq_launch_count, hq_debug_plan,
     Q8_0_BLOCK_BYTES, Q4_0_BLOCK_BYTES, QK, row_bytes,
 )

@@ -20,6 +20,7 @@ HQ_FAULT_WAIT_TIMEOUT = 1
 HQ_FAULT_EXPERT_ID = 2
 HQ_FAULT_ADAPTER_ID = 4
 HQ_FAULT_DRAFT = 8
+HQ_WAIT_MATVEC, HQ_WAIT_CLUSTER, HQ_WAIT_MATMUL, HQ_WAIT_MATMUL_GO = 0, 1, 2, 3
 
 QK = 32
 Q8_0_BLOCK_BYTES = 34
@@ -83,6 +84,7 @@ _SIGS = {
     "hq_verify_drafts": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp], _int),
     "hq_device_fault": ([_vp], _int),
     "hq_selftest_wait_timeout": ([_i64, _vp], _int),
+    "hq_selftest_wait": ([_int, ctypes.c_uint32, _i64, _vp], _int),
     "hq_launch_count": ([], ctypes.c_uint64),
     "hq_debug_plan": ([_int, _int, _i64, _i64, _int, _int, _int, ctypes.POINTER(ctypes.c_int64), _int], _int),
 }
@@ -306,6 +308,11 @@ def hq_requant_params(M, n: int, mult, shift) -> int:
 def hq_requant_i32_debug(acc, mult, shift, y, n: int, rows: int, stream=None) -> int:
     return _check(lib().hq_requant_i32_debug(_addr(acc), _addr(mult), _addr(shift), _addr(y), n, rows,
                                              _stream(stream)))
+
+
+def hq_selftest_wait(wait: int, fault: int, cycles: int, stream=None) -> int:
+    """Test-only: one of the library's bounded waits times out after `cycles` SM cycles, with `fault` in the fault word."""
+    return _check(lib().hq_selftest_wait(int(wait), int(fault), int(cycles), _stream(stream)))
 
 
 def hq_selftest_wait_timeout(cycles: int, stream=None) -> int:

@@ -598,6 +598,17 @@ hq_status hq_selftest_wait_timeout(int64_t cycles, hq_stream_t stream) {
     return finish(launch_wait_timeout_selftest(dev->fault, cycles, (cudaStream_t)stream));
 }
 
+hq_status hq_selftest_wait(int wait, uint32_t fault, int64_t cycles, hq_stream_t stream) {
+    if (wait < HQ_WAIT_MATVEC || wait > HQ_WAIT_MATMUL_GO) return set_error(HQ_ERR_UNSUPPORTED, "wait %d is not HQ_WAIT_*", wait);
+    if (fault & ~(HQ_FAULT_EXPERT_ID | HQ_FAULT_ADAPTER_ID | HQ_FAULT_DRAFT))
+        return set_error(HQ_ERR_UNSUPPORTED, "fault 0x%x has bits that are no data fault's", fault);
+    if (cycles < 1 || cycles > 4000000000LL) return set_error(HQ_ERR_SHAPE, "cycles %lld not in [1, 4e9]", (long long)cycles);
+    DeviceInfo *dev = nullptr;
+    hq_status st = device_info(&dev);
+    if (st != HQ_OK) return st;
+    return finish(launch_wait_selftest(wait, fault, dev->fault, cycles, (cudaStream_t)stream));
+}
+
 hq_status hq_device_fault(uint32_t *fault) {
     if (!fault) return set_error(HQ_ERR_NULL, "fault must be non-null");
     DeviceInfo *dev = nullptr;

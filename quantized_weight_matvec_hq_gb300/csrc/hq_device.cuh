@@ -68,6 +68,11 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parit
     return ok != 0;
 }
 
+// A wait that gave up sets its bit whatever the word holds already; where it happened is kept if it is the word's first fault.
+__device__ __forceinline__ void note_timeout(uint32_t *fault, uint32_t site) {
+    if (atomicCAS(fault, 0u, site | kFaultWaitTimeout) != 0u) atomicOr(fault, kFaultWaitTimeout);
+}
+
 // Bounded wait on phase `parity` of an mbarrier (at most limit_cycles SM cycles).  `abort` is CTA-shared: once
 // any wait in the CTA (or, through the fault word, in any CTA) has timed out,
 // later waits return false at once so the kernel drains in bounded time.  The clock and
@@ -89,7 +94,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
                 // bits 8..31 keep where the first timeout happened: the CTA and
                 // whether the waiter was a consumer (bit 8 set) or the producer
                 const uint32_t site = ((blockIdx.x & 0x7fffffu) << 9) | ((threadIdx.x < 128u) ? 0x100u : 0u);
-                atomicCAS(fault, 0u, site | kFaultWaitTimeout);
+                note_timeout(fault, site);
                 *abort = 1;
                 return false;
             }
@@ -136,7 +141,8 @@ __device__ __forceinline__ void st_shared_cluster_s32(uint32_t addr, int v) {
 
 // As mbar_wait, with cluster-scope acquire (for barriers other CTAs arrive on).
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
-                                                  volatile int *abort, uint32_t *fault) {
+                                                  volatile int *abort, uint32_t *fault,
+                                                  long long limit_cycles = kWaitTimeoutCycles) {
     const long long t0 = sm_cycles();
 #pragma unroll 1
     for (uint32_t it = 0;; ++it) {
@@ -144,9 +150,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         if ((it & 255u) == 255u) {
             if (*abort) return false;
             if (*(volatile uint32_t *)fault & kFaultWaitTimeout) { *abort = 1; return false; }
-            if (sm_cycles() - t0 > kWaitTimeoutCycles) {
+            if (sm_cycles() - t0 > limit_cycles) {
                 const uint32_t site = ((blockIdx.x & 0x7fffffu) << 9) | 0x100u;
-                atomicCAS(fault, 0u, site | kFaultWaitTimeout);
+                note_timeout(fault, site);
                 *abort = 1;
                 return false;
             }

@@ -1499,6 +1499,26 @@ __global__ void __launch_bounds__(1024) weight_exponents_kernel(int bytes, const
     }
 }
 
+// Test-only: one of the library's bounded waits, on a barrier that nothing arrives on.
+__global__ void __launch_bounds__(32) wait_selftest_kernel(int wait, uint32_t prior, uint32_t *fault, long long limit_cycles) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int abort;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bar), 1);
+        abort = 0;
+        fence_mbar_init();
+        if (prior) atomicOr(fault, prior);
+    }
+    __syncwarp();
+    if (threadIdx.x == 0) {
+        if (wait == 0) mbar_wait(smem_u32(&bar), 0, &abort, fault, limit_cycles);
+        else if (wait == 1) mbar_wait_cluster(smem_u32(&bar), 0, &abort, fault, limit_cycles);
+        else if (wait == 2) tc_wait(smem_u32(&bar), 0, &abort, fault, (uint32_t)limit_cycles);
+        else tc_wait_go(false, smem_u32(&bar), 0, &abort, fault, max(1u, (uint32_t)(limit_cycles >> 16)));
+    }
+    __syncwarp();
+}
+
 // ------------------------------------------------------------------ host side
 
 template <class... P, class... A>
@@ -1843,6 +1863,14 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
                     (const float *)(ws + l.part), a.router_w, a.y, (long long)a.n_tokens, a.n_active, (long long)a.rows, a.dtype);
     }
     return st;
+}
+
+hq_status launch_wait_selftest(int wait, uint32_t prior, uint32_t *fault, int64_t cycles, cudaStream_t stream) {
+    note_launch();
+    wait_selftest_kernel<<<1, 32, 0, stream>>>(wait, prior, fault, (long long)cycles);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return set_error(HQ_ERR_LAUNCH, "self-test launch: %s", cudaGetErrorString(e));
+    return HQ_OK;
 }
 
 hq_status launch_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_mats, int64_t rows, int64_t cols,
