@@ -382,7 +382,7 @@ hq_status hq_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_
  *   x, y  : `dtype`, the layouts of hq_moe_matvec_q8_0_ex with n_tokens for
  *           n_vec; x 16-byte aligned, y aligned to its element.
  *   n_tokens : >= 0 (0 returns HQ_OK and launches nothing);
- *       n_tokens * n_active <= 2^27; n_experts <= 8192.  cols % 256 == 0; HQ_MOE_EPI_SWIGLU
+ *       n_tokens * n_active <= 2^27 (and fewer than 2^31 tiles of 16 of them and 128 rows); n_experts <= 8192.  cols % 256 == 0; HQ_MOE_EPI_SWIGLU
  *       needs an even number of rows; y may not overlap x.
  *   workspace : device memory of hq_moe_matmul_workspace() bytes, 256-byte
  *       aligned, not in use by other work until the call's kernels end.
@@ -423,7 +423,7 @@ hq_status hq_moe_matmul_q8_0(const void *W_bank, const int32_t *w_exp, const int
  *   scales : fp32 [n_adapters], finite.   rank : 1..64 (adapters of smaller rank are padded with zeros).
  *   n_adapters : >= 0; with 0 the adapter arguments are not read (they may be NULL) and the
  *       call is the plain many-token product.
- *   n_tokens : 0..2^27 (0 launches nothing).  cols % 256 == 0.
+ *   n_tokens : 0..2^27 (0 launches nothing; fewer than 2^31 tiles of 16 of them and 128 rows).  cols % 256 == 0.
  *   workspace : hq_matmul_adapters_workspace() bytes, 256-byte aligned (a HOST
  *       function; negative: the hq_status of refused arguments).
  * Each token's row depends on its own adapter only: infinities and NaN of another's stay with that one's tokens.

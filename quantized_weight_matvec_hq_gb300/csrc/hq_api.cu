@@ -402,6 +402,7 @@ static hq_status check_adapter_sizes(int rank, int64_t rows, int64_t cols, int64
 
 static hq_status check_workspace(const MatmulArgs &a, int64_t workspace_bytes) {
     const int64_t need = matmul_workspace(a);
+    if (need < 0) return (hq_status)need;
     if (need > 0 && !a.workspace) return set_error(HQ_ERR_NULL, "workspace must be non-null");
     if (workspace_bytes < need)
         return set_error(HQ_ERR_SHAPE, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
@@ -423,8 +424,8 @@ int64_t hq_moe_matmul_workspace(int64_t n_experts, int n_active, int64_t rows, i
     a.x_per_slot = x_per_slot;
     a.dtype = dtype;
     a.epilogue = epilogue;
-    finish(HQ_OK);
-    return matmul_workspace(a);
+    const int64_t need = matmul_workspace(a);
+    return need < 0 ? need : (finish(HQ_OK), need);
 }
 
 hq_status hq_moe_matmul_q8_0(const void *W_bank, const int32_t *w_exp, const int32_t *expert_ids, const void *x,
@@ -472,8 +473,8 @@ int64_t hq_matmul_adapters_workspace(int rank, int64_t rows, int64_t cols, int64
     a.cols = cols;
     a.n_tokens = n_tokens;
     a.dtype = dtype;
-    finish(HQ_OK);
-    return matmul_workspace(a);
+    const int64_t need = matmul_workspace(a);
+    return need < 0 ? need : (finish(HQ_OK), need);
 }
 
 static hq_status matmul_adapters(int fmt, const void *W, const int32_t *w_exp, const void *x,
@@ -540,7 +541,7 @@ hq_status hq_softmax_rows(const void *logits, const float *temperature, float *p
                           int dtype, hq_stream_t stream) {
     hq_status st = check_dtype(dtype);
     if (st != HQ_OK) return st;
-    if (n_rows < 0 || n_rows > (1LL << 28) || vocab < 1 || vocab > (1LL << 22))
+    if (n_rows < 0 || n_rows >= (1LL << 28) || vocab < 1 || vocab > (1LL << 22))
         return set_error(HQ_ERR_SHAPE, "bad shape n_rows=%lld vocab=%lld", (long long)n_rows, (long long)vocab);
     if (n_rows == 0) return finish(HQ_OK);
     if (!logits || !p) return set_error(HQ_ERR_NULL, "logits and p must be non-null");

@@ -84,7 +84,7 @@ struct MatmulArgs {
     int rank = 0;
     void *workspace = nullptr;
 };
-int64_t matmul_workspace(const MatmulArgs &a);
+int64_t matmul_workspace(const MatmulArgs &a);         // bytes, or the (negative) hq_status of sizes it refuses
 hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream);
 hq_status launch_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_mats, int64_t rows, int64_t cols,
                                   cudaStream_t stream);

@@ -1701,7 +1701,11 @@ hq_status launch_tc(const TcArgs &t, const TcPlan &p, bool split, int out, cudaS
 
 }  // namespace
 
-int64_t matmul_workspace(const MatmulArgs &a) { return layout(a).total; }
+int64_t matmul_workspace(const MatmulArgs &a) {
+    if (most_tiles(a) * ((a.rows + kTileRows - 1) / kTileRows) > 0x7fff0000LL)     // (a few steps of the grid fit an int behind them)
+        return set_error(HQ_ERR_SHAPE, "more than 2^31 tiles of 16 tokens and 128 rows");
+    return layout(a).total;
+}
 
 hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
     DeviceInfo *dev = nullptr;
@@ -1711,8 +1715,6 @@ hq_status launch_matmul(const MatmulArgs &a, cudaStream_t stream) {
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     const bool split = a.dtype == HQ_DT_F32;
     const int64_t slots = a.n_tokens * a.n_active, n_rt = (a.rows + kTileRows - 1) / kTileRows;
-    if (most_tiles(a) * n_rt > 0x7fff0000LL)                  // (a few steps of the grid fit an int behind them)
-        return set_error(HQ_ERR_SHAPE, "more than 2^31 tiles");
     const int chunk = a.fmt == 8 ? Fmt<8>::kChunk : Fmt<4>::kChunk;
     const int n_chunks = (int)(a.cols / 256);
 
