@@ -396,6 +396,8 @@ hq_status hq_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_
  * product below 2^-20 (weights below 2^-17 of their matrix's largest: 2^-36 of that; elements of x below 2^-17 of
  * their row's largest: 2^-38 of that).
  * The fp32 sums of f32 leave the tensor core every 256 columns.
+ * HQ_MOE_EPI_SWIGLU, of the gate z = the product's result: z / (1 + e^-z) to a relative 2^-20, 0 below z = -88.7 (f32), or
+ * to 2^-21 (1 + |z| / 4), 0 below z = -87 (f16, bf16).
  * Deterministic: the bits of a token's y do not depend on the other tokens, except through the
  * split of the columns over CTAs that the launch's sizes choose.
  * An id outside [0, n_experts): as for hq_moe_matvec_q8_0 (NaN, HQ_FAULT_EXPERT_ID).

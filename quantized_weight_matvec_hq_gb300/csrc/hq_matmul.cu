@@ -247,8 +247,19 @@ __device__ __forceinline__ void store_elem(void *y, long long i, int dtype, floa
     else static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
 }
 
-// z / (1 + e^-z).  The approximate exponential and quotient are within 2^-21 (1 + |z| / 4) of it.
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+// z / (1 + e^-z).  fp32 outputs: the accurate power and the hardware's reciprocal (within an ulp), together within 2^-20 of it
+// wherever e^-z is a float (z above -88.7; 0 below).  16-bit outputs: the approximate power as well, within
+// 2^-21 (1 + |z| / 4) of it, 0 below z = -87.  (f32, 600 tokens, 8 of 128 experts, 1536 x 2048: 270 us, 258 us with that one.)
+template <int OT>
+__device__ __forceinline__ float silu(float z) {
+    if constexpr (OT == HQ_DT_F32) {
+        float r;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + expf(-z)));
+        return z * r;
+    } else {
+        return __fdividef(z, 1.f + __expf(-z));
+    }
+}
 
 template <int OT>
 __device__ __forceinline__ void store_out(void *y, float v) {
@@ -283,7 +294,7 @@ __device__ __forceinline__ void finish(const Columns *m, bool swiglu, bool wide,
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
             const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-            const float h = silu(odd ? got : v[j]) * (odd ? v[j + 1] : got);
+            const float h = silu<OT>(odd ? got : v[j]) * (odd ? v[j + 1] : got);
             if (live && c0 + j + (odd ? 1 : 0) < n) store_out<OT>(out + (uint64_t)(uint32_t)(odd ? slot[j + 1] : slot[j]) * pitch * kOut, h);
         }
         return;

@@ -163,6 +163,30 @@ def test_softmax_at_the_ends_of_the_temperature(hq, vocab):
         assert (np.abs(got - ref) <= tol).all(), (r, got[:8], ref[:8])
 
 
+def test_swiglu_of_fp32_tokens_uses_the_accurate_power(hq):
+    """Gates that the product gives exactly (one weight and one power of two
+    each): z / (1 + e^-z) within 2^-21 for z down to -88, where e^-z is still
+    a float (2 ulps of the power, an ulp each for sum, quotient and product)."""
+    n, cols = 216, 256
+    z = np.arange(n) - 88
+    q = np.zeros((2 * n, 8, 34), np.uint8)
+    q[:, :, :2] = np.frombuffer(np.float16(1).tobytes(), np.uint8)
+    q[0::2, 0, 2] = z.astype(np.int8).view(np.uint8)
+    q[1::2, 0, 2] = 1
+    q[0::2, 1, 2] = np.where(z > 127, 1, 0)
+    q[0::2, 0, 2] = np.where(z > 127, 127, z).astype(np.int8).view(np.uint8)
+    W = dev(q.reshape(-1))
+    x = torch.zeros((3, cols), device="cuda")
+    x[:, 0] = torch.tensor([1.0, 0.25, 2.0 ** -10], device="cuda")
+    ids = torch.zeros((3, 1), dtype=torch.int32, device="cuda")
+    e = exponents(hq, "q8_0", W, 1, 2 * n, cols)
+    y = tb.run_moe(hq, W, e, ids, x, 0, None, hq.HQ_MOE_EPI_SWIGLU, 1, 2 * n, cols, "f32")[:, 0].double().cpu().numpy()
+    for t, s in enumerate((1.0, 0.25, 2.0 ** -10)):
+        zs = np.minimum(z, 127) * s
+        ref = zs / (1 + np.exp(-zs)) * s
+        assert (np.abs(y[t] - ref) <= 2.0 ** -21 * np.abs(ref)).all(), (s, np.max(np.abs(y[t] - ref) / np.maximum(np.abs(ref), 1e-300)))
+
+
 def test_output_rows_of_4_gigabytes(hq):
     """2^30 rows of fp32 outputs: the second token's row begins at byte 2^32.
     4-bit weights of one block of columns, 155 GB of them."""
