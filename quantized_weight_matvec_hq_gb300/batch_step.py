@@ -37,17 +37,33 @@ def positions(offsets) -> tuple[np.ndarray, np.ndarray]:
     return request, np.arange(len(request)) - (np.asarray(offsets, np.int64)[request] + request)
 
 
+def _expect(name, t, shape, dtype, device=None):
+    """The library's calls take addresses: what a tensor holds is checked here."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or (device is not None and t.device != device):
+        raise ValueError(f"{name}: {tuple(shape)} of {dtype}, contiguous{'' if device is None else f' on {device}'}, expected; "
+                         f"got {tuple(t.shape)} of {t.dtype}, strides {t.stride()}, on {t.device}")
+
+
 class BatchStep:
     def __init__(self, gate_up, down, head, adapters, *, n_experts, n_active, hidden, ffn, vocab, most_tokens, dtype="bf16"):
         """gate_up: Q8_0 blocks of [n_experts][2 ffn][hidden] (gate and up rows interleaved), down: of
         [n_experts][hidden][ffn], head: of [vocab][hidden]; uint8 device tensors.  adapters: (A, B, scales) as
-        hq_matmul_q8_0_adapters takes them, or None."""
+        hq_matmul_q8_0_adapters takes them, or None.  Steps may run on another stream than the current one if it comes
+        behind it (the set-up of the weights runs here)."""
+        dev = gate_up.device
+        for name, W, rows, cols in (("gate_up", gate_up, n_experts * 2 * ffn, hidden), ("down", down, n_experts * hidden, ffn),
+                                    ("head", head, vocab, hidden)):
+            _expect(name, W.view(-1) if W.is_contiguous() else W, (rows * (cols // hq.QK) * hq.Q8_0_BLOCK_BYTES,), torch.uint8, dev)
+        if adapters is not None:
+            n, rank = adapters[0].shape[:2]
+            _expect("lora_A", adapters[0], (n, rank, hidden), torch.bfloat16, dev)
+            _expect("lora_B", adapters[1], (n, vocab, rank), torch.bfloat16, dev)
+            _expect("scales", adapters[2], (n,), torch.float32, dev)
         self.gate_up, self.down, self.head = gate_up, down, head
         self.A, self.B, self.scales = adapters if adapters is not None else (None, None, None)
         self.n_adapters, self.rank = (self.A.shape[0], self.A.shape[1]) if adapters is not None else (0, 1)
         self.E, self.k, self.hidden, self.ffn, self.vocab, self.most = n_experts, n_active, hidden, ffn, vocab, most_tokens
-        self.dtype = hq.DTYPE_CODES[dtype]
-        dev = gate_up.device
+        self.dtype, self.x_dtype, self.device = hq.DTYPE_CODES[dtype], TORCH_DTYPES[dtype], dev
 
         def exponents(W, mats, rows, cols):
             e = torch.empty(mats, dtype=torch.int32, device=dev)
@@ -73,14 +89,30 @@ class BatchStep:
             raise ValueError("sizes that the library refuses")
         return max(1, *need)
 
+    def _check_inputs(self, x, expert_ids, router_w, adapter_ids, temperature, drafts, offsets, u_accept, u_sample, q):
+        T, D, R = x.shape[0], drafts.shape[0], u_sample.shape[0]
+        i32, f32 = torch.int32, torch.float32
+        for name, t, shape, dtype in (("x", x, (T, self.hidden), self.x_dtype), ("expert_ids", expert_ids, (T, self.k), i32),
+                                      ("router_w", router_w, (T, self.k), f32), ("drafts", drafts, (D,), i32),
+                                      ("offsets", offsets, (R + 1,), i32), ("u_accept", u_accept, (D,), f32),
+                                      ("u_sample", u_sample, (R,), f32)):
+            _expect(name, t, shape, dtype, self.device)
+        if self.n_adapters:
+            _expect("adapter_ids", adapter_ids, (T,), i32, self.device)
+        if temperature is not None:
+            _expect("temperature", temperature, (T,), f32, self.device)
+        if q is not None:
+            _expect("q", q, (D, self.vocab), f32, self.device)
+
     def __call__(self, x, expert_ids, router_w, adapter_ids, temperature, drafts, offsets, u_accept, u_sample, q=None,
                  stream=None):
         """x [T][hidden], expert_ids int32 and router_w fp32 [T][n_active], adapter_ids int32 and temperature fp32 [T],
         for the T = len(drafts) + len(u_sample) positions; the rest as hq_verify_drafts takes it, device
-        tensors all.  Returns its n_accepted and tokens, which the next call overwrites."""
+        tensors all; others are refused with a ValueError.  Returns its n_accepted and tokens, which the next call overwrites."""
         T, R = x.shape[0], u_sample.shape[0]
         if T != drafts.shape[0] + R or T > self.most:
             raise ValueError(f"{T} positions for {drafts.shape[0]} drafts and {R} requests, {self.most} at most")
+        self._check_inputs(x, expert_ids, router_w, adapter_ids, temperature, drafts, offsets, u_accept, u_sample, q)
         ws = self.workspace
         hq.hq_moe_matmul_q8_0(self.gate_up, self.e_gate_up, expert_ids, x, 0, None, self.h, self.E, self.k, 2 * self.ffn,
                               self.hidden, T, self.dtype, hq.HQ_MOE_EPI_SWIGLU, ws, ws.numel(), stream=stream)
