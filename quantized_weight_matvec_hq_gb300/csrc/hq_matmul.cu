@@ -861,16 +861,17 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                     for (int g = side; g < n8; g += kSides) {
                         float v[8], x[8], r[8];
                         tmem_ld8(from + 8 * g, v);
-                        if (i >= own) tmem_ld8(from + z.tile_n + 8 * g, x);         // the small products
-                        if (i > 0) tmem_ld8(base + 8 * g, r);
+                        // (loaded whether they count or not: registers on their way may not be moved, as where branches join)
+                        tmem_ld8(from + z.tile_n + 8 * g, x);       // the small products
+                        tmem_ld8(base + 8 * g, r);
                         tmem_wait_ld(v);
+                        tmem_wait_ld(x);
+                        tmem_wait_ld(r);
                         if (i >= own) {
-                            tmem_wait_ld(x);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) v[j] += x[j];
                         }
                         if (i > 0) {
-                            tmem_wait_ld(r);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) v[j] += r[j];
                         }
@@ -900,7 +901,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 tmem_wait_st();
             }
             if (ks == 1) {
-                // 8 columns at a time, the next ones on their way meanwhile
+                // 8 columns at a time, the next ones (at the end, these again) on their way meanwhile
                 float v[8], next[8];
                 tmem_ld8(base + 8 * side, next);
                 tmem_wait_ld(next);
@@ -908,7 +909,7 @@ __global__ void __launch_bounds__(Roles<SPLIT>::kThreads, 1) matmul_tc_kernel(co
                 for (int g = side; g < n8; g += kSides) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = next[j];
-                    if (g + kSides < n8) tmem_ld8(base + 8 * (g + kSides), next);
+                    tmem_ld8(base + 8 * (g + kSides < n8 ? g + kSides : g), next);
                     finish<OT>(&m->columns[item & 1], swiglu, wide, 8 * g, cur.n, row < z.rows, out, pitch, v);
                     tmem_wait_ld(next);
                 }

@@ -57,3 +57,12 @@ def test_weights_are_copied_early_only_behind_a_kernel_that_has_waited():
     first = bodies["matmul_tc_kernel"].index("griddep_wait()")
     assert bodies["matmul_tc_kernel"][:first].endswith("if (!z.early || warp != kWarpW) ")
     assert "z.early = !a.moe && prep_grid > 0;" in source("hq_matmul.cu")
+
+
+def test_tensor_memory_loads_are_in_no_branch_of_their_own():
+    """A load from tensor memory is under way until it is waited for.  Under a
+    condition its registers could be copied where the branches join, before
+    the wait."""
+    text = source("hq_matmul.cu")
+    assert len(re.findall(r"\btmem_ld8\(", text)) > 3
+    assert not re.findall(r"\b(?:if|else)\b[^;{}]*\btmem_ld8\(", text)
