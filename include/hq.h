@@ -396,6 +396,8 @@ hq_status hq_weight_exponents(int fmt, const void *W, int32_t *w_exp, int64_t n_
  * product below 2^-20 (weights below 2^-17 of their matrix's largest: 2^-36 of that; elements of x below 2^-17 of
  * their row's largest: 2^-38 of that).
  * The fp32 sums of f32 leave the tensor core every 256 columns.
+ * An infinity in x gives infinities of its weights' signs, and NaN where the weight (f16, bf16: rounded) is zero; it
+ * and NaN stay in their own token's row.
  * HQ_MOE_EPI_SWIGLU, of the gate z = the product's result: z / (1 + e^-z) to a relative 2^-20, 0 below z = -88.7 (f32), or
  * to 2^-21 (1 + |z| / 4), 0 below z = -87 (f16, bf16).
  * Deterministic: the bits of a token's y do not depend on the other tokens, except through the
@@ -484,9 +486,10 @@ hq_status hq_softmax_rows(const void *logits, const float *temperature, float *p
  *   draft_offsets : int32 [n_req + 1] (device), from 0 to n_drafts.
  *   n_req : 0..2^24 (0 launches nothing); n_drafts >= 0 (0: drafts, q and u_accept are not read);
  *   n_drafts + n_req <= 2^30; vocab 1..2^22.
- * Probabilities are clamped to [0, 1], NaN counts as 0.  A draft outside
- * [0, vocab) is refused and sets HQ_FAULT_DRAFT, as do offsets that do not rise from 0 to n_drafts
- * (that request's outputs are then left unwritten).
+ * p and q are probabilities as hq_softmax_rows gives them.  Of other values: a draft whose p or q is NaN is refused, and s is
+ * clamped to [0, 1], a NaN in it counting as 0.  A draft outside
+ * [0, vocab) is refused and sets HQ_FAULT_DRAFT if all before it were accepted (those behind a refused one are not looked at).
+ * Offsets that do not rise from 0 to n_drafts set it too (that request's outputs are then left unwritten).
  * Source: "DeepSeek-V4 on Hanzo Engine", the speculative-verify widths q in [1, 8].
  */
 hq_status hq_verify_drafts(const float *p, const float *q, const int32_t *drafts, const int32_t *draft_offsets,

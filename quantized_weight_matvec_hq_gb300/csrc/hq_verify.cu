@@ -6,9 +6,10 @@
 // CTA, so that few rows still occupy several SMs; the parts' results are exchanged
 // through distributed shared memory.
 //
-// Measured: softmax of 512 rows of 128256 fp32 columns 153 us, 3.4 TB/s read and written, at half the issue
-// slots (43 instructions a column, most of them the accurate power); 5 rows of 151936 10 us, the latencies of three passes over a
-// part.  Verification of 64 requests of 0 to 7 drafts 31 us, 2.1 TB/s; of one 11 us.
+// Measured: softmax of 512 rows of 128256 fp32 columns 155 us, 3.4 TB/s read and written, at half the issue
+// slots (43 instructions a column, most of them the accurate power) and with phases that do not overlap inside a block; 5 rows of
+// 151936 10 us, three passes over a part and an exchange, on the 40 multiprocessors that clusters of eight occupy.
+// Verification of 64 requests of 0 to 7 drafts 31 us, 2.1 TB/s; of one 11 us.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -270,8 +271,9 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 
 // A cluster takes a request.  Every warp finds the accepted drafts by itself (a lane a draft), and owns a contiguous
 // part of the vocabulary, of which it sums the integers of the residual.  The sums tell which warp holds the
-// sampled token; that warp reads its part again (from L1 or L2) and finds it.  Bound by that chain of reads: 17 us for one
-// request, 31 us for 64, whose rows of p and q are 66 MB.
+// sampled token; that warp reads its part again (from L1 or L2) and finds it.  One request: that chain of reads and two
+// exchanges, 11 us (17 us with nothing in L2 or the instruction caches).  64 requests, whose rows of p and q are 66 MB: 31 us; of their 512
+// blocks 456 fit at once (40 registers a thread), so that seven clusters run behind the others.
 __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
     __shared__ unsigned long long sums[kWarps], peer[2][kMaxCluster];
     if (a.cluster > 1) cluster_arrive_relaxed();
