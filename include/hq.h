@@ -497,6 +497,110 @@ hq_status hq_verify_drafts(const float *p, const float *q, const int32_t *drafts
                            int64_t n_req, int64_t n_drafts, int64_t vocab, hq_stream_t stream);
 
 /*
+ * The key/value cache: rows of the batched step's positions, quantized as they
+ * are written, and the attention that reads them.
+ *
+ * A pool of n_pages pages holds page_size positions each, for all key/value
+ * heads, as blocks of Q8_0 or Q4_0 (fmt HQ_FMT_Q8_0, HQ_FMT_Q4_0; 32 values along
+ * the head, one fp16 scale).  It is device memory of
+ * n_pages * hq_cache_page_bytes() bytes, 16-byte aligned, that need not be set to
+ * anything.  Its inner layout is the library's:
+ *   page  : [n_kv_heads][page_size / 16] cells of 16 positions
+ *   cell  : quants of the keys, quants of the values, scales of the keys
+ *           [16][head_dim / 32], scales of the values [8][head_dim / 32][2]
+ *   quants: unsigned (q + 128, or the nibble n).  A key is [units][4][unit bytes]:
+ *           lane c of 4 holds elements 8c .. 8c+7 of every block of 32 (Q4_0: a word
+ *           a block, nibble i/2 + 4 (i mod 2) for element i).  The values of two
+ *           neighbouring positions are [units][8][unit bytes]: lane g of 8 holds elements
+ *           g, 8+g, 16+g and 24+g of every block, the halves of a word the two
+ *           positions'.  A lane's bytes (head_dim / 8 for Q4_0, head_dim / 4 for Q8_0) are cut
+ *           into units of 16 (8 where it has no more).
+ *
+ * Arguments that the calls share
+ *   page_size    : 16, 32, 64, 128, 256, 512 or 1024.   n_pages : 1..2^31-1.
+ *   page_table   : int32 [n_req][table_width] (device), table_width >= 1,
+ *                  table_width * page_size <= 2^30: position p of request r is
+ *                  in page page_table[r][p / page_size].  Entries behind a request's length are not read.
+ *   offsets      : int32 [n_req + 1] (device): request r brings the tokens
+ *                  offsets[r] .. offsets[r+1]-1 (none where they are equal).
+ *   lengths      : int32 [n_req] (device), the positions of request r, its
+ *                  tokens included: its token i of n is at position lengths[r] - n + i.
+ *                  0 <= lengths[r] <= table_width * page_size.  A token at a negative position
+ *                  (a length below n) has no place in the cache: it is not written, reads as zeros, sees nothing.
+ *   n_req        : 0..2^20 (0 launches nothing).
+ *   n_tokens     : 0..2^27 (0 launches nothing), the rows of the token tensors;
+ *                  offsets[n_req] <= n_tokens.  Rows that are no request's (behind the last one's) stay as they are.
+ *   n_kv_heads   : 1..1024.   head_dim : 64, 128 or 256.
+ *   *_stride     : elements from one token to the next, a multiple of 16 bytes, at least
+ *                  heads * head_dim; the heads of a token lie together.  So the
+ *                  parts of one projection's rows can be passed as they are.  Token tensors are 16-byte aligned.
+ *   dtype        : of the token tensors, HQ_DT_*.
+ * Offsets and lengths outside these ranges set HQ_FAULT_CACHE, and that request is
+ * left out (nothing of it is written).  So does a page number outside [0, n_pages) that a call looks
+ * up: nothing is written there, what is read there is NaN.
+ */
+/* HOST function: bytes of a page; negative: the hq_status of refused arguments. */
+int64_t hq_cache_page_bytes(int fmt, int n_kv_heads, int head_dim, int page_size);
+
+/*
+ * hq_cache_write -- the tokens' key and value rows into the cache.
+ *   k, v : `dtype` [n_tokens][n_kv_heads][head_dim].
+ * Blocks are quantized as hq_quantize_q8_0 and hq_quantize_q4_0 do (fp32, correctly rounded
+ * division), with two additions: the scale is at most the largest fp16 in
+ * size, and a block with an infinity or a NaN is stored as a scale of NaN, so that all 32 read as NaN.
+ * Two tokens for one place of the pool (shared pages) are the caller's to avoid.
+ * Source: "One Native Stack ...", section "The Unified Quant Core" (the block
+ * formats); "DeepSeek-V4 on Hanzo Engine" (the cache that decoding reads).
+ */
+hq_status hq_cache_write(int fmt, const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *pool,
+                         int64_t n_pages, int page_size, const int32_t *page_table, int64_t table_width,
+                         const int32_t *offsets, const int32_t *lengths, int64_t n_req, int64_t n_tokens,
+                         int n_kv_heads, int head_dim, int dtype, hq_stream_t stream);
+
+/*
+ * hq_cache_read -- the values of the tokens' positions: d q or d (n - 8), rounded
+ * once to `dtype`.  To take a whole cache out, offsets are the sums of the lengths.
+ *   k, v : `dtype` [n_tokens][n_kv_heads][head_dim], written.
+ */
+hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_stride, const void *pool,
+                        int64_t n_pages, int page_size, const int32_t *page_table, int64_t table_width,
+                        const int32_t *offsets, const int32_t *lengths, int64_t n_req, int64_t n_tokens,
+                        int n_kv_heads, int head_dim, int dtype, hq_stream_t stream);
+
+/*
+ * hq_cache_attention -- attention of every request's tokens over its cached positions:
+ *   out[t][h] = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale * (q[t][h] . k_p)),
+ * k_p and v_p the stored values of key/value head h / (n_heads / n_kv_heads) at position p.
+ *   q, out  : `dtype` [n_tokens][n_heads][head_dim]; out may be q itself (same stride), not overlap it otherwise.
+ *   n_heads : a multiple of n_kv_heads, at most 4096.
+ *   scale   : finite.
+ *   causal  : 1: a token sees the positions up to its own; 0: all of its request's.
+ *   window  : w > 0: of those, the last w up to its own (needs causal 1); 0: no window.
+ *   workspace : hq_cache_attention_workspace() bytes, 256-byte aligned, not in
+ *       use by other work until the call's kernels end (a HOST function;
+ *       negative: the hq_status of refused arguments).
+ * A token that sees no position gets zeros.  Positions that a token does not see do
+ * not touch it, whatever they hold.  One whose key has a NaN or infinite scale makes the rows that
+ * see it NaN; a value block's makes that block's 32 elements NaN.
+ * Accuracy: scores, maxima, sums and outputs are fp32.  f32 tokens: quants are exact, q and the weights
+ * times the values' scales are taken in two 11-bit terms.  f16 and bf16: the weights (times the values' scales) are rounded to 11 bits,
+ * and with many rows a key/value head (more than 16 of the mean request) the stored keys and values too, or to 2^-19 of
+ * their largest in 128 neighbouring positions, whichever is coarser.  q is exact (f16, bf16).
+ * Deterministic: a token's bits depend on its own request, and on the others only through
+ * the split of the positions over CTAs.
+ * Source: "DeepSeek-V4 on Hanzo Engine", section "A Fused Attention Kernel
+ * for 512-Wide Latent Heads" (attention over the decode cache, one to eight
+ * verified rows a request).
+ */
+int64_t hq_cache_attention_workspace(int fmt, int page_size, int64_t table_width, int64_t n_req, int64_t n_tokens,
+                                     int n_heads, int n_kv_heads, int head_dim, int dtype);
+hq_status hq_cache_attention(int fmt, const void *q, int64_t q_stride, const void *pool, int64_t n_pages, int page_size,
+                             const int32_t *page_table, int64_t table_width, const int32_t *offsets,
+                             const int32_t *lengths, int64_t n_req, int64_t n_tokens, int n_heads, int n_kv_heads,
+                             int head_dim, float scale, int causal, int64_t window, void *out, int64_t out_stride,
+                             int dtype, void *workspace, int64_t workspace_bytes, hq_stream_t stream);
+
+/*
  * hq_requant_params -- HOST function: real multipliers M[i] in (0, 1) to
  * (mult, shift) with M ~= mult * 2^-31 * 2^-shift: M = f * 2^-shift with
  * f in [0.5, 1), mult = round(f * 2^31) (half away from zero; 2^31 becomes
@@ -534,6 +638,7 @@ hq_status hq_requant_i32_debug(const int32_t *acc, const int32_t *mult, const in
 #define HQ_FAULT_EXPERT_ID    2u   /* an expert id outside [0, n_experts)      */
 #define HQ_FAULT_ADAPTER_ID   4u   /* an adapter id outside [-1, n_adapters)   */
 #define HQ_FAULT_DRAFT        8u   /* draft offsets that do not rise from 0 to n_drafts, or a draft outside [0, vocab) */
+#define HQ_FAULT_CACHE       16u   /* a cache's offsets, lengths or page numbers out of range */
 hq_status hq_device_fault(uint32_t *fault);
 
 /*

@@ -20,6 +20,7 @@ HQ_FAULT_WAIT_TIMEOUT = 1
 HQ_FAULT_EXPERT_ID = 2
 HQ_FAULT_ADAPTER_ID = 4
 HQ_FAULT_DRAFT = 8
+HQ_FAULT_CACHE = 16
 HQ_WAIT_MATVEC, HQ_WAIT_CLUSTER, HQ_WAIT_MATMUL, HQ_WAIT_MATMUL_GO = 0, 1, 2, 3
 
 QK = 32
@@ -82,6 +83,14 @@ _SIGS = {
                                  _vp], _int),
     "hq_softmax_rows": ([_vp, _vp, _vp, _i64, _i64, _int, _vp], _int),
     "hq_verify_drafts": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp], _int),
+    "hq_cache_page_bytes": ([_int, _int, _int, _int], _i64),
+    "hq_cache_write": ([_int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp, _i64, _i64, _int, _int, _int,
+                        _vp], _int),
+    "hq_cache_read": ([_int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp, _i64, _i64, _int, _int, _int,
+                       _vp], _int),
+    "hq_cache_attention_workspace": ([_int, _int, _i64, _i64, _i64, _int, _int, _int, _int], _i64),
+    "hq_cache_attention": ([_int, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp, _i64, _i64, _int, _int, _int,
+                            ctypes.c_float, _int, _i64, _vp, _i64, _int, _vp, _i64, _vp], _int),
     "hq_device_fault": ([_vp], _int),
     "hq_selftest_wait_timeout": ([_i64, _vp], _int),
     "hq_selftest_wait": ([_int, ctypes.c_uint32, _i64, _vp], _int),
@@ -286,6 +295,45 @@ def hq_verify_drafts(p, q, drafts, draft_offsets, u_accept, u_sample, n_accepted
     return _check(lib().hq_verify_drafts(_addr(p), _addr(q), _addr(drafts), _addr(draft_offsets), _addr(u_accept),
                                          _addr(u_sample), _addr(n_accepted), _addr(tokens), n_req, n_drafts, vocab,
                                          _stream(stream)))
+
+
+def hq_cache_page_bytes(fmt: int, n_kv_heads: int, head_dim: int, page_size: int) -> int:
+    """HOST function: bytes of one page of a key/value cache."""
+    return _check_size(lib().hq_cache_page_bytes(int(fmt), int(n_kv_heads), int(head_dim), int(page_size)))
+
+
+def hq_cache_write(fmt: int, k, k_stride: int, v, v_stride: int, pool, n_pages: int, page_size: int, page_table,
+                   table_width: int, offsets, lengths, n_req: int, n_tokens: int, n_kv_heads: int, head_dim: int,
+                   dtype: int, stream=None) -> int:
+    return _check(lib().hq_cache_write(int(fmt), _addr(k), k_stride, _addr(v), v_stride, _addr(pool), n_pages,
+                                       int(page_size), _addr(page_table), table_width, _addr(offsets), _addr(lengths),
+                                       n_req, n_tokens, int(n_kv_heads), int(head_dim), int(dtype), _stream(stream)))
+
+
+def hq_cache_read(fmt: int, k, k_stride: int, v, v_stride: int, pool, n_pages: int, page_size: int, page_table,
+                  table_width: int, offsets, lengths, n_req: int, n_tokens: int, n_kv_heads: int, head_dim: int,
+                  dtype: int, stream=None) -> int:
+    return _check(lib().hq_cache_read(int(fmt), _addr(k), k_stride, _addr(v), v_stride, _addr(pool), n_pages,
+                                      int(page_size), _addr(page_table), table_width, _addr(offsets), _addr(lengths),
+                                      n_req, n_tokens, int(n_kv_heads), int(head_dim), int(dtype), _stream(stream)))
+
+
+def hq_cache_attention_workspace(fmt: int, page_size: int, table_width: int, n_req: int, n_tokens: int, n_heads: int,
+                                 n_kv_heads: int, head_dim: int, dtype: int) -> int:
+    """HOST function: bytes of the workspace that hq_cache_attention takes."""
+    return _check_size(lib().hq_cache_attention_workspace(int(fmt), int(page_size), table_width, n_req, n_tokens,
+                                                          int(n_heads), int(n_kv_heads), int(head_dim), int(dtype)))
+
+
+def hq_cache_attention(fmt: int, q, q_stride: int, pool, n_pages: int, page_size: int, page_table, table_width: int,
+                       offsets, lengths, n_req: int, n_tokens: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                       scale: float, causal: int, window: int, out, out_stride: int, dtype: int, workspace,
+                       workspace_bytes: int, stream=None) -> int:
+    return _check(lib().hq_cache_attention(int(fmt), _addr(q), q_stride, _addr(pool), n_pages, int(page_size),
+                                           _addr(page_table), table_width, _addr(offsets), _addr(lengths), n_req,
+                                           n_tokens, int(n_heads), int(n_kv_heads), int(head_dim), float(scale),
+                                           int(causal), window, _addr(out), out_stride, int(dtype), _addr(workspace),
+                                           workspace_bytes, _stream(stream)))
 
 
 def hq_quantize_q8_0(W, out, rows: int, cols: int, stream=None) -> int:

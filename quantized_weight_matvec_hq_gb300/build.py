@@ -19,9 +19,10 @@ LIB = os.path.join(HERE, "libhq.so")
 # (source, extra defines, object name): the kernel file is compiled in five parts
 # (Q8_0, Q4_0, int8 and helpers, MoE, Q4_K)
 SOURCES = [("hq_api.cu", [], "hq_api.o"), ("hq_quant.cu", [], "hq_quant.o"),
-           ("hq_matmul.cu", [], "hq_matmul.o"), ("hq_verify.cu", [], "hq_verify.o")] + [
+           ("hq_matmul.cu", [], "hq_matmul.o"), ("hq_verify.cu", [], "hq_verify.o"),
+           ("hq_cache.cu", [], "hq_cache.o"), ("hq_attention.cu", [], "hq_attention.o")] + [
     ("hq_kernels.cu", [f"-DHQ_PART={i}"], f"hq_kernels_{i}.o") for i in range(5)]
-HEADERS = ["hq_device.cuh", "hq_internal.h", "hq_tc.cuh"]
+HEADERS = ["hq_cache.cuh", "hq_device.cuh", "hq_internal.h", "hq_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-DNDEBUG"]

@@ -567,6 +567,164 @@ hq_status hq_verify_drafts(const float *p, const float *q, const int32_t *drafts
                                 vocab, (cudaStream_t)stream));
 }
 
+// ------------------------------------------------------------------ the key/value cache
+
+static hq_status check_cache_sizes(int fmt, int n_kv_heads, int head_dim, int page_size) {
+    if (fmt != HQ_FMT_Q8_0 && fmt != HQ_FMT_Q4_0)
+        return set_error(HQ_ERR_UNSUPPORTED, "fmt %d: 8 (Q8_0) or 4 (Q4_0)", fmt);
+    if (n_kv_heads < 1 || n_kv_heads > 1024 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+        return set_error(HQ_ERR_SHAPE,
+                         "bad cache n_kv_heads=%d head_dim=%d page_size=%d (need 1..1024, 64|128|256, a power of two in 16..1024)",
+                         n_kv_heads, head_dim, page_size);
+    return HQ_OK;
+}
+
+static hq_status check_cache_batch(const CacheArgs &c) {
+    hq_status st = check_cache_sizes(c.fmt, c.n_kv_heads, c.head_dim, c.page_size);
+    if (st != HQ_OK) return st;
+    st = check_dtype(c.dtype);
+    if (st != HQ_OK) return st;
+    if (c.n_req < 0 || c.n_req > (1LL << 20) || c.n_tokens < 0 || c.n_tokens > (1LL << 27) || c.table_width < 1 ||
+        c.table_width > (1LL << 30) / c.page_size)
+        return set_error(HQ_ERR_SHAPE, "bad batch n_req=%lld n_tokens=%lld table_width=%lld", (long long)c.n_req,
+                         (long long)c.n_tokens, (long long)c.table_width);
+    return HQ_OK;
+}
+
+static hq_status check_cache_memory(const CacheArgs &c) {
+    if (!c.pool || !c.page_table || !c.offsets || !c.lengths)
+        return set_error(HQ_ERR_NULL, "pool, page_table, offsets and lengths must be non-null");
+    if (c.n_pages < 1 || c.n_pages > 0x7fffffffLL)
+        return set_error(HQ_ERR_SHAPE, "n_pages %lld out of range", (long long)c.n_pages);
+    if (!aligned(c.pool, 16) || !aligned(c.page_table, 4) || !aligned(c.offsets, 4) || !aligned(c.lengths, 4))
+        return set_error(HQ_ERR_ALIGN, "pool must be 16-byte aligned, page_table, offsets and lengths 4-byte");
+    return HQ_OK;
+}
+
+static hq_status check_rows(const char *name, const void *p, int64_t stride, int64_t heads, const CacheArgs &c) {
+    if (!p) return set_error(HQ_ERR_NULL, "%s must be non-null", name);
+    if (stride < heads * c.head_dim || stride > (1LL << 31))
+        return set_error(HQ_ERR_SHAPE, "%s stride %lld below %lld heads of %d", name, (long long)stride, (long long)heads,
+                         c.head_dim);
+    if (!aligned(p, 16) || stride * dtype_bytes(c.dtype) % 16 != 0)
+        return set_error(HQ_ERR_ALIGN, "%s must be 16-byte aligned, and its stride a multiple of 16 bytes", name);
+    return HQ_OK;
+}
+
+int64_t hq_cache_page_bytes(int fmt, int n_kv_heads, int head_dim, int page_size) {
+    hq_status st = check_cache_sizes(fmt, n_kv_heads, head_dim, page_size);
+    if (st != HQ_OK) return st;
+    finish(HQ_OK);
+    // keys and values: head_dim quants of 8 or 4 bits and head_dim / 32 scales a position
+    return (int64_t)n_kv_heads * page_size * 2 * (head_dim * (fmt == HQ_FMT_Q8_0 ? 8 : 4) / 8 + head_dim / 16);
+}
+
+static hq_status cache_rows(bool write, CacheArgs &c, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                            hq_stream_t stream) {
+    hq_status st = check_cache_batch(c);
+    if (st != HQ_OK) return st;
+    if (c.n_req == 0 || c.n_tokens == 0) return finish(HQ_OK);
+    if ((st = check_cache_memory(c)) != HQ_OK) return st;
+    if ((st = check_rows("k", k, k_stride, c.n_kv_heads, c)) != HQ_OK) return st;
+    if ((st = check_rows("v", v, v_stride, c.n_kv_heads, c)) != HQ_OK) return st;
+    if (write) return finish(launch_cache_write(c, k, k_stride, v, v_stride, (cudaStream_t)stream));
+    return finish(launch_cache_read(c, const_cast<void *>(k), k_stride, const_cast<void *>(v), v_stride, (cudaStream_t)stream));
+}
+
+static CacheArgs cache_args(int fmt, const void *pool, int64_t n_pages, int page_size, const int32_t *page_table,
+                            int64_t table_width, const int32_t *offsets, const int32_t *lengths, int64_t n_req,
+                            int64_t n_tokens, int n_kv_heads, int head_dim, int dtype) {
+    CacheArgs c;
+    c.fmt = fmt;
+    c.pool = static_cast<uint8_t *>(const_cast<void *>(pool));
+    c.n_pages = n_pages;
+    c.page_size = page_size;
+    c.page_table = page_table;
+    c.table_width = table_width;
+    c.offsets = offsets;
+    c.lengths = lengths;
+    c.n_req = n_req;
+    c.n_tokens = n_tokens;
+    c.n_kv_heads = n_kv_heads;
+    c.head_dim = head_dim;
+    c.dtype = dtype;
+    return c;
+}
+
+hq_status hq_cache_write(int fmt, const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *pool,
+                         int64_t n_pages, int page_size, const int32_t *page_table, int64_t table_width,
+                         const int32_t *offsets, const int32_t *lengths, int64_t n_req, int64_t n_tokens,
+                         int n_kv_heads, int head_dim, int dtype, hq_stream_t stream) {
+    CacheArgs c = cache_args(fmt, pool, n_pages, page_size, page_table, table_width, offsets, lengths, n_req, n_tokens,
+                             n_kv_heads, head_dim, dtype);
+    return cache_rows(true, c, k, k_stride, v, v_stride, stream);
+}
+
+hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_stride, const void *pool,
+                        int64_t n_pages, int page_size, const int32_t *page_table, int64_t table_width,
+                        const int32_t *offsets, const int32_t *lengths, int64_t n_req, int64_t n_tokens,
+                        int n_kv_heads, int head_dim, int dtype, hq_stream_t stream) {
+    CacheArgs c = cache_args(fmt, pool, n_pages, page_size, page_table, table_width, offsets, lengths, n_req, n_tokens,
+                             n_kv_heads, head_dim, dtype);
+    return cache_rows(false, c, k, k_stride, v, v_stride, stream);
+}
+
+static hq_status check_attention_sizes(const AttentionArgs &a) {
+    hq_status st = check_cache_batch(a.cache);
+    if (st != HQ_OK) return st;
+    if (a.n_heads < 1 || a.n_heads > 4096 || a.n_heads % a.cache.n_kv_heads != 0)
+        return set_error(HQ_ERR_SHAPE, "n_heads %d: a multiple of n_kv_heads %d in 1..4096", a.n_heads, a.cache.n_kv_heads);
+    return HQ_OK;
+}
+
+int64_t hq_cache_attention_workspace(int fmt, int page_size, int64_t table_width, int64_t n_req, int64_t n_tokens,
+                                     int n_heads, int n_kv_heads, int head_dim, int dtype) {
+    AttentionArgs a;
+    a.cache = cache_args(fmt, nullptr, 0, page_size, nullptr, table_width, nullptr, nullptr, n_req, n_tokens, n_kv_heads,
+                         head_dim, dtype);
+    a.n_heads = n_heads;
+    hq_status st = check_attention_sizes(a);
+    if (st != HQ_OK) return st;
+    finish(HQ_OK);
+    return n_req == 0 || n_tokens == 0 ? 0 : attention_workspace(a);
+}
+
+hq_status hq_cache_attention(int fmt, const void *q, int64_t q_stride, const void *pool, int64_t n_pages, int page_size,
+                             const int32_t *page_table, int64_t table_width, const int32_t *offsets,
+                             const int32_t *lengths, int64_t n_req, int64_t n_tokens, int n_heads, int n_kv_heads,
+                             int head_dim, float scale, int causal, int64_t window, void *out, int64_t out_stride,
+                             int dtype, void *workspace, int64_t workspace_bytes, hq_stream_t stream) {
+    AttentionArgs a;
+    a.cache = cache_args(fmt, pool, n_pages, page_size, page_table, table_width, offsets, lengths, n_req, n_tokens,
+                         n_kv_heads, head_dim, dtype);
+    a.q = q;
+    a.out = out;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.n_heads = n_heads;
+    a.scale = scale;
+    a.causal = causal;
+    a.window = window;
+    a.workspace = workspace;
+    hq_status st = check_attention_sizes(a);
+    if (st != HQ_OK) return st;
+    if (!std::isfinite(scale)) return set_error(HQ_ERR_SHAPE, "scale must be finite");
+    if (causal != 0 && causal != 1) return set_error(HQ_ERR_UNSUPPORTED, "causal %d is not 0 or 1", causal);
+    if (window < 0 || (window > 0 && !causal))
+        return set_error(HQ_ERR_SHAPE, "window %lld: 0, or positive with causal attention", (long long)window);
+    if (n_req == 0 || n_tokens == 0) return finish(HQ_OK);
+    if ((st = check_cache_memory(a.cache)) != HQ_OK) return st;
+    if ((st = check_rows("q", q, q_stride, n_heads, a.cache)) != HQ_OK) return st;
+    if ((st = check_rows("out", out, out_stride, n_heads, a.cache)) != HQ_OK) return st;
+    const int64_t need = attention_workspace(a);
+    if (need > 0 && !workspace) return set_error(HQ_ERR_NULL, "workspace must be non-null");
+    if (workspace_bytes < need)
+        return set_error(HQ_ERR_SHAPE, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
+    if (!aligned(workspace, 256)) return set_error(HQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+    return finish(launch_attention(a, (cudaStream_t)stream));
+}
+
 hq_status hq_requant_params(const double *M, int64_t n, int32_t *mult, int32_t *shift) {
     if (!M || !mult || !shift) return set_error(HQ_ERR_NULL, "M, mult and shift must be non-null");
     for (int64_t i = 0; i < n; ++i) {

@@ -20,6 +20,7 @@ constexpr uint32_t kFaultWaitTimeout = 1u;
 constexpr uint32_t kFaultExpertId = 2u;
 constexpr uint32_t kFaultAdapterId = 4u;
 constexpr uint32_t kFaultDraft = 8u;
+constexpr uint32_t kFaultCache = 16u;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -93,6 +93,35 @@ hq_status launch_softmax(const void *logits, const float *temperature, float *p,
 hq_status launch_verify(const float *p, const float *q, const int32_t *drafts, const int32_t *off,
                         const float *u_accept, const float *u_sample, int32_t *n_accepted, int32_t *tokens,
                         int64_t n_req, int64_t n_drafts, int64_t vocab, cudaStream_t stream);
+// The key/value cache (hq_cache.cu) and the attention over it (hq_attention.cu).
+struct CacheArgs {
+    int fmt = 8;                        // 8 Q8_0, 4 Q4_0
+    uint8_t *pool = nullptr;
+    int64_t n_pages = 0;
+    int page_size = 16;
+    const int32_t *page_table = nullptr;
+    int64_t table_width = 0;
+    const int32_t *offsets = nullptr, *lengths = nullptr;
+    int64_t n_req = 0, n_tokens = 0;
+    int n_kv_heads = 1, head_dim = 128, dtype = 0;
+};
+struct AttentionArgs {
+    CacheArgs cache;
+    const void *q = nullptr;
+    void *out = nullptr;
+    int64_t q_stride = 0, out_stride = 0;
+    int n_heads = 1;
+    float scale = 1.f;
+    int causal = 1;
+    int64_t window = 0;                 // 0: none
+    void *workspace = nullptr;
+};
+hq_status launch_cache_write(const CacheArgs &c, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                             cudaStream_t stream);
+hq_status launch_cache_read(const CacheArgs &c, void *k, int64_t k_stride, void *v, int64_t v_stride,
+                            cudaStream_t stream);
+int64_t attention_workspace(const AttentionArgs &a);    // bytes
+hq_status launch_attention(const AttentionArgs &a, cudaStream_t stream);
 // Test-only plan queries (no device touched): see hq_debug_plan in hq.h.
 hq_status debug_plan_float_q8_0(int n_vec, int64_t rows, int64_t cols, int num_sms, int smem_optin, int regs,
                                 int64_t *out);
