@@ -17,12 +17,13 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhq.so")
 # (source, extra defines, object name): the kernel file is compiled in five parts
-# (Q8_0, Q4_0, int8 and helpers, MoE, Q4_K)
+# (Q8_0, Q4_0, int8 and helpers, MoE, Q4_K), the attention in two (16-bit tokens, f32)
 SOURCES = [("hq_api.cu", [], "hq_api.o"), ("hq_quant.cu", [], "hq_quant.o"),
            ("hq_matmul.cu", [], "hq_matmul.o"), ("hq_verify.cu", [], "hq_verify.o"),
-           ("hq_cache.cu", [], "hq_cache.o"), ("hq_attention.cu", [], "hq_attention.o")] + [
+           ("hq_cache.cu", [], "hq_cache.o"), ("hq_attention.cu", ["-DHQ_PART=0"], "hq_attention_0.o"),
+           ("hq_attention.cu", ["-DHQ_PART=1"], "hq_attention_1.o")] + [
     ("hq_kernels.cu", [f"-DHQ_PART={i}"], f"hq_kernels_{i}.o") for i in range(5)]
-HEADERS = ["hq_cache.cuh", "hq_device.cuh", "hq_internal.h", "hq_tc.cuh"]
+HEADERS = ["hq_attention.cuh", "hq_cache.cuh", "hq_device.cuh", "hq_internal.h", "hq_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-DNDEBUG"]

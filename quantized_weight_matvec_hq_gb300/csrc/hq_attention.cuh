@@ -1,0 +1,217 @@
+// hq_attention.cuh -- how the attention of a batch is divided among blocks.
+//
+// An item is a tile of a request's query rows on one key/value head: up to `tokens` neighbouring tokens with all heads
+// of the group, or, where a group has more heads than a tile has rows, one token with a part of them.  The positions that an item
+// sees are cut into units of kUnit; the units of all items, one after another, are dealt to the blocks in equal
+// contiguous ranges.  Lengths are known on the device only, so every block finds its range itself.
+// An item that one block has whole is finished there; of the others each block leaves a partial result (its maximum, sum
+// and weighted sum), and the combine kernel joins them.
+#pragma once
+
+#include <type_traits>
+
+#include "hq_cache.cuh"
+
+namespace hq {
+
+constexpr int kUnit = 128;
+
+struct AttnArgs {
+    CacheView c;
+    const void *q;
+    void *out;
+    long long q_stride, out_stride;
+    int dtype;                          // of q and out: HQ_DT_*
+    int n_heads, group;                 // heads, and those that share a key/value head
+    int tokens, part_heads, parts;      // of a tile: tokens, heads of a group, and tiles a group takes
+    int causal;
+    float scale;
+    long long window;                   // 0: none
+    float *partial;                     // [2 blocks][rows][head_dim], then [2 blocks][rows][2]: maximum, sum
+    int blocks, min_units;
+};
+
+// sum of floor((a i + b) / m) for i < n; a, b >= 0 (the Euclidean recursion)
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+    long long s = 0;
+    while (n > 0) {
+        s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const long long top = a * n + b;
+        if (top < m) break;
+        n = top / m;
+        b = top % m;
+        const long long t = m;
+        m = a;
+        a = t;
+    }
+    return s;
+}
+
+// sum of floor(max(0, c + tokens j) / kUnit) for j < n
+__device__ __forceinline__ long long unit_sum(int n, long long c, int tokens) {
+    if (n <= 0) return 0;
+    if (n == 1) return c > 0 ? (long long)((unsigned)c / kUnit) : 0;
+    const long long skip = c < 0 ? (-c + tokens - 1) / tokens : 0;
+    return floor_sum(n - skip, kUnit, tokens, c + skip * tokens);
+}
+
+// Positions [lo, hi) that a token sees.
+struct Range { int lo, hi; };
+__device__ __forceinline__ Range seen_by(const AttnArgs &a, const Request &q, int token) {
+    const int at = q.length - q.n + token;
+    Range s;
+    s.hi = a.causal ? max(at + 1, 0) : q.length;
+    s.lo = a.window > 0 && a.window <= at ? at + 1 - (int)a.window : 0;
+    return s;
+}
+
+__device__ __forceinline__ int tiles_of(const AttnArgs &a, const Request &q) { return (q.n + a.tokens - 1) / a.tokens; }
+
+// Units of the tiles before tile j, on one head and part.  A tile sees what its first token's window begins with up to its
+// last token's position; it has at least one unit, so that rows that see nothing are written too.
+__device__ __forceinline__ long long units_before(const AttnArgs &a, const Request &q, int j) {
+    if (j == 0) return 0;
+    if (!a.causal) return (long long)j * max(1, (q.length + kUnit - 1) / kUnit);
+    const int base = q.length - q.n, n = tiles_of(a, q);
+    long long u = j;                                        // 1 + floor((last position) / kUnit) each
+    u += unit_sum(j - (j == n), (long long)base + a.tokens - 1, a.tokens);
+    if (j == n && q.length > 0) u += (q.length - 1) / kUnit;
+    if (a.window > 0) u -= unit_sum(j, (long long)base + 1 - a.window, a.tokens);
+    return u;
+}
+
+__device__ __forceinline__ long long request_units(const AttnArgs &a, const Request &q) {
+    return q.n == 0 ? 0 : units_before(a, q, tiles_of(a, q)) * a.c.n_kv_heads * a.parts;
+}
+
+// A block's way through the units: the request that it is at.
+struct Walk {
+    long long start, next;              // units before the request, and up to its end
+    int r;                              // that request
+    Request q;
+};
+
+// The item of the walk's next unit, and which of its units that is.
+struct Item {
+    int tile, kv_head, part;            // of request r
+    long long first;                    // its first unit
+    int units, unit;                    // how many it has, and which one x is
+};
+
+struct WalkShared {
+    long long warp_sum[32];
+    Walk walk;
+    Item item;
+};
+
+// Inclusive scan over the block; every thread gets the block's sum.
+template <int THREADS>
+__device__ __forceinline__ long long block_scan(long long v, long long &sum, WalkShared &s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long w = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += w;
+    }
+    __syncthreads();
+    if (lane == 31) s.warp_sum[warp] = v;
+    __syncthreads();
+    sum = 0;
+    long long before = 0;
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < warp) before += s.warp_sum[i];
+        sum += s.warp_sum[i];
+    }
+    return v + before;
+}
+
+// Takes the walk to the request with its next unit x, looking from request r0 on, which begins at unit `start`.  The whole
+// block calls it; x is below the batch's units.
+template <int THREADS>
+__device__ __forceinline__ void walk_to(const AttnArgs &a, long long x, int r0, long long start, WalkShared &s) {
+    for (long long i = r0; i < a.c.n_req; i += THREADS) {
+        const long long r = i + threadIdx.x;
+        Request q = {0, 0, 0, false};
+        if (r < a.c.n_req) q = request_of(a.c, (int)r);
+        const long long u = request_units(a, q);
+        long long sum;
+        const long long upto = start + block_scan<THREADS>(u, sum, s);
+        if (x >= upto - u && x < upto) {
+            s.walk.r = (int)r;
+            s.walk.start = upto - u;
+            s.walk.next = upto;
+            s.walk.q = q;
+        }
+        start += sum;
+        if (x < start) break;
+    }
+    __syncthreads();
+}
+
+// The first unit of block `b`.  Few units go to few blocks, min_units each.
+__device__ __forceinline__ long long first_unit(const AttnArgs &a, long long total, int b) {
+    const long long n = min((long long)a.blocks, max(1ll, total / a.min_units));
+    return b >= n ? total : total * b / n;
+}
+
+template <int THREADS>
+__device__ __forceinline__ long long batch_units(const AttnArgs &a, WalkShared &s) {
+    long long mine = 0, total;
+    for (int r = threadIdx.x; r < a.c.n_req; r += THREADS) mine += request_units(a, request_of(a.c, r));
+    block_scan<THREADS>(mine, total, s);
+    return total;
+}
+
+__device__ __forceinline__ Item item_at(const AttnArgs &a, const Walk &w, long long x) {
+    const long long local = x - w.start, heads = (long long)a.c.n_kv_heads * a.parts;
+    int lo = 0, hi = tiles_of(a, w.q);                      // the last tile with units_before * heads <= local
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (units_before(a, w.q, mid) * heads <= local) lo = mid; else hi = mid;
+    }
+    const long long before = units_before(a, w.q, lo);
+    Item it;
+    it.tile = lo;
+    it.units = (int)(units_before(a, w.q, lo + 1) - before);
+    const long long rest = local - before * heads;
+    const int h = (int)(rest / it.units);
+    it.kv_head = h / a.parts;
+    it.part = h % a.parts;
+    it.unit = (int)(rest - (long long)h * it.units);
+    it.first = x - it.unit;
+    return it;
+}
+
+// Row i of an item is token tile * tokens + i / part_heads of the request, and of its group head part * part_heads + i % part_heads.
+__device__ __forceinline__ bool row_of(const AttnArgs &a, const Request &q, const Item &it, int i, int &token, int &head) {
+    token = it.tile * a.tokens + i / a.part_heads;
+    const int h = it.part * a.part_heads + i % a.part_heads;
+    head = it.kv_head * a.group + h;
+    return i < a.tokens * a.part_heads && token < q.n && h < a.group;
+}
+
+// 8 neighbouring elements of a token's row of type WIDE ? fp32 : a.dtype.
+template <bool WIDE>
+__device__ __forceinline__ void load_row8(const AttnArgs &a, long long at, float (&v)[8]) {
+    if (WIDE) load8(static_cast<const float *>(a.q) + at, v);
+    else if (a.dtype == HQ_DT_F16) load8(static_cast<const __half *>(a.q) + at, v);
+    else load8(static_cast<const __nv_bfloat16 *>(a.q) + at, v);
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_row8(const AttnArgs &a, long long at, const float (&v)[8]) {
+    if (WIDE) store8(static_cast<float *>(a.out) + at, v);
+    else if (a.dtype == HQ_DT_F16) store8(static_cast<__half *>(a.out) + at, v);
+    else store8(static_cast<__nv_bfloat16 *>(a.out) + at, v);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+}  // namespace hq

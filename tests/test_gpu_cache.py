@@ -8,7 +8,8 @@ Tolerance of attention.  With weights p_i of the formula, an error d_i of score 
           key near it), and the sums.  The argument of the power is a product and a difference in fp32: 2^-23 (|s| + |max|).
   weights: the power 2^-21; f16 and bf16: a rounding to 11 bits of the weight, of the weight times the value's scale, and of the
           stored value, 2^-11 each; f32: two terms, 2^-21.  Weights below 2^-24 of the largest may vanish (their number times
-          2^-24 of the largest |v| there); the same for values far below others near them (2^-19 of the largest).
+          2^-24 of the largest |v| there; f32, where scales are held in [2^8, 2^9) and the second term is rounded to 2^-25: 2^-33);
+          the same for values far below others near them (2^-19 of the largest).
   sums:   n positions in fp32, the accumulators truncating: n / 16 steps of 2^-23 at most, of the sum of |terms|.
 The output is rounded once, half a step of its type.
 """
@@ -226,7 +227,7 @@ def check_attention(out, q, cache, lengths, new, heads, kv, dim, dtype, causal=1
     n = ref.shape[0]
     got = out[:n].double()
     if dtype == "f32":
-        ds, dw, tiny = score * 2.0 ** -20, 2.0 ** -20, 2.0 ** -35
+        ds, dw, tiny = score * 2.0 ** -20, 2.0 ** -20, 2.0 ** -33
     else:
         ds, dw, tiny = score * (2.0 ** -11 + 2.0 ** -17), 2.0 ** -10, 2.0 ** -24
     ds = ds + spread * 2.0 ** -22
