@@ -14,13 +14,15 @@
 #include <type_traits>
 
 #include <algorithm>
+#include <atomic>
 
 #include "hq_attention.cuh"
 
 namespace hq {
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kUnitCells = kUnit / kCell;
+constexpr int kCombineThreads = 128;
 constexpr float kSlack = 5.f;
 
 // ------------------------------------------------------------------ operands
@@ -61,18 +63,20 @@ __device__ __forceinline__ void decode_q8(uint32_t w0, uint32_t w1, uint32_t (&h
     h[3] = h2_bits(__hadd2(bits_h2(prmt(w1, 0x64646464u, SEL1)), off));
 }
 
-// WORDS 32-bit words that nothing writes while the kernel runs.
+// WORDS 32-bit words of shared memory.
 template <int WORDS>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *v) {
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&v)[WORDS]) {
     if constexpr (WORDS == 1) {
-        asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v[0]) : "l"(p));
+        v[0] = *reinterpret_cast<const uint32_t *>(p);
     } else if constexpr (WORDS == 2) {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p));
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        v[0] = x.x; v[1] = x.y;
     } else {
 #pragma unroll
-        for (int i = 0; i < WORDS; i += 4)
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]) : "l"(p + 4 * i));
+        for (int i = 0; i < WORDS; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+        }
     }
 }
 
@@ -83,89 +87,49 @@ struct Stream {
     using L = CellLayout<BITS, D>;
     static constexpr bool WIDE = WIDE_;                     // q and the weights in two terms
     static constexpr int TERMS = WIDE ? 2 : 1;
-    static constexpr int ROWS = 8 * NT, NB = L::NB, LW = L::LANE / 4;
-    static constexpr int CELLS = L::LANE <= 16 && NT == 1 ? 2 : 1;          // of an iteration of a warp
-    static constexpr int STEP = kCell * CELLS;
-    // by the registers that a thread needs: loaded cells, outputs, operands and the rest
-    static constexpr int REGS = CELLS * (4 * LW + 3 * NB) + 8 * NB * NT + 12 * NT + (WIDE ? 24 : 0) + 52;
-    static constexpr int MIN_BLOCKS = REGS <= 128 ? 4 : REGS <= 168 ? 3 : 2;
+    static constexpr int ROWS = 8 * NT, NB = L::NB;
+    static constexpr int STAGE = kUnitCells * L::BYTES;     // a stage of the ring is a unit
+    // Consumer warps, and behind them the producer; two blocks a multiprocessor where 96 registers are enough for a thread.
+    static constexpr int WARPS = NB * NT >= 16 ? 4 : 8, CONSUMERS = 32 * WARPS, THREADS = CONSUMERS + 32;
+    static constexpr int MIN_BLOCKS = NT == 1 && NB * (WIDE ? 2 : 1) <= 4 ? 2 : 1;
+    static constexpr int MAX_STAGES = 6;
 
     struct Shared {
         WalkShared walk;
         uint4 q[TERMS][NT][NB][32];                         // the Q operand: lane (row g, c) has elements 8 c .. + 7 of a block
-        float factor[ROWS];                                 // scores = sum * factor, in powers of two
-        Range seen[ROWS], part;
-        float m[kWarps][ROWS], l[kWarps][ROWS];
+        Part part[2];                                       // this part and the one the producer is ahead with
+        alignas(8) float factor[ROWS];                                // scores = sum * factor, in powers of two
+        Range seen[ROWS];
+        float m[WARPS][ROWS], l[WARPS][ROWS];
         uint32_t bad[ROWS];                                 // value blocks that are no numbers and that the row sees
-        alignas(16) float o[kWarps][ROWS][D + 4];           // read as float4
+        alignas(16) float o[WARPS / 2][ROWS][D + 4];       // read as float4
+        alignas(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], part_full[2], part_empty[2];
+        uint32_t cells[MAX_STAGES];                         // of a stage: bit i: cell i is there; bit 16 + i: its page is out of range
+        int abort;
     };
-
-    struct Raw {                                            // what a lane loads of an iteration's cells
-        uint32_t k[CELLS][2][LW], v[CELLS][2][LW], ks[CELLS][2][NB / 2], vs[CELLS][2][NB];
-    };
-
-    static __device__ __forceinline__ void load_keys(const uint64_t (&cell)[CELLS], Raw &w) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-#pragma unroll
-        for (int j = 0; j < CELLS; ++j) {
-            const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[j]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (cell[j] > 1) {
-#pragma unroll
-                    for (int u = 0; u < L::UNITS; ++u)
-                        load_words<L::UW>(p + L::k_word(g + 8 * h, c, u * L::UW), &w.k[j][h][u * L::UW]);
-                    load_words<NB / 2>(p + L::k_scale(g + 8 * h, 0), w.ks[j][h]);
-                } else {                                    // nothing there: masked; a page out of range: NaN
-#pragma unroll
-                    for (int i = 0; i < LW; ++i) w.k[j][h][i] = 0;
-#pragma unroll
-                    for (int i = 0; i < NB / 2; ++i) w.ks[j][h][i] = cell[j] ? 0x7fff7fffu : 0u;
-                }
-            }
-        }
-    }
-    static __device__ __forceinline__ void load_values(const uint64_t (&cell)[CELLS], Raw &w) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-#pragma unroll
-        for (int j = 0; j < CELLS; ++j) {
-            const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[j]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (cell[j] > 1) {
-#pragma unroll
-                    for (int u = 0; u < L::UNITS; ++u)
-                        load_words<L::UW>(p + L::v_word(c + 4 * h, g, u * L::UW), &w.v[j][h][u * L::UW]);
-                    load_words<NB>(p + L::v_scale(2 * (c + 4 * h), 0), w.vs[j][h]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < LW; ++i) w.v[j][h][i] = 0;
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) w.vs[j][h][i] = 0;
-                }
-            }
-        }
-    }
+    static constexpr int FIXED = ((int)sizeof(Shared) + 127) / 128 * 128;
+    static constexpr int LIMIT = (MIN_BLOCKS == 2 ? 113 : 226) * 1024;
+    static constexpr int STAGES = (LIMIT - FIXED) / STAGE < MAX_STAGES ? (LIMIT - FIXED) / STAGE : MAX_STAGES;
+    static constexpr int SMEM = FIXED + STAGES * STAGE;
+    static_assert(STAGES >= 2, "the ring needs two stages");
 
     // The query rows of an item, each times a power of two that takes its largest element to [2^14, 2^15), as 16-bit terms.
-    static __device__ __forceinline__ void prepare_rows(const AttnArgs &a, Shared &s) {
-        const Walk &w = s.walk.walk;
-        const Item &it = s.walk.item;
+    static __device__ __forceinline__ void prepare_rows(const AttnArgs &a, const Part &part, Shared &s) {
         constexpr int LANES = D / 8;                        // lanes of a row
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = lane % LANES;
 #pragma unroll
-        for (int r0 = 0; r0 < ROWS; r0 += kThreads / LANES) {
+        for (int r0 = 0; r0 < ROWS; r0 += CONSUMERS / LANES) {
             const int row = r0 + warp * (32 / LANES) + lane / LANES;
             int token = 0, head = 0;
-            const bool live = row < ROWS && row_of(a, w.q, it, row, token, head);
+            const bool live = row < ROWS && row_of(a, part.q, part.item, row, token, head);
             float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (live) load_row8<WIDE>(a, ((long long)w.q.first + token) * a.q_stride + (long long)head * D + 8 * at, v);
+            if (live) load_row8<WIDE>(a, ((long long)part.q.first + token) * a.q_stride + (long long)head * D + 8 * at, v);
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
 #pragma unroll
             for (int d = 1; d < LANES; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const int e = min(253, 268 - (int)(top >> 23));        // exponent field of the power: its value 2^(e - 127)
+            const int e = min(253, 268 - (int)(top >> 23)); // exponent field of the power: its value is 2^(e - 127)
             const float up = __uint_as_float((uint32_t)e << 23);
             uint32_t h[4], r[4];
 #pragma unroll
@@ -184,75 +148,96 @@ struct Stream {
                     s.factor[row] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
                                                        : a.scale * kLog2e * __uint_as_float((uint32_t)(254 - e) << 23);
                     s.bad[row] = 0;
-                    s.seen[row] = seen_by(a, w.q, min(token, w.q.n - 1));
+                    s.seen[row] = seen_by(a, part.q, min(token, part.q.n - 1));
                 }
             }
         }
     }
 };
 
-// An item's part: `take` units from the one that the walk is at.
+// The producer warp: tells the consumers the parts, one after another, and copies their cells into the ring, a cell a lane.
 template <bool WIDE, int BITS, int D, int NT>
-__device__ __forceinline__ void stream_part(const AttnArgs &a, int take, int slot, typename Stream<WIDE, BITS, D, NT>::Shared &s) {
+__device__ __forceinline__ void stream_produce(const AttnArgs &a, typename Stream<WIDE, BITS, D, NT>::Shared &s, uint32_t ring,
+                                               long long x0, long long end) {
     using S = Stream<WIDE, BITS, D, NT>;
     using L = typename S::L;
-    constexpr int NB = S::NB, CELLS = S::CELLS, STEP = S::STEP, ROWS = S::ROWS;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    // Every row of the tile sees [last_lo, first_hi) of its part; some row sees [begin, end), which is in shared memory.
-    int first_hi, last_lo, p_begin;
-    {
-        const Walk &w = s.walk.walk;
-        const Item &it = s.walk.item;
-        const int t0 = it.tile * a.tokens, t1 = min(t0 + a.tokens, w.q.n) - 1;
-        const Range first = seen_by(a, w.q, t0), last = seen_by(a, w.q, t1);
-        first_hi = first.hi;
-        last_lo = last.lo;
-        p_begin = (first.lo / kUnit + it.unit) * kUnit;
-        if (threadIdx.x == 0) s.part = {first.lo, min(p_begin + take * kUnit, last.hi)};
-        __syncthreads();
-    }
-    constexpr int ITS = kUnit / (kWarps * STEP);
-    const int n_it = take * ITS;
-
-    // Lane i knows cell i % CELLS of iteration (of 32 / CELLS) i / CELLS: its address, 0 where there is none, 1 where the page is out of range.
-    uint64_t mine = 0;
-    auto place = [&](int i) { return p_begin + (i * kWarps + warp) * STEP; };
-    auto look_up = [&](int i0) {
-        const int p = place(i0 + lane / CELLS) + kCell * (lane % CELLS);
-        mine = 0;
-        if (i0 + lane / CELLS < n_it && p < s.part.hi && p + kCell > s.part.lo) {
-            uint8_t *cells = page_cells(a.c, s.walk.walk.r, p, s.walk.item.kv_head);
-            mine = cells ? reinterpret_cast<uint64_t>(cell_of<L>(a.c, cells, p)) : 1;
+    constexpr int AHEAD = 32 / kUnitCells;                  // units whose cells are looked up at once
+    const int lane = threadIdx.x & 31;
+    volatile int *abort = &s.abort;
+    const uint64_t policy = l2_evict_first_policy();
+    int n = 0, stage = 0;                                   // parts and units so far
+    uint32_t phase = 1;
+    for (long long x = x0;; ++n) {
+        const int at = n & 1;
+        if (!mbar_wait(smem_u32(&s.part_empty[at]), (n >> 1 & 1) ^ 1, abort, a.c.fault)) break;
+        if (x >= end) {                                     // the end
+            if (lane == 0) {
+                s.part[at].take = 0;
+                mbar_arrive(smem_u32(&s.part_full[at]));
+            }
+            return;
         }
-    };
-    auto cells_of = [&](int i, uint64_t (&cell)[CELLS]) {
-#pragma unroll
-        for (int j = 0; j < CELLS; ++j) cell[j] = __shfl_sync(0xffffffffu, mine, (i * CELLS + j) & 31);
-    };
-    typename S::Raw raw;
-    look_up(0);
-    bool here = false;                                      // the iteration has a cell (the whole warp)
-    {
-        uint64_t cell[CELLS];
-        cells_of(0, cell);
-#pragma unroll
-        for (int j = 0; j < CELLS; ++j) here |= cell[j] != 0;
-        S::load_keys(cell, raw);
-        S::load_values(cell, raw);
+        if (x >= s.walk.walk.next) walk_to<32>(a, x, s.walk.walk.r + 1, s.walk.walk.next, s.walk);
+        const Part p = part_at(a, s.walk.walk, x, x0, end);
+        if (lane == 0) {
+            s.part[at] = p;
+            mbar_arrive(smem_u32(&s.part_full[at]));
+        }
+        uint64_t cell = 0;
+        for (int u = 0; u < p.take; ++u) {
+            if (u % AHEAD == 0) {                           // lane i: cell i of the next units; 0: none, 1: its page is out of range
+                const int pos = p.begin + u * kUnit + lane * kCell;
+                cell = 0;
+                if (pos < p.span.hi && pos + kCell > p.span.lo) {
+                    uint8_t *cells = page_cells(a.c, s.walk.walk.r, pos, p.item.kv_head);
+                    cell = cells ? reinterpret_cast<uint64_t>(cell_of<L>(a.c, cells, pos)) : 1;
+                }
+            }
+            if (!mbar_wait(smem_u32(&s.empty[stage]), phase, abort, a.c.fault)) goto drain;
+            const int first = u % AHEAD * kUnitCells;
+            const uint32_t there = __ballot_sync(0xffffffffu, cell > 1) >> first & 0xffu;
+            const uint32_t bad = __ballot_sync(0xffffffffu, cell == 1) >> first & 0xffu;
+            const uint32_t full = smem_u32(&s.full[stage]);
+            if (lane == 0) {
+                s.cells[stage] = there | bad << 16;
+                mbar_arrive_expect_tx(full, __popc(there) * L::BYTES);
+            }
+            __syncwarp();
+            if (lane / kUnitCells == u % AHEAD && cell > 1)
+                bulk_load(ring + stage * S::STAGE + lane % kUnitCells * L::BYTES, reinterpret_cast<const void *>(cell), L::BYTES, full, policy);
+            if (++stage == S::STAGES) { stage = 0; phase ^= 1; }
+        }
+        x += p.take;
     }
+drain:
+    // after a time-out: the copies under way end before the block does
+    for (int i = 0; i < S::STAGES; ++i) {
+        const bool lapped = i < stage;
+        const uint32_t parity = lapped ? phase ^ 1 : phase;
+        for (int k = 0; k < 100000 && !mbar_try_wait_sleep(smem_u32(&s.full[i]), parity, 20000u); ++k) {}
+    }
+}
 
-    __syncthreads();                                        // the part before is done with the shared memory
-    S::prepare_rows(a, s);
-    __syncthreads();
+// A consumer warp's way through a part: a cell of every unit.  False after a time-out.
+template <bool WIDE, int BITS, int D, int NT>
+__device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &part, typename Stream<WIDE, BITS, D, NT>::Shared &s,
+                                               const uint8_t *ring, uint32_t &lap) {
+    using S = Stream<WIDE, BITS, D, NT>;
+    using L = typename S::L;
+    constexpr int NB = S::NB, ROWS = S::ROWS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
 
-    float o[NT][NB][2][4], m[NT][2], l[NT][2], factor[NT][2];
+    named_barrier(1, S::CONSUMERS);                           // the part before is done with the shared memory
+    S::prepare_rows(a, part, s);
+    named_barrier(1, S::CONSUMERS);
+
+    float o[NT][NB][2][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             m[n][i] = -INFINITY;
             l[n][i] = 0.f;
-            factor[n][i] = s.factor[8 * n + 2 * c + i];
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -260,223 +245,231 @@ __device__ __forceinline__ void stream_part(const AttnArgs &a, int take, int slo
             for (int i = 0; i < 4; ++i) o[n][b][0][i] = o[n][b][1][i] = 0.f;
     }
     int up = 23;                                            // the values' scales are taken times 2^up
-
-    for (int i = 0; i < n_it; ++i) {
-        const int p0 = place(i);
-        if ((i + 1) % (32 / CELLS) == 0) look_up(i + 1);
-        uint64_t next[CELLS];
-        cells_of(i + 1, next);                              // past the last iteration: not loaded below
-        const bool more = i + 1 < n_it;
-        const bool now = here;
-        here = false;
-#pragma unroll
-        for (int j = 0; j < CELLS; ++j) here |= next[j] != 0;
-        if (!now) {
-            if (more) { S::load_keys(next, raw); S::load_values(next, raw); }
-            continue;
-        }
-        // ---- scores
-        float z[NT][CELLS][4];
-#pragma unroll
-        for (int j = 0; j < CELLS; ++j) {
+    bool ok = true;
+    for (int u = 0; u < part.take; ++u) {
+        const uint32_t stage = lap >> 1;                    // the ring's stage, and below it the phase of its barrier
+        if (!mbar_wait(smem_u32(&s.full[stage]), lap & 1, &s.abort, a.c.fault)) { ok = false; break; }
+        const uint32_t states = s.cells[stage];
+#pragma unroll 1
+        for (int j = warp; j < kUnitCells; j += S::WARPS) {
+            const uint32_t state = states >> j & 0x10001u;
+            if (state == 0) continue;                       // the whole warp
+            const uint8_t *cell = ring + stage * S::STAGE + j * L::BYTES;
+            const int p0 = part.begin + u * kUnit + j * kCell;
+            // ---- scores
+            float z[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z[n][j][e] = 0.f;
+                for (int e = 0; e < 4; ++e) z[n][e] = 0.f;
+            uint32_t ks0[NB / 2], ks1[NB / 2];
+            load_words(cell + L::k_scale(g, 0), ks0);
+            load_words(cell + L::k_scale(g + 8, 0), ks1);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                uint32_t ka[4], kb[4];
-                if constexpr (BITS == 4) {
-                    decode_q4(raw.k[j][0][b], ka);
-                    decode_q4(raw.k[j][1][b], kb);
-                } else {
-                    decode_q8<0x4140, 0x4342>(raw.k[j][0][2 * b], raw.k[j][0][2 * b + 1], ka);
-                    decode_q8<0x4140, 0x4342>(raw.k[j][1][2 * b], raw.k[j][1][2 * b + 1], kb);
-                }
-                const __half2 d0 = bits_h2(raw.ks[j][0][b / 2]), d1 = bits_h2(raw.ks[j][1][b / 2]);
-                const float f0 = b % 2 ? __high2float(d0) : __low2float(d0), f1 = b % 2 ? __high2float(d1) : __low2float(d1);
+            for (int v = 0; v < L::UNITS; ++v) {
+                uint32_t k0[L::UW], k1[L::UW];
+                load_words(cell + L::k_word(g, c, v * L::UW), k0);
+                load_words(cell + L::k_word(g + 8, c, v * L::UW), k1);
+                constexpr int BLOCKS = NB / L::UNITS;       // of a unit
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int t = S::TERMS - 1; t >= 0; --t) {
-                        const uint4 q = s.q[t][n][b][lane];
-                        mma16816(acc, ka[0], kb[0], ka[1], kb[1], q.x, q.y);
-                        mma16816(acc, ka[2], kb[2], ka[3], kb[3], q.z, q.w);
+                for (int i = 0; i < BLOCKS; ++i) {
+                    const int b = v * BLOCKS + i;
+                    uint32_t ka[4], kb[4];
+                    if constexpr (BITS == 4) {
+                        decode_q4(k0[i], ka);
+                        decode_q4(k1[i], kb);
+                    } else {
+                        decode_q8<0x4140, 0x4342>(k0[2 * i], k0[2 * i + 1], ka);
+                        decode_q8<0x4140, 0x4342>(k1[2 * i], k1[2 * i + 1], kb);
                     }
-                    z[n][j][0] = fmaf(acc[0], f0, z[n][j][0]);
-                    z[n][j][1] = fmaf(acc[1], f0, z[n][j][1]);
-                    z[n][j][2] = fmaf(acc[2], f1, z[n][j][2]);
-                    z[n][j][3] = fmaf(acc[3], f1, z[n][j][3]);
+                    const __half2 d0 = bits_h2(ks0[b / 2]), d1 = bits_h2(ks1[b / 2]);
+                    const float f0 = b % 2 ? __high2float(d0) : __low2float(d0), f1 = b % 2 ? __high2float(d1) : __low2float(d1);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int t = S::TERMS - 1; t >= 0; --t) {
+                            const uint4 q = s.q[t][n][b][lane];
+                            mma16816(acc, ka[0], kb[0], ka[1], kb[1], q.x, q.y);
+                            mma16816(acc, ka[2], kb[2], ka[3], kb[3], q.z, q.w);
+                        }
+                        z[n][0] = fmaf(acc[0], f0, z[n][0]);
+                        z[n][1] = fmaf(acc[1], f0, z[n][1]);
+                        z[n][2] = fmaf(acc[2], f1, z[n][2]);
+                        z[n][3] = fmaf(acc[3], f1, z[n][3]);
+                    }
                 }
             }
-        }
-        if (more) S::load_keys(next, raw);
-        // ---- softmax: lane (g, c) has positions g and g + 8 of each cell, of rows 2 c and 2 c + 1
-        const bool edge = p0 < last_lo || p0 + STEP > first_hi;
-        bool raise = false;
+            // ---- softmax: lane (g, c) has positions g and g + 8, of rows 2 c and 2 c + 1
+            uint32_t vs[2][NB];
+            load_words(cell + L::v_scale(2 * c, 0), vs[0]);
+            load_words(cell + L::v_scale(2 * c + 8, 0), vs[1]);
+            const bool gone = state >> 16;                  // a page out of range: NaN
+            if (gone)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+                for (int b = 0; b < NB; ++b) vs[0][b] = vs[1][b] = 0;
+            const bool edge = p0 < part.all_lo || p0 + kCell > part.all_hi;
+            bool raise = false;
 #pragma unroll
-            for (int j = 0; j < CELLS; ++j)
+            for (int n = 0; n < NT; ++n) {
+                const float2 factor = *reinterpret_cast<const float2 *>(&s.factor[8 * n + 2 * c]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    z[n][j][e] *= factor[n][e & 1];
+                    z[n][e] *= e & 1 ? factor.y : factor.x;
+                    if (gone) z[n][e] = __uint_as_float(0x7fffffffu);
                     if (edge) {
-                        const int p = p0 + kCell * j + g + 8 * (e >> 1);
+                        const int p = p0 + g + 8 * (e >> 1);
                         const Range x = s.seen[8 * n + 2 * c + (e & 1)];
-                        if (p < x.lo || p >= x.hi) z[n][j][e] = -INFINITY;
+                        if (p < x.lo || p >= x.hi) z[n][e] = -INFINITY;
                     }
-                    raise |= z[n][j][e] > m[n][e & 1] + kSlack;
+                    raise |= z[n][e] > m[n][e & 1] + kSlack;
                 }
-        if (__any_sync(0xffffffffu, raise)) {
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float t = fmaxf(m[n][k], fmaxf(z[n][k], z[n][k + 2]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+                        const float f = t == m[n][k] ? 1.f : ex2(m[n][k] - t);      // 0 from -inf
+                        m[n][k] = t;
+                        l[n][k] *= f;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                o[n][b][h][k] *= f;
+                                o[n][b][h][k + 2] *= f;
+                            }
+                    }
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float t = m[n][k];
-#pragma unroll
-                    for (int j = 0; j < CELLS; ++j) t = fmaxf(t, fmaxf(z[n][j][k], z[n][j][k + 2]));
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-                    const float f = t == m[n][k] ? 1.f : ex2(m[n][k] - t);      // 0 from -inf
-                    m[n][k] = t;
-                    l[n][k] *= f;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            o[n][b][h][k] *= f;
-                            o[n][b][h][k + 2] *= f;
-                        }
-                }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < CELLS; ++j)
-#pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    z[n][j][e] = ex2(z[n][j][e] - fmaxf(m[n][e & 1], -3e38f));    // nothing seen yet: 0
-                    l[n][e & 1] += z[n][j][e];
+                    z[n][e] = ex2(z[n][e] - fmaxf(m[n][e & 1], -3e38f));            // nothing seen yet: 0
+                    l[n][e & 1] += z[n][e];
                 }
-        // ---- the power of two of the values' scales, and blocks that are no numbers
-        if (edge) {                                         // positions that no row sees count for nothing
-            const int begin = s.part.lo, end = s.part.hi;
-#pragma unroll
-            for (int j = 0; j < CELLS; ++j)
+            // ---- the power of two of the values' scales, and blocks that are no numbers
+            if (edge) {                                     // positions that no row sees count for nothing
+                const int begin = part.span.lo, end = part.span.hi;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int p = p0 + kCell * j + 2 * (c + 4 * h);
+                    const int p = p0 + 2 * (c + 4 * h);
                     const uint32_t keep = (p >= begin && p < end ? 0xffffu : 0u) | (p + 1 >= begin && p + 1 < end ? 0xffff0000u : 0u);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) raw.vs[j][h][b] &= keep;
+                    for (int b = 0; b < NB; ++b) vs[h][b] &= keep;
                 }
-        }
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < CELLS; ++j)
+            }
+            uint32_t top = 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int b = 0; b < NB; ++b) top = __vmaxu2(top, raw.vs[j][h][b] & 0x7fff7fffu);
-        top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-        if (top >= 0x7c00u) {                               // an infinity or a NaN: its block leaves the product, its rows are marked
-            top = 0;
-#pragma unroll
-            for (int j = 0; j < CELLS; ++j)
+                for (int b = 0; b < NB; ++b) top = __vmaxu2(top, vs[h][b] & 0x7fff7fffu);
+            top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+            if (top >= 0x7c00u) {                           // an infinity or a NaN: its block leaves the product, its rows are marked
+                top = 0;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint32_t d = raw.vs[j][h][b] >> (16 * k) & 0x7fffu;
+                            const uint32_t d = vs[h][b] >> (16 * k) & 0x7fffu;
                             if (d < 0x7c00u) { top = max(top, d); continue; }
-                            raw.vs[j][h][b] &= k ? 0x0000ffffu : 0xffff0000u;
-                            const int p = p0 + kCell * j + 2 * (c + 4 * h) + k;
+                            vs[h][b] &= k ? 0x0000ffffu : 0xffff0000u;
+                            const int p = p0 + 2 * (c + 4 * h) + k;
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
                                 const Range x = s.seen[8 * n + g];
                                 if (p >= x.lo && p < x.hi) atomicOr(&s.bad[8 * n + g], 1u << b);
                             }
                         }
-            top = __reduce_max_sync(0xffffffffu, top);
-        }
-        const int want = 23 - (int)(top >> 10);
-        if (want < up) {
-            const float f = __uint_as_float((uint32_t)(127 + want - up) << 23);
+                top = __reduce_max_sync(0xffffffffu, top);
+            }
+            const int want = 23 - (int)(top >> 10);
+            if (want < up) {
+                const float f = __uint_as_float((uint32_t)(127 + want - up) << 23);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                    for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) { o[n][b][0][e] *= f; o[n][b][1][e] *= f; }
-            up = want;
-        }
-        const __half2 up1 = __half2half2(__ushort_as_half((uint16_t)((15 + min(up, 15)) << 10)));
-        const __half2 up2 = __half2half2(__ushort_as_half((uint16_t)((15 + up - min(up, 15)) << 10)));
-        // ---- outputs
-#pragma unroll
-        for (int j = 0; j < CELLS; ++j) {
+                        for (int e = 0; e < 4; ++e) { o[n][b][0][e] *= f; o[n][b][1][e] *= f; }
+                up = want;
+            }
+            const __half2 up1 = __half2half2(__ushort_as_half((uint16_t)((15 + min(up, 15)) << 10)));
+            const __half2 up2 = __half2half2(__ushort_as_half((uint16_t)((15 + up - min(up, 15)) << 10)));
+            // ---- outputs
             uint32_t ph[NT][2], pr[NT][2];                  // the weights, positions along a register: pairs c and c + 4
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const __half2 x = __floats2half2_rn(z[n][j][2 * h], z[n][j][2 * h + 1]);
+                    const __half2 x = __floats2half2_rn(z[n][2 * h], z[n][2 * h + 1]);
                     ph[n][h] = transpose8x8(h2_bits(x));
                     if (S::WIDE) {
                         const float2 f = __half22float2(x);
-                        pr[n][h] = transpose8x8(h2_bits(__floats2half2_rn((z[n][j][2 * h] - f.x) * 2048.f,
-                                                                          (z[n][j][2 * h + 1] - f.y) * 2048.f)));
+                        pr[n][h] = transpose8x8(h2_bits(__floats2half2_rn((z[n][2 * h] - f.x) * 2048.f, (z[n][2 * h + 1] - f.y) * 2048.f)));
                     }
                 }
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                uint32_t va[4], vb[4];
-                if constexpr (BITS == 4) {
-                    decode_q4(raw.v[j][0][b], va);
-                    decode_q4(raw.v[j][1][b], vb);
-                } else {
-                    decode_q8<0x4240, 0x4341>(raw.v[j][0][2 * b], raw.v[j][0][2 * b + 1], va);
-                    decode_q8<0x4240, 0x4341>(raw.v[j][1][2 * b], raw.v[j][1][2 * b + 1], vb);
-                }
-                __half2 d[2];
+            for (int v = 0; v < L::UNITS; ++v) {
+                uint32_t v0[L::UW], v1[L::UW];
+                load_words(cell + L::v_word(c, g, v * L::UW), v0);
+                load_words(cell + L::v_word(c + 4, g, v * L::UW), v1);
+                constexpr int BLOCKS = NB / L::UNITS;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    d[h] = __hmul2(bits_h2(raw.vs[j][h][b]), up1);
-                    if (up > 15) d[h] = __hmul2(d[h], up2);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    uint32_t p[2], r[2];
+                for (int i = 0; i < BLOCKS; ++i) {
+                    const int b = v * BLOCKS + i;
+                    uint32_t va[4], vb[4];
+                    if constexpr (BITS == 4) {
+                        decode_q4(v0[i], va);
+                        decode_q4(v1[i], vb);
+                    } else {
+                        decode_q8<0x4240, 0x4341>(v0[2 * i], v0[2 * i + 1], va);
+                        decode_q8<0x4240, 0x4341>(v1[2 * i], v1[2 * i + 1], vb);
+                    }
+                    __half2 d[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (S::WIDE) {
-                            const float2 x = __half22float2(bits_h2(ph[n][h])), y = __half22float2(bits_h2(pr[n][h]));
-                            const float2 e = __half22float2(d[h]);
-                            const float u0 = fmaf(y.x, 0x1p-11f, x.x) * e.x, u1 = fmaf(y.y, 0x1p-11f, x.y) * e.y;
-                            const __half2 t = __floats2half2_rn(u0, u1);
-                            const float2 f = __half22float2(t);
-                            p[h] = h2_bits(t);
-                            r[h] = h2_bits(__floats2half2_rn(u0 - f.x, u1 - f.y));
-                        } else {
-                            p[h] = h2_bits(__hmul2(bits_h2(ph[n][h]), d[h]));
-                        }
+                        d[h] = __hmul2(bits_h2(vs[h][b]), up1);
+                        if (up > 15) d[h] = __hmul2(d[h], up2);
                     }
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (S::WIDE) mma16816(o[n][b][t], va[2 * t], va[2 * t + 1], vb[2 * t], vb[2 * t + 1], r[0], r[1]);
-                        mma16816(o[n][b][t], va[2 * t], va[2 * t + 1], vb[2 * t], vb[2 * t + 1], p[0], p[1]);
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t p[2], r[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (S::WIDE) {
+                                const float2 x = __half22float2(bits_h2(ph[n][h])), y = __half22float2(bits_h2(pr[n][h]));
+                                const float2 e = __half22float2(d[h]);
+                                const float u0 = fmaf(y.x, 0x1p-11f, x.x) * e.x, u1 = fmaf(y.y, 0x1p-11f, x.y) * e.y;
+                                const __half2 t = __floats2half2_rn(u0, u1);
+                                const float2 f = __half22float2(t);
+                                p[h] = h2_bits(t);
+                                r[h] = h2_bits(__floats2half2_rn(u0 - f.x, u1 - f.y));
+                            } else {
+                                p[h] = h2_bits(__hmul2(bits_h2(ph[n][h]), d[h]));
+                            }
+                        }
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (S::WIDE) mma16816(o[n][b][t], va[2 * t], va[2 * t + 1], vb[2 * t], vb[2 * t + 1], r[0], r[1]);
+                            mma16816(o[n][b][t], va[2 * t], va[2 * t + 1], vb[2 * t], vb[2 * t + 1], p[0], p[1]);
+                        }
                     }
                 }
             }
         }
-        if (more) S::load_values(next, raw);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.empty[stage]));
+        lap = stage == S::STAGES - 1 ? (lap & 1) ^ 1 : lap + 2;
     }
 
-    // ---- the warps' results together
+    // ---- the warps' results together: the upper half's to the lower half's, then those
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -488,38 +481,45 @@ __device__ __forceinline__ void stream_part(const AttnArgs &a, int take, int slo
                 s.l[warp][8 * n + 2 * c + k] = l[n][k];
             }
         }
-    __syncthreads();
+    named_barrier(1, S::CONSUMERS);
     const float down = __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int turn = 0; turn < 2; ++turn) {
+        if (warp / (S::WARPS / 2) == 1 - turn) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int row = 8 * n + 2 * c + k;
-            float t = s.m[0][row];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 1; i < kWarps; ++i) t = fmaxf(t, s.m[i][row]);
-            const float f = (m[n][k] == t ? 1.f : ex2(m[n][k] - t)) * down;
+                for (int k = 0; k < 2; ++k) {
+                    const int row = 8 * n + 2 * c + k;
+                    float t = s.m[0][row];
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+                    for (int i = 1; i < S::WARPS; ++i) t = fmaxf(t, s.m[i][row]);
+                    const float f = (m[n][k] == t ? 1.f : ex2(m[n][k] - t)) * down;
+                    float *to = s.o[warp % (S::WARPS / 2)][row] + g;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    s.o[warp][row][32 * b + 16 * h + g] = o[n][b][h][k] * f;
-                    s.o[warp][row][32 * b + 16 * h + 8 + g] = o[n][b][h][k + 2] * f;
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float *x = to + 32 * b + 16 * h;
+                            x[0] = (turn ? x[0] : 0.f) + o[n][b][h][k] * f;
+                            x[8] = (turn ? x[8] : 0.f) + o[n][b][h][k + 2] * f;
+                        }
                 }
         }
-    __syncthreads();
+        named_barrier(1, S::CONSUMERS);
+    }
     constexpr int CHUNKS = D / 8;                           // 8 columns a thread
-    const Walk &w = s.walk.walk;
-    for (int i = threadIdx.x; i < ROWS * CHUNKS; i += kThreads) {
+    for (int i = threadIdx.x; i < ROWS * CHUNKS; i += S::CONSUMERS) {
         const int row = i / CHUNKS, at = i % CHUNKS;
         int token, head;
-        if (!row_of(a, w.q, s.walk.item, row, token, head)) continue;
+        if (!row_of(a, part.q, part.item, row, token, head)) continue;
         float t = s.m[0][row], sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 1; k < kWarps; ++k) t = fmaxf(t, s.m[k][row]);
+        for (int k = 1; k < S::WARPS; ++k) t = fmaxf(t, s.m[k][row]);
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            sum += s.l[k][row] * (s.m[k][row] == t ? 1.f : ex2(s.m[k][row] - t));
+        for (int k = 0; k < S::WARPS; ++k) sum += s.l[k][row] * (s.m[k][row] == t ? 1.f : ex2(s.m[k][row] - t));
+#pragma unroll
+        for (int k = 0; k < S::WARPS / 2; ++k) {
             const float4 x = *reinterpret_cast<const float4 *>(&s.o[k][row][8 * at]);
             const float4 y = *reinterpret_cast<const float4 *>(&s.o[k][row][8 * at + 4]);
             v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w; v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
@@ -527,94 +527,135 @@ __device__ __forceinline__ void stream_part(const AttnArgs &a, int take, int slo
         if (s.bad[row] >> (at / 4) & 1u)
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(0x7fffffffu);
-        if (slot < 0) {
+        if (part.slot < 0) {
             const float f = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);         // a row that sees nothing: zeros
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] *= f;
-            store_row8<WIDE>(a, ((long long)w.q.first + token) * a.out_stride + (long long)head * D + 8 * at, v);
+            store_row8<WIDE>(a, ((long long)part.q.first + token) * a.out_stride + (long long)head * D + 8 * at, v);
         } else {
-            const long long r = (long long)slot * ROWS + row;
+            const long long r = (long long)part.slot * ROWS + row;
             store8(a.partial + r * D + 8 * at, v);
             if (at == 0)
                 *reinterpret_cast<float2 *>(a.partial + 2ll * a.blocks * ROWS * D + 2 * r) = make_float2(t, sum);
         }
     }
+    return ok;
 }
 
 template <bool WIDE, int BITS, int D, int NT>
-__global__ void __launch_bounds__(kThreads, (Stream<WIDE, BITS, D, NT>::MIN_BLOCKS)) attention_stream_kernel(const __grid_constant__ AttnArgs a) {
-    __shared__ typename Stream<WIDE, BITS, D, NT>::Shared s;
+__global__ void __launch_bounds__((Stream<WIDE, BITS, D, NT>::THREADS), (Stream<WIDE, BITS, D, NT>::MIN_BLOCKS)) attention_stream_kernel(const __grid_constant__ AttnArgs a) {
+    using S = Stream<WIDE, BITS, D, NT>;
+    extern __shared__ __align__(128) uint8_t memory[];
+    typename S::Shared &s = *reinterpret_cast<typename S::Shared *>(memory);
+    uint8_t *ring = memory + S::FIXED;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            mbar_init(smem_u32(&s.full[i]), 1);
+            mbar_init(smem_u32(&s.empty[i]), S::WARPS);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&s.part_full[i]), 1);
+            mbar_init(smem_u32(&s.part_empty[i]), S::WARPS);
+        }
+        fence_mbar_init();
+        s.abort = 0;
+    }
     griddep_launch_dependents();
     griddep_wait();
     if (blockIdx.x == 0)
-        for (int r = threadIdx.x; r < a.c.n_req; r += kThreads)
+        for (int r = threadIdx.x; r < a.c.n_req; r += S::THREADS)
             if (request_of(a.c, r).bad) atomicOr(a.c.fault, kFaultCache);
-    const long long total = batch_units<kThreads>(a, s.walk);
+    const long long total = batch_units<S::THREADS>(a, s.walk);               // (barriers, which the mbarriers' set-up needs)
     const long long x0 = first_unit(a, total, blockIdx.x), end = first_unit(a, total, blockIdx.x + 1);
     if (x0 >= end) return;
-    walk_to<kThreads>(a, x0, 0, 0, s.walk);
-    for (long long x = x0; x < end;) {
-        if (threadIdx.x == 0) s.walk.item = item_at(a, s.walk.walk, x);
-        __syncthreads();
-        const int units = s.walk.item.units, take = (int)min((long long)(units - s.walk.item.unit), end - x);
-        const int slot = take == units ? -1 : 2 * (int)blockIdx.x + (x == x0 ? 0 : 1);
-        stream_part<WIDE, BITS, D, NT>(a, take, slot, s);
-        __syncthreads();
-        x += take;
-        if (x < end && x >= s.walk.walk.next) walk_to<kThreads>(a, x, s.walk.walk.r + 1, s.walk.walk.next, s.walk);
+    walk_to<S::THREADS>(a, x0, 0, 0, s.walk);
+    if (threadIdx.x >= S::CONSUMERS) {
+        stream_produce<WIDE, BITS, D, NT>(a, s, smem_u32(ring), x0, end);
+        return;
+    }
+    uint32_t lap = 0;
+    for (int n = 0;; ++n) {
+        const int at = n & 1;
+        if (!mbar_wait(smem_u32(&s.part_full[at]), n >> 1 & 1, &s.abort, a.c.fault)) break;
+        if (s.part[at].take == 0) break;
+        const bool ok = stream_consume<WIDE, BITS, D, NT>(a, s.part[at], s, ring, lap);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&s.part_empty[at]));
+        if (!ok) break;
     }
 }
 
-// Joins the partial results of one item: block b has that of the item that goes on past the end of block b's units and does
-// not begin before them.
+// Joins the partial results of a row (blockIdx.y) of one item: block b has that of the item that goes on past the end of block b's
+// units and does not begin before them.  D / 8 lanes a partial result, the block's groups of them take every GROUPS-th.
 template <bool WIDE, int D>
-__global__ void __launch_bounds__(kThreads) attention_combine_kernel(const __grid_constant__ AttnArgs a, int rows) {
+__global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(const __grid_constant__ AttnArgs a, int rows) {
+    constexpr int LANES = D / 8, GROUPS = kCombineThreads / LANES;
     __shared__ WalkShared s;
+    __shared__ float gm[GROUPS], gl[GROUPS];
+    __shared__ alignas(16) float go[GROUPS][D];
     griddep_launch_dependents();
     griddep_wait();
-    const long long total = batch_units<kThreads>(a, s);
-    const int b = blockIdx.x;
+    const long long total = batch_units<kCombineThreads>(a, s);
+    const int b = blockIdx.x, row = blockIdx.y;
     const long long x0 = first_unit(a, total, b), x = first_unit(a, total, b + 1);
     if (x == x0 || x >= total) return;
-    walk_to<kThreads>(a, x, 0, 0, s);
+    walk_to<kCombineThreads>(a, x, 0, 0, s);
     const Item it = item_at(a, s.walk, x);
     if (it.unit == 0 || it.first < x0) return;              // it begins with this unit, or in a block before
+    int token, head;
+    if (!row_of(a, s.walk.q, it, row, token, head)) return;
     const long long end = it.first + it.units;
-    int last = b;                                           // the last block that has a part
-    while (first_unit(a, total, last + 1) < end) ++last;
-    const float *stat = a.partial + 2ll * a.blocks * rows * D;
-    constexpr int CHUNKS = D / 8;
-    for (int i = threadIdx.x; i < rows * CHUNKS; i += kThreads) {
-        const int row = i / CHUNKS, at = i % CHUNKS;
-        int token, head;
-        if (!row_of(a, s.walk.q, it, row, token, head)) continue;
-        float t = -INFINITY, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int k = b; k <= last; ++k) {
-            const long long r = (2ll * k + (k == b && it.first != x0 ? 1 : 0)) * rows + row;
-            const float2 ml = *reinterpret_cast<const float2 *>(stat + 2 * r);
-            float y[8];
-            load8(a.partial + r * D + 8 * at, y);
-            const float t1 = fmaxf(t, ml.x);
-            const float f0 = t == t1 ? 1.f : ex2(t - t1), f1 = ml.x == t1 ? 1.f : ex2(ml.x - t1);
-            sum = sum * f0 + ml.y * f1;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * f0 + y[e] * f1;
-            t = t1;
-        }
-        const float f = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= f;
-        store_row8<WIDE>(a, ((long long)s.walk.q.first + token) * a.out_stride + (long long)head * D + 8 * at, v);
+    int lo = b + 1, hi = a.blocks;                          // the first block that begins at the item's end or behind it
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (first_unit(a, total, mid) < end) lo = mid + 1; else hi = mid;
     }
+    const float *stat = a.partial + 2ll * a.blocks * rows * D;
+    const int group = threadIdx.x / LANES, at = threadIdx.x % LANES;
+    float t = -INFINITY, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = b + group; k < lo; k += GROUPS) {
+        const long long r = (2ll * k + (k == b && it.first != x0 ? 1 : 0)) * rows + row;
+        const float2 ml = *reinterpret_cast<const float2 *>(stat + 2 * r);
+        float y[8];
+        load8(a.partial + r * D + 8 * at, y);
+        const float t1 = fmaxf(t, ml.x);
+        const float f0 = t == t1 ? 1.f : ex2(t - t1), f1 = ml.x == t1 ? 1.f : ex2(ml.x - t1);
+        sum = sum * f0 + ml.y * f1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * f0 + y[e] * f1;
+        t = t1;
+    }
+    if (at == 0) { gm[group] = t; gl[group] = sum; }
+    store8(&go[group][8 * at], v);
+    __syncthreads();
+    if (group != 0) return;
+    for (int k = 0; k < GROUPS; ++k) t = fmaxf(t, gm[k]);
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    for (int k = 0; k < GROUPS; ++k) {
+        const float f = gm[k] == t ? 1.f : ex2(gm[k] - t);
+        float y[8];
+        load8(&go[k][8 * at], y);
+        sum += gl[k] * f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += y[e] * f;
+    }
+    const float f = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+    store_row8<WIDE>(a, ((long long)s.walk.q.first + token) * a.out_stride + (long long)head * D + 8 * at, v);
 }
 
 // ------------------------------------------------------------------ host side
 
 template <class K, class... A>
-hq_status launch(K kern, unsigned grid, cudaStream_t stream, const char *what, const A &... args) {
+hq_status launch(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, const char *what, const A &... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -627,12 +668,24 @@ hq_status launch(K kern, unsigned grid, cudaStream_t stream, const char *what, c
     return HQ_OK;
 }
 
-constexpr int kMaxBlocks = 608;                             // the workspace holds two partial results of each
+// Allows a kernel its shared memory, once a device.
+template <class K>
+hq_status allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
+    int d = 0;
+    cudaGetDevice(&d);
+    if (d >= 0 && d < 64 && done[d].load(std::memory_order_acquire)) return HQ_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return set_error(HQ_ERR_LAUNCH, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    if (d >= 0 && d < 64) done[d].store(true, std::memory_order_release);
+    return HQ_OK;
+}
+
+constexpr int kMaxBlocks = 304;                             // the workspace holds two partial results of each
 
 // Rows of a tile: the mean request's query rows a key/value head decide.
 int stream_tiles(const AttentionArgs &x) {
     const int64_t rows = (x.cache.n_tokens + x.cache.n_req - 1) / x.cache.n_req * (x.n_heads / x.cache.n_kv_heads);
-    return x.cache.head_dim == 256 || rows <= 8 ? 1 : 2;
+    return rows <= 8 || (x.cache.head_dim == 256 && x.cache.dtype == HQ_DT_F32) ? 1 : 2;
 }
 
 template <bool WIDE, int BITS, int D, int NT>
@@ -648,15 +701,21 @@ hq_status run_stream(const AttentionArgs &x, AttnArgs a, int num_sms, cudaStream
     a.blocks = std::min(kMaxBlocks, num_sms * S::MIN_BLOCKS);
     if (most < a.blocks) a.blocks = (int)most;
     a.min_units = 1;
-    hq_status st = launch(attention_stream_kernel<WIDE, BITS, D, NT>, (unsigned)a.blocks, stream, "attention", a);
+    static std::atomic<bool> done[64];
+    hq_status st = allow_smem(attention_stream_kernel<WIDE, BITS, D, NT>, S::SMEM, done);
+    if (st != HQ_OK) return st;
+    st = launch(attention_stream_kernel<WIDE, BITS, D, NT>, dim3((unsigned)a.blocks), S::THREADS, S::SMEM, stream, "attention", a);
     if (st != HQ_OK || a.blocks < 2 || per_tile < 2) return st;             // an item of one unit is never divided
-    return launch(attention_combine_kernel<WIDE, D>, (unsigned)(a.blocks - 1), stream, "attention combine", a, S::ROWS);
+    return launch(attention_combine_kernel<WIDE, D>, dim3((unsigned)(a.blocks - 1), S::ROWS), kCombineThreads, 0, stream, "attention combine",
+                  a, S::ROWS);
 }
 
 template <bool WIDE, int BITS>
 hq_status run_dim(const AttentionArgs &x, const AttnArgs &a, int num_sms, cudaStream_t stream) {
     const int nt = stream_tiles(x);
-    if (x.cache.head_dim == 256) return run_stream<WIDE, BITS, 256, 1>(x, a, num_sms, stream);
+    if (x.cache.head_dim == 256)                            // f32: the registers are for 8 rows
+        return nt == 1 ? run_stream<WIDE, BITS, 256, 1>(x, a, num_sms, stream)
+                       : run_stream<WIDE, BITS, 256, WIDE ? 1 : 2>(x, a, num_sms, stream);
     if (x.cache.head_dim == 128)
         return nt == 1 ? run_stream<WIDE, BITS, 128, 1>(x, a, num_sms, stream) : run_stream<WIDE, BITS, 128, 2>(x, a, num_sms, stream);
     return nt == 1 ? run_stream<WIDE, BITS, 64, 1>(x, a, num_sms, stream) : run_stream<WIDE, BITS, 64, 2>(x, a, num_sms, stream);

@@ -93,20 +93,19 @@ struct Walk {
     Request q;
 };
 
-// The item of the walk's next unit, and which of its units that is.
+// The item of a unit, and which of its units that is.
 struct Item {
-    int tile, kv_head, part;            // of request r
+    int tile, kv_head, part;            // of a request
     long long first;                    // its first unit
-    int units, unit;                    // how many it has, and which one x is
+    int units, unit;                    // how many it has, and which one it is
 };
 
 struct WalkShared {
     long long warp_sum[32];
     Walk walk;
-    Item item;
 };
 
-// Inclusive scan over the block; every thread gets the block's sum.
+// Inclusive scan over the THREADS threads that call (the block, or a warp); every thread gets their sum.
 template <int THREADS>
 __device__ __forceinline__ long long block_scan(long long v, long long &sum, WalkShared &s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -115,24 +114,30 @@ __device__ __forceinline__ long long block_scan(long long v, long long &sum, Wal
         const long long w = __shfl_up_sync(0xffffffffu, v, d);
         if (lane >= d) v += w;
     }
-    __syncthreads();
-    if (lane == 31) s.warp_sum[warp] = v;
-    __syncthreads();
-    sum = 0;
-    long long before = 0;
-    for (int i = 0; i < THREADS / 32; ++i) {
-        if (i < warp) before += s.warp_sum[i];
-        sum += s.warp_sum[i];
+    if constexpr (THREADS == 32) {
+        sum = __shfl_sync(0xffffffffu, v, 31);
+        return v;
+    } else {
+        __syncthreads();
+        if (lane == 31) s.warp_sum[warp] = v;
+        __syncthreads();
+        sum = 0;
+        long long before = 0;
+        for (int i = 0; i < THREADS / 32; ++i) {
+            if (i < warp) before += s.warp_sum[i];
+            sum += s.warp_sum[i];
+        }
+        return v + before;
     }
-    return v + before;
 }
 
-// Takes the walk to the request with its next unit x, looking from request r0 on, which begins at unit `start`.  The whole
-// block calls it; x is below the batch's units.
+// Takes the walk to the request with unit x, looking from request r0 on, which begins at unit `start`.  The whole
+// block calls it, or (THREADS 32) one warp; x is below the batch's units.
 template <int THREADS>
 __device__ __forceinline__ void walk_to(const AttnArgs &a, long long x, int r0, long long start, WalkShared &s) {
+    const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
     for (long long i = r0; i < a.c.n_req; i += THREADS) {
-        const long long r = i + threadIdx.x;
+        const long long r = i + tid;
         Request q = {0, 0, 0, false};
         if (r < a.c.n_req) q = request_of(a.c, (int)r);
         const long long u = request_units(a, q);
@@ -147,7 +152,7 @@ __device__ __forceinline__ void walk_to(const AttnArgs &a, long long x, int r0, 
         start += sum;
         if (x < start) break;
     }
-    __syncthreads();
+    if (THREADS == 32) __syncwarp(); else __syncthreads();
 }
 
 // The first unit of block `b`.  Few units go to few blocks, min_units each.
@@ -182,6 +187,30 @@ __device__ __forceinline__ Item item_at(const AttnArgs &a, const Walk &w, long l
     it.unit = (int)(rest - (long long)h * it.units);
     it.first = x - it.unit;
     return it;
+}
+
+// A block's part of an item: `take` units from `unit` on.  What the producer warp tells the consumers.
+struct Part {
+    Request q;
+    Item item;
+    int take, slot;                     // 0: no more; where the partial result goes, or -1: the whole item
+    int begin;                          // the position of its first unit
+    Range span;                         // positions of it that some row sees
+    int all_lo, all_hi;                 // every row sees [all_lo, all_hi) of them
+};
+__device__ __forceinline__ Part part_at(const AttnArgs &a, const Walk &w, long long x, long long x0, long long end) {
+    Part p;
+    p.q = w.q;
+    p.item = item_at(a, w, x);
+    p.take = (int)min((long long)(p.item.units - p.item.unit), end - x);
+    p.slot = p.take == p.item.units ? -1 : 2 * (int)blockIdx.x + (x == x0 ? 0 : 1);
+    const int t0 = p.item.tile * a.tokens, t1 = min(t0 + a.tokens, w.q.n) - 1;
+    const Range first = seen_by(a, w.q, t0), last = seen_by(a, w.q, t1);
+    p.begin = (first.lo / kUnit + p.item.unit) * kUnit;
+    p.span = {first.lo, min(p.begin + p.take * kUnit, last.hi)};
+    p.all_lo = last.lo;
+    p.all_hi = first.hi;
+    return p;
 }
 
 // Row i of an item is token tile * tokens + i / part_heads of the request, and of its group head part * part_heads + i % part_heads.
