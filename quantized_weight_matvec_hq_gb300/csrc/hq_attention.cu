@@ -9,8 +9,7 @@
 // multiplies the weights, which go from one operand's layout to the other's by movmatrix.
 //
 // Weights are exp2(z - m) with m within 2^5 of the row's running maximum: it is raised, and the outputs so far
-// are rescaled, only when a score passes it by that much.  Values' scales are brought to [2^8, 2^9) by a power of two that a
-// warp holds, so that 16 bits keep the products' relative precision down to 2^-23 of the largest.
+// are rescaled, only when a score passes it by that much.
 #include <type_traits>
 
 #include <algorithm>
@@ -21,7 +20,8 @@
 namespace hq {
 namespace {
 
-constexpr int kUnitCells = kUnit / kCell;
+constexpr int kWarps = 4, kConsumers = 32 * kWarps, kThreads = kConsumers + 32;     // the last warp is the producer
+constexpr int kUnit = kCell * kWarps;                       // a consumer warp has a cell of every unit
 constexpr int kCombineThreads = 128;
 constexpr float kSlack = 5.f;
 
@@ -63,6 +63,24 @@ __device__ __forceinline__ void decode_q8(uint32_t w0, uint32_t w1, uint32_t (&h
     h[3] = h2_bits(__hadd2(bits_h2(prmt(w1, 0x64646464u, SEL1)), off));
 }
 
+// The same with the quants left unsigned, as 16-bit floats of n 2^-24 (pairs 0 and 2) and n 2^-20, or of u 2^-24: subnormal numbers,
+// which the bits are already.
+template <class = void>
+__device__ __forceinline__ void decode_q4_raw(uint32_t w, uint32_t (&h)[4]) {
+    const uint32_t v = w >> 8;
+    h[0] = w & 0x000f000fu;
+    h[1] = w & 0x00f000f0u;
+    h[2] = v & 0x000f000fu;
+    h[3] = v & 0x00f000f0u;
+}
+template <class = void>
+__device__ __forceinline__ void decode_q8_raw(uint32_t w0, uint32_t w1, uint32_t (&h)[4]) {
+    h[0] = prmt(w0, 0, 0x4140);
+    h[1] = prmt(w0, 0, 0x4342);
+    h[2] = prmt(w1, 0, 0x4140);
+    h[3] = prmt(w1, 0, 0x4342);
+}
+
 // WORDS 32-bit words of shared memory.
 template <int WORDS>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&v)[WORDS]) {
@@ -87,28 +105,37 @@ struct Stream {
     using L = CellLayout<BITS, D>;
     static constexpr bool WIDE = WIDE_;                     // q and the weights in two terms
     static constexpr int TERMS = WIDE ? 2 : 1;
+    // Keys unsigned: the offset's part of a block's sum, -8 or -128 times the sum of q, is where the sum starts.  Its rounding is 2^-22 of
+    // the largest key times the sum of |q|; f32 decodes the signed quants instead.
+    static constexpr bool RAW = !WIDE;
     static constexpr int ROWS = 8 * NT, NB = L::NB;
-    static constexpr int STAGE = kUnitCells * L::BYTES;     // a stage of the ring is a unit
-    // Consumer warps, and behind them the producer; two blocks a multiprocessor where 96 registers are enough for a thread.
-    static constexpr int WARPS = NB * NT >= 16 ? 4 : 8, CONSUMERS = 32 * WARPS, THREADS = CONSUMERS + 32;
-    static constexpr int MIN_BLOCKS = NT == 1 && NB * (WIDE ? 2 : 1) <= 4 ? 2 : 1;
+    static constexpr int STAGE = kWarps * L::BYTES;     // a stage of the ring is a unit
+    // Blocks a multiprocessor, by the registers that a thread needs (of 5 warps each; 4: 96, 3: 128, 2: 168).
+    static constexpr int MIN_BLOCKS = NT == 1 ? (D == 256 ? 2 : WIDE && D == 128 ? 3 : 4) : D == 64 && !WIDE ? 3 : 2;
     static constexpr int MAX_STAGES = 6;
+
+    // The power of two for scales with this largest exponent field (the value is in [2^(e - 15), 2^(e - 14))).
+    // 16 bits: none between 2^-12 and 2: with weights of up to 2^15 (2^10 at the running maximum) the products stay in range,
+    // and keep their 11 bits down to 2^-12 of the largest at least.  f32: to [2^8, 2^9), for its second terms.
+    static constexpr float WEIGHT = WIDE ? 0.f : 10.f;      // weights are exp2(z - m + WEIGHT)
+    static __device__ __forceinline__ int shift_of(int e) { return WIDE ? 23 - e : e > 15 ? 15 - e : e < 3 ? 10 : 0; }
 
     struct Shared {
         WalkShared walk;
         uint4 q[TERMS][NT][NB][32];                         // the Q operand: lane (row g, c) has elements 8 c .. + 7 of a block
         Part part[2];                                       // this part and the one the producer is ahead with
+        alignas(8) float offset[NB][ROWS];
         alignas(8) float factor[ROWS];                                // scores = sum * factor, in powers of two
         Range seen[ROWS];
-        float m[WARPS][ROWS], l[WARPS][ROWS];
+        float m[kWarps][ROWS], l[kWarps][ROWS];
         uint32_t bad[ROWS];                                 // value blocks that are no numbers and that the row sees
-        alignas(16) float o[WARPS / 2][ROWS][D + 4];       // read as float4
+        alignas(16) float o[kWarps / 2][ROWS][D + 4];       // read as float4
         alignas(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], part_full[2], part_empty[2];
         uint32_t cells[MAX_STAGES];                         // of a stage: bit i: cell i is there; bit 16 + i: its page is out of range
         int abort;
     };
     static constexpr int FIXED = ((int)sizeof(Shared) + 127) / 128 * 128;
-    static constexpr int LIMIT = (MIN_BLOCKS == 2 ? 113 : 226) * 1024;
+    static constexpr int LIMIT = (228 / MIN_BLOCKS - 1) * 1024;
     static constexpr int STAGES = (LIMIT - FIXED) / STAGE < MAX_STAGES ? (LIMIT - FIXED) / STAGE : MAX_STAGES;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
     static_assert(STAGES >= 2, "the ring needs two stages");
@@ -118,7 +145,7 @@ struct Stream {
         constexpr int LANES = D / 8;                        // lanes of a row
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = lane % LANES;
 #pragma unroll
-        for (int r0 = 0; r0 < ROWS; r0 += CONSUMERS / LANES) {
+        for (int r0 = 0; r0 < ROWS; r0 += kConsumers / LANES) {
             const int row = r0 + warp * (32 / LANES) + lane / LANES;
             int token = 0, head = 0;
             const bool live = row < ROWS && row_of(a, part.q, part.item, row, token, head);
@@ -132,12 +159,20 @@ struct Stream {
             const int e = min(253, 268 - (int)(top >> 23)); // exponent field of the power: its value is 2^(e - 127)
             const float up = __uint_as_float((uint32_t)e << 23);
             uint32_t h[4], r[4];
+            float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const __half2 x = __floats2half2_rn(v[2 * i] * up, v[2 * i + 1] * up);
                 h[i] = h2_bits(x);
                 const float2 f = __half22float2(x);
+                sum += f.x + f.y;
+                if (RAW && BITS == 4 && (i & 1)) h[i] = h2_bits(__hmul2(x, __half2half2(__ushort_as_half(0x2c00))));      // times 1/16, for quants times 16
                 r[i] = h2_bits(__floats2half2_rn(v[2 * i] * up - f.x, v[2 * i + 1] * up - f.y));
+            }
+            if (RAW) {                                      // of the block: four lanes
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (row < ROWS && (at & 3) == 0) s.offset[at >> 2][row] = sum * (BITS == 4 ? -0x1p-21f : -0x1p-17f);
             }
             if (row < ROWS) {
                 const int to = (row & 7) * 4 + (at & 3);
@@ -146,7 +181,7 @@ struct Stream {
                 if (at == 0) {
                     // a row that holds no number makes all its scores NaN
                     s.factor[row] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
-                                                       : a.scale * kLog2e * __uint_as_float((uint32_t)(254 - e) << 23);
+                                                       : a.scale * kLog2e * (RAW ? 0x1p24f : 1.f) * __uint_as_float((uint32_t)(254 - e) << 23);
                     s.bad[row] = 0;
                     s.seen[row] = seen_by(a, part.q, min(token, part.q.n - 1));
                 }
@@ -161,7 +196,7 @@ __device__ __forceinline__ void stream_produce(const AttnArgs &a, typename Strea
                                                long long x0, long long end) {
     using S = Stream<WIDE, BITS, D, NT>;
     using L = typename S::L;
-    constexpr int AHEAD = 32 / kUnitCells;                  // units whose cells are looked up at once
+    constexpr int AHEAD = 32 / kWarps;                  // units whose cells are looked up at once
     const int lane = threadIdx.x & 31;
     volatile int *abort = &s.abort;
     const uint64_t policy = l2_evict_first_policy();
@@ -194,17 +229,17 @@ __device__ __forceinline__ void stream_produce(const AttnArgs &a, typename Strea
                 }
             }
             if (!mbar_wait(smem_u32(&s.empty[stage]), phase, abort, a.c.fault)) goto drain;
-            const int first = u % AHEAD * kUnitCells;
-            const uint32_t there = __ballot_sync(0xffffffffu, cell > 1) >> first & 0xffu;
-            const uint32_t bad = __ballot_sync(0xffffffffu, cell == 1) >> first & 0xffu;
+            const int first = u % AHEAD * kWarps;
+            const uint32_t there = __ballot_sync(0xffffffffu, cell > 1) >> first & ((1u << kWarps) - 1);
+            const uint32_t bad = __ballot_sync(0xffffffffu, cell == 1) >> first & ((1u << kWarps) - 1);
             const uint32_t full = smem_u32(&s.full[stage]);
             if (lane == 0) {
                 s.cells[stage] = there | bad << 16;
                 mbar_arrive_expect_tx(full, __popc(there) * L::BYTES);
             }
             __syncwarp();
-            if (lane / kUnitCells == u % AHEAD && cell > 1)
-                bulk_load(ring + stage * S::STAGE + lane % kUnitCells * L::BYTES, reinterpret_cast<const void *>(cell), L::BYTES, full, policy);
+            if (lane / kWarps == u % AHEAD && cell > 1)
+                bulk_load(ring + stage * S::STAGE + lane % kWarps * L::BYTES, reinterpret_cast<const void *>(cell), L::BYTES, full, policy);
             if (++stage == S::STAGES) { stage = 0; phase ^= 1; }
         }
         x += p.take;
@@ -227,9 +262,9 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
     constexpr int NB = S::NB, ROWS = S::ROWS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
 
-    named_barrier(1, S::CONSUMERS);                           // the part before is done with the shared memory
+    named_barrier(1, kConsumers);                           // the part before is done with the shared memory
     S::prepare_rows(a, part, s);
-    named_barrier(1, S::CONSUMERS);
+    named_barrier(1, kConsumers);
 
     float o[NT][NB][2][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -244,18 +279,16 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[n][b][0][i] = o[n][b][1][i] = 0.f;
     }
-    int up = 23;                                            // the values' scales are taken times 2^up
+    int up = S::shift_of(0);                                // the values' scales are taken times 2^up
     bool ok = true;
     for (int u = 0; u < part.take; ++u) {
         const uint32_t stage = lap >> 1;                    // the ring's stage, and below it the phase of its barrier
         if (!mbar_wait(smem_u32(&s.full[stage]), lap & 1, &s.abort, a.c.fault)) { ok = false; break; }
         const uint32_t states = s.cells[stage];
-#pragma unroll 1
-        for (int j = warp; j < kUnitCells; j += S::WARPS) {
-            const uint32_t state = states >> j & 0x10001u;
-            if (state == 0) continue;                       // the whole warp
-            const uint8_t *cell = ring + stage * S::STAGE + j * L::BYTES;
-            const int p0 = part.begin + u * kUnit + j * kCell;
+        const uint32_t state = states >> warp & 0x10001u;
+        if (state != 0) {                                   // the whole warp
+            const uint8_t *cell = ring + stage * S::STAGE + warp * L::BYTES;
+            const int p0 = part.begin + u * kUnit + warp * kCell;
             // ---- scores
             float z[NT][4];
 #pragma unroll
@@ -275,7 +308,13 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                 for (int i = 0; i < BLOCKS; ++i) {
                     const int b = v * BLOCKS + i;
                     uint32_t ka[4], kb[4];
-                    if constexpr (BITS == 4) {
+                    if constexpr (S::RAW && BITS == 4) {
+                        decode_q4_raw(k0[i], ka);
+                        decode_q4_raw(k1[i], kb);
+                    } else if constexpr (S::RAW) {
+                        decode_q8_raw(k0[2 * i], k0[2 * i + 1], ka);
+                        decode_q8_raw(k1[2 * i], k1[2 * i + 1], kb);
+                    } else if constexpr (BITS == 4) {
                         decode_q4(k0[i], ka);
                         decode_q4(k1[i], kb);
                     } else {
@@ -287,6 +326,11 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                        if (S::RAW) {
+                            const float2 x = *reinterpret_cast<const float2 *>(&s.offset[b][8 * n + 2 * c]);
+                            acc[0] = acc[2] = x.x;
+                            acc[1] = acc[3] = x.y;
+                        }
 #pragma unroll
                         for (int t = S::TERMS - 1; t >= 0; --t) {
                             const uint4 q = s.q[t][n][b][lane];
@@ -349,26 +393,34 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    z[n][e] = ex2(z[n][e] - fmaxf(m[n][e & 1], -3e38f));            // nothing seen yet: 0
+                    z[n][e] = ex2(z[n][e] - (fmaxf(m[n][e & 1], -3e38f) - S::WEIGHT));      // nothing seen yet: 0
                     l[n][e & 1] += z[n][e];
                 }
-            // ---- the power of two of the values' scales, and blocks that are no numbers
-            if (edge) {                                     // positions that no row sees count for nothing
-                const int begin = part.span.lo, end = part.span.hi;
+            // ---- the power of two of the values' scales, and blocks that are no numbers: a word (two positions' scale) a lane
+            constexpr int WORDS = (8 * NB + 31) / 32;
+            uint32_t mine[WORDS], top = 0;
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                const int at = (lane + 32 * i) % (8 * NB);
+                mine[i] = *reinterpret_cast<const uint32_t *>(cell + L::VS + 4 * at) & 0x7fff7fffu;
+                if (edge) {                                 // positions that no row sees count for nothing
+                    const int p = p0 + 2 * (at / NB);
+                    mine[i] &= (p >= part.span.lo && p < part.span.hi ? 0xffffu : 0u) |
+                               (p + 1 >= part.span.lo && p + 1 < part.span.hi ? 0xffff0000u : 0u);
+                }
+                top = max(top, max(mine[i] & 0xffffu, mine[i] >> 16));
+            }
+            top = gone ? 0u : __reduce_max_sync(0xffffffffu, top);
+            if (edge) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int p = p0 + 2 * (c + 4 * h);
-                    const uint32_t keep = (p >= begin && p < end ? 0xffffu : 0u) | (p + 1 >= begin && p + 1 < end ? 0xffff0000u : 0u);
+                    const uint32_t keep = (p >= part.span.lo && p < part.span.hi ? 0xffffu : 0u) |
+                                          (p + 1 >= part.span.lo && p + 1 < part.span.hi ? 0xffff0000u : 0u);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) vs[h][b] &= keep;
                 }
             }
-            uint32_t top = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int b = 0; b < NB; ++b) top = __vmaxu2(top, vs[h][b] & 0x7fff7fffu);
-            top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
             if (top >= 0x7c00u) {                           // an infinity or a NaN: its block leaves the product, its rows are marked
                 top = 0;
 #pragma unroll
@@ -389,7 +441,7 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                         }
                 top = __reduce_max_sync(0xffffffffu, top);
             }
-            const int want = 23 - (int)(top >> 10);
+            const int want = S::shift_of((int)(top >> 10));
             if (want < up) {
                 const float f = __uint_as_float((uint32_t)(127 + want - up) << 23);
 #pragma unroll
@@ -400,8 +452,15 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                         for (int e = 0; e < 4; ++e) { o[n][b][0][e] *= f; o[n][b][1][e] *= f; }
                 up = want;
             }
-            const __half2 up1 = __half2half2(__ushort_as_half((uint16_t)((15 + min(up, 15)) << 10)));
-            const __half2 up2 = __half2half2(__ushort_as_half((uint16_t)((15 + up - min(up, 15)) << 10)));
+            if (up != 0) {
+                const int part1 = min(max(up, -14), 15);    // two factors that are normal numbers
+                const __half2 up1 = __half2half2(__ushort_as_half((uint16_t)((15 + part1) << 10)));
+                const __half2 up2 = __half2half2(__ushort_as_half((uint16_t)((15 + up - part1) << 10)));
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) vs[h][b] = h2_bits(__hmul2(__hmul2(bits_h2(vs[h][b]), up1), up2));
+            }
             // ---- outputs
             uint32_t ph[NT][2], pr[NT][2];                  // the weights, positions along a register: pairs c and c + 4
 #pragma unroll
@@ -432,12 +491,7 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                         decode_q8<0x4240, 0x4341>(v0[2 * i], v0[2 * i + 1], va);
                         decode_q8<0x4240, 0x4341>(v1[2 * i], v1[2 * i + 1], vb);
                     }
-                    __half2 d[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        d[h] = __hmul2(bits_h2(vs[h][b]), up1);
-                        if (up > 15) d[h] = __hmul2(d[h], up2);
-                    }
+                    const __half2 d[2] = {bits_h2(vs[0][b]), bits_h2(vs[1][b])};
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         uint32_t p[2], r[2];
@@ -481,11 +535,11 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                 s.l[warp][8 * n + 2 * c + k] = l[n][k];
             }
         }
-    named_barrier(1, S::CONSUMERS);
+    named_barrier(1, kConsumers);
     const float down = __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
     for (int turn = 0; turn < 2; ++turn) {
-        if (warp / (S::WARPS / 2) == 1 - turn) {
+        if (warp / (kWarps / 2) == 1 - turn) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -493,9 +547,9 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                     const int row = 8 * n + 2 * c + k;
                     float t = s.m[0][row];
 #pragma unroll
-                    for (int i = 1; i < S::WARPS; ++i) t = fmaxf(t, s.m[i][row]);
+                    for (int i = 1; i < kWarps; ++i) t = fmaxf(t, s.m[i][row]);
                     const float f = (m[n][k] == t ? 1.f : ex2(m[n][k] - t)) * down;
-                    float *to = s.o[warp % (S::WARPS / 2)][row] + g;
+                    float *to = s.o[warp % (kWarps / 2)][row] + g;
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -506,20 +560,20 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                         }
                 }
         }
-        named_barrier(1, S::CONSUMERS);
+        named_barrier(1, kConsumers);
     }
     constexpr int CHUNKS = D / 8;                           // 8 columns a thread
-    for (int i = threadIdx.x; i < ROWS * CHUNKS; i += S::CONSUMERS) {
+    for (int i = threadIdx.x; i < ROWS * CHUNKS; i += kConsumers) {
         const int row = i / CHUNKS, at = i % CHUNKS;
         int token, head;
         if (!row_of(a, part.q, part.item, row, token, head)) continue;
         float t = s.m[0][row], sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 1; k < S::WARPS; ++k) t = fmaxf(t, s.m[k][row]);
+        for (int k = 1; k < kWarps; ++k) t = fmaxf(t, s.m[k][row]);
 #pragma unroll
-        for (int k = 0; k < S::WARPS; ++k) sum += s.l[k][row] * (s.m[k][row] == t ? 1.f : ex2(s.m[k][row] - t));
+        for (int k = 0; k < kWarps; ++k) sum += s.l[k][row] * (s.m[k][row] == t ? 1.f : ex2(s.m[k][row] - t));
 #pragma unroll
-        for (int k = 0; k < S::WARPS / 2; ++k) {
+        for (int k = 0; k < kWarps / 2; ++k) {
             const float4 x = *reinterpret_cast<const float4 *>(&s.o[k][row][8 * at]);
             const float4 y = *reinterpret_cast<const float4 *>(&s.o[k][row][8 * at + 4]);
             v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w; v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
@@ -543,7 +597,7 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
 }
 
 template <bool WIDE, int BITS, int D, int NT>
-__global__ void __launch_bounds__((Stream<WIDE, BITS, D, NT>::THREADS), (Stream<WIDE, BITS, D, NT>::MIN_BLOCKS)) attention_stream_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, (Stream<WIDE, BITS, D, NT>::MIN_BLOCKS)) attention_stream_kernel(const __grid_constant__ AttnArgs a) {
     using S = Stream<WIDE, BITS, D, NT>;
     extern __shared__ __align__(128) uint8_t memory[];
     typename S::Shared &s = *reinterpret_cast<typename S::Shared *>(memory);
@@ -551,11 +605,11 @@ __global__ void __launch_bounds__((Stream<WIDE, BITS, D, NT>::THREADS), (Stream<
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
             mbar_init(smem_u32(&s.full[i]), 1);
-            mbar_init(smem_u32(&s.empty[i]), S::WARPS);
+            mbar_init(smem_u32(&s.empty[i]), kWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s.part_full[i]), 1);
-            mbar_init(smem_u32(&s.part_empty[i]), S::WARPS);
+            mbar_init(smem_u32(&s.part_empty[i]), kWarps);
         }
         fence_mbar_init();
         s.abort = 0;
@@ -563,13 +617,13 @@ __global__ void __launch_bounds__((Stream<WIDE, BITS, D, NT>::THREADS), (Stream<
     griddep_launch_dependents();
     griddep_wait();
     if (blockIdx.x == 0)
-        for (int r = threadIdx.x; r < a.c.n_req; r += S::THREADS)
+        for (int r = threadIdx.x; r < a.c.n_req; r += kThreads)
             if (request_of(a.c, r).bad) atomicOr(a.c.fault, kFaultCache);
-    const long long total = batch_units<S::THREADS>(a, s.walk);               // (barriers, which the mbarriers' set-up needs)
+    const long long total = batch_units<kThreads>(a, s.walk);               // (barriers, which the mbarriers' set-up needs)
     const long long x0 = first_unit(a, total, blockIdx.x), end = first_unit(a, total, blockIdx.x + 1);
     if (x0 >= end) return;
-    walk_to<S::THREADS>(a, x0, 0, 0, s.walk);
-    if (threadIdx.x >= S::CONSUMERS) {
+    walk_to<kThreads>(a, x0, 0, 0, s.walk);
+    if (threadIdx.x >= kConsumers) {
         stream_produce<WIDE, BITS, D, NT>(a, s, smem_u32(ring), x0, end);
         return;
     }
@@ -680,12 +734,12 @@ hq_status allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
     return HQ_OK;
 }
 
-constexpr int kMaxBlocks = 304;                             // the workspace holds two partial results of each
+constexpr int kMaxBlocks = 608;                             // the workspace holds two partial results of each
 
 // Rows of a tile: the mean request's query rows a key/value head decide.
 int stream_tiles(const AttentionArgs &x) {
     const int64_t rows = (x.cache.n_tokens + x.cache.n_req - 1) / x.cache.n_req * (x.n_heads / x.cache.n_kv_heads);
-    return rows <= 8 || (x.cache.head_dim == 256 && x.cache.dtype == HQ_DT_F32) ? 1 : 2;
+    return rows <= 8 || x.cache.head_dim == 256 ? 1 : 2;
 }
 
 template <bool WIDE, int BITS, int D, int NT>
@@ -701,10 +755,12 @@ hq_status run_stream(const AttentionArgs &x, AttnArgs a, int num_sms, cudaStream
     a.blocks = std::min(kMaxBlocks, num_sms * S::MIN_BLOCKS);
     if (most < a.blocks) a.blocks = (int)most;
     a.min_units = 1;
+    static_assert(kUnit == 64, "2^6");
+    a.unit_shift = 6;
     static std::atomic<bool> done[64];
     hq_status st = allow_smem(attention_stream_kernel<WIDE, BITS, D, NT>, S::SMEM, done);
     if (st != HQ_OK) return st;
-    st = launch(attention_stream_kernel<WIDE, BITS, D, NT>, dim3((unsigned)a.blocks), S::THREADS, S::SMEM, stream, "attention", a);
+    st = launch(attention_stream_kernel<WIDE, BITS, D, NT>, dim3((unsigned)a.blocks), kThreads, S::SMEM, stream, "attention", a);
     if (st != HQ_OK || a.blocks < 2 || per_tile < 2) return st;             // an item of one unit is never divided
     return launch(attention_combine_kernel<WIDE, D>, dim3((unsigned)(a.blocks - 1), S::ROWS), kCombineThreads, 0, stream, "attention combine",
                   a, S::ROWS);
@@ -713,9 +769,7 @@ hq_status run_stream(const AttentionArgs &x, AttnArgs a, int num_sms, cudaStream
 template <bool WIDE, int BITS>
 hq_status run_dim(const AttentionArgs &x, const AttnArgs &a, int num_sms, cudaStream_t stream) {
     const int nt = stream_tiles(x);
-    if (x.cache.head_dim == 256)                            // f32: the registers are for 8 rows
-        return nt == 1 ? run_stream<WIDE, BITS, 256, 1>(x, a, num_sms, stream)
-                       : run_stream<WIDE, BITS, 256, WIDE ? 1 : 2>(x, a, num_sms, stream);
+    if (x.cache.head_dim == 256) return run_stream<WIDE, BITS, 256, 1>(x, a, num_sms, stream);
     if (x.cache.head_dim == 128)
         return nt == 1 ? run_stream<WIDE, BITS, 128, 1>(x, a, num_sms, stream) : run_stream<WIDE, BITS, 128, 2>(x, a, num_sms, stream);
     return nt == 1 ? run_stream<WIDE, BITS, 64, 1>(x, a, num_sms, stream) : run_stream<WIDE, BITS, 64, 2>(x, a, num_sms, stream);

@@ -2,7 +2,7 @@
 //
 // An item is a tile of a request's query rows on one key/value head: up to `tokens` neighbouring tokens with all heads
 // of the group, or, where a group has more heads than a tile has rows, one token with a part of them.  The positions that an item
-// sees are cut into units of kUnit; the units of all items, one after another, are dealt to the blocks in equal
+// sees are cut into units of 2^unit_shift; the units of all items, one after another, are dealt to the blocks in equal
 // contiguous ranges.  Lengths are known on the device only, so every block finds its range itself.
 // An item that one block has whole is finished there; of the others each block leaves a partial result (its maximum, sum
 // and weighted sum), and the combine kernel joins them.
@@ -13,8 +13,6 @@
 #include "hq_cache.cuh"
 
 namespace hq {
-
-constexpr int kUnit = 128;
 
 struct AttnArgs {
     CacheView c;
@@ -28,7 +26,7 @@ struct AttnArgs {
     float scale;
     long long window;                   // 0: none
     float *partial;                     // [2 blocks][rows][head_dim], then [2 blocks][rows][2]: maximum, sum
-    int blocks, min_units;
+    int unit_shift, blocks, min_units;
 };
 
 // sum of floor((a i + b) / m) for i < n; a, b >= 0 (the Euclidean recursion)
@@ -49,12 +47,12 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
     return s;
 }
 
-// sum of floor(max(0, c + tokens j) / kUnit) for j < n
-__device__ __forceinline__ long long unit_sum(int n, long long c, int tokens) {
+// sum of floor(max(0, c + tokens j) / 2^shift) for j < n
+__device__ __forceinline__ long long unit_sum(int n, long long c, int tokens, int shift) {
     if (n <= 0) return 0;
-    if (n == 1) return c > 0 ? (long long)((unsigned)c / kUnit) : 0;
+    if (n == 1) return c > 0 ? c >> shift : 0;
     const long long skip = c < 0 ? (-c + tokens - 1) / tokens : 0;
-    return floor_sum(n - skip, kUnit, tokens, c + skip * tokens);
+    return floor_sum(n - skip, 1ll << shift, tokens, c + skip * tokens);
 }
 
 // Positions [lo, hi) that a token sees.
@@ -73,12 +71,12 @@ __device__ __forceinline__ int tiles_of(const AttnArgs &a, const Request &q) { r
 // last token's position; it has at least one unit, so that rows that see nothing are written too.
 __device__ __forceinline__ long long units_before(const AttnArgs &a, const Request &q, int j) {
     if (j == 0) return 0;
-    if (!a.causal) return (long long)j * max(1, (q.length + kUnit - 1) / kUnit);
+    if (!a.causal) return (long long)j * max(1, (q.length + (1 << a.unit_shift) - 1) >> a.unit_shift);
     const int base = q.length - q.n, n = tiles_of(a, q);
-    long long u = j;                                        // 1 + floor((last position) / kUnit) each
-    u += unit_sum(j - (j == n), (long long)base + a.tokens - 1, a.tokens);
-    if (j == n && q.length > 0) u += (q.length - 1) / kUnit;
-    if (a.window > 0) u -= unit_sum(j, (long long)base + 1 - a.window, a.tokens);
+    long long u = j;                                        // 1 + floor((last position) / unit) each
+    u += unit_sum(j - (j == n), (long long)base + a.tokens - 1, a.tokens, a.unit_shift);
+    if (j == n && q.length > 0) u += (q.length - 1) >> a.unit_shift;
+    if (a.window > 0) u -= unit_sum(j, (long long)base + 1 - a.window, a.tokens, a.unit_shift);
     return u;
 }
 
@@ -206,8 +204,8 @@ __device__ __forceinline__ Part part_at(const AttnArgs &a, const Walk &w, long l
     p.slot = p.take == p.item.units ? -1 : 2 * (int)blockIdx.x + (x == x0 ? 0 : 1);
     const int t0 = p.item.tile * a.tokens, t1 = min(t0 + a.tokens, w.q.n) - 1;
     const Range first = seen_by(a, w.q, t0), last = seen_by(a, w.q, t1);
-    p.begin = (first.lo / kUnit + p.item.unit) * kUnit;
-    p.span = {first.lo, min(p.begin + p.take * kUnit, last.hi)};
+    p.begin = ((first.lo >> a.unit_shift) + p.item.unit) << a.unit_shift;
+    p.span = {first.lo, min(p.begin + (p.take << a.unit_shift), last.hi)};
     p.all_lo = last.lo;
     p.all_hi = first.hi;
     return p;
