@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kWarps = 4, kConsumers = 32 * kWarps, kThreads = kConsumers + 32;     // the last warp is the producer
 constexpr int kUnit = kCell * kWarps;                       // a consumer warp has a cell of every unit
-constexpr int kCombineThreads = 128;
+constexpr int kCombineThreads = 256, kCombineRows = 2;
 constexpr float kSlack = 5.f;
 
 // ------------------------------------------------------------------ operands
@@ -43,6 +43,7 @@ __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cas
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
 
 // A word of eight nibbles n -> four pairs n - 8: the magic 0x6400 | n is 1024 + n (0x6400 | n << 4: 1024 + 16 n), exact.
+template <class = void>
 __device__ __forceinline__ void decode_q4(uint32_t w, uint32_t (&h)[4]) {
     const __half2 off = __half2half2(__ushort_as_half(0xe408));                     // -1032
     const __half2 r16 = __half2half2(__ushort_as_half(0x2c00)), off16 = __half2half2(__ushort_as_half(0xd480));   // 1/16, -72
@@ -73,12 +74,12 @@ __device__ __forceinline__ void decode_q4_raw(uint32_t w, uint32_t (&h)[4]) {
     h[2] = v & 0x000f000fu;
     h[3] = v & 0x00f000f0u;
 }
-template <class = void>
+template <uint32_t SEL0, uint32_t SEL1>
 __device__ __forceinline__ void decode_q8_raw(uint32_t w0, uint32_t w1, uint32_t (&h)[4]) {
-    h[0] = prmt(w0, 0, 0x4140);
-    h[1] = prmt(w0, 0, 0x4342);
-    h[2] = prmt(w1, 0, 0x4140);
-    h[3] = prmt(w1, 0, 0x4342);
+    h[0] = prmt(w0, 0, SEL0);
+    h[1] = prmt(w0, 0, SEL1);
+    h[2] = prmt(w1, 0, SEL0);
+    h[3] = prmt(w1, 0, SEL1);
 }
 
 // WORDS 32-bit words of shared memory.
@@ -107,7 +108,11 @@ struct Stream {
     static constexpr int TERMS = WIDE ? 2 : 1;
     // Keys unsigned: the offset's part of a block's sum, -8 or -128 times the sum of q, is where the sum starts.  Its rounding is 2^-22 of
     // the largest key times the sum of |q|; f32 decodes the signed quants instead.
+    // The values' offset is a second product, with the negative offset for a quant (elements g of a block times 2^-24, g + 8 times 2^-20 or
+    // 2^-24): each cell's is taken off at once, so that no large sum of offsets builds up.
     static constexpr bool RAW = !WIDE;
+    static constexpr uint32_t LESS0 = BITS == 4 ? 0x80088008u : 0x80808080u, LESS1 = 0x80808080u;       // -8 2^-24 or -128 2^-24; -8 2^-20
+    static constexpr float BACK0 = RAW ? 0x1p24f : 1.f, BACK1 = RAW ? BITS == 4 ? 0x1p20f : 0x1p24f : 1.f;
     static constexpr int ROWS = 8 * NT, NB = L::NB;
     static constexpr int STAGE = kWarps * L::BYTES;     // a stage of the ring is a unit
     // Blocks a multiprocessor, by the registers that a thread needs (of 5 warps each; 4: 96, 3: 128, 2: 168).
@@ -193,7 +198,7 @@ struct Stream {
 // The producer warp: tells the consumers the parts, one after another, and copies their cells into the ring, a cell a lane.
 template <bool WIDE, int BITS, int D, int NT>
 __device__ __forceinline__ void stream_produce(const AttnArgs &a, typename Stream<WIDE, BITS, D, NT>::Shared &s, uint32_t ring,
-                                               long long x0, long long end) {
+                                               long long total, long long x0, long long end) {
     using S = Stream<WIDE, BITS, D, NT>;
     using L = typename S::L;
     constexpr int AHEAD = 32 / kWarps;                  // units whose cells are looked up at once
@@ -202,6 +207,8 @@ __device__ __forceinline__ void stream_produce(const AttnArgs &a, typename Strea
     const uint64_t policy = l2_evict_first_policy();
     int n = 0, stage = 0;                                   // parts and units so far
     uint32_t phase = 1;
+    Join join;
+    join.valid = 0;
     for (long long x = x0;; ++n) {
         const int at = n & 1;
         if (!mbar_wait(smem_u32(&s.part_empty[at]), (n >> 1 & 1) ^ 1, abort, a.c.fault)) break;
@@ -209,6 +216,7 @@ __device__ __forceinline__ void stream_produce(const AttnArgs &a, typename Strea
             if (lane == 0) {
                 s.part[at].take = 0;
                 mbar_arrive(smem_u32(&s.part_full[at]));
+                a.joins[blockIdx.x] = join;
             }
             return;
         }
@@ -218,6 +226,8 @@ __device__ __forceinline__ void stream_produce(const AttnArgs &a, typename Strea
             s.part[at] = p;
             mbar_arrive(smem_u32(&s.part_full[at]));
         }
+        if (p.item.unit + p.take < p.item.units && p.item.first >= x0)
+            join = {p.q, p.item, 1, p.slot, block_of(a, total, p.item.first + p.item.units - 1)};
         uint64_t cell = 0;
         for (int u = 0; u < p.take; ++u) {
             if (u % AHEAD == 0) {                           // lane i: cell i of the next units; 0: none, 1: its page is out of range
@@ -312,8 +322,8 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                         decode_q4_raw(k0[i], ka);
                         decode_q4_raw(k1[i], kb);
                     } else if constexpr (S::RAW) {
-                        decode_q8_raw(k0[2 * i], k0[2 * i + 1], ka);
-                        decode_q8_raw(k1[2 * i], k1[2 * i + 1], kb);
+                        decode_q8_raw<0x4140, 0x4342>(k0[2 * i], k0[2 * i + 1], ka);
+                        decode_q8_raw<0x4140, 0x4342>(k1[2 * i], k1[2 * i + 1], kb);
                     } else if constexpr (BITS == 4) {
                         decode_q4(k0[i], ka);
                         decode_q4(k1[i], kb);
@@ -484,7 +494,13 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                 for (int i = 0; i < BLOCKS; ++i) {
                     const int b = v * BLOCKS + i;
                     uint32_t va[4], vb[4];
-                    if constexpr (BITS == 4) {
+                    if constexpr (S::RAW && BITS == 4) {
+                        decode_q4_raw(v0[i], va);
+                        decode_q4_raw(v1[i], vb);
+                    } else if constexpr (S::RAW) {
+                        decode_q8_raw<0x4240, 0x4341>(v0[2 * i], v0[2 * i + 1], va);
+                        decode_q8_raw<0x4240, 0x4341>(v1[2 * i], v1[2 * i + 1], vb);
+                    } else if constexpr (BITS == 4) {
                         decode_q4(v0[i], va);
                         decode_q4(v1[i], vb);
                     } else {
@@ -511,6 +527,7 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                         }
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
+                            if (S::RAW) mma16816(o[n][b][t], S::LESS0, S::LESS1, S::LESS0, S::LESS1, p[0], p[1]);
                             if (S::WIDE) mma16816(o[n][b][t], va[2 * t], va[2 * t + 1], vb[2 * t], vb[2 * t + 1], r[0], r[1]);
                             mma16816(o[n][b][t], va[2 * t], va[2 * t + 1], vb[2 * t], vb[2 * t + 1], p[0], p[1]);
                         }
@@ -555,8 +572,8 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             float *x = to + 32 * b + 16 * h;
-                            x[0] = (turn ? x[0] : 0.f) + o[n][b][h][k] * f;
-                            x[8] = (turn ? x[8] : 0.f) + o[n][b][h][k + 2] * f;
+                            x[0] = (turn ? x[0] : 0.f) + o[n][b][h][k] * f * S::BACK0;
+                            x[8] = (turn ? x[8] : 0.f) + o[n][b][h][k + 2] * f * S::BACK1;
                         }
                 }
         }
@@ -590,7 +607,7 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
             const long long r = (long long)part.slot * ROWS + row;
             store8(a.partial + r * D + 8 * at, v);
             if (at == 0)
-                *reinterpret_cast<float2 *>(a.partial + 2ll * a.blocks * ROWS * D + 2 * r) = make_float2(t, sum);
+                a.stat[r] = make_float2(t, sum);
         }
     }
     return ok;
@@ -616,15 +633,14 @@ __global__ void __launch_bounds__(kThreads, (Stream<WIDE, BITS, D, NT>::MIN_BLOC
     }
     griddep_launch_dependents();
     griddep_wait();
-    if (blockIdx.x == 0)
-        for (int r = threadIdx.x; r < a.c.n_req; r += kThreads)
-            if (request_of(a.c, r).bad) atomicOr(a.c.fault, kFaultCache);
-    const long long total = batch_units<kThreads>(a, s.walk);               // (barriers, which the mbarriers' set-up needs)
-    const long long x0 = first_unit(a, total, blockIdx.x), end = first_unit(a, total, blockIdx.x + 1);
-    if (x0 >= end) return;
-    walk_to<kThreads>(a, x0, 0, 0, s.walk);
+    long long total, x0, end;
+    deal<kThreads>(a, total, x0, end, s.walk);              // (with barriers, which the mbarriers' set-up needs)
+    if (x0 >= end) {
+        if (threadIdx.x == 0) a.joins[blockIdx.x].valid = 0;
+        return;
+    }
     if (threadIdx.x >= kConsumers) {
-        stream_produce<WIDE, BITS, D, NT>(a, s, smem_u32(ring), x0, end);
+        stream_produce<WIDE, BITS, D, NT>(a, s, smem_u32(ring), total, x0, end);
         return;
     }
     uint32_t lap = 0;
@@ -639,67 +655,58 @@ __global__ void __launch_bounds__(kThreads, (Stream<WIDE, BITS, D, NT>::MIN_BLOC
     }
 }
 
-// Joins the partial results of a row (blockIdx.y) of one item: block b has that of the item that goes on past the end of block b's
-// units and does not begin before them.  D / 8 lanes a partial result, the block's groups of them take every GROUPS-th.
+// Joins the partial results of kCombineRows rows (blockIdx.y) of the item that block blockIdx.x tells of.  D / 8 lanes a row of
+// a partial result, the groups of them that a row has take every GROUPS-th block's.
 template <bool WIDE, int D>
 __global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(const __grid_constant__ AttnArgs a, int rows) {
-    constexpr int LANES = D / 8, GROUPS = kCombineThreads / LANES;
-    __shared__ WalkShared s;
-    __shared__ float gm[GROUPS], gl[GROUPS];
-    __shared__ alignas(16) float go[GROUPS][D];
+    constexpr int LANES = D / 8, GROUPS = kCombineThreads / LANES / kCombineRows;
+    __shared__ float gm[kCombineRows][GROUPS], gl[kCombineRows][GROUPS];
+    __shared__ alignas(16) float go[kCombineRows][GROUPS][D];
     griddep_launch_dependents();
     griddep_wait();
-    const long long total = batch_units<kCombineThreads>(a, s);
-    const int b = blockIdx.x, row = blockIdx.y;
-    const long long x0 = first_unit(a, total, b), x = first_unit(a, total, b + 1);
-    if (x == x0 || x >= total) return;
-    walk_to<kCombineThreads>(a, x, 0, 0, s);
-    const Item it = item_at(a, s.walk, x);
-    if (it.unit == 0 || it.first < x0) return;              // it begins with this unit, or in a block before
+    const int b = blockIdx.x;
+    if (!a.joins[b].valid) return;
+    const Join join = a.joins[b];
+    const int mine = threadIdx.x / (LANES * GROUPS), row = blockIdx.y * kCombineRows + mine;
+    const int group = threadIdx.x / LANES % GROUPS, at = threadIdx.x % LANES;
     int token, head;
-    if (!row_of(a, s.walk.q, it, row, token, head)) return;
-    const long long end = it.first + it.units;
-    int lo = b + 1, hi = a.blocks;                          // the first block that begins at the item's end or behind it
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (first_unit(a, total, mid) < end) lo = mid + 1; else hi = mid;
-    }
-    const float *stat = a.partial + 2ll * a.blocks * rows * D;
-    const int group = threadIdx.x / LANES, at = threadIdx.x % LANES;
+    const bool live = row_of(a, join.q, join.item, row, token, head);
     float t = -INFINITY, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (live) {
 #pragma unroll 4
-    for (int k = b + group; k < lo; k += GROUPS) {
-        const long long r = (2ll * k + (k == b && it.first != x0 ? 1 : 0)) * rows + row;
-        const float2 ml = *reinterpret_cast<const float2 *>(stat + 2 * r);
-        float y[8];
-        load8(a.partial + r * D + 8 * at, y);
-        const float t1 = fmaxf(t, ml.x);
-        const float f0 = t == t1 ? 1.f : ex2(t - t1), f1 = ml.x == t1 ? 1.f : ex2(ml.x - t1);
-        sum = sum * f0 + ml.y * f1;
+        for (int k = b + group; k <= join.last; k += GROUPS) {
+            const long long r = (long long)(k == b ? join.slot : 2 * k) * rows + row;
+            const float2 ml = a.stat[r];
+            float y[8];
+            load8(a.partial + r * D + 8 * at, y);
+            const float t1 = fmaxf(t, ml.x);
+            const float f0 = t == t1 ? 1.f : ex2(t - t1), f1 = ml.x == t1 ? 1.f : ex2(ml.x - t1);
+            sum = sum * f0 + ml.y * f1;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * f0 + y[e] * f1;
-        t = t1;
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * f0 + y[e] * f1;
+            t = t1;
+        }
     }
-    if (at == 0) { gm[group] = t; gl[group] = sum; }
-    store8(&go[group][8 * at], v);
+    if (at == 0) { gm[mine][group] = t; gl[mine][group] = sum; }
+    store8(&go[mine][group][8 * at], v);
     __syncthreads();
-    if (group != 0) return;
-    for (int k = 0; k < GROUPS; ++k) t = fmaxf(t, gm[k]);
+    if (group != 0 || !live) return;
+    for (int k = 0; k < GROUPS; ++k) t = fmaxf(t, gm[mine][k]);
     sum = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.f;
     for (int k = 0; k < GROUPS; ++k) {
-        const float f = gm[k] == t ? 1.f : ex2(gm[k] - t);
+        const float f = gm[mine][k] == t ? 1.f : ex2(gm[mine][k] - t);
         float y[8];
-        load8(&go[k][8 * at], y);
-        sum += gl[k] * f;
+        load8(&go[mine][k][8 * at], y);
+        sum += gl[mine][k] * f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += y[e] * f;
     }
     const float f = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= f;
-    store_row8<WIDE>(a, ((long long)s.walk.q.first + token) * a.out_stride + (long long)head * D + 8 * at, v);
+    store_row8<WIDE>(a, ((long long)join.q.first + token) * a.out_stride + (long long)head * D + 8 * at, v);
 }
 
 // ------------------------------------------------------------------ host side
@@ -755,6 +762,8 @@ hq_status run_stream(const AttentionArgs &x, AttnArgs a, int num_sms, cudaStream
     a.blocks = std::min(kMaxBlocks, num_sms * S::MIN_BLOCKS);
     if (most < a.blocks) a.blocks = (int)most;
     a.min_units = 1;
+    a.stat = reinterpret_cast<float2 *>(a.partial + 2ll * a.blocks * S::ROWS * D);
+    a.joins = reinterpret_cast<Join *>(a.stat + 2ll * a.blocks * S::ROWS);
     static_assert(kUnit == 64, "2^6");
     a.unit_shift = 6;
     static std::atomic<bool> done[64];
@@ -762,7 +771,7 @@ hq_status run_stream(const AttentionArgs &x, AttnArgs a, int num_sms, cudaStream
     if (st != HQ_OK) return st;
     st = launch(attention_stream_kernel<WIDE, BITS, D, NT>, dim3((unsigned)a.blocks), kThreads, S::SMEM, stream, "attention", a);
     if (st != HQ_OK || a.blocks < 2 || per_tile < 2) return st;             // an item of one unit is never divided
-    return launch(attention_combine_kernel<WIDE, D>, dim3((unsigned)(a.blocks - 1), S::ROWS), kCombineThreads, 0, stream, "attention combine",
+    return launch(attention_combine_kernel<WIDE, D>, dim3((unsigned)(a.blocks - 1), S::ROWS / kCombineRows), kCombineThreads, 0, stream, "attention combine",
                   a, S::ROWS);
 }
 
@@ -794,7 +803,7 @@ hq_status run_attention_f32(const AttentionArgs &x, const AttnArgs &a, int num_s
 
 int64_t attention_workspace(const AttentionArgs &x) {
     const int64_t rows = 8 * stream_tiles(x);
-    return 2ll * kMaxBlocks * rows * (x.cache.head_dim + 2) * 4;
+    return 2ll * kMaxBlocks * rows * (x.cache.head_dim + 2) * 4 + kMaxBlocks * (int64_t)sizeof(Join);
 }
 
 hq_status launch_attention(const AttentionArgs &x, cudaStream_t stream) {

@@ -25,7 +25,9 @@ struct AttnArgs {
     int causal;
     float scale;
     long long window;                   // 0: none
-    float *partial;                     // [2 blocks][rows][head_dim], then [2 blocks][rows][2]: maximum, sum
+    float *partial;                     // [2 blocks][rows][head_dim]
+    float2 *stat;                       // [2 blocks][rows]: maximum and sum of a partial result
+    struct Join *joins;                 // [blocks]
     int unit_shift, blocks, min_units;
 };
 
@@ -159,12 +161,37 @@ __device__ __forceinline__ long long first_unit(const AttnArgs &a, long long tot
     return b >= n ? total : total * b / n;
 }
 
+// The block that has a unit.
+__device__ __forceinline__ int block_of(const AttnArgs &a, long long total, long long unit) {
+    const long long n = min((long long)a.blocks, max(1ll, total / a.min_units));
+    return (int)(((unit + 1) * n - 1) / total);
+}
+
+// This block's units [x0, end) of the batch's `total`, and the walk at the first one's request.  The whole block calls it.
 template <int THREADS>
-__device__ __forceinline__ long long batch_units(const AttnArgs &a, WalkShared &s) {
-    long long mine = 0, total;
-    for (int r = threadIdx.x; r < a.c.n_req; r += THREADS) mine += request_units(a, request_of(a.c, r));
-    block_scan<THREADS>(mine, total, s);
-    return total;
+__device__ __forceinline__ void deal(const AttnArgs &a, long long &total, long long &x0, long long &end, WalkShared &s) {
+    long long mine = 0;
+    Request q = {0, 0, 0, false};
+    for (int r = threadIdx.x; r < a.c.n_req; r += THREADS) {
+        q = request_of(a.c, r);
+        if (q.bad && blockIdx.x == 0) atomicOr(a.c.fault, kFaultCache);
+        mine += request_units(a, q);
+    }
+    const long long upto = block_scan<THREADS>(mine, total, s);
+    x0 = first_unit(a, total, blockIdx.x);
+    end = first_unit(a, total, blockIdx.x + 1);
+    if (x0 >= end) return;
+    if (a.c.n_req > THREADS) {
+        walk_to<THREADS>(a, x0, 0, 0, s);
+        return;
+    }
+    if (x0 >= upto - mine && x0 < upto) {                   // a request a thread: its own
+        s.walk.r = threadIdx.x;
+        s.walk.start = upto - mine;
+        s.walk.next = upto;
+        s.walk.q = q;
+    }
+    __syncthreads();
 }
 
 __device__ __forceinline__ Item item_at(const AttnArgs &a, const Walk &w, long long x) {
@@ -210,6 +237,14 @@ __device__ __forceinline__ Part part_at(const AttnArgs &a, const Walk &w, long l
     p.all_hi = first.hi;
     return p;
 }
+
+// What the combine kernel is told: the item that begins in a block (with its first unit, or with the block's) and goes on
+// past its end, in which of the block's two partial results it begins, and the last block that has one.
+struct Join {
+    Request q;
+    Item item;
+    int valid, slot, last;
+};
 
 // Row i of an item is token tile * tokens + i / part_heads of the request, and of its group head part * part_heads + i % part_heads.
 __device__ __forceinline__ bool row_of(const AttnArgs &a, const Request &q, const Item &it, int i, int &token, int &head) {
