@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libhq.so")
 SOURCES = [("hq_api.cu", [], "hq_api.o"), ("hq_quant.cu", [], "hq_quant.o"),
            ("hq_matmul.cu", [], "hq_matmul.o"), ("hq_verify.cu", [], "hq_verify.o"),
            ("hq_cache.cu", [], "hq_cache.o"), ("hq_attention.cu", ["-DHQ_PART=0"], "hq_attention_0.o"),
-           ("hq_attention.cu", ["-DHQ_PART=1"], "hq_attention_1.o")] + [
+           ("hq_attention.cu", ["-DHQ_PART=1"], "hq_attention_1.o"),
+           ("hq_attention_tile.cu", [], "hq_attention_tile.o")] + [
     ("hq_kernels.cu", [f"-DHQ_PART={i}"], f"hq_kernels_{i}.o") for i in range(5)]
 HEADERS = ["hq_attention.cuh", "hq_cache.cuh", "hq_device.cuh", "hq_internal.h", "hq_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

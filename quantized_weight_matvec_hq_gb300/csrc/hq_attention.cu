@@ -12,9 +12,6 @@
 // are rescaled, only when a score passes it by that much.
 #include <type_traits>
 
-#include <algorithm>
-#include <atomic>
-
 #include "hq_attention.cuh"
 
 namespace hq {
@@ -711,77 +708,39 @@ __global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(cons
 
 // ------------------------------------------------------------------ host side
 
-template <class K, class... A>
-hq_status launch(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, const char *what, const A &... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-    if (e != cudaSuccess) return set_error(HQ_ERR_LAUNCH, "%s launch: %s", what, cudaGetErrorString(e));
-    note_launch();
-    return HQ_OK;
+// Query rows a key/value head of the mean request.
+int64_t mean_rows(const AttentionArgs &x) {
+    return (x.cache.n_tokens + x.cache.n_req - 1) / x.cache.n_req * (x.n_heads / x.cache.n_kv_heads);
 }
+bool on_tiles(const AttentionArgs &x) { return x.cache.dtype != HQ_DT_F32 && mean_rows(x) > 16; }
+int stream_rows(const AttentionArgs &x) { return mean_rows(x) <= 8 || x.cache.head_dim == 256 ? 8 : 16; }
 
-// Allows a kernel its shared memory, once a device.
-template <class K>
-hq_status allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
-    int d = 0;
-    cudaGetDevice(&d);
-    if (d >= 0 && d < 64 && done[d].load(std::memory_order_acquire)) return HQ_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return set_error(HQ_ERR_LAUNCH, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    if (d >= 0 && d < 64) done[d].store(true, std::memory_order_release);
-    return HQ_OK;
-}
-
-constexpr int kMaxBlocks = 608;                             // the workspace holds two partial results of each
-
-// Rows of a tile: the mean request's query rows a key/value head decide.
-int stream_tiles(const AttentionArgs &x) {
-    const int64_t rows = (x.cache.n_tokens + x.cache.n_req - 1) / x.cache.n_req * (x.n_heads / x.cache.n_kv_heads);
-    return rows <= 8 || x.cache.head_dim == 256 ? 1 : 2;
+template <bool WIDE, int D>
+hq_status run_combine(const AttnArgs &a, int rows, cudaStream_t stream) {
+    if (a.blocks < 2 || a.most_units < 2) return HQ_OK;     // an item of one unit is never divided
+    return launch_blocks(attention_combine_kernel<WIDE, D>, dim3((unsigned)(a.blocks - 1), rows / kCombineRows), kCombineThreads, 0,
+                         stream, "attention combine", a, rows);
 }
 
 template <bool WIDE, int BITS, int D, int NT>
-hq_status run_stream(const AttentionArgs &x, AttnArgs a, int num_sms, cudaStream_t stream) {
+hq_status run_stream(AttnArgs a, int num_sms, cudaStream_t stream) {
     using S = Stream<WIDE, BITS, D, NT>;
-    a.tokens = a.group <= S::ROWS ? S::ROWS / a.group : 1;
-    a.part_heads = a.group <= S::ROWS ? a.group : S::ROWS;
-    a.parts = (a.group + a.part_heads - 1) / a.part_heads;
-    // no more blocks than there can be units
-    const int64_t tiles = std::min(x.cache.n_tokens, x.cache.n_tokens / a.tokens + x.cache.n_req);
-    const int64_t per_tile = (x.cache.table_width * x.cache.page_size + kUnit - 1) / kUnit;
-    const double most = (double)tiles * a.c.n_kv_heads * a.parts * per_tile;
-    a.blocks = std::min(kMaxBlocks, num_sms * S::MIN_BLOCKS);
-    if (most < a.blocks) a.blocks = (int)most;
-    a.min_units = 1;
-    a.stat = reinterpret_cast<float2 *>(a.partial + 2ll * a.blocks * S::ROWS * D);
-    a.joins = reinterpret_cast<Join *>(a.stat + 2ll * a.blocks * S::ROWS);
-    static_assert(kUnit == 64, "2^6");
-    a.unit_shift = 6;
     static std::atomic<bool> done[64];
     hq_status st = allow_smem(attention_stream_kernel<WIDE, BITS, D, NT>, S::SMEM, done);
     if (st != HQ_OK) return st;
-    st = launch(attention_stream_kernel<WIDE, BITS, D, NT>, dim3((unsigned)a.blocks), kThreads, S::SMEM, stream, "attention", a);
-    if (st != HQ_OK || a.blocks < 2 || per_tile < 2) return st;             // an item of one unit is never divided
-    return launch(attention_combine_kernel<WIDE, D>, dim3((unsigned)(a.blocks - 1), S::ROWS / kCombineRows), kCombineThreads, 0, stream, "attention combine",
-                  a, S::ROWS);
+    static_assert(kUnit == 1 << 6, "unit_shift");
+    deal_rows(a, S::ROWS, D, 6, num_sms * S::MIN_BLOCKS);
+    st = launch_blocks(attention_stream_kernel<WIDE, BITS, D, NT>, dim3((unsigned)a.blocks), kThreads, S::SMEM, stream, "attention", a);
+    return st != HQ_OK ? st : run_combine<WIDE, D>(a, S::ROWS, stream);
 }
 
 template <bool WIDE, int BITS>
 hq_status run_dim(const AttentionArgs &x, const AttnArgs &a, int num_sms, cudaStream_t stream) {
-    const int nt = stream_tiles(x);
-    if (x.cache.head_dim == 256) return run_stream<WIDE, BITS, 256, 1>(x, a, num_sms, stream);
+    const bool few = stream_rows(x) == 8;
+    if (x.cache.head_dim == 256) return run_stream<WIDE, BITS, 256, 1>(a, num_sms, stream);
     if (x.cache.head_dim == 128)
-        return nt == 1 ? run_stream<WIDE, BITS, 128, 1>(x, a, num_sms, stream) : run_stream<WIDE, BITS, 128, 2>(x, a, num_sms, stream);
-    return nt == 1 ? run_stream<WIDE, BITS, 64, 1>(x, a, num_sms, stream) : run_stream<WIDE, BITS, 64, 2>(x, a, num_sms, stream);
+        return few ? run_stream<WIDE, BITS, 128, 1>(a, num_sms, stream) : run_stream<WIDE, BITS, 128, 2>(a, num_sms, stream);
+    return few ? run_stream<WIDE, BITS, 64, 1>(a, num_sms, stream) : run_stream<WIDE, BITS, 64, 2>(a, num_sms, stream);
 }
 
 template <bool WIDE>
@@ -801,8 +760,13 @@ hq_status run_attention_f32(const AttentionArgs &x, const AttnArgs &a, int num_s
 
 hq_status run_attention_f32(const AttentionArgs &x, const AttnArgs &a, int num_sms, cudaStream_t stream);
 
+hq_status run_attention_combine(const AttnArgs &a, int rows, int dim, cudaStream_t stream) {
+    return dim == 64 ? run_combine<false, 64>(a, rows, stream) : dim == 128 ? run_combine<false, 128>(a, rows, stream)
+                                                                             : run_combine<false, 256>(a, rows, stream);
+}
+
 int64_t attention_workspace(const AttentionArgs &x) {
-    const int64_t rows = 8 * stream_tiles(x);
+    const int64_t rows = on_tiles(x) ? 128 : stream_rows(x);
     return 2ll * kMaxBlocks * rows * (x.cache.head_dim + 2) * 4 + kMaxBlocks * (int64_t)sizeof(Join);
 }
 
@@ -823,6 +787,7 @@ hq_status launch_attention(const AttentionArgs &x, cudaStream_t stream) {
     a.window = x.window;
     a.partial = static_cast<float *>(x.workspace);
     a.dtype = x.cache.dtype;
+    if (on_tiles(x)) return run_attention_tile(a, x.cache.fmt, x.cache.head_dim, dev->num_sms, stream);
     return a.dtype == HQ_DT_F32 ? run_attention_f32(x, a, dev->num_sms, stream) : run_fmt<false>(x, a, dev->num_sms, stream);
 }
 

@@ -8,6 +8,8 @@
 // and weighted sum), and the combine kernel joins them.
 #pragma once
 
+#include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "hq_cache.cuh"
@@ -29,6 +31,7 @@ struct AttnArgs {
     float2 *stat;                       // [2 blocks][rows]: maximum and sum of a partial result
     struct Join *joins;                 // [blocks]
     int unit_shift, blocks, min_units;
+    long long most_units;               // an item can have
 };
 
 // sum of floor((a i + b) / m) for i < n; a, b >= 0 (the Euclidean recursion)
@@ -275,5 +278,60 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------------ host side
+
+constexpr int kMaxBlocks = 608;                             // of an attention kernel: the workspace holds two partial results of each
+
+// Allows a kernel its shared memory, once a device.
+template <class K>
+hq_status allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
+    int d = 0;
+    cudaGetDevice(&d);
+    if (d >= 0 && d < 64 && done[d].load(std::memory_order_acquire)) return HQ_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return set_error(HQ_ERR_LAUNCH, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    if (d >= 0 && d < 64) done[d].store(true, std::memory_order_release);
+    return HQ_OK;
+}
+
+template <class K, class... A>
+hq_status launch_blocks(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, const char *what, const A &... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e != cudaSuccess) return set_error(HQ_ERR_LAUNCH, "%s launch: %s", what, cudaGetErrorString(e));
+    note_launch();
+    return HQ_OK;
+}
+
+// Tiles of `rows` query rows, units of 2^unit_shift positions, no more blocks than there can be units, and the workspace.
+inline void deal_rows(AttnArgs &a, int rows, int dim, int unit_shift, int blocks) {
+    a.tokens = a.group <= rows ? rows / a.group : 1;
+    a.part_heads = a.group <= rows ? a.group : rows;
+    a.parts = (a.group + a.part_heads - 1) / a.part_heads;
+    a.unit_shift = unit_shift;
+    const long long tiles = std::min(a.c.n_tokens, a.c.n_tokens / a.tokens + a.c.n_req);
+    a.most_units = ((a.c.table_width << a.c.page_shift) + (1 << unit_shift) - 1) >> unit_shift;
+    const double most = (double)tiles * a.c.n_kv_heads * a.parts * a.most_units;
+    a.blocks = std::min(kMaxBlocks, blocks);
+    if (most < a.blocks) a.blocks = (int)most;
+    a.min_units = 1;
+    a.stat = reinterpret_cast<float2 *>(a.partial + 2ll * a.blocks * rows * dim);
+    a.joins = reinterpret_cast<Join *>(a.stat + 2ll * a.blocks * rows);
+}
+
+// Joins partial results, where there can be any: 16-bit tokens, tiles of `rows`.
+hq_status run_attention_combine(const AttnArgs &a, int rows, int dim, cudaStream_t stream);
+// The kernel for many rows, 16-bit tokens.
+hq_status run_attention_tile(const AttnArgs &a, int fmt, int dim, int num_sms, cudaStream_t stream);
 
 }  // namespace hq

@@ -1,0 +1,656 @@
+// hq_attention_tile.cu -- attention over the quantized key/value cache for many
+// query rows a key/value head (prompts, wide groups of verified drafts), 16-bit
+// tokens, on the tensor cores.
+//
+// A tile is 128 query rows (tokens with their group's heads), a unit 128 positions.  Per unit, with the shared memory of a block
+// holding one tile of Q, K and V^T as 16-bit floats:
+//   4 decode warps   the stored bytes, from global memory to registers, become K [128 positions][D] and V^T [D][128 positions]
+//   1 thread         S = Q K^T and O += P V, tcgen05.mma with accumulators in tensor memory (P is an operand there)
+//   4 softmax warps  a thread a row: maxima, weights into tensor memory, rescaling of O where the maximum has risen
+//   1 walker warp    finds the parts and the addresses of their cells, and asks for them ahead into L2
+// Two blocks a multiprocessor (D 256: one) fill each other's gaps.
+//
+// Ranges.  Q rows are scaled as in the kernel for few rows.  K and V^T of 32 neighbouring positions are scaled by
+// the power of two that takes their largest scale to the top of what 16 bits hold (2^-6 or 2^-2 for the largest element), so an element
+// is rounded to 11 bits or 2^-19 of the largest near it.  Scores of those 32 columns get K's power back in fp32; V's joins
+// the exponent of the weights, whose reference is thus the largest weight times value, and the sum of the weights leaves it out.
+#include <algorithm>
+#include <atomic>
+
+#include "hq_attention.cuh"
+#include "hq_tc.cuh"
+
+namespace hq {
+namespace {
+
+constexpr int kRows = 128, kUnit = 128, kCells = kUnit / kCell;
+constexpr int kSoftmax = 4, kDecode = 4;                    // warps
+constexpr int kWalker = kSoftmax + kDecode, kProducts = kWalker + 1;
+constexpr int kThreads = 32 * (kProducts + 1);
+constexpr int kSlots = 4;                                   // units whose addresses are known ahead
+constexpr float kSlack = 8.f, kWeight = 6.f;                // weights up to 2^(slack + weight); 2^weight at the reference
+
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+__device__ __forceinline__ __half2 power_h2(int e) {        // 2^e, -14 <= e <= 15
+    return __half2half2(__ushort_as_half((uint16_t)((15 + e) << 10)));
+}
+
+// D[128][N] (+)= A[128][16] B[N][16]^T, both in shared memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+}
+
+// This warp's 32 lanes x 32 columns, waited for.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+          "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+          "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+template <int WORDS>
+__device__ __forceinline__ void load_global(const uint8_t *p, uint32_t *v) {
+    if constexpr (WORDS == 1) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v[0]) : "l"(p));
+    else if constexpr (WORDS == 2) asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p));
+    else {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 4)
+            asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]) : "l"(p + 4 * i));
+    }
+}
+
+template <int BITS, int D>
+struct Tile {
+    using L = CellLayout<BITS, D>;
+    static constexpr int NB = L::NB;
+    static constexpr int MIN_BLOCKS = D == 256 ? 1 : 2;
+    static constexpr uint32_t TMEM = D == 256 ? 512 : 256;  // columns: scores (and in their place weights) 0..127, outputs from 128
+    static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = kUnit * D * 2, V_BYTES = kUnit * D * 2;
+    struct Shared {
+        WalkShared walk;
+        Part part[2];
+        uint64_t part_full[2], part_empty[2], cell_full[kSlots], cell_empty[kSlots];
+        uint64_t q_full, k_full, v_full, s_full, p_full, pv_done;
+        uint64_t cell[kSlots][kCells];                      // addresses; 0: no position that is seen, 1: page out of range
+        float factor[kRows];
+        int k_exp[2][kDecode], v_exp[2][kDecode];           // of 32 positions: the stored value is the tile's times 2^exp
+        uint32_t any_bad[2][kDecode];                       // some value block of the 32 positions is no number
+        uint8_t bad[2][kUnit];                              // then: of each position, bit b: block b
+        uint32_t tmem;
+        int abort;
+    };
+    static constexpr int FIXED = ((int)sizeof(Shared) + 1023) / 1024 * 1024;
+    static constexpr int SMEM = FIXED + Q_BYTES + K_BYTES + V_BYTES;
+    static_assert(SMEM <= (228 / MIN_BLOCKS - 1) * 1024, "shared memory");
+};
+
+// Raw 16-bit floats of unsigned quants: pairs 0 and 2 times 2^-24, pairs 1 and 3 times 2^-20 (4 bits) or 2^-24 (8 bits).
+template <int BITS, uint32_t SEL0, uint32_t SEL1>
+__device__ __forceinline__ void raw_pairs(const uint32_t *w, uint32_t (&h)[4]) {
+    if constexpr (BITS == 4) {
+        const uint32_t v = w[0] >> 8;
+        h[0] = w[0] & 0x000f000fu;
+        h[1] = w[0] & 0x00f000f0u;
+        h[2] = v & 0x000f000fu;
+        h[3] = v & 0x00f000f0u;
+    } else {
+        h[0] = prmt(w[0], 0, SEL0);
+        h[1] = prmt(w[0], 0, SEL1);
+        h[2] = prmt(w[1], 0, SEL0);
+        h[3] = prmt(w[1], 0, SEL1);
+    }
+}
+
+// raw quants times scale d (normalised): 4 bits: d 2^-20 (n - 8), 8 bits: d 2^-24 (u - 128); one rounding each.
+template <int BITS>
+__device__ __forceinline__ void scaled_pairs(uint32_t (&h)[4], __half2 d) {
+    const __half2 off = __hmul2(d, __half2half2(__ushort_as_half(0x8080)));         // -2^-17
+    const __half2 big = BITS == 4 ? __hmul2(d, power_h2(4)) : d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = h2_bits(__hfma2(bits_h2(h[i]), BITS == 4 && (i & 1) == 0 ? big : d, off));
+}
+
+// ------------------------------------------------------------------ the walker
+
+template <int BITS, int D>
+__device__ __forceinline__ void walk(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, long long total, long long x0, long long end) {
+    using L = CellLayout<BITS, D>;
+    constexpr int AHEAD = 32 / kCells;
+    const int lane = threadIdx.x & 31;
+    volatile int *abort = &s.abort;
+    int slot = 0;
+    uint32_t phase = 1;
+    Join join;
+    join.valid = 0;
+    for (long long x = x0, n = 0;; ++n) {
+        const int at = (int)n & 1;
+        if (!tc_wait(smem_u32(&s.part_empty[at]), (uint32_t)(n >> 1 & 1) ^ 1, abort, a.c.fault)) return;
+        if (x >= end) {
+            if (lane == 0) {
+                s.part[at].take = 0;
+                mbar_arrive(smem_u32(&s.part_full[at]));
+                a.joins[blockIdx.x] = join;
+            }
+            return;
+        }
+        if (x >= s.walk.walk.next) walk_to<32>(a, x, s.walk.walk.r + 1, s.walk.walk.next, s.walk);
+        const Part p = part_at(a, s.walk.walk, x, x0, end);
+        if (lane == 0) {
+            s.part[at] = p;
+            mbar_arrive(smem_u32(&s.part_full[at]));
+        }
+        if (p.item.unit + p.take < p.item.units && p.item.first >= x0)
+            join = {p.q, p.item, 1, p.slot, block_of(a, total, p.item.first + p.item.units - 1)};
+        uint64_t cell = 0;
+        for (int u = 0; u < p.take; ++u) {
+            if (u % AHEAD == 0) {                           // lane i: cell i of the next units
+                const int pos = p.begin + u * kUnit + lane * kCell;
+                cell = 0;
+                if (lane / kCells + u < p.take && pos < p.span.hi && pos + kCell > p.span.lo) {
+                    uint8_t *cells = page_cells(a.c, s.walk.walk.r, pos, p.item.kv_head);
+                    cell = cells ? reinterpret_cast<uint64_t>(cell_of<L>(a.c, cells, pos)) : 1;
+                    if (cells) prefetch_l2(reinterpret_cast<const void *>(cell), L::BYTES);
+                }
+            }
+            if (!tc_wait(smem_u32(&s.cell_empty[slot]), phase, abort, a.c.fault)) return;
+            if (lane / kCells == u % AHEAD) s.cell[slot][lane % kCells] = cell;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.cell_full[slot]));
+            if (++slot == kSlots) { slot = 0; phase ^= 1; }
+        }
+        x += p.take;
+    }
+}
+
+// ------------------------------------------------------------------ decoding
+
+// A decode warp has 32 positions of a unit: two cells.
+template <int BITS, int D>
+__device__ __forceinline__ void decode(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t k_tile, uint32_t v_tile) {
+    using T = Tile<BITS, D>;
+    using L = typename T::L;
+    constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS;        // words of a block, blocks of a unit
+    constexpr int SCALES = NB / 2;                          // words of a lane's share of 32 positions' scales: 16 NB of keys, as many of values
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftmax;
+    volatile int *abort = &s.abort;
+    // keys: four neighbouring lanes have a row; rows x and x ^ 5 side by side, so that neither loads nor stores meet in a bank
+    const int c = lane & 3, kr = (lane >> 3) ^ (lane & 4 ? 5 : 0);
+    const int q = lane >> 3, g = lane & 7;                  // values: eight positions from 8 q, elements g of the blocks
+    int slot = 0;
+    uint32_t slot_phase = 0, n = 0;                         // units so far
+    uint64_t cell[2];
+    uint32_t raw[L::UNITS][4][L::UW], ks[4][NB / 2], tk[SCALES], tv[SCALES];
+
+    auto load_keys = [&]() -> bool {                        // of the next unit
+        if (!tc_wait(smem_u32(&s.cell_full[slot]), slot_phase, abort, a.c.fault)) return false;
+        cell[0] = s.cell[slot][2 * w];
+        cell[1] = s.cell[slot][2 * w + 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.cell_empty[slot]));
+        if (++slot == kSlots) { slot = 0; slot_phase ^= 1; }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                       // rows 8 i + kr
+            const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[i >> 1]);
+            const int pos = 8 * (i & 1) + kr;
+            if (cell[i >> 1] > 1) {
+#pragma unroll
+                for (int u = 0; u < L::UNITS; ++u) load_global<L::UW>(p + L::k_word(pos, c, u * L::UW), raw[u][i]);
+                load_global<NB / 2>(p + L::k_scale(pos, 0), ks[i]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < L::UNITS; ++u)
+#pragma unroll
+                    for (int k = 0; k < L::UW; ++k) raw[u][i][k] = 0;
+#pragma unroll
+                for (int k = 0; k < NB / 2; ++k) ks[i][k] = cell[i >> 1] ? 0x7fff7fffu : 0u;        // a page out of range: NaN
+            }
+        }
+        // scales for the powers of two: 16 lanes a cell
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[lane >> 4]);
+#pragma unroll
+        for (int k = 0; k < SCALES; ++k) {
+            tk[k] = tv[k] = 0;
+            if (cell[lane >> 4] > 1) {
+                load_global<1>(p + L::KS + 4 * ((lane & 15) * SCALES + k), &tk[k]);
+                load_global<1>(p + L::VS + 4 * ((lane & 15) * SCALES + k), &tv[k]);
+            }
+        }
+        return true;
+    };
+    auto load_values = [&]() {
+        const uint64_t from = cell[q >> 1];
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(from);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                       // pairs 4 (q % 2) + i
+#pragma unroll
+            for (int u = 0; u < L::UNITS; ++u) {
+                if (from > 1) load_global<L::UW>(p + L::v_word(4 * (q & 1) + i, g, u * L::UW), raw[u][i]);
+                else
+#pragma unroll
+                    for (int k = 0; k < L::UW; ++k) raw[u][i][k] = 0;
+            }
+        }
+    };
+
+    for (int part_n = 0;; ++part_n) {
+        const int at = part_n & 1;
+        if (!tc_wait(smem_u32(&s.part_full[at]), (uint32_t)(part_n >> 1 & 1), abort, a.c.fault)) return;
+        const int take = s.part[at].take;
+        if (take == 0) return;
+        if (!load_keys()) return;
+        for (int u = 0; u < take; ++u, ++n) {
+            const int p0 = s.part[at].begin + u * kUnit + 32 * w;           // of this warp's positions
+            const int lo = s.part[at].span.lo, hi = s.part[at].span.hi;
+            const bool edge = p0 < lo || p0 + 32 > hi;
+            const int par = n & 1;
+            // ---- powers of two, of what is a number and seen by some row
+            uint32_t top_k = 0, top_v = 0;
+            bool odd = false;
+#pragma unroll
+            for (int k = 0; k < SCALES; ++k) {
+                const int i = (lane & 15) * SCALES + k;     // word of the cell's: keys: [16][NB / 2], values: [8][NB] of two positions
+                const int pk = p0 + kCell * (lane >> 4) + i / (NB / 2), pv = p0 + kCell * (lane >> 4) + 2 * (i / NB);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = tk[k] >> (16 * h) & 0x7fffu, y = tv[k] >> (16 * h) & 0x7fffu;
+                    if (x < 0x7c00u && pk >= lo && pk < hi) top_k = max(top_k, x);
+                    if (pv + h >= lo && pv + h < hi) {
+                        if (y < 0x7c00u) top_v = max(top_v, y); else odd = true;
+                    }
+                }
+            }
+            const int ek = (int)(__reduce_max_sync(0xffffffffu, top_k) >> 10), ev = (int)(__reduce_max_sync(0xffffffffu, top_v) >> 10);
+            odd = __any_sync(0xffffffffu, odd);
+            if (lane == 0) {
+                s.k_exp[par][w] = ek - 5;
+                s.v_exp[par][w] = ev - 5;
+            }
+            constexpr int TO = BITS == 4 ? 25 : 29;         // scales go to [2^10, 2^11) or [2^14, 2^15)
+            // ---- keys
+            if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;      // the tile is free
+            {
+                const int x = TO - ek, x1 = min(x, 15);
+                const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 32 * w + 8 * i + kr;
+#pragma unroll
+                    for (int b = 0; b < NB; b += 2) {
+                        const __half2 d = __hmul2(__hmul2(bits_h2(ks[i][b / 2]), up1), up2);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t h[4];
+                            raw_pairs<BITS, 0x4140, 0x4342>(&raw[(b + e) / BLOCKS][i][(b + e) % BLOCKS * WB], h);
+                            scaled_pairs<BITS>(h, e ? __high2half2(d) : __low2half2(d));
+                            const int chunk = 4 * ((b + e) & 1) + c;
+                            const uint32_t to = k_tile + (b >> 1) * (kUnit * 128) + row * 128 + ((chunk ^ (row & 7)) << 4);
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+                        }
+                    }
+                }
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&s.k_full));
+                mbar_arrive(smem_u32(&s.s_full));
+            }
+            // ---- values
+            load_values();
+            uint32_t vs[4][NB];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t from = cell[q >> 1];
+                const int pos = 8 * (q & 1) + 2 * i, p = p0 + 8 * q + 2 * i;
+                if (from > 1) load_global<NB>(reinterpret_cast<const uint8_t *>(from) + L::v_scale(pos, 0), vs[i]);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    if (from <= 1) vs[i][b] = 0;
+                    if (edge) vs[i][b] &= (p >= lo && p < hi ? 0xffffu : 0u) | (p + 1 >= lo && p + 1 < hi ? 0xffff0000u : 0u);
+                }
+            }
+            if (n > 0 && !tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault)) return;
+            if (lane == 0) s.any_bad[par][w] = odd;         // (the softmax warps are done with those of two units before)
+            if (odd) {                                      // blocks that are no numbers leave the product, and are marked
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t bits[2] = {0, 0};
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        if ((vs[i][b] & 0x7c00u) == 0x7c00u) { bits[0] |= 1u << b; vs[i][b] &= 0xffff0000u; }
+                        if ((vs[i][b] & 0x7c000000u) == 0x7c000000u) { bits[1] |= 1u << b; vs[i][b] &= 0x0000ffffu; }
+                    }
+                    if (g == 0) {
+                        s.bad[par][32 * w + 8 * q + 2 * i] = (uint8_t)bits[0];
+                        s.bad[par][32 * w + 8 * q + 2 * i + 1] = (uint8_t)bits[1];
+                    }
+                }
+            }
+            {
+                const int x = TO - ev, x1 = min(x, 15);
+                const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    uint32_t h[4][4];                       // [pair][j]
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        raw_pairs<BITS, 0x4240, 0x4341>(&raw[b / BLOCKS][i][b % BLOCKS * WB], h[i]);
+                        scaled_pairs<BITS>(h[i], __hmul2(__hmul2(bits_h2(vs[i][b]), up1), up2));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = 32 * b + 8 * j + g, chunk = 4 * (w & 1) + q;
+                        const uint32_t to = v_tile + (w >> 1) * (D * 128) + row * 128 + ((chunk ^ g) << 4);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0][j]), "r"(h[1][j]), "r"(h[2][j]), "r"(h[3][j]) : "memory");
+                    }
+                }
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.v_full));
+            if (u + 1 < take && !load_keys()) return;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.part_empty[at]));
+    }
+}
+
+// ------------------------------------------------------------------ products
+
+template <int BITS, int D>
+__device__ __forceinline__ void products(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t q_tile, uint32_t k_tile,
+                                         uint32_t v_tile, uint32_t tmem) {
+    volatile int *abort = &s.abort;
+    const uint32_t qk = tc_idesc(kUnit, false), pv = tc_idesc(D, false);
+    const uint32_t scores = tmem, outputs = tmem + 128;
+    uint32_t n = 0;
+    bool fine = true;
+    for (uint32_t part_n = 0; fine; ++part_n) {
+        const int at = part_n & 1;
+        if (!tc_wait(smem_u32(&s.part_full[at]), part_n >> 1 & 1, abort, a.c.fault)) break;
+        const int take = s.part[at].take;
+        if (take == 0) break;
+        if (!tc_wait(smem_u32(&s.q_full), part_n & 1, abort, a.c.fault)) break;
+        for (int u = 0; u < take; ++u, ++n) {
+            if (!tc_wait(smem_u32(&s.k_full), n & 1, abort, a.c.fault) ||
+                (n > 0 && !tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault))) { fine = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                tc_mma_ss(scores, tc_desc_sw128(q_tile + k / 4 * (kRows * 128) + k % 4 * 32),
+                          tc_desc_sw128(k_tile + k / 4 * (kUnit * 128) + k % 4 * 32), qk, k > 0);
+            tc_commit(smem_u32(&s.s_full));
+            if (!tc_wait(smem_u32(&s.v_full), n & 1, abort, a.c.fault) ||
+                !tc_wait(smem_u32(&s.p_full), n & 1, abort, a.c.fault)) { fine = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kUnit / 16; ++k)
+                tc_mma(outputs, scores + 8 * k, tc_desc_sw128(v_tile + k / 4 * (D * 128) + k % 4 * 32), pv, u > 0 || k > 0);
+            tc_commit(smem_u32(&s.pv_done));
+        }
+        if (fine) mbar_arrive(smem_u32(&s.part_empty[at]));
+    }
+    if (!fine || *abort) {
+        // after a time-out: what was issued ends before the tensor memory is given back
+        tc_commit(smem_u32(&s.pv_done));
+        for (int k = 0; k < 1000 && !mbar_try_wait_sleep(smem_u32(&s.pv_done), n & 1, 20000u); ++k) {}
+    }
+}
+
+// ------------------------------------------------------------------ softmax
+
+template <int BITS, int D>
+__device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint8_t *q_tile, uint32_t tmem) {
+    constexpr int LANES = D / 8, ROWS = 32 / LANES;         // lanes of a query row's loads, rows at once
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = threadIdx.x;
+    volatile int *abort = &s.abort;
+    const uint32_t scores = tmem + ((uint32_t)(32 * warp) << 16), outputs = scores + 128;
+    uint32_t n = 0;
+    for (uint32_t part_n = 0;; ++part_n) {
+        const int at = part_n & 1;
+        if (!tc_wait(smem_u32(&s.part_full[at]), part_n >> 1 & 1, abort, a.c.fault)) return;
+        const Part &part = s.part[at];
+        const int take = part.take;
+        if (take == 0) return;
+        // ---- the tile of Q: times a power of two a row, and the scale's sign
+        {
+            const float sign = a.scale < 0.f ? -1.f : 1.f;
+            const int col = lane % LANES;
+#pragma unroll 4
+            for (int i = 0; i < 32; i += ROWS) {
+                const int row = 32 * warp + i + lane / LANES;
+                int token, head;
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (row_of(a, part.q, part.item, row, token, head))
+                    load_row8<false>(a, ((long long)part.q.first + token) * a.q_stride + (long long)head * D + 8 * col, v);
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+#pragma unroll
+                for (int d = 1; d < LANES; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const int e = min(253, 268 - (int)(top >> 23));
+                const float up = __uint_as_float((uint32_t)e << 23) * sign;
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = h2_bits(__floats2half2_rn(v[2 * k] * up, v[2 * k + 1] * up));
+                *reinterpret_cast<uint4 *>(q_tile + (col / 8) * (kRows * 128) + row * 128 + ((col % 8 ^ (row & 7)) << 4)) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+                if (col == 0)
+                    s.factor[row] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
+                                                       : fabsf(a.scale) * kLog2e * __uint_as_float((uint32_t)(254 - e) << 23);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
+        }
+        const float factor = s.factor[me];
+        int token, head;
+        const bool live = row_of(a, part.q, part.item, me, token, head);
+        const bool work = __any_sync(0xffffffffu, live);    // some row of the warp
+        const Range see = seen_by(a, part.q, min(token, part.q.n - 1));
+        float ref = -INFINITY, l = 0.f;                     // the reference of the weights, their sum
+        uint32_t bad = 0;
+        int p0 = part.begin;
+        // value blocks of a unit that are no numbers and that the row sees
+        auto look_at_bad = [&](uint32_t unit, int first) {
+            const uint32_t *f = s.any_bad[unit & 1];
+            if ((f[0] | f[1] | f[2] | f[3]) == 0) return;
+            for (int k = 0; k < kUnit; ++k)
+                if (f[k >> 5] && first + k >= see.lo && first + k < see.hi && first + k >= part.span.lo && first + k < part.span.hi)
+                    bad |= s.bad[unit & 1][k];
+        };
+        for (int u = 0; u < take; ++u, ++n, p0 += kUnit) {
+            if (!tc_wait(smem_u32(&s.s_full), n & 1, abort, a.c.fault)) return;
+            tc_fence_after();
+            if (work) {
+                if (u > 0) look_at_bad(n - 1, p0 - kUnit);
+                const int first = see.lo - p0, last = see.hi - p0;          // columns that the row sees: [first, last)
+                const bool edge = __any_sync(0xffffffffu, first > 0 || last < kUnit);
+                float fk[4], ev[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    fk[c] = factor * __uint_as_float((uint32_t)(127 + s.k_exp[n & 1][c]) << 23);
+                    ev[c] = (float)s.v_exp[n & 1][c];
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32], m = -INFINITY;
+                    tmem_load32(scores + 32 * c, v);
+                    if (edge) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) if (32 * c + k < first || 32 * c + k >= last) v[k] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) m = fmaxf(m, v[k]);
+                    if (m > -INFINITY) top = fmaxf(top, fmaf(m, fk[c], ev[c]));
+                }
+                const bool raise = top > ref + kSlack;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float now = raise ? top : ref, f = raise ? ex2(ref - now) : 1.f;         // 0 from -inf
+                    l *= f;
+                    ref = now;
+                    if (u > 0) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            float v[32];
+                            tmem_load32(outputs + 32 * c, v);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] *= f;
+#pragma unroll
+                            for (int k = 0; k < 32; k += 16) {
+                                uint32_t x[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(v[k + i]);
+                                tmem_st16(outputs + 32 * c + k, x);
+                            }
+                        }
+                    }
+                }
+                const float base = kWeight - fmaxf(ref, -3e38f);            // nothing seen yet: all columns are hidden
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32], sum = 0.f;
+                    tmem_load32(scores + 32 * c, v);
+                    const float b = base + ev[c];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        v[k] = fmaf(v[k], fk[c], b);
+                        if (edge && (32 * c + k < first || 32 * c + k >= last)) v[k] = -INFINITY;
+                        v[k] = ex2(v[k]);
+                    }
+                    uint32_t x[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        sum += v[2 * k] + v[2 * k + 1];
+                        x[k] = h2_bits(__floats2half2_rn(v[2 * k], v[2 * k + 1]));
+                    }
+                    l = fmaf(sum, __uint_as_float((uint32_t)(127 - s.v_exp[n & 1][c]) << 23), l);
+                    tmem_st16(scores + 16 * c, x);
+                }
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.p_full));
+        }
+        // ---- the tile's outputs
+        if (!tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault)) return;
+        tc_fence_after();
+        if (work) {
+            look_at_bad(n - 1, p0 - kUnit);
+            const float f = part.slot >= 0 ? 1.f : l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+            const long long r = (long long)part.slot * kRows + me;
+            const long long to = ((long long)part.q.first + token) * a.out_stride + (long long)head * D;
+            if (live && part.slot >= 0) a.stat[r] = make_float2(ref - kWeight, l);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                float v[32];
+                tmem_load32(outputs + 32 * c, v);
+                const bool gone = bad >> c & 1u;
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = gone ? __uint_as_float(0x7fffffffu) : v[k + i] * f;
+                    if (!live) continue;
+                    if (part.slot >= 0) store8(a.partial + r * D + 32 * c + k, y);
+                    else store_row8<false>(a, to + 32 * c + k, y);
+                }
+            }
+            tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.part_empty[at]));
+    }
+}
+
+template <int BITS, int D>
+__global__ void __launch_bounds__(kThreads, (Tile<BITS, D>::MIN_BLOCKS)) attention_tile_kernel(const __grid_constant__ AttnArgs a) {
+    using T = Tile<BITS, D>;
+    extern __shared__ __align__(1024) uint8_t memory[];
+    typename T::Shared &s = *reinterpret_cast<typename T::Shared *>(memory);
+    uint8_t *q_tile = memory + T::FIXED;
+    const uint32_t q = smem_u32(q_tile), k = q + T::Q_BYTES, v = k + T::K_BYTES;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&s.part_full[i]), 1);
+            mbar_init(smem_u32(&s.part_empty[i]), kSoftmax + kDecode + 1);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(smem_u32(&s.cell_full[i]), 1);
+            mbar_init(smem_u32(&s.cell_empty[i]), kDecode);
+        }
+        mbar_init(smem_u32(&s.q_full), kSoftmax);
+        mbar_init(smem_u32(&s.k_full), kDecode);
+        mbar_init(smem_u32(&s.v_full), kDecode);
+        mbar_init(smem_u32(&s.s_full), 1 + kDecode);         // the products, and the exponents of K and V
+        mbar_init(smem_u32(&s.p_full), kSoftmax);
+        mbar_init(smem_u32(&s.pv_done), 1);
+        fence_mbar_init();
+        s.abort = 0;
+    }
+    // Tensor memory is taken after what precedes is done and before what follows may start: neither can hold it while it
+    // waits for this kernel, or the other way round.
+    griddep_wait();
+    if (warp == 0) tmem_alloc(smem_u32(&s.tmem), T::TMEM);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();
+    const uint32_t tmem = s.tmem;
+    long long total, x0, end;
+    deal<kThreads>(a, total, x0, end, s.walk);
+    if (x0 >= end) {
+        if (threadIdx.x == 0) a.joins[blockIdx.x].valid = 0;
+    } else if (warp < kSoftmax) {
+        softmax<BITS, D>(a, s, q_tile, tmem);
+    } else if (warp < kWalker) {
+        decode<BITS, D>(a, s, k, v);
+    } else if (warp == kWalker) {
+        walk<BITS, D>(a, s, total, x0, end);
+    } else if (elect_one()) {
+        products<BITS, D>(a, s, q, k, v, tmem);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, T::TMEM);
+}
+
+template <int BITS, int D>
+hq_status run(AttnArgs a, int num_sms, cudaStream_t stream) {
+    using T = Tile<BITS, D>;
+    static std::atomic<bool> done[64];
+    hq_status st = allow_smem(attention_tile_kernel<BITS, D>, T::SMEM, done);
+    if (st != HQ_OK) return st;
+    deal_rows(a, kRows, D, 7, num_sms * T::MIN_BLOCKS);
+    st = launch_blocks(attention_tile_kernel<BITS, D>, dim3((unsigned)a.blocks), kThreads, T::SMEM, stream, "attention", a);
+    return st != HQ_OK ? st : run_attention_combine(a, kRows, D, stream);
+}
+
+}  // namespace
+
+hq_status run_attention_tile(const AttnArgs &a, int fmt, int dim, int num_sms, cudaStream_t stream) {
+    if (fmt == HQ_FMT_Q8_0)
+        return dim == 64 ? run<8, 64>(a, num_sms, stream) : dim == 128 ? run<8, 128>(a, num_sms, stream) : run<8, 256>(a, num_sms, stream);
+    return dim == 64 ? run<4, 64>(a, num_sms, stream) : dim == 128 ? run<4, 128>(a, num_sms, stream) : run<4, 256>(a, num_sms, stream);
+}
+
+}  // namespace hq
