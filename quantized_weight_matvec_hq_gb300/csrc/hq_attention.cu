@@ -204,8 +204,6 @@ __device__ __forceinline__ void stream_produce(const AttnArgs &a, typename Strea
     const uint64_t policy = l2_evict_first_policy();
     int n = 0, stage = 0;                                   // parts and units so far
     uint32_t phase = 1;
-    Join join;
-    join.valid = 0;
     for (long long x = x0;; ++n) {
         const int at = n & 1;
         if (!mbar_wait(smem_u32(&s.part_empty[at]), (n >> 1 & 1) ^ 1, abort, a.c.fault)) break;
@@ -213,18 +211,13 @@ __device__ __forceinline__ void stream_produce(const AttnArgs &a, typename Strea
             if (lane == 0) {
                 s.part[at].take = 0;
                 mbar_arrive(smem_u32(&s.part_full[at]));
-                a.joins[blockIdx.x] = join;
             }
             return;
         }
         if (x >= s.walk.walk.next) walk_to<32>(a, x, s.walk.walk.r + 1, s.walk.walk.next, s.walk);
-        const Part p = part_at(a, s.walk.walk, x, x0, end);
-        if (lane == 0) {
-            s.part[at] = p;
-            mbar_arrive(smem_u32(&s.part_full[at]));
-        }
-        if (p.item.unit + p.take < p.item.units && p.item.first >= x0)
-            join = {p.q, p.item, 1, p.slot, block_of(a, total, p.item.first + p.item.units - 1)};
+        tell_part(a, s.walk.walk, x, x0, end, total, s.part[at]);
+        const Part &p = s.part[at];
+        if (lane == 0) mbar_arrive(smem_u32(&s.part_full[at]));
         uint64_t cell = 0;
         for (int u = 0; u < p.take; ++u) {
             if (u % AHEAD == 0) {                           // lane i: cell i of the next units; 0: none, 1: its page is out of range
@@ -632,10 +625,7 @@ __global__ void __launch_bounds__(kThreads, (Stream<WIDE, BITS, D, NT>::MIN_BLOC
     griddep_wait();
     long long total, x0, end;
     deal<kThreads>(a, total, x0, end, s.walk);              // (with barriers, which the mbarriers' set-up needs)
-    if (x0 >= end) {
-        if (threadIdx.x == 0) a.joins[blockIdx.x].valid = 0;
-        return;
-    }
+    if (x0 >= end) return;
     if (threadIdx.x >= kConsumers) {
         stream_produce<WIDE, BITS, D, NT>(a, s, smem_u32(ring), total, x0, end);
         return;

@@ -34,20 +34,22 @@ struct AttnArgs {
     long long most_units;               // an item can have
 };
 
-// sum of floor((a i + b) / m) for i < n; a, b >= 0 (the Euclidean recursion)
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
-    long long s = 0;
-    while (n > 0) {
-        s += (n - 1) * n / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
-        const long long top = a * n + b;
-        if (top < m) break;
-        n = top / m;
-        b = top % m;
-        const long long t = m;
-        m = a;
-        a = t;
+// sum of floor((a i + b) / 2^shift) for i < n; a, b >= 0, a n below 2^31 (the Euclidean recursion; behind its first step
+// everything fits 32 bits, whose divisions are a fraction of the 64-bit ones')
+__device__ __forceinline__ long long floor_sum(long long n, int shift, long long a, long long b) {
+    if (n <= 0) return 0;
+    unsigned m = 1u << shift;
+    long long s = (n - 1) * n / 2 * (a >> shift) + n * (b >> shift);
+    unsigned x = (unsigned)a & (m - 1), y = (unsigned)b & (m - 1), top = x * (unsigned)n + y;
+    while (top >= m) {
+        const unsigned k = top / m;                         // the next sum: k terms, of slope m over x
+        y = top % m;
+        s += (long long)(k - 1) * k / 2 * (m / x) + (long long)k * (y / x);
+        const unsigned slope = m % x;
+        y %= x;
+        top = slope * k + y;
+        m = x;
+        x = slope;
     }
     return s;
 }
@@ -57,7 +59,7 @@ __device__ __forceinline__ long long unit_sum(int n, long long c, int tokens, in
     if (n <= 0) return 0;
     if (n == 1) return c > 0 ? c >> shift : 0;
     const long long skip = c < 0 ? (-c + tokens - 1) / tokens : 0;
-    return floor_sum(n - skip, 1ll << shift, tokens, c + skip * tokens);
+    return floor_sum(n - skip, shift, tokens, c + skip * tokens);
 }
 
 // Positions [lo, hi) that a token sees.
@@ -101,6 +103,23 @@ struct Item {
     int tile, kv_head, part;            // of a request
     long long first;                    // its first unit
     int units, unit;                    // how many it has, and which one it is
+};
+
+// A block's part of an item: `take` units from `unit` on.  What the producer warp tells the consumers.
+struct Part {
+    Request q;
+    Item item;
+    int take, slot;                     // 0: no more; where the partial result goes, or -1: the whole item
+    int begin;                          // the position of its first unit
+    Range span;                         // positions of it that some row sees
+    int all_lo, all_hi;                 // every row sees [all_lo, all_hi) of them
+};
+// What the combine kernel is told: the item that begins in a block (with its first unit, or with the block's) and goes on
+// past its end, in which of the block's two partial results it begins, and the last block that has one.
+struct Join {
+    Request q;
+    Item item;
+    int valid, slot, last;
 };
 
 struct WalkShared {
@@ -173,6 +192,7 @@ __device__ __forceinline__ int block_of(const AttnArgs &a, long long total, long
 // This block's units [x0, end) of the batch's `total`, and the walk at the first one's request.  The whole block calls it.
 template <int THREADS>
 __device__ __forceinline__ void deal(const AttnArgs &a, long long &total, long long &x0, long long &end, WalkShared &s) {
+    if (threadIdx.x == 0) a.joins[blockIdx.x].valid = 0;
     long long mine = 0;
     Request q = {0, 0, 0, false};
     for (int r = threadIdx.x; r < a.c.n_req; r += THREADS) {
@@ -197,19 +217,24 @@ __device__ __forceinline__ void deal(const AttnArgs &a, long long &total, long l
     __syncthreads();
 }
 
+// The whole warp calls it, all lanes for the same unit: each step of the search looks at 32 tiles.
 __device__ __forceinline__ Item item_at(const AttnArgs &a, const Walk &w, long long x) {
-    const long long local = x - w.start, heads = (long long)a.c.n_kv_heads * a.parts;
-    int lo = 0, hi = tiles_of(a, w.q);                      // the last tile with units_before * heads <= local
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (units_before(a, w.q, mid) * heads <= local) lo = mid; else hi = mid;
+    const long long local = x - w.start;
+    const int heads = a.c.n_kv_heads * a.parts, lane = threadIdx.x & 31;
+    int lo = 0, n = tiles_of(a, w.q);                       // the last tile with units_before * heads <= local is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const uint32_t m = __ballot_sync(0xffffffffu, at < n && units_before(a, w.q, lo + at) * heads <= local);
+        const int k = 31 - __clz(m);                        // (lane 0 always is)
+        lo += k * step;
+        n = min(step, n - k * step);
     }
     const long long before = units_before(a, w.q, lo);
     Item it;
     it.tile = lo;
     it.units = (int)(units_before(a, w.q, lo + 1) - before);
     const long long rest = local - before * heads;
-    const int h = (int)(rest / it.units);
+    const int h = rest >> 32 ? (int)(rest / it.units) : (int)((unsigned)rest / (unsigned)it.units);
     it.kv_head = h / a.parts;
     it.part = h % a.parts;
     it.unit = (int)(rest - (long long)h * it.units);
@@ -217,37 +242,35 @@ __device__ __forceinline__ Item item_at(const AttnArgs &a, const Walk &w, long l
     return it;
 }
 
-// A block's part of an item: `take` units from `unit` on.  What the producer warp tells the consumers.
-struct Part {
-    Request q;
-    Item item;
-    int take, slot;                     // 0: no more; where the partial result goes, or -1: the whole item
-    int begin;                          // the position of its first unit
-    Range span;                         // positions of it that some row sees
-    int all_lo, all_hi;                 // every row sees [all_lo, all_hi) of them
-};
-__device__ __forceinline__ Part part_at(const AttnArgs &a, const Walk &w, long long x, long long x0, long long end) {
-    Part p;
-    p.q = w.q;
-    p.item = item_at(a, w, x);
-    p.take = (int)min((long long)(p.item.units - p.item.unit), end - x);
-    p.slot = p.take == p.item.units ? -1 : 2 * (int)blockIdx.x + (x == x0 ? 0 : 1);
-    const int t0 = p.item.tile * a.tokens, t1 = min(t0 + a.tokens, w.q.n) - 1;
-    const Range first = seen_by(a, w.q, t0), last = seen_by(a, w.q, t1);
-    p.begin = ((first.lo >> a.unit_shift) + p.item.unit) << a.unit_shift;
-    p.span = {first.lo, min(p.begin + (p.take << a.unit_shift), last.hi)};
-    p.all_lo = last.lo;
-    p.all_hi = first.hi;
-    return p;
+// The part at unit x of a block with units [x0, end), into shared memory; and the block's join, if that is it.  A whole warp.
+__device__ __forceinline__ void tell_part(const AttnArgs &a, const Walk &w, long long x, long long x0, long long end, long long total,
+                                          Part &p) {
+    const Item it = item_at(a, w, x);
+    if ((threadIdx.x & 31) == 0) {
+        const int take = (int)min((long long)(it.units - it.unit), end - x);
+        const int slot = take == it.units ? -1 : 2 * (int)blockIdx.x + (x == x0 ? 0 : 1);
+        const int t0 = it.tile * a.tokens, t1 = min(t0 + a.tokens, w.q.n) - 1;
+        const Range first = seen_by(a, w.q, t0), last = seen_by(a, w.q, t1);
+        const int begin = ((first.lo >> a.unit_shift) + it.unit) << a.unit_shift;
+        p.q = w.q;
+        p.item = it;
+        p.take = take;
+        p.slot = slot;
+        p.begin = begin;
+        p.span = {first.lo, min(begin + (take << a.unit_shift), last.hi)};
+        p.all_lo = last.lo;
+        p.all_hi = first.hi;
+        if (it.unit + take < it.units && it.first >= x0) {
+            Join &j = a.joins[blockIdx.x];
+            j.q = w.q;
+            j.item = it;
+            j.slot = slot;
+            j.last = block_of(a, total, it.first + it.units - 1);
+            j.valid = 1;
+        }
+    }
+    __syncwarp();
 }
-
-// What the combine kernel is told: the item that begins in a block (with its first unit, or with the block's) and goes on
-// past its end, in which of the block's two partial results it begins, and the last block that has one.
-struct Join {
-    Request q;
-    Item item;
-    int valid, slot, last;
-};
 
 // Row i of an item is token tile * tokens + i / part_heads of the request, and of its group head part * part_heads + i % part_heads.
 __device__ __forceinline__ bool row_of(const AttnArgs &a, const Request &q, const Item &it, int i, int &token, int &head) {

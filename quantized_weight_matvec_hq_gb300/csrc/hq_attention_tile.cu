@@ -4,7 +4,7 @@
 //
 // A tile is 128 query rows (tokens with their group's heads), a unit 128 positions.  Per unit, with the shared memory of a block
 // holding one tile of Q, K and V^T as 16-bit floats:
-//   4 decode warps   the stored bytes, from global memory to registers, become K [128 positions][D] and V^T [D][128 positions]
+//   4 + 4 warps      the stored bytes, from global memory to registers, become K [128 positions][D] and V^T [D][128 positions]
 //   1 thread         S = Q K^T and O += P V, tcgen05.mma with accumulators in tensor memory (P is an operand there)
 //   4 softmax warps  a thread a row: maxima, weights into tensor memory, rescaling of O where the maximum has risen
 //   1 walker warp    finds the parts and the addresses of their cells, and asks for them ahead into L2
@@ -24,14 +24,20 @@ namespace hq {
 namespace {
 
 constexpr int kRows = 128, kUnit = 128, kCells = kUnit / kCell;
-constexpr int kSoftmax = 4, kDecode = 4;                    // warps
-constexpr int kWalker = kSoftmax + kDecode, kProducts = kWalker + 1;
+constexpr int kSoftmax = 4, kDecode = 4;                    // warps: softmax, then of keys, of values
+constexpr int kValues = kSoftmax + kDecode, kWalker = kValues + kDecode, kProducts = kWalker + 1;
 constexpr int kThreads = 32 * (kProducts + 1);
 constexpr int kSlots = 4;                                   // units whose addresses are known ahead
 constexpr float kSlack = 8.f, kWeight = 6.f;                // weights up to 2^(slack + weight); 2^weight at the reference
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+// Bits [lo, hi) of 16.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+    const int a = min(max(lo, 0), 16), b = min(max(hi, a), 16);
+    return (1u << b) - (1u << a);
+}
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }     // 2^e
 __device__ __forceinline__ __half2 power_h2(int e) {        // 2^e, -14 <= e <= 15
     return __half2half2(__ushort_as_half((uint16_t)((15 + e) << 10)));
 }
@@ -44,17 +50,10 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, ui
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
 }
 
-// This warp's 32 lanes x 32 columns, waited for.
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
-          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
-          "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
-          "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-        : "r"(addr) : "memory");
+// 8 columns' pairs of 16-bit floats.
+__device__ __forceinline__ void tmem_st4u(uint32_t addr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0,%1,%2,%3};"
+                 ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
@@ -134,8 +133,6 @@ __device__ __forceinline__ void walk(const AttnArgs &a, typename Tile<BITS, D>::
     volatile int *abort = &s.abort;
     int slot = 0;
     uint32_t phase = 1;
-    Join join;
-    join.valid = 0;
     for (long long x = x0, n = 0;; ++n) {
         const int at = (int)n & 1;
         if (!tc_wait(smem_u32(&s.part_empty[at]), (uint32_t)(n >> 1 & 1) ^ 1, abort, a.c.fault)) return;
@@ -143,18 +140,13 @@ __device__ __forceinline__ void walk(const AttnArgs &a, typename Tile<BITS, D>::
             if (lane == 0) {
                 s.part[at].take = 0;
                 mbar_arrive(smem_u32(&s.part_full[at]));
-                a.joins[blockIdx.x] = join;
             }
             return;
         }
         if (x >= s.walk.walk.next) walk_to<32>(a, x, s.walk.walk.r + 1, s.walk.walk.next, s.walk);
-        const Part p = part_at(a, s.walk.walk, x, x0, end);
-        if (lane == 0) {
-            s.part[at] = p;
-            mbar_arrive(smem_u32(&s.part_full[at]));
-        }
-        if (p.item.unit + p.take < p.item.units && p.item.first >= x0)
-            join = {p.q, p.item, 1, p.slot, block_of(a, total, p.item.first + p.item.units - 1)};
+        tell_part(a, s.walk.walk, x, x0, end, total, s.part[at]);
+        const Part &p = s.part[at];
+        if (lane == 0) mbar_arrive(smem_u32(&s.part_full[at]));
         uint64_t cell = 0;
         for (int u = 0; u < p.take; ++u) {
             if (u % AHEAD == 0) {                           // lane i: cell i of the next units
@@ -178,128 +170,103 @@ __device__ __forceinline__ void walk(const AttnArgs &a, typename Tile<BITS, D>::
 
 // ------------------------------------------------------------------ decoding
 
-// A decode warp has 32 positions of a unit: two cells.
+// The addresses of a decode warp's cells, unit after unit.
 template <int BITS, int D>
-__device__ __forceinline__ void decode(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t k_tile, uint32_t v_tile) {
-    using T = Tile<BITS, D>;
-    using L = typename T::L;
-    constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS;        // words of a block, blocks of a unit
-    constexpr int SCALES = NB / 2;                          // words of a lane's share of 32 positions' scales: 16 NB of keys, as many of values
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftmax;
-    volatile int *abort = &s.abort;
-    // keys: four neighbouring lanes have a row; rows x and x ^ 5 side by side, so that neither loads nor stores meet in a bank
-    const int c = lane & 3, kr = (lane >> 3) ^ (lane & 4 ? 5 : 0);
-    const int q = lane >> 3, g = lane & 7;                  // values: eight positions from 8 q, elements g of the blocks
-    int slot = 0;
-    uint32_t slot_phase = 0, n = 0;                         // units so far
-    uint64_t cell[2];
-    uint32_t raw[L::UNITS][4][L::UW], ks[4][NB / 2], tk[SCALES], tv[SCALES];
-
-    auto load_keys = [&]() -> bool {                        // of the next unit
-        if (!tc_wait(smem_u32(&s.cell_full[slot]), slot_phase, abort, a.c.fault)) return false;
+struct Cells {
+    typename Tile<BITS, D>::Shared &s;
+    uint32_t at;                                            // slot, and below it the phase of its barrier
+    __device__ __forceinline__ bool next(const AttnArgs &a, int w, uint64_t (&cell)[2]) {
+        const uint32_t slot = at >> 1;
+        if (!tc_wait(smem_u32(&s.cell_full[slot]), at & 1, &s.abort, a.c.fault)) return false;
         cell[0] = s.cell[slot][2 * w];
         cell[1] = s.cell[slot][2 * w + 1];
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.cell_empty[slot]));
-        if (++slot == kSlots) { slot = 0; slot_phase ^= 1; }
+        if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&s.cell_empty[slot]));
+        at = slot == kSlots - 1 ? (at & 1) ^ 1 : at + 2;
+        return true;
+    }
+};
+
+// A key warp has 32 positions of a unit: two cells.  Four neighbouring lanes have a row; rows x and x ^ 5 lie side by
+// side, so that the stores do not meet in a bank.  The next unit's bytes are asked for while this one's products run.
+template <int BITS, int D>
+__device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t k_tile) {
+    using T = Tile<BITS, D>;
+    using L = typename T::L;
+    constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS;        // words of a block, blocks of a unit
+    constexpr int SCALES = NB / 2;                          // words of a lane's share of the scales: 16 lanes a cell
+    constexpr int TO = BITS == 4 ? 25 : 29;                 // scales go to [2^10, 2^11) or [2^14, 2^15)
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftmax;
+    const int c = lane & 3, kr = (lane >> 3) ^ (lane & 4 ? 5 : 0);
+    volatile int *abort = &s.abort;
+    Cells<BITS, D> cells = {s, 0};
+    uint32_t n = 0;                                         // units so far
+    uint64_t cell[2];
+    uint32_t raw[4][L::UW], ks[4][NB / 2], tk[SCALES];
+    auto load_unit = [&](int u) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {                       // rows 8 i + kr
             const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[i >> 1]);
-            const int pos = 8 * (i & 1) + kr;
-            if (cell[i >> 1] > 1) {
+            if (cell[i >> 1] > 1) load_global<L::UW>(p + L::k_word(8 * (i & 1) + kr, c, u * L::UW), raw[i]);
+            else
 #pragma unroll
-                for (int u = 0; u < L::UNITS; ++u) load_global<L::UW>(p + L::k_word(pos, c, u * L::UW), raw[u][i]);
-                load_global<NB / 2>(p + L::k_scale(pos, 0), ks[i]);
-            } else {
+                for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
+        }
+    };
+    auto load = [&]() {
+        load_unit(0);
 #pragma unroll
-                for (int u = 0; u < L::UNITS; ++u)
-#pragma unroll
-                    for (int k = 0; k < L::UW; ++k) raw[u][i][k] = 0;
+        for (int i = 0; i < 4; ++i) {
+            if (cell[i >> 1] > 1) load_global<NB / 2>(reinterpret_cast<const uint8_t *>(cell[i >> 1]) + L::k_scale(8 * (i & 1) + kr, 0), ks[i]);
+            else
 #pragma unroll
                 for (int k = 0; k < NB / 2; ++k) ks[i][k] = cell[i >> 1] ? 0x7fff7fffu : 0u;        // a page out of range: NaN
-            }
         }
-        // scales for the powers of two: 16 lanes a cell
         const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[lane >> 4]);
 #pragma unroll
         for (int k = 0; k < SCALES; ++k) {
-            tk[k] = tv[k] = 0;
-            if (cell[lane >> 4] > 1) {
-                load_global<1>(p + L::KS + 4 * ((lane & 15) * SCALES + k), &tk[k]);
-                load_global<1>(p + L::VS + 4 * ((lane & 15) * SCALES + k), &tv[k]);
-            }
-        }
-        return true;
-    };
-    auto load_values = [&]() {
-        const uint64_t from = cell[q >> 1];
-        const uint8_t *p = reinterpret_cast<const uint8_t *>(from);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {                       // pairs 4 (q % 2) + i
-#pragma unroll
-            for (int u = 0; u < L::UNITS; ++u) {
-                if (from > 1) load_global<L::UW>(p + L::v_word(4 * (q & 1) + i, g, u * L::UW), raw[u][i]);
-                else
-#pragma unroll
-                    for (int k = 0; k < L::UW; ++k) raw[u][i][k] = 0;
-            }
+            tk[k] = 0;
+            if (cell[lane >> 4] > 1) load_global<1>(p + L::KS + 4 * ((lane & 15) * SCALES + k), &tk[k]);
         }
     };
-
     for (int part_n = 0;; ++part_n) {
         const int at = part_n & 1;
         if (!tc_wait(smem_u32(&s.part_full[at]), (uint32_t)(part_n >> 1 & 1), abort, a.c.fault)) return;
-        const int take = s.part[at].take;
-        if (take == 0) return;
-        if (!load_keys()) return;
-        for (int u = 0; u < take; ++u, ++n) {
+        if (s.part[at].take == 0) return;
+        if (!cells.next(a, w, cell)) return;
+        load();
+        for (int u = 0; u < s.part[at].take; ++u, ++n) {
             const int p0 = s.part[at].begin + u * kUnit + 32 * w;           // of this warp's positions
             const int lo = s.part[at].span.lo, hi = s.part[at].span.hi;
-            const bool edge = p0 < lo || p0 + 32 > hi;
-            const int par = n & 1;
-            // ---- powers of two, of what is a number and seen by some row
-            uint32_t top_k = 0, top_v = 0;
-            bool odd = false;
+            uint32_t top = 0;                               // of what is a number and seen by some row
 #pragma unroll
             for (int k = 0; k < SCALES; ++k) {
-                const int i = (lane & 15) * SCALES + k;     // word of the cell's: keys: [16][NB / 2], values: [8][NB] of two positions
-                const int pk = p0 + kCell * (lane >> 4) + i / (NB / 2), pv = p0 + kCell * (lane >> 4) + 2 * (i / NB);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t x = tk[k] >> (16 * h) & 0x7fffu, y = tv[k] >> (16 * h) & 0x7fffu;
-                    if (x < 0x7c00u && pk >= lo && pk < hi) top_k = max(top_k, x);
-                    if (pv + h >= lo && pv + h < hi) {
-                        if (y < 0x7c00u) top_v = max(top_v, y); else odd = true;
-                    }
+                const int p = p0 + kCell * (lane >> 4) + ((lane & 15) * SCALES + k) / (NB / 2);
+                if (p >= lo && p < hi) {
+                    const uint32_t x = tk[k] & 0x7fffu, y = tk[k] >> 16 & 0x7fffu;
+                    top = max(top, max(x < 0x7c00u ? x : 0u, y < 0x7c00u ? y : 0u));
                 }
             }
-            const int ek = (int)(__reduce_max_sync(0xffffffffu, top_k) >> 10), ev = (int)(__reduce_max_sync(0xffffffffu, top_v) >> 10);
-            odd = __any_sync(0xffffffffu, odd);
-            if (lane == 0) {
-                s.k_exp[par][w] = ek - 5;
-                s.v_exp[par][w] = ev - 5;
-            }
-            constexpr int TO = BITS == 4 ? 25 : 29;         // scales go to [2^10, 2^11) or [2^14, 2^15)
-            // ---- keys
+            const int e = (int)(__reduce_max_sync(0xffffffffu, top) >> 10);
             if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;      // the tile is free
-            {
-                const int x = TO - ek, x1 = min(x, 15);
-                const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
+            if (lane == 0) s.k_exp[n & 1][w] = e - 5;
+            const int x = TO - e, x1 = min(x, 15);
+            const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
+#pragma unroll
+            for (int v = 0; v < L::UNITS; ++v) {
+                if (v > 0) load_unit(v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = 32 * w + 8 * i + kr;
 #pragma unroll
-                    for (int b = 0; b < NB; b += 2) {
+                    for (int k = 0; k < BLOCKS; ++k) {
+                        const int b = v * BLOCKS + k;
                         const __half2 d = __hmul2(__hmul2(bits_h2(ks[i][b / 2]), up1), up2);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            uint32_t h[4];
-                            raw_pairs<BITS, 0x4140, 0x4342>(&raw[(b + e) / BLOCKS][i][(b + e) % BLOCKS * WB], h);
-                            scaled_pairs<BITS>(h, e ? __high2half2(d) : __low2half2(d));
-                            const int chunk = 4 * ((b + e) & 1) + c;
-                            const uint32_t to = k_tile + (b >> 1) * (kUnit * 128) + row * 128 + ((chunk ^ (row & 7)) << 4);
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-                        }
+                        uint32_t h[4];
+                        raw_pairs<BITS, 0x4140, 0x4342>(&raw[i][k * WB], h);
+                        scaled_pairs<BITS>(h, b & 1 ? __high2half2(d) : __low2half2(d));
+                        const uint32_t to = k_tile + (b >> 1) * (kUnit * 128) + row * 128 + (((4 * (b & 1) + c) ^ (row & 7)) << 4);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
                     }
                 }
             }
@@ -307,54 +274,133 @@ __device__ __forceinline__ void decode(const AttnArgs &a, typename Tile<BITS, D>
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(smem_u32(&s.k_full));
-                mbar_arrive(smem_u32(&s.s_full));
+                mbar_arrive(smem_u32(&s.s_full));           // (the softmax warps read the exponents)
             }
-            // ---- values
-            load_values();
-            uint32_t vs[4][NB];
+            if (u + 1 < s.part[at].take) {
+                if (!cells.next(a, w, cell)) return;
+                load();
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.part_empty[at]));
+    }
+}
+
+// A value warp has 32 positions of a unit.  A lane turns eight positions' elements g, 8 + g, .. into rows of V^T: 16 bytes
+// each, the rows of eight neighbouring lanes in different banks.
+template <int BITS, int D>
+__device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t v_tile) {
+    using T = Tile<BITS, D>;
+    using L = typename T::L;
+    constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS;
+    constexpr int SCALES = NB / 2;
+    constexpr int TO = BITS == 4 ? 25 : 29;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kValues;
+    const int q = lane >> 3, g = lane & 7;                  // eight positions from 8 q, elements g of each eight
+    volatile int *abort = &s.abort;
+    Cells<BITS, D> cells = {s, 0};
+    uint32_t n = 0;
+    uint64_t cell[2];
+    uint32_t raw[4][L::UW], vs[4][BLOCKS], tv[SCALES];
+    auto load_unit = [&](int u) {
+        const uint64_t from = cell[q >> 1];
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(from);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint64_t from = cell[q >> 1];
-                const int pos = 8 * (q & 1) + 2 * i, p = p0 + 8 * q + 2 * i;
-                if (from > 1) load_global<NB>(reinterpret_cast<const uint8_t *>(from) + L::v_scale(pos, 0), vs[i]);
+        for (int i = 0; i < 4; ++i) {                       // pairs 4 (q % 2) + i
+            if (from > 1) {
+                load_global<L::UW>(p + L::v_word(4 * (q & 1) + i, g, u * L::UW), raw[i]);
+                load_global<BLOCKS>(p + L::v_scale(8 * (q & 1) + 2 * i, u * BLOCKS), vs[i]);
+            } else {
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    if (from <= 1) vs[i][b] = 0;
-                    if (edge) vs[i][b] &= (p >= lo && p < hi ? 0xffffu : 0u) | (p + 1 >= lo && p + 1 < hi ? 0xffff0000u : 0u);
+                for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
+#pragma unroll
+                for (int k = 0; k < BLOCKS; ++k) vs[i][k] = 0;
+            }
+        }
+    };
+    auto load = [&]() {
+        load_unit(0);
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[lane >> 4]);
+#pragma unroll
+        for (int k = 0; k < SCALES; ++k) {
+            tv[k] = 0;
+            if (cell[lane >> 4] > 1) load_global<1>(p + L::VS + 4 * ((lane & 15) * SCALES + k), &tv[k]);
+        }
+    };
+    for (int part_n = 0;; ++part_n) {
+        const int at = part_n & 1;
+        if (!tc_wait(smem_u32(&s.part_full[at]), (uint32_t)(part_n >> 1 & 1), abort, a.c.fault)) return;
+        if (s.part[at].take == 0) return;
+        if (!cells.next(a, w, cell)) return;
+        load();
+        for (int u = 0; u < s.part[at].take; ++u, ++n) {
+            const int p0 = s.part[at].begin + u * kUnit + 32 * w;
+            const int lo = s.part[at].span.lo, hi = s.part[at].span.hi, par = n & 1;
+            const bool edge = p0 < lo || p0 + 32 > hi;
+            uint32_t top = 0;
+            bool odd = false;                               // a block that is no number
+#pragma unroll
+            for (int k = 0; k < SCALES; ++k) {
+                const int p = p0 + kCell * (lane >> 4) + 2 * (((lane & 15) * SCALES + k) / NB);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = tv[k] >> (16 * h) & 0x7fffu;
+                    if (p + h >= lo && p + h < hi) {
+                        if (x < 0x7c00u) top = max(top, x); else odd = true;
+                    }
                 }
             }
-            if (n > 0 && !tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault)) return;
+            const int e = (int)(__reduce_max_sync(0xffffffffu, top) >> 10);
+            odd = __any_sync(0xffffffffu, odd);
+            if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;
+            if (lane == 0) {
+                s.v_exp[par][w] = e - 5;
+                mbar_arrive(smem_u32(&s.s_full));           // (the softmax warps read the exponents)
+            }
+            if (n > 0 && !tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault)) return;     // the tile is free
             if (lane == 0) s.any_bad[par][w] = odd;         // (the softmax warps are done with those of two units before)
-            if (odd) {                                      // blocks that are no numbers leave the product, and are marked
+            if (odd) {                                      // a lane a position: marks of its blocks
+                uint32_t marks = 0;
+                const uint64_t from = cell[lane >> 4];
+#pragma unroll 1
+                for (int b = 0; b < NB && from > 1 && p0 + lane >= lo && p0 + lane < hi; ++b) {
+                    const uint16_t d = *reinterpret_cast<const uint16_t *>(reinterpret_cast<const uint8_t *>(from) + L::v_scale(lane & 15, b));
+                    if ((d & 0x7c00u) == 0x7c00u) marks |= 1u << b;
+                }
+                s.bad[par][32 * w + lane] = (uint8_t)marks;
+            }
+            const int x = TO - e, x1 = min(x, 15);
+            const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t bits[2] = {0, 0};
+            for (int v = 0; v < L::UNITS; ++v) {
+                if (v > 0) load_unit(v);
+                if (edge) {                                 // positions that no row sees are zeros
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        if ((vs[i][b] & 0x7c00u) == 0x7c00u) { bits[0] |= 1u << b; vs[i][b] &= 0xffff0000u; }
-                        if ((vs[i][b] & 0x7c000000u) == 0x7c000000u) { bits[1] |= 1u << b; vs[i][b] &= 0x0000ffffu; }
-                    }
-                    if (g == 0) {
-                        s.bad[par][32 * w + 8 * q + 2 * i] = (uint8_t)bits[0];
-                        s.bad[par][32 * w + 8 * q + 2 * i + 1] = (uint8_t)bits[1];
+                    for (int i = 0; i < 4; ++i) {
+                        const int p = p0 + 8 * q + 2 * i;
+                        const uint32_t keep = (p >= lo && p < hi ? 0xffffu : 0u) | (p + 1 >= lo && p + 1 < hi ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int k = 0; k < BLOCKS; ++k) vs[i][k] &= keep;
                     }
                 }
-            }
-            {
-                const int x = TO - ev, x1 = min(x, 15);
-                const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
+                if (odd) {                                  // blocks that are no numbers leave the product
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < BLOCKS; ++k) vs[i][k] &= ~__vcmpeq2(vs[i][k] & 0x7c007c00u, 0x7c007c00u);
+                }
+#pragma unroll
+                for (int k = 0; k < BLOCKS; ++k) {
                     uint32_t h[4][4];                       // [pair][j]
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        raw_pairs<BITS, 0x4240, 0x4341>(&raw[b / BLOCKS][i][b % BLOCKS * WB], h[i]);
-                        scaled_pairs<BITS>(h[i], __hmul2(__hmul2(bits_h2(vs[i][b]), up1), up2));
+                        raw_pairs<BITS, 0x4240, 0x4341>(&raw[i][k * WB], h[i]);
+                        scaled_pairs<BITS>(h[i], __hmul2(__hmul2(bits_h2(vs[i][k]), up1), up2));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int row = 32 * b + 8 * j + g, chunk = 4 * (w & 1) + q;
-                        const uint32_t to = v_tile + (w >> 1) * (D * 128) + row * 128 + ((chunk ^ g) << 4);
+                        const int row = 32 * (v * BLOCKS + k) + 8 * j + g;
+                        const uint32_t to = v_tile + (w >> 1) * (D * 128) + row * 128 + (((4 * (w & 1) + q) ^ g) << 4);
                         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0][j]), "r"(h[1][j]), "r"(h[2][j]), "r"(h[3][j]) : "memory");
                     }
                 }
@@ -362,7 +408,10 @@ __device__ __forceinline__ void decode(const AttnArgs &a, typename Tile<BITS, D>
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.v_full));
-            if (u + 1 < take && !load_keys()) return;
+            if (u + 1 < s.part[at].take) {
+                if (!cells.next(a, w, cell)) return;
+                load();
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.part_empty[at]));
@@ -478,69 +527,82 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
             tc_fence_after();
             if (work) {
                 if (u > 0) look_at_bad(n - 1, p0 - kUnit);
-                const int first = see.lo - p0, last = see.hi - p0;          // columns that the row sees: [first, last)
+                int first = see.lo - p0, last = see.hi - p0;                // columns that the row sees: [first, last)
                 const bool edge = __any_sync(0xffffffffu, first > 0 || last < kUnit);
-                float fk[4], ev[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    fk[c] = factor * __uint_as_float((uint32_t)(127 + s.k_exp[n & 1][c]) << 23);
-                    ev[c] = (float)s.v_exp[n & 1][c];
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32], m = -INFINITY;
-                    tmem_load32(scores + 32 * c, v);
+                const int *ke = s.k_exp[n & 1], *ve = s.v_exp[n & 1];       // of 32 columns
+                // The columns' loads run eight ahead of their use; behind the last ones the first eight again, which the second pass
+                // begins with.  (Loops that stay loops: unrolled, what each eight needs would be kept in registers all at once.)
+                float v0[8], v1[8], top = -INFINITY;
+                auto highest = [&](float (&v)[8], int at) {
                     if (edge) {
+                        const uint32_t seen = bits_between(first - at, last - at);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) if (32 * c + k < first || 32 * c + k >= last) v[k] = -INFINITY;
+                        for (int k = 0; k < 8; ++k) if (!(seen >> k & 1u)) v[k] = -INFINITY;
                     }
+                    float m = v[0];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) m = fmaxf(m, v[k]);
-                    if (m > -INFINITY) top = fmaxf(top, fmaf(m, fk[c], ev[c]));
+                    for (int k = 1; k < 8; ++k) m = fmaxf(m, v[k]);
+                    return m;
+                };
+                tmem_ld8(scores, v0);
+#pragma unroll 1
+                for (int c = 0; c < kUnit; c += 16) {
+                    tmem_wait_ld(v0);
+                    tmem_ld8(scores + c + 8, v1);
+                    float m = highest(v0, c);
+                    tmem_wait_ld(v1);
+                    tmem_ld8(scores + ((c + 16) & (kUnit - 1)), v0);
+                    m = fmaxf(m, highest(v1, c + 8));
+                    if (m > -INFINITY) top = fmaxf(top, fmaf(m, factor * power(ke[c >> 5]), (float)ve[c >> 5]));
                 }
+                tmem_wait_ld(v0);
                 const bool raise = top > ref + kSlack;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float now = raise ? top : ref, f = raise ? ex2(ref - now) : 1.f;         // 0 from -inf
                     l *= f;
                     ref = now;
                     if (u > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 8) {
+                            float y[8];
+                            tmem_ld8(outputs + c, y);
+                            tmem_wait_ld(y);
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            float v[32];
-                            tmem_load32(outputs + 32 * c, v);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] *= f;
-#pragma unroll
-                            for (int k = 0; k < 32; k += 16) {
-                                uint32_t x[16];
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(v[k + i]);
-                                tmem_st16(outputs + 32 * c + k, x);
-                            }
+                            for (int k = 0; k < 8; ++k) y[k] *= f;
+                            tmem_st8(outputs + c, y);
                         }
                     }
                 }
                 const float base = kWeight - fmaxf(ref, -3e38f);            // nothing seen yet: all columns are hidden
+                // weights of 8 columns into tensor memory, in place of scores that are in registers by then
+                auto weigh = [&](float (&v)[8], int at, float2 f2, float2 b2, float2 &sum) {
+                    uint32_t x[4];
+                    const uint32_t seen = edge ? bits_between(first - at, last - at) : 0xffu;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32], sum = 0.f;
-                    tmem_load32(scores + 32 * c, v);
-                    const float b = base + ev[c];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        v[k] = fmaf(v[k], fk[c], b);
-                        if (edge && (32 * c + k < first || 32 * c + k >= last)) v[k] = -INFINITY;
-                        v[k] = ex2(v[k]);
+                    for (int k = 0; k < 4; ++k) {
+                        float2 z = ffma2(make_float2(v[2 * k], v[2 * k + 1]), f2, b2);
+                        if (edge) {
+                            if (!(seen >> (2 * k) & 1u)) z.x = -INFINITY;
+                            if (!(seen >> (2 * k + 1) & 1u)) z.y = -INFINITY;
+                        }
+                        z = make_float2(ex2(z.x), ex2(z.y));
+                        sum = fadd2(sum, z);
+                        x[k] = h2_bits(__floats2half2_rn(z.x, z.y));
                     }
-                    uint32_t x[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        sum += v[2 * k] + v[2 * k + 1];
-                        x[k] = h2_bits(__floats2half2_rn(v[2 * k], v[2 * k + 1]));
-                    }
-                    l = fmaf(sum, __uint_as_float((uint32_t)(127 - s.v_exp[n & 1][c]) << 23), l);
-                    tmem_st16(scores + 16 * c, x);
+                    tmem_st4u(scores + at / 2, x);
+                };
+#pragma unroll 1
+                for (int c = 0; c < kUnit; c += 16) {
+                    const float fk = factor * power(ke[c >> 5]), b = base + (float)ve[c >> 5];
+                    const float2 f2 = make_float2(fk, fk), b2 = make_float2(b, b);
+                    float2 sum = make_float2(0.f, 0.f);
+                    tmem_ld8(scores + c + 8, v1);
+                    weigh(v0, c, f2, b2, sum);
+                    tmem_wait_ld(v1);
+                    tmem_ld8(scores + ((c + 16) & (kUnit - 1)), v0);        // (behind the last ones: not used)
+                    weigh(v1, c + 8, f2, b2, sum);
+                    tmem_wait_ld(v0);
+                    l = fmaf(sum.x + sum.y, power(-ve[c >> 5]), l);
                 }
                 tmem_wait_st();
             }
@@ -557,20 +619,17 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
             const long long r = (long long)part.slot * kRows + me;
             const long long to = ((long long)part.q.first + token) * a.out_stride + (long long)head * D;
             if (live && part.slot >= 0) a.stat[r] = make_float2(ref - kWeight, l);
+#pragma unroll 2
+            for (int c = 0; c < D; c += 8) {
+                float v[8];
+                tmem_ld8(outputs + c, v);
+                tmem_wait_ld(v);
+                const bool gone = bad >> (c >> 5) & 1u;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float v[32];
-                tmem_load32(outputs + 32 * c, v);
-                const bool gone = bad >> c & 1u;
-#pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    float y[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = gone ? __uint_as_float(0x7fffffffu) : v[k + i] * f;
-                    if (!live) continue;
-                    if (part.slot >= 0) store8(a.partial + r * D + 32 * c + k, y);
-                    else store_row8<false>(a, to + 32 * c + k, y);
-                }
+                for (int i = 0; i < 8; ++i) v[i] = gone ? __uint_as_float(0x7fffffffu) : v[i] * f;
+                if (!live) continue;
+                if (part.slot >= 0) store8(a.partial + r * D + c, v);
+                else store_row8<false>(a, to + c, v);
             }
             tc_fence_before();
         }
@@ -590,16 +649,16 @@ __global__ void __launch_bounds__(kThreads, (Tile<BITS, D>::MIN_BLOCKS)) attenti
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s.part_full[i]), 1);
-            mbar_init(smem_u32(&s.part_empty[i]), kSoftmax + kDecode + 1);
+            mbar_init(smem_u32(&s.part_empty[i]), kSoftmax + 2 * kDecode + 1);
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_u32(&s.cell_full[i]), 1);
-            mbar_init(smem_u32(&s.cell_empty[i]), kDecode);
+            mbar_init(smem_u32(&s.cell_empty[i]), 2 * kDecode);
         }
         mbar_init(smem_u32(&s.q_full), kSoftmax);
         mbar_init(smem_u32(&s.k_full), kDecode);
         mbar_init(smem_u32(&s.v_full), kDecode);
-        mbar_init(smem_u32(&s.s_full), 1 + kDecode);         // the products, and the exponents of K and V
+        mbar_init(smem_u32(&s.s_full), 1 + 2 * kDecode);         // the products, and the exponents of K and V
         mbar_init(smem_u32(&s.p_full), kSoftmax);
         mbar_init(smem_u32(&s.pv_done), 1);
         fence_mbar_init();
@@ -617,11 +676,12 @@ __global__ void __launch_bounds__(kThreads, (Tile<BITS, D>::MIN_BLOCKS)) attenti
     long long total, x0, end;
     deal<kThreads>(a, total, x0, end, s.walk);
     if (x0 >= end) {
-        if (threadIdx.x == 0) a.joins[blockIdx.x].valid = 0;
     } else if (warp < kSoftmax) {
         softmax<BITS, D>(a, s, q_tile, tmem);
+    } else if (warp < kValues) {
+        decode_keys<BITS, D>(a, s, k);
     } else if (warp < kWalker) {
-        decode<BITS, D>(a, s, k, v);
+        decode_values<BITS, D>(a, s, v);
     } else if (warp == kWalker) {
         walk<BITS, D>(a, s, total, x0, end);
     } else if (elect_one()) {
