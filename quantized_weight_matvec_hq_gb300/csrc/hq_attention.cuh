@@ -24,6 +24,7 @@ struct AttnArgs {
     int dtype;                          // of q and out: HQ_DT_*
     int n_heads, group;                 // heads, and those that share a key/value head
     int tokens, part_heads, parts;      // of a tile: tokens, heads of a group, and tiles a group takes
+    int inv_heads;                      // 2^16 / part_heads, rounded up: quotients of numbers below 128
     int causal;
     float scale;
     long long window;                   // 0: none
@@ -274,8 +275,9 @@ __device__ __forceinline__ void tell_part(const AttnArgs &a, const Walk &w, long
 
 // Row i of an item is token tile * tokens + i / part_heads of the request, and of its group head part * part_heads + i % part_heads.
 __device__ __forceinline__ bool row_of(const AttnArgs &a, const Request &q, const Item &it, int i, int &token, int &head) {
-    token = it.tile * a.tokens + i / a.part_heads;
-    const int h = it.part * a.part_heads + i % a.part_heads;
+    const int t = i * a.inv_heads >> 16;                    // i / part_heads
+    token = it.tile * a.tokens + t;
+    const int h = it.part * a.part_heads + i - t * a.part_heads;
     head = it.kv_head * a.group + h;
     return i < a.tokens * a.part_heads && token < q.n && h < a.group;
 }
@@ -341,6 +343,7 @@ inline void deal_rows(AttnArgs &a, int rows, int dim, int unit_shift, int blocks
     a.tokens = a.group <= rows ? rows / a.group : 1;
     a.part_heads = a.group <= rows ? a.group : rows;
     a.parts = (a.group + a.part_heads - 1) / a.part_heads;
+    a.inv_heads = (65536 + a.part_heads - 1) / a.part_heads;
     a.unit_shift = unit_shift;
     const long long tiles = std::min(a.c.n_tokens, a.c.n_tokens / a.tokens + a.c.n_req);
     a.most_units = ((a.c.table_width << a.c.page_shift) + (1 << unit_shift) - 1) >> unit_shift;

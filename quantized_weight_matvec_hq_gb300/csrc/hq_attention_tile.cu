@@ -32,10 +32,10 @@ constexpr float kSlack = 8.f, kWeight = 6.f;                // weights up to 2^(
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
-// Bits [lo, hi) of 16.
+// Bits [lo, hi) of 32.
 __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
-    const int a = min(max(lo, 0), 16), b = min(max(hi, a), 16);
-    return (1u << b) - (1u << a);
+    const int a = min(max(lo, 0), 32), b = min(max(hi, a), 32);
+    return (uint32_t)((1ull << b) - (1ull << a));
 }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }     // 2^e
 __device__ __forceinline__ __half2 power_h2(int e) {        // 2^e, -14 <= e <= 15
@@ -50,10 +50,30 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, ui
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
 }
 
-// 8 columns' pairs of 16-bit floats.
-__device__ __forceinline__ void tmem_st4u(uint32_t addr, const uint32_t (&v)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0,%1,%2,%3};"
-                 ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(addr) : "memory");
+// This warp's 32 lanes x 32 columns, waited for.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+          "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+          "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(addr) : "memory");
+}
+// 16 columns' pairs of 16-bit floats.
+__device__ __forceinline__ void tmem_st8u(uint32_t addr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
+                 ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
@@ -292,7 +312,7 @@ template <int BITS, int D>
 __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t v_tile) {
     using T = Tile<BITS, D>;
     using L = typename T::L;
-    constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS;
+    constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS, TWO = BLOCKS < 2 ? BLOCKS : 2;     // scales in registers: of TWO blocks
     constexpr int SCALES = NB / 2;
     constexpr int TO = BITS == 4 ? 25 : 29;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kValues;
@@ -301,22 +321,25 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
     Cells<BITS, D> cells = {s, 0};
     uint32_t n = 0;
     uint64_t cell[2];
-    uint32_t raw[4][L::UW], vs[4][BLOCKS], tv[SCALES];
-    auto load_unit = [&](int u) {
+    uint32_t raw[4][L::UW], vs[4][TWO], tv[SCALES];
+    auto load_scales = [&](int b) {
         const uint64_t from = cell[q >> 1];
-        const uint8_t *p = reinterpret_cast<const uint8_t *>(from);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {                       // pairs 4 (q % 2) + i
-            if (from > 1) {
-                load_global<L::UW>(p + L::v_word(4 * (q & 1) + i, g, u * L::UW), raw[i]);
-                load_global<BLOCKS>(p + L::v_scale(8 * (q & 1) + 2 * i, u * BLOCKS), vs[i]);
-            } else {
 #pragma unroll
-                for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
-#pragma unroll
-                for (int k = 0; k < BLOCKS; ++k) vs[i][k] = 0;
-            }
+            for (int k = 0; k < TWO; ++k) vs[i][k] = 0;
+            if (from > 1) load_global<TWO>(reinterpret_cast<const uint8_t *>(from) + L::v_scale(8 * (q & 1) + 2 * i, b), vs[i]);
         }
+    };
+    auto load_unit = [&](int u) {
+        const uint64_t from = cell[q >> 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
+            if (from > 1) load_global<L::UW>(reinterpret_cast<const uint8_t *>(from) + L::v_word(4 * (q & 1) + i, g, u * L::UW), raw[i]);
+        }
+        load_scales(u * BLOCKS);
     };
     auto load = [&]() {
         load_unit(0);
@@ -371,31 +394,34 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
             }
             const int x = TO - e, x1 = min(x, 15);
             const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
-#pragma unroll
+#pragma unroll 1
             for (int v = 0; v < L::UNITS; ++v) {
                 if (v > 0) load_unit(v);
-                if (edge) {                                 // positions that no row sees are zeros
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int p = p0 + 8 * q + 2 * i;
-                        const uint32_t keep = (p >= lo && p < hi ? 0xffffu : 0u) | (p + 1 >= lo && p + 1 < hi ? 0xffff0000u : 0u);
-#pragma unroll
-                        for (int k = 0; k < BLOCKS; ++k) vs[i][k] &= keep;
-                    }
-                }
-                if (odd) {                                  // blocks that are no numbers leave the product
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int k = 0; k < BLOCKS; ++k) vs[i][k] &= ~__vcmpeq2(vs[i][k] & 0x7c007c00u, 0x7c007c00u);
-                }
 #pragma unroll
                 for (int k = 0; k < BLOCKS; ++k) {
+                    if (k > 0 && k % TWO == 0) load_scales(v * BLOCKS + k);
+                    if (k % TWO == 0) {
+                        if (edge) {                         // positions that no row sees are zeros
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int p = p0 + 8 * q + 2 * i;
+                                const uint32_t keep = (p >= lo && p < hi ? 0xffffu : 0u) | (p + 1 >= lo && p + 1 < hi ? 0xffff0000u : 0u);
+#pragma unroll
+                                for (int j = 0; j < TWO; ++j) vs[i][j] &= keep;
+                            }
+                        }
+                        if (odd) {                          // blocks that are no numbers leave the product
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int j = 0; j < TWO; ++j) vs[i][j] &= ~__vcmpeq2(vs[i][j] & 0x7c007c00u, 0x7c007c00u);
+                        }
+                    }
                     uint32_t h[4][4];                       // [pair][j]
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         raw_pairs<BITS, 0x4240, 0x4341>(&raw[i][k * WB], h[i]);
-                        scaled_pairs<BITS>(h[i], __hmul2(__hmul2(bits_h2(vs[i][k]), up1), up2));
+                        scaled_pairs<BITS>(h[i], __hmul2(__hmul2(bits_h2(vs[i][k % TWO]), up1), up2));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -479,28 +505,41 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
         {
             const float sign = a.scale < 0.f ? -1.f : 1.f;
             const int col = lane % LANES;
-#pragma unroll 4
-            for (int i = 0; i < 32; i += ROWS) {
-                const int row = 32 * warp + i + lane / LANES;
-                int token, head;
-                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (row_of(a, part.q, part.item, row, token, head))
-                    load_row8<false>(a, ((long long)part.q.first + token) * a.q_stride + (long long)head * D + 8 * col, v);
-                uint32_t top = 0;
+            constexpr int BATCH = 4;                        // loads under way at once
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32; i0 += BATCH * ROWS) {
+                uint4 raw[BATCH];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+                for (int i = 0; i < BATCH; ++i) {
+                    const int row = 32 * warp + i0 + i * ROWS + lane / LANES;
+                    int token, head;
+                    const bool live = row_of(a, part.q, part.item, row, token, head);
+                    const long long from = live ? ((long long)part.q.first + token) * a.q_stride + (long long)head * D + 8 * col : 0;
+                    raw[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + from);
+                    if (!live) raw[i] = make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-                for (int d = 1; d < LANES; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                const int e = min(253, 268 - (int)(top >> 23));
-                const float up = __uint_as_float((uint32_t)e << 23) * sign;
-                uint32_t h[4];
+                for (int i = 0; i < BATCH; ++i) {
+                    const int row = 32 * warp + i0 + i * ROWS + lane / LANES;
+                    float v[8];
+                    if (a.dtype == HQ_DT_F16) load8(reinterpret_cast<const __half *>(&raw[i]), v);
+                    else load8(reinterpret_cast<const __nv_bfloat16 *>(&raw[i]), v);
+                    uint32_t top = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = h2_bits(__floats2half2_rn(v[2 * k] * up, v[2 * k + 1] * up));
-                *reinterpret_cast<uint4 *>(q_tile + (col / 8) * (kRows * 128) + row * 128 + ((col % 8 ^ (row & 7)) << 4)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
-                if (col == 0)
-                    s.factor[row] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
-                                                       : fabsf(a.scale) * kLog2e * __uint_as_float((uint32_t)(254 - e) << 23);
+                    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+#pragma unroll
+                    for (int d = 1; d < LANES; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    const int e = min(253, 268 - (int)(top >> 23));
+                    const float up = __uint_as_float((uint32_t)e << 23) * sign;
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[k] = h2_bits(__floats2half2_rn(v[2 * k] * up, v[2 * k + 1] * up));
+                    *reinterpret_cast<uint4 *>(q_tile + (col / 8) * (kRows * 128) + row * 128 + ((col % 8 ^ (row & 7)) << 4)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                    if (col == 0)
+                        s.factor[row] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
+                                                           : fabsf(a.scale) * kLog2e * __uint_as_float((uint32_t)(254 - e) << 23);
+                }
             }
             fence_proxy_async_shared();
             __syncwarp();
@@ -530,32 +569,24 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
                 int first = see.lo - p0, last = see.hi - p0;                // columns that the row sees: [first, last)
                 const bool edge = __any_sync(0xffffffffu, first > 0 || last < kUnit);
                 const int *ke = s.k_exp[n & 1], *ve = s.v_exp[n & 1];       // of 32 columns
-                // The columns' loads run eight ahead of their use; behind the last ones the first eight again, which the second pass
-                // begins with.  (Loops that stay loops: unrolled, what each eight needs would be kept in registers all at once.)
-                float v0[8], v1[8], top = -INFINITY;
-                auto highest = [&](float (&v)[8], int at) {
-                    if (edge) {
-                        const uint32_t seen = bits_between(first - at, last - at);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) if (!(seen >> k & 1u)) v[k] = -INFINITY;
-                    }
-                    float m = v[0];
-#pragma unroll
-                    for (int k = 1; k < 8; ++k) m = fmaxf(m, v[k]);
-                    return m;
-                };
-                tmem_ld8(scores, v0);
+                // (Loops that stay loops: unrolled, what each 32 columns need would be kept in registers all at once.)
+                float top = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < kUnit; c += 16) {
-                    tmem_wait_ld(v0);
-                    tmem_ld8(scores + c + 8, v1);
-                    float m = highest(v0, c);
-                    tmem_wait_ld(v1);
-                    tmem_ld8(scores + ((c + 16) & (kUnit - 1)), v0);
-                    m = fmaxf(m, highest(v1, c + 8));
-                    if (m > -INFINITY) top = fmaxf(top, fmaf(m, factor * power(ke[c >> 5]), (float)ve[c >> 5]));
+                for (int c = 0; c < 4; ++c) {
+                    float v[32], m[4];
+                    tmem_load32(scores + 32 * c, v);
+                    if (edge) {
+                        const uint32_t seen = bits_between(first - 32 * c, last - 32 * c);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) if (!(seen >> k & 1u)) v[k] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m[k] = v[k];
+#pragma unroll
+                    for (int k = 4; k < 32; ++k) m[k & 3] = fmaxf(m[k & 3], v[k]);
+                    m[0] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                    if (m[0] > -INFINITY) top = fmaxf(top, fmaf(m[0], factor * power(ke[c]), (float)ve[c]));
                 }
-                tmem_wait_ld(v0);
                 const bool raise = top > ref + kSlack;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float now = raise ? top : ref, f = raise ? ex2(ref - now) : 1.f;         // 0 from -inf
@@ -563,46 +594,45 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
                     ref = now;
                     if (u > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 8) {
-                            float y[8];
-                            tmem_ld8(outputs + c, y);
-                            tmem_wait_ld(y);
+                        for (int c = 0; c < D; c += 16) {
+                            float y[16];
+                            tmem_load16(outputs + c, y);
+                            uint32_t z[16];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) y[k] *= f;
-                            tmem_st8(outputs + c, y);
+                            for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(y[k] * f);
+                            tmem_st16(outputs + c, z);
                         }
                     }
                 }
                 const float base = kWeight - fmaxf(ref, -3e38f);            // nothing seen yet: all columns are hidden
-                // weights of 8 columns into tensor memory, in place of scores that are in registers by then
-                auto weigh = [&](float (&v)[8], int at, float2 f2, float2 b2, float2 &sum) {
-                    uint32_t x[4];
-                    const uint32_t seen = edge ? bits_between(first - at, last - at) : 0xffu;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float2 z = ffma2(make_float2(v[2 * k], v[2 * k + 1]), f2, b2);
-                        if (edge) {
-                            if (!(seen >> (2 * k) & 1u)) z.x = -INFINITY;
-                            if (!(seen >> (2 * k + 1) & 1u)) z.y = -INFINITY;
-                        }
-                        z = make_float2(ex2(z.x), ex2(z.y));
-                        sum = fadd2(sum, z);
-                        x[k] = h2_bits(__floats2half2_rn(z.x, z.y));
-                    }
-                    tmem_st4u(scores + at / 2, x);
-                };
+                // weights into tensor memory, in place of scores that are in registers by then
 #pragma unroll 1
-                for (int c = 0; c < kUnit; c += 16) {
-                    const float fk = factor * power(ke[c >> 5]), b = base + (float)ve[c >> 5];
+                for (int c = 0; c < 4; ++c) {
+                    const float fk = factor * power(ke[c]), b = base + (float)ve[c];
                     const float2 f2 = make_float2(fk, fk), b2 = make_float2(b, b);
-                    float2 sum = make_float2(0.f, 0.f);
-                    tmem_ld8(scores + c + 8, v1);
-                    weigh(v0, c, f2, b2, sum);
-                    tmem_wait_ld(v1);
-                    tmem_ld8(scores + ((c + 16) & (kUnit - 1)), v0);        // (behind the last ones: not used)
-                    weigh(v1, c + 8, f2, b2, sum);
-                    tmem_wait_ld(v0);
-                    l = fmaf(sum.x + sum.y, power(-ve[c >> 5]), l);
+                    float v[32];
+                    tmem_load32(scores + 32 * c, v);
+                    const uint32_t seen = edge ? bits_between(first - 32 * c, last - 32 * c) : 0xffffffffu;
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int at = 16 * h + 2 * k;
+                            float2 z = ffma2(make_float2(v[at], v[at + 1]), f2, b2);
+                            if (edge) {
+                                if (!(seen >> at & 1u)) z.x = -INFINITY;
+                                if (!(seen >> (at + 1) & 1u)) z.y = -INFINITY;
+                            }
+                            z = make_float2(ex2(z.x), ex2(z.y));
+                            sum[k & 1] = fadd2(sum[k & 1], z);
+                            x[k] = h2_bits(__floats2half2_rn(z.x, z.y));
+                        }
+                        tmem_st8u(scores + 16 * c + 8 * h, x);
+                    }
+                    sum[0] = fadd2(sum[0], sum[1]);
+                    l = fmaf(sum[0].x + sum[0].y, power(-ve[c]), l);
                 }
                 tmem_wait_st();
             }
@@ -619,17 +649,20 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
             const long long r = (long long)part.slot * kRows + me;
             const long long to = ((long long)part.q.first + token) * a.out_stride + (long long)head * D;
             if (live && part.slot >= 0) a.stat[r] = make_float2(ref - kWeight, l);
-#pragma unroll 2
-            for (int c = 0; c < D; c += 8) {
-                float v[8];
-                tmem_ld8(outputs + c, v);
-                tmem_wait_ld(v);
-                const bool gone = bad >> (c >> 5) & 1u;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                float v[32];
+                tmem_load32(outputs + 32 * c, v);
+                const bool gone = bad >> c & 1u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = gone ? __uint_as_float(0x7fffffffu) : v[i] * f;
-                if (!live) continue;
-                if (part.slot >= 0) store8(a.partial + r * D + c, v);
-                else store_row8<false>(a, to + c, v);
+                for (int k = 0; k < 32; k += 8) {
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = gone ? __uint_as_float(0x7fffffffu) : v[k + i] * f;
+                    if (!live) continue;
+                    if (part.slot >= 0) store8(a.partial + r * D + 32 * c + k, y);
+                    else store_row8<false>(a, to + 32 * c + k, y);
+                }
             }
             tc_fence_before();
         }
