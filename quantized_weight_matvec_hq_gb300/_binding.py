@@ -124,19 +124,31 @@ def lib() -> ctypes.CDLL:
 def _addr(t) -> int:
     if t is None:
         return 0
+    try:
+        return t.data_ptr()                       # a torch tensor: the usual case first
+    except AttributeError:
+        pass
     if isinstance(t, int):
         return t
-    if hasattr(t, "data_ptr"):
-        return int(t.data_ptr())
     if hasattr(t, "ctypes"):                      # numpy array (host functions)
         return int(t.ctypes.data)
     raise TypeError(f"cannot take the address of {type(t)}")
 
 
+_raw_stream = _device = None                      # torch's own look-ups, without a Stream object a call
+
+
 def _stream(s) -> int:
+    global _raw_stream, _device
     if s is None:
+        if _raw_stream is not None:
+            return _raw_stream(_device())
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        stream = int(torch.cuda.current_stream().cuda_stream)         # sets CUDA up
+        get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if get is not None and dev is not None:
+            _device, _raw_stream = dev, get
+        return stream
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)

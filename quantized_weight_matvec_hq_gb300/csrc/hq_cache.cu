@@ -12,6 +12,7 @@ namespace hq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFewBlocks = 304;                             // two a multiprocessor
 
 struct RowsArgs {
     CacheView c;
@@ -107,8 +108,20 @@ __device__ __forceinline__ void check_requests(const CacheView &c) {
         if (request_of(c, r).bad) atomicOr(c.fault, kFaultCache);
 }
 
-template <class T, int BITS, int D>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(RowsArgs a) {
+// 16 bytes (fp32: 32) of a token's row, as they come.
+template <class T>
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const { load8(reinterpret_cast<const T *>(w), v); }
+};
+
+// A warp's rows, of HEADS heads: what finding them costs is paid once, and the heads' loads are under way together.
+template <class T, int BITS, int D, int HEADS>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ RowsArgs a) {
     using L = CellLayout<BITS, D>;
     griddep_launch_dependents();
     griddep_wait();
@@ -116,59 +129,69 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(RowsArgs a) {
     long long t;
     int r, p;
     const bool ok = find_row<D>(a.c, t, r, p) && p >= 0;
-    const int head = blockIdx.y;
-    uint8_t *cell = nullptr;
+    const int head = blockIdx.y * HEADS, heads = min(HEADS, a.c.n_kv_heads - head);
+    uint8_t *cell0 = nullptr;
     if (ok) {
         uint8_t *cells = page_cells(a.c, r, p, head);
-        if (cells) cell = cell_of<L>(a.c, cells, p);
+        if (cells) cell0 = cell_of<L>(a.c, cells, p);
     }
     const int at = threadIdx.x & (Rows<D>::LANES - 1), b = at / 4, g = at % 4, pos = p & (kCell - 1);
-    float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    __half scale;
-    uint32_t q[2];
-    if (cell) load8(static_cast<const T *>(a.k) + t * a.k_stride + head * D + 8 * at, w);
-    quantize8<BITS>(w, scale, q);
-    if (cell) {
-        if (BITS == 8) {
-            *reinterpret_cast<uint32_t *>(cell + L::k_word(pos, g, 2 * b)) = q[0];
-            *reinterpret_cast<uint32_t *>(cell + L::k_word(pos, g, 2 * b + 1)) = q[1];
-        } else {
-            // bytes e0 e1 e2 e3 | e4 .. e7 -> nibbles e0 e2 e4 e6 e1 e3 e5 e7
-            const uint32_t lo = q[0] | (q[0] >> 12), hi = q[1] | (q[1] >> 12);      // byte 0: e0 | e2 << 4, byte 1: e1 | e3 << 4
-            *reinterpret_cast<uint32_t *>(cell + L::k_word(pos, g, b)) = prmt(lo, hi, 0x5140);
-        }
-        if (g == 0) *reinterpret_cast<__half *>(cell + L::k_scale(pos, b)) = scale;
-        load8(static_cast<const T *>(a.v) + t * a.v_stride + head * D + 8 * at, w);
-    }
-    quantize8<BITS>(w, scale, q);
-    // lane c holds elements 8 c + g, g = 0..7; it gets those of g = 2 c and 2 c + 1, of all four lanes:
-    // a 4 x 4 transposition of pairs of bytes
-    const uint32_t s0 = __shfl_xor_sync(0xffffffffu, (g & 2) ? q[0] : q[1], 2);
-    const uint32_t own = (g & 2) ? q[1] : q[0];             // bytes g = 4 (c / 2) .. + 3 of this lane and of lane c ^ 2
-    const uint32_t x0 = (g & 2) ? s0 : own, x1 = (g & 2) ? own : s0;        // of j = c % 2, and of j = 2 + c % 2
-    const uint32_t give = (g & 1) ? prmt(x0, x1, 0x5410) : prmt(x0, x1, 0x7632);
-    const uint32_t keep = (g & 1) ? prmt(x0, x1, 0x7632) : prmt(x0, x1, 0x5410);
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
-    const uint32_t j0 = (g & 1) ? got : keep, j1 = (g & 1) ? keep : got;    // bytes: j0: (j 0: g, g+1; j 2: g, g+1), j1: j 1 and 3
-    if (cell) {
-        const int odd = pos & 1;
+    Raw8<T> k[HEADS], v[HEADS];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t j = prmt(j0, j1, i == 0 ? 0x6240 : 0x7351);      // bytes j = 0, 1, 2, 3 of g = 2 c + i
-            if (BITS == 8) {
-                *reinterpret_cast<uint16_t *>(cell + L::v_word(pos / 2, 2 * g + i, 2 * b) + 2 * odd) = (uint16_t)j;
-                *reinterpret_cast<uint16_t *>(cell + L::v_word(pos / 2, 2 * g + i, 2 * b + 1) + 2 * odd) = (uint16_t)(j >> 16);
-            } else {
-                const uint32_t n = j | (j >> 4);            // bytes 0 and 2: j 0 | j 1 << 4, j 2 | j 3 << 4
-                *reinterpret_cast<uint16_t *>(cell + L::v_word(pos / 2, 2 * g + i, b) + 2 * odd) = (uint16_t)prmt(n, 0, 0x4420);
-            }
+    for (int h = 0; h < HEADS; ++h)
+        if (cell0 && h < heads) {
+            k[h].load(static_cast<const T *>(a.k) + t * a.k_stride + (head + h) * D + 8 * at);
+            v[h].load(static_cast<const T *>(a.v) + t * a.v_stride + (head + h) * D + 8 * at);
         }
-        if (g == 0) *reinterpret_cast<__half *>(cell + L::v_scale(pos, b)) = scale;
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h) {
+        uint8_t *cell = cell0 && h < heads ? cell0 + h * a.c.head_bytes : nullptr;
+        float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        __half scale;
+        uint32_t q[2];
+        if (cell) k[h].values(w);
+        quantize8<BITS>(w, scale, q);
+        if (cell) {
+            if (BITS == 8) {
+                *reinterpret_cast<uint2 *>(cell + L::k_word(pos, g, 2 * b)) = make_uint2(q[0], q[1]);
+            } else {
+                // bytes e0 e1 e2 e3 | e4 .. e7 -> nibbles e0 e2 e4 e6 e1 e3 e5 e7
+                const uint32_t lo = q[0] | (q[0] >> 12), hi = q[1] | (q[1] >> 12);  // byte 0: e0 | e2 << 4, byte 1: e1 | e3 << 4
+                *reinterpret_cast<uint32_t *>(cell + L::k_word(pos, g, b)) = prmt(lo, hi, 0x5140);
+            }
+            if (g == 0) *reinterpret_cast<__half *>(cell + L::k_scale(pos, b)) = scale;
+            v[h].values(w);
+        }
+        quantize8<BITS>(w, scale, q);
+        // lane c holds elements 8 c + g, g = 0..7; it gets those of g = 2 c and 2 c + 1, of all four lanes:
+        // a 4 x 4 transposition of pairs of bytes
+        const uint32_t s0 = __shfl_xor_sync(0xffffffffu, (g & 2) ? q[0] : q[1], 2);
+        const uint32_t own = (g & 2) ? q[1] : q[0];         // bytes g = 4 (c / 2) .. + 3 of this lane and of lane c ^ 2
+        const uint32_t x0 = (g & 2) ? s0 : own, x1 = (g & 2) ? own : s0;            // of j = c % 2, and of j = 2 + c % 2
+        const uint32_t give = (g & 1) ? prmt(x0, x1, 0x5410) : prmt(x0, x1, 0x7632);
+        const uint32_t keep = (g & 1) ? prmt(x0, x1, 0x7632) : prmt(x0, x1, 0x5410);
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+        const uint32_t j0 = (g & 1) ? got : keep, j1 = (g & 1) ? keep : got;        // bytes: j0: (j 0: g, g+1; j 2: g, g+1), j1: j 1 and 3
+        if (cell) {
+            const int odd = pos & 1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t j = prmt(j0, j1, i == 0 ? 0x6240 : 0x7351);          // bytes j = 0, 1, 2, 3 of g = 2 c + i
+                if (BITS == 8) {
+                    *reinterpret_cast<uint16_t *>(cell + L::v_word(pos / 2, 2 * g + i, 2 * b) + 2 * odd) = (uint16_t)j;
+                    *reinterpret_cast<uint16_t *>(cell + L::v_word(pos / 2, 2 * g + i, 2 * b + 1) + 2 * odd) = (uint16_t)(j >> 16);
+                } else {
+                    const uint32_t n = j | (j >> 4);        // bytes 0 and 2: j 0 | j 1 << 4, j 2 | j 3 << 4
+                    *reinterpret_cast<uint16_t *>(cell + L::v_word(pos / 2, 2 * g + i, b) + 2 * odd) = (uint16_t)prmt(n, 0, 0x4420);
+                }
+            }
+            if (g == 0) *reinterpret_cast<__half *>(cell + L::v_scale(pos, b)) = scale;
+        }
     }
 }
 
-template <class T, int BITS, int D>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(RowsArgs a) {
+template <class T, int BITS, int D, int HEADS>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ RowsArgs a) {
     using L = CellLayout<BITS, D>;
     griddep_launch_dependents();
     griddep_wait();
@@ -176,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(RowsArgs a) {
     long long t;
     int r, p;
     const bool ok = find_row<D>(a.c, t, r, p);
-    const int head = blockIdx.y;
+    const int head = blockIdx.y * HEADS, heads = min(HEADS, a.c.n_kv_heads - head);
     const uint8_t *cell = nullptr;
     float other = 0.f;                                      // what a row without a cell reads as
     if (ok && p >= 0) {
@@ -185,59 +208,69 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(RowsArgs a) {
         else other = __uint_as_float(0x7fffffffu);
     }
     const int at = threadIdx.x & (Rows<D>::LANES - 1), b = at / 4, g = at % 4, pos = p & (kCell - 1), odd = pos & 1;
-    float ks = 0.f, vs = 0.f;
-    uint32_t q[2] = {0, 0}, j[2] = {0, 0};                  // j[i]: bytes j = 0..3 of g = 2 c + i
-    if (cell) {
-        ks = __half2float(*reinterpret_cast<const __half *>(cell + L::k_scale(pos, b)));
-        vs = __half2float(*reinterpret_cast<const __half *>(cell + L::v_scale(pos, b)));
-        if (BITS == 8) {
-            q[0] = *reinterpret_cast<const uint32_t *>(cell + L::k_word(pos, g, 2 * b));
-            q[1] = *reinterpret_cast<const uint32_t *>(cell + L::k_word(pos, g, 2 * b + 1));
-        } else {
-            q[0] = *reinterpret_cast<const uint32_t *>(cell + L::k_word(pos, g, b));
-        }
+    __half ks[HEADS], vs[HEADS];
+    uint2 k[HEADS];
+    uint16_t v[HEADS][2][BITS / 4];                         // the values' halves of words of g = 2 c and 2 c + 1
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (BITS == 8) {
-                const uint32_t lo = *reinterpret_cast<const uint16_t *>(cell + L::v_word(pos / 2, 2 * g + i, 2 * b) + 2 * odd);
-                const uint32_t hi = *reinterpret_cast<const uint16_t *>(cell + L::v_word(pos / 2, 2 * g + i, 2 * b + 1) + 2 * odd);
-                j[i] = lo | (hi << 16);
-            } else {
-                const uint32_t n = *reinterpret_cast<const uint16_t *>(cell + L::v_word(pos / 2, 2 * g + i, b) + 2 * odd);
-                j[i] = (n & 0xfu) | ((n & 0xf0u) << 4) | ((n & 0xf00u) << 8) | ((n & 0xf000u) << 12);
-            }
+    for (int h = 0; h < HEADS; ++h) {
+        k[h] = make_uint2(0, 0);
+        ks[h] = vs[h] = __ushort_as_half(0);
+#pragma unroll
+        for (int i = 0; i < BITS / 2; ++i) v[h][i / (BITS / 4)][i % (BITS / 4)] = 0;
+        if (cell && h < heads) {
+            const uint8_t *from = cell + h * a.c.head_bytes;
+            ks[h] = *reinterpret_cast<const __half *>(from + L::k_scale(pos, b));
+            vs[h] = *reinterpret_cast<const __half *>(from + L::v_scale(pos, b));
+            if (BITS == 8) k[h] = *reinterpret_cast<const uint2 *>(from + L::k_word(pos, g, 2 * b));
+            else k[h].x = *reinterpret_cast<const uint32_t *>(from + L::k_word(pos, g, b));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int n = 0; n < BITS / 4; ++n)
+                    v[h][i][n] = *reinterpret_cast<const uint16_t *>(from + L::v_word(pos / 2, 2 * g + i, BITS / 4 * b + n) + 2 * odd);
         }
-    }
-    if (BITS == 4) {                                        // nibbles e0 e2 e4 e6 e1 e3 e5 e7 -> bytes e0..e3, e4..e7
-        const uint32_t n = prmt(q[0], 0, 0x3120);           // bytes: e0 e2 | e1 e3 | e4 e6 | e5 e7
-        const uint32_t lo = n & 0x0f0f0f0fu, hi = (n >> 4) & 0x0f0f0f0fu;
-        q[0] = prmt(lo, hi, 0x5410);                        // lo: e0 e1 e4 e5, hi: e2 e3 e6 e7
-        q[1] = prmt(lo, hi, 0x7632);
     }
     constexpr float kMid = BITS == 8 ? 128.f : 8.f;
-    float w[8];
-    const bool here = ok;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = cell ? ((float)((q[i / 4] >> (8 * (i % 4))) & 0xffu) - kMid) * ks : other;
-    if (here) store8(static_cast<T *>(a.k) + t * a.k_stride + head * D + 8 * at, w);
-    // the transposition of the write, backwards
-    const uint32_t j0 = prmt(j[0], j[1], 0x6240), j1 = prmt(j[0], j[1], 0x7351);    // (j 0: g, g+1; j 2: g, g+1), (j 1; j 3)
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, (g & 1) ? j0 : j1, 1);
-    const uint32_t keep = (g & 1) ? j1 : j0;
-    const uint32_t x0 = (g & 1) ? prmt(got, keep, 0x5410) : prmt(keep, got, 0x5410);
-    const uint32_t x1 = (g & 1) ? prmt(got, keep, 0x7632) : prmt(keep, got, 0x7632);
-    const uint32_t s0 = __shfl_xor_sync(0xffffffffu, (g & 2) ? x0 : x1, 2);
-    q[0] = (g & 2) ? s0 : x0;
-    q[1] = (g & 2) ? x1 : s0;
+    for (int h = 0; h < HEADS; ++h) {
+        uint32_t q[2] = {k[h].x, k[h].y};
+        if (BITS == 4) {                                    // nibbles e0 e2 e4 e6 e1 e3 e5 e7 -> bytes e0..e3, e4..e7
+            const uint32_t n = prmt(q[0], 0, 0x3120);       // bytes: e0 e2 | e1 e3 | e4 e6 | e5 e7
+            const uint32_t lo = n & 0x0f0f0f0fu, hi = (n >> 4) & 0x0f0f0f0fu;
+            q[0] = prmt(lo, hi, 0x5410);                    // lo: e0 e1 e4 e5, hi: e2 e3 e6 e7
+            q[1] = prmt(lo, hi, 0x7632);
+        }
+        float w[8];
+        const float dk = __half2float(ks[h]), dv = __half2float(vs[h]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = cell ? ((float)((q[i / 4] >> (8 * (i % 4))) & 0xffu) - kMid) * vs : other;
-    if (here) store8(static_cast<T *>(a.v) + t * a.v_stride + head * D + 8 * at, w);
+        for (int i = 0; i < 8; ++i) w[i] = cell ? ((float)((q[i / 4] >> (8 * (i % 4))) & 0xffu) - kMid) * dk : other;
+        if (ok && h < heads) store8(static_cast<T *>(a.k) + t * a.k_stride + (head + h) * D + 8 * at, w);
+        uint32_t j[2];                                      // j[i]: bytes j = 0..3 of g = 2 c + i
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t n = v[h][i][0];
+            j[i] = BITS == 8 ? n | (uint32_t)v[h][i][BITS / 4 - 1] << 16
+                             : (n & 0xfu) | ((n & 0xf0u) << 4) | ((n & 0xf00u) << 8) | ((n & 0xf000u) << 12);
+        }
+        // the transposition of the write, backwards
+        const uint32_t j0 = prmt(j[0], j[1], 0x6240), j1 = prmt(j[0], j[1], 0x7351);    // (j 0: g, g+1; j 2: g, g+1), (j 1; j 3)
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, (g & 1) ? j0 : j1, 1);
+        const uint32_t keep = (g & 1) ? j1 : j0;
+        const uint32_t x0 = (g & 1) ? prmt(got, keep, 0x5410) : prmt(keep, got, 0x5410);
+        const uint32_t x1 = (g & 1) ? prmt(got, keep, 0x7632) : prmt(keep, got, 0x7632);
+        const uint32_t s0 = __shfl_xor_sync(0xffffffffu, (g & 2) ? x0 : x1, 2);
+        q[0] = (g & 2) ? s0 : x0;
+        q[1] = (g & 2) ? x1 : s0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = cell ? ((float)((q[i / 4] >> (8 * (i % 4))) & 0xffu) - kMid) * dv : other;
+        if (ok && h < heads) store8(static_cast<T *>(a.v) + t * a.v_stride + (head + h) * D + 8 * at, w);
+    }
 }
 
-template <class T, int BITS, int D>
+template <class T, int BITS, int D, int HEADS>
 hq_status launch_rows(bool write, const RowsArgs &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.c.n_tokens + Rows<D>::BLOCK - 1) / Rows<D>::BLOCK), (unsigned)a.c.n_kv_heads);
+    cfg.gridDim = dim3((unsigned)((a.c.n_tokens + Rows<D>::BLOCK - 1) / Rows<D>::BLOCK), (unsigned)((a.c.n_kv_heads + HEADS - 1) / HEADS));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -245,17 +278,24 @@ hq_status launch_rows(bool write, const RowsArgs &a, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, write ? cache_write_kernel<T, BITS, D> : cache_read_kernel<T, BITS, D>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, write ? cache_write_kernel<T, BITS, D, HEADS> : cache_read_kernel<T, BITS, D, HEADS>, a);
     if (e != cudaSuccess) return set_error(HQ_ERR_LAUNCH, "cache %s launch: %s", write ? "write" : "read", cudaGetErrorString(e));
     note_launch();
     return HQ_OK;
 }
 
+// Four heads a block where that leaves blocks for every multiprocessor; few rows spread over more blocks.
+template <class T, int BITS, int D>
+hq_status launch_heads(bool write, const RowsArgs &a, cudaStream_t stream) {
+    const long long blocks = (a.c.n_tokens + Rows<D>::BLOCK - 1) / Rows<D>::BLOCK * a.c.n_kv_heads;
+    return blocks > 4 * kFewBlocks ? launch_rows<T, BITS, D, 4>(write, a, stream) : launch_rows<T, BITS, D, 1>(write, a, stream);
+}
+
 template <class T, int BITS>
 hq_status launch_dim(bool write, int dim, const RowsArgs &a, cudaStream_t stream) {
-    if (dim == 64) return launch_rows<T, BITS, 64>(write, a, stream);
-    if (dim == 128) return launch_rows<T, BITS, 128>(write, a, stream);
-    return launch_rows<T, BITS, 256>(write, a, stream);
+    if (dim == 64) return launch_heads<T, BITS, 64>(write, a, stream);
+    if (dim == 128) return launch_heads<T, BITS, 128>(write, a, stream);
+    return launch_heads<T, BITS, 256>(write, a, stream);
 }
 
 template <class T>
