@@ -719,7 +719,7 @@ hq_status run_stream(AttnArgs a, int num_sms, cudaStream_t stream) {
     hq_status st = allow_smem(attention_stream_kernel<WIDE, BITS, D, NT>, S::SMEM, done);
     if (st != HQ_OK) return st;
     static_assert(kUnit == 1 << 6, "unit_shift");
-    deal_rows(a, S::ROWS, D, 6, num_sms * S::MIN_BLOCKS);
+    deal_rows(a, S::ROWS, D, 6, std::min(kStreamBlocks, num_sms * S::MIN_BLOCKS));
     st = launch_blocks(attention_stream_kernel<WIDE, BITS, D, NT>, dim3((unsigned)a.blocks), kThreads, S::SMEM, stream, "attention", a);
     return st != HQ_OK ? st : run_combine<WIDE, D>(a, S::ROWS, stream);
 }
@@ -756,8 +756,8 @@ hq_status run_attention_combine(const AttnArgs &a, int rows, int dim, cudaStream
 }
 
 int64_t attention_workspace(const AttentionArgs &x) {
-    const int64_t rows = on_tiles(x) ? 128 : stream_rows(x);
-    return 2ll * kMaxBlocks * rows * (x.cache.head_dim + 2) * 4 + kMaxBlocks * (int64_t)sizeof(Join);
+    const int64_t rows = on_tiles(x) ? 128 : stream_rows(x), blocks = on_tiles(x) ? kTileBlocks : kStreamBlocks;
+    return 2 * blocks * rows * (x.cache.head_dim + 2) * 4 + blocks * (int64_t)sizeof(Join);
 }
 
 hq_status launch_attention(const AttentionArgs &x, cudaStream_t stream) {

@@ -306,7 +306,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ host side
 
-constexpr int kMaxBlocks = 608;                             // of an attention kernel: the workspace holds two partial results of each
+constexpr int kStreamBlocks = 608, kTileBlocks = 304;       // at most: the workspace holds two partial results of each
 
 // Allows a kernel its shared memory, once a device.
 template <class K>
@@ -348,7 +348,7 @@ inline void deal_rows(AttnArgs &a, int rows, int dim, int unit_shift, int blocks
     const long long tiles = std::min(a.c.n_tokens, a.c.n_tokens / a.tokens + a.c.n_req);
     a.most_units = ((a.c.table_width << a.c.page_shift) + (1 << unit_shift) - 1) >> unit_shift;
     const double most = (double)tiles * a.c.n_kv_heads * a.parts * a.most_units;
-    a.blocks = std::min(kMaxBlocks, blocks);
+    a.blocks = blocks;
     if (most < a.blocks) a.blocks = (int)most;
     a.min_units = 1;
     a.stat = reinterpret_cast<float2 *>(a.partial + 2ll * a.blocks * rows * dim);

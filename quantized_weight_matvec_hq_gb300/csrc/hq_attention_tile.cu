@@ -733,7 +733,7 @@ hq_status run(AttnArgs a, int num_sms, cudaStream_t stream) {
     static std::atomic<bool> done[64];
     hq_status st = allow_smem(attention_tile_kernel<BITS, D>, T::SMEM, done);
     if (st != HQ_OK) return st;
-    deal_rows(a, kRows, D, 7, num_sms * T::MIN_BLOCKS);
+    deal_rows(a, kRows, D, 7, std::min(kTileBlocks, num_sms * T::MIN_BLOCKS));
     st = launch_blocks(attention_tile_kernel<BITS, D>, dim3((unsigned)a.blocks), kThreads, T::SMEM, stream, "attention", a);
     return st != HQ_OK ? st : run_attention_combine(a, kRows, D, stream);
 }

@@ -121,7 +121,7 @@ struct Raw8 {
 
 // A warp's rows, of HEADS heads: what finding them costs is paid once, and the heads' loads are under way together.
 template <class T, int BITS, int D, int HEADS>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 4 : 2)) cache_write_kernel(const __grid_constant__ RowsArgs a) {
     using L = CellLayout<BITS, D>;
     griddep_launch_dependents();
     griddep_wait();
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
 }
 
 template <class T, int BITS, int D, int HEADS>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 4 : 2)) cache_read_kernel(const __grid_constant__ RowsArgs a) {
     using L = CellLayout<BITS, D>;
     griddep_launch_dependents();
     griddep_wait();
