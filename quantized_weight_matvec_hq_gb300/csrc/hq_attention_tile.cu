@@ -2,18 +2,17 @@
 // query rows a key/value head (prompts, wide groups of verified drafts), 16-bit
 // tokens, on the tensor cores.
 //
-// A tile is 128 query rows (tokens with their group's heads), a unit 64 positions.  Per unit, with the shared memory of a block
-// holding one tile of Q, and K and V^T of two units as 16-bit floats:
-//   4 + 4 warps      the stored bytes, from global memory to registers, become K [64 positions][D] and V^T [D][64 positions]
-//   1 thread         S = Q K^T and O += P V, tcgen05.mma with accumulators in tensor memory (P is an operand there, in place of S);
-//                    the next unit's scores are computed while this one's weights are
+// A tile is 128 query rows (tokens with their group's heads), a unit 128 positions.  Per unit, with the shared memory of a block
+// holding one tile of Q, K and V^T as 16-bit floats:
+//   4 + 4 warps      the stored bytes, from global memory to registers, become K [128 positions][D] and V^T [D][128 positions]
+//   1 thread         S = Q K^T and O += P V, tcgen05.mma with accumulators in tensor memory (P is an operand there)
 //   4 softmax warps  a thread a row: maxima, weights into tensor memory, rescaling of O where the maximum has risen
 //   1 walker warp    finds the parts and the addresses of their cells, and asks for them ahead into L2
 // Two blocks a multiprocessor (D 256: one) fill each other's gaps.
 //
-// Ranges.  Q rows are scaled as in the kernel for few rows.  K and V^T of 16 neighbouring positions (a cell) are scaled by
+// Ranges.  Q rows are scaled as in the kernel for few rows.  K and V^T of 32 neighbouring positions are scaled by
 // the power of two that takes their largest scale to the top of what 16 bits hold (2^-6 or 2^-2 for the largest element), so an element
-// is rounded to 11 bits or 2^-19 of the largest near it.  Scores of those 16 columns get K's power back in fp32; V's joins
+// is rounded to 11 bits or 2^-19 of the largest near it.  Scores of those 32 columns get K's power back in fp32; V's joins
 // the exponent of the weights, whose reference is thus the largest weight times value, and the sum of the weights leaves it out.
 #include <algorithm>
 #include <atomic>
@@ -24,12 +23,11 @@
 namespace hq {
 namespace {
 
-constexpr int kRows = 128, kUnit = 64, kCells = kUnit / kCell;
+constexpr int kRows = 128, kUnit = 128, kCells = kUnit / kCell;
 constexpr int kSoftmax = 4, kDecode = 4;                    // warps: softmax, then of keys, of values
 constexpr int kValues = kSoftmax + kDecode, kWalker = kValues + kDecode, kProducts = kWalker + 1;
 constexpr int kThreads = 32 * (kProducts + 1);
-constexpr int kSlots = 8;                                   // units whose addresses are known ahead
-constexpr int kKept = 4;                                    // units whose exponents and marks are kept
+constexpr int kSlots = 4;                                   // units whose addresses are known ahead
 constexpr float kSlack = 8.f, kWeight = 6.f;                // weights up to 2^(slack + weight); 2^weight at the reference
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
@@ -64,6 +62,14 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
           "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(addr) : "memory");
+}
 // 16 columns' pairs of 16-bit floats.
 __device__ __forceinline__ void tmem_st8u(uint32_t addr, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
@@ -91,25 +97,23 @@ struct Tile {
     using L = CellLayout<BITS, D>;
     static constexpr int NB = L::NB;
     static constexpr int MIN_BLOCKS = D == 256 ? 1 : 2;
-    static constexpr uint32_t TMEM = D == 256 ? 512 : 256;  // columns: scores (and in their place weights) of two units, outputs from 128
-    static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = kUnit * D * 2, V_BYTES = kUnit * D * 2;         // of one unit
+    static constexpr uint32_t TMEM = D == 256 ? 512 : 256;  // columns: scores (and in their place weights) 0..127, outputs from 128
+    static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = kUnit * D * 2, V_BYTES = kUnit * D * 2;
     struct Shared {
         WalkShared walk;
         Part part[2];
         uint64_t part_full[2], part_empty[2], cell_full[kSlots], cell_empty[kSlots];
-        // unit n's barriers are those of n % 2: their next phase is unit n + 2's, which no wait for unit n can miss
-        uint64_t q_full, k_full[2], v_full[2], s_full[2], p_full[2], pv_done[2], drained;
+        uint64_t q_full, k_full, v_full, s_full, p_full, pv_done;
         uint64_t cell[kSlots][kCells];                      // addresses; 0: no position that is seen, 1: page out of range
         float factor[kRows];
-        // of a unit's cells: keys are the tile's times k_power, values times 2^v_exp; v_back = 2^-v_exp
-        alignas(16) float k_power[kKept][kDecode], v_exp[kKept][kDecode], v_back[kKept][kDecode];
-        uint32_t any_bad[kKept][kDecode];                   // some value block of the cell is no number
-        uint8_t bad[kKept][kUnit];                          // then: of each position, bit b: block b
+        int k_exp[2][kDecode], v_exp[2][kDecode];           // of 32 positions: the stored value is the tile's times 2^exp
+        uint32_t any_bad[2][kDecode];                       // some value block of the 32 positions is no number
+        uint8_t bad[2][kUnit];                              // then: of each position, bit b: block b
         uint32_t tmem;
         int abort;
     };
     static constexpr int FIXED = ((int)sizeof(Shared) + 1023) / 1024 * 1024;
-    static constexpr int SMEM = FIXED + Q_BYTES + 2 * K_BYTES + 2 * V_BYTES;
+    static constexpr int SMEM = FIXED + Q_BYTES + K_BYTES + V_BYTES;
     static_assert(SMEM <= (228 / MIN_BLOCKS - 1) * 1024, "shared memory");
 };
 
@@ -191,10 +195,11 @@ template <int BITS, int D>
 struct Cells {
     typename Tile<BITS, D>::Shared &s;
     uint32_t at;                                            // slot, and below it the phase of its barrier
-    __device__ __forceinline__ bool next(const AttnArgs &a, int w, uint64_t &cell) {
+    __device__ __forceinline__ bool next(const AttnArgs &a, int w, uint64_t (&cell)[2]) {
         const uint32_t slot = at >> 1;
         if (!tc_wait(smem_u32(&s.cell_full[slot]), at & 1, &s.abort, a.c.fault)) return false;
-        cell = s.cell[slot][w];
+        cell[0] = s.cell[slot][2 * w];
+        cell[1] = s.cell[slot][2 * w + 1];
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&s.cell_empty[slot]));
         at = slot == kSlots - 1 ? (at & 1) ^ 1 : at + 2;
@@ -202,73 +207,46 @@ struct Cells {
     }
 };
 
-// Whether unit m's phase of one of its barriers is over (units below 0: at once).
-__device__ __forceinline__ bool unit_wait(const uint64_t (&bar)[2], int m, const AttnArgs &a, volatile int *abort) {
-    return m < 0 || tc_wait(smem_u32(&bar[m & 1]), (uint32_t)(m >> 1) & 1, abort, a.c.fault);
-}
-
-// The largest exponent field of a cell's scales `t` (KEYS: [16][NB], else [8 pairs][NB][2]), of those that are numbers and whose position is in
-// [lo, hi) from the cell's first one; `odd`: some that is seen is no number.
-template <int NB, bool KEYS, int SCALES>
-__device__ __forceinline__ int top_exponent(const uint32_t (&t)[SCALES], int lo, int hi, bool &odd) {
-    const int lane = threadIdx.x & 31;
-    uint32_t top = 0;
-    odd = false;
-#pragma unroll
-    for (int k = 0; k < SCALES; ++k) {
-        const int i = (lane * SCALES + k) % (8 * NB);       // the word: two blocks of a key, or two positions' values
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int p = KEYS ? i / (NB / 2) : 2 * (i / NB) + h;
-            const uint32_t x = t[k] >> (16 * h) & 0x7fffu;
-            if (p >= lo && p < hi) {
-                if (x < 0x7c00u) top = max(top, x); else odd = true;
-            }
-        }
-    }
-    odd = __any_sync(0xffffffffu, odd);
-    return (int)(__reduce_max_sync(0xffffffffu, top) >> 10);
-}
-
-template <int BITS>
-constexpr int kTo = BITS == 4 ? 25 : 29;                    // scales go to [2^10, 2^11) or [2^14, 2^15)
-
-// A key warp has 16 positions of a unit: a cell.  Four neighbouring lanes have a row; rows x and x ^ 5 lie side by
+// A key warp has 32 positions of a unit: two cells.  Four neighbouring lanes have a row; rows x and x ^ 5 lie side by
 // side, so that the stores do not meet in a bank.  The next unit's bytes are asked for while this one's products run.
 template <int BITS, int D>
-__device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t k_tiles) {
+__device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t k_tile) {
     using T = Tile<BITS, D>;
     using L = typename T::L;
-    constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS;        // words of a block, blocks of a unit of the layout
-    constexpr int SCALES = NB < 4 ? 1 : NB / 4;             // words of a lane's share of the scales
+    constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS;        // words of a block, blocks of a unit
+    constexpr int SCALES = NB / 2;                          // words of a lane's share of the scales: 16 lanes a cell
+    constexpr int TO = BITS == 4 ? 25 : 29;                 // scales go to [2^10, 2^11) or [2^14, 2^15)
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftmax;
     const int c = lane & 3, kr = (lane >> 3) ^ (lane & 4 ? 5 : 0);
     volatile int *abort = &s.abort;
     Cells<BITS, D> cells = {s, 0};
-    int n = 0;                                              // units so far
-    uint64_t cell = 0;
-    uint32_t raw[2][L::UW], ks[2][NB / 2], t[SCALES];
+    uint32_t n = 0;                                         // units so far
+    uint64_t cell[2];
+    uint32_t raw[4][L::UW], ks[4][NB / 2], tk[SCALES];
     auto load_unit = [&](int u) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {                       // rows 8 i + kr
+        for (int i = 0; i < 4; ++i) {                       // rows 8 i + kr
+            const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[i >> 1]);
+            if (cell[i >> 1] > 1) load_global<L::UW>(p + L::k_word(8 * (i & 1) + kr, c, u * L::UW), raw[i]);
+            else
 #pragma unroll
-            for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
-            if (cell > 1) load_global<L::UW>(reinterpret_cast<const uint8_t *>(cell) + L::k_word(8 * i + kr, c, u * L::UW), raw[i]);
+                for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
         }
     };
     auto load = [&]() {
         load_unit(0);
-        const uint8_t *p = reinterpret_cast<const uint8_t *>(cell);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            if (cell[i >> 1] > 1) load_global<NB / 2>(reinterpret_cast<const uint8_t *>(cell[i >> 1]) + L::k_scale(8 * (i & 1) + kr, 0), ks[i]);
+            else
 #pragma unroll
-            for (int k = 0; k < NB / 2; ++k) ks[i][k] = cell ? 0x7fff7fffu : 0u;    // a page out of range: NaN
-            if (cell > 1) load_global<NB / 2>(p + L::k_scale(8 * i + kr, 0), ks[i]);
+                for (int k = 0; k < NB / 2; ++k) ks[i][k] = cell[i >> 1] ? 0x7fff7fffu : 0u;        // a page out of range: NaN
         }
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[lane >> 4]);
 #pragma unroll
         for (int k = 0; k < SCALES; ++k) {
-            t[k] = 0;
-            if (cell > 1) load_global<1>(p + L::KS + 4 * ((lane * SCALES + k) % (8 * NB)), &t[k]);
+            tk[k] = 0;
+            if (cell[lane >> 4] > 1) load_global<1>(p + L::KS + 4 * ((lane & 15) * SCALES + k), &tk[k]);
         }
     };
     for (int part_n = 0;; ++part_n) {
@@ -278,20 +256,28 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
         if (!cells.next(a, w, cell)) return;
         load();
         for (int u = 0; u < s.part[at].take; ++u, ++n) {
-            const int p0 = s.part[at].begin + u * kUnit + kCell * w;        // of this warp's positions
-            bool odd;
-            const int e = top_exponent<NB, true, SCALES>(t, s.part[at].span.lo - p0, s.part[at].span.hi - p0, odd);
-            if (!unit_wait(s.s_full, n - 2, a, abort)) return;              // the tile is free
-            if (lane == 0) s.k_power[n % kKept][w] = power(e - 5);
-            const uint32_t k_tile = k_tiles + (n & 1) * T::K_BYTES;
-            const int x = kTo<BITS> - e, x1 = min(x, 15);
+            const int p0 = s.part[at].begin + u * kUnit + 32 * w;           // of this warp's positions
+            const int lo = s.part[at].span.lo, hi = s.part[at].span.hi;
+            uint32_t top = 0;                               // of what is a number and seen by some row
+#pragma unroll
+            for (int k = 0; k < SCALES; ++k) {
+                const int p = p0 + kCell * (lane >> 4) + ((lane & 15) * SCALES + k) / (NB / 2);
+                if (p >= lo && p < hi) {
+                    const uint32_t x = tk[k] & 0x7fffu, y = tk[k] >> 16 & 0x7fffu;
+                    top = max(top, max(x < 0x7c00u ? x : 0u, y < 0x7c00u ? y : 0u));
+                }
+            }
+            const int e = (int)(__reduce_max_sync(0xffffffffu, top) >> 10);
+            if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;      // the tile is free
+            if (lane == 0) s.k_exp[n & 1][w] = e - 5;
+            const int x = TO - e, x1 = min(x, 15);
             const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
 #pragma unroll
             for (int v = 0; v < L::UNITS; ++v) {
                 if (v > 0) load_unit(v);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = kCell * w + 8 * i + kr;
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 32 * w + 8 * i + kr;
 #pragma unroll
                     for (int k = 0; k < BLOCKS; ++k) {
                         const int b = v * BLOCKS + k;
@@ -307,8 +293,8 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(smem_u32(&s.k_full[n & 1]));
-                mbar_arrive(smem_u32(&s.s_full[n & 1]));    // (the softmax warps read the power)
+                mbar_arrive(smem_u32(&s.k_full));
+                mbar_arrive(smem_u32(&s.s_full));           // (the softmax warps read the exponents)
             }
             if (u + 1 < s.part[at].take) {
                 if (!cells.next(a, w, cell)) return;
@@ -320,43 +306,48 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
     }
 }
 
-// A value warp has a cell of a unit.  A lane turns eight positions' elements g, 8 + g, .. of half the blocks into rows of V^T: 16 bytes
+// A value warp has 32 positions of a unit.  A lane turns eight positions' elements g, 8 + g, .. into rows of V^T: 16 bytes
 // each, the rows of eight neighbouring lanes in different banks.
 template <int BITS, int D>
-__device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t v_tiles) {
+__device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t v_tile) {
     using T = Tile<BITS, D>;
     using L = typename T::L;
-    constexpr int NB = T::NB, WB = BITS / 4;
-    constexpr int LW = L::LANE / 8;                         // words of a lane's half of the blocks, STEP of them at a time
-    constexpr int STEP = LW < 4 ? LW : 4, BLOCKS = STEP / WB;
-    constexpr int SCALES = NB < 4 ? 1 : NB / 4;
+    constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS, TWO = BLOCKS < 2 ? BLOCKS : 2;     // scales in registers: of TWO blocks
+    constexpr int SCALES = NB / 2;
+    constexpr int TO = BITS == 4 ? 25 : 29;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kValues;
-    const int g = lane & 7, eight = lane >> 3 & 1, half = lane >> 4;
+    const int q = lane >> 3, g = lane & 7;                  // eight positions from 8 q, elements g of each eight
     volatile int *abort = &s.abort;
     Cells<BITS, D> cells = {s, 0};
-    int n = 0;
-    uint64_t cell = 0;
-    uint32_t raw[4][STEP], vs[4][BLOCKS], t[SCALES];
-    auto load_step = [&](int st) {
-        const uint8_t *p = reinterpret_cast<const uint8_t *>(cell);
+    uint32_t n = 0;
+    uint64_t cell[2];
+    uint32_t raw[4][L::UW], vs[4][TWO], tv[SCALES];
+    auto load_scales = [&](int b) {
+        const uint64_t from = cell[q >> 1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {                       // pairs 4 eight + i
+        for (int i = 0; i < 4; ++i) {                       // pairs 4 (q % 2) + i
 #pragma unroll
-            for (int k = 0; k < STEP; ++k) raw[i][k] = 0;
-#pragma unroll
-            for (int k = 0; k < BLOCKS; ++k) vs[i][k] = 0;
-            if (cell > 1) {
-                load_global<STEP>(p + L::v_word(4 * eight + i, g, half * LW + st * STEP), raw[i]);
-                load_global<BLOCKS>(p + L::v_scale(8 * eight + 2 * i, half * (NB / 2) + st * BLOCKS), vs[i]);
-            }
+            for (int k = 0; k < TWO; ++k) vs[i][k] = 0;
+            if (from > 1) load_global<TWO>(reinterpret_cast<const uint8_t *>(from) + L::v_scale(8 * (q & 1) + 2 * i, b), vs[i]);
         }
     };
+    auto load_unit = [&](int u) {
+        const uint64_t from = cell[q >> 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
+            if (from > 1) load_global<L::UW>(reinterpret_cast<const uint8_t *>(from) + L::v_word(4 * (q & 1) + i, g, u * L::UW), raw[i]);
+        }
+        load_scales(u * BLOCKS);
+    };
     auto load = [&]() {
-        load_step(0);
+        load_unit(0);
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[lane >> 4]);
 #pragma unroll
         for (int k = 0; k < SCALES; ++k) {
-            t[k] = 0;
-            if (cell > 1) load_global<1>(reinterpret_cast<const uint8_t *>(cell) + L::VS + 4 * ((lane * SCALES + k) % (8 * NB)), &t[k]);
+            tv[k] = 0;
+            if (cell[lane >> 4] > 1) load_global<1>(p + L::VS + 4 * ((lane & 15) * SCALES + k), &tv[k]);
         }
     };
     for (int part_n = 0;; ++part_n) {
@@ -366,69 +357,83 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
         if (!cells.next(a, w, cell)) return;
         load();
         for (int u = 0; u < s.part[at].take; ++u, ++n) {
-            const int p0 = s.part[at].begin + u * kUnit + kCell * w;
-            const int lo = s.part[at].span.lo - p0, hi = s.part[at].span.hi - p0;   // the cell's positions that some row sees
-            const int kept = n % kKept;
-            bool odd;                                       // a block that is no number
-            const int e = top_exponent<NB, false, SCALES>(t, lo, hi, odd);
-            if (!unit_wait(s.s_full, n - 2, a, abort)) return;
-            if (lane == 0) {
-                s.v_exp[kept][w] = (float)(e - 5);
-                s.v_back[kept][w] = power(5 - e);
-                mbar_arrive(smem_u32(&s.s_full[n & 1]));    // (the softmax warps read them)
-            }
-            if (!unit_wait(s.pv_done, n - 2, a, abort)) return;             // the tile is free
-            if (lane == 0) s.any_bad[kept][w] = odd;
-            if (odd && lane < kCell) {                      // a lane a position: marks of its blocks
-                uint32_t marks = 0;
-#pragma unroll 1
-                for (int b = 0; b < NB && cell > 1 && lane >= lo && lane < hi; ++b) {
-                    const uint16_t d = *reinterpret_cast<const uint16_t *>(reinterpret_cast<const uint8_t *>(cell) + L::v_scale(lane, b));
-                    if ((d & 0x7c00u) == 0x7c00u) marks |= 1u << b;
-                }
-                s.bad[kept][kCell * w + lane] = (uint8_t)marks;
-            }
-            const uint32_t v_tile = v_tiles + (n & 1) * T::V_BYTES;
-            const int x = kTo<BITS> - e, x1 = min(x, 15);
-            const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
-            const bool edge = lo > 0 || hi < kCell;
+            const int p0 = s.part[at].begin + u * kUnit + 32 * w;
+            const int lo = s.part[at].span.lo, hi = s.part[at].span.hi, par = n & 1;
+            const bool edge = p0 < lo || p0 + 32 > hi;
+            uint32_t top = 0;
+            bool odd = false;                               // a block that is no number
 #pragma unroll
-            for (int st = 0; st < LW / STEP; ++st) {
-                if (st > 0) load_step(st);
-                if (edge) {                                 // positions that no row sees are zeros
+            for (int k = 0; k < SCALES; ++k) {
+                const int p = p0 + kCell * (lane >> 4) + 2 * (((lane & 15) * SCALES + k) / NB);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int p = 8 * eight + 2 * i;
-                        const uint32_t keep = (p >= lo && p < hi ? 0xffffu : 0u) | (p + 1 >= lo && p + 1 < hi ? 0xffff0000u : 0u);
-#pragma unroll
-                        for (int k = 0; k < BLOCKS; ++k) vs[i][k] &= keep;
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = tv[k] >> (16 * h) & 0x7fffu;
+                    if (p + h >= lo && p + h < hi) {
+                        if (x < 0x7c00u) top = max(top, x); else odd = true;
                     }
                 }
-                if (odd) {                                  // blocks that are no numbers leave the product
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int k = 0; k < BLOCKS; ++k) vs[i][k] &= ~__vcmpeq2(vs[i][k] & 0x7c007c00u, 0x7c007c00u);
+            }
+            const int e = (int)(__reduce_max_sync(0xffffffffu, top) >> 10);
+            odd = __any_sync(0xffffffffu, odd);
+            if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;
+            if (lane == 0) {
+                s.v_exp[par][w] = e - 5;
+                mbar_arrive(smem_u32(&s.s_full));           // (the softmax warps read the exponents)
+            }
+            if (n > 0 && !tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault)) return;     // the tile is free
+            if (lane == 0) s.any_bad[par][w] = odd;         // (the softmax warps are done with those of two units before)
+            if (odd) {                                      // a lane a position: marks of its blocks
+                uint32_t marks = 0;
+                const uint64_t from = cell[lane >> 4];
+#pragma unroll 1
+                for (int b = 0; b < NB && from > 1 && p0 + lane >= lo && p0 + lane < hi; ++b) {
+                    const uint16_t d = *reinterpret_cast<const uint16_t *>(reinterpret_cast<const uint8_t *>(from) + L::v_scale(lane & 15, b));
+                    if ((d & 0x7c00u) == 0x7c00u) marks |= 1u << b;
                 }
+                s.bad[par][32 * w + lane] = (uint8_t)marks;
+            }
+            const int x = TO - e, x1 = min(x, 15);
+            const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
+#pragma unroll 1
+            for (int v = 0; v < L::UNITS; ++v) {
+                if (v > 0) load_unit(v);
 #pragma unroll
                 for (int k = 0; k < BLOCKS; ++k) {
+                    if (k > 0 && k % TWO == 0) load_scales(v * BLOCKS + k);
+                    if (k % TWO == 0) {
+                        if (edge) {                         // positions that no row sees are zeros
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int p = p0 + 8 * q + 2 * i;
+                                const uint32_t keep = (p >= lo && p < hi ? 0xffffu : 0u) | (p + 1 >= lo && p + 1 < hi ? 0xffff0000u : 0u);
+#pragma unroll
+                                for (int j = 0; j < TWO; ++j) vs[i][j] &= keep;
+                            }
+                        }
+                        if (odd) {                          // blocks that are no numbers leave the product
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int j = 0; j < TWO; ++j) vs[i][j] &= ~__vcmpeq2(vs[i][j] & 0x7c007c00u, 0x7c007c00u);
+                        }
+                    }
                     uint32_t h[4][4];                       // [pair][j]
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         raw_pairs<BITS, 0x4240, 0x4341>(&raw[i][k * WB], h[i]);
-                        scaled_pairs<BITS>(h[i], __hmul2(__hmul2(bits_h2(vs[i][k]), up1), up2));
+                        scaled_pairs<BITS>(h[i], __hmul2(__hmul2(bits_h2(vs[i][k % TWO]), up1), up2));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int row = 32 * (half * (NB / 2) + st * BLOCKS + k) + 8 * j + g;
-                        const uint32_t to = v_tile + row * 128 + (((2 * w + eight) ^ g) << 4);
+                        const int row = 32 * (v * BLOCKS + k) + 8 * j + g;
+                        const uint32_t to = v_tile + (w >> 1) * (D * 128) + row * 128 + (((4 * (w & 1) + q) ^ g) << 4);
                         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0][j]), "r"(h[1][j]), "r"(h[2][j]), "r"(h[3][j]) : "memory");
                     }
                 }
             }
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s.v_full[n & 1]));
+            if (lane == 0) mbar_arrive(smem_u32(&s.v_full));
             if (u + 1 < s.part[at].take) {
                 if (!cells.next(a, w, cell)) return;
                 load();
@@ -442,45 +447,42 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
 // ------------------------------------------------------------------ products
 
 template <int BITS, int D>
-__device__ __forceinline__ void products(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t q_tile, uint32_t k_tiles,
-                                         uint32_t v_tiles, uint32_t tmem) {
-    using T = Tile<BITS, D>;
+__device__ __forceinline__ void products(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t q_tile, uint32_t k_tile,
+                                         uint32_t v_tile, uint32_t tmem) {
     volatile int *abort = &s.abort;
-    const uint32_t qk = tc_idesc(kUnit, false), pv = tc_idesc(D, false), outputs = tmem + 128;
-    int n = 0;
-    // S of unit m, whose place is free once the outputs of the unit two before have been added
-    auto scores = [&](int m) -> bool {
-        if (!unit_wait(s.k_full, m, a, abort) || !unit_wait(s.pv_done, m - 2, a, abort)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-            tc_mma_ss(tmem + (m & 1) * kUnit, tc_desc_sw128(q_tile + k / 4 * (kRows * 128) + k % 4 * 32),
-                      tc_desc_sw128(k_tiles + (m & 1) * T::K_BYTES + k / 4 * (kUnit * 128) + k % 4 * 32), qk, k > 0);
-        tc_commit(smem_u32(&s.s_full[m & 1]));
-        return true;
-    };
+    const uint32_t qk = tc_idesc(kUnit, false), pv = tc_idesc(D, false);
+    const uint32_t scores = tmem, outputs = tmem + 128;
+    uint32_t n = 0;
     bool fine = true;
     for (uint32_t part_n = 0; fine; ++part_n) {
         const int at = part_n & 1;
         if (!tc_wait(smem_u32(&s.part_full[at]), part_n >> 1 & 1, abort, a.c.fault)) break;
         const int take = s.part[at].take;
         if (take == 0) break;
-        fine = tc_wait(smem_u32(&s.q_full), part_n & 1, abort, a.c.fault) && scores(n);
-        for (int u = 0; fine && u < take; ++u, ++n) {
-            fine = (u + 1 == take || scores(n + 1)) && unit_wait(s.v_full, n, a, abort) && unit_wait(s.p_full, n, a, abort);
-            if (!fine) break;
+        if (!tc_wait(smem_u32(&s.q_full), part_n & 1, abort, a.c.fault)) break;
+        for (int u = 0; u < take; ++u, ++n) {
+            if (!tc_wait(smem_u32(&s.k_full), n & 1, abort, a.c.fault) ||
+                (n > 0 && !tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault))) { fine = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                tc_mma_ss(scores, tc_desc_sw128(q_tile + k / 4 * (kRows * 128) + k % 4 * 32),
+                          tc_desc_sw128(k_tile + k / 4 * (kUnit * 128) + k % 4 * 32), qk, k > 0);
+            tc_commit(smem_u32(&s.s_full));
+            if (!tc_wait(smem_u32(&s.v_full), n & 1, abort, a.c.fault) ||
+                !tc_wait(smem_u32(&s.p_full), n & 1, abort, a.c.fault)) { fine = false; break; }
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < kUnit / 16; ++k)
-                tc_mma(outputs, tmem + (n & 1) * kUnit + 8 * k, tc_desc_sw128(v_tiles + (n & 1) * T::V_BYTES + k * 32), pv, u > 0 || k > 0);
-            tc_commit(smem_u32(&s.pv_done[n & 1]));
+                tc_mma(outputs, scores + 8 * k, tc_desc_sw128(v_tile + k / 4 * (D * 128) + k % 4 * 32), pv, u > 0 || k > 0);
+            tc_commit(smem_u32(&s.pv_done));
         }
         if (fine) mbar_arrive(smem_u32(&s.part_empty[at]));
     }
     if (!fine || *abort) {
         // after a time-out: what was issued ends before the tensor memory is given back
-        tc_commit(smem_u32(&s.drained));
-        for (int k = 0; k < 1000 && !mbar_try_wait_sleep(smem_u32(&s.drained), 0, 20000u); ++k) {}
+        tc_commit(smem_u32(&s.pv_done));
+        for (int k = 0; k < 1000 && !mbar_try_wait_sleep(smem_u32(&s.pv_done), n & 1, 20000u); ++k) {}
     }
 }
 
@@ -491,8 +493,8 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
     constexpr int LANES = D / 8, ROWS = 32 / LANES;         // lanes of a query row's loads, rows at once
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = threadIdx.x;
     volatile int *abort = &s.abort;
-    const uint32_t tmem_row = tmem + ((uint32_t)(32 * warp) << 16), outputs = tmem_row + 128;
-    int n = 0;
+    const uint32_t scores = tmem + ((uint32_t)(32 * warp) << 16), outputs = scores + 128;
+    uint32_t n = 0;
     for (uint32_t part_n = 0;; ++part_n) {
         const int at = part_n & 1;
         if (!tc_wait(smem_u32(&s.part_full[at]), part_n >> 1 & 1, abort, a.c.fault)) return;
@@ -552,51 +554,38 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
         uint32_t bad = 0;
         int p0 = part.begin;
         // value blocks of a unit that are no numbers and that the row sees
-        auto look_at_bad = [&](int unit, int first) {
-            const uint32_t *f = s.any_bad[unit % kKept];
+        auto look_at_bad = [&](uint32_t unit, int first) {
+            const uint32_t *f = s.any_bad[unit & 1];
             if ((f[0] | f[1] | f[2] | f[3]) == 0) return;
             for (int k = 0; k < kUnit; ++k)
-                if (f[k / kCell] && first + k >= see.lo && first + k < see.hi && first + k >= part.span.lo && first + k < part.span.hi)
-                    bad |= s.bad[unit % kKept][k];
+                if (f[k >> 5] && first + k >= see.lo && first + k < see.hi && first + k >= part.span.lo && first + k < part.span.hi)
+                    bad |= s.bad[unit & 1][k];
         };
         for (int u = 0; u < take; ++u, ++n, p0 += kUnit) {
-            if (!unit_wait(s.s_full, n, a, abort)) return;
+            if (!tc_wait(smem_u32(&s.s_full), n & 1, abort, a.c.fault)) return;
             tc_fence_after();
             if (work) {
-                // (of the unit before, the values may still be on their way; the scores of this one waited for those before it)
-                if (u > 1) look_at_bad(n - 2, p0 - 2 * kUnit);
-                const int first = see.lo - p0, last = see.hi - p0;          // columns that the row sees: [first, last)
+                if (u > 0) look_at_bad(n - 1, p0 - kUnit);
+                int first = see.lo - p0, last = see.hi - p0;                // columns that the row sees: [first, last)
                 const bool edge = __any_sync(0xffffffffu, first > 0 || last < kUnit);
-                const float *kp = s.k_power[n % kKept], *ve = s.v_exp[n % kKept], *vb = s.v_back[n % kKept];
-                const uint32_t scores = tmem_row + (n & 1) * kUnit;
-                // (Loops that stay loops, and the hidden columns in a pass of their own: the warps of a multiprocessor run many
-                // different paths, and what they do not find in the instruction caches they wait for.)
-                if (edge) {
-#pragma unroll 1
-                    for (int c = 0; c < kUnit; c += 8) {
-                        float v[8];
-                        tmem_ld8(scores + c, v);
-                        tmem_wait_ld(v);
-                        const uint32_t seen = bits_between(first - c, last - c);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) if (!(seen >> k & 1u)) v[k] = -INFINITY;
-                        tmem_st8(scores + c, v);
-                    }
-                    tmem_wait_st();
-                }
+                const int *ke = s.k_exp[n & 1], *ve = s.v_exp[n & 1];       // of 32 columns
+                // (Loops that stay loops: unrolled, what each 32 columns need would be kept in registers all at once.)
                 float top = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < kUnit / 32; ++c) {
-                    float v[32];
+                for (int c = 0; c < 4; ++c) {
+                    float v[32], m[4];
                     tmem_load32(scores + 32 * c, v);
+                    if (edge) {
+                        const uint32_t seen = bits_between(first - 32 * c, last - 32 * c);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float m[2] = {v[16 * h], v[16 * h + 1]};
-#pragma unroll
-                        for (int k = 2; k < 16; ++k) m[k & 1] = fmaxf(m[k & 1], v[16 * h + k]);
-                        m[0] = fmaxf(m[0], m[1]);
-                        if (m[0] > -INFINITY) top = fmaxf(top, fmaf(m[0], factor * kp[2 * c + h], ve[2 * c + h]));
+                        for (int k = 0; k < 32; ++k) if (!(seen >> k & 1u)) v[k] = -INFINITY;
                     }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m[k] = v[k];
+#pragma unroll
+                    for (int k = 4; k < 32; ++k) m[k & 3] = fmaxf(m[k & 3], v[k]);
+                    m[0] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                    if (m[0] > -INFINITY) top = fmaxf(top, fmaf(m[0], factor * power(ke[c]), (float)ve[c]));
                 }
                 const bool raise = top > ref + kSlack;
                 if (__any_sync(0xffffffffu, raise)) {
@@ -604,56 +593,57 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
                     l *= f;
                     ref = now;
                     if (u > 0) {
-                        if (!unit_wait(s.pv_done, n - 1, a, abort)) return;                        // what is being added
-                        tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 8) {
-                            float y[8];
-                            tmem_ld8(outputs + c, y);
-                            tmem_wait_ld(y);
+                        for (int c = 0; c < D; c += 16) {
+                            float y[16];
+                            tmem_load16(outputs + c, y);
+                            uint32_t z[16];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) y[k] *= f;
-                            tmem_st8(outputs + c, y);
+                            for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(y[k] * f);
+                            tmem_st16(outputs + c, z);
                         }
                     }
                 }
                 const float base = kWeight - fmaxf(ref, -3e38f);            // nothing seen yet: all columns are hidden
                 // weights into tensor memory, in place of scores that are in registers by then
 #pragma unroll 1
-                for (int c = 0; c < kUnit / 32; ++c) {
+                for (int c = 0; c < 4; ++c) {
+                    const float fk = factor * power(ke[c]), b = base + (float)ve[c];
+                    const float2 f2 = make_float2(fk, fk), b2 = make_float2(b, b);
                     float v[32];
                     tmem_load32(scores + 32 * c, v);
+                    const uint32_t seen = edge ? bits_between(first - 32 * c, last - 32 * c) : 0xffffffffu;
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float fk = factor * kp[2 * c + h];
-                        if (fk == 0.f) fk = 1e-37f;                         // a hidden column's -inf stays one
-                        const float b = base + ve[2 * c + h];
-                        const float2 f2 = make_float2(fk, fk), b2 = make_float2(b, b);
-                        float2 sum = make_float2(0.f, 0.f);
                         uint32_t x[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const int at = 16 * h + 2 * k;
                             float2 z = ffma2(make_float2(v[at], v[at + 1]), f2, b2);
+                            if (edge) {
+                                if (!(seen >> at & 1u)) z.x = -INFINITY;
+                                if (!(seen >> (at + 1) & 1u)) z.y = -INFINITY;
+                            }
                             z = make_float2(ex2(z.x), ex2(z.y));
-                            sum = fadd2(sum, z);
+                            sum[k & 1] = fadd2(sum[k & 1], z);
                             x[k] = h2_bits(__floats2half2_rn(z.x, z.y));
                         }
                         tmem_st8u(scores + 16 * c + 8 * h, x);
-                        l = fmaf(sum.x + sum.y, vb[2 * c + h], l);
                     }
+                    sum[0] = fadd2(sum[0], sum[1]);
+                    l = fmaf(sum[0].x + sum[0].y, power(-ve[c]), l);
                 }
                 tmem_wait_st();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s.p_full[n & 1]));
+            if (lane == 0) mbar_arrive(smem_u32(&s.p_full));
         }
         // ---- the tile's outputs
-        if (!unit_wait(s.pv_done, n - 1, a, abort)) return;
+        if (!tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault)) return;
         tc_fence_after();
         if (work) {
-            if (take > 1) look_at_bad(n - 2, p0 - 2 * kUnit);
             look_at_bad(n - 1, p0 - kUnit);
             const float f = part.slot >= 0 ? 1.f : l == 0.f ? 0.f : __fdiv_rn(1.f, l);
             const long long r = (long long)part.slot * kRows + me;
@@ -687,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<BITS, D>::MIN_BLOCKS)) attenti
     extern __shared__ __align__(1024) uint8_t memory[];
     typename T::Shared &s = *reinterpret_cast<typename T::Shared *>(memory);
     uint8_t *q_tile = memory + T::FIXED;
-    const uint32_t q = smem_u32(q_tile), k = q + T::Q_BYTES, v = k + 2 * T::K_BYTES;
+    const uint32_t q = smem_u32(q_tile), k = q + T::Q_BYTES, v = k + T::K_BYTES;
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -699,14 +689,11 @@ __global__ void __launch_bounds__(kThreads, (Tile<BITS, D>::MIN_BLOCKS)) attenti
             mbar_init(smem_u32(&s.cell_empty[i]), 2 * kDecode);
         }
         mbar_init(smem_u32(&s.q_full), kSoftmax);
-        mbar_init(smem_u32(&s.drained), 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&s.k_full[i]), kDecode);
-            mbar_init(smem_u32(&s.v_full[i]), kDecode);
-            mbar_init(smem_u32(&s.s_full[i]), 1 + 2 * kDecode);             // the products, and the powers of K and V
-            mbar_init(smem_u32(&s.p_full[i]), kSoftmax);
-            mbar_init(smem_u32(&s.pv_done[i]), 1);
-        }
+        mbar_init(smem_u32(&s.k_full), kDecode);
+        mbar_init(smem_u32(&s.v_full), kDecode);
+        mbar_init(smem_u32(&s.s_full), 1 + 2 * kDecode);         // the products, and the exponents of K and V
+        mbar_init(smem_u32(&s.p_full), kSoftmax);
+        mbar_init(smem_u32(&s.pv_done), 1);
         fence_mbar_init();
         s.abort = 0;
     }
@@ -746,7 +733,7 @@ hq_status run(AttnArgs a, int num_sms, cudaStream_t stream) {
     static std::atomic<bool> done[64];
     hq_status st = allow_smem(attention_tile_kernel<BITS, D>, T::SMEM, done);
     if (st != HQ_OK) return st;
-    deal_rows(a, kRows, D, 6, std::min(kTileBlocks, num_sms * T::MIN_BLOCKS));
+    deal_rows(a, kRows, D, 7, std::min(kTileBlocks, num_sms * T::MIN_BLOCKS));
     st = launch_blocks(attention_tile_kernel<BITS, D>, dim3((unsigned)a.blocks), kThreads, T::SMEM, stream, "attention", a);
     return st != HQ_OK ? st : run_attention_combine(a, kRows, D, stream);
 }
