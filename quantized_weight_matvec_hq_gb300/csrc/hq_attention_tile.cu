@@ -62,14 +62,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
           "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
-          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-        : "r"(addr) : "memory");
-}
 // 16 columns' pairs of 16-bit floats.
 __device__ __forceinline__ void tmem_st8u(uint32_t addr, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
@@ -221,27 +213,25 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
     volatile int *abort = &s.abort;
     Cells<BITS, D> cells = {s, 0};
     uint32_t n = 0;                                         // units so far
-    uint64_t cell[2];
-    uint32_t raw[4][L::UW], ks[4][NB / 2], tk[SCALES];
+    uint64_t cell[2] = {0, 0};
+    uint32_t raw[4][L::UW], ks[4][BLOCKS / 2], tk[SCALES];
     auto load_unit = [&](int u) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {                       // rows 8 i + kr
-            const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[i >> 1]);
-            if (cell[i >> 1] > 1) load_global<L::UW>(p + L::k_word(8 * (i & 1) + kr, c, u * L::UW), raw[i]);
-            else
+            const uint64_t from = cell[i >> 1];
+            const uint8_t *p = reinterpret_cast<const uint8_t *>(from);
 #pragma unroll
-                for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
+            for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
+#pragma unroll
+            for (int k = 0; k < BLOCKS / 2; ++k) ks[i][k] = from ? 0x7fff7fffu : 0u;        // a page out of range: NaN
+            if (from > 1) {
+                load_global<L::UW>(p + L::k_word(8 * (i & 1) + kr, c, u * L::UW), raw[i]);
+                load_global<BLOCKS / 2>(p + L::k_scale(8 * (i & 1) + kr, u * BLOCKS), ks[i]);
+            }
         }
     };
     auto load = [&]() {
         load_unit(0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (cell[i >> 1] > 1) load_global<NB / 2>(reinterpret_cast<const uint8_t *>(cell[i >> 1]) + L::k_scale(8 * (i & 1) + kr, 0), ks[i]);
-            else
-#pragma unroll
-                for (int k = 0; k < NB / 2; ++k) ks[i][k] = cell[i >> 1] ? 0x7fff7fffu : 0u;        // a page out of range: NaN
-        }
         const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[lane >> 4]);
 #pragma unroll
         for (int k = 0; k < SCALES; ++k) {
@@ -272,7 +262,7 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
             if (lane == 0) s.k_exp[n & 1][w] = e - 5;
             const int x = TO - e, x1 = min(x, 15);
             const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
-#pragma unroll
+#pragma unroll 1
             for (int v = 0; v < L::UNITS; ++v) {
                 if (v > 0) load_unit(v);
 #pragma unroll
@@ -281,11 +271,11 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
 #pragma unroll
                     for (int k = 0; k < BLOCKS; ++k) {
                         const int b = v * BLOCKS + k;
-                        const __half2 d = __hmul2(__hmul2(bits_h2(ks[i][b / 2]), up1), up2);
+                        const __half2 d = __hmul2(__hmul2(bits_h2(ks[i][k / 2]), up1), up2);
                         uint32_t h[4];
                         raw_pairs<BITS, 0x4140, 0x4342>(&raw[i][k * WB], h);
-                        scaled_pairs<BITS>(h, b & 1 ? __high2half2(d) : __low2half2(d));
-                        const uint32_t to = k_tile + (b >> 1) * (kUnit * 128) + row * 128 + (((4 * (b & 1) + c) ^ (row & 7)) << 4);
+                        scaled_pairs<BITS>(h, k & 1 ? __high2half2(d) : __low2half2(d));
+                        const uint32_t to = k_tile + (b >> 1) * (kUnit * 128) + row * 128 + (((4 * (k & 1) + c) ^ (row & 7)) << 4);
                         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
                     }
                 }
@@ -312,7 +302,7 @@ template <int BITS, int D>
 __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t v_tile) {
     using T = Tile<BITS, D>;
     using L = typename T::L;
-    constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS, TWO = BLOCKS < 2 ? BLOCKS : 2;     // scales in registers: of TWO blocks
+    constexpr int NB = T::NB, WB = BITS / 4, STEP = 2;      // words of a block; blocks at a time
     constexpr int SCALES = NB / 2;
     constexpr int TO = BITS == 4 ? 25 : 29;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kValues;
@@ -320,29 +310,25 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
     volatile int *abort = &s.abort;
     Cells<BITS, D> cells = {s, 0};
     uint32_t n = 0;
-    uint64_t cell[2];
-    uint32_t raw[4][L::UW], vs[4][TWO], tv[SCALES];
-    auto load_scales = [&](int b) {
+    uint64_t cell[2] = {0, 0};
+    uint32_t raw[4][STEP * WB], vs[4][STEP], tv[SCALES];
+    auto load_step = [&](int b) {                           // blocks b .. + STEP - 1
         const uint64_t from = cell[q >> 1];
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(from);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {                       // pairs 4 (q % 2) + i
 #pragma unroll
-            for (int k = 0; k < TWO; ++k) vs[i][k] = 0;
-            if (from > 1) load_global<TWO>(reinterpret_cast<const uint8_t *>(from) + L::v_scale(8 * (q & 1) + 2 * i, b), vs[i]);
-        }
-    };
-    auto load_unit = [&](int u) {
-        const uint64_t from = cell[q >> 1];
+            for (int k = 0; k < STEP * WB; ++k) raw[i][k] = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
-            if (from > 1) load_global<L::UW>(reinterpret_cast<const uint8_t *>(from) + L::v_word(4 * (q & 1) + i, g, u * L::UW), raw[i]);
+            for (int k = 0; k < STEP; ++k) vs[i][k] = 0;
+            if (from > 1) {
+                load_global<STEP * WB>(p + L::v_word(4 * (q & 1) + i, g, b * WB), raw[i]);
+                load_global<STEP>(p + L::v_scale(8 * (q & 1) + 2 * i, b), vs[i]);
+            }
         }
-        load_scales(u * BLOCKS);
     };
     auto load = [&]() {
-        load_unit(0);
+        load_step(0);
         const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[lane >> 4]);
 #pragma unroll
         for (int k = 0; k < SCALES; ++k) {
@@ -395,37 +381,34 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
             const int x = TO - e, x1 = min(x, 15);
             const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
 #pragma unroll 1
-            for (int v = 0; v < L::UNITS; ++v) {
-                if (v > 0) load_unit(v);
+            for (int b = 0; b < NB; b += STEP) {
+                if (b > 0) load_step(b);
+                if (edge) {                                 // positions that no row sees are zeros
 #pragma unroll
-                for (int k = 0; k < BLOCKS; ++k) {
-                    if (k > 0 && k % TWO == 0) load_scales(v * BLOCKS + k);
-                    if (k % TWO == 0) {
-                        if (edge) {                         // positions that no row sees are zeros
+                    for (int i = 0; i < 4; ++i) {
+                        const int p = p0 + 8 * q + 2 * i;
+                        const uint32_t keep = (p >= lo && p < hi ? 0xffffu : 0u) | (p + 1 >= lo && p + 1 < hi ? 0xffff0000u : 0u);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int p = p0 + 8 * q + 2 * i;
-                                const uint32_t keep = (p >= lo && p < hi ? 0xffffu : 0u) | (p + 1 >= lo && p + 1 < hi ? 0xffff0000u : 0u);
-#pragma unroll
-                                for (int j = 0; j < TWO; ++j) vs[i][j] &= keep;
-                            }
-                        }
-                        if (odd) {                          // blocks that are no numbers leave the product
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int j = 0; j < TWO; ++j) vs[i][j] &= ~__vcmpeq2(vs[i][j] & 0x7c007c00u, 0x7c007c00u);
-                        }
+                        for (int k = 0; k < STEP; ++k) vs[i][k] &= keep;
                     }
+                }
+                if (odd) {                                  // blocks that are no numbers leave the product
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < STEP; ++k) vs[i][k] &= ~__vcmpeq2(vs[i][k] & 0x7c007c00u, 0x7c007c00u);
+                }
+#pragma unroll
+                for (int k = 0; k < STEP; ++k) {
                     uint32_t h[4][4];                       // [pair][j]
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         raw_pairs<BITS, 0x4240, 0x4341>(&raw[i][k * WB], h[i]);
-                        scaled_pairs<BITS>(h[i], __hmul2(__hmul2(bits_h2(vs[i][k % TWO]), up1), up2));
+                        scaled_pairs<BITS>(h[i], __hmul2(__hmul2(bits_h2(vs[i][k]), up1), up2));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int row = 32 * (v * BLOCKS + k) + 8 * j + g;
+                        const int row = 32 * (b + k) + 8 * j + g;
                         const uint32_t to = v_tile + (w >> 1) * (D * 128) + row * 128 + (((4 * (w & 1) + q) ^ g) << 4);
                         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0][j]), "r"(h[1][j]), "r"(h[2][j]), "r"(h[3][j]) : "memory");
                     }
@@ -566,20 +549,29 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
             tc_fence_after();
             if (work) {
                 if (u > 0) look_at_bad(n - 1, p0 - kUnit);
-                int first = see.lo - p0, last = see.hi - p0;                // columns that the row sees: [first, last)
+                const int first = see.lo - p0, last = see.hi - p0;          // columns that the row sees: [first, last)
                 const bool edge = __any_sync(0xffffffffu, first > 0 || last < kUnit);
                 const int *ke = s.k_exp[n & 1], *ve = s.v_exp[n & 1];       // of 32 columns
-                // (Loops that stay loops: unrolled, what each 32 columns need would be kept in registers all at once.)
+                // (Loops that stay loops, and the hidden columns in a pass of their own: the warps of a multiprocessor run many
+                // different paths, and what they do not find in the instruction caches they wait for.)
+                if (edge) {
+#pragma unroll 1
+                    for (int c = 0; c < kUnit; c += 8) {
+                        float v[8];
+                        tmem_ld8(scores + c, v);
+                        tmem_wait_ld(v);
+                        const uint32_t seen = bits_between(first - c, last - c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) if (!(seen >> k & 1u)) v[k] = -INFINITY;
+                        tmem_st8(scores + c, v);
+                    }
+                    tmem_wait_st();
+                }
                 float top = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float v[32], m[4];
                     tmem_load32(scores + 32 * c, v);
-                    if (edge) {
-                        const uint32_t seen = bits_between(first - 32 * c, last - 32 * c);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) if (!(seen >> k & 1u)) v[k] = -INFINITY;
-                    }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) m[k] = v[k];
 #pragma unroll
@@ -594,13 +586,13 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
                     ref = now;
                     if (u > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            float y[16];
-                            tmem_load16(outputs + c, y);
-                            uint32_t z[16];
+                        for (int c = 0; c < D; c += 8) {
+                            float y[8];
+                            tmem_ld8(outputs + c, y);
+                            tmem_wait_ld(y);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(y[k] * f);
-                            tmem_st16(outputs + c, z);
+                            for (int k = 0; k < 8; ++k) y[k] *= f;
+                            tmem_st8(outputs + c, y);
                         }
                     }
                 }
@@ -608,11 +600,11 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
                 // weights into tensor memory, in place of scores that are in registers by then
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    const float fk = factor * power(ke[c]), b = base + (float)ve[c];
+                    float v[32], fk = factor * power(ke[c]);
+                    if (fk == 0.f) fk = 1e-37f;             // a hidden column's -inf stays one
+                    const float b = base + (float)ve[c];
                     const float2 f2 = make_float2(fk, fk), b2 = make_float2(b, b);
-                    float v[32];
                     tmem_load32(scores + 32 * c, v);
-                    const uint32_t seen = edge ? bits_between(first - 32 * c, last - 32 * c) : 0xffffffffu;
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -621,10 +613,6 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
                         for (int k = 0; k < 8; ++k) {
                             const int at = 16 * h + 2 * k;
                             float2 z = ffma2(make_float2(v[at], v[at + 1]), f2, b2);
-                            if (edge) {
-                                if (!(seen >> at & 1u)) z.x = -INFINITY;
-                                if (!(seen >> (at + 1) & 1u)) z.y = -INFINITY;
-                            }
                             z = make_float2(ex2(z.x), ex2(z.y));
                             sum[k & 1] = fadd2(sum[k & 1], z);
                             x[k] = h2_bits(__floats2half2_rn(z.x, z.y));
