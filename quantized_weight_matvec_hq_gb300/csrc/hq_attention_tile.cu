@@ -68,6 +68,12 @@ __device__ __forceinline__ void tmem_st8u(uint32_t addr, const uint32_t (&v)[8])
                  ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(addr) : "memory");
 }
 
+// 16 bytes into shared memory, zeros without `live`; this thread's, waited for by copy_async_wait.
+__device__ __forceinline__ void copy_async16(uint32_t to, const void *from, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
@@ -97,7 +103,7 @@ struct Tile {
         uint64_t part_full[2], part_empty[2], cell_full[kSlots], cell_empty[kSlots];
         uint64_t q_full, k_full, v_full, s_full, p_full, pv_done;
         uint64_t cell[kSlots][kCells];                      // addresses; 0: no position that is seen, 1: page out of range
-        float factor[kRows];
+        float factor[2][kRows];                             // of the queries of a part
         int k_exp[2][kDecode], v_exp[2][kDecode];           // of 32 positions: the stored value is the tile's times 2^exp
         uint32_t any_bad[2][kDecode];                       // some value block of the 32 positions is no number
         uint8_t bad[2][kUnit];                              // then: of each position, bit b: block b
@@ -199,10 +205,53 @@ struct Cells {
     }
 };
 
+// The decode warps prepare the tile of Q at a part's start, 16 rows each, while the softmax warps may still write the part before:
+// rows times a power of two that takes their largest element to [2^14, 2^15), and the scale's sign.
+template <int BITS, int D>
+__device__ __forceinline__ void prepare_queries(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint8_t *q_tile, int at) {
+    constexpr int LANES = D / 8, ROWS = 32 / LANES, MINE = kRows / (2 * kDecode);       // lanes of a row, rows at once, rows of a warp
+    const Part &part = s.part[at];
+    const int lane = threadIdx.x & 31, col = lane % LANES, row0 = MINE * ((threadIdx.x >> 5) - kSoftmax) + lane / LANES;
+    auto place = [&](int row) { return q_tile + (col / 8) * (kRows * 128) + row * 128 + ((col % 8 ^ (row & 7)) << 4); };
+    // all of the warp's rows on their way into the tile at once, then scaled in place, each lane what it copied
+#pragma unroll 1
+    for (int i = 0; i < MINE; i += ROWS) {
+        int token, head;
+        const bool live = row_of(a, part.q, part.item, row0 + i, token, head);
+        const long long from = live ? ((long long)part.q.first + token) * a.q_stride + (long long)head * D + 8 * col : 0;
+        copy_async16(smem_u32(place(row0 + i)), static_cast<const uint16_t *>(a.q) + from, live);
+    }
+    copy_async_wait();
+#pragma unroll 1
+    for (int i = 0; i < MINE; i += ROWS) {
+        const int row = row0 + i;
+        float v[8];
+        if (a.dtype == HQ_DT_F16) load8(reinterpret_cast<const __half *>(place(row)), v);
+        else load8(reinterpret_cast<const __nv_bfloat16 *>(place(row)), v);
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+#pragma unroll
+        for (int d = 1; d < LANES; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const int e = min(253, 268 - (int)(top >> 23));
+        const float up = __uint_as_float((uint32_t)e << 23) * (a.scale < 0.f ? -1.f : 1.f);
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = h2_bits(__floats2half2_rn(v[2 * k] * up, v[2 * k + 1] * up));
+        *reinterpret_cast<uint4 *>(place(row)) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (col == 0)
+            s.factor[at][row] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
+                                                   : fabsf(a.scale) * kLog2e * __uint_as_float((uint32_t)(254 - e) << 23);
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
+}
+
 // A key warp has 32 positions of a unit: two cells.  Four neighbouring lanes have a row; rows x and x ^ 5 lie side by
 // side, so that the stores do not meet in a bank.  The next unit's bytes are asked for while this one's products run.
 template <int BITS, int D>
-__device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t k_tile) {
+__device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint8_t *q_tile, uint32_t k_tile) {
     using T = Tile<BITS, D>;
     using L = typename T::L;
     constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS;        // words of a block, blocks of a unit
@@ -243,6 +292,8 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
         const int at = part_n & 1;
         if (!tc_wait(smem_u32(&s.part_full[at]), (uint32_t)(part_n >> 1 & 1), abort, a.c.fault)) return;
         if (s.part[at].take == 0) return;
+        if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;          // the tile of Q is free
+        prepare_queries<BITS, D>(a, s, q_tile, at);
         if (!cells.next(a, w, cell)) return;
         load();
         for (int u = 0; u < s.part[at].take; ++u, ++n) {
@@ -299,7 +350,7 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
 // A value warp has 32 positions of a unit.  A lane turns eight positions' elements g, 8 + g, .. into rows of V^T: 16 bytes
 // each, the rows of eight neighbouring lanes in different banks.
 template <int BITS, int D>
-__device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t v_tile) {
+__device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint8_t *q_tile, uint32_t v_tile) {
     using T = Tile<BITS, D>;
     using L = typename T::L;
     constexpr int NB = T::NB, WB = BITS / 4, STEP = 2;      // words of a block; blocks at a time
@@ -340,6 +391,8 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
         const int at = part_n & 1;
         if (!tc_wait(smem_u32(&s.part_full[at]), (uint32_t)(part_n >> 1 & 1), abort, a.c.fault)) return;
         if (s.part[at].take == 0) return;
+        if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;          // the tile of Q is free
+        prepare_queries<BITS, D>(a, s, q_tile, at);
         if (!cells.next(a, w, cell)) return;
         load();
         for (int u = 0; u < s.part[at].take; ++u, ++n) {
@@ -472,8 +525,7 @@ __device__ __forceinline__ void products(const AttnArgs &a, typename Tile<BITS, 
 // ------------------------------------------------------------------ softmax
 
 template <int BITS, int D>
-__device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint8_t *q_tile, uint32_t tmem) {
-    constexpr int LANES = D / 8, ROWS = 32 / LANES;         // lanes of a query row's loads, rows at once
+__device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t tmem) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = threadIdx.x;
     volatile int *abort = &s.abort;
     const uint32_t scores = tmem + ((uint32_t)(32 * warp) << 16), outputs = scores + 128;
@@ -484,51 +536,7 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
         const Part &part = s.part[at];
         const int take = part.take;
         if (take == 0) return;
-        // ---- the tile of Q: times a power of two a row, and the scale's sign
-        {
-            const float sign = a.scale < 0.f ? -1.f : 1.f;
-            const int col = lane % LANES;
-            constexpr int BATCH = 4;                        // loads under way at once
-#pragma unroll 1
-            for (int i0 = 0; i0 < 32; i0 += BATCH * ROWS) {
-                uint4 raw[BATCH];
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int row = 32 * warp + i0 + i * ROWS + lane / LANES;
-                    int token, head;
-                    const bool live = row_of(a, part.q, part.item, row, token, head);
-                    const long long from = live ? ((long long)part.q.first + token) * a.q_stride + (long long)head * D + 8 * col : 0;
-                    raw[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + from);
-                    if (!live) raw[i] = make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int row = 32 * warp + i0 + i * ROWS + lane / LANES;
-                    float v[8];
-                    if (a.dtype == HQ_DT_F16) load8(reinterpret_cast<const __half *>(&raw[i]), v);
-                    else load8(reinterpret_cast<const __nv_bfloat16 *>(&raw[i]), v);
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
-#pragma unroll
-                    for (int d = 1; d < LANES; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    const int e = min(253, 268 - (int)(top >> 23));
-                    const float up = __uint_as_float((uint32_t)e << 23) * sign;
-                    uint32_t h[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) h[k] = h2_bits(__floats2half2_rn(v[2 * k] * up, v[2 * k + 1] * up));
-                    *reinterpret_cast<uint4 *>(q_tile + (col / 8) * (kRows * 128) + row * 128 + ((col % 8 ^ (row & 7)) << 4)) =
-                        make_uint4(h[0], h[1], h[2], h[3]);
-                    if (col == 0)
-                        s.factor[row] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
-                                                           : fabsf(a.scale) * kLog2e * __uint_as_float((uint32_t)(254 - e) << 23);
-                }
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
-        }
-        const float factor = s.factor[me];
+        float factor = 0.f;                                 // (known with the part's first scores)
         int token, head;
         const bool live = row_of(a, part.q, part.item, me, token, head);
         const bool work = __any_sync(0xffffffffu, live);    // some row of the warp
@@ -547,6 +555,7 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
         for (int u = 0; u < take; ++u, ++n, p0 += kUnit) {
             if (!tc_wait(smem_u32(&s.s_full), n & 1, abort, a.c.fault)) return;
             tc_fence_after();
+            if (u == 0) factor = s.factor[at][me];
             if (work) {
                 if (u > 0) look_at_bad(n - 1, p0 - kUnit);
                 const int first = see.lo - p0, last = see.hi - p0;          // columns that the row sees: [first, last)
@@ -676,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<BITS, D>::MIN_BLOCKS)) attenti
             mbar_init(smem_u32(&s.cell_full[i]), 1);
             mbar_init(smem_u32(&s.cell_empty[i]), 2 * kDecode);
         }
-        mbar_init(smem_u32(&s.q_full), kSoftmax);
+        mbar_init(smem_u32(&s.q_full), 2 * kDecode);
         mbar_init(smem_u32(&s.k_full), kDecode);
         mbar_init(smem_u32(&s.v_full), kDecode);
         mbar_init(smem_u32(&s.s_full), 1 + 2 * kDecode);         // the products, and the exponents of K and V
@@ -698,11 +707,11 @@ __global__ void __launch_bounds__(kThreads, (Tile<BITS, D>::MIN_BLOCKS)) attenti
     deal<kThreads>(a, total, x0, end, s.walk);
     if (x0 >= end) {
     } else if (warp < kSoftmax) {
-        softmax<BITS, D>(a, s, q_tile, tmem);
+        softmax<BITS, D>(a, s, tmem);
     } else if (warp < kValues) {
-        decode_keys<BITS, D>(a, s, k);
+        decode_keys<BITS, D>(a, s, q_tile, k);
     } else if (warp < kWalker) {
-        decode_values<BITS, D>(a, s, v);
+        decode_values<BITS, D>(a, s, q_tile, v);
     } else if (warp == kWalker) {
         walk<BITS, D>(a, s, total, x0, end);
     } else if (elect_one()) {
