@@ -353,7 +353,8 @@ template <int BITS, int D>
 __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint8_t *q_tile, uint32_t v_tile) {
     using T = Tile<BITS, D>;
     using L = typename T::L;
-    constexpr int NB = T::NB, WB = BITS / 4, STEP = 2;      // words of a block; blocks at a time
+    constexpr int NB = T::NB, WB = BITS / 4;                // words of a block
+    constexpr int STEP = BITS == 8 && D == 128 ? 1 : 2;     // blocks at a time (two are more than 72 registers there)
     constexpr int SCALES = NB / 2;
     constexpr int TO = BITS == 4 ? 25 : 29;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kValues;
