@@ -30,6 +30,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// As mma16816, with what is added to: c0 in columns 0 and c1 in columns 1 of a thread's pairs.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1, float c0, float c1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -325,22 +333,21 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                     const float f0 = b % 2 ? __high2float(d0) : __low2float(d0), f1 = b % 2 ? __high2float(d1) : __low2float(d1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                        if (S::RAW) {
-                            const float2 x = *reinterpret_cast<const float2 *>(&s.offset[b][8 * n + 2 * c]);
-                            acc[0] = acc[2] = x.x;
-                            acc[1] = acc[3] = x.y;
-                        }
+                        float acc[4];
+                        const float2 start = S::RAW ? *reinterpret_cast<const float2 *>(&s.offset[b][8 * n + 2 * c]) : make_float2(0.f, 0.f);
 #pragma unroll
                         for (int t = S::TERMS - 1; t >= 0; --t) {
                             const uint4 q = s.q[t][n][b][lane];
-                            mma16816(acc, ka[0], kb[0], ka[1], kb[1], q.x, q.y);
+                            if (t == S::TERMS - 1) mma16816_from(acc, ka[0], kb[0], ka[1], kb[1], q.x, q.y, start.x, start.y);
+                            else mma16816(acc, ka[0], kb[0], ka[1], kb[1], q.x, q.y);
                             mma16816(acc, ka[2], kb[2], ka[3], kb[3], q.z, q.w);
                         }
-                        z[n][0] = fmaf(acc[0], f0, z[n][0]);
-                        z[n][1] = fmaf(acc[1], f0, z[n][1]);
-                        z[n][2] = fmaf(acc[2], f1, z[n][2]);
-                        z[n][3] = fmaf(acc[3], f1, z[n][3]);
+                        const float2 z0 = ffma2(make_float2(acc[0], acc[1]), make_float2(f0, f0), make_float2(z[n][0], z[n][1]));
+                        const float2 z1 = ffma2(make_float2(acc[2], acc[3]), make_float2(f1, f1), make_float2(z[n][2], z[n][3]));
+                        z[n][0] = z0.x;
+                        z[n][1] = z0.y;
+                        z[n][2] = z1.x;
+                        z[n][3] = z1.y;
                     }
                 }
             }

@@ -178,16 +178,21 @@ __device__ __forceinline__ void walk_to(const AttnArgs &a, long long x, int r0, 
     if (THREADS == 32) __syncwarp(); else __syncthreads();
 }
 
+// a / b for a >= 0, b > 0: in 32 bits where they fit, a fraction of the instructions.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // The first unit of block `b`.  Few units go to few blocks, min_units each.
 __device__ __forceinline__ long long first_unit(const AttnArgs &a, long long total, int b) {
-    const long long n = min((long long)a.blocks, max(1ll, total / a.min_units));
-    return b >= n ? total : total * b / n;
+    const long long n = min((long long)a.blocks, max(1ll, quotient(total, a.min_units)));
+    return b >= n ? total : quotient(total * b, n);
 }
 
 // The block that has a unit.
 __device__ __forceinline__ int block_of(const AttnArgs &a, long long total, long long unit) {
-    const long long n = min((long long)a.blocks, max(1ll, total / a.min_units));
-    return (int)(((unit + 1) * n - 1) / total);
+    const long long n = min((long long)a.blocks, max(1ll, quotient(total, a.min_units)));
+    return (int)quotient((unit + 1) * n - 1, total);
 }
 
 // This block's units [x0, end) of the batch's `total`, and the walk at the first one's request.  The whole block calls it.
@@ -235,7 +240,7 @@ __device__ __forceinline__ Item item_at(const AttnArgs &a, const Walk &w, long l
     it.tile = lo;
     it.units = (int)(units_before(a, w.q, lo + 1) - before);
     const long long rest = local - before * heads;
-    const int h = rest >> 32 ? (int)(rest / it.units) : (int)((unsigned)rest / (unsigned)it.units);
+    const int h = (int)quotient(rest, it.units);
     it.kv_head = h / a.parts;
     it.part = h % a.parts;
     it.unit = (int)(rest - (long long)h * it.units);
