@@ -288,10 +288,9 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
             for (int i = 0; i < 4; ++i) o[n][b][0][i] = o[n][b][1][i] = 0.f;
     }
     int up = S::shift_of(0);                                // the values' scales are taken times 2^up
-    bool ok = true;
     for (int u = 0; u < part.take; ++u) {
         const uint32_t stage = lap >> 1;                    // the ring's stage, and below it the phase of its barrier
-        if (!mbar_wait(smem_u32(&s.full[stage]), lap & 1, &s.abort, a.c.fault)) { ok = false; break; }
+        if (!mbar_wait(smem_u32(&s.full[stage]), lap & 1, &s.abort, a.c.fault)) break;
         const uint32_t states = s.cells[stage];
         const uint32_t state = states >> warp & 0x10001u;
         if (state != 0) {                                   // the whole warp
@@ -551,7 +550,7 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
         }
     named_barrier(1, kConsumers);
     const float down = __uint_as_float((uint32_t)(127 - up) << 23);
-#pragma unroll
+#pragma unroll 1
     for (int turn = 0; turn < 2; ++turn) {
         if (warp / (kWarps / 2) == 1 - turn) {
 #pragma unroll
@@ -607,7 +606,7 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
                 a.stat[r] = make_float2(t, sum);
         }
     }
-    return ok;
+    return *(volatile int *)&s.abort == 0;
 }
 
 template <bool WIDE, int BITS, int D, int NT>
@@ -709,7 +708,7 @@ __global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(cons
 int64_t mean_rows(const AttentionArgs &x) {
     return (x.cache.n_tokens + x.cache.n_req - 1) / x.cache.n_req * (x.n_heads / x.cache.n_kv_heads);
 }
-bool on_tiles(const AttentionArgs &x) { return x.cache.dtype != HQ_DT_F32 && mean_rows(x) > 16; }
+[[maybe_unused]] [[maybe_unused]] bool on_tiles(const AttentionArgs &x) { return x.cache.dtype != HQ_DT_F32 && mean_rows(x) > 16; }
 int stream_rows(const AttentionArgs &x) { return mean_rows(x) <= 8 || x.cache.head_dim == 256 ? 8 : 16; }
 
 template <bool WIDE, int D>
