@@ -759,7 +759,7 @@ hq_status hq_selftest_wait_timeout(int64_t cycles, hq_stream_t stream) {
 
 hq_status hq_selftest_wait(int wait, uint32_t fault, int64_t cycles, hq_stream_t stream) {
     if (wait < HQ_WAIT_MATVEC || wait > HQ_WAIT_MATMUL_GO) return set_error(HQ_ERR_UNSUPPORTED, "wait %d is not HQ_WAIT_*", wait);
-    if (fault & ~(HQ_FAULT_EXPERT_ID | HQ_FAULT_ADAPTER_ID | HQ_FAULT_DRAFT))
+    if (fault & ~(HQ_FAULT_EXPERT_ID | HQ_FAULT_ADAPTER_ID | HQ_FAULT_DRAFT | HQ_FAULT_CACHE))
         return set_error(HQ_ERR_UNSUPPORTED, "fault 0x%x has bits that are no data fault's", fault);
     if (cycles < 1 || cycles > 4000000000LL) return set_error(HQ_ERR_SHAPE, "cycles %lld not in [1, 4e9]", (long long)cycles);
     DeviceInfo *dev = nullptr;

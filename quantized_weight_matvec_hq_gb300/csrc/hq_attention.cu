@@ -648,8 +648,8 @@ __global__ void __launch_bounds__(kThreads, (Stream<WIDE, BITS, D, NT>::MIN_BLOC
     }
 }
 
-// Joins the partial results of kCombineRows rows (blockIdx.y) of the item that block blockIdx.x tells of.  D / 8 lanes a row of
-// a partial result, the groups of them that a row has take every GROUPS-th block's.
+// Joins the partial results of the item that block blockIdx.x tells of, kCombineRows rows at a time (gridDim.y blocks share them).  D / 8
+// lanes a row of a partial result, the groups of them that a row has take every GROUPS-th block's.
 template <bool WIDE, int D>
 __global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(const __grid_constant__ AttnArgs a, int rows) {
     constexpr int LANES = D / 8, GROUPS = kCombineThreads / LANES / kCombineRows;
@@ -660,46 +660,50 @@ __global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(cons
     const int b = blockIdx.x;
     if (!a.joins[b].valid) return;
     const Join join = a.joins[b];
-    const int mine = threadIdx.x / (LANES * GROUPS), row = blockIdx.y * kCombineRows + mine;
-    const int group = threadIdx.x / LANES % GROUPS, at = threadIdx.x % LANES;
-    int token, head;
-    const bool live = row_of(a, join.q, join.item, row, token, head);
-    float t = -INFINITY, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (live) {
+    const int mine = threadIdx.x / (LANES * GROUPS), group = threadIdx.x / LANES % GROUPS, at = threadIdx.x % LANES;
+    for (int row0 = blockIdx.y * kCombineRows; row0 < rows; row0 += gridDim.y * kCombineRows) {
+        const int row = row0 + mine;
+        int token, head;
+        const bool live = row_of(a, join.q, join.item, row, token, head);
+        float t = -INFINITY, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (live) {
 #pragma unroll 4
-        for (int k = b + group; k <= join.last; k += GROUPS) {
-            const long long r = (long long)(k == b ? join.slot : 2 * k) * rows + row;
-            const float2 ml = a.stat[r];
-            float y[8];
-            load8(a.partial + r * D + 8 * at, y);
-            const float t1 = fmaxf(t, ml.x);
-            const float f0 = t == t1 ? 1.f : ex2(t - t1), f1 = ml.x == t1 ? 1.f : ex2(ml.x - t1);
-            sum = sum * f0 + ml.y * f1;
+            for (int k = b + group; k <= join.last; k += GROUPS) {
+                const long long r = (long long)(k == b ? join.slot : 2 * k) * rows + row;
+                const float2 ml = a.stat[r];
+                float y[8];
+                load8(a.partial + r * D + 8 * at, y);
+                const float t1 = fmaxf(t, ml.x);
+                const float f0 = t == t1 ? 1.f : ex2(t - t1), f1 = ml.x == t1 ? 1.f : ex2(ml.x - t1);
+                sum = sum * f0 + ml.y * f1;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * f0 + y[e] * f1;
-            t = t1;
+                for (int e = 0; e < 8; ++e) v[e] = v[e] * f0 + y[e] * f1;
+                t = t1;
+            }
         }
+        if (at == 0) { gm[mine][group] = t; gl[mine][group] = sum; }
+        store8(&go[mine][group][8 * at], v);
+        __syncthreads();
+        if (group == 0 && live) {
+            for (int k = 0; k < GROUPS; ++k) t = fmaxf(t, gm[mine][k]);
+            sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+            for (int k = 0; k < GROUPS; ++k) {
+                const float f = gm[mine][k] == t ? 1.f : ex2(gm[mine][k] - t);
+                float y[8];
+                load8(&go[mine][k][8 * at], y);
+                sum += gl[mine][k] * f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += y[e] * f;
+            }
+            const float f = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= f;
+            store_row8<WIDE>(a, ((long long)join.q.first + token) * a.out_stride + (long long)head * D + 8 * at, v);
+        }
+        __syncthreads();
     }
-    if (at == 0) { gm[mine][group] = t; gl[mine][group] = sum; }
-    store8(&go[mine][group][8 * at], v);
-    __syncthreads();
-    if (group != 0 || !live) return;
-    for (int k = 0; k < GROUPS; ++k) t = fmaxf(t, gm[mine][k]);
-    sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    for (int k = 0; k < GROUPS; ++k) {
-        const float f = gm[mine][k] == t ? 1.f : ex2(gm[mine][k] - t);
-        float y[8];
-        load8(&go[mine][k][8 * at], y);
-        sum += gl[mine][k] * f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += y[e] * f;
-    }
-    const float f = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= f;
-    store_row8<WIDE>(a, ((long long)join.q.first + token) * a.out_stride + (long long)head * D + 8 * at, v);
 }
 
 // ------------------------------------------------------------------ host side
@@ -714,7 +718,7 @@ int stream_rows(const AttentionArgs &x) { return mean_rows(x) <= 8 || x.cache.he
 template <bool WIDE, int D>
 hq_status run_combine(const AttnArgs &a, int rows, cudaStream_t stream) {
     if (a.blocks < 2 || a.most_units < 2) return HQ_OK;     // an item of one unit is never divided
-    return launch_blocks(attention_combine_kernel<WIDE, D>, dim3((unsigned)(a.blocks - 1), rows / kCombineRows), kCombineThreads, 0,
+    return launch_blocks(attention_combine_kernel<WIDE, D>, dim3((unsigned)(a.blocks - 1), std::min(rows / kCombineRows, 8)), kCombineThreads, 0,
                          stream, "attention combine", a, rows);
 }
 

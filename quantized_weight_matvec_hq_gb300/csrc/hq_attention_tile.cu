@@ -556,7 +556,7 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
         for (int u = 0; u < take; ++u, ++n, p0 += kUnit) {
             if (!tc_wait(smem_u32(&s.s_full), n & 1, abort, a.c.fault)) return;
             tc_fence_after();
-            if (u == 0) factor = s.factor[at][me];
+            if (u == 0) factor = see.hi > see.lo ? s.factor[at][me] : 0.f;      // (a row that sees nothing is zeros, whatever its query)
             if (work) {
                 if (u > 0) look_at_bad(n - 1, p0 - kUnit);
                 const int first = see.lo - p0, last = see.hi - p0;          // columns that the row sees: [first, last)

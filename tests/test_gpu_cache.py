@@ -499,6 +499,42 @@ def test_rows_that_see_nothing(hq, heads, new, dtype):
         check_attention(out, q, cache, b.lengths, b.new, heads, 2, 64, dtype, causal)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_that_see_nothing_whatever_their_query(hq, dtype):
+    g = synthetic.rng(1705)
+    b = Batch(hq, g, "q8_0", 1, 64, 16, [3, 2], [30, 2])
+    b.fill(g)
+    q = torch.full((b.T, 8, 64), float("nan"), dtype=DT[dtype], device="cuda")
+    out = b.attend(q, 8)
+    assert bool((out[:27] == 0).all()) and bool(torch.isnan(out[27:32]).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("heads,kv,dim", [(300, 1, 64), (258, 2, 128), (130, 1, 256)])
+def test_groups_wider_than_a_tile(hq, heads, kv, dim, dtype):
+    """One token's heads in several tiles, the last of them not full."""
+    lengths, new = [70, 1, 300, 0], [1, 1, 3, 0]
+    g = synthetic.rng(1706 + heads)
+    b = Batch(hq, g, "q4_0", kv, dim, 32, lengths, new)
+    cache = b.fill(g)
+    q = torch.from_numpy(g.standard_normal((b.T, heads, dim)).astype(np.float32)).cuda().to(DT[dtype])
+    out = b.attend(q, heads)
+    check_attention(out, q, cache, lengths, new, heads, kv, dim, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_units_of_many_requests_and_windows(hq, dtype):
+    """Windows and tokens that do not divide a unit: every block finds its units alike."""
+    g = synthetic.rng(1707)
+    lengths, new = [1000, 37, 640, 641, 1500, 64], [333, 37, 64, 65, 1, 63]
+    b = Batch(hq, g, "q8_0", 3, 64, 64, lengths, new)
+    cache = b.fill(g)
+    for heads, window in ((9, 0), (15, 63), (21, 65), (3, 200)):
+        q = torch.from_numpy(g.standard_normal((b.T, heads, 64)).astype(np.float32)).cuda().to(DT[dtype])
+        out = b.attend(q, heads, window=window)
+        check_attention(out, q, cache, lengths, new, heads, 3, 64, dtype, 1, window, what=(heads, window))
+
+
 @pytest.mark.parametrize("heads,new", [(4, 1), (8, 20)])
 def test_pages_out_of_range_make_their_rows_nan(hq, heads, new):
     g = synthetic.rng(1710)
