@@ -57,17 +57,27 @@ __device__ __forceinline__ void quantize8(const float (&w)[8], __half &scale, ui
     const float d = BITS == 8 ? fminf(__fdiv_rn(top, 127.f), 65504.f)
                               : fminf(fmaxf(__fdiv_rn(m, -8.f), -65504.f), 65504.f);
     const bool none = odd || d == 0.f;
+    // Quotients by the reciprocal and one correction by the remainder are correctly rounded, as the reciprocal is (P. Markstein, IBM Journal of
+    // Research and Development 34, 1990, theorem 7), where nothing on the way leaves the normal range; a third of the division's instructions.
+    const float inverse = __frcp_rn(d);
+    const bool plain = fabsf(d) > 1e-30f;
     scale = odd ? __ushort_as_half(0x7fff) : __float2half_rn(d);
     q[0] = q[1] = 0;
+    auto code = [&](int i, float z) {
+        uint32_t u;
+        if (BITS == 8) u = (uint32_t)(max(-127, min(127, (int)roundf(z))) + 128);
+        else u = (uint32_t)max(0, min(15, (int)floorf(__fadd_rn(z, 8.5f))));
+        q[i / 4] |= (none ? (BITS == 8 ? 128u : 8u) : u) << (8 * (i % 4));
+    };
+    if (__all_sync(0xffffffffu, plain || none)) {           // the whole warp
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t u = BITS == 8 ? 128u : 8u;
-        if (!none) {
-            const float z = __fdiv_rn(w[i], d);
-            if (BITS == 8) u = (uint32_t)(max(-127, min(127, (int)roundf(z))) + 128);
-            else u = (uint32_t)max(0, min(15, (int)floorf(__fadd_rn(z, 8.5f))));
+        for (int i = 0; i < 8; ++i) {
+            const float z = __fmul_rn(w[i], inverse);
+            code(i, __fmaf_rn(__fmaf_rn(-z, d, w[i]), inverse, z));
         }
-        q[i / 4] |= u << (8 * (i % 4));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) code(i, __fdiv_rn(w[i], d));
     }
 }
 

@@ -313,6 +313,28 @@ def test_values_that_are_no_numbers_and_very_large_ones(hq, fmt):
         assert int(torch.isnan(y).sum()) == 3 * 32
 
 
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_quotients_are_those_of_a_division(hq, fmt, dtype):
+    """Millions of blocks of every size, many of whose quotients lie at the middle between two quants: to the bit."""
+    g = synthetic.rng(1115)
+    n, dim = 9000, 256
+    b = Batch(hq, g, fmt, 1, dim, 256, [n], [n], tail=0)
+    x = g.standard_normal((n, 1, dim)).astype(np.float32) * np.exp2(g.integers(-14, 15, (n, 1, 1))).astype(np.float32)
+    if dtype == "f32":
+        x[::3] *= np.exp2(g.integers(-110, 90, (len(x[::3]), 1, 1))).astype(np.float32)
+    top = np.abs(x.reshape(n, 1, -1, 32)).max(-1, keepdims=True)
+    half = top * (g.integers(-253, 254, (n, 1, dim // 32, 32)) / (254 if fmt == "q8_0" else 16)).astype(np.float32)
+    x = np.where(g.uniform(0, 1, (n, 1, dim // 32, 32)) < 0.5, x.reshape(n, 1, -1, 32), np.clip(half, -top, top)).reshape(n, 1, dim)
+    k = dev(x).to(DT[dtype])
+    k = torch.where(torch.isfinite(k), k, torch.zeros_like(k))
+    b.write(k, k.flip(2))
+    got = b.read("f32")
+    for y, rows in zip(got, (k, k.flip(2))):
+        want = values(*stored(rows.float().cpu().numpy(), fmt))
+        assert torch.equal(y, torch.from_numpy(want).float().cuda())
+
+
 def test_tokens_without_a_place_and_pages_out_of_range(hq):
     """A length below the tokens leaves the first ones without a position; a page number out of range reads as NaN."""
     g = synthetic.rng(1120)
