@@ -573,7 +573,8 @@ hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_s
  * k_p and v_p the stored values of key/value head h / (n_heads / n_kv_heads) at position p.
  *   q, out  : `dtype` [n_tokens][n_heads][head_dim]; out may be q itself (same stride), not overlap it otherwise.
  *   n_heads : a multiple of n_kv_heads, at most 4096.
- *   scale   : finite.
+ *   scale   : at most 2^100 in size.  Scores are fp32: they have to fit it, and a row of q whose largest element times
+ *       scale passes 2^116 may come out as NaN.
  *   causal  : 1: a token sees the positions up to its own; 0: all of its request's.
  *   window  : w > 0: of those, the last w up to its own (needs causal 1); 0: no window.
  *   workspace : hq_cache_attention_workspace() bytes, 256-byte aligned, not in
@@ -583,9 +584,11 @@ hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_s
  * not touch it, whatever they hold.  One whose key has a NaN or infinite scale makes the rows that
  * see it NaN; a value block's makes that block's 32 elements NaN.
  * Accuracy: scores, maxima, sums and outputs are fp32.  f32 tokens: quants are exact, q and the weights
- * times the values' scales are taken in two 11-bit terms.  f16 and bf16: the weights (times the values' scales) are rounded to 11 bits,
- * and with many rows a key/value head (more than 16 of the mean request) the stored keys and values too, or to 2^-19 of
- * their largest in 128 neighbouring positions, whichever is coarser.  q is exact (f16, bf16).
+ * times the values' scales are taken in two 11-bit terms.  f16 and bf16, at most 16 rows a key/value head of the mean
+ * request: the weights times their value block's scale are rounded to 11 bits; scores are off by up to 2^-22 of the position's
+ * largest key element times the sum of |q|.  f16 and bf16, more rows: the weights are rounded to 11 bits, and
+ * so are the stored keys and values, or to 2^-19 of their largest in 32 neighbouring positions where that is coarser.  q is exact,
+ * but for elements below 2^-24 of their row's largest.
  * Deterministic: a token's bits depend on its own request, and on the others only through
  * the split of the positions over CTAs.
  * Source: "DeepSeek-V4 on Hanzo Engine", section "A Fused Attention Kernel

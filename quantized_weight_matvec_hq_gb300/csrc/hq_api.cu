@@ -709,7 +709,7 @@ hq_status hq_cache_attention(int fmt, const void *q, int64_t q_stride, const voi
     a.workspace = workspace;
     hq_status st = check_attention_sizes(a);
     if (st != HQ_OK) return st;
-    if (!std::isfinite(scale)) return set_error(HQ_ERR_SHAPE, "scale must be finite");
+    if (!(std::fabs(scale) <= 0x1p100f)) return set_error(HQ_ERR_SHAPE, "scale %g: at most 2^100 in size", scale);
     if (causal != 0 && causal != 1) return set_error(HQ_ERR_UNSUPPORTED, "causal %d is not 0 or 1", causal);
     if (window < 0 || (window > 0 && !causal))
         return set_error(HQ_ERR_SHAPE, "window %lld: 0, or positive with causal attention", (long long)window);

@@ -239,9 +239,10 @@ __device__ __forceinline__ void prepare_queries(const AttnArgs &a, typename Tile
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[k] = h2_bits(__floats2half2_rn(v[2 * k] * up, v[2 * k + 1] * up));
         *reinterpret_cast<uint4 *>(place(row)) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (col == 0)
-            s.factor[at][row] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
-                                                   : fabsf(a.scale) * kLog2e * __uint_as_float((uint32_t)(254 - e) << 23);
+        if (col == 0) {                                     // as in the kernel for few rows
+            const float f = fabsf(a.scale) * kLog2e * __uint_as_float((uint32_t)(254 - e) << 23);
+            s.factor[at][row] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __fmaf_rn(f, 0.f, f);
+        }
     }
     fence_proxy_async_shared();
     __syncwarp();

@@ -49,7 +49,7 @@ def test_attention_refusals(hq):
     for name in ("q", "out", "pool", "table", "off", "lens"):
         assert attend(hq, **{name: 0}) == hq.HQ_ERR_NULL, name
     for bad in SHARED_SHAPES + [dict(qs=1016), dict(os=0), dict(heads=0), dict(heads=7), dict(heads=4098), dict(window=-1),
-                                dict(window=5, causal=0), dict(scale=float("inf")), dict(scale=float("nan"))]:
+                                dict(window=5, causal=0), dict(scale=float("inf")), dict(scale=float("nan")), dict(scale=2.0 ** 101)]:
         assert attend(hq, **bad) == hq.HQ_ERR_SHAPE, bad
     for bad in (dict(fmt=75), dict(dt=3), dict(causal=2), dict(causal=-1)):
         assert attend(hq, **bad) == hq.HQ_ERR_UNSUPPORTED, bad

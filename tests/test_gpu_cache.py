@@ -435,6 +435,22 @@ def test_long_requests_are_split(hq, lengths, new, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [3, 40])
+def test_rows_past_the_largest_float_are_nan(hq, new, dtype):
+    """The largest scale: a row of q that times it is past fp32 is NaN (2^160, times keys of about 1), the others are as ever."""
+    g = synthetic.rng(1590 + new)
+    b = Batch(hq, g, "q4_0", 2, 64, 16, [70], [new])
+    cache = b.fill(g)
+    x = g.standard_normal((b.T, 8, 64)) * 2.0 ** -100
+    x[1, 2] = 2.0 ** 60
+    q = torch.from_numpy(x.astype(np.float32)).cuda().to(DT[dtype])
+    out = b.attend(q, 8, scale=2.0 ** 100)
+    assert bool(torch.isnan(out[1, 2]).all())
+    q[1, 2], out[1, 2] = 0, b.attend(torch.zeros_like(q), 8, scale=2.0 ** 100)[1, 2]
+    check_attention(out, q, cache, [70], [new], 8, 2, 64, dtype, scale=2.0 ** 100)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("batch", ["ragged", "drafts", "prompts"])
 def test_scales_signs_and_sizes(hq, batch, dtype):
     """Large scores (a softmax of one position), equal ones, negative and zero scales, caches of very small and large values,
