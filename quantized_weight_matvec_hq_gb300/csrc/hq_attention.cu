@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kWarps = 4, kConsumers = 32 * kWarps, kThreads = kConsumers + 32;     // the last warp is the producer
 constexpr int kUnit = kCell * kWarps;                       // a consumer warp has a cell of every unit
-constexpr int kCombineThreads = 256, kCombineRows = 2;
+constexpr int kCombineThreads = 256;
 constexpr float kSlack = 5.f;
 
 // ------------------------------------------------------------------ operands
@@ -649,20 +649,24 @@ __global__ void __launch_bounds__(kThreads, (Stream<WIDE, BITS, D, NT>::MIN_BLOC
     }
 }
 
-// Joins the partial results of the item that block blockIdx.x tells of, kCombineRows rows at a time (gridDim.y blocks share them).  D / 8
+// Joins the partial results of the item that block blockIdx.x tells of, AT_ONCE rows at a time (gridDim.y blocks share them).  D / 8
 // lanes a row of a partial result, the groups of them that a row has take every GROUPS-th block's.
-template <bool WIDE, int D>
+// It is bound by the latency of its loads, so its shape is a matter of how many are under way.  Few rows: two at a time with 4 to 16 groups
+// (7 us of 64 requests' 56, from a cold start; eight rows a block 61 in all); an item may lie on many blocks (131071 positions of 8 heads: 76
+// each).  Tiles: mostly two or three blocks an item, and 128 rows, so a group a row and nothing to exchange; eight groups a row,
+// with two barriers for every two rows, took 43 us of a prompt of 2011 tokens (152 in all) where this takes 11.6 (126).
+template <bool WIDE, int D, int AT_ONCE>
 __global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(const __grid_constant__ AttnArgs a, int rows) {
-    constexpr int LANES = D / 8, GROUPS = kCombineThreads / LANES / kCombineRows;
-    __shared__ float gm[kCombineRows][GROUPS], gl[kCombineRows][GROUPS];
-    __shared__ alignas(16) float go[kCombineRows][GROUPS][D];
+    constexpr int LANES = D / 8, GROUPS = kCombineThreads / LANES / AT_ONCE;
+    __shared__ float gm[AT_ONCE][GROUPS], gl[AT_ONCE][GROUPS];
+    __shared__ alignas(16) float go[GROUPS > 1 ? AT_ONCE : 1][GROUPS][D];
     griddep_launch_dependents();
     griddep_wait();
     const int b = blockIdx.x;
     if (!a.joins[b].valid) return;
     const Join join = a.joins[b];
     const int mine = threadIdx.x / (LANES * GROUPS), group = threadIdx.x / LANES % GROUPS, at = threadIdx.x % LANES;
-    for (int row0 = blockIdx.y * kCombineRows; row0 < rows; row0 += gridDim.y * kCombineRows) {
+    for (int row0 = blockIdx.y * AT_ONCE; row0 < rows; row0 += gridDim.y * AT_ONCE) {
         const int row = row0 + mine;
         int token, head;
         const bool live = row_of(a, join.q, join.item, row, token, head);
@@ -682,28 +686,32 @@ __global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(cons
                 t = t1;
             }
         }
-        if (at == 0) { gm[mine][group] = t; gl[mine][group] = sum; }
-        store8(&go[mine][group][8 * at], v);
-        __syncthreads();
-        if (group == 0 && live) {
-            for (int k = 0; k < GROUPS; ++k) t = fmaxf(t, gm[mine][k]);
-            sum = 0.f;
+        if constexpr (GROUPS > 1) {
+            if (at == 0) { gm[mine][group] = t; gl[mine][group] = sum; }
+            store8(&go[mine][group][8 * at], v);
+            __syncthreads();
+            if (group == 0 && live) {
+                for (int k = 0; k < GROUPS; ++k) t = fmaxf(t, gm[mine][k]);
+                sum = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-            for (int k = 0; k < GROUPS; ++k) {
-                const float f = gm[mine][k] == t ? 1.f : ex2(gm[mine][k] - t);
-                float y[8];
-                load8(&go[mine][k][8 * at], y);
-                sum += gl[mine][k] * f;
+                for (int e = 0; e < 8; ++e) v[e] = 0.f;
+                for (int k = 0; k < GROUPS; ++k) {
+                    const float f = gm[mine][k] == t ? 1.f : ex2(gm[mine][k] - t);
+                    float y[8];
+                    load8(&go[mine][k][8 * at], y);
+                    sum += gl[mine][k] * f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += y[e] * f;
+                    for (int e = 0; e < 8; ++e) v[e] += y[e] * f;
+                }
             }
+        }
+        if (group == 0 && live) {
             const float f = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= f;
             store_row8<WIDE>(a, ((long long)join.q.first + token) * a.out_stride + (long long)head * D + 8 * at, v);
         }
-        __syncthreads();
+        if constexpr (GROUPS > 1) __syncthreads();
     }
 }
 
@@ -716,11 +724,14 @@ int64_t mean_rows(const AttentionArgs &x) {
 [[maybe_unused]] bool on_tiles(const AttentionArgs &x) { return x.cache.dtype != HQ_DT_F32 && mean_rows(x) > 16; }
 int stream_rows(const AttentionArgs &x) { return mean_rows(x) <= 8 || x.cache.head_dim == 256 ? 8 : 16; }
 
-template <bool WIDE, int D>
+// MANY rows at once, or two where there are so few items that each may lie on more than 32 blocks.
+template <bool WIDE, int D, int MANY>
 hq_status run_combine(const AttnArgs &a, int rows, cudaStream_t stream) {
     if (a.blocks < 2 || a.most_units < 2) return HQ_OK;     // an item of one unit is never divided
-    return launch_blocks(attention_combine_kernel<WIDE, D>, dim3((unsigned)(a.blocks - 1), std::min(rows / kCombineRows, 8)), kCombineThreads, 0,
-                         stream, "attention combine", a, rows);
+    const long long items = (a.c.n_tokens / a.tokens + a.c.n_req) * a.c.n_kv_heads * a.parts;  // at most
+    const bool few = 32 * items < a.blocks;
+    return launch_blocks(few ? attention_combine_kernel<WIDE, D, 2> : attention_combine_kernel<WIDE, D, MANY>,
+                         dim3((unsigned)(a.blocks - 1), rows / (few ? 2 : MANY)), kCombineThreads, 0, stream, "attention combine", a, rows);
 }
 
 template <bool WIDE, int BITS, int D, int NT>
@@ -732,7 +743,7 @@ hq_status run_stream(AttnArgs a, int num_sms, cudaStream_t stream) {
     static_assert(kUnit == 1 << 6, "unit_shift");
     deal_rows(a, S::ROWS, D, 6, std::min(kStreamBlocks, num_sms * S::MIN_BLOCKS));
     st = launch_blocks(attention_stream_kernel<WIDE, BITS, D, NT>, dim3((unsigned)a.blocks), kThreads, S::SMEM, stream, "attention", a);
-    return st != HQ_OK ? st : run_combine<WIDE, D>(a, S::ROWS, stream);
+    return st != HQ_OK ? st : run_combine<WIDE, D, 2>(a, S::ROWS, stream);
 }
 
 template <bool WIDE, int BITS>
@@ -761,9 +772,11 @@ hq_status run_attention_f32(const AttentionArgs &x, const AttnArgs &a, int num_s
 
 hq_status run_attention_f32(const AttentionArgs &x, const AttnArgs &a, int num_sms, cudaStream_t stream);
 
+// Of tiles: a group of lanes a row.
 hq_status run_attention_combine(const AttnArgs &a, int rows, int dim, cudaStream_t stream) {
-    return dim == 64 ? run_combine<false, 64>(a, rows, stream) : dim == 128 ? run_combine<false, 128>(a, rows, stream)
-                                                                             : run_combine<false, 256>(a, rows, stream);
+    return dim == 64    ? run_combine<false, 64, kCombineThreads / 8>(a, rows, stream)
+           : dim == 128 ? run_combine<false, 128, kCombineThreads / 16>(a, rows, stream)
+                        : run_combine<false, 256, kCombineThreads / 32>(a, rows, stream);
 }
 
 int64_t attention_workspace(const AttentionArgs &x) {

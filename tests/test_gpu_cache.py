@@ -422,7 +422,7 @@ def test_masks(hq, batch, causal, window, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("lengths,new", [([20000], [1]), ([9000, 1, 12000], [5, 1, 8]), ([4100], [1030])])
+@pytest.mark.parametrize("lengths,new", [([20000], [1]), ([9000, 1, 12000], [5, 1, 8]), ([4100], [1030]), ([30000], [16])])
 def test_long_requests_are_split(hq, lengths, new, dtype):
     g = synthetic.rng(1400)
     b = Batch(hq, g, "q4_0", 2, 128, 64, lengths, new)
