@@ -1,15 +1,24 @@
 // hq_attention.cu -- attention of a batch's tokens over the quantized key/value
 // cache: few query rows a key/value head (single tokens, verified drafts).
 //
-// For 8 or 16 query rows of one key/value head the cache's bytes are the work, and the loads go straight from global
-// memory to the registers that decode them.  The layout of a cell is made for that: with mma.sync m16n8k16, scores are
-// S^T = K Q^T, 16 positions by 8 rows, and a lane's unit of a key's row is its part of the K operand; outputs are O^T = V^T P^T,
-// and a lane's unit of a pair of positions is its part of the V^T operand (halves of a register are neighbouring positions).
-// Quants enter as exact 16-bit integers.  A key block's scale multiplies that block's sum in fp32; a value block's scale
-// multiplies the weights, which go from one operand's layout to the other's by movmatrix.
+// For 8 or 16 query rows of one key/value head the cache's bytes are the work.  A producer warp copies cells into a ring in
+// shared memory, four to a unit, and each of four warps takes a cell of every unit.  The layout of a cell is made for that: with mma.sync
+// m16n8k16, scores are S^T = K Q^T, 16 positions by 8 rows, and a lane's unit of a key's row is its part of the K operand; outputs
+// are O^T = V^T P^T, and a lane's unit of a pair of positions is its part of the V^T operand (halves of a register are neighbouring
+// positions).  So a cell is used where it lies, without a pass that lays its quants out anew; tcgen05 would want them as a tile of
+// 128 positions in shared memory, for a product of which 8 of 128 rows are used.  Quants enter as exact 16-bit floats.  A key
+// block's scale multiplies that block's sum in fp32; a value block's scale multiplies the weights, which go from one operand's
+// layout to the other's by movmatrix.
 //
-// Weights are exp2(z - m) with m within 2^5 of the row's running maximum: it is raised, and the outputs so far
+// Weights are exp2(z - m) with m at most 5 below the row's running maximum: it is raised, and the outputs so far
 // are rescaled, only when a score passes it by that much.
+//
+// Measured (Q4_0, heads of 128): 64 requests of 100 to 8191 positions, 8 key/value heads, 4 query heads each (133 MB), 56 us = 2.4 TB/s, of
+// which 7 the joins: bound by instructions (335 a cell and warp at 0.50 to 0.67 a cycle and scheduler; tensor pipe 22 %), and by what a block
+// does before its first unit, 15 of its 90 thousand cycles.  Q8_0: one request of 131071 positions (143 MB) 38 us = 3.8 TB/s, whose
+// loop keeps up with 4 of 5 bytes of the copy rate; 10 us are the start and the joins.  Steps on the way, of these two: 6235 and 164011 with
+// a thread an output; 72 and 81 with loads from global memory to registers; 60 and 43 with the ring; 56 and 37 with units of 64
+// positions and quants that stay unsigned.
 #include <type_traits>
 
 #include "hq_attention.cuh"
@@ -652,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, (Stream<WIDE, BITS, D, NT>::MIN_BLOC
 // Joins the partial results of the item that block blockIdx.x tells of, AT_ONCE rows at a time (gridDim.y blocks share them).  D / 8
 // lanes a row of a partial result, the groups of them that a row has take every GROUPS-th block's.
 // It is bound by the latency of its loads, so its shape is a matter of how many are under way.  Few rows: two at a time with 4 to 16 groups
-// (7 us of 64 requests' 56, from a cold start; eight rows a block 61 in all); an item may lie on many blocks (131071 positions of 8 heads: 76
+// (7 us of 64 requests' 56, from a cold start; eight rows a block 61 in all); an item may lie on many blocks (131071 positions of 4 heads: 152
 // each).  Tiles: mostly two or three blocks an item, and 128 rows, so a group a row and nothing to exchange; eight groups a row,
 // with two barriers for every two rows, took 43 us of a prompt of 2011 tokens (152 in all) where this takes 11.6 (126).
 template <bool WIDE, int D, int AT_ONCE>
