@@ -86,14 +86,16 @@ __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// Plain loads: the cells may have been written by the kernel in front of this one while this block was already there, which the wait at the
+// start orders for plain loads, not for those of memory that nobody writes (times as before: 4096 tokens 1132 us).
 template <int WORDS>
 __device__ __forceinline__ void load_global(const uint8_t *p, uint32_t *v) {
-    if constexpr (WORDS == 1) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v[0]) : "l"(p));
-    else if constexpr (WORDS == 2) asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p));
+    if constexpr (WORDS == 1) asm volatile("ld.global.u32 %0, [%1];" : "=r"(v[0]) : "l"(p));
+    else if constexpr (WORDS == 2) asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p));
     else {
 #pragma unroll
         for (int i = 0; i < WORDS; i += 4)
-            asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+            asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]) : "l"(p + 4 * i));
     }
 }
