@@ -576,7 +576,7 @@ hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_s
  *   scale   : at most 2^100 in size.  Scores are fp32: they have to fit it, and a row of q whose largest element times
  *       scale passes 2^116 may come out as NaN.
  *   causal  : 1: a token sees the positions up to its own; 0: all of its request's.
- *   window  : w > 0: of those, the last w up to its own (needs causal 1); 0: no window.
+ *   window  : w > 0: of those, the last w up to its own (needs causal 1; any size: past every position it is no window); 0: no window.
  *   workspace : hq_cache_attention_workspace() bytes, 256-byte aligned, not in
  *       use by other work until the call's kernels end (a HOST function;
  *       negative: the hq_status of refused arguments).

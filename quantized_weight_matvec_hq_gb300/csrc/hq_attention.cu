@@ -807,7 +807,7 @@ hq_status launch_attention(const AttentionArgs &x, cudaStream_t stream) {
     a.group = x.n_heads / x.cache.n_kv_heads;
     a.causal = x.causal;
     a.scale = x.scale;
-    a.window = x.window;
+    a.window = window_of(x.window, a.c);
     a.partial = static_cast<float *>(x.workspace);
     a.dtype = x.cache.dtype;
     if (on_tiles(x)) return run_attention_tile(a, x.cache.fmt, x.cache.head_dim, dev->num_sms, stream);

@@ -343,6 +343,10 @@ hq_status launch_blocks(K kern, dim3 grid, int threads, int smem, cudaStream_t s
     return HQ_OK;
 }
 
+// A window of at least the positions that a request can have hides none of them: it is no window.  (Windows of any size are
+// allowed, and the sums of units are for those below 2^30.)
+inline long long window_of(long long window, const CacheView &c) { return window < c.table_width << c.page_shift ? window : 0; }
+
 // Tiles of `rows` query rows, units of 2^unit_shift positions, no more blocks than there can be units, and the workspace.
 inline void deal_rows(AttnArgs &a, int rows, int dim, int unit_shift, int blocks) {
     a.tokens = a.group <= rows ? rows / a.group : 1;

@@ -37,3 +37,19 @@ def test_rows_written_by_the_call_in_front(hq, dtype, new):
         for i in range(len(x)):
             step(i)
         assert all(torch.equal(a, w) for a, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths,new", [([40, 7, 300, 517, 1, 0, 129], [40, 7, 300, 130, 1, 0, 128]), ([16, 130, 64], [3, 5, 2])])
+def test_windows_of_any_size(hq, lengths, new, dtype):
+    """A window past every position is no window, to the bit: up to the largest number that the call takes."""
+    g = synthetic.rng(1780)
+    b = Batch(hq, g, "q8_0", 2, 128, 16, lengths, new)
+    cache = b.fill(g)
+    q = torch.from_numpy(g.standard_normal((b.T, 6, 128)).astype(np.float32)).cuda().to(DT[dtype])
+    want = b.attend(q, 6)
+    check_attention(want, q, cache, lengths, new, 6, 2, 128, dtype)
+    for window in (b.width * 16, 2 ** 30, 2 ** 31 - 1, 2 ** 31 + 7, 2 ** 40, 2 ** 63 - 20, 2 ** 63 - 1):
+        assert torch.equal(b.attend(q, 6, window=window), want), window
+    below = b.attend(q, 6, window=b.width * 16 - 1)             # (hides nothing either, but is counted as a window)
+    check_attention(below, q, cache, lengths, new, 6, 2, 128, dtype)
