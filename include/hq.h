@@ -536,7 +536,8 @@ hq_status hq_verify_drafts(const float *p, const float *q, const int32_t *drafts
  *                  parts of one projection's rows can be passed as they are.  Token tensors are 16-byte aligned.
  *   dtype        : of the token tensors, HQ_DT_*.
  * Offsets and lengths outside these ranges set HQ_FAULT_CACHE, and that request is
- * left out (nothing of it is written).  So does a page number outside [0, n_pages) that a call looks
+ * left out (nothing of it is written); the others are served.  (Of two requests in range whose tokens overlap, since offsets fall between
+ * them, a token is either's.)  So does a page number outside [0, n_pages) that a call looks
  * up: nothing is written there, what is read there is NaN.
  */
 /* HOST function: bytes of a page; negative: the hq_status of refused arguments. */

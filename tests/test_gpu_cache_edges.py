@@ -53,3 +53,54 @@ def test_windows_of_any_size(hq, lengths, new, dtype):
         assert torch.equal(b.attend(q, 6, window=window), want), window
     below = b.attend(q, 6, window=b.width * 16 - 1)             # (hides nothing either, but is counted as a window)
     check_attention(below, q, cache, lengths, new, 6, 2, 128, dtype)
+
+
+@pytest.mark.parametrize("R,spoil", [(3, {2: -1}), (3, {1: 1 << 30}), (3, {0: -5}), (64, {33: -1}), (64, {20: -(2 ** 31)}), (64, {40: 2 ** 31 - 1}),
+                                     (64, {3: 10 ** 6, 31: -7, 32: -7, 60: -1}), (700, {k: -1 for k in range(0, 700, 50)}), (64, {64: 10 ** 6}),
+                                     (1, {0: -1})])
+def test_a_bad_offset_leaves_out_its_own_requests_alone(hq, R, spoil):
+    """Wherever offsets are out of range: the rows of every good request are written and read, and no others."""
+    g = synthetic.rng(1790 + R)
+    new = g.integers(0, 4, R).astype(np.int32)
+    new[0] = 3
+    lengths = new + g.integers(0, 30, R).astype(np.int32)
+    b = Batch(hq, g, "q8_0", 2, 64, 16, lengths, new, tail=5)
+    start = b.pool.clone()
+    o = b.offsets.copy()
+    for i, x in spoil.items():
+        o[i] = x
+    good = [r for r in range(R) if 0 <= o[r] <= o[r + 1] <= b.T]
+    x = torch.from_numpy(g.standard_normal((b.T, 2, 64)).astype(np.float32)).cuda()
+    want_k = torch.full_like(x, 77.0)
+    want_v = want_k.clone()
+    table, whole = b.d_table, (b.d_offsets, b.d_lengths, b.lengths)
+    for r in good:                              # each in a call of its own
+        b.d_table, b.d_lengths, b.lengths = table[r:r + 1], dev(lengths[r:r + 1]), lengths[r:r + 1]
+        off = dev(o[r:r + 2])
+        b.write(x, -x, off)
+        hq.hq_cache_read(8, want_k, want_k.stride(0), want_v, want_v.stride(0), *b.args(off), 2, 64, 0)
+    assert hq.hq_device_fault() == 0
+    want = b.pool.clone()
+    b.d_table, (_, b.d_lengths, b.lengths) = table, whole
+    b.pool.copy_(start)
+    off = dev(o)
+    b.write(x, -x, off)
+    assert hq.hq_device_fault() == hq.HQ_FAULT_CACHE
+    assert torch.equal(b.pool, want)
+    k, v = b.read("f32", off)
+    assert hq.hq_device_fault() == hq.HQ_FAULT_CACHE
+    assert torch.equal(k, want_k) and torch.equal(v, want_v)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tokens_in_front_of_the_first_request(hq, dtype):
+    """Offsets need not begin at 0: the rows in front are no request's."""
+    g = synthetic.rng(1795)
+    b = Batch(hq, g, "q4_0", 2, 64, 16, [9, 30], [4, 2], tail=0)
+    cache = b.fill(g)
+    b.d_offsets, b.T = b.d_offsets + 6, b.T + 8
+    q = torch.from_numpy(g.standard_normal((b.T, 4, 64)).astype(np.float32)).cuda().to(DT[dtype])
+    out = b.attend(q, 4)
+    for rows in (out, *b.read("f32")):
+        assert bool((rows[:6] == 77).all()) and bool((rows[12:] == 77).all()) and not bool((rows[6:12] == 77).any())
+    check_attention(out[6:], q[6:], cache, [9, 30], [4, 2], 4, 2, 64, dtype)
