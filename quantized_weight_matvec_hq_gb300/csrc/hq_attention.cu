@@ -372,9 +372,17 @@ __device__ __forceinline__ bool stream_consume(const AttnArgs &a, const Part &pa
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float2 factor = *reinterpret_cast<const float2 *>(&s.factor[8 * n + 2 * c]);
+                // A sum is infinite through an infinite scale alone (quants and q are at most 2^15): 0 times it takes the row to NaN, where its
+                // sign could make it a score of -inf, the mark of what is not seen.
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 sums = make_float2(z[n][e], z[n][e + 1]), none = make_float2(0.f, 0.f);
+                    const float2 x = ffma2(sums, factor, ffma2(sums, none, none));
+                    z[n][e] = x.x;
+                    z[n][e + 1] = x.y;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    z[n][e] *= e & 1 ? factor.y : factor.x;
                     if (gone) z[n][e] = __uint_as_float(0x7fffffffu);
                     if (edge) {
                         const int p = p0 + g + 8 * (e >> 1);

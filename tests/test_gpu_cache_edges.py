@@ -104,3 +104,40 @@ def test_tokens_in_front_of_the_first_request(hq, dtype):
     for rows in (out, *b.read("f32")):
         assert bool((rows[:6] == 77).all()) and bool((rows[12:] == 77).all()) and not bool((rows[6:12] == 77).any())
     check_attention(out[6:], q[6:], cache, [9, 30], [4, 2], 4, 2, 64, dtype)
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("dtype,heads,new", [("bf16", 4, 2), ("f16", 8, 2), ("f32", 16, 3), ("bf16", 16, 9), ("f16", 8, 40)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_infinite_scales(hq, fmt, dtype, heads, new, dim):
+    """A pool from elsewhere: an infinite scale of a key makes the rows that see it NaN, whatever sign their sums with its quants
+    have; that of a value its block of 32.  Other rows keep their bits."""
+    g = synthetic.rng(1850 + dim + heads)
+    L = 150
+    b = Batch(hq, g, fmt, 1, dim, 32, [L], [new], tail=0)
+    b.fill(g)
+    q = torch.from_numpy(g.standard_normal((new, heads, dim)).astype(np.float32)).cuda().to(DT[dtype])
+    clean = {scale: b.attend(q, heads, scale=scale) for scale in (0.1, -0.1)}
+    bits, nb = {"q8_0": 8, "q4_0": 4}[fmt], dim // 32
+    quants = 2 * 16 * dim * bits // 8
+    cell = quants + 2 * 16 * nb * 2
+    pool = b.pool.view(torch.int16)
+    for p, block in ((3, 0), (L - 2, nb - 1), (L - 1, 1)):
+        at = int(b.table[0, p // 32]) * b.page_bytes + p % 32 // 16 * cell + quants
+        key = at + (p % 16 * nb + block) * 2
+        value = at + 16 * nb * 2 + ((p % 16 // 2 * nb + block) * 2 + p % 2) * 2
+        sees = torch.arange(L - new, L, device="cuda") >= p
+        for where in (key, value):
+            kept = pool[where // 2].clone()
+            for infinity in (0x7c00, 0xfc00 - 0x10000):
+                pool[where // 2] = infinity
+                for scale in clean:
+                    out = b.attend(q, heads, scale=scale)
+                    want = clean[scale].clone()
+                    if where == key:
+                        want[sees] = float("nan")
+                    else:
+                        want[sees, :, 32 * block:32 * block + 32] = float("nan")
+                    assert torch.equal(torch.isnan(out), torch.isnan(want)), (p, where == key, infinity, scale)
+                    assert torch.equal(out[~torch.isnan(want)], want[~torch.isnan(want)])
+            pool[where // 2] = kept
