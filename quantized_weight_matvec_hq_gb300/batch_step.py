@@ -59,9 +59,16 @@ def _expect(name, t, shape, dtype, device=None):
                          f"got {tuple(t.shape)} of {t.dtype}, strides {t.stride()}, on {t.device}")
 
 
+def _expect_current(device):
+    """The library's calls run on the current device, whatever device their addresses are of."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"calls run on the current CUDA device; what they were given is on {device}")
+
+
 class KeyValueCache:
     """A paged key/value cache in blocks of Q8_0 or Q4_0, and the library's calls on it.  A batch is told of by
-    (offsets, lengths, page_table), int32 device tensors as hq_cache_write takes them; the pages are the caller's to hand out."""
+    (offsets, lengths, page_table), int32 device tensors as hq_cache_write takes them; the pages are the caller's to hand out.
+    Calls with another device current than the cache's are refused with a ValueError."""
 
     def __init__(self, fmt, n_pages, page_size, n_kv_heads, head_dim, device="cuda"):
         self.fmt, self.n_pages, self.page, self.kv, self.dim = hq.FMT_CODES[fmt], n_pages, page_size, n_kv_heads, head_dim
@@ -89,15 +96,17 @@ class KeyValueCache:
         """k and v [tokens][n_kv_heads][head_dim] to their positions (hq_cache_write)."""
         if k.shape[0] != v.shape[0]:
             raise ValueError(f"{k.shape[0]} tokens of keys, {v.shape[0]} of values")
-        hq.hq_cache_write(self.fmt, *self._rows("k", k, self.kv), *self._rows("v", v, self.kv, k.dtype), *self._batch(batch, k.shape[0]),
-                          self.kv, self.dim, DTYPE_OF[k.dtype], stream=stream)
+        args = *self._rows("k", k, self.kv), *self._rows("v", v, self.kv, k.dtype), *self._batch(batch, k.shape[0])
+        _expect_current(self.device)
+        hq.hq_cache_write(self.fmt, *args, self.kv, self.dim, DTYPE_OF[k.dtype], stream=stream)
 
     def read(self, k, v, batch, stream=None):
         """The values of the tokens' positions into k and v (hq_cache_read)."""
         if k.shape[0] != v.shape[0]:
             raise ValueError(f"{k.shape[0]} tokens of keys, {v.shape[0]} of values")
-        hq.hq_cache_read(self.fmt, *self._rows("k", k, self.kv), *self._rows("v", v, self.kv, k.dtype), *self._batch(batch, k.shape[0]),
-                         self.kv, self.dim, DTYPE_OF[k.dtype], stream=stream)
+        args = *self._rows("k", k, self.kv), *self._rows("v", v, self.kv, k.dtype), *self._batch(batch, k.shape[0])
+        _expect_current(self.device)
+        hq.hq_cache_read(self.fmt, *args, self.kv, self.dim, DTYPE_OF[k.dtype], stream=stream)
 
     def workspace_bytes(self, n_req, table_width, n_tokens, n_heads, dtype):
         return hq.hq_cache_attention_workspace(self.fmt, self.page, table_width, n_req, n_tokens, n_heads, self.kv, self.dim,
@@ -112,6 +121,7 @@ class KeyValueCache:
         q, q_stride = self._rows("q", q, heads)
         out, out_stride = self._rows("out", out, heads, q.dtype)
         _expect("workspace", workspace, (workspace.numel(),), torch.uint8, self.device)
+        _expect_current(self.device)
         hq.hq_cache_attention(self.fmt, q, q_stride, *args, heads, self.kv, self.dim, self.dim ** -0.5 if scale is None else scale,
                               int(causal), window, out, out_stride, DTYPE_OF[q.dtype], workspace, workspace.numel(), stream=stream)
 
@@ -147,6 +157,7 @@ class BatchStep:
         self.E, self.k, self.hidden, self.ffn, self.vocab, self.most = n_experts, n_active, hidden, ffn, vocab, most_tokens
         self.dtype_name = dtype
         self.dtype, self.x_dtype, self.device = hq.DTYPE_CODES[dtype], TORCH_DTYPES[dtype], dev
+        _expect_current(dev)
 
         def exponents(W, mats, rows, cols):
             e = torch.empty(mats, dtype=torch.int32, device=dev)
@@ -223,7 +234,7 @@ class BatchStep:
                  cache=None, stream=None):
         """x [T][hidden], expert_ids int32 and router_w fp32 [T][n_active], adapter_ids int32 and temperature fp32 [T],
         for the T = len(drafts) + len(u_sample) positions; the rest as hq_verify_drafts takes it, device
-        tensors all; others are refused with a ValueError.  cache (with an Attention): (position_offsets(offsets), lengths,
+        tensors all, on the current device; others are refused with a ValueError.  cache (with an Attention): (position_offsets(offsets), lengths,
         page_table), lengths with this step's positions in them.  Returns its n_accepted and tokens, which the next call overwrites."""
         T, R = x.shape[0], u_sample.shape[0]
         if T != drafts.shape[0] + R or T > self.most:
@@ -231,6 +242,7 @@ class BatchStep:
         self._check_inputs(x, expert_ids, router_w, adapter_ids, temperature, drafts, offsets, u_accept, u_sample, q)
         if (cache is not None) != (self.attention is not None):
             raise ValueError("a cache is given with an Attention, and only then")
+        _expect_current(self.device)
         ws = self.workspace
         if self.attention is not None:
             x = self._attend(x, cache, T, R, stream)
