@@ -588,7 +588,8 @@ hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_s
  * times the values' scales are taken in two 11-bit terms.  f16 and bf16, at most 16 rows a key/value head of the mean
  * request: the weights times their value block's scale are rounded to 11 bits; scores are off by up to 2^-22 of the position's
  * largest key element times the sum of |q|.  f16 and bf16, more rows: the weights are rounded to 11 bits, and
- * so are the stored keys and values, or to 2^-19 of their largest in 32 neighbouring positions where that is coarser.  q is exact,
+ * so are the stored keys and values, or to 2^-17 (Q4_0) or 2^-20 (Q8_0) of the largest that 32 neighbouring positions can hold (8 or
+ * 127 times their largest scale) where that is coarser.  q is exact,
  * but for elements below 2^-24 of their row's largest.
  * Deterministic: a token's bits depend on its own request, and on the others only through
  * the split of the positions over CTAs.

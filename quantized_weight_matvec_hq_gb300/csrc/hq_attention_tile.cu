@@ -20,7 +20,8 @@
 //
 // Ranges.  Q rows are scaled as in the kernel for few rows.  K and V^T of 32 neighbouring positions are scaled by
 // the power of two that takes their largest scale to the top of what 16 bits hold (2^-6 or 2^-2 for the largest element), so an element
-// is rounded to 11 bits or 2^-19 of the largest near it.  Scores of those 32 columns get K's power back in fp32; V's joins
+// is rounded to 11 bits, or, where its scale is so far below that the offset's product is subnormal, to 2^-17 (Q4_0) or 2^-20 (Q8_0) of the
+// largest near it: two roundings of half the finest step, 2^-25, of at least 2^-7 or 2^-3.  Scores of those 32 columns get K's power back in fp32; V's joins
 // the exponent of the weights, whose reference is thus the largest weight times value, and the sum of the weights leaves it out.
 #include <algorithm>
 #include <atomic>
@@ -142,7 +143,8 @@ __device__ __forceinline__ void raw_pairs(const uint32_t *w, uint32_t (&h)[4]) {
     }
 }
 
-// raw quants times scale d (normalised): 4 bits: d 2^-20 (n - 8), 8 bits: d 2^-24 (u - 128); one rounding each.
+// raw quants times scale d (normalised): 4 bits: d 2^-20 (n - 8), 8 bits: d 2^-24 (u - 128); one rounding each, and one
+// of the offset's product where that is subnormal.
 template <int BITS>
 __device__ __forceinline__ void scaled_pairs(uint32_t (&h)[4], __half2 d) {
     const __half2 off = __hmul2(d, __half2half2(__ushort_as_half(0x8080)));         // -2^-17

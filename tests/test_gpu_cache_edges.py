@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from quantized_weight_matvec_hq_gb300 import synthetic
-from test_gpu_cache import DT, Batch, check_attention, dev, hq, no_device_fault  # noqa: F401
+from test_gpu_cache import DT, Batch, check_attention, dev, hq, no_device_fault, stored, values  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -141,3 +141,26 @@ def test_infinite_scales(hq, fmt, dtype, heads, new, dim):
                     assert torch.equal(torch.isnan(out), torch.isnan(want)), (p, where == key, infinity, scale)
                     assert torch.equal(out[~torch.isnan(want)], want[~torch.isnan(want)])
             pool[where // 2] = kept
+
+
+@pytest.mark.parametrize("fmt,bound", [("q4_0", 2.0 ** -17), ("q8_0", 2.0 ** -20)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_values_far_below_others_in_tiles(hq, fmt, bound, dim):
+    """Rows that see one position each give its stored values: 11 bits, or `bound` of the largest that the scales of 32
+    neighbouring positions allow (test_tile_rounding has the proof), times a weight over itself (2^-11: the weight's own 11 bits,
+    the power and the quotient), rounded to f16."""
+    g = synthetic.rng(1900 + dim)
+    n, heads = 256, 2
+    b = Batch(hq, g, fmt, 1, dim, 64, [n], [n], "f16", tail=0)
+    size = np.exp2(-g.uniform(0, 13, (n, 1, dim // 32, 1)))
+    size[::8] = 1                               # the largest is near every position
+    v = (g.uniform(-1, 1, (n, 1, dim // 32, 32)) * size * 512).astype(np.float32).reshape(n, 1, dim)
+    b.write(torch.zeros((n, 1, dim), device="cuda"), dev(v))
+    d, quants = stored(v, fmt)
+    exact = torch.from_numpy(values(d, quants)).cuda()
+    most = np.abs(d.astype(np.float64)).reshape(n // 32, -1).max(1).repeat(32) * (127 if fmt == "q8_0" else 8)
+    q = torch.zeros((n, heads, dim), dtype=torch.float16, device="cuda")
+    got = b.attend(q, heads, window=1).double()
+    tol = bound * torch.from_numpy(most).cuda()[:, None, None] + 2.0 ** -10 * exact.abs()
+    tol = tol + 2.0 ** -11 * (exact.abs() + tol) + 2.0 ** -25
+    assert bool(((got - exact).abs() <= tol).all()), float(((got - exact).abs() / tol).max())
