@@ -526,7 +526,8 @@ hq_status hq_verify_drafts(const float *p, const float *q, const int32_t *drafts
  *   lengths      : int32 [n_req] (device), the positions of request r, its
  *                  tokens included: its token i of n is at position lengths[r] - n + i.
  *                  0 <= lengths[r] <= table_width * page_size.  A token at a negative position
- *                  (a length below n) has no place in the cache: it is not written, reads as zeros, sees nothing.
+ *                  (a length below n) has no place in the cache: it is not written, reads as zeros, and sees nothing
+ *                  where attention is causal (where it is not, what every token of its request sees).
  *   n_req        : 0..2^20 (0 launches nothing).
  *   n_tokens     : 0..2^27 (0 launches nothing), the rows of the token tensors;
  *                  offsets[n_req] <= n_tokens.  Rows that are no request's (behind the last one's) stay as they are.

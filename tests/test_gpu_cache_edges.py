@@ -164,3 +164,19 @@ def test_values_far_below_others_in_tiles(hq, fmt, bound, dim):
     tol = bound * torch.from_numpy(most).cuda()[:, None, None] + 2.0 ** -10 * exact.abs()
     tol = tol + 2.0 ** -11 * (exact.abs() + tol) + 2.0 ** -25
     assert bool(((got - exact).abs() <= tol).all()), float(((got - exact).abs() / tol).max())
+
+
+@pytest.mark.parametrize("dtype,heads,new", [("bf16", 2, 6), ("f32", 2, 6), ("f16", 8, 30)])
+def test_tokens_at_negative_positions(hq, dtype, heads, new):
+    """Causal: zeros.  Not causal: what their request's other tokens see, to the bit with the same query."""
+    g = synthetic.rng(1950)
+    b = Batch(hq, g, "q8_0", 1, 64, 16, [4, 1], [new, 3])
+    cache = b.fill(g)
+    q = torch.from_numpy(g.standard_normal((1, heads, 64)).astype(np.float32)).cuda().to(DT[dtype]).repeat(b.T, 1, 1)
+    out = b.attend(q, heads, causal=1)
+    assert bool((out[:new - 4] == 0).all()) and bool((out[new:new + 2] == 0).all())
+    check_attention(out, q, cache, [4, 1], [new, 3], heads, 1, 64, dtype)
+    out = b.attend(q, heads, causal=0)
+    for rows in (out[:new], out[new:new + 3]):
+        assert torch.equal(rows, rows[-1:].expand_as(rows)) and bool((rows != 0).any())
+    check_attention(out, q, cache, [4, 1], [new, 3], heads, 1, 64, dtype, 0)
