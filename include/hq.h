@@ -587,13 +587,14 @@ hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_s
  * see it NaN; a value block's makes that block's 32 elements NaN.
  * Accuracy: scores, maxima, sums and outputs are fp32.  f32 tokens: quants are exact, q and the weights
  * times the values' scales are taken in two 11-bit terms.  f16 and bf16, at most 16 rows a key/value head of the mean
- * request: the weights times their value block's scale are rounded to 11 bits; scores are off by up to 2^-22 of the position's
+ * request (n_tokens / n_req, rounded up, times n_heads / n_kv_heads): the weights times their value block's scale are rounded to 11 bits; scores are off by up to 2^-22 of the position's
  * largest key element times the sum of |q|.  f16 and bf16, more rows: the weights are rounded to 11 bits, and
  * so are the stored keys and values, or to 2^-17 (Q4_0) or 2^-20 (Q8_0) of the largest that 32 neighbouring positions can hold (8 or
  * 127 times their largest scale) where that is coarser.  q is exact,
  * but for elements below 2^-24 of their row's largest.
- * Deterministic: a token's bits depend on its own request, and on the others only through
- * the split of the positions over CTAs.
+ * Deterministic: the same call gives the same bits.  Between batches a token's bits may differ, within the accuracy above: the rest of the
+ * batch decides the split of the positions over CTAs, and n_tokens / n_req (rows behind the last request and requests without tokens
+ * count) decides which of the two kernels runs, and with it the rounding of f16 and bf16 tokens.
  * Source: "DeepSeek-V4 on Hanzo Engine", section "A Fused Attention Kernel
  * for 512-Wide Latent Heads" (attention over the decode cache, one to eight
  * verified rows a request).

@@ -180,3 +180,23 @@ def test_tokens_at_negative_positions(hq, dtype, heads, new):
     for rows in (out[:new], out[new:new + 3]):
         assert torch.equal(rows, rows[-1:].expand_as(rows)) and bool((rows != 0).any())
     check_attention(out, q, cache, [4, 1], [new, 3], heads, 1, 64, dtype, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("new", [2, 40])
+def test_one_request_in_different_batches(hq, dtype, new):
+    """Alone, beside requests without tokens and before rows that are no request's: either kernel runs, by the mean request.  The
+    bits may differ between these, each is within the tolerance, and the same call gives the same bits."""
+    g = synthetic.rng(1960 + new)
+    heads, kv, dim, L = 8, 2, 128, 333
+    q = torch.from_numpy(g.standard_normal((new + 200, heads, dim)).astype(np.float32)).cuda().to(DT[dtype])
+    for idle in (0, 1, 15, 63):
+        for tail in (0, 200):
+            g = synthetic.rng(1961)
+            b = Batch(hq, g, "q4_0", kv, dim, 16, [L] + [50] * idle, [new] + [0] * idle, tail=tail)
+            cache = b.fill(g)
+            rows = q[:new + tail]
+            out = b.attend(rows, heads)
+            assert bool((out[new:] == 77).all())
+            check_attention(out, rows, cache, [L], [new], heads, kv, dim, dtype, what=(idle, tail))
+            assert torch.equal(b.attend(rows, heads), out)
