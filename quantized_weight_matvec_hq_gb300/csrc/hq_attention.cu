@@ -129,8 +129,7 @@ struct Stream {
     static constexpr float BACK0 = RAW ? 0x1p24f : 1.f, BACK1 = RAW ? BITS == 4 ? 0x1p20f : 0x1p24f : 1.f;
     static constexpr int ROWS = 8 * NT, NB = L::NB;
     static constexpr int STAGE = kWarps * L::BYTES;     // a stage of the ring is a unit
-    // Blocks a multiprocessor, by the registers that a thread needs (of 5 warps each; 4: 96, 3: 128, 2: 168).
-    static constexpr int MIN_BLOCKS = NT == 1 ? (D == 256 ? 2 : WIDE && D == 128 ? 3 : 4) : D == 64 && !WIDE ? 3 : 2;
+    static constexpr int MIN_BLOCKS = stream_blocks(WIDE, D, ROWS);
     static constexpr int MAX_STAGES = 6;
 
     // The power of two for scales with this largest exponent field (the value is in [2^(e - 15), 2^(e - 14))).
@@ -758,7 +757,7 @@ hq_status run_stream(AttnArgs a, int num_sms, cudaStream_t stream) {
     hq_status st = allow_smem(attention_stream_kernel<WIDE, BITS, D, NT>, S::SMEM, done);
     if (st != HQ_OK) return st;
     static_assert(kUnit == 1 << 6, "unit_shift");
-    deal_rows(a, S::ROWS, D, 6, std::min(kStreamBlocks, num_sms * S::MIN_BLOCKS));
+    deal_rows(a, S::ROWS, D, 6, std::min(kSms, num_sms) * S::MIN_BLOCKS);
     st = launch_blocks(attention_stream_kernel<WIDE, BITS, D, NT>, dim3((unsigned)a.blocks), kThreads, S::SMEM, stream, "attention", a);
     return st != HQ_OK ? st : run_combine<WIDE, D, 2>(a, S::ROWS, stream);
 }
@@ -797,8 +796,9 @@ hq_status run_attention_combine(const AttnArgs &a, int rows, int dim, cudaStream
 }
 
 int64_t attention_workspace(const AttentionArgs &x) {
-    const int64_t rows = on_tiles(x) ? 128 : stream_rows(x), blocks = on_tiles(x) ? kTileBlocks : kStreamBlocks;
-    return 2 * blocks * rows * (x.cache.head_dim + 2) * 4 + blocks * (int64_t)sizeof(Join);
+    const int dim = x.cache.head_dim, rows = on_tiles(x) ? 128 : stream_rows(x);
+    const int64_t blocks = (int64_t)kSms * (on_tiles(x) ? tile_blocks(dim) : stream_blocks(x.cache.dtype == HQ_DT_F32, dim, rows));
+    return 2 * blocks * rows * (dim + 2) * 4 + blocks * (int64_t)sizeof(Join);
 }
 
 hq_status launch_attention(const AttentionArgs &x, cudaStream_t stream) {

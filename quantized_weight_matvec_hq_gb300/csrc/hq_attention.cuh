@@ -311,7 +311,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ host side
 
-constexpr int kStreamBlocks = 608, kTileBlocks = 304;       // at most: the workspace holds two partial results of each
+// Blocks of a launch: those that fit a multiprocessor, by the registers that a thread needs (few rows, of 5 warps each: 4 blocks 96, 3: 128,
+// 2: 168), or the shared memory (tiles).  At most kSms times that: the workspace holds two partial results of each.
+constexpr int kSms = 152;
+constexpr int stream_blocks(bool wide, int dim, int rows) {
+    return rows == 8 ? (dim == 256 ? 2 : wide && dim == 128 ? 3 : 4) : dim == 64 && !wide ? 3 : 2;
+}
+constexpr int tile_blocks(int dim) { return dim == 256 ? 1 : 2; }
 
 // Allows a kernel its shared memory, once a device.
 template <class K>

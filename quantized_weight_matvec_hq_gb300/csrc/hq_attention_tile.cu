@@ -105,7 +105,7 @@ template <int BITS, int D>
 struct Tile {
     using L = CellLayout<BITS, D>;
     static constexpr int NB = L::NB;
-    static constexpr int MIN_BLOCKS = D == 256 ? 1 : 2;
+    static constexpr int MIN_BLOCKS = tile_blocks(D);
     static constexpr uint32_t TMEM = D == 256 ? 512 : 256;  // columns: scores (and in their place weights) 0..127, outputs from 128
     static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = kUnit * D * 2, V_BYTES = kUnit * D * 2;
     struct Shared {
@@ -744,7 +744,7 @@ hq_status run(AttnArgs a, int num_sms, cudaStream_t stream) {
     static std::atomic<bool> done[64];
     hq_status st = allow_smem(attention_tile_kernel<BITS, D>, T::SMEM, done);
     if (st != HQ_OK) return st;
-    deal_rows(a, kRows, D, 7, std::min(kTileBlocks, num_sms * T::MIN_BLOCKS));
+    deal_rows(a, kRows, D, 7, std::min(kSms, num_sms) * T::MIN_BLOCKS);
     st = launch_blocks(attention_tile_kernel<BITS, D>, dim3((unsigned)a.blocks), kThreads, T::SMEM, stream, "attention", a);
     return st != HQ_OK ? st : run_attention_combine(a, kRows, D, stream);
 }
