@@ -581,7 +581,8 @@ hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_s
  *   window  : w > 0: of those, the last w up to its own (needs causal 1; any size: past every position it is no window); 0: no window.
  *   workspace : hq_cache_attention_workspace() bytes, 256-byte aligned, not in
  *       use by other work until the call's kernels end (a HOST function;
- *       negative: the hq_status of refused arguments).
+ *       negative: the hq_status of refused arguments).  It is enough for batches of fewer tokens or requests too, and
+ *       does not grow with them without end: at most 39 MiB.
  * A token that sees no position gets zeros.  Positions that a token does not see do
  * not touch it, whatever they hold.  One whose key has a NaN or infinite scale makes the rows that
  * see it NaN; a value block's makes that block's 32 elements NaN.

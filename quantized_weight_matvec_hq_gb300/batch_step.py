@@ -109,6 +109,7 @@ class KeyValueCache:
         hq.hq_cache_read(self.fmt, *args, self.kv, self.dim, DTYPE_OF[k.dtype], stream=stream)
 
     def workspace_bytes(self, n_req, table_width, n_tokens, n_heads, dtype):
+        """Of a batch, and of every one of fewer tokens or requests (hq_cache_attention_workspace)."""
         return hq.hq_cache_attention_workspace(self.fmt, self.page, table_width, n_req, n_tokens, n_heads, self.kv, self.dim,
                                                hq.DTYPE_CODES[dtype])
 
@@ -192,10 +193,9 @@ class BatchStep:
                 hq.hq_matmul_adapters_workspace(self.rank, self.vocab, self.hidden, T, self.dtype))
         if self.attention is not None:
             a, c = self.attention, self.attention.cache
-            # which of the attention's kernels runs goes by the tokens of the mean request: one request with all, or one each
             need += (hq.hq_matmul_adapters_workspace(1, self.width, self.hidden, T, self.dtype),
                      hq.hq_matmul_adapters_workspace(1, self.hidden, a.heads * c.dim, T, self.dtype),
-                     *(c.workspace_bytes(R, a.most_pages, T, a.heads, self.dtype_name) for R in (1, T)))
+                     c.workspace_bytes(T, a.most_pages, T, a.heads, self.dtype_name))
         if min(need) < 0:
             raise ValueError("sizes that the library refuses")
         return max(1, *need)

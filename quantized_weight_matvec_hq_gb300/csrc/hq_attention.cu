@@ -795,10 +795,21 @@ hq_status run_attention_combine(const AttnArgs &a, int rows, int dim, cudaStream
                         : run_combine<false, 256, kCombineThreads / 32>(a, rows, stream);
 }
 
+// Of the batch and of every one of fewer tokens or requests, whose mean request has group to n_tokens * group query rows a key/value
+// head: a buffer for the largest batch serves the others.
 int64_t attention_workspace(const AttentionArgs &x) {
-    const int dim = x.cache.head_dim, rows = on_tiles(x) ? 128 : stream_rows(x);
-    const int64_t blocks = (int64_t)kSms * (on_tiles(x) ? tile_blocks(dim) : stream_blocks(x.cache.dtype == HQ_DT_F32, dim, rows));
-    return 2 * blocks * rows * (dim + 2) * 4 + blocks * (int64_t)sizeof(Join);
+    const int dim = x.cache.head_dim;
+    const bool wide = x.cache.dtype == HQ_DT_F32;
+    auto bytes = [&](int64_t rows, int blocks) {
+        return (int64_t)kSms * blocks * (2 * rows * (dim + 2) * 4 + (int64_t)sizeof(Join));
+    };
+    AttentionArgs least = x, most = x;
+    least.cache.n_req = least.cache.n_tokens;
+    most.cache.n_req = 1;
+    int64_t need = 0;
+    for (const int rows : {8, 16})
+        if (stream_rows(least) <= rows && rows <= stream_rows(most)) need = std::max(need, bytes(rows, stream_blocks(wide, dim, rows)));
+    return on_tiles(most) ? std::max(need, bytes(128, tile_blocks(dim))) : need;
 }
 
 hq_status launch_attention(const AttentionArgs &x, cudaStream_t stream) {

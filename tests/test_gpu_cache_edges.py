@@ -200,3 +200,19 @@ def test_one_request_in_different_batches(hq, dtype, new):
             assert bool((out[new:] == 77).all())
             check_attention(out, rows, cache, [L], [new], heads, kv, dim, dtype, what=(idle, tail))
             assert torch.equal(b.attend(rows, heads), out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_one_workspace_for_batches_of_every_size(hq, dim, dtype):
+    """What 64 single tokens need is enough for each batch of fewer tokens or requests; nothing behind it is written."""
+    g = synthetic.rng(1970 + dim)
+    heads, kv = 8, 2
+    need = hq.hq_cache_attention_workspace(8, 16, 64, 64, 64, heads, kv, dim, hq.DTYPE_CODES[dtype])
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+    for lengths, new in (([300] * 64, [1] * 64), ([900], [64]), ([900], [1]), ([700, 800], [5, 30]), ([90] * 20, [3] * 20)):
+        b = Batch(hq, g, "q8_0", kv, dim, 16, lengths, new, width=64, tail=0)
+        b.fill(g)
+        q = torch.from_numpy(g.standard_normal((b.T, heads, dim)).astype(np.float32)).cuda().to(DT[dtype])
+        assert torch.equal(b.attend(q, heads, ws=ws[:need]), b.attend(q, heads))
+        assert bool((ws[need:] == 255).all())
