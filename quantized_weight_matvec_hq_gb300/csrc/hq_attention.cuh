@@ -31,7 +31,7 @@ struct AttnArgs {
     float *partial;                     // [2 blocks][rows][head_dim]
     float2 *stat;                       // [2 blocks][rows]: maximum and sum of a partial result
     struct Join *joins;                 // [blocks]
-    int unit_shift, blocks, min_units;
+    int unit_shift, blocks;
     long long most_units;               // an item can have
 };
 
@@ -183,15 +183,15 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
     return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
-// The first unit of block `b`.  Few units go to few blocks, min_units each.
+// The first unit of block `b`.  Fewer units than blocks go to as many blocks.
 __device__ __forceinline__ long long first_unit(const AttnArgs &a, long long total, int b) {
-    const long long n = min((long long)a.blocks, max(1ll, quotient(total, a.min_units)));
+    const long long n = min((long long)a.blocks, total);
     return b >= n ? total : quotient(total * b, n);
 }
 
 // The block that has a unit.
 __device__ __forceinline__ int block_of(const AttnArgs &a, long long total, long long unit) {
-    const long long n = min((long long)a.blocks, max(1ll, quotient(total, a.min_units)));
+    const long long n = min((long long)a.blocks, total);
     return (int)quotient((unit + 1) * n - 1, total);
 }
 
@@ -365,7 +365,6 @@ inline void deal_rows(AttnArgs &a, int rows, int dim, int unit_shift, int blocks
     const double most = (double)tiles * a.c.n_kv_heads * a.parts * a.most_units;
     a.blocks = blocks;
     if (most < a.blocks) a.blocks = (int)most;
-    a.min_units = 1;
     a.stat = reinterpret_cast<float2 *>(a.partial + 2ll * a.blocks * rows * dim);
     a.joins = reinterpret_cast<Join *>(a.stat + 2ll * a.blocks * rows);
 }

@@ -8,7 +8,7 @@ import subprocess
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "quantized_weight_matvec_hq_gb300", "csrc")
-FUNCTIONS = ("floor_sum", "unit_sum", "seen_by", "tiles_of", "units_before", "window_of")
+FUNCTIONS = ("floor_sum", "unit_sum", "seen_by", "tiles_of", "units_before", "window_of", "quotient", "first_unit", "block_of")
 
 HARNESS = r"""
 #include <algorithm>
@@ -18,13 +18,31 @@ HARNESS = r"""
 #define __forceinline__ inline
 using std::max; using std::min;
 struct CacheView { long long table_width; int page_shift; };
-struct AttnArgs { CacheView c; int tokens, causal, unit_shift; long long window; };
+struct AttnArgs { CacheView c; int tokens, causal, unit_shift, blocks; long long window; };
 struct Request { int first, n, length; bool bad; };
 %s
 // argv: the window of the call, then a request's tokens and length, a tile's tokens, the unit, causal.  Prints the units before
 // each tile, and counted tile by tile: from the first position that its first token sees to the last one's last.
+// With two arguments, the units and the blocks: that the blocks' ranges follow one another to the end, and which block has a unit.
 int main(int argc, char **argv) {
     AttnArgs a;
+    if (argc == 3) {
+        const long long total = std::atoll(argv[1]);
+        a.blocks = std::atoi(argv[2]);
+        long long at = 0, wrong = first_unit(a, total, 0) != 0, most = 0, least = total;
+        for (int b = 0; b < a.blocks; ++b) {
+            const long long x0 = first_unit(a, total, b), end = first_unit(a, total, b + 1);
+            wrong += x0 != at || end < x0;
+            if (end > x0) {
+                wrong += block_of(a, total, x0) != b || block_of(a, total, end - 1) != b || block_of(a, total, (x0 + end) / 2) != b;
+                most = max(most, end - x0);
+                least = min(least, end - x0);
+            }
+            at = end;
+        }
+        std::printf("%%lld\n", wrong + (at != total) + (total > 0 && most - least > 1));
+        return 0;
+    }
     a.c = {1 << 10, 6};
     a.window = window_of(std::atoll(argv[1]), a.c);
     const Request q = {0, std::atoi(argv[2]), std::atoi(argv[3]), false};
@@ -75,3 +93,10 @@ def test_units_of_tiles(harness, window):
                 lines = subprocess.run([harness, *args], check=True, capture_output=True, text=True).stdout.split("\n")[:-1]
                 wrong = [i for i in lines if len(set(i.split())) != 1]
                 assert not wrong, (args, len(wrong), len(lines), wrong[:2])
+
+
+@pytest.mark.parametrize("total", [0, 1, 2, 7, 303, 304, 305, 607, 608, 609, 12345, 10 ** 6, 2 ** 31 + 1, 2 ** 40 + 12345])
+def test_units_of_blocks(harness, total):
+    """Equal contiguous shares, one unit apart at most; a block finds the block of any unit."""
+    for blocks in (1, 2, 152, 304, 456, 608):
+        assert subprocess.run([harness, str(total), str(blocks)], check=True, capture_output=True, text=True).stdout == "0\n", blocks
