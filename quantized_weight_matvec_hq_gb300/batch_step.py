@@ -90,7 +90,7 @@ class KeyValueCache:
                 t.dtype not in TORCH_DTYPES.values() or (t.shape[0] > 0 and (t.stride(2) != 1 or t.stride(1) != self.dim)):
             raise ValueError(f"{name}: [tokens][{heads}][{self.dim}], a token's heads together, on {self.device} expected; got "
                              f"{tuple(t.shape)} of {t.dtype}, strides {t.stride()}, on {t.device}")
-        return t, max(t.stride(0), heads * self.dim) if t.shape[0] < 2 else t.stride(0)
+        return t, heads * self.dim if t.shape[0] < 2 else t.stride(0)          # (one token's may be anything)
 
     def write(self, k, v, batch, stream=None):
         """k and v [tokens][n_kv_heads][head_dim] to their positions (hq_cache_write)."""
