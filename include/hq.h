@@ -537,8 +537,8 @@ hq_status hq_verify_drafts(const float *p, const float *q, const int32_t *drafts
  *                  parts of one projection's rows can be passed as they are.  Token tensors are 16-byte aligned.
  *   dtype        : of the token tensors, HQ_DT_*.
  * Offsets and lengths outside these ranges set HQ_FAULT_CACHE, and that request is
- * left out (nothing of it is written); the others are served.  (Of two requests in range whose tokens overlap, since offsets fall between
- * them, a token is either's.)  So does a page number outside [0, n_pages) that a call looks
+ * left out (nothing of it is written); the others are served.  (Where offsets fall, requests in range may overlap:
+ * a token's row is then either's, or parts of both.)  So does a page number outside [0, n_pages) that a call looks
  * up: nothing is written there, what is read there is NaN.
  */
 /* HOST function: bytes of a page; negative: the hq_status of refused arguments. */
@@ -598,7 +598,7 @@ hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_s
  * count) decides which of the two kernels runs, and with it the rounding of f16 and bf16 tokens.
  * Source: "DeepSeek-V4 on Hanzo Engine", section "A Fused Attention Kernel
  * for 512-Wide Latent Heads" (attention over the decode cache, one to eight
- * verified rows a request).
+ * verified rows a request; its heads of 512 are wider than those here).
  */
 int64_t hq_cache_attention_workspace(int fmt, int page_size, int64_t table_width, int64_t n_req, int64_t n_tokens,
                                      int n_heads, int n_kv_heads, int head_dim, int dtype);

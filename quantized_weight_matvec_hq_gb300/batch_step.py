@@ -130,7 +130,8 @@ class KeyValueCache:
 class Attention:
     """The attention layer of a step: qkv: Q8_0 blocks of [(n_heads + 2 n_kv_heads) head_dim][hidden], out: of
     [hidden][n_heads head_dim] (uint8 device tensors), over a KeyValueCache; a request has at most
-    `most_pages` pages.  window: 0, or how many positions a token looks back on, its own included."""
+    `most_pages` pages.  window: 0, or how many positions a token looks back on, its own included.  There are no norms, rotary
+    positions or residual sums in it: a model with those calls KeyValueCache between its own steps."""
 
     def __init__(self, qkv, out, n_heads, cache, most_pages, window=0):
         self.qkv, self.out, self.heads, self.cache, self.most_pages, self.window = qkv, out, n_heads, cache, most_pages, window

@@ -737,6 +737,8 @@ __global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(cons
 int64_t mean_rows(const AttentionArgs &x) {
     return (x.cache.n_tokens + x.cache.n_req - 1) / x.cache.n_req * (x.n_heads / x.cache.n_kv_heads);
 }
+// Tiles above 16 rows: 32 requests of 500 to 4000 positions take (few rows / tiles) 30 / 35 us at 16 rows and 47 / 36 at 32 with heads of 128, 34 / 45 and
+// 54 / 46 with heads of 64, 33 / 47 and 52 / 48 with heads of 256.
 [[maybe_unused]] bool on_tiles(const AttentionArgs &x) { return x.cache.dtype != HQ_DT_F32 && mean_rows(x) > 16; }
 int stream_rows(const AttentionArgs &x) { return mean_rows(x) <= 8 || x.cache.head_dim == 256 ? 8 : 16; }
 

@@ -10,7 +10,7 @@
 //   1 walker warp    finds the parts and the addresses of their cells, and asks for them ahead into L2
 // Two blocks a multiprocessor (D 256: one) fill each other's gaps.
 //
-// Measured: Q4_0, f16, heads of 128, 4096 tokens behind 12289 positions, 32 on 8 heads (962 GFLOP): 1135 us = 848 TFLOP/s, 44 % of what a
+// Measured: Q4_0, f16, heads of 128, 4096 tokens behind 12289 positions, 32 on 8 heads (962 GFLOP): 1131 us = 851 TFLOP/s, 44 % of what a
 // large bf16 product reaches.  A prompt of 2011 tokens, Q8_0 (33 GFLOP): 126 us.  Bound by the chain of a unit, S, softmax, O: the weights take the
 // place of the scores in tensor memory, so the next unit's S waits for O, and two blocks hide part of that (tensor pipe 36 % busy, issue slots
 // 57 %).  The short prompt: 14 units a block, among them the start and end of two or three tiles, then 12 us of joins.  On the way, of these

@@ -7,7 +7,7 @@
 //
 // Measured, Q8_0, 8 heads of 128.  Written: 11296 tokens of three prompts, f16 (71 MB in and out), 32 us from a cold start, 2.2 TB/s: bound by
 // instructions (0.71 a cycle and scheduler), of which the quotients are the largest part; a division each took 38 us.  Written and
-// read back, 62 us with a head a block, 51 with four, 44 without divisions.  Read: the positions of 16 requests, bf16 (563 MB), 119 us = 4.7 TB/s, 0.70 of the copy rate (0.61 a cycle and scheduler, otherwise
+// read back, 62 us with a head a block, 51 with four, 44 without divisions.  Read: the positions of 16 requests, bf16 (563 MB), 120 us = 4.7 TB/s, 0.70 of the copy rate (0.62 a cycle and scheduler, otherwise
 // waits for loads of the cells' 2- and 8-byte pieces, four heads' under way at once); a head a block 158.
 #include <type_traits>
 
@@ -337,7 +337,7 @@ hq_status launch_rows(bool write, const RowsArgs &a, cudaStream_t stream) {
     return HQ_OK;
 }
 
-// Four heads a block where that leaves blocks for every multiprocessor (16 requests read 121 us, a head a block 158); few rows spread over
+// Four heads a block where that leaves blocks for every multiprocessor (16 requests read 120 us, a head a block 158); few rows spread over
 // more blocks (64 tokens: a block each of 8 tokens and a head).
 template <class T, int BITS, int D>
 hq_status launch_heads(bool write, const RowsArgs &a, cudaStream_t stream) {
