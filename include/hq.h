@@ -589,9 +589,9 @@ hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_s
  * Accuracy: scores, maxima, sums and outputs are fp32.  f32 tokens: quants are exact, q and the weights
  * times the values' scales are taken in two 11-bit terms.  f16 and bf16, at most 16 rows a key/value head of the mean
  * request (n_tokens / n_req, rounded up, times n_heads / n_kv_heads): the weights times their value block's scale are rounded to 11 bits; scores are off by up to 2^-22 of the position's
- * largest key element times the sum of |q|.  f16 and bf16, more rows: the weights are rounded to 11 bits, and
- * so are the stored keys and values, or to 2^-17 (Q4_0) or 2^-20 (Q8_0) of the largest that 32 neighbouring positions can hold (8 or
- * 127 times their largest scale) where that is coarser.  q is exact,
+ * largest key element times the sum of |q|.  f16 and bf16, more rows: the weights are rounded to 11 bits; the
+ * stored keys and values to 11 bits with bf16 tokens, with f16 ones to 14 (Q8_0) or not at all (Q4_0); or to 2^-17 (Q4_0) or 2^-20 (Q8_0) of the
+ * largest that 32 neighbouring positions can hold (8 or 127 times their largest scale) where that is coarser.  q is exact,
  * but for elements below 2^-24 of their row's largest.
  * Deterministic: the same call gives the same bits.  Between batches a token's bits may differ, within the accuracy above: the rest of the
  * batch decides the split of the positions over CTAs, and n_tokens / n_req (rows behind the last request and requests without tokens

@@ -10,7 +10,11 @@
 //   1 walker warp    finds the parts and the addresses of their cells, and asks for them ahead into L2
 // Two blocks a multiprocessor (D 256: one) fill each other's gaps.
 //
-// Measured: Q4_0, f16, heads of 128, 4096 tokens behind 12289 positions, 32 on 8 heads (962 GFLOP): 1131 us = 851 TFLOP/s, 44 % of what a
+// f16 tokens: K and V^T in two terms, units of 64 positions, whose second terms take the tiles' other half; the same weights meet both of V's.
+// With one term f16 outputs were off by 3.9e-4 (Q4_0) to 6.9e-4 (Q8_0) of their norm, where their own rounding is 2.1e-4: keys 2.5 and 5.9, values 1.6 and
+// 2.1, weights 1.7; with two by 2.9e-4.  bf16 outputs' own rounding is 1.7e-3, and one term stays.
+//
+// Measured: Q4_0, heads of 128, 4096 tokens behind 12289 positions, 32 on 8 heads (962 GFLOP): f16 1838 us, with one term 1131 us = 851 TFLOP/s, 44 % of what a
 // large bf16 product reaches.  A prompt of 2011 tokens, Q8_0 (33 GFLOP): 126 us.  Bound by the chain of a unit, S, softmax, O: the weights take the
 // place of the scores in tensor memory, so the next unit's S waits for O, and two blocks hide part of that (tensor pipe 36 % busy, issue slots
 // 57 %).  The short prompt: 14 units a block, among them the start and end of two or three tiles, then 12 us of joins.  On the way, of these
@@ -32,7 +36,7 @@
 namespace hq {
 namespace {
 
-constexpr int kRows = 128, kUnit = 128, kCells = kUnit / kCell;
+constexpr int kRows = 128, kTile = 128;                     // query rows, and rows of K (columns of V^T) that a tile holds
 constexpr int kSoftmax = 4, kDecode = 4;                    // warps: softmax, then of keys, of values
 constexpr int kValues = kSoftmax + kDecode, kWalker = kValues + kDecode, kProducts = kWalker + 1;
 constexpr int kThreads = 32 * (kProducts + 1);
@@ -101,23 +105,26 @@ __device__ __forceinline__ void load_global(const uint8_t *p, uint32_t *v) {
     }
 }
 
-template <int BITS, int D>
+template <int BITS, int D, int TERMS_>
 struct Tile {
     using L = CellLayout<BITS, D>;
+    static constexpr int TERMS = TERMS_;                    // of keys and values
+    static constexpr int UNIT = kTile / TERMS, CELLS = UNIT / kCell;        // positions of a unit
+    static constexpr int GROUPS = kDecode / TERMS;          // 32 positions that one warp, or two, decode
     static constexpr int NB = L::NB;
     static constexpr int MIN_BLOCKS = tile_blocks(D);
     static constexpr uint32_t TMEM = D == 256 ? 512 : 256;  // columns: scores (and in their place weights) 0..127, outputs from 128
-    static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = kUnit * D * 2, V_BYTES = kUnit * D * 2;
+    static constexpr int Q_BYTES = kRows * D * 2, K_BYTES = kTile * D * 2, V_BYTES = kTile * D * 2;
     struct Shared {
         WalkShared walk;
         Part part[2];
         uint64_t part_full[2], part_empty[2], cell_full[kSlots], cell_empty[kSlots];
         uint64_t q_full, k_full, v_full, s_full, p_full, pv_done;
-        uint64_t cell[kSlots][kCells];                      // addresses; 0: no position that is seen, 1: page out of range
+        uint64_t cell[kSlots][CELLS];                       // addresses; 0: no position that is seen, 1: page out of range
         float factor[2][kRows];                             // of the queries of a part
-        int k_exp[2][kDecode], v_exp[2][kDecode];           // of 32 positions: the stored value is the tile's times 2^exp
-        uint32_t any_bad[2][kDecode];                       // some value block of the 32 positions is no number
-        uint8_t bad[2][kUnit];                              // then: of each position, bit b: block b
+        int k_exp[2][GROUPS], v_exp[2][GROUPS];             // of 32 positions: the stored value is the tile's times 2^exp
+        uint32_t any_bad[2][GROUPS];                        // some value block of the 32 positions is no number
+        uint8_t bad[2][UNIT];                               // then: of each position, bit b: block b
         uint32_t tmem;
         int abort;
     };
@@ -145,20 +152,39 @@ __device__ __forceinline__ void raw_pairs(const uint32_t *w, uint32_t (&h)[4]) {
 
 // raw quants times scale d (normalised): 4 bits: d 2^-20 (n - 8), 8 bits: d 2^-24 (u - 128); one rounding each, and one
 // of the offset's product where that is subnormal.
+struct Scale {                                              // of two blocks, or of two positions
+    __half2 d, off, big;
+    template <int BITS>
+    static __device__ __forceinline__ Scale of(__half2 d) {
+        return {d, __hmul2(d, __half2half2(__ushort_as_half(0x8080))), BITS == 4 ? __hmul2(d, power_h2(4)) : d};       // -2^-17
+    }
+    __device__ __forceinline__ Scale block(int b) const {
+        return b ? Scale{__high2half2(d), __high2half2(off), __high2half2(big)} : Scale{__low2half2(d), __low2half2(off), __low2half2(big)};
+    }
+};
 template <int BITS>
-__device__ __forceinline__ void scaled_pairs(uint32_t (&h)[4], __half2 d) {
-    const __half2 off = __hmul2(d, __half2half2(__ushort_as_half(0x8080)));         // -2^-17
-    const __half2 big = BITS == 4 ? __hmul2(d, power_h2(4)) : d;
+__device__ __forceinline__ void scaled_pairs(uint32_t (&h)[4], const Scale &s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = h2_bits(__hfma2(bits_h2(h[i]), BITS == 4 && (i & 1) == 0 ? big : d, off));
+    for (int i = 0; i < 4; ++i) h[i] = h2_bits(__hfma2(bits_h2(h[i]), BITS == 4 && (i & 1) == 0 ? s.big : s.d, s.off));
+}
+
+// Term t of a scale d.  Two: its first bits, so few that their product with any quant has 11 bits, and the rest: Q4_0 values are exact
+// then, Q8_0 ones rounded to 2^-4 2^-11 of themselves.  Scales below 2^3, whose products are subnormal, stay whole: two more roundings
+// of 2^-25 would cost what the rest adds.
+template <int BITS, int TERMS>
+__device__ __forceinline__ __half2 term(__half2 d, int t) {
+    if (TERMS == 1) return d;
+    const uint32_t large = __hge2_mask(__habs2(d), __half2half2(__ushort_as_half(0x4800)));
+    const __half2 first = bits_h2(h2_bits(d) & (~large | (BITS == 4 ? 0xfff8fff8u : 0xff80ff80u)));
+    return t == 0 ? first : __hsub2(d, first);
 }
 
 // ------------------------------------------------------------------ the walker
 
-template <int BITS, int D>
-__device__ __forceinline__ void walk(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, long long total, long long x0, long long end) {
+template <int BITS, int D, int TERMS>
+__device__ __forceinline__ void walk(const AttnArgs &a, typename Tile<BITS, D, TERMS>::Shared &s, long long total, long long x0, long long end) {
     using L = CellLayout<BITS, D>;
-    constexpr int AHEAD = 32 / kCells;
+    constexpr int UNIT = Tile<BITS, D, TERMS>::UNIT, CELLS = Tile<BITS, D, TERMS>::CELLS, AHEAD = 32 / CELLS;
     const int lane = threadIdx.x & 31;
     volatile int *abort = &s.abort;
     int slot = 0;
@@ -180,16 +206,16 @@ __device__ __forceinline__ void walk(const AttnArgs &a, typename Tile<BITS, D>::
         uint64_t cell = 0;
         for (int u = 0; u < p.take; ++u) {
             if (u % AHEAD == 0) {                           // lane i: cell i of the next units
-                const int pos = p.begin + u * kUnit + lane * kCell;
+                const int pos = p.begin + u * UNIT + lane * kCell;
                 cell = 0;
-                if (lane / kCells + u < p.take && pos < p.span.hi && pos + kCell > p.span.lo) {
+                if (lane / CELLS + u < p.take && pos < p.span.hi && pos + kCell > p.span.lo) {
                     uint8_t *cells = page_cells(a.c, s.walk.walk.r, pos, p.item.kv_head);
                     cell = cells ? reinterpret_cast<uint64_t>(cell_of<L>(a.c, cells, pos)) : 1;
                     if (cells) prefetch_l2(reinterpret_cast<const void *>(cell), L::BYTES);
                 }
             }
             if (!tc_wait(smem_u32(&s.cell_empty[slot]), phase, abort, a.c.fault)) return;
-            if (lane / kCells == u % AHEAD) s.cell[slot][lane % kCells] = cell;
+            if (lane / CELLS == u % AHEAD) s.cell[slot][lane % CELLS] = cell;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.cell_full[slot]));
             if (++slot == kSlots) { slot = 0; phase ^= 1; }
@@ -201,15 +227,15 @@ __device__ __forceinline__ void walk(const AttnArgs &a, typename Tile<BITS, D>::
 // ------------------------------------------------------------------ decoding
 
 // The addresses of a decode warp's cells, unit after unit.
-template <int BITS, int D>
+template <int BITS, int D, int TERMS>
 struct Cells {
-    typename Tile<BITS, D>::Shared &s;
+    typename Tile<BITS, D, TERMS>::Shared &s;
     uint32_t at;                                            // slot, and below it the phase of its barrier
-    __device__ __forceinline__ bool next(const AttnArgs &a, int w, uint64_t (&cell)[2]) {
+    __device__ __forceinline__ bool next(const AttnArgs &a, int group, uint64_t (&cell)[2]) {
         const uint32_t slot = at >> 1;
         if (!tc_wait(smem_u32(&s.cell_full[slot]), at & 1, &s.abort, a.c.fault)) return false;
-        cell[0] = s.cell[slot][2 * w];
-        cell[1] = s.cell[slot][2 * w + 1];
+        cell[0] = s.cell[slot][2 * group];
+        cell[1] = s.cell[slot][2 * group + 1];
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&s.cell_empty[slot]));
         at = slot == kSlots - 1 ? (at & 1) ^ 1 : at + 2;
@@ -219,8 +245,8 @@ struct Cells {
 
 // The decode warps prepare the tile of Q at a part's start, 16 rows each, while the softmax warps may still write the part before:
 // rows times a power of two that takes their largest element to [2^14, 2^15), and the scale's sign.
-template <int BITS, int D>
-__device__ __forceinline__ void prepare_queries(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint8_t *q_tile, int at) {
+template <int BITS, int D, int TERMS>
+__device__ __forceinline__ void prepare_queries(const AttnArgs &a, typename Tile<BITS, D, TERMS>::Shared &s, uint8_t *q_tile, int at) {
     constexpr int LANES = D / 8, ROWS = 32 / LANES, MINE = kRows / (2 * kDecode);       // lanes of a row, rows at once, rows of a warp
     const Part &part = s.part[at];
     const int lane = threadIdx.x & 31, col = lane % LANES, row0 = MINE * ((threadIdx.x >> 5) - kSoftmax) + lane / LANES;
@@ -261,26 +287,27 @@ __device__ __forceinline__ void prepare_queries(const AttnArgs &a, typename Tile
     if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
 }
 
-// A key warp has 32 positions of a unit: two cells.  Four neighbouring lanes have a row; rows x and x ^ 5 lie side by
+// A key warp has 32 positions of a unit: two cells (two terms: one of them, and a power of two with the warp of the other).  Four neighbouring lanes have a row; rows x and x ^ 5 lie side by
 // side, so that the stores do not meet in a bank.  The next unit's bytes are asked for while this one's products run.
-template <int BITS, int D>
-__device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint8_t *q_tile, uint32_t k_tile) {
-    using T = Tile<BITS, D>;
+template <int BITS, int D, int TERMS>
+__device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BITS, D, TERMS>::Shared &s, uint8_t *q_tile, uint32_t k_tile) {
+    using T = Tile<BITS, D, TERMS>;
     using L = typename T::L;
     constexpr int NB = T::NB, WB = BITS / 4, BLOCKS = NB / L::UNITS;        // words of a block, blocks of a unit
     constexpr int SCALES = NB / 2;                          // words of a lane's share of the scales: 16 lanes a cell
     constexpr int TO = BITS == 4 ? 25 : 29;                 // scales go to [2^10, 2^11) or [2^14, 2^15)
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftmax;
+    constexpr int UNIT = T::UNIT, ROWS = 4 / TERMS;         // of a lane, 8 apart
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftmax, group = w / TERMS, half = w % TERMS;
     const int c = lane & 3, kr = (lane >> 3) ^ (lane & 4 ? 5 : 0);
     volatile int *abort = &s.abort;
-    Cells<BITS, D> cells = {s, 0};
+    Cells<BITS, D, TERMS> cells = {s, 0};
     uint32_t n = 0;                                         // units so far
     uint64_t cell[2] = {0, 0};
-    uint32_t raw[4][L::UW], ks[4][BLOCKS / 2], tk[SCALES];
+    uint32_t raw[ROWS][L::UW], ks[ROWS][BLOCKS / 2], tk[SCALES];
     auto load_unit = [&](int u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {                       // rows 8 i + kr
-            const uint64_t from = cell[i >> 1];
+        for (int i = 0; i < ROWS; ++i) {                    // rows 8 i + kr (and 16 half)
+            const uint64_t from = cell[TERMS == 1 ? i >> 1 : half];
             const uint8_t *p = reinterpret_cast<const uint8_t *>(from);
 #pragma unroll
             for (int k = 0; k < L::UW; ++k) raw[i][k] = 0;
@@ -306,11 +333,11 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
         if (!tc_wait(smem_u32(&s.part_full[at]), (uint32_t)(part_n >> 1 & 1), abort, a.c.fault)) return;
         if (s.part[at].take == 0) return;
         if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;          // the tile of Q is free
-        prepare_queries<BITS, D>(a, s, q_tile, at);
-        if (!cells.next(a, w, cell)) return;
+        prepare_queries<BITS, D, TERMS>(a, s, q_tile, at);
+        if (!cells.next(a, group, cell)) return;
         load();
         for (int u = 0; u < s.part[at].take; ++u, ++n) {
-            const int p0 = s.part[at].begin + u * kUnit + 32 * w;           // of this warp's positions
+            const int p0 = s.part[at].begin + u * UNIT + 32 * group;        // of this warp's positions
             const int lo = s.part[at].span.lo, hi = s.part[at].span.hi;
             uint32_t top = 0;                               // of what is a number and seen by some row
 #pragma unroll
@@ -323,24 +350,32 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
             }
             const int e = (int)(__reduce_max_sync(0xffffffffu, top) >> 10);
             if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;      // the tile is free
-            if (lane == 0) s.k_exp[n & 1][w] = e - 5;
+            if (lane == 0 && half == 0) s.k_exp[n & 1][group] = e - 5;
             const int x = TO - e, x1 = min(x, 15);
             const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
 #pragma unroll 1
             for (int v = 0; v < L::UNITS; ++v) {
                 if (v > 0) load_unit(v);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 32 * w + 8 * i + kr;
+                for (int i = 0; i < ROWS; ++i) {
+                    const int row = 32 * group + 16 * half + 8 * i + kr;
+                    Scale d[TERMS];
 #pragma unroll
                     for (int k = 0; k < BLOCKS; ++k) {
                         const int b = v * BLOCKS + k;
-                        const __half2 d = __hmul2(__hmul2(bits_h2(ks[i][k / 2]), up1), up2);
-                        uint32_t h[4];
-                        raw_pairs<BITS, 0x4140, 0x4342>(&raw[i][k * WB], h);
-                        scaled_pairs<BITS>(h, k & 1 ? __high2half2(d) : __low2half2(d));
-                        const uint32_t to = k_tile + (b >> 1) * (kUnit * 128) + row * 128 + (((4 * (k & 1) + c) ^ (row & 7)) << 4);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+                        if (k % 2 == 0) {
+                            const __half2 both = __hmul2(__hmul2(bits_h2(ks[i][k / 2]), up1), up2);
+#pragma unroll
+                            for (int t = 0; t < TERMS; ++t) d[t] = Scale::of<BITS>(term<BITS, TERMS>(both, t));
+                        }
+#pragma unroll
+                        for (int t = 0; t < TERMS; ++t) {
+                            uint32_t h[4];
+                            raw_pairs<BITS, 0x4140, 0x4342>(&raw[i][k * WB], h);
+                            scaled_pairs<BITS>(h, d[t].block(k & 1));
+                            const uint32_t to = k_tile + (b >> 1) * (kTile * 128) + (row + t * UNIT) * 128 + (((4 * (k & 1) + c) ^ (row & 7)) << 4);
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+                        }
                     }
                 }
             }
@@ -351,7 +386,7 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
                 mbar_arrive(smem_u32(&s.s_full));           // (the softmax warps read the exponents)
             }
             if (u + 1 < s.part[at].take) {
-                if (!cells.next(a, w, cell)) return;
+                if (!cells.next(a, group, cell)) return;
                 load();
             }
         }
@@ -360,20 +395,21 @@ __device__ __forceinline__ void decode_keys(const AttnArgs &a, typename Tile<BIT
     }
 }
 
-// A value warp has 32 positions of a unit.  A lane turns eight positions' elements g, 8 + g, .. into rows of V^T: 16 bytes
+// A value warp has 32 positions of a unit (two terms: half of the blocks of them).  A lane turns eight positions' elements g, 8 + g, .. into rows of V^T: 16 bytes
 // each, the rows of eight neighbouring lanes in different banks.
-template <int BITS, int D>
-__device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint8_t *q_tile, uint32_t v_tile) {
-    using T = Tile<BITS, D>;
+template <int BITS, int D, int TERMS>
+__device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<BITS, D, TERMS>::Shared &s, uint8_t *q_tile, uint32_t v_tile) {
+    using T = Tile<BITS, D, TERMS>;
     using L = typename T::L;
     constexpr int NB = T::NB, WB = BITS / 4;                // words of a block
-    constexpr int STEP = BITS == 8 && D == 128 ? 1 : 2;     // blocks at a time (two are more than 72 registers there)
+    constexpr int UNIT = T::UNIT, MINE = NB / TERMS;        // blocks of a warp
+    constexpr int STEP = MINE == 1 || (BITS == 8 && D == 128) ? 1 : 2;      // blocks at a time (two are more than 72 registers there)
     constexpr int SCALES = NB / 2;
     constexpr int TO = BITS == 4 ? 25 : 29;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kValues;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kValues, group = w / TERMS, half = w % TERMS, first = half * MINE;
     const int q = lane >> 3, g = lane & 7;                  // eight positions from 8 q, elements g of each eight
     volatile int *abort = &s.abort;
-    Cells<BITS, D> cells = {s, 0};
+    Cells<BITS, D, TERMS> cells = {s, 0};
     uint32_t n = 0;
     uint64_t cell[2] = {0, 0};
     uint32_t raw[4][STEP * WB], vs[4][STEP], tv[SCALES];
@@ -393,7 +429,7 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
         }
     };
     auto load = [&]() {
-        load_step(0);
+        load_step(first);
         const uint8_t *p = reinterpret_cast<const uint8_t *>(cell[lane >> 4]);
 #pragma unroll
         for (int k = 0; k < SCALES; ++k) {
@@ -406,11 +442,11 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
         if (!tc_wait(smem_u32(&s.part_full[at]), (uint32_t)(part_n >> 1 & 1), abort, a.c.fault)) return;
         if (s.part[at].take == 0) return;
         if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;          // the tile of Q is free
-        prepare_queries<BITS, D>(a, s, q_tile, at);
-        if (!cells.next(a, w, cell)) return;
+        prepare_queries<BITS, D, TERMS>(a, s, q_tile, at);
+        if (!cells.next(a, group, cell)) return;
         load();
         for (int u = 0; u < s.part[at].take; ++u, ++n) {
-            const int p0 = s.part[at].begin + u * kUnit + 32 * w;
+            const int p0 = s.part[at].begin + u * UNIT + 32 * group;
             const int lo = s.part[at].span.lo, hi = s.part[at].span.hi, par = n & 1;
             const bool edge = p0 < lo || p0 + 32 > hi;
             uint32_t top = 0;
@@ -430,12 +466,12 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
             odd = __any_sync(0xffffffffu, odd);
             if (n > 0 && !tc_wait(smem_u32(&s.s_full), (n - 1) & 1, abort, a.c.fault)) return;
             if (lane == 0) {
-                s.v_exp[par][w] = e - 5;
+                if (half == 0) s.v_exp[par][group] = e - 5;
                 mbar_arrive(smem_u32(&s.s_full));           // (the softmax warps read the exponents)
             }
             if (n > 0 && !tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault)) return;     // the tile is free
-            if (lane == 0) s.any_bad[par][w] = odd;         // (the softmax warps are done with those of two units before)
-            if (odd) {                                      // a lane a position: marks of its blocks
+            if (lane == 0 && half == 0) s.any_bad[par][group] = odd;         // (the softmax warps are done with those of two units before)
+            if (odd && half == 0) {                         // a lane a position: marks of its blocks
                 uint32_t marks = 0;
                 const uint64_t from = cell[lane >> 4];
 #pragma unroll 1
@@ -443,13 +479,13 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
                     const uint16_t d = *reinterpret_cast<const uint16_t *>(reinterpret_cast<const uint8_t *>(from) + L::v_scale(lane & 15, b));
                     if ((d & 0x7c00u) == 0x7c00u) marks |= 1u << b;
                 }
-                s.bad[par][32 * w + lane] = (uint8_t)marks;
+                s.bad[par][32 * group + lane] = (uint8_t)marks;
             }
             const int x = TO - e, x1 = min(x, 15);
             const __half2 up1 = power_h2(x1), up2 = power_h2(x - x1);
 #pragma unroll 1
-            for (int b = 0; b < NB; b += STEP) {
-                if (b > 0) load_step(b);
+            for (int b = first; b < first + MINE; b += STEP) {
+                if (b > first) load_step(b);
                 if (edge) {                                 // positions that no row sees are zeros
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -466,17 +502,19 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
                         for (int k = 0; k < STEP; ++k) vs[i][k] &= ~__vcmpeq2(vs[i][k] & 0x7c007c00u, 0x7c007c00u);
                 }
 #pragma unroll
-                for (int k = 0; k < STEP; ++k) {
+                for (int k = 0; k < STEP; ++k)
+#pragma unroll 1
+                for (int t = 0; t < TERMS; ++t) {
                     uint32_t h[4][4];                       // [pair][j]
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         raw_pairs<BITS, 0x4240, 0x4341>(&raw[i][k * WB], h[i]);
-                        scaled_pairs<BITS>(h[i], __hmul2(__hmul2(bits_h2(vs[i][k]), up1), up2));
+                        scaled_pairs<BITS>(h[i], Scale::of<BITS>(term<BITS, TERMS>(__hmul2(__hmul2(bits_h2(vs[i][k]), up1), up2), t)));
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int row = 32 * (b + k) + 8 * j + g;
-                        const uint32_t to = v_tile + (w >> 1) * (D * 128) + row * 128 + (((4 * (w & 1) + q) ^ g) << 4);
+                        const int row = 32 * (b + k) + 8 * j + g, column = t * UNIT + 32 * group + 8 * q;       // of 128, 64 to a row of 128 bytes
+                        const uint32_t to = v_tile + column / 64 * (D * 128) + row * 128 + ((column / 8 % 8 ^ g) << 4);
                         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0][j]), "r"(h[1][j]), "r"(h[2][j]), "r"(h[3][j]) : "memory");
                     }
                 }
@@ -485,7 +523,7 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.v_full));
             if (u + 1 < s.part[at].take) {
-                if (!cells.next(a, w, cell)) return;
+                if (!cells.next(a, group, cell)) return;
                 load();
             }
         }
@@ -496,11 +534,12 @@ __device__ __forceinline__ void decode_values(const AttnArgs &a, typename Tile<B
 
 // ------------------------------------------------------------------ products
 
-template <int BITS, int D>
-__device__ __forceinline__ void products(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t q_tile, uint32_t k_tile,
+template <int BITS, int D, int TERMS>
+__device__ __forceinline__ void products(const AttnArgs &a, typename Tile<BITS, D, TERMS>::Shared &s, uint32_t q_tile, uint32_t k_tile,
                                          uint32_t v_tile, uint32_t tmem) {
     volatile int *abort = &s.abort;
-    const uint32_t qk = tc_idesc(kUnit, false), pv = tc_idesc(D, false);
+    constexpr int UNIT = Tile<BITS, D, TERMS>::UNIT;
+    const uint32_t qk = tc_idesc(UNIT, false), pv = tc_idesc(D, false);
     const uint32_t scores = tmem, outputs = tmem + 128;
     uint32_t n = 0;
     bool fine = true;
@@ -515,16 +554,18 @@ __device__ __forceinline__ void products(const AttnArgs &a, typename Tile<BITS, 
                 (n > 0 && !tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault))) { fine = false; break; }
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                tc_mma_ss(scores, tc_desc_sw128(q_tile + k / 4 * (kRows * 128) + k % 4 * 32),
-                          tc_desc_sw128(k_tile + k / 4 * (kUnit * 128) + k % 4 * 32), qk, k > 0);
+            for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc_mma_ss(scores, tc_desc_sw128(q_tile + k / 4 * (kRows * 128) + k % 4 * 32),
+                              tc_desc_sw128(k_tile + k / 4 * (kTile * 128) + t * UNIT * 128 + k % 4 * 32), qk, t + k > 0);
             tc_commit(smem_u32(&s.s_full));
             if (!tc_wait(smem_u32(&s.v_full), n & 1, abort, a.c.fault) ||
                 !tc_wait(smem_u32(&s.p_full), n & 1, abort, a.c.fault)) { fine = false; break; }
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kUnit / 16; ++k)
-                tc_mma(outputs, scores + 8 * k, tc_desc_sw128(v_tile + k / 4 * (D * 128) + k % 4 * 32), pv, u > 0 || k > 0);
+            for (int k = 0; k < kTile / 16; ++k)            // (of each term's columns the weights are the same)
+                tc_mma(outputs, scores + 8 * (k % (UNIT / 16)), tc_desc_sw128(v_tile + k / 4 * (D * 128) + k % 4 * 32), pv, u > 0 || k > 0);
             tc_commit(smem_u32(&s.pv_done));
         }
         if (fine) mbar_arrive(smem_u32(&s.part_empty[at]));
@@ -538,8 +579,9 @@ __device__ __forceinline__ void products(const AttnArgs &a, typename Tile<BITS, 
 
 // ------------------------------------------------------------------ softmax
 
-template <int BITS, int D>
-__device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D>::Shared &s, uint32_t tmem) {
+template <int BITS, int D, int TERMS>
+__device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D, TERMS>::Shared &s, uint32_t tmem) {
+    constexpr int UNIT = Tile<BITS, D, TERMS>::UNIT, GROUPS = Tile<BITS, D, TERMS>::GROUPS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = threadIdx.x;
     volatile int *abort = &s.abort;
     const uint32_t scores = tmem + ((uint32_t)(32 * warp) << 16), outputs = scores + 128;
@@ -561,25 +603,28 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
         // value blocks of a unit that are no numbers and that the row sees
         auto look_at_bad = [&](uint32_t unit, int first) {
             const uint32_t *f = s.any_bad[unit & 1];
-            if ((f[0] | f[1] | f[2] | f[3]) == 0) return;
-            for (int k = 0; k < kUnit; ++k)
+            uint32_t any = 0;
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k) any |= f[k];
+            if (any == 0) return;
+            for (int k = 0; k < UNIT; ++k)
                 if (f[k >> 5] && first + k >= see.lo && first + k < see.hi && first + k >= part.span.lo && first + k < part.span.hi)
                     bad |= s.bad[unit & 1][k];
         };
-        for (int u = 0; u < take; ++u, ++n, p0 += kUnit) {
+        for (int u = 0; u < take; ++u, ++n, p0 += UNIT) {
             if (!tc_wait(smem_u32(&s.s_full), n & 1, abort, a.c.fault)) return;
             tc_fence_after();
             if (u == 0) factor = see.hi > see.lo ? s.factor[at][me] : 0.f;      // (a row that sees nothing is zeros, whatever its query)
             if (work) {
-                if (u > 0) look_at_bad(n - 1, p0 - kUnit);
+                if (u > 0) look_at_bad(n - 1, p0 - UNIT);
                 const int first = see.lo - p0, last = see.hi - p0;          // columns that the row sees: [first, last)
-                const bool edge = __any_sync(0xffffffffu, first > 0 || last < kUnit);
+                const bool edge = __any_sync(0xffffffffu, first > 0 || last < UNIT);
                 const int *ke = s.k_exp[n & 1], *ve = s.v_exp[n & 1];       // of 32 columns
                 // (Loops that stay loops, and the hidden columns in a pass of their own: the warps of a multiprocessor run many
                 // different paths, and what they do not find in the instruction caches they wait for.)
                 if (edge) {
 #pragma unroll 1
-                    for (int c = 0; c < kUnit; c += 8) {
+                    for (int c = 0; c < UNIT; c += 8) {
                         float v[8];
                         tmem_ld8(scores + c, v);
                         tmem_wait_ld(v);
@@ -592,7 +637,7 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
                 }
                 float top = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < GROUPS; ++c) {
                     float v[32], m[4];
                     tmem_load32(scores + 32 * c, v);
 #pragma unroll
@@ -622,7 +667,7 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
                 const float base = kWeight - fmaxf(ref, -3e38f);            // nothing seen yet: all columns are hidden
                 // weights into tensor memory, in place of scores that are in registers by then
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < GROUPS; ++c) {
                     float v[32], fk = factor * power(ke[c]);
                     if (fk == 0.f) fk = 1e-37f;             // a hidden column's -inf stays one
                     const float b = base + (float)ve[c];
@@ -655,7 +700,7 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
         if (!tc_wait(smem_u32(&s.pv_done), (n - 1) & 1, abort, a.c.fault)) return;
         tc_fence_after();
         if (work) {
-            look_at_bad(n - 1, p0 - kUnit);
+            look_at_bad(n - 1, p0 - UNIT);
             const float f = part.slot >= 0 ? 1.f : l == 0.f ? 0.f : __fdiv_rn(1.f, l);
             const long long r = (long long)part.slot * kRows + me;
             const long long to = ((long long)part.q.first + token) * a.out_stride + (long long)head * D;
@@ -682,9 +727,9 @@ __device__ __forceinline__ void softmax(const AttnArgs &a, typename Tile<BITS, D
     }
 }
 
-template <int BITS, int D>
-__global__ void __launch_bounds__(kThreads, (Tile<BITS, D>::MIN_BLOCKS)) attention_tile_kernel(const __grid_constant__ AttnArgs a) {
-    using T = Tile<BITS, D>;
+template <int BITS, int D, int TERMS>
+__global__ void __launch_bounds__(kThreads, (Tile<BITS, D, TERMS>::MIN_BLOCKS)) attention_tile_kernel(const __grid_constant__ AttnArgs a) {
+    using T = Tile<BITS, D, TERMS>;
     extern __shared__ __align__(1024) uint8_t memory[];
     typename T::Shared &s = *reinterpret_cast<typename T::Shared *>(memory);
     uint8_t *q_tile = memory + T::FIXED;
@@ -721,15 +766,15 @@ __global__ void __launch_bounds__(kThreads, (Tile<BITS, D>::MIN_BLOCKS)) attenti
     deal<kThreads>(a, total, x0, end, s.walk);
     if (x0 >= end) {
     } else if (warp < kSoftmax) {
-        softmax<BITS, D>(a, s, tmem);
+        softmax<BITS, D, TERMS>(a, s, tmem);
     } else if (warp < kValues) {
-        decode_keys<BITS, D>(a, s, q_tile, k);
+        decode_keys<BITS, D, TERMS>(a, s, q_tile, k);
     } else if (warp < kWalker) {
-        decode_values<BITS, D>(a, s, q_tile, v);
+        decode_values<BITS, D, TERMS>(a, s, q_tile, v);
     } else if (warp == kWalker) {
-        walk<BITS, D>(a, s, total, x0, end);
+        walk<BITS, D, TERMS>(a, s, total, x0, end);
     } else if (elect_one()) {
-        products<BITS, D>(a, s, q, k, v, tmem);
+        products<BITS, D, TERMS>(a, s, q, k, v, tmem);
     }
     __syncwarp();
     tc_fence_before();
@@ -738,23 +783,33 @@ __global__ void __launch_bounds__(kThreads, (Tile<BITS, D>::MIN_BLOCKS)) attenti
     if (warp == 0) tmem_dealloc(tmem, T::TMEM);
 }
 
-template <int BITS, int D>
+template <int BITS, int D, int TERMS>
 hq_status run(AttnArgs a, int num_sms, cudaStream_t stream) {
-    using T = Tile<BITS, D>;
+    using T = Tile<BITS, D, TERMS>;
     static std::atomic<bool> done[64];
-    hq_status st = allow_smem(attention_tile_kernel<BITS, D>, T::SMEM, done);
+    hq_status st = allow_smem(attention_tile_kernel<BITS, D, TERMS>, T::SMEM, done);
     if (st != HQ_OK) return st;
-    deal_rows(a, kRows, D, 7, std::min(kSms, num_sms) * T::MIN_BLOCKS);
-    st = launch_blocks(attention_tile_kernel<BITS, D>, dim3((unsigned)a.blocks), kThreads, T::SMEM, stream, "attention", a);
+    static_assert(T::UNIT == 1 << (8 - TERMS), "unit_shift");
+    deal_rows(a, kRows, D, 8 - TERMS, std::min(kSms, num_sms) * T::MIN_BLOCKS);
+    st = launch_blocks(attention_tile_kernel<BITS, D, TERMS>, dim3((unsigned)a.blocks), kThreads, T::SMEM, stream, "attention", a);
     return st != HQ_OK ? st : run_attention_combine(a, kRows, D, stream);
+}
+
+template <int TERMS>
+hq_status run_fmt(const AttnArgs &a, int fmt, int dim, int num_sms, cudaStream_t stream) {
+    if (fmt == HQ_FMT_Q8_0)
+        return dim == 64    ? run<8, 64, TERMS>(a, num_sms, stream)
+               : dim == 128 ? run<8, 128, TERMS>(a, num_sms, stream)
+                            : run<8, 256, TERMS>(a, num_sms, stream);
+    return dim == 64    ? run<4, 64, TERMS>(a, num_sms, stream)
+           : dim == 128 ? run<4, 128, TERMS>(a, num_sms, stream)
+                        : run<4, 256, TERMS>(a, num_sms, stream);
 }
 
 }  // namespace
 
 hq_status run_attention_tile(const AttnArgs &a, int fmt, int dim, int num_sms, cudaStream_t stream) {
-    if (fmt == HQ_FMT_Q8_0)
-        return dim == 64 ? run<8, 64>(a, num_sms, stream) : dim == 128 ? run<8, 128>(a, num_sms, stream) : run<8, 256>(a, num_sms, stream);
-    return dim == 64 ? run<4, 64>(a, num_sms, stream) : dim == 128 ? run<4, 128>(a, num_sms, stream) : run<4, 256>(a, num_sms, stream);
+    return a.dtype == HQ_DT_F16 ? run_fmt<2>(a, fmt, dim, num_sms, stream) : run_fmt<1>(a, fmt, dim, num_sms, stream);
 }
 
 }  // namespace hq

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from quantized_weight_matvec_hq_gb300 import synthetic
-from test_gpu_cache import DT, Batch, check_attention, dev, hq, no_device_fault, stored, values  # noqa: F401
+from test_gpu_cache import DT, Batch, check_attention, dev, formula, hq, no_device_fault, stored, values  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -216,3 +216,21 @@ def test_one_workspace_for_batches_of_every_size(hq, dim, dtype):
         q = torch.from_numpy(g.standard_normal((b.T, heads, dim)).astype(np.float32)).cuda().to(DT[dtype])
         assert torch.equal(b.attend(q, heads, ws=ws[:need]), b.attend(q, heads))
         assert bool((ws[need:] == 255).all())
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [2, 200])
+def test_f16_outputs_are_near_their_own_rounding(hq, fmt, dim, new):
+    """Over many outputs, f16 rows are off by at most 1.5 times what rounding the formula's results to f16 is.  Beside that rounding, either
+    kernel rounds one more number of 11 bits for every term of an output (a weight, or a weight times a scale), whose error over
+    many terms of random sign is no larger, relative to the result: sqrt(2) in all, and the rest of the errors is 2^-3 of it."""
+    g = synthetic.rng(1980 + dim)
+    heads, kv, L = 8, 2, 3000
+    b = Batch(hq, g, fmt, kv, dim, 64, [L], [new], "f16", tail=0)
+    cache = b.fill(g)
+    q = torch.from_numpy(g.standard_normal((new, heads, dim)).astype(np.float32)).cuda().half()
+    out = b.attend(q, heads).double()
+    ref = formula(q, cache, [L], [new], heads, kv, dim, 1, 0, dim ** -0.5)[0]
+    off, rounding = (out - ref).norm() / ref.norm(), (ref.half().double() - ref).norm() / ref.norm()
+    assert off <= 1.5 * rounding, (float(off), float(rounding))
