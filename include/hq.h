@@ -587,7 +587,7 @@ hq_status hq_cache_read(int fmt, void *k, int64_t k_stride, void *v, int64_t v_s
  * not touch it, whatever they hold.  One whose key has a NaN or infinite scale makes the rows that
  * see it NaN; a value block's makes that block's 32 elements NaN.
  * Accuracy: scores, maxima, sums and outputs are fp32.  f32 tokens: quants are exact, q and the weights
- * times the values' scales are taken in two 11-bit terms.  f16 and bf16, at most 16 rows a key/value head of the mean
+ * times the values' scales are taken in two 11-bit terms.  bf16 up to 16 rows and f16 up to 32 a key/value head of the mean
  * request (n_tokens / n_req, rounded up, times n_heads / n_kv_heads): the weights times their value block's scale are rounded to 11 bits; scores are off by up to 2^-22 of the position's
  * largest key element times the sum of |q|.  f16 and bf16, more rows: the weights are rounded to 11 bits; the
  * stored keys and values to 11 bits with bf16 tokens, with f16 ones to 14 (Q8_0) or not at all (Q4_0); or to 2^-17 (Q4_0) or 2^-20 (Q8_0) of the

@@ -737,9 +737,12 @@ __global__ void __launch_bounds__(kCombineThreads) attention_combine_kernel(cons
 int64_t mean_rows(const AttentionArgs &x) {
     return (x.cache.n_tokens + x.cache.n_req - 1) / x.cache.n_req * (x.n_heads / x.cache.n_kv_heads);
 }
-// Tiles above 16 rows: 32 requests of 500 to 4000 positions take (few rows / tiles) 30 / 35 us at 16 rows and 47 / 36 at 32 with heads of 128, 34 / 45 and
-// 54 / 46 with heads of 64, 33 / 47 and 52 / 48 with heads of 256.
-[[maybe_unused]] bool on_tiles(const AttentionArgs &x) { return x.cache.dtype != HQ_DT_F32 && mean_rows(x) > 16; }
+// Tiles above 16 rows (bf16) or 32 (f16, whose tiles take two terms).  32 requests of 500 to 4000 positions, few rows / tiles, us at 16 and 32
+// rows: bf16, heads of 128 30 / 35, 47 / 36; of 64 34 / 45, 54 / 46; of 256 33 / 47, 52 / 48.  f16, at 32 and 48 rows: 48 / 50, 66 / 51; 54 / 62, 75 / 62;
+// 52 / 66, 72 / 69.
+[[maybe_unused]] bool on_tiles(const AttentionArgs &x) {
+    return x.cache.dtype != HQ_DT_F32 && mean_rows(x) > (x.cache.dtype == HQ_DT_F16 ? 32 : 16);
+}
 int stream_rows(const AttentionArgs &x) { return mean_rows(x) <= 8 || x.cache.head_dim == 256 ? 8 : 16; }
 
 // MANY rows at once, or two where there are so few items that each may lie on more than 32 blocks.
